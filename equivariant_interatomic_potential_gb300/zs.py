@@ -81,6 +81,24 @@ def load(build_if_missing: bool = True):
         lib.zs_check_timeouts.argtypes = []
         lib.zs_set_timeout_flag.restype = ctypes.c_int
         lib.zs_set_timeout_flag.argtypes = [P]
+        F32 = ctypes.c_float
+        lib.zs_grouped_matmul.restype = ctypes.c_int
+        lib.zs_grouped_matmul.argtypes = [I32, P, I64, P, P, P, I64, I32, I32, I32, P, I64, P]
+        lib.zs_grouped_matmul_dx.restype = ctypes.c_int
+        lib.zs_grouped_matmul_dx.argtypes = [I32, P, I64, P, P, P, I64, I32, I32, I32, P, I64, P]
+        lib.zs_grouped_matmul_dw_workspace_bytes.restype = SZ
+        lib.zs_grouped_matmul_dw_workspace_bytes.argtypes = [I32, I64, I32, I32, I32]
+        lib.zs_grouped_matmul_dw.restype = ctypes.c_int
+        lib.zs_grouped_matmul_dw.argtypes = [I32, P, I64, P, I64, P, P, I64, I32, I32, I32, P, P, SZ, P]
+        lib.zs_norm_gate_residual.restype = ctypes.c_int
+        lib.zs_norm_gate_residual.argtypes = [I32, I32, P, I64, P, I64, P, I64, I32, P, P, P, F32, I64, I32, P, P, P, P]
+        lib.zs_norm_gate_residual_backward_workspace_bytes.restype = SZ
+        lib.zs_norm_gate_residual_backward_workspace_bytes.argtypes = [I64, I32]
+        lib.zs_norm_gate_residual_backward.restype = ctypes.c_int
+        lib.zs_norm_gate_residual_backward.argtypes = [I32, I32, P, I64, P, I64, P, I64, P, I64, P, I64, I32, P, P, P, P,
+                                                       I64, I32, P, P, P, P, P, P, P, SZ, P]
+        lib.zs_adamw_step.restype = ctypes.c_int
+        lib.zs_adamw_step.argtypes = [P, I32, I32, I32, P, P, P]
         _lib = lib
         return lib
 
@@ -440,3 +458,265 @@ def zs_forward_noalloc(coup: torch.Tensor, rad: torch.Tensor, row_ptr: torch.Ten
     _check("zs_forward_noalloc", load().zs_forward_noalloc(_ptr(coup), _ptr(rad), _ptr(row_ptr), _ptr(perm),
                                                            E, N, C, lmax, _ptr(out), _stream(stream)))
     return out
+
+
+# ---------------------------------------------------------------------------
+# Training operators: products grouped by a CSR, residual norms with a gate,
+# the AdamW step.
+
+DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+NORM_KINDS = {"rms": 0, "layer": 1}
+ADAMW_BLOCK = 256          # elements that share a scale of an 8-bit state
+
+
+def _dtype(t: torch.Tensor, name: str) -> int:
+    d = DTYPES.get(t.dtype)
+    if d is None:
+        raise ValueError(f"{name} must be float32, bfloat16 or float16, got {t.dtype}")
+    return d
+
+
+def _matrix(t: torch.Tensor, name: str, dtype: torch.dtype, rows: int, cols: int) -> int:
+    """Checks a CUDA matrix whose rows are contiguous (a row-strided view
+    allowed) and returns its row stride in elements."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != (rows, cols):
+        raise ValueError(f"{name} must have shape {(rows, cols)}, got {tuple(t.shape)}")
+    ld, step = t.stride()
+    if rows > 1 and ld < cols or cols > 1 and step != 1:
+        if t.numel():
+            raise ValueError(f"{name} must have contiguous rows (stride (ld, 1) with ld >= {cols})")
+    return ld if rows > 1 and ld >= cols else cols
+
+
+def _grouped_shapes(w: torch.Tensor, row_ptr: torch.Tensor, perm: torch.Tensor | None, M: int):
+    """Checks what the three grouped products share; returns (dtype, G, N, K)."""
+    d = _dtype(w, "w")
+    if w.dim() != 3:
+        raise ValueError(f"w must have shape (G, N, K), got {tuple(w.shape)}")
+    G, N, K = w.shape
+    _need(w, "w", w.dtype, (G, N, K))
+    _need(row_ptr, "row_ptr", torch.int32, (G + 1,))
+    if perm is not None:
+        _need(perm, "perm", torch.int32, (M,))
+    return d, G, N, K
+
+
+def _rows(t: torch.Tensor, name: str) -> int:
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be a matrix, got shape {tuple(t.shape)}")
+    return t.shape[0]
+
+
+def zs_grouped_matmul(x: torch.Tensor, w: torch.Tensor, row_ptr: torch.Tensor, perm: torch.Tensor | None = None,
+                      out=None, stream=None) -> torch.Tensor:
+    """y[i] = w[g(i)] x[i] for rows grouped by the CSR (row_ptr, perm); perm None: rows
+    are in group order already.  x (M, K) and w (G, N, K) float32, bfloat16 or
+    float16; returns y (M, N).  x and out may be row-strided views."""
+    M = _rows(x, "x")
+    d, G, N, K = _grouped_shapes(w, row_ptr, perm, M)
+    x_ld = _matrix(x, "x", w.dtype, M, K)
+    if out is None:
+        out = torch.empty((M, N), dtype=w.dtype, device=x.device)
+    out_ld = _matrix(out, "out", w.dtype, M, N)
+    _check("zs_grouped_matmul", load().zs_grouped_matmul(d, _ptr(x), x_ld, _ptr(w), row_ptr.data_ptr(), _ptr(perm), M, K, N,
+                                                         G, _ptr(out), out_ld, _stream(stream)))
+    return out
+
+
+def zs_grouped_matmul_dx(dy: torch.Tensor, w: torch.Tensor, row_ptr: torch.Tensor, perm: torch.Tensor | None = None,
+                         out=None, stream=None) -> torch.Tensor:
+    """dx[i] = w[g(i)]^T dy[i]: the gradient of zs_grouped_matmul in x, (M, K)."""
+    M = _rows(dy, "dy")
+    d, G, N, K = _grouped_shapes(w, row_ptr, perm, M)
+    dy_ld = _matrix(dy, "dy", w.dtype, M, N)
+    if out is None:
+        out = torch.empty((M, K), dtype=w.dtype, device=dy.device)
+    out_ld = _matrix(out, "out", w.dtype, M, K)
+    _check("zs_grouped_matmul_dx", load().zs_grouped_matmul_dx(d, _ptr(dy), dy_ld, _ptr(w), row_ptr.data_ptr(), _ptr(perm),
+                                                               M, K, N, G, _ptr(out), out_ld, _stream(stream)))
+    return out
+
+
+def zs_grouped_matmul_dw_workspace_bytes(dtype: torch.dtype, M: int, K: int, N: int, G: int) -> int:
+    return int(load().zs_grouped_matmul_dw_workspace_bytes(DTYPES[dtype], M, K, N, G))
+
+
+def zs_grouped_matmul_dw(dy: torch.Tensor, x: torch.Tensor, row_ptr: torch.Tensor, perm: torch.Tensor | None = None,
+                         out=None, workspace=None, stream=None) -> torch.Tensor:
+    """dw[g] = sum over the rows of group g of dy[i] x[i]^T: the gradient of
+    zs_grouped_matmul in w, (G, N, K) with G = row_ptr.numel() - 1."""
+    M = _rows(x, "x")
+    K, N, G = x.shape[1], dy.shape[-1], row_ptr.numel() - 1
+    d = _dtype(x, "x")
+    x_ld = _matrix(x, "x", x.dtype, M, K)
+    dy_ld = _matrix(dy, "dy", x.dtype, M, N)
+    _need(row_ptr, "row_ptr", torch.int32, (G + 1,))
+    if perm is not None:
+        _need(perm, "perm", torch.int32, (M,))
+    if out is None:
+        out = torch.empty((G, N, K), dtype=x.dtype, device=x.device)
+    _need(out, "out", x.dtype, (G, N, K))
+    if workspace is None:
+        workspace = _workspace(load().zs_grouped_matmul_dw_workspace_bytes(d, M, K, N, G), x.device)
+    wbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check("zs_grouped_matmul_dw", load().zs_grouped_matmul_dw(d, _ptr(dy), dy_ld, _ptr(x), x_ld, row_ptr.data_ptr(),
+                                                               _ptr(perm), M, K, N, G, _ptr(out), _ptr(workspace), wbytes,
+                                                               _stream(stream)))
+    return out
+
+
+def zs_grouped_matmul_backward(dy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, row_ptr: torch.Tensor,
+                               perm: torch.Tensor | None = None, stream=None):
+    """Both gradients of zs_grouped_matmul: (dx (M, K), dw (G, N, K))."""
+    return (zs_grouped_matmul_dx(dy, w, row_ptr, perm, stream=stream),
+            zs_grouped_matmul_dw(dy, x, row_ptr, perm, stream=stream))
+
+
+def _norm_operands(h, x, gate, w_post, scale, w_pre, kind):
+    """Checks the operands of the residual norms; returns (dtype, kind, M, C, the
+    arguments h..w_pre of the C call)."""
+    M = _rows(h, "h")
+    C = h.shape[1]
+    d = _dtype(h, "h")
+    if kind not in NORM_KINDS:
+        raise ValueError(f"kind must be one of {sorted(NORM_KINDS)}, got {kind!r}")
+    h_ld = _matrix(h, "h", h.dtype, M, C)
+    x_ld = _matrix(x, "x", h.dtype, M, C)
+    gate_ptr, gate_ld, gate_cols = None, 0, 0
+    if gate is not None:
+        if gate.dim() != 2 or gate.shape[1] not in (1, C):
+            raise ValueError(f"gate must have shape {(M, C)} or {(M, 1)}, got {tuple(gate.shape)}")
+        gate_cols = gate.shape[1]
+        gate_ld = _matrix(gate, "gate", h.dtype, M, gate_cols)
+        gate_ptr = _ptr(gate)
+    for t, name in ((w_post, "w_post"), (scale, "scale"), (w_pre, "w_pre")):
+        _need(t, name, torch.float32, (C,))
+    return d, NORM_KINDS[kind], M, C, (_ptr(h), h_ld, _ptr(x), x_ld, gate_ptr, gate_ld, gate_cols, w_post.data_ptr(),
+                                       scale.data_ptr(), w_pre.data_ptr())
+
+
+def zs_norm_gate_residual(h: torch.Tensor, x: torch.Tensor, gate: torch.Tensor | None, w_post: torch.Tensor,
+                          scale: torch.Tensor, w_pre: torch.Tensor, eps: float = 1e-6, kind: str = "rms",
+                          want_stats: bool = True, stream=None):
+    """y = x + scale * sigmoid(gate) * (norm(h) * w_post), u = norm(y) * w_pre.
+
+    h, x (M, C) float32, bfloat16 or float16 (row-strided views allowed), gate the
+    same, (M, 1), or None; w_post, scale, w_pre (C,) float32; kind "rms" or "layer".
+    Returns (y, u, stats): stats (M, 4) float32 is what the backward reads (None
+    when want_stats is False)."""
+    d, k, M, C, args = _norm_operands(h, x, gate, w_post, scale, w_pre, kind)
+    y = torch.empty((M, C), dtype=h.dtype, device=h.device)
+    u = torch.empty_like(y)
+    stats = torch.empty((M, 4), dtype=torch.float32, device=h.device) if want_stats else None
+    _check("zs_norm_gate_residual", load().zs_norm_gate_residual(d, k, *args, eps, M, C, _ptr(y), _ptr(u), _ptr(stats),
+                                                                 _stream(stream)))
+    return y, u, stats
+
+
+def zs_norm_gate_residual_backward(dy: torch.Tensor | None, du: torch.Tensor | None, h: torch.Tensor, x: torch.Tensor,
+                                   gate: torch.Tensor | None, w_post: torch.Tensor, scale: torch.Tensor,
+                                   w_pre: torch.Tensor, stats: torch.Tensor, kind: str = "rms", stream=None):
+    """Gradients of zs_norm_gate_residual for the cotangents dy of y and du of u (None:
+    zeros): (dh, dx, dgate, dw_post, dscale, dw_pre); dgate is None without a gate."""
+    d, k, M, C, args = _norm_operands(h, x, gate, w_post, scale, w_pre, kind)
+    dy_ld = 0 if dy is None else _matrix(dy, "dy", h.dtype, M, C)
+    du_ld = 0 if du is None else _matrix(du, "du", h.dtype, M, C)
+    _need(stats, "stats", torch.float32, (M, 4))
+    dh = torch.empty((M, C), dtype=h.dtype, device=h.device)
+    dx = torch.empty_like(dh)
+    dgate = None if gate is None else torch.empty(gate.shape, dtype=h.dtype, device=h.device)
+    sums = torch.empty((3, C), dtype=torch.float32, device=h.device)
+    need = load().zs_norm_gate_residual_backward_workspace_bytes(M, C)
+    workspace = _workspace(need, h.device)
+    base = sums.data_ptr()
+    _check("zs_norm_gate_residual_backward", load().zs_norm_gate_residual_backward(
+        d, k, _ptr(dy), dy_ld, _ptr(du), du_ld, *args, _ptr(stats), M, C, _ptr(dh), _ptr(dx), _ptr(dgate), base,
+        base + 4 * C, base + 8 * C, _ptr(workspace), need, _stream(stream)))
+    return dh, dx, dgate, sums[0], sums[1], sums[2]
+
+
+class _AdamWTensor(ctypes.Structure):
+    _fields_ = [("param", ctypes.c_void_p), ("grad", ctypes.c_void_p), ("exp_avg", ctypes.c_void_p),
+                ("exp_avg_sq", ctypes.c_void_p), ("exp_avg_scale", ctypes.c_void_p),
+                ("exp_avg_sq_scale", ctypes.c_void_p), ("numel", ctypes.c_int64)]
+
+
+class _AdamWHyper(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("weight_decay", ctypes.c_double), ("step", ctypes.c_int64)]
+
+
+class AdamWPlan:
+    """The tensors of an AdamW step, checked once: lists of parameters, gradients and
+    states, on one device, every parameter and gradient of one type.
+
+    32-bit states: exp_avg and exp_avg_sq float32 of the parameters' sizes.  8-bit
+    states: torch.float8_e4m3fn of the parameters' sizes (exp_avg_sq holds the root of
+    the second moment), with exp_avg_scale and exp_avg_sq_scale float32 of
+    ceil(numel / 256) elements each.  Every tensor is contiguous and is held by the
+    plan; ``zs_adamw_step`` updates them in place.  ``set_grads`` puts other gradient
+    tensors (of the same sizes) in place of the plan's."""
+
+    def __init__(self, params, grads, exp_avg, exp_avg_sq, exp_avg_scale=None, exp_avg_sq_scale=None):
+        self.params, self.exp_avg, self.exp_avg_sq = list(params), list(exp_avg), list(exp_avg_sq)
+        n = len(self.params)
+        if not n:
+            raise ValueError("a plan needs at least one parameter")
+        if (exp_avg_scale is None) != (exp_avg_sq_scale is None):
+            raise ValueError("8-bit states take both lists of scales, 32-bit states none")
+        self.state_bits = 32 if exp_avg_scale is None else 8
+        self.scales = [] if exp_avg_scale is None else [list(exp_avg_scale), list(exp_avg_sq_scale)]
+        self.dtype = _dtype(self.params[0], "params[0]")
+        self.device = self.params[0].device
+        self._table = (_AdamWTensor * n)()
+        state_dtype = torch.float32 if self.state_bits == 32 else torch.float8_e4m3fn
+        for lst, name in ((self.exp_avg, "exp_avg"), (self.exp_avg_sq, "exp_avg_sq"),
+                          *zip(self.scales, ("exp_avg_scale", "exp_avg_sq_scale"))):
+            if len(lst) != n:
+                raise ValueError(f"{name} has {len(lst)} tensors, params {n}")
+        for i, p in enumerate(self.params):
+            e = self._table[i]
+            self._one(p, f"params[{i}]", self.params[0].dtype, p.shape)
+            self._one(self.exp_avg[i], f"exp_avg[{i}]", state_dtype, p.shape)
+            self._one(self.exp_avg_sq[i], f"exp_avg_sq[{i}]", state_dtype, p.shape)
+            e.param, e.exp_avg, e.exp_avg_sq = _ptr(p), _ptr(self.exp_avg[i]), _ptr(self.exp_avg_sq[i])
+            e.numel = p.numel()
+            if self.scales:
+                for lst, name in zip(self.scales, ("exp_avg_scale", "exp_avg_sq_scale")):
+                    self._one(lst[i], f"{name}[{i}]", torch.float32, (-(-p.numel() // ADAMW_BLOCK),))
+                    setattr(e, name, _ptr(lst[i]))
+        self._hyper = _AdamWHyper()
+        self.set_grads(grads)
+
+    def _one(self, t, name, dtype, shape):
+        _need(t, name, dtype, tuple(shape))
+        if t.device != self.device:
+            raise ValueError(f"{name} is on {t.device}, the plan on {self.device}")
+
+    def set_grads(self, grads) -> None:
+        grads = list(grads)
+        if len(grads) != len(self.params):
+            raise ValueError(f"grads has {len(grads)} tensors, params {len(self.params)}")
+        for i, (g, p) in enumerate(zip(grads, self.params)):
+            self._one(g, f"grads[{i}]", p.dtype, p.shape)
+        for i, g in enumerate(grads):
+            self._table[i].grad = _ptr(g)
+        self.grads = grads
+
+
+def zs_adamw_step(plan: AdamWPlan, step: int, lr: float, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,
+                  weight_decay: float = 0.01, grad_scale: torch.Tensor | None = None, stream=None) -> None:
+    """One AdamW step (number ``step``, from 1) over the plan's tensors, in place.
+    grad_scale: one float32 element on the device that multiplies every gradient."""
+    if grad_scale is not None:
+        if grad_scale.numel() != 1 or grad_scale.dtype != torch.float32 or grad_scale.device != plan.device:
+            raise ValueError(f"grad_scale must be one float32 element on {plan.device}")
+    h = plan._hyper
+    h.lr, h.beta1, h.beta2, h.eps, h.weight_decay, h.step = lr, beta1, beta2, eps, weight_decay, step
+    _check("zs_adamw_step", load().zs_adamw_step(ctypes.addressof(plan._table), len(plan.params), plan.dtype,
+                                                 plan.state_bits, ctypes.addressof(h), _ptr(grad_scale),
+                                                 _stream(stream)))

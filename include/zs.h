@@ -318,6 +318,164 @@ ZS_API zs_status zs_check_timeouts(void);
  */
 ZS_API zs_status zs_selftest_bounded_wait(uint32_t max_spins, zs_stream_t stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * Training operators of a species-resolved update block: products grouped by
+ * a CSR, residual norms with a gate, and the AdamW step.  The pages have no
+ * counterpart.  The conventions at the top hold for them too (device
+ * pointers, caller-owned memory, asynchronous, bitwise deterministic), except
+ * that their operands may be 16-bit, as each dtype argument says; every sum
+ * is formed in 32 bits and each result rounded once.
+ */
+typedef enum zs_dtype {
+    ZS_F32 = 0,
+    ZS_BF16 = 1,
+    ZS_F16 = 2
+} zs_dtype;
+
+/*
+ * Matrix products grouped by a CSR over rows: with (row_ptr, perm) the CSR
+ * zs_build_csr gives for the group of each row (its species, or species and
+ * degree), g(i) the group of row i,
+ *   y[i,:] = w[g(i)] x[i,:]        y[i,n] = sum_k w[g(i),n,k] * x[i,k]
+ * Rows stay in their own order; the gather and the scatter happen inside.
+ *   dtype            zs_dtype of x, w and y (one type for all three)
+ *   x (M, K)         rows x_ld elements apart (x_ld >= K)
+ *   w (G, N, K)      contiguous
+ *   row_ptr (G+1,)   group g owns positions [row_ptr[g], row_ptr[g+1])
+ *   perm (M,)        row at each position; NULL: position p is row p
+ *   y (M, N)         rows y_ld elements apart (y_ld >= N), fully written:
+ *                    rows at positions >= row_ptr[G] (no group) are zeros
+ * M < 2^31, any K >= 1, N >= 1, G >= 0.  Values outside a row's own group
+ * never reach its result.
+ */
+ZS_API zs_status zs_grouped_matmul(int32_t dtype, const void* x, int64_t x_ld, const void* w,
+                                   const int32_t* row_ptr, const int32_t* perm,
+                                   int64_t M, int32_t K, int32_t N, int32_t G,
+                                   void* y, int64_t y_ld, zs_stream_t stream);
+
+/*
+ * Gradient of zs_grouped_matmul in x:  dx[i,:] = w[g(i)]^T dy[i,:].
+ *   dy (M, N) rows dy_ld apart, dx (M, K) rows dx_ld apart, fully written
+ *   (rows of no group are zeros).  Other arguments as above.
+ */
+ZS_API zs_status zs_grouped_matmul_dx(int32_t dtype, const void* dy, int64_t dy_ld, const void* w,
+                                      const int32_t* row_ptr, const int32_t* perm,
+                                      int64_t M, int32_t K, int32_t N, int32_t G,
+                                      void* dx, int64_t dx_ld, zs_stream_t stream);
+
+/*
+ * Gradient of zs_grouped_matmul in w:  dw[g] = sum over rows i of group g of
+ * dy[i,:]^T x[i,:].
+ *   dw (G, N, K)  contiguous, of the operands' type, fully written (a group
+ *                 without rows gets zeros)
+ *   workspace     zs_grouped_matmul_dw_workspace_bytes(dtype, M, K, N, G)
+ *                 bytes, 256-byte aligned; its contents need not start at zero
+ */
+ZS_API size_t zs_grouped_matmul_dw_workspace_bytes(int32_t dtype, int64_t M, int32_t K, int32_t N, int32_t G);
+ZS_API zs_status zs_grouped_matmul_dw(int32_t dtype, const void* dy, int64_t dy_ld, const void* x, int64_t x_ld,
+                                      const int32_t* row_ptr, const int32_t* perm,
+                                      int64_t M, int32_t K, int32_t N, int32_t G,
+                                      void* dw, void* workspace, size_t workspace_bytes, zs_stream_t stream);
+
+/* Row norms: v / sqrt(mean(v^2) + eps), or the same of v - mean(v). */
+typedef enum zs_norm_kind {
+    ZS_NORM_RMS = 0,
+    ZS_NORM_LAYER = 1
+} zs_norm_kind;
+
+/*
+ * The norms around a block fused with its gate, residual scale and residual
+ * sum: with q = sigmoid(gate) (1 without a gate),
+ *   y = x + scale * q * (norm(h) * w_post)      the residual stream
+ *   u = norm(y) * w_pre                         the next block's input
+ * y enters its norm unrounded.
+ *   dtype        zs_dtype of h, x, gate, y and u
+ *   h, x (M, C)  rows h_ld, x_ld elements apart
+ *   gate         (M, gate_cols), rows gate_ld apart; gate_cols is C (a gate
+ *                for each channel), 1 (one for each row) or, with gate NULL, 0
+ *   w_post, scale, w_pre (C,)  fp32
+ *   y, u (M, C)  contiguous, fully written
+ *   stats (M, 4) fp32, may be NULL: mean and 1/root of h, then of y (means 0
+ *                for ZS_NORM_RMS); what the backward reads; 16-byte aligned
+ * 1 <= C <= 16384 (else ZS_ERR_UNSUPPORTED), eps >= 0.
+ */
+ZS_API zs_status zs_norm_gate_residual(int32_t dtype, int32_t kind, const void* h, int64_t h_ld,
+                                       const void* x, int64_t x_ld, const void* gate, int64_t gate_ld,
+                                       int32_t gate_cols, const float* w_post, const float* scale,
+                                       const float* w_pre, float eps, int64_t M, int32_t C,
+                                       void* y, void* u, float* stats, zs_stream_t stream);
+
+/*
+ * Backward of zs_norm_gate_residual for the cotangents dy of y and du of u
+ * (either may be NULL: zeros).
+ *   dh, dx (M, C)  contiguous; dgate (M, gate_cols) contiguous, NULL without
+ *                  a gate; all of the operands' type
+ *   dw_post, dscale, dw_pre (C,)  fp32
+ *   workspace      zs_norm_gate_residual_backward_workspace_bytes(M, C)
+ *                  bytes, 256-byte aligned
+ * Every output is fully written (M = 0 gives zero dw_post, dscale, dw_pre).
+ */
+ZS_API size_t zs_norm_gate_residual_backward_workspace_bytes(int64_t M, int32_t C);
+ZS_API zs_status zs_norm_gate_residual_backward(int32_t dtype, int32_t kind, const void* dy, int64_t dy_ld,
+                                                const void* du, int64_t du_ld, const void* h, int64_t h_ld,
+                                                const void* x, int64_t x_ld, const void* gate, int64_t gate_ld,
+                                                int32_t gate_cols, const float* w_post, const float* scale,
+                                                const float* w_pre, const float* stats, int64_t M, int32_t C,
+                                                void* dh, void* dx, void* dgate, float* dw_post, float* dscale,
+                                                float* dw_pre, void* workspace, size_t workspace_bytes,
+                                                zs_stream_t stream);
+
+/*
+ * One tensor of an AdamW step: numel contiguous elements of each array.
+ * With 32-bit states exp_avg and exp_avg_sq are fp32 and the scales unused.
+ * With 8-bit states they hold e4m3 codes, with one fp32 scale for each block
+ * of 256 elements (the last one may be short): exp_avg the first moment,
+ * exp_avg_sq the square root of the second.
+ */
+typedef struct zs_adamw_tensor {
+    void* param;
+    const void* grad;
+    void* exp_avg;
+    void* exp_avg_sq;
+    float* exp_avg_scale;
+    float* exp_avg_sq_scale;
+    int64_t numel;
+} zs_adamw_tensor;
+
+typedef struct zs_adamw_hyper {
+    double lr, beta1, beta2, eps, weight_decay;
+    int64_t step;   /* 1 for the first step */
+} zs_adamw_hyper;
+
+/*
+ * One AdamW step over many tensors, in place.  For every element, in fp32
+ * with each operation rounded once, in this order:
+ *   g = grad * grad_scale
+ *   m = beta1 * m + (1 - beta1) * g
+ *   v = beta2 * v + (1 - beta2) * (g * g)
+ *   p = p * (1 - lr * weight_decay)
+ *       - (lr / (1 - beta1^step)) * (m / (sqrt(v) * (1 / sqrt(1 - beta2^step)) + eps))
+ * (the constants are formed in 64 bits and rounded once), p rounded to the
+ * parameter's type.  8-bit states read m = code * scale, and sqrt(v) = code *
+ * scale squared; they are written with scale = top / 448, top the largest
+ * finite magnitude in the block, code the e4m3 value nearest to the value
+ * times (1 / top) * 448 (ties to even); a positive root is held as at least
+ * the smallest positive code, so that a held first moment never meets a zero
+ * denominator; a value that is not finite is held as NaN and leaves the rest
+ * of its block alone; a block whose top is below 1e-30 is held as zeros.
+ *   tensors      HOST array of `count` entries; read before the call returns
+ *   dtype        zs_dtype of the parameters and gradients (every tensor)
+ *   state_bits   32 or 8 (every tensor)
+ *   hyper        host; step >= 1, 0 <= beta < 1, eps >= 0
+ *   grad_scale   (1,) fp32 on the device, may be NULL (1): the reciprocal of a
+ *                loss scale, a clipping factor
+ * The arrays of one call must not overlap.  Tensors of any element alignment;
+ * 16-byte aligned ones take wide loads.
+ */
+ZS_API zs_status zs_adamw_step(const zs_adamw_tensor* tensors, int32_t count, int32_t dtype, int32_t state_bits,
+                               const zs_adamw_hyper* hyper, const float* grad_scale, zs_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

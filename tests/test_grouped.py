@@ -1,0 +1,334 @@
+"""Products grouped by a CSR, against the plain implementation in 64 bits.
+
+Tolerance, fixed before the first run: a product of n terms summed in fp32
+(in any order, each addition off by at most an ulp) is off by at most
+n 2^-23 sum|terms|, typically sqrt(n) 2^-24 sum|terms|; 1e-5 sum|terms| holds
+for the lengths here, as for the zonal scatter.  The one rounding to the
+output's type adds half an ulp of the result."""
+import numpy as np
+import pytest
+import torch
+
+from equivariant_interatomic_potential_gb300 import zs
+from train_refs import HALF_ULP, STEP, TORCH, csr, f64, grouped, held
+
+INVALID, UNSUPPORTED = 1, 2
+FAKE = 1 << 20
+TOL = 1e-5
+
+
+def close(got, ref, absum, dtype, what):
+    got = f64(got)
+    assert got.shape == ref.shape, what
+    bound = TOL * absum + HALF_ULP[dtype] * (1 + 1e-3) * np.abs(ref) + STEP[dtype]
+    bad = ~(np.abs(got - ref) <= bound)
+    assert not bad.any(), f"{what}: {bad.sum()} of {bad.size} off, worst {np.nanmax(np.abs(got - ref) / bound):.2f} x the bound"
+
+
+def draw(M, K, N, G, dtype, seed, sizes="uniform", bad=0.0):
+    rng = np.random.default_rng(seed)
+    if sizes == "zipf":
+        p = (np.arange(G) + 1.0) ** -1.5
+        group = rng.permutation(G)[rng.choice(G, M, p=p / p.sum())]
+    elif sizes == "one":
+        group = np.full(M, G // 2)
+    else:
+        group = rng.integers(0, max(G, 1), M)
+    if bad:
+        group = np.where(rng.random(M) < bad, G + 3, group)
+    x, xd = held(rng.standard_normal((M, K)), dtype)
+    w, wd = held(rng.standard_normal((G, N, K)) / np.sqrt(K), dtype)
+    dy, dyd = held(rng.standard_normal((M, N)), dtype)
+    return group, (x, w, dy), (xd, wd, dyd)
+
+
+def run(group, G, x, w, dy, ordered=False):
+    row_ptr, perm = csr(group, G)
+    rp, pm = torch.from_numpy(row_ptr).cuda(), None if ordered else torch.from_numpy(perm).cuda()
+    y = zs.zs_grouped_matmul(x, w, rp, pm)
+    dx, dw = zs.zs_grouped_matmul_backward(dy, x, w, rp, pm)
+    torch.cuda.synchronize()
+    zs.zs_check_timeouts()
+    return y, dx, dw
+
+
+def check_all(group, t, d, dtype, ordered=False):
+    y, dx, dw = run(group, t[1].shape[0], *(a.cuda() for a in t), ordered=ordered)
+    ry, ay, rdx, adx, rdw, adw = grouped(d[0], d[1], group, d[2])
+    close(y, ry, ay, dtype, "y")
+    close(dx, rdx, adx, dtype, "dx")
+    close(dw, rdw, adw, dtype, "dw")
+    return y, dx, dw
+
+
+SHAPES = [
+    (1, 32, 32, 1), (1, 1, 1, 1), (64, 32, 32, 4), (127, 32, 32, 5), (128, 64, 64, 1), (129, 64, 128, 3),
+    (300, 48, 80, 7), (1000, 256, 256, 3), (513, 8, 520, 9), (700, 520, 8, 2), (257, 72, 264, 4),
+    (400, 33, 65, 6), (333, 187, 301, 11), (50, 1, 300, 3), (50, 300, 1, 3), (2000, 7, 5, 40), (90, 130, 96, 120),
+    (4100, 128, 384, 2), (260, 1100, 200, 2), (640, 200, 1030, 2),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("M,K,N,G", SHAPES)
+def test_products_and_gradients(M, K, N, G, dtype):
+    check_all(*draw(M, K, N, G, dtype, seed=M + 3 * K + 5 * N + G, sizes="zipf", bad=0.1 if M > 10 else 0.0), dtype)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("sizes", ["uniform", "one"])
+def test_rows_in_order(sizes, dtype):
+    # perm None: position p is row p; with every row in one group most groups are empty
+    group, t, d = draw(1500, 96, 160, 8, dtype, 3, sizes)
+    group = np.sort(group)
+    check_all(group, t, d, dtype, ordered=True)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f32", "f16"])
+def test_no_rows_no_groups(dtype):
+    dt = TORCH[dtype]
+    e = lambda *s: torch.full(s, 7.0, dtype=dt, device="cuda")  # noqa: E731
+    rp = torch.zeros(4, dtype=torch.int32, device="cuda")
+    y = zs.zs_grouped_matmul(e(0, 32), e(3, 48, 32), rp)
+    dx, dw = zs.zs_grouped_matmul_backward(e(0, 48), e(0, 32), e(3, 48, 32), rp)
+    assert y.shape == (0, 48) and dx.shape == (0, 32) and dw.shape == (3, 48, 32) and bool((dw == 0).all())
+    # no group at all, and no row in any group: every row is zero
+    for G in (0, 3):
+        y = zs.zs_grouped_matmul(e(70, 32), e(G, 48, 32), rp[:G + 1].contiguous())
+        dx, dw = zs.zs_grouped_matmul_backward(e(70, 48), e(70, 32), e(G, 48, 32), rp[:G + 1].contiguous())
+        assert bool((y == 0).all()) and bool((dx == 0).all()) and bool((dw == 0).all()) and dw.shape == (G, 48, 32)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("K,N", [(64, 64), (36, 44)])
+def test_values_stay_in_their_group(K, N, dtype):
+    # a row, or a group's weights, of NaN and infinities reach nothing beyond the row, or its group
+    M, G = 900, 5
+    group, t, d = draw(M, K, N, G, dtype, 9)
+    x, w, dy = (a.clone() for a in t)
+    sick = int(np.flatnonzero(group == 1)[3])
+    x[sick, 0::2], x[sick, 1::2] = float("nan"), float("inf")
+    dy[sick] = float("-inf")
+    w[3] = float("nan")
+    y, dx, dw = run(group, G, x.cuda(), w.cuda(), dy.cuda())
+    ry, ay, rdx, adx, rdw, adw = grouped(d[0], d[1], group, d[2])
+    keep = (np.arange(M) != sick) & (group != 3)
+    close(y[keep], ry[keep], ay[keep], dtype, "y")
+    close(dx[keep], rdx[keep], adx[keep], dtype, "dx")
+    clean = np.arange(G) != 1
+    close(dw[clean], rdw[clean], adw[clean], dtype, "dw")
+    assert not bool(torch.isfinite(y[sick]).any()) and not bool(torch.isfinite(dw[1]).any())
+    assert bool(torch.isnan(y[torch.from_numpy(group == 3).cuda()]).all())
+
+
+@pytest.mark.gpu
+def test_rows_of_no_group_are_not_read():
+    # rows outside every group may hold anything; their results are zeros, and neighbours keep theirs
+    group, t, d = draw(700, 64, 64, 4, "bf16", 21, bad=0.3)
+    none = group >= 4
+    x, w, dy = (a.clone() for a in t)
+    x[torch.from_numpy(none)] = float("nan")
+    dy[torch.from_numpy(none)] = float("inf")
+    y, dx, dw = run(group, 4, x.cuda(), w.cuda(), dy.cuda())
+    ry, ay, rdx, adx, rdw, adw = grouped(d[0], d[1], group, d[2])
+    close(y, ry, ay, "bf16", "y")
+    close(dx, rdx, adx, "bf16", "dx")
+    close(dw, rdw, adw, "bf16", "dw")
+    assert bool((y[torch.from_numpy(none).cuda()] == 0).all())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("pad,shift", [(0, 0), (8, 0), (8, 8), (3, 1), (24, 4)])
+def test_row_strides_and_alignment(pad, shift, dtype):
+    # x, dy and the results as column ranges of wider matrices, at any element offset; what lies around stays
+    M, K, N, G = 517, 64, 96, 3
+    group, (x, w, dy), d = draw(M, K, N, G, dtype, 5)
+    row_ptr, perm = (torch.from_numpy(a).cuda() for a in csr(group, G))
+
+    def wide(a):
+        base = torch.full((a.shape[0], a.shape[1] + pad + shift), 9.0, dtype=a.dtype, device="cuda")
+        view = base[:, shift:shift + a.shape[1]]
+        view.copy_(a.cuda())
+        return base, view
+
+    xv, dyv, wc = wide(x)[1], wide(dy)[1], w.cuda()
+    (yb, yv), (dxb, dxv) = wide(torch.zeros(M, N, dtype=x.dtype)), wide(torch.zeros(M, K, dtype=x.dtype))
+    zs.zs_grouped_matmul(xv, wc, row_ptr, perm, out=yv)
+    zs.zs_grouped_matmul_dx(dyv, wc, row_ptr, perm, out=dxv)
+    dw = zs.zs_grouped_matmul_dw(dyv, xv, row_ptr, perm)
+    ry, ay, rdx, adx, rdw, adw = grouped(d[0], d[1], group, d[2])
+    close(yv, ry, ay, dtype, "y")
+    close(dxv, rdx, adx, dtype, "dx")
+    close(dw, rdw, adw, dtype, "dw")
+    for base, cols in ((yb, N), (dxb, K)):
+        around = torch.ones(base.shape[1], dtype=torch.bool)
+        around[shift:shift + cols] = False
+        assert bool((base[:, around.cuda()] == 9.0).all())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_weights_at_any_alignment(dtype):
+    group, (x, w, dy), d = draw(300, 40, 56, 3, dtype, 12)
+    row_ptr, perm = (torch.from_numpy(a).cuda() for a in csr(group, 3))
+    flat = torch.zeros(w.numel() + 1, dtype=w.dtype, device="cuda")
+    wv = flat[1:].view(w.shape)
+    wv.copy_(w.cuda())
+    dwf = torch.full((w.numel() + 2,), 9.0, dtype=w.dtype, device="cuda")
+    dwv = dwf[1:-1].view(w.shape)
+    ry, ay, rdx, adx, rdw, adw = grouped(d[0], d[1], group, d[2])
+    close(zs.zs_grouped_matmul(x.cuda(), wv, row_ptr, perm), ry, ay, dtype, "y")
+    close(zs.zs_grouped_matmul_dx(dy.cuda(), wv, row_ptr, perm), rdx, adx, dtype, "dx")
+    zs.zs_grouped_matmul_dw(dy.cuda(), x.cuda(), row_ptr, perm, out=dwv)
+    close(dwv, rdw, adw, dtype, "dw")
+    assert float(dwf[0]) == 9.0 and float(dwf[-1]) == 9.0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+def test_run_to_run_bits(dtype):
+    group, t, _ = draw(5000, 96, 64, 5, dtype, 17, "zipf")
+    t = [a.cuda() for a in t]
+    first = run(group, 5, *t)
+    for _ in range(5):
+        assert all(torch.equal(a, b) for a, b in zip(run(group, 5, *t), first))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,scale", [("f32", 1e30), ("f32", 1e-30), ("bf16", 1e30)])
+def test_large_and_small_magnitudes(dtype, scale):
+    # products stay within fp32's range although an operand is near its ends
+    group, (x, w, dy), _ = draw(200, 64, 32, 3, dtype, 8)
+    x, xd = held(x.float().numpy() * scale, dtype)
+    wd, dyd = f64(w), f64(dy)
+    y, dx, dw = run(group, 3, x.cuda(), w.cuda(), dy.cuda())
+    ry, ay, rdx, adx, rdw, adw = grouped(xd, wd, group, dyd)
+    close(y, ry, ay, dtype, "y")
+    close(dw, rdw, adw, dtype, "dw")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_skewed_and_long_sums(dtype):
+    # one group holds nearly every row: its weight gradient is one sum of many thousand terms
+    rng = np.random.default_rng(2)
+    M, K, N, G = 60000, 32, 48, 6
+    group = np.where(rng.random(M) < 0.97, 4, rng.integers(0, G, M))
+    x, xd = held(rng.standard_normal((M, K)), dtype)
+    w, wd = held(rng.standard_normal((G, N, K)), dtype)
+    dy, dyd = held(rng.standard_normal((M, N)), dtype)
+    check_all(group, (x, w, dy), (xd, wd, dyd), dtype)
+
+
+@pytest.mark.gpu
+def test_side_stream_and_graph():
+    group, t, d = draw(800, 64, 64, 4, "bf16", 30)
+    x, w, dy = (a.cuda() for a in t)
+    row_ptr, perm = (torch.from_numpy(a).cuda() for a in csr(group, 4))
+    run(group, 4, x, w, dy)
+    graph, s = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s), torch.cuda.graph(graph, stream=s):
+        y = zs.zs_grouped_matmul(x, w, row_ptr, perm)
+        dx, dw = zs.zs_grouped_matmul_backward(dy, x, w, row_ptr, perm)
+    torch.cuda.synchronize()
+    for seed in (31, 32):
+        group, t2, d2 = draw(800, 64, 64, 4, "bf16", seed)
+        rp, pm = csr(group, 4)
+        for a, b in ((x, t2[0]), (w, t2[1]), (dy, t2[2]), (row_ptr, torch.from_numpy(rp)), (perm, torch.from_numpy(pm))):
+            a.copy_(b)
+        graph.replay()
+        torch.cuda.synchronize()
+        ry, ay, rdx, adx, rdw, adw = grouped(d2[0], d2[1], group, d2[2])
+        close(y, ry, ay, "bf16", "y")
+        close(dx, rdx, adx, "bf16", "dx")
+        close(dw, rdw, adw, "bf16", "dw")
+
+
+@pytest.mark.gpu
+def test_gradients_against_differences():
+    # y is linear in x and in w, so central differences have no truncation error
+    group, t, _ = draw(400, 48, 40, 3, "f32", 6, bad=0.1)
+    x, w, dy = (a.cuda() for a in t)
+    row_ptr, perm = (torch.from_numpy(a).cuda() for a in csr(group, 3))
+    dx, dw = zs.zs_grouped_matmul_backward(dy, x, w, row_ptr, perm)
+    loss = lambda a, b: (zs.zs_grouped_matmul(a, b, row_ptr, perm).double() * dy.double()).sum()  # noqa: E731
+    for grad, at, call in ((dx, x, lambda e: loss(x + e, w)), (dw, w, lambda e: loss(x, w + e))):
+        v = torch.randn_like(at)
+        slope = (call(v) - call(-v)) / 2
+        want = (grad.double() * v.double()).sum()
+        # fp32 rounding of about 1e-6 in each of the 16000 terms of the loss
+        assert abs(float(slope - want)) <= 1e-5 * float((grad.double() * v.double()).abs().sum())
+
+
+def test_reference_gradients_against_differences():
+    rng = np.random.default_rng(0)
+    x, w, dy = rng.standard_normal((9, 4)), rng.standard_normal((3, 5, 4)), rng.standard_normal((9, 5))
+    group = np.array([0, 2, 2, 0, 7, 0, 2, 0, 2])
+    _, _, dx, _, dw, _ = grouped(x, w, group, dy)
+    for at, grad in ((x, dx), (w, dw)):
+        for i in np.ndindex(at.shape):
+            old, e = at[i], 0.5
+            at[i] = old + e
+            up = (grouped(x, w, group)[0] * dy).sum()
+            at[i] = old - e
+            down = (grouped(x, w, group)[0] * dy).sum()
+            at[i] = old
+            assert abs((up - down) / (2 * e) - grad[i]) < 1e-12
+    assert not dw[1].any() and not dx[4].any()
+
+
+def test_argument_checks():
+    lib = zs.load()
+    ok = dict(dtype=0, x=FAKE, x_ld=32, w=FAKE, rp=FAKE, perm=FAKE, M=10, K=32, N=48, G=3, y=FAKE, y_ld=48)
+
+    def fwd(**kw):
+        a = {**ok, **kw}
+        return lib.zs_grouped_matmul(a["dtype"], a["x"], a["x_ld"], a["w"], a["rp"], a["perm"], a["M"], a["K"], a["N"],
+                                     a["G"], a["y"], a["y_ld"], None)
+
+    def dx(**kw):
+        a = {**ok, "x_ld": 48, "y_ld": 32, **kw}
+        return lib.zs_grouped_matmul_dx(a["dtype"], a["x"], a["x_ld"], a["w"], a["rp"], a["perm"], a["M"], a["K"], a["N"],
+                                        a["G"], a["y"], a["y_ld"], None)
+
+    for call in (fwd, dx):
+        assert call(dtype=3) == UNSUPPORTED and b"dtype" in lib.zs_last_error()
+        for kw in (dict(M=-1), dict(M=1 << 31), dict(K=0), dict(N=0), dict(G=-1), dict(x=None), dict(w=None), dict(y=None),
+                   dict(rp=None), dict(x_ld=31), dict(y_ld=31), dict(x=FAKE + 2), dict(dtype=1, y=FAKE + 1),
+                   dict(perm=FAKE + 2)):
+            assert call(**kw) == INVALID, kw
+        assert call(M=0, x=None, y=None) == 0      # enqueues nothing
+
+    def dw(**kw):
+        a = {**ok, "ws": FAKE, "bytes": 1 << 40, **kw}
+        return lib.zs_grouped_matmul_dw(a["dtype"], a["x"], 48, a["w"], 32, a["rp"], a["perm"], a["M"], a["K"], a["N"],
+                                        a["G"], a["y"], a["ws"], a["bytes"], None)
+
+    assert dw(dtype=-1) == UNSUPPORTED
+    for kw in (dict(M=-1), dict(K=0), dict(N=-4), dict(x=None), dict(w=None), dict(y=None), dict(rp=None), dict(ws=FAKE + 8)):
+        assert dw(**kw) == INVALID, kw
+    need = lib.zs_grouped_matmul_dw_workspace_bytes(0, 10, 32, 48, 3)
+    if need:
+        assert dw(bytes=need - 1) == INVALID and dw(ws=None) == INVALID
+    assert dw(G=0, y=None, w=None, x=None) == 0
+    assert lib.zs_grouped_matmul_dw_workspace_bytes(0, -1, 32, 48, 3) == 0
+    assert lib.zs_grouped_matmul_dw_workspace_bytes(9, 10, 32, 48, 3) == 0
+
+
+def test_binding_refusals():
+    x, w = torch.zeros(4, 8), torch.zeros(2, 6, 8)
+    rp = torch.zeros(3, dtype=torch.int32)
+    with pytest.raises(ValueError, match="CUDA"):
+        zs.zs_grouped_matmul(x, w, rp)
+    with pytest.raises(ValueError, match="float32, bfloat16 or float16"):
+        zs.zs_grouped_matmul(x, w.double(), rp)
+    with pytest.raises(ValueError, match="matrix"):
+        zs.zs_grouped_matmul(x[0], w, rp)
+    with pytest.raises(ValueError, match="shape"):
+        zs.zs_grouped_matmul(x, w[0], rp)
