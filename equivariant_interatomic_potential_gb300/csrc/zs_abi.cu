@@ -2,6 +2,8 @@
 #include <stdarg.h>
 #include <stdio.h>
 
+#include <initializer_list>
+
 #include "zs_common.cuh"
 
 namespace {
@@ -28,8 +30,12 @@ zs_status check_launch(const char* what) {
 
 unsigned int take_timeouts_forward();
 unsigned int take_timeouts_backward();
+unsigned int take_timeouts_grouped_rows();
+unsigned int take_timeouts_grouped_weights();
 cudaError_t set_timeout_flag_forward(unsigned int* flag);
 cudaError_t set_timeout_flag_backward(unsigned int* flag);
+cudaError_t set_timeout_flag_grouped_rows(unsigned int* flag);
+cudaError_t set_timeout_flag_grouped_weights(unsigned int* flag);
 zs_status selftest_bounded_wait(uint32_t max_spins, cudaStream_t s);
 
 // The driver's cuCtxGetCurrent and cuCtxGetId, resolved once through the
@@ -70,11 +76,15 @@ uint64_t current_context_id() {
 extern "C" {
 
 zs_status zs_check_timeouts(void) {
-    const unsigned int f = zs::take_timeouts_forward();
-    const unsigned int b = zs::take_timeouts_backward();
-    if (f == 0xffffffffu || b == 0xffffffffu)
-        return zs::fail(ZS_ERR_CUDA, "zs_check_timeouts: %s", cudaGetErrorString(cudaGetLastError()));
-    if (f + b) return zs::fail(ZS_ERR_TIMEOUT, "zs_check_timeouts: %u bounded waits ran out", f + b);
+    unsigned int sum = 0;
+    for (auto take : {zs::take_timeouts_forward, zs::take_timeouts_backward, zs::take_timeouts_grouped_rows,
+                      zs::take_timeouts_grouped_weights}) {
+        const unsigned int v = take();
+        if (v == 0xffffffffu)
+            return zs::fail(ZS_ERR_CUDA, "zs_check_timeouts: %s", cudaGetErrorString(cudaGetLastError()));
+        sum += v;
+    }
+    if (sum) return zs::fail(ZS_ERR_TIMEOUT, "zs_check_timeouts: %u bounded waits ran out", sum);
     return ZS_OK;
 }
 
@@ -99,6 +109,8 @@ zs_status zs_set_timeout_flag(uint32_t* flag) {
     unsigned int* f = reinterpret_cast<unsigned int*>(flag);
     cudaError_t err = zs::set_timeout_flag_forward(f);
     if (err == cudaSuccess) err = zs::set_timeout_flag_backward(f);
+    if (err == cudaSuccess) err = zs::set_timeout_flag_grouped_rows(f);
+    if (err == cudaSuccess) err = zs::set_timeout_flag_grouped_weights(f);
     if (err != cudaSuccess) return zs::fail(ZS_ERR_CUDA, "zs_set_timeout_flag: %s", cudaGetErrorString(err));
     return ZS_OK;
 }
