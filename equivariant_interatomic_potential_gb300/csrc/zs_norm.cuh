@@ -1,0 +1,330 @@
+// The norms around a block fused with its gate, residual scale and residual
+// sum, and their backward:
+//   nh = norm(h), q = sigmoid(gate), a = scale * w_post
+//   y = x + q a nh,  ny = norm(y),  u = ny * w_pre
+// and for the cotangents dy, du
+//   dx = dy + norm'(du * w_pre; ny, ry),  dh = norm'(dx q a; nh, rh)
+//   dgate = dx q a nh (1 - q)
+//   dw_pre = sum_rows du ny, and with B = sum_rows dx q nh:
+//   dw_post = scale * B, dscale = w_post * B
+// with norm'(d; n, r) = r (d - mean(d n) n), minus r mean(d) for the layer
+// norm.  The backward forms y again from x, h and the gate (as many bytes as
+// reading y, and unrounded), and keeps only four floats a row.
+//
+// Bound by HBM.  A row lives in the registers of 8 to 256 threads, or of a
+// cluster of CTAs that exchange their sums through distributed shared memory,
+// each thread holding up to NV pieces of VEC elements, so that every operand
+// is read once; while a row is worked on the next one's pieces are on their
+// way.  Rows go round the CTAs of a persistent grid, whose threads keep the
+// parameters of their columns, and in the backward the running column sums,
+// in registers.
+//
+// Rows that do not start on 16-byte boundaries (odd channel counts) are still
+// read in 16-byte pieces of memory: a row's first and last piece bring some of
+// its neighbours' elements along, which count as zeros (at the two ends of
+// the matrix they go element by element, as they always do when stored).  The distance `phase` of a row's start past a
+// boundary repeats every VEC rows, so a thread that steps by a multiple of
+// VEC rows keeps its columns.  That needs all operands to be at the same
+// phase; where they are not (views at odd offsets), VEC is 1.
+#pragma once
+
+#include <initializer_list>
+
+#include "zs_types.cuh"
+
+namespace zs {
+
+constexpr int kNormMaxC = 8192;
+constexpr int kNormThreads = 256;     // of a CTA, at most
+constexpr int kNormWarps = kNormThreads / 32;
+constexpr int kNormCluster = 5;       // CTAs that share a row, at most
+constexpr int kNormCtas = 304;        // of the backward, at most: rows of the partial column sums
+
+struct NormShape {
+    int64_t M;
+    int32_t C;
+    int32_t tpr;        // threads that hold a row: 8, 16, or a multiple of 32
+    int32_t cluster;    // CTAs that hold a row (1: a CTA holds one or more rows)
+    int32_t gate_cols;  // 0, 1 or C
+    int32_t layer;      // subtract the mean
+    float eps, inv_c;
+};
+
+struct NormView {
+    const void* p;
+    int64_t ld;
+};
+
+struct NormArgs {
+    NormShape s;
+    NormView dy, du, h, x, gate;
+    const float *w_post, *scale, *w_pre;
+    const float4* stats_in;
+    void *out0, *out1, *out2;   // y, u  |  dh, dx, dgate
+    float4* stats_out;
+    float *dw_post, *dscale, *dw_pre, *partial;
+};
+
+// How a thread's columns are laid out: piece k covers the VEC columns from
+// (k * tpr + lane) * VEC - phase on.
+struct NormLane {
+    int tpr, lane, C, phase;
+};
+
+template <typename T, int VEC, int NV, bool kEdges>
+struct NormCols {
+    static constexpr int E = VEC * NV;
+    static_assert(VEC == 1 || VEC == kVec<T>, "whole 16-byte pieces or single elements");
+
+    // f(k, c0, whole): piece k starts at column c0; whole: all of it is in the row
+    template <typename F>
+    static __device__ __forceinline__ void each(const NormLane& l, F&& f) {
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int c0 = (k * l.tpr + l.lane) * VEC - (kEdges ? l.phase : 0);
+            if (c0 < l.C) f(k, c0, !kEdges || VEC == 1 || (c0 >= 0 && c0 + VEC <= l.C));
+        }
+    }
+    static __device__ __forceinline__ bool in_row(const NormLane& l, int c) {
+        return !kEdges || VEC == 1 || (unsigned)c < (unsigned)l.C;
+    }
+    // A row as it travels: raw pieces, so that loads can be issued well before use.
+    struct Raw {
+        Piece<T> v[VEC == 1 ? 1 : NV];
+        T s[VEC == 1 ? NV : 1];
+    };
+    // row r of the M rows of v
+    static __device__ __forceinline__ void load(Raw& w, const NormView& v, int64_t r, int64_t M, const NormLane& l) {
+        const T* row = static_cast<const T*>(v.p) + r * v.ld;
+        each(l, [&](int k, int c0, bool whole) {
+            if constexpr (VEC == 1) {
+                w.s[k] = row[c0];
+            } else if (whole || (r * v.ld + c0 >= 0 && c0 + VEC <= (M - 1 - r) * v.ld + l.C)) {
+                w.v[k].raw = ld_piece(row + c0);
+            } else {
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) w.v[k].e[i] = in_row(l, c0 + i) ? row[c0 + i] : from_f32<T>(0.f);
+            }
+        });
+    }
+    static __device__ __forceinline__ void open(const Raw& r, float (&f)[E], const NormLane& l) {
+#pragma unroll
+        for (int i = 0; i < E; ++i) f[i] = 0.f;
+        each(l, [&](int k, int c0, bool) {
+            if constexpr (VEC == 1) {
+                f[k] = to_f32(r.s[k]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) f[k * VEC + i] = in_row(l, c0 + i) ? to_f32(r.v[k].e[i]) : 0.f;
+            }
+        });
+    }
+    static __device__ __forceinline__ void store(T* row, const float (&f)[E], const NormLane& l) {
+        each(l, [&](int k, int c0, bool whole) {
+            if constexpr (VEC == 1) {
+                row[c0] = from_f32<T>(f[k]);
+            } else {
+                float q[VEC];
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) q[i] = f[k * VEC + i];
+                if (whole) {
+                    st_piece(row + c0, pack<T>(q));
+                } else {
+#pragma unroll
+                    for (int i = 0; i < VEC; ++i)
+                        if (in_row(l, c0 + i)) row[c0 + i] = from_f32<T>(q[i]);
+                }
+            }
+        });
+    }
+    // f[i] = g(column) for the columns of the row, 0 beyond
+    template <typename G>
+    static __device__ __forceinline__ void columns(float (&f)[E], const NormLane& l, G&& g) {
+#pragma unroll
+        for (int i = 0; i < E; ++i) f[i] = 0.f;
+        each(l, [&](int k, int c0, bool) {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i)
+                if (in_row(l, c0 + i)) f[k * VEC + i] = g(c0 + i);
+        });
+    }
+    template <typename G>
+    static __device__ __forceinline__ void for_columns(const NormLane& l, G&& g) {
+        each(l, [&](int k, int c0, bool) {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i)
+                if (in_row(l, c0 + i)) g(k * VEC + i, c0 + i);
+        });
+    }
+    // Zero outside the row, so that sums over a thread's elements need no care.
+    static __device__ __forceinline__ void clear_outside(float (&f)[E], const NormLane& l) {
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int c0 = (k * l.tpr + l.lane) * VEC - (kEdges ? l.phase : 0);
+#pragma unroll
+            for (int i = 0; i < VEC; ++i)
+                if (c0 >= l.C || !in_row(l, c0 + i)) f[k * VEC + i] = 0.f;
+        }
+    }
+};
+
+__device__ __forceinline__ void cluster_barrier() {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// Sums over the threads of a row.  Rows of up to 32 threads stay within a
+// warp.  Wider ones go through shared memory: `red` holds two rounds of a
+// float4 for each warp of each CTA of the row, taken in turn, so that one
+// barrier a round is enough: who writes a round's slots again has passed the
+// barrier of the round between.  Every thread adds them in the same order.
+struct NormSums {
+    float4 red[2][kNormCluster * kNormWarps];
+};
+template <int NQ>
+__device__ __forceinline__ void row_sum(float (&q)[NQ], const NormShape& s, NormSums& sums, int& round) {
+    static_assert(NQ <= 4, "a float4 per warp");
+    const int lim = s.tpr < 32 ? s.tpr : 32;
+    for (int o = lim >> 1; o > 0; o >>= 1) {
+#pragma unroll
+        for (int i = 0; i < NQ; ++i) q[i] += __shfl_xor_sync(0xffffffffu, q[i], o);
+    }
+    if (s.tpr <= 32) return;
+    const int warp = threadIdx.x >> 5, per_row = s.tpr >> 5;
+    float4* slot = sums.red[round & 1];
+    ++round;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    float* ve = &v.x;
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) ve[i] = q[i];
+    int first;
+    if (s.cluster == 1) {
+        first = warp / per_row * per_row;
+        if ((threadIdx.x & 31) == 0) slot[warp] = v;
+        __syncthreads();
+    } else {
+        first = 0;
+        uint32_t rank;
+        asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+        const int lane = threadIdx.x & 31;
+        if (lane < s.cluster) {   // lane i writes this warp's part to CTA i
+            const uint32_t mine = (uint32_t)__cvta_generic_to_shared(slot + rank * (blockDim.x >> 5) + warp);
+            uint32_t there;
+            asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(mine), "r"(lane));
+            asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};"
+                         :: "r"(there), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
+        }
+        cluster_barrier();
+    }
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) q[i] = 0.f;
+    for (int w = 0; w < per_row; ++w) {
+        const float4 p = slot[first + w];
+        const float* pe = &p.x;
+#pragma unroll
+        for (int i = 0; i < NQ; ++i) q[i] += pe[i];
+    }
+}
+
+// Where a thread stands: its row group within the CTA, and the persistent
+// grid's step.
+struct NormPlace {
+    int sub, rows;
+    int64_t first, step;
+    int lane;
+    int64_t group;    // of the grid: CTA or cluster
+    __device__ __forceinline__ explicit NormPlace(const NormShape& s) {
+        if (s.cluster == 1) {
+            sub = threadIdx.x / s.tpr;
+            rows = blockDim.x / s.tpr;
+            lane = threadIdx.x - sub * s.tpr;
+            group = blockIdx.x;
+            step = (int64_t)gridDim.x * rows;
+        } else {
+            sub = 0;
+            rows = 1;
+            lane = blockIdx.x % s.cluster * blockDim.x + threadIdx.x;
+            group = blockIdx.x / s.cluster;
+            step = gridDim.x / s.cluster;
+        }
+        first = group * rows;
+    }
+};
+
+__device__ __forceinline__ float sigmoid(float z) { return __frcp_rn(1.f + expf(-z)); }
+
+// How a row is spread: over as many threads as need nv pieces each, with the
+// largest nv up to `most` unless a smaller one leaves a fifth fewer slots empty.
+struct NormPlan {
+    int nv, tpr, cluster, threads, rows;
+};
+inline NormPlan norm_plan(int32_t C, int vec, bool edges, int most) {
+    const int pieces = (C + (edges ? vec - 1 : 0) + vec - 1) / vec;   // a phase may add one
+    NormPlan best = {};
+    int least = 0;
+    for (int nv = most; nv >= 1; nv /= 2) {
+        NormPlan p;
+        p.nv = nv;
+        int t = (pieces + nv - 1) / nv;
+        p.cluster = (t + kNormThreads - 1) / kNormThreads;
+        if (p.cluster > kNormCluster) continue;
+        if (t <= 32) {
+            p.tpr = t <= 8 ? 8 : t <= 16 ? 16 : 32;
+        } else {
+            t = (t + p.cluster - 1) / p.cluster;
+            p.tpr = p.cluster * ((t + 31) / 32 * 32);
+        }
+        p.rows = p.cluster > 1 ? 1 : kNormThreads / p.tpr;
+        p.threads = p.cluster > 1 ? p.tpr / p.cluster : p.rows * p.tpr;
+        if (least == 0 || p.tpr * nv * 5 < least * 4) best = p, least = p.tpr * nv;
+    }
+    return best;
+}
+// Groups of rows (CTAs, or clusters) for M rows, `most` at most: a multiple of
+// 8 where a group takes several rounds, so that its phase stays.
+inline int norm_groups(int64_t M, int rows, int most) {
+    const int64_t need = (M + rows - 1) / rows;
+    return (int)(need <= most ? need : imax(8, most / 8 * 8));
+}
+
+template <typename K>
+inline void norm_launch(K kernel, int groups, const NormPlan& p, size_t smem, cudaStream_t s, const NormArgs& a) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(groups * p.cluster);
+    cfg.blockDim = dim3(p.threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = p.cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = p.cluster > 1 ? 2 : 1;
+    cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
+// 16-byte pieces can be used (whole rows, or all operands at one phase) for
+// these (pointer, row stride) pairs; NULLs are skipped.
+struct NormAccess {
+    bool wide, edges;
+};
+template <typename T>
+NormAccess norm_access(int32_t C, std::initializer_list<NormView> views) {
+    NormAccess a{true, C % kVec<T> != 0};
+    int64_t at = -1, step = -1;
+    for (const NormView& v : views) {
+        if (!v.p) continue;
+        const int64_t x = (int64_t)(reinterpret_cast<uintptr_t>(v.p) & 15u), y = v.ld * (int64_t)sizeof(T) & 15;
+        if (at < 0) at = x, step = y;
+        if (x != at || y != step) a.wide = false;
+        if (x != 0 || y != 0) a.edges = true;
+    }
+    return a;
+}
+
+zs_status norm_forward(int32_t dtype, NormArgs& a, cudaStream_t s);
+zs_status norm_backward(int32_t dtype, NormArgs& a, cudaStream_t s);
+
+}  // namespace zs

@@ -36,6 +36,8 @@ def library_path() -> str:
 def load(build_if_missing: bool = True):
     """Load libzs.so (building it with nvcc first if it is missing or stale)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -124,9 +126,17 @@ def _ptr(t) -> int | None:
     return t.data_ptr() if t.numel() > 0 else None
 
 
+# The current stream's handle without building a Stream object for it (0.2
+# against 2.9 us a call on the host of a GB300).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_raw_device = getattr(torch._C, "_cuda_getDevice", None)
+
+
 def _stream(stream) -> int | None:
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        if _raw_stream is None or _raw_device is None:
+            return torch.cuda.current_stream().cuda_stream
+        return _raw_stream(_raw_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -462,7 +472,8 @@ def zs_forward_noalloc(coup: torch.Tensor, rad: torch.Tensor, row_ptr: torch.Ten
 
 # ---------------------------------------------------------------------------
 # Training operators: products grouped by a CSR, residual norms with a gate,
-# the AdamW step.
+# the AdamW step.  Small calls last as long as their host side, so the checks
+# have a short way for operands that are as they should be.
 
 DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 NORM_KINDS = {"rms": 0, "layer": 1}
@@ -476,9 +487,18 @@ def _dtype(t: torch.Tensor, name: str) -> int:
     return d
 
 
+def _array(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple) -> int:
+    """Checks a contiguous CUDA tensor and returns its address."""
+    if not (t.is_cuda and t.dtype is dtype and t.shape == shape and t.is_contiguous()):
+        _need(t, name, dtype, shape)
+    return t.data_ptr()
+
+
 def _matrix(t: torch.Tensor, name: str, dtype: torch.dtype, rows: int, cols: int) -> int:
     """Checks a CUDA matrix whose rows are contiguous (a row-strided view
     allowed) and returns its row stride in elements."""
+    if t.is_cuda and t.dtype is dtype and t.shape == (rows, cols) and t.is_contiguous():
+        return cols
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dtype != dtype:
@@ -486,29 +506,25 @@ def _matrix(t: torch.Tensor, name: str, dtype: torch.dtype, rows: int, cols: int
     if t.shape != (rows, cols):
         raise ValueError(f"{name} must have shape {(rows, cols)}, got {tuple(t.shape)}")
     ld, step = t.stride()
-    if rows > 1 and ld < cols or cols > 1 and step != 1:
-        if t.numel():
-            raise ValueError(f"{name} must have contiguous rows (stride (ld, 1) with ld >= {cols})")
+    if t.numel() and (rows > 1 and ld < cols or cols > 1 and step != 1):
+        raise ValueError(f"{name} must have contiguous rows (stride (ld, 1) with ld >= {cols})")
     return ld if rows > 1 and ld >= cols else cols
 
 
-def _grouped_shapes(w: torch.Tensor, row_ptr: torch.Tensor, perm: torch.Tensor | None, M: int):
-    """Checks what the three grouped products share; returns (dtype, G, N, K)."""
+def _rows(t: torch.Tensor, name: str) -> tuple[int, int]:
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be a matrix, got shape {tuple(t.shape)}")
+    return t.shape
+
+
+def _groups(w: torch.Tensor, row_ptr: torch.Tensor, perm: torch.Tensor | None, M: int):
+    """Checks the weights and the CSR; returns (dtype, G, N, K, their addresses)."""
     d = _dtype(w, "w")
     if w.dim() != 3:
         raise ValueError(f"w must have shape (G, N, K), got {tuple(w.shape)}")
     G, N, K = w.shape
-    _need(w, "w", w.dtype, (G, N, K))
-    _need(row_ptr, "row_ptr", torch.int32, (G + 1,))
-    if perm is not None:
-        _need(perm, "perm", torch.int32, (M,))
-    return d, G, N, K
-
-
-def _rows(t: torch.Tensor, name: str) -> int:
-    if t.dim() != 2:
-        raise ValueError(f"{name} must be a matrix, got shape {tuple(t.shape)}")
-    return t.shape[0]
+    return (d, G, N, K, _array(w, "w", w.dtype, (G, N, K)), _array(row_ptr, "row_ptr", torch.int32, (G + 1,)),
+            None if perm is None else _array(perm, "perm", torch.int32, (M,)))
 
 
 def zs_grouped_matmul(x: torch.Tensor, w: torch.Tensor, row_ptr: torch.Tensor, perm: torch.Tensor | None = None,
@@ -516,28 +532,37 @@ def zs_grouped_matmul(x: torch.Tensor, w: torch.Tensor, row_ptr: torch.Tensor, p
     """y[i] = w[g(i)] x[i] for rows grouped by the CSR (row_ptr, perm); perm None: rows
     are in group order already.  x (M, K) and w (G, N, K) float32, bfloat16 or
     float16; returns y (M, N).  x and out may be row-strided views."""
-    M = _rows(x, "x")
-    d, G, N, K = _grouped_shapes(w, row_ptr, perm, M)
-    x_ld = _matrix(x, "x", w.dtype, M, K)
+    M, _ = _rows(x, "x")
+    d, G, N, K, wp, rp, pp = _groups(w, row_ptr, perm, M)
+    dt = w.dtype
+    x_ld = _matrix(x, "x", dt, M, K)
+    out_ld = N
     if out is None:
-        out = torch.empty((M, N), dtype=w.dtype, device=x.device)
-    out_ld = _matrix(out, "out", w.dtype, M, N)
-    _check("zs_grouped_matmul", load().zs_grouped_matmul(d, _ptr(x), x_ld, _ptr(w), row_ptr.data_ptr(), _ptr(perm), M, K, N,
-                                                         G, _ptr(out), out_ld, _stream(stream)))
+        out = torch.empty((M, N), dtype=dt, device=x.device)
+    else:
+        out_ld = _matrix(out, "out", dt, M, N)
+    st = load().zs_grouped_matmul(d, x.data_ptr(), x_ld, wp, rp, pp, M, K, N, G, out.data_ptr(), out_ld, _stream(stream))
+    if st:
+        _check("zs_grouped_matmul", st)
     return out
 
 
 def zs_grouped_matmul_dx(dy: torch.Tensor, w: torch.Tensor, row_ptr: torch.Tensor, perm: torch.Tensor | None = None,
                          out=None, stream=None) -> torch.Tensor:
     """dx[i] = w[g(i)]^T dy[i]: the gradient of zs_grouped_matmul in x, (M, K)."""
-    M = _rows(dy, "dy")
-    d, G, N, K = _grouped_shapes(w, row_ptr, perm, M)
-    dy_ld = _matrix(dy, "dy", w.dtype, M, N)
+    M, _ = _rows(dy, "dy")
+    d, G, N, K, wp, rp, pp = _groups(w, row_ptr, perm, M)
+    dt = w.dtype
+    dy_ld = _matrix(dy, "dy", dt, M, N)
+    out_ld = K
     if out is None:
-        out = torch.empty((M, K), dtype=w.dtype, device=dy.device)
-    out_ld = _matrix(out, "out", w.dtype, M, K)
-    _check("zs_grouped_matmul_dx", load().zs_grouped_matmul_dx(d, _ptr(dy), dy_ld, _ptr(w), row_ptr.data_ptr(), _ptr(perm),
-                                                               M, K, N, G, _ptr(out), out_ld, _stream(stream)))
+        out = torch.empty((M, K), dtype=dt, device=dy.device)
+    else:
+        out_ld = _matrix(out, "out", dt, M, K)
+    st = load().zs_grouped_matmul_dx(d, dy.data_ptr(), dy_ld, wp, rp, pp, M, K, N, G, out.data_ptr(), out_ld,
+                                     _stream(stream))
+    if st:
+        _check("zs_grouped_matmul_dx", st)
     return out
 
 
@@ -549,23 +574,28 @@ def zs_grouped_matmul_dw(dy: torch.Tensor, x: torch.Tensor, row_ptr: torch.Tenso
                          out=None, workspace=None, stream=None) -> torch.Tensor:
     """dw[g] = sum over the rows of group g of dy[i] x[i]^T: the gradient of
     zs_grouped_matmul in w, (G, N, K) with G = row_ptr.numel() - 1."""
-    M = _rows(x, "x")
-    K, N, G = x.shape[1], dy.shape[-1], row_ptr.numel() - 1
-    d = _dtype(x, "x")
-    x_ld = _matrix(x, "x", x.dtype, M, K)
-    dy_ld = _matrix(dy, "dy", x.dtype, M, N)
-    _need(row_ptr, "row_ptr", torch.int32, (G + 1,))
-    if perm is not None:
-        _need(perm, "perm", torch.int32, (M,))
+    M, K = _rows(x, "x")
+    _, N = _rows(dy, "dy")
+    G = row_ptr.numel() - 1
+    d, dt, dev = _dtype(x, "x"), x.dtype, x.device
+    x_ld = _matrix(x, "x", dt, M, K)
+    dy_ld = _matrix(dy, "dy", dt, M, N)
+    rp = _array(row_ptr, "row_ptr", torch.int32, (G + 1,))
+    pp = None if perm is None else _array(perm, "perm", torch.int32, (M,))
     if out is None:
-        out = torch.empty((G, N, K), dtype=x.dtype, device=x.device)
-    _need(out, "out", x.dtype, (G, N, K))
+        out = torch.empty((G, N, K), dtype=dt, device=dev)
+    op = _array(out, "out", dt, (G, N, K))
+    lib = load()
     if workspace is None:
-        workspace = _workspace(load().zs_grouped_matmul_dw_workspace_bytes(d, M, K, N, G), x.device)
-    wbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _check("zs_grouped_matmul_dw", load().zs_grouped_matmul_dw(d, _ptr(dy), dy_ld, _ptr(x), x_ld, row_ptr.data_ptr(),
-                                                               _ptr(perm), M, K, N, G, _ptr(out), _ptr(workspace), wbytes,
-                                                               _stream(stream)))
+        wbytes = lib.zs_grouped_matmul_dw_workspace_bytes(d, M, K, N, G)
+        if wbytes:
+            workspace = torch.empty(wbytes, dtype=torch.uint8, device=dev)
+    else:
+        wbytes = workspace.numel() * workspace.element_size()
+    st = lib.zs_grouped_matmul_dw(d, dy.data_ptr(), dy_ld, x.data_ptr(), x_ld, rp, pp, M, K, N, G, op, _ptr(workspace),
+                                  wbytes, _stream(stream))
+    if st:
+        _check("zs_grouped_matmul_dw", st)
     return out
 
 
@@ -579,24 +609,24 @@ def zs_grouped_matmul_backward(dy: torch.Tensor, x: torch.Tensor, w: torch.Tenso
 def _norm_operands(h, x, gate, w_post, scale, w_pre, kind):
     """Checks the operands of the residual norms; returns (dtype, kind, M, C, the
     arguments h..w_pre of the C call)."""
-    M = _rows(h, "h")
-    C = h.shape[1]
-    d = _dtype(h, "h")
-    if kind not in NORM_KINDS:
+    M, C = _rows(h, "h")
+    d, dt = _dtype(h, "h"), h.dtype
+    k = NORM_KINDS.get(kind)
+    if k is None:
         raise ValueError(f"kind must be one of {sorted(NORM_KINDS)}, got {kind!r}")
-    h_ld = _matrix(h, "h", h.dtype, M, C)
-    x_ld = _matrix(x, "x", h.dtype, M, C)
+    h_ld = _matrix(h, "h", dt, M, C)
+    x_ld = _matrix(x, "x", dt, M, C)
     gate_ptr, gate_ld, gate_cols = None, 0, 0
     if gate is not None:
-        if gate.dim() != 2 or gate.shape[1] not in (1, C):
+        gate_cols = gate.shape[1] if gate.dim() == 2 else 0
+        if gate_cols != 1 and gate_cols != C:
             raise ValueError(f"gate must have shape {(M, C)} or {(M, 1)}, got {tuple(gate.shape)}")
-        gate_cols = gate.shape[1]
-        gate_ld = _matrix(gate, "gate", h.dtype, M, gate_cols)
-        gate_ptr = _ptr(gate)
-    for t, name in ((w_post, "w_post"), (scale, "scale"), (w_pre, "w_pre")):
-        _need(t, name, torch.float32, (C,))
-    return d, NORM_KINDS[kind], M, C, (_ptr(h), h_ld, _ptr(x), x_ld, gate_ptr, gate_ld, gate_cols, w_post.data_ptr(),
-                                       scale.data_ptr(), w_pre.data_ptr())
+        gate_ld = _matrix(gate, "gate", dt, M, gate_cols)
+        gate_ptr = gate.data_ptr()
+    f32, shape = torch.float32, (C,)
+    return d, k, M, C, (h.data_ptr(), h_ld, x.data_ptr(), x_ld, gate_ptr, gate_ld, gate_cols,
+                        _array(w_post, "w_post", f32, shape), _array(scale, "scale", f32, shape),
+                        _array(w_pre, "w_pre", f32, shape))
 
 
 def zs_norm_gate_residual(h: torch.Tensor, x: torch.Tensor, gate: torch.Tensor | None, w_post: torch.Tensor,
@@ -609,11 +639,14 @@ def zs_norm_gate_residual(h: torch.Tensor, x: torch.Tensor, gate: torch.Tensor |
     Returns (y, u, stats): stats (M, 4) float32 is what the backward reads (None
     when want_stats is False)."""
     d, k, M, C, args = _norm_operands(h, x, gate, w_post, scale, w_pre, kind)
-    y = torch.empty((M, C), dtype=h.dtype, device=h.device)
-    u = torch.empty_like(y)
-    stats = torch.empty((M, 4), dtype=torch.float32, device=h.device) if want_stats else None
-    _check("zs_norm_gate_residual", load().zs_norm_gate_residual(d, k, *args, eps, M, C, _ptr(y), _ptr(u), _ptr(stats),
-                                                                 _stream(stream)))
+    dt, dev = h.dtype, h.device
+    y = torch.empty((M, C), dtype=dt, device=dev)
+    u = torch.empty((M, C), dtype=dt, device=dev)
+    stats = torch.empty((M, 4), dtype=torch.float32, device=dev) if want_stats else None
+    st = load().zs_norm_gate_residual(d, k, *args, eps, M, C, y.data_ptr(), u.data_ptr(),
+                                      stats.data_ptr() if want_stats else None, _stream(stream))
+    if st:
+        _check("zs_norm_gate_residual", st)
     return y, u, stats
 
 
@@ -623,20 +656,24 @@ def zs_norm_gate_residual_backward(dy: torch.Tensor | None, du: torch.Tensor | N
     """Gradients of zs_norm_gate_residual for the cotangents dy of y and du of u (None:
     zeros): (dh, dx, dgate, dw_post, dscale, dw_pre); dgate is None without a gate."""
     d, k, M, C, args = _norm_operands(h, x, gate, w_post, scale, w_pre, kind)
-    dy_ld = 0 if dy is None else _matrix(dy, "dy", h.dtype, M, C)
-    du_ld = 0 if du is None else _matrix(du, "du", h.dtype, M, C)
-    _need(stats, "stats", torch.float32, (M, 4))
-    dh = torch.empty((M, C), dtype=h.dtype, device=h.device)
-    dx = torch.empty_like(dh)
-    dgate = None if gate is None else torch.empty(gate.shape, dtype=h.dtype, device=h.device)
-    sums = torch.empty((3, C), dtype=torch.float32, device=h.device)
-    need = load().zs_norm_gate_residual_backward_workspace_bytes(M, C)
-    workspace = _workspace(need, h.device)
-    base = sums.data_ptr()
-    _check("zs_norm_gate_residual_backward", load().zs_norm_gate_residual_backward(
-        d, k, _ptr(dy), dy_ld, _ptr(du), du_ld, *args, _ptr(stats), M, C, _ptr(dh), _ptr(dx), _ptr(dgate), base,
-        base + 4 * C, base + 8 * C, _ptr(workspace), need, _stream(stream)))
-    return dh, dx, dgate, sums[0], sums[1], sums[2]
+    dt, dev, f32 = h.dtype, h.device, torch.float32
+    dy_ld = 0 if dy is None else _matrix(dy, "dy", dt, M, C)
+    du_ld = 0 if du is None else _matrix(du, "du", dt, M, C)
+    stats_ptr = _array(stats, "stats", f32, (M, 4))
+    dh = torch.empty((M, C), dtype=dt, device=dev)
+    dx = torch.empty((M, C), dtype=dt, device=dev)
+    dgate = None if gate is None else torch.empty((M, args[6]), dtype=dt, device=dev)
+    sums = [torch.empty((C,), dtype=f32, device=dev) for _ in range(3)]
+    lib = load()
+    need = lib.zs_norm_gate_residual_backward_workspace_bytes(M, C)
+    workspace = _workspace(need, dev)
+    st = lib.zs_norm_gate_residual_backward(
+        d, k, None if dy is None else dy.data_ptr(), dy_ld, None if du is None else du.data_ptr(), du_ld, *args, stats_ptr,
+        M, C, dh.data_ptr(), dx.data_ptr(), None if gate is None else dgate.data_ptr(), *(t.data_ptr() for t in sums),
+        _ptr(workspace), need, _stream(stream))
+    if st:
+        _check("zs_norm_gate_residual_backward", st)
+    return dh, dx, dgate, *sums
 
 
 class _AdamWTensor(ctypes.Structure):
@@ -689,7 +726,7 @@ class AdamWPlan:
                 for lst, name in zip(self.scales, ("exp_avg_scale", "exp_avg_sq_scale")):
                     self._one(lst[i], f"{name}[{i}]", torch.float32, (-(-p.numel() // ADAMW_BLOCK),))
                     setattr(e, name, _ptr(lst[i]))
-        self._hyper = _AdamWHyper()
+        self._table_ptr = ctypes.addressof(self._table)
         self.set_grads(grads)
 
     def _one(self, t, name, dtype, shape):
@@ -712,11 +749,13 @@ def zs_adamw_step(plan: AdamWPlan, step: int, lr: float, beta1: float = 0.9, bet
                   weight_decay: float = 0.01, grad_scale: torch.Tensor | None = None, stream=None) -> None:
     """One AdamW step (number ``step``, from 1) over the plan's tensors, in place.
     grad_scale: one float32 element on the device that multiplies every gradient."""
+    scale_ptr = None
     if grad_scale is not None:
         if grad_scale.numel() != 1 or grad_scale.dtype != torch.float32 or grad_scale.device != plan.device:
             raise ValueError(f"grad_scale must be one float32 element on {plan.device}")
-    h = plan._hyper
-    h.lr, h.beta1, h.beta2, h.eps, h.weight_decay, h.step = lr, beta1, beta2, eps, weight_decay, step
-    _check("zs_adamw_step", load().zs_adamw_step(ctypes.addressof(plan._table), len(plan.params), plan.dtype,
-                                                 plan.state_bits, ctypes.addressof(h), _ptr(grad_scale),
-                                                 _stream(stream)))
+        scale_ptr = grad_scale.data_ptr()
+    hyper = _AdamWHyper(lr, beta1, beta2, eps, weight_decay, step)
+    st = load().zs_adamw_step(plan._table_ptr, len(plan.params), plan.dtype, plan.state_bits, ctypes.addressof(hyper),
+                              scale_ptr, _stream(stream))
+    if st:
+        _check("zs_adamw_step", st)

@@ -224,7 +224,7 @@ def test_argument_checks():
             a["dw"], a["dw"], a["dw"], a["ws"], a["bytes"], None)
 
     need = lib.zs_norm_gate_residual_backward_workspace_bytes(4, 32)
-    assert need == 4 * 3 * 32 * 4
+    assert need == 4 * 2 * 32 * 4
     assert lib.zs_norm_gate_residual_backward_workspace_bytes(0, 32) == 0
     for kw in (dict(dh=None), dict(dgate=None), dict(dw=None), dict(stats=None), dict(bytes=need - 1), dict(ws=None),
                dict(ws=FAKE + 16), dict(h_ld=3), dict(M=-2), dict(dy=FAKE + 1)):
