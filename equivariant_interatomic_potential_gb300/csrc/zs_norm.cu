@@ -65,7 +65,8 @@ zs_status zs_norm_gate_residual(int32_t dtype, int32_t kind, const void* h, int6
     if (M == 0) return ZS_OK;
     if (!h || !x || !y || !u) return fail(ZS_ERR_INVALID_ARG, "%s: NULL h, x, y or u", fn);
     a.s.eps = eps;
-    return norm_forward(dtype, a, reinterpret_cast<cudaStream_t>(stream));
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    return dtype == ZS_F32 ? norm_forward<float>(a, s) : dtype == ZS_BF16 ? norm_forward<__nv_bfloat16>(a, s) : norm_forward<__half>(a, s);
 }
 
 size_t zs_norm_gate_residual_backward_workspace_bytes(int64_t M, int32_t C) {
@@ -102,7 +103,8 @@ zs_status zs_norm_gate_residual_backward(int32_t dtype, int32_t kind, const void
         if (reinterpret_cast<uintptr_t>(workspace) & 255u)
             return fail(ZS_ERR_INVALID_ARG, "%s: workspace is not 256-byte aligned", fn);
     }
-    return norm_backward(dtype, a, reinterpret_cast<cudaStream_t>(stream));
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    return dtype == ZS_F32 ? norm_backward<float>(a, s) : dtype == ZS_BF16 ? norm_backward<__nv_bfloat16>(a, s) : norm_backward<__half>(a, s);
 }
 
 }  // extern "C"

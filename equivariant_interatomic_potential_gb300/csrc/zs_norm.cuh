@@ -14,10 +14,11 @@
 // Bound by HBM.  A row lives in the registers of 8 to 256 threads, or of a
 // cluster of CTAs that exchange their sums through distributed shared memory,
 // each thread holding up to NV pieces of VEC elements, so that every operand
-// is read once; while a row is worked on the next one's pieces are on their
-// way.  Rows go round the CTAs of a persistent grid, whose threads keep the
-// parameters of their columns, and in the backward the running column sums,
-// in registers.
+// is read once.  Rows go round the CTAs of a persistent grid, whose threads
+// keep the parameters of their columns, and in the backward the running
+// column sums, in registers; the pieces of the next rows are on their way
+// into shared memory meanwhile, each thread's own ones into slots that it
+// alone reads, so that no barrier stands between the copy and its use.
 //
 // Rows that do not start on 16-byte boundaries (odd channel counts) are still
 // read in 16-byte pieces of memory: a row's first and last piece bring some of
@@ -37,7 +38,7 @@ namespace zs {
 constexpr int kNormMaxC = 8192;
 constexpr int kNormThreads = 256;     // of a CTA, at most
 constexpr int kNormWarps = kNormThreads / 32;
-constexpr int kNormCluster = 5;       // CTAs that share a row, at most
+constexpr int kNormCluster = 8;       // CTAs that share a row, at most
 constexpr int kNormCtas = 304;        // of the backward, at most: rows of the partial column sums
 
 struct NormShape {
@@ -76,94 +77,129 @@ struct NormCols {
     static constexpr int E = VEC * NV;
     static_assert(VEC == 1 || VEC == kVec<T>, "whole 16-byte pieces or single elements");
 
-    // f(k, c0, whole): piece k starts at column c0; whole: all of it is in the row
+    static __device__ __forceinline__ int start(const NormLane& l, int k) {
+        return (k * l.tpr + l.lane) * VEC - (kEdges ? l.phase : 0);
+    }
+    static __device__ __forceinline__ bool whole(const NormLane& l, int c0) {
+        return !kEdges || (c0 >= 0 && c0 + VEC <= l.C);
+    }
+    // f(i, c) for this thread's columns c of the row, element i of its E
     template <typename F>
-    static __device__ __forceinline__ void each(const NormLane& l, F&& f) {
+    static __device__ __forceinline__ void for_columns(const NormLane& l, F&& f) {
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            const int c0 = (k * l.tpr + l.lane) * VEC - (kEdges ? l.phase : 0);
-            if (c0 < l.C) f(k, c0, !kEdges || VEC == 1 || (c0 >= 0 && c0 + VEC <= l.C));
+            const int c0 = start(l, k);
+#pragma unroll
+            for (int i = 0; i < VEC; ++i)
+                if (kEdges ? (unsigned)(c0 + i) < (unsigned)l.C : c0 < l.C) f(k * VEC + i, c0 + i);
         }
     }
-    static __device__ __forceinline__ bool in_row(const NormLane& l, int c) {
-        return !kEdges || VEC == 1 || (unsigned)c < (unsigned)l.C;
+    template <typename F>
+    static __device__ __forceinline__ void columns(float (&v)[E], const NormLane& l, F&& f) {
+#pragma unroll
+        for (int i = 0; i < E; ++i) v[i] = 0.f;
+        for_columns(l, [&](int i, int c) { v[i] = f(c); });
     }
-    // A row as it travels: raw pieces, so that loads can be issued well before use.
-    struct Raw {
-        Piece<T> v[VEC == 1 ? 1 : NV];
-        T s[VEC == 1 ? NV : 1];
-    };
-    // row r of the M rows of v
-    static __device__ __forceinline__ void load(Raw& w, const NormView& v, int64_t r, int64_t M, const NormLane& l) {
-        const T* row = static_cast<const T*>(v.p) + r * v.ld;
-        each(l, [&](int k, int c0, bool whole) {
-            if constexpr (VEC == 1) {
-                w.s[k] = row[c0];
-            } else if (whole || (r * v.ld + c0 >= 0 && c0 + VEC <= (M - 1 - r) * v.ld + l.C)) {
-                w.v[k].raw = ld_piece(row + c0);
-            } else {
+    // Zero outside the row.
+    static __device__ __forceinline__ void clear_outside(float (&v)[E], const NormLane& l) {
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) w.v[k].e[i] = in_row(l, c0 + i) ? row[c0 + i] : from_f32<T>(0.f);
-            }
-        });
-    }
-    static __device__ __forceinline__ void open(const Raw& r, float (&f)[E], const NormLane& l) {
+        for (int k = 0; k < NV; ++k) {
+            const int c0 = start(l, k);
 #pragma unroll
-        for (int i = 0; i < E; ++i) f[i] = 0.f;
-        each(l, [&](int k, int c0, bool) {
-            if constexpr (VEC == 1) {
-                f[k] = to_f32(r.s[k]);
-            } else {
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) f[k * VEC + i] = in_row(l, c0 + i) ? to_f32(r.v[k].e[i]) : 0.f;
-            }
-        });
+            for (int i = 0; i < VEC; ++i)
+                if (!(kEdges ? (unsigned)(c0 + i) < (unsigned)l.C : c0 < l.C)) v[k * VEC + i] = 0.f;
+        }
     }
     static __device__ __forceinline__ void store(T* row, const float (&f)[E], const NormLane& l) {
-        each(l, [&](int k, int c0, bool whole) {
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int c0 = start(l, k);
+            if (c0 >= l.C) continue;
             if constexpr (VEC == 1) {
                 row[c0] = from_f32<T>(f[k]);
             } else {
                 float q[VEC];
 #pragma unroll
                 for (int i = 0; i < VEC; ++i) q[i] = f[k * VEC + i];
-                if (whole) {
+                if (whole(l, c0)) {
                     st_piece(row + c0, pack<T>(q));
                 } else {
 #pragma unroll
                     for (int i = 0; i < VEC; ++i)
-                        if (in_row(l, c0 + i)) row[c0 + i] = from_f32<T>(q[i]);
+                        if ((unsigned)(c0 + i) < (unsigned)l.C) row[c0 + i] = from_f32<T>(q[i]);
                 }
             }
-        });
+        }
     }
-    // f[i] = g(column) for the columns of the row, 0 beyond
-    template <typename G>
-    static __device__ __forceinline__ void columns(float (&f)[E], const NormLane& l, G&& g) {
-#pragma unroll
-        for (int i = 0; i < E; ++i) f[i] = 0.f;
-        each(l, [&](int k, int c0, bool) {
-#pragma unroll
-            for (int i = 0; i < VEC; ++i)
-                if (in_row(l, c0 + i)) f[k * VEC + i] = g(c0 + i);
-        });
+};
+
+// The rows on their way: kNormStages stages of NA operands, NV pieces each, in
+// shared memory; a piece of this thread lies `stride` (a slot for each thread
+// of the CTA) after the one before.
+constexpr int kNormStages = 4;
+template <typename T, int VEC, int NV, int NA, bool kEdges>
+struct NormRing {
+    using Co = NormCols<T, VEC, NV, kEdges>;
+    static constexpr int kSlot = VEC == 1 ? 4 : 16;
+    unsigned char* mine;    // this thread's first slot
+    uint32_t mine_s;        // its shared address
+    uint32_t stride;
+
+    __device__ __forceinline__ void init(unsigned char* smem) {
+        mine = smem + threadIdx.x * kSlot;
+        mine_s = (uint32_t)__cvta_generic_to_shared(mine);
+        stride = blockDim.x * kSlot;
+        // pieces outside the row are never copied: they stay zero
+        for (int i = 0; i < kNormStages * NA * NV; ++i) {
+            if constexpr (VEC == 1) *reinterpret_cast<uint32_t*>(mine + i * stride) = 0;
+            else *reinterpret_cast<uint4*>(mine + i * stride) = make_uint4(0, 0, 0, 0);
+        }
     }
-    template <typename G>
-    static __device__ __forceinline__ void for_columns(const NormLane& l, G&& g) {
-        each(l, [&](int k, int c0, bool) {
-#pragma unroll
-            for (int i = 0; i < VEC; ++i)
-                if (in_row(l, c0 + i)) g(k * VEC + i, c0 + i);
-        });
-    }
-    // Zero outside the row, so that sums over a thread's elements need no care.
-    static __device__ __forceinline__ void clear_outside(float (&f)[E], const NormLane& l) {
+    // Row r of the M rows of v on its way into a stage.
+    __device__ __forceinline__ void issue(int stage, int a, const NormView& v, int64_t r, int64_t M, const NormLane& l) {
+        const T* row = static_cast<const T*>(v.p) + r * v.ld;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            const int c0 = (k * l.tpr + l.lane) * VEC - (kEdges ? l.phase : 0);
+            const int c0 = Co::start(l, k);
+            if (c0 >= l.C) continue;
+            const uint32_t slot = ((stage * NA + a) * NV + k) * stride;
+            if constexpr (VEC == 1) {
+                *reinterpret_cast<T*>(mine + slot) = row[c0];
+            } else if (Co::whole(l, c0) || (r * v.ld + c0 >= 0 && c0 + VEC <= (M - 1 - r) * v.ld + l.C)) {
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(mine_s + slot), "l"(row + c0) : "memory");
+            } else {
 #pragma unroll
-            for (int i = 0; i < VEC; ++i)
-                if (c0 >= l.C || !in_row(l, c0 + i)) f[k * VEC + i] = 0.f;
+                for (int i = 0; i < VEC; ++i)
+                    if ((unsigned)(c0 + i) < (unsigned)l.C) *reinterpret_cast<T*>(mine + slot + i * sizeof(T)) = row[c0 + i];
+            }
+        }
+    }
+    static __device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+    // All but the last kNormStages - 1 groups have landed.
+    static __device__ __forceinline__ void wait() { asm volatile("cp.async.wait_group %0;" :: "n"(kNormStages - 1) : "memory"); }
+    static __device__ __forceinline__ void drain() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+    // The elements of operand a in a stage; a neighbour's count as zeros.
+    __device__ __forceinline__ void open(int stage, int a, float (&f)[Co::E], const NormLane& l) const {
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const unsigned char* slot = mine + ((stage * NA + a) * NV + k) * stride;
+            if constexpr (VEC == 1) {
+                f[k] = to_f32(*reinterpret_cast<const T*>(slot));
+            } else {
+                float q[VEC];
+                unpack<T>(*reinterpret_cast<const uint4*>(slot), q);
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) f[k * VEC + i] = q[i];
+                if constexpr (kEdges) {
+                    const int c0 = Co::start(l, k);
+                    if (!Co::whole(l, c0)) {
+#pragma unroll
+                        for (int i = 0; i < VEC; ++i)
+                            f[k * VEC + i] = (unsigned)(c0 + i) < (unsigned)l.C ? f[k * VEC + i] : 0.f;
+                    }
+                }
+            }
         }
     }
 };
@@ -190,7 +226,7 @@ __device__ __forceinline__ void row_sum(float (&q)[NQ], const NormShape& s, Norm
         for (int i = 0; i < NQ; ++i) q[i] += __shfl_xor_sync(0xffffffffu, q[i], o);
     }
     if (s.tpr <= 32) return;
-    const int warp = threadIdx.x >> 5, per_row = s.tpr >> 5;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, per_row = s.tpr >> 5;
     float4* slot = sums.red[round & 1];
     ++round;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -200,13 +236,12 @@ __device__ __forceinline__ void row_sum(float (&q)[NQ], const NormShape& s, Norm
     int first;
     if (s.cluster == 1) {
         first = warp / per_row * per_row;
-        if ((threadIdx.x & 31) == 0) slot[warp] = v;
+        if (lane == 0) slot[warp] = v;
         __syncthreads();
     } else {
         first = 0;
         uint32_t rank;
         asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
-        const int lane = threadIdx.x & 31;
         if (lane < s.cluster) {   // lane i writes this warp's part to CTA i
             const uint32_t mine = (uint32_t)__cvta_generic_to_shared(slot + rank * (blockDim.x >> 5) + warp);
             uint32_t there;
@@ -278,7 +313,7 @@ inline NormPlan norm_plan(int32_t C, int vec, bool edges, int most) {
         p.threads = p.cluster > 1 ? p.tpr / p.cluster : p.rows * p.tpr;
         if (least == 0 || p.tpr * nv * 5 < least * 4) best = p, least = p.tpr * nv;
     }
-    return best;
+    return least || most >= 4 ? best : norm_plan(C, vec, edges, 2 * most);   // the row takes more pieces a thread
 }
 // Groups of rows (CTAs, or clusters) for M rows, `most` at most: a multiple of
 // 8 where a group takes several rounds, so that its phase stays.
@@ -324,7 +359,9 @@ NormAccess norm_access(int32_t C, std::initializer_list<NormView> views) {
     return a;
 }
 
-zs_status norm_forward(int32_t dtype, NormArgs& a, cudaStream_t s);
-zs_status norm_backward(int32_t dtype, NormArgs& a, cudaStream_t s);
+template <typename T>
+zs_status norm_forward(NormArgs& a, cudaStream_t s);
+template <typename T>
+zs_status norm_backward(NormArgs& a, cudaStream_t s);
 
 }  // namespace zs
