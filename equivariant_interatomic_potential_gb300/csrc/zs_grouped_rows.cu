@@ -1,8 +1,9 @@
 // Grouped products over rows: y[i] = w[g(i)] x[i], and the gradient in x with
-// w transposed.  One persistent kernel: warp 0 brings tiles in by TMA (rows
-// of a CSR by gather), or eight more warps read them where TMA cannot (fp32,
-// which is cut into bf16 planes on the way, and unaligned rows); warp 1
-// issues the products; warps 4 to 7 write finished tiles while the next one
+// w transposed.  One persistent kernel: warp 0 brings tiles in by TMA, eight
+// more warps copy the rows of a CSR in with cp.async, or two groups of eight
+// read everything where neither can (fp32, which is cut into bf16 planes on
+// the way, and unaligned rows); warp 1
+// issues the products; warps 4 to 11 write finished tiles while the next one
 // is being summed.
 #include <initializer_list>
 
@@ -12,8 +13,6 @@
 namespace zs {
 
 namespace {
-
-constexpr int kLoaderWarps = 8;
 
 struct RowsArgs {
     Matrix a;             // rows of the left operand
@@ -31,33 +30,56 @@ struct RowsArgs {
 
 template <typename T, bool kTma, bool kMN, int BN>
 struct RowsShape {
-    static constexpr int P = kPlanes<T>;
-    static constexpr uint32_t kA = kTileM * kBoxRow;
-    static constexpr uint32_t kB = (kMN && BN < kBoxCols ? kBoxCols : BN) * kBoxRow;
+    static constexpr int P = kPlanes<T>, kBox = kStageK<T>;
+    static constexpr uint32_t kA = box_bytes<kBox>(kTileM);
+    static constexpr int kBoxes = kMN ? (BN + kBoxMN - 1) / kBoxMN : 1;                       // of the right operand
+    static constexpr uint32_t kBoxB = kMN ? box_bytes<kBoxMN>(kBox) : box_bytes<kBox>(BN);
+    static constexpr uint32_t kB = kBoxes * kBoxB;
     static constexpr uint32_t kStage = P * (kA + kB);
-    static constexpr int kFixed = 4 * kStageWarp + 1024 + 512;   // staging, alignment, barriers
+    static constexpr int kHalves = BN >= 64 ? 2 : 1;   // warps that share 32 rows of a tile
+    static constexpr uint32_t kTmemCols = tmem_cols(2 * kSums<T> * BN);
+    // what the loader warps copy into before they turn it: 16 bytes a part, two stages for each of the two groups (or
+    // one of unaligned rows, 32 bytes a part)
+    using PartsA = BoxParts<T, kTileM, kBox>;
+    using PartsB = BoxParts<T, kMN ? kBox : BN, kMN ? kBoxMN : kBox>;
+    static constexpr int kParts = PartsA::kSteps + kBoxes * PartsB::kSteps;
+    static constexpr int kSlots = kTma ? 0 : 4 * kParts * 32 * kLoaderWarps * 16;
+    static constexpr int kFixed = kSlots + kEpilogueWarps * kStageWarp + 1024 + 4608;   // staging, alignment, barriers and groups
     static constexpr int kFit = (kSmemMost - kFixed) / (int)kStage;
     static constexpr int S = kFit > 8 ? 8 : kFit;
-    static_assert(S >= 2, "two stages at least");
+    static_assert(kPlanes<T> == 1 || !kMN || BN == kBoxMN, "the planes of an MN-major operand follow each other");
+    static_assert(S >= 2 && Setup<S, kTmemCols, kTileM, 1>::kBytes <= 4608, "two stages at least");
     static constexpr int kSmem = S * (int)kStage + kFixed;
-    static constexpr int kThreads = 256 + (kTma ? 0 : 32 * kLoaderWarps);
-    static constexpr uint32_t kTmemCols = 2 * BN < 32 ? 32 : 2 * BN;
+    static constexpr int kThreads = 32 * (4 + kEpilogueWarps + (kTma ? 1 : 2) * kLoaderWarps);
 };
 
 struct Item {
     int g, p0, p1, n0;
 };
-// The item'th tile of output; false when it is empty.
-__device__ __forceinline__ bool get_item(const RowsArgs& a, const Groups<kTileM>& gr, int item, int BN, Item& t) {
-    const int64_t slot = item / a.ntiles;
-    t.n0 = item % a.ntiles * BN;
-    t.g = gr.find(slot, a.G + 1);
-    const int b = gr.start(t.g), e = gr.start(t.g + 1);
-    const int64_t p0 = b + (slot - (b / kTileM + t.g)) * kTileM;
-    if (p0 >= e) return false;
-    t.p0 = (int)p0;
-    t.p1 = (int)imin<int64_t>(p0 + kTileM, e);
-    return true;
+using RowGroups = Groups<kTileM, 1>;
+
+// The next tile of output with rows in it, from `item` on in steps of the grid.
+__device__ __forceinline__ bool next_item(const RowsArgs& a, const RowGroups& gr, int& item, int BN, Item& t) {
+    for (; item < a.items; item += gridDim.x) {
+        const int slot = item / a.ntiles;
+        t.n0 = item % a.ntiles * BN;
+        t.g = gr.find(slot, a.G + 1);
+        const int b = gr.start(t.g), e = gr.start(t.g + 1);
+        const int64_t p0 = b + (int64_t)(slot - (b / kTileM + t.g)) * kTileM;
+        if (p0 < e) {
+            t.p0 = (int)p0;
+            t.p1 = (int)imin<int64_t>(p0 + kTileM, e);
+            item += gridDim.x;
+            return true;
+        }
+    }
+    return false;
+}
+// The same without the rows of no group, which take no product.
+__device__ __forceinline__ bool next_product(const RowsArgs& a, const RowGroups& gr, int& item, int BN, Item& t) {
+    while (next_item(a, gr, item, BN, t))
+        if (t.g < a.G) return true;
+    return false;
 }
 
 __device__ __forceinline__ int row_at(const RowsArgs& a, int p) {
@@ -68,198 +90,217 @@ __device__ __forceinline__ int row_at(const RowsArgs& a, int p) {
 
 template <typename T, bool kTma, bool kMN, int BN>
 __global__ void __launch_bounds__(RowsShape<T, kTma, kMN, BN>::kThreads, 1)
-rows_mma(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUtensorMap w_map, RowsArgs a) {
+rows_mma(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUtensorMap w_map, const RowsArgs a) {
     using Sh = RowsShape<T, kTma, kMN, BN>;
     constexpr int S = Sh::S;
     extern __shared__ unsigned char raw[];
     unsigned char* ring = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
-    unsigned char* staging = ring + S * Sh::kStage;
-    uint64_t* bars = reinterpret_cast<uint64_t*>(staging + 4 * kStageWarp);
-    volatile int* dead = reinterpret_cast<volatile int*>(bars + 2 * S + 5);
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * S + 6);
-    const uint32_t full = smem_u32(bars), empty = full + 8 * S, tfull = empty + 8 * S, tempty = tfull + 16, done = tempty + 16;
+    unsigned char* slots = ring + S * Sh::kStage;
+    unsigned char* staging = slots + Sh::kSlots;
+    Setup<S, Sh::kTmemCols, kTileM, 1> set;
+    set.begin(staging + kEpilogueWarps * kStageWarp, !kTma ? kLoaderWarps : a.perm ? 1 + kLoaderWarps : 1, 4 * Sh::kHalves, a.row_ptr, a.G, a.M);
+    const RowGroups& gr = set.groups;
+    volatile int* dead = set.dead;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < S; ++i) {
-            mbar_init(full + 8 * i, kTma ? 1 : kLoaderWarps);
-            mbar_init(empty + 8 * i, 1);
-        }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(tfull + 8 * i, 1);
-            mbar_init(tempty + 8 * i, 4);
-        }
-        mbar_init(done, 1);
-        *dead = 0;
-        mbar_fence_init();
-    }
-    pdl_wait();
-    pdl_trigger();
-    if (warp == 2) tmem_alloc(smem_u32(tmem_slot), Sh::kTmemCols);
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
-    const Groups<kTileM> gr{a.row_ptr, a.G, a.M};
-    const int nk = (a.red + kBoxCols - 1) / kBoxCols;
+    constexpr int kBox = Sh::kBox;
+    const int nk = (a.red + kBox - 1) / kBox;
+    constexpr int kPerChunk = kSums<T> > 1 ? kChunk / kBox : 1 << 30;   // stages between hand-overs to the epilogue
+    int item = blockIdx.x;
+    Item t;
 
     if (kTma && warp == 0) {
         RingPos<S> pos;
         int issued = 0;
-        for (int item = blockIdx.x; item < a.items && !*dead; item += gridDim.x) {
-            Item t;
-            if (!get_item(a, gr, item, BN, t) || t.g == a.G) continue;
-            // this lane's four rows; the last one again past the end
-            int4 rows = make_int4(0, 0, 0, 0);
-            const int p = t.p0 + 4 * lane;
-            const bool mine = p < t.p1;
-            if (a.perm && mine) {
-                int* r = &rows.x;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) r[i] = imax(row_at(a, imin(p + i, t.p1 - 1)), 0);
-            }
-            const uint32_t a_bytes = a.perm ? 512u * ((t.p1 - t.p0 + 3) / 4) : Sh::kA;
-            const int boxes = kMN ? (imin(BN, a.cols - t.n0) + kBoxCols - 1) / kBoxCols : 1;
-            const uint32_t bytes = a_bytes + (kMN ? boxes * kBoxCols * kBoxRow : Sh::kB);
-            for (int k = 0; k < nk; ++k, pos.next()) {
-                if (!bounded_wait(empty + 8 * pos.stage, pos.phase ^ 1, dead)) break;
-                const uint32_t bar = full + 8 * pos.stage, at = smem_u32(ring) + pos.stage * Sh::kStage, bt = at + Sh::kA;
-                if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
-                __syncwarp();
-                if (a.perm) {
-                    if (mine) tma_gather4(at + lane * 512, &a_map, k * kBoxCols, rows, bar);
-                } else if (lane == 0) {
-                    tma_2d(at, &a_map, k * kBoxCols, t.p0, bar);
+        while (!is_dead(dead) && next_product(a, gr, item, BN, t)) {
+            const int boxes = kMN ? (imin(BN, a.cols - t.n0) + kBoxMN - 1) / kBoxMN : 1;
+            const uint32_t bytes = (a.perm ? 0 : Sh::kA) + boxes * Sh::kBoxB;
+            if (lane == 0) {
+                for (int k = 0; k < nk; ++k, ++issued, pos.next()) {
+                    if (!bounded_wait_one(set.empty + 8 * pos.stage, pos.phase ^ 1, dead)) break;
+                    const uint32_t bar = set.full + 8 * pos.stage, at = smem_u32(ring) + pos.stage * Sh::kStage, bt = at + Sh::kA;
+                    mbar_arrive_expect_tx(bar, bytes);
+                    if (!a.perm) tma_2d(at, &a_map, k * kBox, t.p0, bar);
+                    for (int i = 0; i < boxes; ++i) {
+                        if (kMN) tma_3d(bt + i * Sh::kBoxB, &w_map, t.n0 + i * kBoxMN, k * kBox, t.g, bar);
+                        else tma_3d(bt, &w_map, k * kBox, t.n0, t.g, bar);
+                    }
                 }
-                if (kMN) {
-                    if (lane < boxes) tma_3d(bt + lane * kBoxCols * kBoxRow, &w_map, t.n0 + lane * kBoxCols, k * kBoxCols, t.g, bar);
-                } else if (lane == 0) {
-                    tma_3d(bt, &w_map, k * kBoxCols, t.n0, t.g, bar);
-                }
-                ++issued;
             }
+            __syncwarp();
         }
-        if (*dead) {   // wait for the copies in flight
-            for (int i = 0; i < imin(issued, S); ++i) {
-                const int k = issued - 1 - i;
-                for (uint32_t n = 0; n < kDrainSpins && !mbar_try_wait(full + 8 * (k % S), (uint32_t)(k / S) & 1); ++n) {}
-            }
-        }
-    } else if (!kTma && warp >= 8) {
+        issued = __shfl_sync(0xffffffffu, issued, 0);
+        if (is_dead(dead)) set.drain_copies(issued);
+    } else if (warp >= 4 + kEpilogueWarps) {
+        const int w = (warp - 4 - kEpilogueWarps) % kLoaderWarps;
+        constexpr int kPerA = kTileM / kLoaderWarps;
         RingPos<S> pos;
-        const int w = warp - 8;
-        for (int item = blockIdx.x; item < a.items && !*dead; item += gridDim.x) {
-            Item t;
-            if (!get_item(a, gr, item, BN, t) || t.g == a.G) continue;
-            constexpr int kRowsA = kTileM / kLoaderWarps;
-            int myrow = -1;   // lane i < 16: the row of tile row 8 i + w
-            if (lane < kRowsA && t.p0 + lane * kLoaderWarps + w < t.p1) myrow = row_at(a, t.p0 + lane * kLoaderWarps + w);
-            Matrix wm = a.w;
-            wm.p = static_cast<const T*>(wm.p) + t.g * a.w_group;
-            for (int k = 0; k < nk; ++k, pos.next()) {
-                if (!bounded_wait(empty + 8 * pos.stage, pos.phase ^ 1, dead)) break;
-                unsigned char* at = ring + pos.stage * Sh::kStage;
-                unsigned char* bt = at + Sh::P * Sh::kA;
-                const int c = k * kBoxCols + 2 * lane;
-                Pair<T> v[kRowsA];
-#pragma unroll
-                for (int i = 0; i < kRowsA; ++i) {
-                    const int r = __shfl_sync(0xffffffffu, myrow, i);
-                    if (r >= 0) v[i] = load_pair<T>(a.a, r, c);
-                    else v[i].a = v[i].b = from_f32<T>(0.f);
-                }
-#pragma unroll
-                for (int i = 0; i < kRowsA; ++i) store_pair<T>(at, Sh::kA, i * kLoaderWarps + w, lane, v[i]);
-                if constexpr (!kMN) {
-                    constexpr int kB8 = BN / kLoaderWarps;
-                    Pair<T> u[kB8];
-#pragma unroll
-                    for (int i = 0; i < kB8; ++i) {
-                        const int n = t.n0 + i * kLoaderWarps + w;
-                        if (n < a.cols) u[i] = load_pair<T>(wm, n, c);
-                        else u[i].a = u[i].b = from_f32<T>(0.f);
-                    }
-#pragma unroll
-                    for (int i = 0; i < kB8; ++i) store_pair<T>(bt, Sh::kB, i * kLoaderWarps + w, lane, u[i]);
-                } else {
-                    constexpr int kR8 = kBoxCols / kLoaderWarps;
-                    for (int box = 0; box * kBoxCols < BN && t.n0 + box * kBoxCols < a.cols; ++box) {
-                        Pair<T> u[kR8];
-#pragma unroll
-                        for (int i = 0; i < kR8; ++i) {
-                            const int r = k * kBoxCols + i * kLoaderWarps + w;
-                            if (r < a.red) u[i] = load_pair<T>(wm, r, t.n0 + box * kBoxCols + 2 * lane);
-                            else u[i].a = u[i].b = from_f32<T>(0.f);
-                        }
-#pragma unroll
-                        for (int i = 0; i < kR8; ++i)
-                            store_pair<T>(bt + box * kBoxCols * kBoxRow, Sh::kB, i * kLoaderWarps + w, lane, u[i]);
+        Item u;
+        auto row_of = [&](const Item& x) {   // lane i (and 16 + i): the row of tile row kPerA w + i
+            const int p = x.p0 + kPerA * w + (lane & 15);
+            return p < x.p1 ? row_at(a, p) : -1;
+        };
+        bool have = (!kTma || a.perm) && next_product(a, gr, item, BN, t);
+        int row = have ? row_of(t) : -1;
+        if constexpr (kTma) {
+            // copies run kLag stages ahead of the arrivals that tell of them
+            constexpr int kLag = S - 1;
+            RingPos<S> told;
+            int ahead = 0;
+            while (have && !is_dead(dead)) {
+                const bool more = next_product(a, gr, item, BN, u);
+                const int row_next = more ? row_of(u) : -1;
+                for (int k = 0; k < nk; ++k, pos.next()) {
+                    if (!bounded_wait(set.empty + 8 * pos.stage, pos.phase ^ 1, dead)) break;
+                    copy_rows<kTileM>(smem_u32(ring) + pos.stage * Sh::kStage, a.a, row, k * kBox, w, lane);
+                    copies_commit();
+                    if (++ahead > kLag) {
+                        copies_wait<kLag>();
+                        fence_async_smem();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(set.full + 8 * told.stage);
+                        told.next();
                     }
                 }
+                t = u;
+                row = row_next;
+                have = more;
+            }
+            copies_wait<0>();
+            fence_async_smem();
+            __syncwarp();
+            for (int i = imin(ahead, kLag); i > 0; --i, told.next())
+                if (lane == 0) mbar_arrive(set.full + 8 * told.stage);
+        } else {
+            // two groups of warps take the stages in turn; while one stage of a group is turned, its next is copied
+            // (rows that are not aligned take the room of both)
+            const int turn = (warp - 4 - kEpilogueWarps) / kLoaderWarps;
+            constexpr uint32_t kStride = 32 * kLoaderWarps * 16;
+            const bool aligned = a.a.aligned && a.w.aligned;
+            const uint32_t stride = aligned ? kStride : 2 * kStride;
+            unsigned char* mine = slots + turn * 2 * Sh::kParts * kStride + (w * 32 + lane) * (aligned ? 16 : 32);
+            uint32_t offs_a = 0, offs_b = 0;
+            int told = turn;   // the stage to be turned next
+            auto turn_stage = [&](unsigned char* from) {
+                const int st = told % S;
+                if (!bounded_wait(set.empty + 8 * st, (uint32_t)(told / S & 1) ^ 1, dead)) return;
+                unsigned char* at = ring + st * Sh::kStage;
+                Sh::PartsA::turn(from, stride, aligned, offs_a, at, Sh::kA, w, lane);
+                from += Sh::PartsA::kSteps * stride;
+#pragma unroll
+                for (int i = 0; i < Sh::kBoxes; ++i)
+                    Sh::PartsB::turn(from + i * Sh::PartsB::kSteps * stride, stride, aligned, offs_b >> (4 * i * Sh::PartsB::kSteps),
+                                     at + Sh::P * Sh::kA + i * Sh::kBoxB, Sh::kB, w, lane);
                 fence_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(full + 8 * pos.stage);
+                if (lane == 0) mbar_arrive(set.full + 8 * st);
+                told += 2;
+            };
+            int n = 0, copied = 0;
+            while (have && !is_dead(dead)) {
+                const bool more = next_product(a, gr, item, BN, u);
+                const int row_next = more ? row_of(u) : -1;
+                Matrix wm = a.w;
+                wm.p = static_cast<const T*>(wm.p) + t.g * a.w_group;
+                for (int k = 0; k < nk; ++k) {
+                    if ((n++ & 1) != turn) continue;
+                    unsigned char* to = mine + (aligned ? (copied & 1) * Sh::kParts * kStride : 0);
+                    const uint32_t to_s = smem_u32(to);
+                    offs_a = Sh::PartsA::copy(a.a, row, k * kBox, to_s, stride, aligned, lane);
+                    const int first = (kMN ? k * kBox : t.n0) + Sh::PartsB::kPer * w + lane % Sh::PartsB::kPer;
+                    const int row_b = first < (kMN ? a.red : a.cols) ? first : -1;
+                    offs_b = 0;
+#pragma unroll
+                    for (int i = 0; i < Sh::kBoxes; ++i)
+                        offs_b |= Sh::PartsB::copy(wm, row_b, kMN ? t.n0 + i * kBoxMN : k * kBox,
+                                                   to_s + (Sh::PartsA::kSteps + i * Sh::PartsB::kSteps) * stride, stride, aligned, lane)
+                                  << (4 * i * Sh::PartsB::kSteps);
+                    copies_commit();
+                    ++copied;
+                    if (!aligned) {
+                        copies_wait<0>();
+                        turn_stage(mine);
+                    } else if (copied > 1) {
+                        copies_wait<1>();
+                        turn_stage(mine + (copied & 1) * Sh::kParts * kStride);
+                    }
+                }
+                t = u;
+                row = row_next;
+                have = more;
             }
+            copies_wait<0>();
+            if (aligned && copied > 0 && !is_dead(dead)) turn_stage(mine + ((copied - 1) & 1) * Sh::kParts * kStride);
         }
     } else if (warp == 1) {
         RingPos<S> pos;
-        const uint32_t idesc = instr_desc<T>(false, kMN, BN);
         int n = 0;
-        for (int item = blockIdx.x; item < a.items && !*dead; item += gridDim.x) {
-            Item t;
-            if (!get_item(a, gr, item, BN, t) || t.g == a.G) continue;
-            const int buf = n & 1;
-            if (!bounded_wait(tempty + 8 * buf, ((n >> 1) & 1) ^ 1, dead)) break;
-            tc_fence_after();
-            for (int k = 0; k < nk; ++k, pos.next()) {
-                if (!bounded_wait(full + 8 * pos.stage, pos.phase, dead)) break;
-                tc_fence_after();
-                if (lane == 0) {
+        while (!is_dead(dead) && next_product(a, gr, item, BN, t)) {
+            if (lane == 0) {
+                for (int k = 0; k < nk; ++k, pos.next()) {
+                    const int buf = n & 1;
+                    if (k % kPerChunk == 0 && !bounded_wait_one(set.tempty + 8 * buf, ((n >> 1) & 1) ^ 1, dead)) break;
+                    if (!bounded_wait_one(set.full + 8 * pos.stage, pos.phase, dead)) break;
+                    tc_fence_after();
                     const uint32_t at = smem_u32(ring) + pos.stage * Sh::kStage;
-                    const int steps = (imin(kBoxCols, a.red - k * kBoxCols) + 15) / 16;
-                    issue_stage<T, false, kMN>(tmem + buf * BN, at, Sh::kA, 0, at + Sh::P * Sh::kA, Sh::kB,
-                                               kBoxCols * kBoxRow, idesc, steps, k > 0);
-                    tc_commit(empty + 8 * pos.stage);
+                    const int steps = (imin(kBox, a.red - k * kBox) + 15) / 16;
+                    issue_stage<T, false, kMN, BN>(set.tmem + buf * kSums<T> * BN, at, Sh::kA, 0, at + Sh::P * Sh::kA, Sh::kBoxB,
+                                                   steps, k % kPerChunk > 0);
+                    tc_commit(set.empty + 8 * pos.stage);
+                    if (k % kPerChunk == kPerChunk - 1 || k == nk - 1) {
+                        tc_commit(set.tfull + 8 * buf);
+                        ++n;
+                    }
                 }
-                __syncwarp();
             }
-            if (lane == 0) tc_commit(tfull + 8 * buf);
             __syncwarp();
-            ++n;
         }
-        if (*dead) {   // wait for the products in flight
-            if (lane == 0) tc_commit(done);
-            for (uint32_t i = 0; i < kDrainSpins && !mbar_try_wait(done, 0); ++i) {}
-        }
-    } else if (warp >= 4 && warp < 8) {
-        const int q = warp - 4;
-        unsigned char* stage = staging + q * kStageWarp;
+        if (is_dead(dead)) set.drain_products();
+    } else if (warp >= 4 && warp < 4 + 4 * Sh::kHalves) {
+        const int q = warp & 3, half = (warp - 4) >> 2;
+        constexpr int kCols = BN / Sh::kHalves;
+        unsigned char* stage = staging + (warp - 4) * kStageWarp;
         int n = 0;
-        for (int item = blockIdx.x; item < a.items && !*dead; item += gridDim.x) {
-            Item t;
-            if (!get_item(a, gr, item, BN, t)) continue;
+        while (!is_dead(dead) && next_item(a, gr, item, BN, t)) {
             const int p = t.p0 + 32 * q + lane;
             const int r = p < t.p1 ? row_at(a, p) : -1;
             T* row = r >= 0 ? static_cast<T*>(a.out) + r * a.out_ld + t.n0 : nullptr;
-            const int cols = imin(BN, a.cols - t.n0);
+            const int c0 = half * kCols, c1 = imin(c0 + kCols, a.cols - t.n0);
             if (t.g == a.G) {
-                store_tile<T>(kNoTile, cols, row, a.out_wide, stage, lane);
+                store_tile<T>(kNoTile, c0, c1, row, a.out_wide, stage, lane);
                 continue;
             }
-            const int buf = n & 1;
-            if (!bounded_wait(tfull + 8 * buf, (n >> 1) & 1, dead)) break;
-            tc_fence_after();
-            store_tile<T>(tmem + buf * BN + ((uint32_t)(32 * q) << 16), cols, row, a.out_wide, stage, lane);
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(tempty + 8 * buf);
-            ++n;
+            const uint32_t lanes = set.tmem + ((uint32_t)(32 * q) << 16);
+            if constexpr (kSums<T> == 1) {
+                const int buf = n & 1;
+                if (!bounded_wait(set.tfull + 8 * buf, (n >> 1) & 1, dead)) break;
+                tc_fence_after();
+                store_tile<T>(lanes + buf * BN, c0, c1, row, a.out_wide, stage, lane);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(set.tempty + 8 * buf);
+                ++n;
+            } else {
+                static_assert(kSums<T> == 1 || kCols == 32, "a warp's columns of an fp32 tile fit one register array");
+                float acc[32];
+#pragma unroll
+                for (int i = 0; i < 32; ++i) acc[i] = 0.f;
+                bool ok = true;
+                for (int k = 0; k < nk; k += kPerChunk, ++n) {
+                    const int buf = n & 1;
+                    if (!(ok = bounded_wait(set.tfull + 8 * buf, (n >> 1) & 1, dead))) break;
+                    tc_fence_after();
+                    const uint32_t from = lanes + buf * kSums<T> * BN + c0;
+                    add_chunk(from, BN, acc);
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(set.tempty + 8 * buf);
+                }
+                if (!ok) break;
+                if (c0 < c1) emit32<T>(acc, c1 - c0, row ? row + c0 : nullptr, a.out_wide, stage, lane);
+            }
         }
     }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    if (warp == 2) tmem_free(tmem, Sh::kTmemCols);
+    set.end();
 }
 
 template <typename T, bool kTma, bool kMN, int BN>
@@ -269,8 +310,8 @@ zs_status launch_rows(const char* fn, RowsArgs a, cudaStream_t s) {
     if (kTma) {
         constexpr bool bf16 = std::is_same<T, __nv_bfloat16>::value;
         const int w_rows = kMN ? a.red : a.cols;
-        if (!encode_boxes(&a_map, bf16, a.a.p, a.red, a.M, a.a.ld, 0, a.perm ? 1 : kTileM) ||
-            !encode_boxes(&w_map, bf16, a.w.p, a.w.ld, w_rows, a.w.ld, a.G, kMN ? kBoxCols : BN))
+        if (!encode_boxes(&a_map, bf16, a.a.p, a.red, a.M, a.a.ld, 0, kTileM) ||
+            !encode_boxes(&w_map, bf16, a.w.p, a.w.ld, w_rows, a.w.ld, a.G, kMN ? kStageK<T> : BN))
             return fail(ZS_ERR_CUDA, "%s: a tensor map was refused", fn);
     }
     a.ntiles = (a.cols + BN - 1) / BN;
@@ -285,11 +326,13 @@ zs_status launch_rows(const char* fn, RowsArgs a, cudaStream_t s) {
 
 template <typename T, bool kTma, bool kMN>
 zs_status launch_rows(const char* fn, const RowsArgs& a, cudaStream_t s) {
-    if (a.cols <= 32) return launch_rows<T, kTma, kMN, 32>(fn, a, s);
-    if (a.cols <= 64) return launch_rows<T, kTma, kMN, 64>(fn, a, s);
+    if constexpr (!kMN || sizeof(T) == 2)   // an MN-major plane of fp32 is a box wide
+        if (a.cols <= 32) return launch_rows<T, kTma, kMN, 32>(fn, a, s);
     if constexpr (kTma)
-        if ((a.cols + 127) / 128 % 2 == 0) return launch_rows<T, kTma, kMN, 256>(fn, a, s);
-    return launch_rows<T, kTma, kMN, 128>(fn, a, s);
+        if (a.cols > 64 && (a.cols + 127) / 128 % 2 == 0) return launch_rows<T, kTma, kMN, 256>(fn, a, s);
+    if constexpr (sizeof(T) == 2)
+        if (a.cols > 64) return launch_rows<T, kTma, kMN, 128>(fn, a, s);
+    return launch_rows<T, kTma, kMN, 64>(fn, a, s);
 }
 
 template <typename T>
@@ -313,8 +356,8 @@ zs_status grouped_rows(const char* fn, int32_t dtype, const void* x, int64_t x_l
     RowsArgs a = {};
     a.red = transposed ? N : K;
     a.cols = transposed ? K : N;
-    a.a = {x, x_ld, a.red, at(x, 2 * es) && x_ld % 2 == 0};
-    a.w = {w, K, K, at(w, 2 * es) && K % 2 == 0};
+    a.a = {x, x_ld, a.red, at(x, 16) && x_ld % per16 == 0};
+    a.w = {w, K, K, at(w, 16) && K % per16 == 0};
     a.w_group = (int64_t)K * N;
     a.row_ptr = row_ptr;
     a.perm = perm;
@@ -323,7 +366,7 @@ zs_status grouped_rows(const char* fn, int32_t dtype, const void* x, int64_t x_l
     a.out_wide = at(out, 16) && out_ld % per16 == 0 && a.cols % per16 == 0;
     a.M = (int)M;
     a.G = G;
-    const bool aligned = at(x, 16) && x_ld % per16 == 0 && at(w, 16) && K % per16 == 0 && G > 0;
+    const bool aligned = a.a.aligned && a.w.aligned && G > 0;
     switch (dtype) {
         case ZS_F32: return rows_product<float>(fn, a, transposed, false, s);
         case ZS_BF16: return rows_product<__nv_bfloat16>(fn, a, transposed, aligned, s);

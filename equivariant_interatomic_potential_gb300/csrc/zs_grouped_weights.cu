@@ -6,9 +6,12 @@
 // the device alone.  A unit of work is 64 positions of one group for one
 // 128 x BN tile of the weights; units are numbered tile by tile, and each CTA
 // takes an equal range of them, so that skewed groups, few tiles and many
-// tiles all keep every SM busy.  A range cuts at most the group it starts in
-// and the group it ends in: those two sums go to the workspace in fp32, and a
-// second kernel adds, for each group that was cut, its CTAs' parts in order.
+// tiles all keep every SM busy.  (Each group also counts kFlush units for
+// writing its tile.)  A range cuts at most the group it starts in and the
+// group it ends in: those two sums go to the workspace in fp32, and a second
+// kernel adds, for each group that was cut, its CTAs' parts in order.
+#include <initializer_list>
+
 #include "zs_grouped.cuh"
 #include "zs_mma.cuh"
 
@@ -16,9 +19,10 @@ namespace zs {
 
 namespace {
 
-constexpr int kLoaderWarps = 8;
-constexpr int kStep = 64;        // positions of a unit: rows of a box
-constexpr int kPartRows = 16;    // rows of a tile that one CTA of the second kernel adds
+constexpr int kFlush = 2;        // units that writing a tile costs
+constexpr int kPartRows = 4;     // rows of a tile that one CTA of the second kernel adds
+template <typename T>
+using WeightGroups = Groups<kStageK<T>, kFlush>;   // a unit's positions are a stage's
 
 struct WeightArgs {
     Matrix dy, x;
@@ -29,62 +33,65 @@ struct WeightArgs {
     bool dw_wide;
     int M, G, N, K;
     int ktiles;
-    int64_t slots;       // units of a tile, empty ones of no group at its end among them
-    int64_t units, per;  // all units, units of a CTA
+    int slots;           // units of a tile, empty ones of no group at its end among them
+    int units, per;      // all units, units of a CTA
 };
 
 template <typename T, bool kTma, int BN>
 struct WeightShape {
-    static constexpr int P = kPlanes<T>;
-    static constexpr int kBBoxes = BN < kBoxCols ? 1 : BN / kBoxCols;
-    static constexpr uint32_t kBox = kStep * kBoxRow;
-    static constexpr uint32_t kA = 2 * kBox, kB = kBBoxes * kBox;
+    static constexpr int P = kPlanes<T>, kUnit = kStageK<T>;
+    static constexpr int kABoxes = kTileM / kBoxMN, kBBoxes = (BN + kBoxMN - 1) / kBoxMN;
+    static constexpr uint32_t kBox = box_bytes<kBoxMN>(kUnit);
+    static constexpr uint32_t kA = kABoxes * kBox, kB = kBBoxes * kBox;
     static constexpr uint32_t kStage = P * (kA + kB);
-    static constexpr int kFixed = 4 * kStageWarp + 1024 + 512;
+    // what the loader warps copy into before they turn it, as in the products over rows
+    using Parts = BoxParts<T, kUnit, kBoxMN>;
+    static constexpr int kParts = (kABoxes + kBBoxes) * Parts::kSteps;
+    static constexpr int kSlots = kTma ? 0 : 4 * kParts * 32 * kLoaderWarps * 16;
+    static constexpr int kHalves = BN >= 64 ? 2 : 1;   // warps that share 32 rows of a tile
+    static constexpr uint32_t kTmemCols = tmem_cols(2 * kSums<T> * BN);
+    static constexpr int kFixed = kSlots + kEpilogueWarps * kStageWarp + 1024 + 4608;   // staging, alignment, barriers and groups
     static constexpr int kFit = (kSmemMost - kFixed) / (int)kStage;
     static constexpr int S = kFit > 8 ? 8 : kFit;
-    static_assert(S >= 2, "two stages at least");
+    static_assert(kPlanes<T> == 1 || BN == kBoxMN, "the planes of the right operand follow each other");
+    static_assert(S >= 2 && Setup<S, kTmemCols, kUnit, kFlush>::kBytes <= 4608, "two stages at least");
     static constexpr int kSmem = S * (int)kStage + kFixed;
-    static constexpr int kThreads = 256 + (kTma ? 0 : 32 * kLoaderWarps);
-    static constexpr uint32_t kTmemCols = 2 * BN;
+    static constexpr int kThreads = 32 * (4 + kEpilogueWarps + (kTma ? 1 : 2) * kLoaderWarps);
 };
 
-// A maximal run of a CTA's units within one group and one tile.
+// The part of one group's sum for one tile that a CTA forms.
 struct Segment {
     int g, n0, k0;
-    int p0, p1;        // positions (p0 == p1: none)
-    bool whole;        // all of the group: written as it is
+    int p0, p1;        // positions (none: an empty group, whose sum is zero)
+    bool whole;        // all of the group's positions: written as it is
     int part;          // else which of the CTA's two partial tiles
 };
 
-// Walks the segments of units [u, end).
-template <int BN>
+// Walks the segments of a CTA's units.  Whole warps.
+template <typename T, int BN>
 struct Walk {
     const WeightArgs& a;
-    Groups<kStep> gr;
-    int64_t u, begin, end;
-    __device__ __forceinline__ Walk(const WeightArgs& args, int64_t cta)
-        : a(args), gr{args.row_ptr, args.G, args.M}, u(cta * args.per), begin(u), end(imin(u + args.per, args.units)) {}
+    const WeightGroups<T>& gr;
+    int u, begin, end, last;
+    __device__ __forceinline__ Walk(const WeightArgs& args, const WeightGroups<T>& groups)
+        : a(args), gr(groups), u(blockIdx.x * args.per), begin(u), end(imin(u + args.per, args.units)), last(groups.slot(args.G)) {}
     __device__ __forceinline__ bool next(Segment& s) {
         while (u < end) {
-            const int64_t t = u / a.slots, slot = u - t * a.slots;
-            const int64_t last = gr.slot(a.G);       // slots of groups
-            if (slot >= last) {
-                u = (t + 1) * a.slots;
+            const int t = u / a.slots, first = t * a.slots, slot = u - first, from = u;
+            if (slot >= last) {          // units of no group
+                u = first + a.slots;
                 continue;
             }
             s.g = gr.find(slot, a.G);
-            const int64_t g0 = gr.slot(s.g), g1 = gr.slot(s.g + 1);
-            const int b = gr.start(s.g), e = gr.start(s.g + 1);
-            const int64_t stop = imin(end, t * a.slots + g1);
-            s.n0 = (int)(t / a.ktiles) * kTileM;
-            s.k0 = (int)(t % a.ktiles) * BN;
-            s.whole = slot == g0 && stop == t * a.slots + g1;
-            s.part = u == begin ? 0 : 1;
-            s.p0 = (int)imin<int64_t>(b + (slot - g0) * kStep, e);
-            s.p1 = (int)imin<int64_t>(b + (stop - t * a.slots - g0) * kStep, e);
-            u = stop;
-            return true;
+            const int g0 = gr.slot(s.g), b = gr.start(s.g), e = gr.start(s.g + 1);
+            u = imin(end, first + gr.slot(s.g + 1));
+            s.n0 = t / a.ktiles * kTileM;
+            s.k0 = t % a.ktiles * BN;
+            s.p0 = (int)imin<int64_t>(b + (int64_t)(slot - g0) * kStageK<T>, e);
+            s.p1 = (int)imin<int64_t>(b + (int64_t)(u - first - g0) * kStageK<T>, e);
+            s.whole = s.p0 == b && s.p1 == e;
+            s.part = from == begin ? 0 : 1;
+            if (s.p0 < s.p1 || (b == e && slot == g0)) return true;   // else only units that count for writing
         }
         return false;
     }
@@ -103,203 +110,268 @@ weights_mma(const __grid_constant__ CUtensorMap dy_map, const __grid_constant__ 
     constexpr int S = Sh::S;
     extern __shared__ unsigned char raw[];
     unsigned char* ring = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
-    unsigned char* staging = ring + S * Sh::kStage;
-    uint64_t* bars = reinterpret_cast<uint64_t*>(staging + 4 * kStageWarp);
-    volatile int* dead = reinterpret_cast<volatile int*>(bars + 2 * S + 5);
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * S + 6);
-    const uint32_t full = smem_u32(bars), empty = full + 8 * S, tfull = empty + 8 * S, tempty = tfull + 16, done = tempty + 16;
+    unsigned char* slots = ring + S * Sh::kStage;
+    unsigned char* staging = slots + Sh::kSlots;
+    constexpr int kUnit = Sh::kUnit;
+    Setup<S, Sh::kTmemCols, kUnit, kFlush> set;
+    set.begin(staging + kEpilogueWarps * kStageWarp, kTma && !a.perm ? 1 : kLoaderWarps, 4 * Sh::kHalves, a.row_ptr, a.G, a.M);
+    volatile int* dead = set.dead;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < S; ++i) {
-            mbar_init(full + 8 * i, kTma ? 1 : kLoaderWarps);
-            mbar_init(empty + 8 * i, 1);
-        }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(tfull + 8 * i, 1);
-            mbar_init(tempty + 8 * i, 4);
-        }
-        mbar_init(done, 1);
-        *dead = 0;
-        mbar_fence_init();
-    }
-    pdl_wait();
-    pdl_trigger();
-    if (warp == 2) tmem_alloc(smem_u32(tmem_slot), Sh::kTmemCols);
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
-    Walk<BN> walk(a, blockIdx.x);
+    Walk<T, BN> walk(a, set.groups);
     Segment s;
+    constexpr int kPerChunk = kSums<T> > 1 ? kChunk : 1 << 30;   // positions between hand-overs to the epilogue
 
-    if (kTma && warp == 0) {
+    if (kTma && warp == 0 && !a.perm) {
         RingPos<S> pos;
         int issued = 0;
-        while (!*dead && walk.next(s)) {
-            const int a_boxes = imin(2, (a.N - s.n0 + kBoxCols - 1) / kBoxCols);
-            const int b_boxes = imin(Sh::kBBoxes, (a.K - s.k0 + kBoxCols - 1) / kBoxCols);
-            for (int p = s.p0; p < s.p1; p += kStep, pos.next()) {
-                // lanes 0..15: four rows each (of 64); the last one again past the end
-                const int quads = imin(kStep / 4, (s.p1 - p + 3) / 4);
-                int4 rows = make_int4(0, 0, 0, 0);
-                if (a.perm && lane < quads) {
-                    int* r = &rows.x;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) r[i] = imax(row_at(a, imin(p + 4 * lane + i, s.p1 - 1)), 0);
+        while (!is_dead(dead) && walk.next(s)) {
+            const int a_boxes = imin(2, (a.N - s.n0 + kBoxMN - 1) / kBoxMN);
+            const int b_boxes = imin(Sh::kBBoxes, (a.K - s.k0 + kBoxMN - 1) / kBoxMN);
+            if (lane == 0) {
+                for (int p = s.p0; p < s.p1; p += kUnit, ++issued, pos.next()) {
+                    if (!bounded_wait_one(set.empty + 8 * pos.stage, pos.phase ^ 1, dead)) break;
+                    const uint32_t bar = set.full + 8 * pos.stage, at = smem_u32(ring) + pos.stage * Sh::kStage, bt = at + Sh::kA;
+                    mbar_arrive_expect_tx(bar, (a_boxes + b_boxes) * Sh::kBox);
+                    for (int i = 0; i < a_boxes; ++i) tma_2d(at + i * Sh::kBox, &dy_map, s.n0 + i * kBoxMN, p, bar);
+                    for (int i = 0; i < b_boxes; ++i) tma_2d(bt + i * Sh::kBox, &x_map, s.k0 + i * kBoxMN, p, bar);
                 }
-                if (!bounded_wait(empty + 8 * pos.stage, pos.phase ^ 1, dead)) break;
-                const uint32_t bar = full + 8 * pos.stage, at = smem_u32(ring) + pos.stage * Sh::kStage, bt = at + Sh::kA;
-                if (lane == 0) mbar_arrive_expect_tx(bar, (a_boxes + b_boxes) * (a.perm ? quads * 512u : Sh::kBox));
-                __syncwarp();
-                if (a.perm) {
-                    if (lane < quads) {
-                        for (int i = 0; i < a_boxes; ++i)
-                            tma_gather4(at + i * Sh::kBox + lane * 512, &dy_map, s.n0 + i * kBoxCols, rows, bar);
-                        for (int i = 0; i < b_boxes; ++i)
-                            tma_gather4(bt + i * Sh::kBox + lane * 512, &x_map, s.k0 + i * kBoxCols, rows, bar);
-                    }
-                } else {
-                    if (lane < a_boxes) tma_2d(at + lane * Sh::kBox, &dy_map, s.n0 + lane * kBoxCols, p, bar);
-                    if (lane < b_boxes) tma_2d(bt + lane * Sh::kBox, &x_map, s.k0 + lane * kBoxCols, p, bar);
-                }
-                ++issued;
             }
+            __syncwarp();
         }
-        if (*dead) {   // wait for the copies in flight
-            for (int i = 0; i < imin(issued, S); ++i) {
-                const int k = issued - 1 - i;
-                for (uint32_t n = 0; n < kDrainSpins && !mbar_try_wait(full + 8 * (k % S), (uint32_t)(k / S) & 1); ++n) {}
-            }
-        }
-    } else if (!kTma && warp >= 8) {
+        issued = __shfl_sync(0xffffffffu, issued, 0);
+        if (is_dead(dead)) set.drain_copies(issued);
+    } else if (warp >= 4 + kEpilogueWarps && (!kTma || a.perm)) {
+        const int w = (warp - 4 - kEpilogueWarps) % kLoaderWarps;
         RingPos<S> pos;
-        const int w = warp - 8;
-        while (!*dead && walk.next(s)) {
-            for (int p = s.p0; p < s.p1; p += kStep, pos.next()) {
-                constexpr int kRows = kStep / kLoaderWarps;
-                int myrow = -1;   // lane i < 8: the row at position p + 8 i + w
-                if (lane < kRows && p + lane * kLoaderWarps + w < s.p1) myrow = row_at(a, p + lane * kLoaderWarps + w);
-                if (!bounded_wait(empty + 8 * pos.stage, pos.phase ^ 1, dead)) break;
-                unsigned char* at = ring + pos.stage * Sh::kStage;
-                auto bring = [&](const Matrix& m, unsigned char* to, uint32_t plane, int c0, int boxes) {
-                    for (int box = 0; box < boxes && c0 + box * kBoxCols < m.cols; ++box) {
-                        Pair<T> v[kRows];
+        constexpr int kPer = kUnit / kLoaderWarps;
+        auto row_of = [&](int p) {   // lane i (and 8 j + i) < 8: the row at position p + 8 w + i
+            const int at = p + kPer * w + (lane & (kPer - 1));
+            return at < s.p1 ? row_at(a, at) : -1;
+        };
+        if constexpr (kTma) {
+            // copies run kLag stages ahead of the arrivals that tell of them
+            constexpr int kLag = S - 1;
+            RingPos<S> told;
+            int ahead = 0;
+            while (!is_dead(dead) && walk.next(s)) {
+                int row = row_of(s.p0);
+                for (int p = s.p0; p < s.p1; p += kUnit, pos.next()) {
+                    const int mine = row;
+                    row = row_of(p + kUnit);
+                    if (!bounded_wait(set.empty + 8 * pos.stage, pos.phase ^ 1, dead)) break;
+                    const uint32_t at = smem_u32(ring) + pos.stage * Sh::kStage;
 #pragma unroll
-                        for (int i = 0; i < kRows; ++i) {
-                            const int r = __shfl_sync(0xffffffffu, myrow, i);
-                            if (r >= 0) v[i] = load_pair<T>(m, r, c0 + box * kBoxCols + 2 * lane);
-                            else v[i].a = v[i].b = from_f32<T>(0.f);
-                        }
+                    for (int i = 0; i < 2; ++i)
+                        if (s.n0 + i * kBoxMN < a.N) copy_rows<kUnit>(at + i * Sh::kBox, a.dy, mine, s.n0 + i * kBoxMN, w, lane);
 #pragma unroll
-                        for (int i = 0; i < kRows; ++i) store_pair<T>(to + box * Sh::kBox, plane, i * kLoaderWarps + w, lane, v[i]);
+                    for (int i = 0; i < Sh::kBBoxes; ++i)
+                        if (s.k0 + i * kBoxMN < a.K) copy_rows<kUnit>(at + Sh::kA + i * Sh::kBox, a.x, mine, s.k0 + i * kBoxMN, w, lane);
+                    copies_commit();
+                    if (++ahead > kLag) {
+                        copies_wait<kLag>();
+                        fence_async_smem();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(set.full + 8 * told.stage);
+                        told.next();
                     }
-                };
-                bring(a.dy, at, Sh::kA, s.n0, 2);
-                bring(a.x, at + Sh::P * Sh::kA, Sh::kB, s.k0, Sh::kBBoxes);
+                }
+            }
+            copies_wait<0>();
+            fence_async_smem();
+            __syncwarp();
+            for (int i = imin(ahead, kLag); i > 0; --i, told.next())
+                if (lane == 0) mbar_arrive(set.full + 8 * told.stage);
+        } else {
+            // two groups of warps take the stages in turn; while one stage of a group is turned, its next is copied
+            // (rows that are not aligned take the room of both)
+            using Parts = typename Sh::Parts;
+            const int turn = (warp - 4 - kEpilogueWarps) / kLoaderWarps;
+            constexpr uint32_t kStride = 32 * kLoaderWarps * 16;
+            const bool aligned = a.dy.aligned && a.x.aligned;
+            const uint32_t stride = aligned ? kStride : 2 * kStride;
+            unsigned char* mine = slots + turn * 2 * Sh::kParts * kStride + (w * 32 + lane) * (aligned ? 16 : 32);
+            constexpr int kAll = Sh::kABoxes + Sh::kBBoxes;
+            uint32_t offs[kAll] = {};
+            int told = turn;   // the stage to be turned next
+            auto turn_stage = [&](const unsigned char* from) {
+                const int st = told % S;
+                if (!bounded_wait(set.empty + 8 * st, (uint32_t)(told / S & 1) ^ 1, dead)) return;
+                unsigned char* at = ring + st * Sh::kStage;
+#pragma unroll
+                for (int i = 0; i < kAll; ++i) {
+                    const bool of_a = i < Sh::kABoxes;
+                    Parts::turn(from + i * Parts::kSteps * stride, stride, aligned, offs[i],
+                                of_a ? at + i * Sh::kBox : at + Sh::P * Sh::kA + (i - Sh::kABoxes) * Sh::kBox,
+                                of_a ? Sh::kA : Sh::kB, w, lane);
+                }
                 fence_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(full + 8 * pos.stage);
+                if (lane == 0) mbar_arrive(set.full + 8 * st);
+                told += 2;
+            };
+            int n = 0, copied = 0;
+            while (!is_dead(dead) && walk.next(s)) {
+                int row = row_of(s.p0);
+                for (int p = s.p0; p < s.p1; p += kUnit) {
+                    const int here = row;
+                    row = row_of(p + kUnit);
+                    if ((n++ & 1) != turn) continue;
+                    unsigned char* to = mine + (aligned ? (copied & 1) * Sh::kParts * kStride : 0);
+                    const uint32_t to_s = smem_u32(to);
+#pragma unroll
+                    for (int i = 0; i < kAll; ++i) {
+                        const bool of_a = i < Sh::kABoxes;
+                        offs[i] = Parts::copy(of_a ? a.dy : a.x, here, of_a ? s.n0 + i * kBoxMN : s.k0 + (i - Sh::kABoxes) * kBoxMN,
+                                              to_s + i * Parts::kSteps * stride, stride, aligned, lane);
+                    }
+                    copies_commit();
+                    ++copied;
+                    if (!aligned) {
+                        copies_wait<0>();
+                        turn_stage(mine);
+                    } else if (copied > 1) {
+                        copies_wait<1>();
+                        turn_stage(mine + (copied & 1) * Sh::kParts * kStride);
+                    }
+                }
             }
+            copies_wait<0>();
+            if (aligned && copied > 0 && !is_dead(dead)) turn_stage(mine + ((copied - 1) & 1) * Sh::kParts * kStride);
         }
     } else if (warp == 1) {
         RingPos<S> pos;
-        const uint32_t idesc = instr_desc<T>(true, true, BN);
         int n = 0;
-        while (!*dead && walk.next(s)) {
-            if (s.p0 == s.p1) continue;
-            const int buf = n & 1;
-            if (!bounded_wait(tempty + 8 * buf, ((n >> 1) & 1) ^ 1, dead)) break;
+        // a stage's products, by lane 0
+        auto products = [&](int p) {
+            const int buf = n & 1, since = (p - s.p0) % kPerChunk, steps = (imin(kUnit, s.p1 - p) + 15) / 16;
+            const uint32_t at = smem_u32(ring) + pos.stage * Sh::kStage;
             tc_fence_after();
-            for (int p = s.p0; p < s.p1; p += kStep, pos.next()) {
-                if (!bounded_wait(full + 8 * pos.stage, pos.phase, dead)) break;
-                const int rows = imin(kStep, s.p1 - p), steps = (rows + 15) / 16;
-                unsigned char* at = ring + pos.stage * Sh::kStage;
-                if (kTma && rows < 16 * steps) {
-                    // positions past the segment's end hold other rows, or nothing: they count as zeros
-                    const int chunks = (16 * steps - rows) * (kBoxRow / 16);
-                    for (int i = lane; i < chunks * (2 + Sh::kBBoxes); i += 32)
-                        *reinterpret_cast<uint4*>(at + (i / chunks) * Sh::kBox + rows * kBoxRow + (i % chunks) * 16) = make_uint4(0, 0, 0, 0);
+            issue_stage<T, true, true, BN>(set.tmem + buf * kSums<T> * BN, at, Sh::kA, Sh::kBox, at + Sh::P * Sh::kA, Sh::kBox,
+                                           steps, since > 0);
+            tc_commit(set.empty + 8 * pos.stage);
+            if (since + kUnit >= kPerChunk || p + kUnit >= s.p1) {
+                tc_commit(set.tfull + 8 * buf);
+                ++n;
+            }
+        };
+        auto ready = [&](int p) {
+            const int buf = n & 1;
+            return ((p - s.p0) % kPerChunk != 0 || bounded_wait_one(set.tempty + 8 * buf, ((n >> 1) & 1) ^ 1, dead)) &&
+                   bounded_wait_one(set.full + 8 * pos.stage, pos.phase, dead);
+        };
+        while (!is_dead(dead) && walk.next(s)) {
+            // positions past the segment's end hold other rows where TMA brought them: they count as zeros
+            const bool ragged = kTma && !a.perm && (s.p1 - s.p0) % 16 != 0;
+            int p = s.p0;
+            if (lane == 0)
+                for (; p < s.p1 && !(ragged && p + kUnit > s.p1) && ready(p); p += kUnit, pos.next()) products(p);
+            if (ragged) {
+                bool ok = true;
+                if (lane == 0) ok = p + kUnit > s.p1 && ready(p);
+                ok = __shfl_sync(0xffffffffu, ok, 0);
+                const int stage_now = __shfl_sync(0xffffffffu, pos.stage, 0);
+                if (ok) {
+                    const int rows = (s.p1 - s.p0) % kUnit, pieces = (((rows + 15) & ~15) - rows) * (kBoxMN / 8);
+                    unsigned char* at = ring + stage_now * Sh::kStage + rows * (kBoxMN * 2);
+                    for (int i = lane; i < pieces * (Sh::kABoxes + Sh::kBBoxes); i += 32)
+                        *reinterpret_cast<uint4*>(at + i / pieces * Sh::kBox + i % pieces * 16) = make_uint4(0, 0, 0, 0);
                     fence_async_smem();
                     __syncwarp();
+                    if (lane == 0) {
+                        products(p);
+                        pos.next();
+                    }
                 }
-                tc_fence_after();
-                if (lane == 0) {
-                    const uint32_t aa = smem_u32(at);
-                    issue_stage<T, true, true>(tmem + buf * BN, aa, Sh::kA, Sh::kBox, aa + Sh::P * Sh::kA, Sh::kB, Sh::kBox,
-                                               idesc, steps, p > s.p0);
-                    tc_commit(empty + 8 * pos.stage);
-                }
-                __syncwarp();
             }
-            if (lane == 0) tc_commit(tfull + 8 * buf);
             __syncwarp();
-            ++n;
         }
-        if (*dead) {   // wait for the products in flight
-            if (lane == 0) tc_commit(done);
-            for (uint32_t i = 0; i < kDrainSpins && !mbar_try_wait(done, 0); ++i) {}
-        }
-    } else if (warp >= 4 && warp < 8) {
-        const int q = warp - 4, r = 32 * q + lane;
-        unsigned char* stage = staging + q * kStageWarp;
+        if (is_dead(dead)) set.drain_products();
+    } else if (warp >= 4 && warp < 4 + 4 * Sh::kHalves) {
+        const int q = warp & 3, half = (warp - 4) >> 2, r = 32 * q + lane;
+        constexpr int kMine = BN / Sh::kHalves;
+        unsigned char* stage = staging + (warp - 4) * kStageWarp;
+        const uint32_t lanes = set.tmem + ((uint32_t)(32 * q) << 16);
         int n = 0;
-        while (!*dead && walk.next(s)) {
-            const bool some = s.p0 < s.p1;
-            const int buf = n & 1;
-            if (some) {
-                if (!bounded_wait(tfull + 8 * buf, (n >> 1) & 1, dead)) break;
-                tc_fence_after();
-            }
-            const uint32_t from = some ? tmem + buf * BN + ((uint32_t)(32 * q) << 16) : kNoTile;
-            const int cols = imin(BN, a.K - s.k0);
-            if (s.whole) {
-                T* row = s.n0 + r < a.N ? static_cast<T*>(a.dw) + ((int64_t)s.g * a.N + s.n0 + r) * a.K + s.k0 : nullptr;
-                store_tile<T>(from, cols, row, a.dw_wide, stage, lane);
+        while (!is_dead(dead) && walk.next(s)) {
+            const bool some = s.p0 < s.p1, mine = s.n0 + r < a.N;
+            const int c0 = half * kMine, c1 = imin(c0 + kMine, a.K - s.k0);
+            T* row = mine ? static_cast<T*>(a.dw) + ((int64_t)s.g * a.N + s.n0 + r) * a.K + s.k0 : nullptr;
+            float* part = mine ? a.partial + (((int64_t)blockIdx.x * 2 + s.part) * kTileM + r) * BN : nullptr;
+            const int c1_part = imin((c1 + 3) / 4 * 4, c0 + kMine);   // whole pieces of a partial tile's rows
+            if constexpr (kSums<T> == 1) {
+                const int buf = n & 1;
+                if (some) {
+                    if (!bounded_wait(set.tfull + 8 * buf, (n >> 1) & 1, dead)) break;
+                    tc_fence_after();
+                }
+                const uint32_t from = some ? lanes + buf * BN : kNoTile;
+                if (s.whole) store_tile<T>(from, c0, c1, row, a.dw_wide, stage, lane);
+                else store_tile<float>(from, c0, c1_part, part, true, stage, lane);
+                if (some) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(set.tempty + 8 * buf);
+                    ++n;
+                }
             } else {
-                float* row = s.n0 + r < a.N ? a.partial + (((int64_t)blockIdx.x * 2 + s.part) * kTileM + r) * BN : nullptr;
-                store_tile<float>(from, (cols + 3) / 4 * 4, row, true, stage, lane);
-            }
-            if (some) {
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(tempty + 8 * buf);
-                ++n;
+                static_assert(kSums<T> == 1 || kMine == 32, "a warp's columns of an fp32 tile fit one register array");
+                float acc[32];
+#pragma unroll
+                for (int i = 0; i < 32; ++i) acc[i] = 0.f;
+                bool ok = true;
+                for (int p = s.p0; p < s.p1; p += kPerChunk, ++n) {
+                    const int buf = n & 1;
+                    if (!(ok = bounded_wait(set.tfull + 8 * buf, (n >> 1) & 1, dead))) break;
+                    tc_fence_after();
+                    const uint32_t from = lanes + buf * kSums<T> * BN + c0;
+                    add_chunk(from, BN, acc);
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(set.tempty + 8 * buf);
+                }
+                if (!ok) break;
+                if (c0 >= c1) continue;
+                if (s.whole) emit32<T>(acc, c1 - c0, row ? row + c0 : nullptr, a.dw_wide, stage, lane);
+                else emit32<float>(acc, c1_part - c0, part ? part + c0 : nullptr, true, stage, lane);
             }
         }
     }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    if (warp == 2) tmem_free(tmem, Sh::kTmemCols);
+    set.end();
 }
 
 // Block (x, y): the group and tile that CTA x + 1's range begins inside of, if
-// CTA x holds its beginning; rows y * kPartRows .. of the tile.
+// CTA x holds its first positions; rows y * kPartRows .. of the tile, 4
+// columns a thread.
 template <typename T, int BN>
 __global__ void __launch_bounds__(256) weights_join(const WeightArgs a) {
     pdl_wait();
     pdl_trigger();
-    const Groups<kStep> gr{a.row_ptr, a.G, a.M};
-    const int64_t cut = (blockIdx.x + 1) * a.per;
+    const WeightGroups<T> gr{a.row_ptr, a.G, a.M, false};
+    const int cut = (blockIdx.x + 1) * a.per;
     if (cut >= a.units) return;
-    const int64_t t = cut / a.slots, slot = cut - t * a.slots;
+    const int t = cut / a.slots, slot = cut - t * a.slots;
     if (slot >= gr.slot(a.G)) return;
     const int g = gr.find(slot, a.G);
-    const int64_t u0 = t * a.slots + gr.slot(g), u1 = imin(t * a.slots + gr.slot(g + 1), a.units);
-    if (u0 >= cut) return;                          // the group begins with CTA x + 1
-    const int64_t first = u0 / a.per, last = (u1 - 1) / a.per;
-    if (first != blockIdx.x) return;                // an earlier block adds it
-    const int first_part = u0 == first * a.per ? 0 : 1;
-    const int n0 = (int)(t / a.ktiles) * kTileM + blockIdx.y * kPartRows, k0 = (int)(t % a.ktiles) * BN;
+    const int b = gr.start(g), e = gr.start(g + 1);
+    const int u0 = t * a.slots + gr.slot(g), u1 = u0 + (e - b + kStageK<T> - 1) / kStageK<T>;   // units with positions
+    if (u0 >= cut || u1 <= cut) return;             // the group is not cut here
+    const int first = u0 / a.per, last = (u1 - 1) / a.per;
+    if (first != (int)blockIdx.x) return;           // an earlier block adds it
+    const int n0 = t / a.ktiles * kTileM + blockIdx.y * kPartRows, k0 = t % a.ktiles * BN;
     const int cols = imin(BN, a.K - k0), rows = imin(kPartRows, a.N - n0);
-    for (int i = threadIdx.x; i < rows * BN; i += blockDim.x) {
-        const int r = i / BN, c = i % BN;
+    constexpr int64_t kTile = (int64_t)kTileM * BN;
+    for (int i = threadIdx.x; i < rows * (BN / 4); i += blockDim.x) {
+        const int r = i / (BN / 4), c = i % (BN / 4) * 4;
         if (c >= cols) continue;
-        const int64_t at = ((int64_t)blockIdx.y * kPartRows + r) * BN + c;
-        float sum = __ldg(a.partial + (first * 2 + first_part) * kTileM * BN + at);
-        for (int64_t p = first + 1; p <= last; ++p) sum += __ldg(a.partial + p * 2 * kTileM * BN + at);
-        static_cast<T*>(a.dw)[((int64_t)g * a.N + n0 + r) * a.K + k0 + c] = from_f32<T>(sum);
+        const float* at = a.partial + ((int64_t)blockIdx.y * kPartRows + r) * BN + c;
+        float4 sum = ld_ro4(at + ((int64_t)first * 2 + (u0 == first * a.per ? 0 : 1)) * kTile);
+#pragma unroll 8
+        for (int p = first + 1; p <= last; ++p) sum = f4_add(sum, ld_ro4(at + (int64_t)p * 2 * kTile));
+        T* out = static_cast<T*>(a.dw) + ((int64_t)g * a.N + n0 + r) * a.K + k0 + c;
+        const float v[4] = {sum.x, sum.y, sum.z, sum.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (c + j < cols) out[j] = from_f32<T>(v[j]);
     }
 }
 
@@ -308,15 +380,14 @@ __global__ void __launch_bounds__(256) weights_join(const WeightArgs a) {
 constexpr int kCtas = 152;
 struct WeightPlan {
     int bn;
-    int64_t tiles, slots, units, per;
+    int64_t slots, units, per;
     int ctas;
 };
-WeightPlan weight_plan(int32_t dtype, int64_t M, int32_t K, int32_t N, int32_t G) {
+WeightPlan weight_plan(int32_t dtype, bool tma, int64_t M, int32_t K, int32_t N, int32_t G) {
     WeightPlan p;
-    p.bn = K <= 32 ? 32 : K <= 64 ? 64 : dtype == ZS_F32 || (K + 127) / 128 % 2 ? 128 : 256;
-    p.tiles = (int64_t)((N + kTileM - 1) / kTileM) * ((K + p.bn - 1) / p.bn);
-    p.slots = M / kStep + G;
-    p.units = p.tiles * p.slots;
+    p.bn = dtype == ZS_F32 ? 64 : K <= 32 ? 32 : K <= 64 ? 64 : (K + 127) / 128 % 2 || !tma ? 128 : 256;
+    p.slots = M / (dtype == ZS_F32 ? kStageK<float> : kStageK<__half>) + (int64_t)G * kFlush;
+    p.units = p.slots * ((N + kTileM - 1) / kTileM) * ((K + p.bn - 1) / p.bn);
     p.per = (p.units + kCtas - 1) / kCtas;
     p.ctas = p.per ? (int)((p.units + p.per - 1) / p.per) : 0;
     return p;
@@ -328,9 +399,8 @@ zs_status launch_weights(const char* fn, WeightArgs a, const WeightPlan& p, cuda
     CUtensorMap dy_map = {}, x_map = {};
     if (kTma) {
         constexpr bool bf16 = std::is_same<T, __nv_bfloat16>::value;
-        const int box = a.perm ? 1 : kStep;
-        if (!encode_boxes(&dy_map, bf16, a.dy.p, a.N, a.M, a.dy.ld, 0, box) ||
-            !encode_boxes(&x_map, bf16, a.x.p, a.K, a.M, a.x.ld, 0, box))
+        if (!a.perm && (!encode_boxes(&dy_map, bf16, a.dy.p, a.N, a.M, a.dy.ld, 0, kStageK<T>) ||
+                        !encode_boxes(&x_map, bf16, a.x.p, a.K, a.M, a.x.ld, 0, kStageK<T>)))
             return fail(ZS_ERR_CUDA, "%s: a tensor map was refused", fn);
     }
     static std::atomic<uint64_t> done[kMaxDevices];
@@ -346,11 +416,13 @@ zs_status launch_weights(const char* fn, WeightArgs a, const WeightPlan& p, cuda
 
 template <typename T, bool kTma>
 zs_status launch_weights(const char* fn, const WeightArgs& a, const WeightPlan& p, cudaStream_t s) {
-    if (p.bn == 32) return launch_weights<T, kTma, 32>(fn, a, p, s);
-    if (p.bn == 64) return launch_weights<T, kTma, 64>(fn, a, p, s);
-    if constexpr (sizeof(T) == 2)
-        if (p.bn == 256) return launch_weights<T, kTma, 256>(fn, a, p, s);
-    return launch_weights<T, kTma, 128>(fn, a, p, s);
+    if constexpr (sizeof(T) == 2) {
+        if (p.bn == 32) return launch_weights<T, kTma, 32>(fn, a, p, s);
+        if constexpr (kTma)
+            if (p.bn == 256) return launch_weights<T, kTma, 256>(fn, a, p, s);
+        if (p.bn == 128) return launch_weights<T, kTma, 128>(fn, a, p, s);
+    }
+    return launch_weights<T, kTma, 64>(fn, a, p, s);
 }
 
 }  // namespace
@@ -359,8 +431,12 @@ unsigned int take_timeouts_grouped_weights() { return take_timeouts_local(); }
 cudaError_t set_timeout_flag_grouped_weights(unsigned int* flag) { return set_timeout_flag_local(flag); }
 
 size_t grouped_weights_workspace(int32_t dtype, int64_t M, int32_t K, int32_t N, int32_t G) {
-    const WeightPlan p = weight_plan(dtype, M, K, N, G);
-    return p.ctas > 1 ? (size_t)p.ctas * 2 * kTileM * p.bn * 4 : 0;
+    size_t bytes = 0;
+    for (bool tma : {false, true}) {   // which one depends on the operands' alignment
+        const WeightPlan p = weight_plan(dtype, tma, M, K, N, G);
+        if (p.ctas > 1 && !(tma && dtype == ZS_F32)) bytes = imax(bytes, (size_t)p.ctas * 2 * kTileM * p.bn * 4);
+    }
+    return bytes;
 }
 
 zs_status grouped_weights(const char* fn, int32_t dtype, const void* dy, int64_t dy_ld, const void* x, int64_t x_ld,
@@ -368,11 +444,12 @@ zs_status grouped_weights(const char* fn, int32_t dtype, const void* dy, int64_t
                           void* workspace, cudaStream_t s) {
     const int es = dtype_bytes(dtype), per16 = 16 / es;
     auto at = [&](const void* p, int bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; };
-    const WeightPlan p = weight_plan(dtype, M, K, N, G);
-    if (p.units >= (int64_t(1) << 40)) return fail(ZS_ERR_INVALID_ARG, "%s: %lld units", fn, (long long)p.units);
+    const bool tma = dtype != ZS_F32 && at(dy, 16) && dy_ld % per16 == 0 && at(x, 16) && x_ld % per16 == 0 && M > 0;
+    const WeightPlan p = weight_plan(dtype, tma, M, K, N, G);
+    if (p.units >= (int64_t(1) << 31) - (1 << 24)) return fail(ZS_ERR_INVALID_ARG, "%s: %lld units", fn, (long long)p.units);
     WeightArgs a = {};
-    a.dy = {dy, dy_ld, N, at(dy, 2 * es) && dy_ld % 2 == 0};
-    a.x = {x, x_ld, K, at(x, 2 * es) && x_ld % 2 == 0};
+    a.dy = {dy, dy_ld, N, at(dy, 16) && dy_ld % per16 == 0};
+    a.x = {x, x_ld, K, at(x, 16) && x_ld % per16 == 0};
     a.row_ptr = row_ptr;
     a.perm = perm;
     a.dw = dw;
@@ -380,13 +457,12 @@ zs_status grouped_weights(const char* fn, int32_t dtype, const void* dy, int64_t
     a.dw_wide = at(dw, 16) && K % per16 == 0;
     a.M = (int)M, a.G = G, a.N = N, a.K = K;
     a.ktiles = (K + p.bn - 1) / p.bn;
-    a.slots = p.slots, a.units = p.units, a.per = p.per;
-    const bool aligned = at(dy, 16) && dy_ld % per16 == 0 && at(x, 16) && x_ld % per16 == 0 && M > 0;
+    a.slots = (int)p.slots, a.units = (int)p.units, a.per = (int)p.per;
     switch (dtype) {
         case ZS_F32: return launch_weights<float, false>(fn, a, p, s);
-        case ZS_BF16: return aligned ? launch_weights<__nv_bfloat16, true>(fn, a, p, s)
+        case ZS_BF16: return tma ? launch_weights<__nv_bfloat16, true>(fn, a, p, s)
                                      : launch_weights<__nv_bfloat16, false>(fn, a, p, s);
-        default: return aligned ? launch_weights<__half, true>(fn, a, p, s) : launch_weights<__half, false>(fn, a, p, s);
+        default: return tma ? launch_weights<__half, true>(fn, a, p, s) : launch_weights<__half, false>(fn, a, p, s);
     }
 }
 

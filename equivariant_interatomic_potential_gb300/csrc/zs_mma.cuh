@@ -2,20 +2,26 @@
 // operands in shared memory and fp32 sums in TMEM, the rings that feed them,
 // and the walk over the groups of a CSR.
 //
-// Operand boxes.  Every operand tile is made of boxes of rows of 64
-// contiguous 16-bit elements (128 bytes), eight rows to a 1024-byte atom
-// whose 16-byte pieces are permuted by the 128-byte swizzle (piece c of row r
-// sits at piece c ^ (r & 7)).  Where the contiguous direction is the one
-// summed over, a box holds all of the tile's rows (K-major); where it is not,
-// a box holds 64 summed-over rows and the tile takes a box for every 64 of
-// its own rows (MN-major).  Either way a box is the plain image of a piece of
-// a row-major matrix, so TMA, or a warp that reads a row, writes it.
+// Operand boxes.  Every operand tile is made of boxes of rows of 64 (or 32)
+// contiguous 16-bit elements, eight rows to an atom whose 16-byte pieces are
+// permuted by the 128-byte (64-byte) swizzle: piece c of row r sits at piece
+// c ^ (r & 7), or c ^ (r / 2 & 3).  Where the contiguous direction is the one
+// summed over, a box holds all of the tile's rows (K-major); where it is not, a
+// box holds summed-over rows and the tile takes a box for every 64 of its own
+// (MN-major; boxes of 32 columns were read a third slower that way).  Either
+// way a box is the plain image of a piece of a row-major matrix, so TMA, or
+// warps that copy rows, write it.
 //
 // fp32 operands are cut into three bf16 planes by truncation, 8 + 8 + 8 bits
 // of the 24, which loses nothing; the six products of planes whose weights
-// reach 2^-16 are summed (what is left out is below 2^-23 of a term).  That
-// costs six bf16 products instead of fp32's rate on the CUDA cores, a factor
-// of about four in time where the product is the bound.
+// reach 2^-16 are summed (what is left out is below 2^-23 of a term), at a
+// sixth of the bf16 rate, about four times fp32's on the CUDA cores.  The
+// right operand's planes lie side by side, so one instruction multiplies a
+// plane of the left one by three, two or one of them, and the products sum up
+// by weight: 1, 2^-8 and 2^-16.  The tensor cores truncate as they add (a sum
+// over n steps comes out about n 2^-24 low, as measured), which only the first
+// of the three sums feels; all leave TMEM every kChunk summed-over elements to
+// be added, rounded to nearest, in registers.
 //
 // Every wait is bounded (zs_wait.cuh).  A wait that runs out marks the CTA
 // dead: every role leaves its loop, the copies and products in flight are
@@ -32,18 +38,43 @@
 namespace zs {
 
 constexpr int kTileM = 128;                    // rows of a product's tile: TMEM lanes
-constexpr int kBoxCols = 64;                   // elements of a box's row
-constexpr int kBoxRow = 128;                   // bytes
+// Summed-over elements of a stage: a K-major box's columns, an MN-major box's
+// rows.  The three planes of fp32 take more room, so its stages are shorter.
+template <typename T>
+constexpr int kStageK = sizeof(T) == 4 ? 32 : 64;
+constexpr int kBoxMN = 64;                     // columns of an MN-major box
+template <int kCols>
+__host__ __device__ constexpr uint32_t box_bytes(int rows) { return (uint32_t)rows * kCols * 2; }
 constexpr uint32_t kDrainSpins = 1u << 16;
 
+constexpr int kEpilogueWarps = 8;              // two for each 32 TMEM lanes
+constexpr int kLoaderWarps = 8;                // of each of the two groups that take stages in turn
+constexpr int kChunk = 128;                    // elements summed in TMEM at a time for fp32 operands
 template <typename T>
 constexpr int kPlanes = sizeof(T) == 4 ? 3 : 1;
+template <typename T>
+constexpr int kSums = sizeof(T) == 4 ? 3 : 1;  // sums of a tile in TMEM
+__host__ __device__ constexpr uint32_t tmem_cols(int n) { return n <= 32 ? 32 : n <= 64 ? 64 : n <= 128 ? 128 : n <= 256 ? 256 : 512; }
 
 // ---------------------------------------------------------------- barriers
 
-// dead: set by the first wait of the CTA that runs out; the others give up
-// soon after.
+// Whole warps.  dead: set by the first wait of the CTA that runs out; the
+// others give up soon after.  Every lane gets the same answer.
 __device__ __forceinline__ bool bounded_wait(uint32_t bar, uint32_t parity, volatile int* dead) {
+    bool ok = false;
+    for (uint32_t i = 0; i < kMaxSpins && !ok; ++i) {
+        ok = mbar_try_wait(bar, parity);
+        if (!ok && (i & 63) == 63 && *dead) break;
+        if (!ok && i == kMaxSpins - 1) {
+            note_timeout();
+            *dead = 1;
+        }
+    }
+    return __all_sync(0xffffffffu, ok);
+}
+// One thread's wait, for the roles that issue: a vote at each stage would cost
+// them a tenth of the tensor cores' time.
+__device__ __forceinline__ bool bounded_wait_one(uint32_t bar, uint32_t parity, volatile int* dead) {
     for (uint32_t i = 0; i < kMaxSpins; ++i) {
         if (mbar_try_wait(bar, parity)) return true;
         if ((i & 63) == 63 && *dead) return false;
@@ -52,6 +83,7 @@ __device__ __forceinline__ bool bounded_wait(uint32_t bar, uint32_t parity, vola
     *dead = 1;
     return false;
 }
+__device__ __forceinline__ bool is_dead(volatile int* dead) { return __any_sync(0xffffffffu, *dead != 0); }
 
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" :: "r"(bar) : "memory");
@@ -98,19 +130,33 @@ __device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t (&r)[32]) {
                    "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
                  : "r"(addr) : "memory");
 }
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t (&r)[16]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+                 "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+                   "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+                 : "r"(addr) : "memory");
+}
 __device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
-// Shared-memory operand descriptor of boxes with the 128-byte swizzle.  Both
-// forms step 1024 bytes (sbo) per 8 box rows; lbo is the distance between
-// the boxes of an MN-major tile (unused by a K-major one).
+// Where 16-byte piece c of row r sits in a box.
+template <int kCols>
+__device__ __forceinline__ uint32_t piece_at(int r, int c) {
+    return r * (kCols * 2) + ((c ^ (kCols == 64 ? r & 7 : (r >> 1) & 3)) << 4);
+}
+// Shared-memory operand descriptor of boxes.  Both forms step one atom (sbo)
+// per 8 box rows; lbo is the distance between the boxes of an MN-major tile
+// (unused by a K-major one).
+template <int kCols>
 __device__ __forceinline__ uint64_t box_desc(uint32_t addr, uint32_t lbo) {
-    return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)((lbo & 0x3FFFFu) >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
-           (uint64_t(1) << 46) | (uint64_t(2) << 61);
+    constexpr uint64_t sbo = 8 * kCols * 2, swizzle = kCols == 64 ? 2 : 4;
+    return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)((lbo & 0x3FFFFu) >> 4) << 16) | ((sbo >> 4) << 32) |
+           (uint64_t(1) << 46) | (swizzle << 61);
 }
 // Descriptor address steps of one product's 16 summed-over elements: 32 bytes
 // along a K-major row, 16 rows of an MN-major box.
-template <bool kMN>
-constexpr uint32_t kDescStep = (kMN ? 16 * kBoxRow : 32) >> 4;
+template <int kCols, bool kMN>
+constexpr uint32_t kDescStep = (kMN ? 16 * kCols * 2 : 32) >> 4;
 
 // Instruction descriptor: 16-bit operands, fp32 sums, 128 x n tile.
 template <typename T>
@@ -120,24 +166,24 @@ __device__ __forceinline__ uint32_t instr_desc(bool a_mn, bool b_mn, int n) {
            ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kTileM >> 4) << 24);
 }
 
-// The products of one stage: `steps` times 16 summed-over elements.
-template <typename T, bool kAMN, bool kBMN>
-__device__ __forceinline__ void issue_stage(uint32_t d, uint32_t a, uint32_t a_plane, uint32_t a_lbo, uint32_t b,
-                                            uint32_t b_plane, uint32_t b_lbo, uint32_t idesc, int steps, bool accumulate) {
-    const uint64_t a0 = box_desc(a, a_lbo), b0 = box_desc(b, b_lbo);
+// The products of one stage: `steps` times 16 summed-over elements, into a tile
+// of BN columns (fp32: three of them).  Planes of the left operand are a_plane
+// bytes apart, those of the right one follow each other.
+template <typename T, bool kAMN, bool kBMN, int BN>
+__device__ __forceinline__ void issue_stage(uint32_t d, uint32_t a, uint32_t a_plane, uint32_t a_lbo, uint32_t b, uint32_t b_lbo,
+                                            int steps, bool accumulate) {
+    constexpr int kACols = kAMN ? kBoxMN : kStageK<T>, kBCols = kBMN ? kBoxMN : kStageK<T>;
+    const uint64_t a0 = box_desc<kACols>(a, a_lbo), b0 = box_desc<kBCols>(b, b_lbo);
     for (int k = 0; k < steps; ++k) {
-        const uint64_t ak = a0 + k * kDescStep<kAMN>, bk = b0 + k * kDescStep<kBMN>;
+        const uint64_t ak = a0 + k * kDescStep<kACols, kAMN>, bk = b0 + k * kDescStep<kBCols, kBMN>;
+        const bool more = accumulate || k > 0;
         if constexpr (kPlanes<T> == 1) {
-            tc_mma(d, ak, bk, idesc, accumulate || k > 0);
+            tc_mma(d, ak, bk, instr_desc<T>(kAMN, kBMN, BN), more);
         } else {
-            // the small products first
-            const uint32_t ap = a_plane >> 4, bp = b_plane >> 4;
-            tc_mma(d, ak + 2 * ap, bk, idesc, accumulate || k > 0);
-            tc_mma(d, ak + ap, bk + bp, idesc, true);
-            tc_mma(d, ak, bk + 2 * bp, idesc, true);
-            tc_mma(d, ak + ap, bk, idesc, true);
-            tc_mma(d, ak, bk + bp, idesc, true);
-            tc_mma(d, ak, bk, idesc, true);
+            const uint32_t ap = a_plane >> 4;
+            tc_mma(d, ak, bk, instr_desc<T>(kAMN, kBMN, 3 * BN), more);
+            tc_mma(d + BN, ak + ap, bk, instr_desc<T>(kAMN, kBMN, 2 * BN), true);
+            tc_mma(d + 2 * BN, ak + 2 * ap, bk, instr_desc<T>(kAMN, kBMN, BN), true);
         }
     }
 }
@@ -152,100 +198,174 @@ __device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* map, int
     asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
                  :: "r"(dst), "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar) : "memory");
 }
-// Four rows of a map whose box is one row high.
-__device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* map, int x, int4 rows, uint32_t bar) {
-    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes "
-                 "[%0], [%1, {%2, %3, %4, %5, %6}], [%7];"
-                 :: "r"(dst), "l"(map), "r"(x), "r"(rows.x), "r"(rows.y), "r"(rows.z), "r"(rows.w), "r"(bar) : "memory");
-}
+// ---------------------------------------------------------------- rows copied by warps
 
-// ---------------------------------------------------------------- rows read by warps
-
-// How a matrix is read: rows `ld` elements apart, `cols` wide; pairs: every
-// pair of elements that starts at an even column is aligned to the pair.
+// How a matrix is read: rows `ld` elements apart, `cols` wide; aligned: every
+// row starts on a 16-byte boundary.
 struct Matrix {
     const void* p;
     int64_t ld;
     int cols;
-    bool pairs;
+    bool aligned;
 };
 
-// Elements 2 i and 2 i + 1 of a row from column c0 on, zeros past its end.
-template <typename T>
-struct alignas(2 * sizeof(T)) Pair {
-    T a, b;
-};
-template <typename T>
-__device__ __forceinline__ Pair<T> load_pair(const Matrix& m, int64_t row, int c) {
-    const T* p = static_cast<const T*>(m.p) + row * m.ld + c;
-    Pair<T> v;
-    if (m.pairs && c + 1 < m.cols) {
-        if constexpr (sizeof(T) == 4) {
-            const float2 f = __ldg(reinterpret_cast<const float2*>(p));
-            v.a = f.x, v.b = f.y;
-        } else {
-            const uint32_t w = __ldg(reinterpret_cast<const unsigned int*>(p));
-            const unsigned short lo = (unsigned short)w, hi = (unsigned short)(w >> 16);
-            v.a = *reinterpret_cast<const T*>(&lo), v.b = *reinterpret_cast<const T*>(&hi);
-        }
-    } else {
-        v.a = c < m.cols ? p[0] : from_f32<T>(0.f);
-        v.b = c + 1 < m.cols ? p[1] : from_f32<T>(0.f);
-    }
-    return v;
+// 16 bytes to shared memory, of which the first n are read and the others zero.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, int n) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(dst), "l"(src), "r"(n) : "memory");
 }
+template <int N>
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" :: "n"(N) : "memory"); }
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 
-// The bf16 planes of a value: x = plane 0 + plane 1 + plane 2 exactly.  A
-// value that is not finite stays whole in plane 0.
-__device__ __forceinline__ void split3(float x, uint32_t (&b)[3]) {
-    const uint32_t u = __float_as_uint(x);
-    const bool fin = (u & 0x7f800000u) != 0x7f800000u;
-    const float r1 = x - __uint_as_float(u & 0xffff0000u);
-    const uint32_t u1 = __float_as_uint(r1) & 0xffff0000u;
-    const float r2 = r1 - __uint_as_float(u1);
-    const uint32_t quiet = (u & 0x007fffffu) ? 0x00400000u : 0u;   // a NaN keeps a bit of its payload
-    b[0] = (fin ? u : u | quiet) >> 16;
-    b[1] = fin ? u1 >> 16 : 0u;
-    b[2] = fin ? __float_as_uint(r2) >> 16 : 0u;
+// Bits 16 to 31 of a, then of b.
+__device__ __forceinline__ uint32_t upper_halves(float a, float b) {
+    return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
 }
+__device__ __forceinline__ float truncated(float x) { return __uint_as_float(__float_as_uint(x) & 0xffff0000u); }
 
-// Writes the pair at (row r, elements 2 lane and 2 lane + 1) of a box.
-template <typename T>
-__device__ __forceinline__ void store_pair(unsigned char* box, uint32_t plane, int r, int lane, Pair<T> v) {
-    const int at = r * kBoxRow + (((lane >> 2) ^ (r & 7)) << 4) + ((lane & 3) << 2);
-    if constexpr (sizeof(T) == 4) {
-        uint32_t x[3], y[3];
-        split3(v.a, x);
-        split3(v.b, y);
+// kRows rows of a box of kCols columns, for operands that are cut into planes
+// or whose rows are not aligned.  A group of kLoaderWarps warps copies them in
+// parts of 16 bytes (of the matrix) into slots of shared memory that are each
+// thread's own, and later turns each part into the box's pieces; nothing is
+// held in registers meanwhile, and no barrier is needed between the two.  A
+// part of an unaligned row is copied as the two aligned pieces that hold it.
+// A lane of warp w holds in `rows` the matrix row of box row kPer w + (lane
+// mod kPer) (negative: zeros, as are columns past the matrix).
+template <typename T, int kRows, int kCols>
+struct BoxParts {
+    static constexpr int kElems = 16 / (int)sizeof(T);
+    static constexpr int kPer = kRows / kLoaderWarps;
+    static constexpr int kLanes = kCols / kElems;        // of a row
+    static constexpr int kAtOnce = 32 / kLanes;          // rows a warp copies at once
+    static constexpr int kSteps = kPer / kAtOnce;        // parts of a thread
+    static_assert(kPer <= 32 && kPer % kAtOnce == 0, "whole rows");
+
+    // offs: bits 4 i .. of this thread's part i say where it starts within its slot (unaligned rows)
+    static __device__ __forceinline__ uint32_t copy(const Matrix& m, int rows, int c0, uint32_t slot, uint32_t stride, bool aligned,
+                                                    int lane) {
+        uint32_t offs = 0;
+        const int c = c0 + kElems * (lane % kLanes);
 #pragma unroll
-        for (int i = 0; i < 3; ++i) *reinterpret_cast<uint32_t*>(box + i * plane + at) = x[i] | (y[i] << 16);
-    } else {
-        *reinterpret_cast<Pair<T>*>(box + at) = v;
+        for (int i = 0; i < kSteps; ++i) {
+            const int r = __shfl_sync(0xffffffffu, rows, i * kAtOnce + lane / kLanes);
+            const bool in = r >= 0 && c < m.cols;
+            const char* at = static_cast<const char*>(m.p) + (in ? (r * m.ld + c) * (int64_t)sizeof(T) : 0);
+            const int left = in ? (m.cols - c) * (int)sizeof(T) : 0;   // bytes to the row's end
+            if (aligned) {
+                copy16(slot + i * stride, at, imin(left, 16));
+            } else {
+                const int off = in ? (int)(reinterpret_cast<uintptr_t>(at) & 15u) : 0;
+                const char* base = reinterpret_cast<const char*>(reinterpret_cast<uintptr_t>(at) & ~uintptr_t(15));
+                copy16(slot + i * stride, base, in ? imin(off + left, 16) : 0);
+                const int more = imin(off + left - 16, 16);
+                copy16(slot + i * stride + 16, more > 0 ? base + 16 : base, imax(more, 0));
+                offs |= (uint32_t)off << (4 * i);
+            }
+        }
+        return offs;
+    }
+
+    // fp32: x = plane 0 + plane 1 + plane 2 exactly, each the upper half of what the ones before leave (a value that is
+    // not finite leaves NaN).
+    static __device__ __forceinline__ void turn(const unsigned char* slot, uint32_t stride, bool aligned, uint32_t offs,
+                                                unsigned char* box, uint32_t plane, int w, int lane) {
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) {
+            uint4 q;
+            if (aligned) {
+                q = *reinterpret_cast<const uint4*>(slot + i * stride);
+            } else {
+                const int off = offs >> (4 * i) & 15;
+                const uint32_t* from = reinterpret_cast<const uint32_t*>(slot + i * stride + (off & 12));
+                uint32_t* qe = &q.x;
+                if constexpr (sizeof(T) == 4) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) qe[j] = from[j];
+                } else {
+                    uint32_t u[5];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) u[j] = from[j];
+                    u[4] = off & 2 ? from[4] : 0;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) qe[j] = __funnelshift_r(u[j], u[j + 1], 8 * (off & 2));
+                }
+            }
+            const int row = kPer * w + i * kAtOnce + lane / kLanes, part = lane % kLanes;
+            if constexpr (sizeof(T) == 4) {
+                unsigned char* to = box + piece_at<kCols>(row, part >> 1) + ((part & 1) << 3);
+                float x[4] = {__uint_as_float(q.x), __uint_as_float(q.y), __uint_as_float(q.z), __uint_as_float(q.w)};
+#pragma unroll
+                for (int p = 0; p < 3; ++p) {
+                    *reinterpret_cast<uint2*>(to + p * plane) = make_uint2(upper_halves(x[0], x[1]), upper_halves(x[2], x[3]));
+                    if (p < 2) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) x[j] -= truncated(x[j]);
+                    }
+                }
+            } else {
+                *reinterpret_cast<uint4*>(box + piece_at<kCols>(row, part)) = q;
+            }
+        }
+    }
+};
+
+// kRows rows of a box of 64 columns of a 16-bit matrix with aligned rows,
+// copied straight to their places.  (TMA gathers four rows in about 40 cycles,
+// which is 12 bytes a cycle of an SM; this took 75 us where that took 104, for
+// 262144 rows of 256 channels.)
+template <int kRows>
+__device__ __forceinline__ void copy_rows(uint32_t box, const Matrix& m, int rows, int c0, int w, int lane) {
+    constexpr int kPer = kRows / kLoaderWarps;
+    const int piece = lane & 7;
+    const int c = c0 + 8 * piece;
+#pragma unroll
+    for (int i = 0; i < kPer / 4; ++i) {
+        const int at = 4 * i + (lane >> 3), r = __shfl_sync(0xffffffffu, rows, at), row = kPer * w + at;
+        const bool in = r >= 0 && c < m.cols;
+        copy16(box + piece_at<64>(row, piece), static_cast<const uint16_t*>(m.p) + (in ? r * m.ld + c : 0),
+               in ? imin(m.cols - c, 8) * 2 : 0);
     }
 }
 
 // ---------------------------------------------------------------- groups of a CSR
 
 // The positions of the groups, cut into slots of kRows positions: group g
-// starts at slot floor(row_ptr[g] / kRows) + g, which leaves room for each
-// group's pieces without a prefix sum.  A slot past its group's last piece is
-// empty.  start(G + 1) is M: the positions of no group are "group" G.
-template <int kRows>
+// starts at slot floor(row_ptr[g] / kRows) + g * kExtra, which leaves room for
+// each group's pieces without a prefix sum (kExtra >= 1).  Slots past a
+// group's last piece are empty.  start(G + 1) is M: the positions of no group
+// are "group" G.  The starts of up to kGroupsHeld groups are kept in shared
+// memory (a search there takes 0.1 us, in global memory one or two).
+constexpr int kGroupsHeld = 1022;
+template <int kRows, int kExtra>
 struct Groups {
-    const int32_t* row_ptr;
+    const int32_t* p;   // start(0 .. G + 1) in shared memory, or row_ptr
     int G, M;
-    __device__ __forceinline__ int start(int g) const {
-        if (g > G) return M;
+    bool held;
+    __device__ __forceinline__ static int clamped(const int32_t* row_ptr, int g, int M) {
         const int v = __ldg(row_ptr + g);
         return v < 0 ? 0 : v > M ? M : v;
     }
-    __device__ __forceinline__ int64_t slot(int g) const { return (int64_t)(start(g) / kRows) + g; }
-    // the group whose slots hold `s` (0 <= s < slot(last)), among groups [0, last)
-    __device__ __forceinline__ int find(int64_t s, int last) const {
-        int lo = 0, hi = last;
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (slot(mid) <= s) lo = mid; else hi = mid;
+    // All threads of the CTA; a barrier has to follow.
+    __device__ __forceinline__ void hold(const int32_t* row_ptr, int G_, int M_, int32_t* smem) {
+        G = G_;
+        M = M_;
+        held = G <= kGroupsHeld;
+        p = held ? smem : row_ptr;
+        if (held)
+            for (int g = threadIdx.x; g <= G + 1; g += blockDim.x) smem[g] = g > G ? M : clamped(row_ptr, g, M);
+    }
+    __device__ __forceinline__ int start(int g) const { return held ? p[g] : g > G ? M : clamped(p, g, M); }
+    __device__ __forceinline__ int slot(int g) const { return start(g) / kRows + g * kExtra; }
+    // The group in [0, last) whose slots hold s (slot(0) <= s < slot(last)), found by the whole warp: 32 samples a round.
+    __device__ __forceinline__ int find(int s, int last) const {
+        const int lane = threadIdx.x & 31;
+        int lo = 0, n = last;   // the answer is in [lo, lo + n)
+        while (n > 1) {
+            const int step = (n + 31) / 32, g = lo + lane * step;
+            const unsigned m = __ballot_sync(0xffffffffu, lane * step < n && slot(g) <= s);
+            const int i = 31 - __clz(m | 1u);
+            lo += i * step;
+            n = imin(step, n - i * step);
         }
         return lo;
     }
@@ -253,66 +373,143 @@ struct Groups {
 
 // ---------------------------------------------------------------- epilogue
 
-// A warp's 32 rows x 128 bytes of results pass through shared memory (rows
-// 144 bytes apart) so that they leave as whole row segments.
-constexpr int kStageRow = 144;
+// A warp's 32 rows x 64 bytes of results pass through shared memory (rows 80
+// bytes apart) so that they leave as whole row segments.
+constexpr int kStageRow = 80;
 constexpr int kStageWarp = 32 * kStageRow;
 
-// Writes columns [0, cols) of this warp's 32 rows of the TMEM tile at `tmem`
-// (zeros where tmem is kNoTile): lane l's row goes to `row` (NULL: nowhere),
-// 16 bytes at a time where `wide`.
-constexpr uint32_t kNoTile = 0xffffffffu;
+// Writes `left` (of 32) columns: lane l holds those of row l, which goes to
+// `row` (NULL: nowhere), 16 bytes at a time where `wide`.
 template <typename TO>
-__device__ __forceinline__ void store_tile(uint32_t tmem, int cols, TO* row, bool wide, unsigned char* stage, int lane) {
-    constexpr int kCols = 128 / (int)sizeof(TO);   // columns of a 128-byte segment
-    for (int c0 = 0; c0 < cols; c0 += kCols) {
-        uint32_t w[32];   // the segment, as 32-bit words
+__device__ __forceinline__ void emit32(const float (&f)[32], int left, TO* row, bool wide, unsigned char* stage, int lane) {
+    constexpr int kCols = 64 / (int)sizeof(TO);   // columns of a 64-byte segment
+    const unsigned long long mine = reinterpret_cast<unsigned long long>(row);
 #pragma unroll
-        for (int half = 0; half < kCols / 32; ++half) {
-            uint32_t f[32];
-            if (tmem != kNoTile) {
-                if (c0 + 32 * half < cols) tmem_ld32(tmem + c0 + 32 * half, f);
-                tmem_ld_wait();
-            } else {
+    for (int part = 0; part < 32 / kCols; ++part) {
+        const int here = left - part * kCols;
+        if (here <= 0) break;
+        __syncwarp();
 #pragma unroll
-                for (int i = 0; i < 32; ++i) f[i] = 0;
-            }
-            if constexpr (sizeof(TO) == 4) {
+        for (int i = 0; i < 4; ++i) {
+            float q[kVec<TO>];
 #pragma unroll
-                for (int i = 0; i < 32; ++i) w[i] = f[i];
-            } else {
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    Pair<TO> v;
-                    v.a = from_f32<TO>(__uint_as_float(f[2 * i]));
-                    v.b = from_f32<TO>(__uint_as_float(f[2 * i + 1]));
-                    w[16 * half + i] = *reinterpret_cast<uint32_t*>(&v);
-                }
-            }
+            for (int j = 0; j < kVec<TO>; ++j) q[j] = f[part * kCols + i * kVec<TO> + j];
+            *reinterpret_cast<uint4*>(stage + lane * kStageRow + 16 * i) = pack<TO>(q);
         }
         __syncwarp();
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            *reinterpret_cast<uint4*>(stage + lane * kStageRow + 16 * i) = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-        __syncwarp();
-        const int left = cols - c0 < kCols ? cols - c0 : kCols;
-        const unsigned long long mine = reinterpret_cast<unsigned long long>(row);
         if (wide) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int r = 4 * i + (lane >> 3), c = (lane & 7) * kVec<TO>;
+            for (int i = 0; i < 4; ++i) {
+                const int r = 8 * i + (lane >> 2), c = (lane & 3) * kVec<TO>;
                 TO* dst = reinterpret_cast<TO*>(__shfl_sync(0xffffffffu, mine, r));
-                if (dst && c < left) st_piece(dst + c0 + c, *reinterpret_cast<const uint4*>(stage + r * kStageRow + c * sizeof(TO)));
+                if (dst && c < here)
+                    st_piece(dst + part * kCols + c, *reinterpret_cast<const uint4*>(stage + r * kStageRow + c * sizeof(TO)));
             }
         } else {
-            for (int r = 0; r < 32; ++r) {
+            constexpr int kAtOnce = 32 / kCols;   // rows of a warp's store
+            for (int r0 = 0; r0 < 32; r0 += kAtOnce) {
+                const int r = r0 + lane / kCols, c = lane % kCols;
                 TO* dst = reinterpret_cast<TO*>(__shfl_sync(0xffffffffu, mine, r));
-                if (!dst) continue;
-                for (int c = lane; c < left; c += 32) dst[c0 + c] = *reinterpret_cast<const TO*>(stage + r * kStageRow + c * sizeof(TO));
+                if (dst && c < here) dst[part * kCols + c] = *reinterpret_cast<const TO*>(stage + r * kStageRow + c * sizeof(TO));
             }
         }
     }
 }
+
+// Writes columns [c0, c1) of this warp's rows of a tile in TMEM (zeros where
+// tmem is kNoTile); row: where column 0 of lane l's row goes.
+constexpr uint32_t kNoTile = 0xffffffffu;
+template <typename TO>
+__device__ __forceinline__ void store_tile(uint32_t tmem, int c0, int c1, TO* row, bool wide, unsigned char* stage, int lane) {
+    for (int c = c0; c < c1; c += 32) {
+        uint32_t w[32];
+        float f[32];
+        if (tmem != kNoTile) {
+            tmem_ld32(tmem + c, w);
+            tmem_ld_wait();
+        } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) w[i] = 0;
+        }
+#pragma unroll
+        for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(w[i]);
+        emit32<TO>(f, imin(32, c1 - c), row ? row + c : nullptr, wide, stage, lane);
+    }
+}
+
+// acc += the three sums, `apart` columns from each other, of 32 columns of an
+// fp32 product's chunk, the smallest first; 16 columns at a time, for the
+// registers.
+__device__ __forceinline__ void add_chunk(uint32_t from, int apart, float (&acc)[32]) {
+#pragma unroll
+    for (int at = 0; at < 32; at += 16) {
+        float sum[16];
+#pragma unroll
+        for (int i = 2; i >= 0; --i) {
+            uint32_t w[16];
+            tmem_ld16(from + i * apart + at, w);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 16; ++j) sum[j] = i == 2 ? __uint_as_float(w[j]) : sum[j] + __uint_as_float(w[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < 16; ++j) acc[at + j] += sum[j];
+    }
+}
+
+// What every grouped kernel sets up: barriers, TMEM, the groups' starts.
+template <int S, uint32_t kTmemCols, int kTile, int kExtra>
+struct Setup {
+    static constexpr int kBytes = (2 * S + 7) * 8 + (kGroupsHeld + 2) * 4;
+    uint32_t full, empty, tfull, tempty, done, tmem;
+    volatile int* dead;
+    Groups<kTile, kExtra> groups;
+    __device__ __forceinline__ void begin(unsigned char* smem, int full_count, int epilogue_warps, const int32_t* row_ptr, int G,
+                                          int M) {
+        uint64_t* bars = reinterpret_cast<uint64_t*>(smem);
+        dead = reinterpret_cast<volatile int*>(bars + 2 * S + 5);
+        uint32_t* slot = reinterpret_cast<uint32_t*>(bars + 2 * S + 6);
+        full = smem_u32(bars), empty = full + 8 * S, tfull = empty + 8 * S, tempty = tfull + 16, done = tempty + 16;
+        if (threadIdx.x == 0) {
+            for (int i = 0; i < S; ++i) {
+                mbar_init(full + 8 * i, full_count);
+                mbar_init(empty + 8 * i, 1);
+            }
+            for (int i = 0; i < 2; ++i) {
+                mbar_init(tfull + 8 * i, 1);
+                mbar_init(tempty + 8 * i, epilogue_warps);
+            }
+            mbar_init(done, 1);
+            *dead = 0;
+            mbar_fence_init();
+        }
+        pdl_wait();
+        pdl_trigger();
+        groups.hold(row_ptr, G, M, reinterpret_cast<int32_t*>(bars + 2 * S + 7));
+        if ((threadIdx.x >> 5) == 2) tmem_alloc(smem_u32(slot), kTmemCols);
+        tc_fence_before();
+        __syncthreads();
+        tc_fence_after();
+        tmem = *slot;
+    }
+    __device__ __forceinline__ void end() {
+        tc_fence_before();
+        __syncthreads();
+        tc_fence_after();
+        if ((threadIdx.x >> 5) == 2) tmem_free(tmem, kTmemCols);
+    }
+    // Where the CTA is dead: what was issued last on each stage has landed.
+    __device__ __forceinline__ void drain_copies(int issued) const {
+        for (int i = 0; i < imin(issued, S); ++i) {
+            const int k = issued - 1 - i;
+            for (uint32_t n = 0; n < kDrainSpins && !mbar_try_wait(full + 8 * (k % S), (uint32_t)(k / S) & 1); ++n) {}
+        }
+    }
+    __device__ __forceinline__ void drain_products() const {
+        if ((threadIdx.x & 31) == 0) tc_commit(done);
+        for (uint32_t i = 0; i < kDrainSpins && !mbar_try_wait(done, 0); ++i) {}
+    }
+};
 
 // ---------------------------------------------------------------- host
 
