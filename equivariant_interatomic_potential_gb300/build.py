@@ -1,8 +1,9 @@
-"""Build libzs.so from csrc/*.cu with nvcc for sm_103a (GB300).
+"""Build libzs.so from csrc/*.cu with nvcc for sm_103a (GB300), and zs_torch.so,
+the binding's short way from torch tensors to it, from csrc/zs_torch.cpp.
 
-Each translation unit compiles in its own nvcc process, in parallel, then one
-link step produces ``_build/libzs.so`` inside the package.  No GPU is needed
-to build.
+Each translation unit compiles in its own process, in parallel, then one link
+step produces ``_build/libzs.so`` inside the package.  No GPU is needed to
+build.
 """
 from __future__ import annotations
 
@@ -19,6 +20,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libzs.so")
+EXT = os.path.join(BUILD, "zs_torch.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
@@ -37,13 +39,14 @@ def sources() -> list[str]:
 
 
 def _deps() -> list[str]:
-    return sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(INCLUDE, "*.h"))
+    return (sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.cpp"))
+            + glob.glob(os.path.join(INCLUDE, "*.h")))
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(EXT):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(EXT))
     return all(os.path.getmtime(p) <= t for p in _deps() + [__file__])
 
 
@@ -60,14 +63,37 @@ def _compile(src: str, verbose: bool) -> str:
     return obj
 
 
+def _build_ext() -> None:
+    """zs_torch.so against the torch and Python that run this."""
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
+    includes = [INCLUDE, *cpp_extension.include_paths(), sysconfig.get_paths()["include"], cuda]
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = EXT + f".{os.getpid()}.tmp"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *(f"-isystem{d}" for d in includes),
+           os.path.join(CSRC, "zs_torch.cpp"), "-o", tmp, f"-L{libs}", f"-Wl,-rpath,{libs}", "-lc10", "-lc10_cuda",
+           "-ltorch_cpu", "-ltorch_python"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"the build of zs_torch.so failed:\n{res.stdout}\n{res.stderr}")
+    os.replace(tmp, EXT)
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile every csrc/*.cu for sm_103a and link libzs.so; returns its path."""
+    """Compile every csrc/*.cu for sm_103a and link libzs.so (its path is returned), and zs_torch.so."""
     if not force and up_to_date():
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     srcs = sources()
-    with concurrent.futures.ThreadPoolExecutor(max_workers=len(srcs)) as ex:
+    with concurrent.futures.ThreadPoolExecutor(max_workers=len(srcs) + 1) as ex:
+        ext = ex.submit(_build_ext)
         objs = list(ex.map(lambda s: _compile(s, verbose), srcs))
+        ext.result()
     tmp = LIB + f".{os.getpid()}.tmp"
     cmd = [nvcc(), *ARCH, "-shared", "-Xcompiler", "-fPIC", "-o", tmp, *objs, "-lcudart_static"]
     res = subprocess.run(cmd, capture_output=True, text=True)

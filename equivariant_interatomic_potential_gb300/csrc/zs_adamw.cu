@@ -116,17 +116,31 @@ __device__ __forceinline__ void decode(uint2 c, float scale, float (&f)[kPer]) {
         f[2 * j + 1] = __fmul_rn(v.y, scale);
     }
 }
+__device__ __forceinline__ float max_or_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+// The codes of a block (a warp's values, zero past its end) and its scale.
+// Blocks of finite values, all but every one, take no care of others.
 template <bool kRoot>
-__device__ __forceinline__ uint2 encode(const float (&f)[kPer], int n, float& scale) {
+__device__ __forceinline__ uint2 encode(const float (&f)[kPer], float& scale) {
     float top = 0.f;
 #pragma unroll
-    for (int j = 0; j < kPer; ++j)
-        if (j < n && finite(f[j])) top = fmaxf(top, fabsf(f[j]));
+    for (int j = 0; j < kPer; ++j) top = max_or_nan(top, fabsf(f[j]));
+    const bool fine = __all_sync(0xffffffffu, finite(top));
+    if (!fine) {
+        top = 0.f;
+#pragma unroll
+        for (int j = 0; j < kPer; ++j)
+            if (finite(f[j])) top = fmaxf(top, fabsf(f[j]));
+    }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     const bool live = top >= kScaleMin;
     scale = live ? __fmul_rn(top, 1.f / kE4m3Max) : 0.f;
     const float inv = live ? __fmul_rn(__frcp_rn(top), kE4m3Max) : 0.f;
+    const float least = live ? kE4m3Tiny : 0.f;
     uint32_t w[2] = {0, 0};
 #pragma unroll
     for (int j = 0; j < kPer; j += 2) {
@@ -135,9 +149,9 @@ __device__ __forceinline__ uint2 encode(const float (&f)[kPer], int n, float& sc
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
             const float x = f[j + k];
-            float v = __fmul_rn(x, inv);
-            if (kRoot && live && x > 0.f) v = fmaxf(v, kE4m3Tiny);
-            qe[k] = finite(x) ? v : __int_as_float(0x7fc00000);
+            qe[k] = __fmul_rn(x, inv);
+            if (kRoot && x > 0.f) qe[k] = fmaxf(qe[k], least);
+            if (!fine && !finite(x)) qe[k] = __int_as_float(0x7fc00000);
         }
         w[j / 4] |= (uint32_t)__nv_cvt_float2_to_fp8x2(q, __NV_SATFINITE, __NV_E4M3) << (16 * ((j / 2) & 1));
     }
@@ -201,8 +215,8 @@ __global__ void __launch_bounds__(kThreads) adamw_step(const __grid_constant__ T
         }
         store(param, i, n, pw, p);
         float ms, rs;
-        store_codes(ma, i, n, mw, encode<false>(m, n, ms));
-        store_codes(va, i, n, vw, encode<true>(r, n, rs));
+        store_codes(ma, i, n, mw, encode<false>(m, ms));
+        store_codes(va, i, n, vw, encode<true>(r, rs));
         if ((threadIdx.x & 31) == 0) {
             t.exp_avg_scale[b] = ms;
             t.exp_avg_sq_scale[b] = rs;

@@ -8,6 +8,7 @@ there is no fallback, and a missing or unbuildable library raises.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 import re
 import threading
@@ -103,6 +104,24 @@ def load(build_if_missing: bool = True):
         lib.zs_adamw_step.argtypes = [P, I32, I32, I32, P, P, P]
         _lib = lib
         return lib
+
+
+class _Fast:
+    """zs_torch.so, the short way for ordinary operands; loaded on first use."""
+
+    def __getattr__(self, name):
+        lib = load()
+        spec = importlib.util.spec_from_file_location("zs_torch", _build.EXT)
+        ext = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(ext)
+        names = [n for n in declared_functions() if n.startswith(("zs_grouped", "zs_norm"))]
+        ext.bind({n: ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names}, _check)
+        for n in ("matmul", "dw", "norm", "norm_backward"):
+            setattr(self, n, getattr(ext, n))
+        return getattr(self, name)
+
+
+_fast = _Fast()
 
 
 def declared_functions(header: str | None = None) -> list[str]:
@@ -532,6 +551,10 @@ def zs_grouped_matmul(x: torch.Tensor, w: torch.Tensor, row_ptr: torch.Tensor, p
     """y[i] = w[g(i)] x[i] for rows grouped by the CSR (row_ptr, perm); perm None: rows
     are in group order already.  x (M, K) and w (G, N, K) float32, bfloat16 or
     float16; returns y (M, N).  x and out may be row-strided views."""
+    if out is None and stream is None:
+        y = _fast.matmul(x, w, row_ptr, perm, False)
+        if y is not NotImplemented:
+            return y
     M, _ = _rows(x, "x")
     d, G, N, K, wp, rp, pp = _groups(w, row_ptr, perm, M)
     dt = w.dtype
@@ -550,6 +573,10 @@ def zs_grouped_matmul(x: torch.Tensor, w: torch.Tensor, row_ptr: torch.Tensor, p
 def zs_grouped_matmul_dx(dy: torch.Tensor, w: torch.Tensor, row_ptr: torch.Tensor, perm: torch.Tensor | None = None,
                          out=None, stream=None) -> torch.Tensor:
     """dx[i] = w[g(i)]^T dy[i]: the gradient of zs_grouped_matmul in x, (M, K)."""
+    if out is None and stream is None:
+        dx = _fast.matmul(dy, w, row_ptr, perm, True)
+        if dx is not NotImplemented:
+            return dx
     M, _ = _rows(dy, "dy")
     d, G, N, K, wp, rp, pp = _groups(w, row_ptr, perm, M)
     dt = w.dtype
@@ -574,6 +601,10 @@ def zs_grouped_matmul_dw(dy: torch.Tensor, x: torch.Tensor, row_ptr: torch.Tenso
                          out=None, workspace=None, stream=None) -> torch.Tensor:
     """dw[g] = sum over the rows of group g of dy[i] x[i]^T: the gradient of
     zs_grouped_matmul in w, (G, N, K) with G = row_ptr.numel() - 1."""
+    if out is None and workspace is None and stream is None:
+        dw = _fast.dw(dy, x, row_ptr, perm)
+        if dw is not NotImplemented:
+            return dw
     M, K = _rows(x, "x")
     _, N = _rows(dy, "dy")
     G = row_ptr.numel() - 1
@@ -638,6 +669,10 @@ def zs_norm_gate_residual(h: torch.Tensor, x: torch.Tensor, gate: torch.Tensor |
     same, (M, 1), or None; w_post, scale, w_pre (C,) float32; kind "rms" or "layer".
     Returns (y, u, stats): stats (M, 4) float32 is what the backward reads (None
     when want_stats is False)."""
+    if stream is None and kind in NORM_KINDS:
+        r = _fast.norm(h, x, gate, w_post, scale, w_pre, eps, NORM_KINDS[kind], want_stats)
+        if r is not NotImplemented:
+            return r
     d, k, M, C, args = _norm_operands(h, x, gate, w_post, scale, w_pre, kind)
     dt, dev = h.dtype, h.device
     y = torch.empty((M, C), dtype=dt, device=dev)
@@ -655,6 +690,10 @@ def zs_norm_gate_residual_backward(dy: torch.Tensor | None, du: torch.Tensor | N
                                    w_pre: torch.Tensor, stats: torch.Tensor, kind: str = "rms", stream=None):
     """Gradients of zs_norm_gate_residual for the cotangents dy of y and du of u (None:
     zeros): (dh, dx, dgate, dw_post, dscale, dw_pre); dgate is None without a gate."""
+    if stream is None and kind in NORM_KINDS:
+        r = _fast.norm_backward(dy, du, h, x, gate, w_post, scale, w_pre, stats, NORM_KINDS[kind])
+        if r is not NotImplemented:
+            return r
     d, k, M, C, args = _norm_operands(h, x, gate, w_post, scale, w_pre, kind)
     dt, dev, f32 = h.dtype, h.device, torch.float32
     dy_ld = 0 if dy is None else _matrix(dy, "dy", dt, M, C)
