@@ -72,8 +72,10 @@ zs_status zs_grouped_matmul(int32_t dtype, const void* x, int64_t x_ld, const vo
     if (zs_status st = check_ld(fn, "x_ld", x_ld, K, M)) return st;
     if (zs_status st = check_ld(fn, "y_ld", y_ld, N, M)) return st;
     if (M == 0) return ZS_OK;
-    return grouped_rows(fn, dtype, x, M > 1 ? x_ld : K, w, row_ptr, perm, M, K, N, G, y, y_ld, false,
-                        reinterpret_cast<cudaStream_t>(stream));
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (grouped_is_few(dtype, 0, M, N, G)) return grouped_few(fn, dtype, 0, x, x_ld, w, K, row_ptr, perm, M, K, N, G, y, y_ld, s);
+    if (grouped_is_small(K, N)) return grouped_small_rows(fn, dtype, 0, x, x_ld, w, row_ptr, perm, M, K, N, G, y, y_ld, s);
+    return grouped_rows(fn, dtype, x, M > 1 ? x_ld : K, w, row_ptr, perm, M, K, N, G, y, y_ld, false, s);
 }
 
 zs_status zs_grouped_matmul_dx(int32_t dtype, const void* dy, int64_t dy_ld, const void* w, const int32_t* row_ptr,
@@ -86,13 +88,15 @@ zs_status zs_grouped_matmul_dx(int32_t dtype, const void* dy, int64_t dy_ld, con
     if (zs_status st = check_ld(fn, "dy_ld", dy_ld, N, M)) return st;
     if (zs_status st = check_ld(fn, "dx_ld", dx_ld, K, M)) return st;
     if (M == 0) return ZS_OK;
-    return grouped_rows(fn, dtype, dy, M > 1 ? dy_ld : N, w, row_ptr, perm, M, K, N, G, dx, dx_ld, true,
-                        reinterpret_cast<cudaStream_t>(stream));
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (grouped_is_few(dtype, 1, M, N, G)) return grouped_few(fn, dtype, 1, dy, dy_ld, w, K, row_ptr, perm, M, K, N, G, dx, dx_ld, s);
+    if (grouped_is_small(K, N)) return grouped_small_rows(fn, dtype, 1, dy, dy_ld, w, row_ptr, perm, M, K, N, G, dx, dx_ld, s);
+    return grouped_rows(fn, dtype, dy, M > 1 ? dy_ld : N, w, row_ptr, perm, M, K, N, G, dx, dx_ld, true, s);
 }
 
 size_t zs_grouped_matmul_dw_workspace_bytes(int32_t dtype, int64_t M, int32_t K, int32_t N, int32_t G) {
     if (!zs::known_dtype(dtype) || M < 0 || M >= (int64_t(1) << 31) || K < 1 || N < 1 || G < 1) return 0;
-    return zs::grouped_weights_workspace(dtype, M, K, N, G);
+    return zs::grouped_is_few(dtype, 2, M, N, G) ? 0 : zs::grouped_weights_workspace(dtype, M, K, N, G);
 }
 
 zs_status zs_grouped_matmul_dw(int32_t dtype, const void* dy, int64_t dy_ld, const void* x, int64_t x_ld,
@@ -111,6 +115,8 @@ zs_status zs_grouped_matmul_dw(int32_t dtype, const void* dy, int64_t dy_ld, con
     if (reinterpret_cast<uintptr_t>(workspace) & 255u)
         return fail(ZS_ERR_INVALID_ARG, "%s: workspace is not 256-byte aligned", fn);
     if (G == 0) return ZS_OK;
+    if (grouped_is_few(dtype, 2, M, N, G))
+        return grouped_few(fn, dtype, 2, dy, dy_ld, x, x_ld, row_ptr, perm, M, K, N, G, dw, K, reinterpret_cast<cudaStream_t>(stream));
     return grouped_weights(fn, dtype, dy, M > 1 ? dy_ld : N, x, M > 1 ? x_ld : K, row_ptr, perm, M, K, N, G, dw, workspace,
                            reinterpret_cast<cudaStream_t>(stream));
 }

@@ -1,41 +1,16 @@
 // Grouped products' gradient in the weights: dw[g] = sum over the rows of
 // group g of dy[i]^T x[i].
 //
-// The summed-over direction is the rows', which both operands have across
-// their memory rows (MN-major boxes), and the groups' lengths are known on
-// the device alone.  A unit of work is 64 positions of one group for one
-// 128 x BN tile of the weights; units are numbered tile by tile, and each CTA
-// takes an equal range of them, so that skewed groups, few tiles and many
-// tiles all keep every SM busy.  (Each group also counts kFlush units for
-// writing its tile.)  A range cuts at most the group it starts in and the
-// group it ends in: those two sums go to the workspace in fp32, and a second
-// kernel adds, for each group that was cut, its CTAs' parts in order.
+// Both operands have the summed-over direction across their memory rows
+// (MN-major boxes); zs_grouped_walk.cuh says how the work is shared out.
 #include <initializer_list>
 
 #include "zs_grouped.cuh"
-#include "zs_mma.cuh"
+#include "zs_grouped_walk.cuh"
 
 namespace zs {
 
 namespace {
-
-constexpr int kFlush = 2;        // units that writing a tile costs
-constexpr int kPartRows = 4;     // rows of a tile that one CTA of the second kernel adds
-template <typename T>
-using WeightGroups = Groups<kStageK<T>, kFlush>;   // a unit's positions are a stage's
-
-struct WeightArgs {
-    Matrix dy, x;
-    const int32_t* row_ptr;
-    const int32_t* perm;
-    void* dw;
-    float* partial;      // [CTA][2][128][BN]
-    bool dw_wide;
-    int M, G, N, K;
-    int ktiles;
-    int slots;           // units of a tile, empty ones of no group at its end among them
-    int units, per;      // all units, units of a CTA
-};
 
 template <typename T, bool kTma, int BN>
 struct WeightShape {
@@ -58,50 +33,6 @@ struct WeightShape {
     static constexpr int kSmem = S * (int)kStage + kFixed;
     static constexpr int kThreads = 32 * (4 + kEpilogueWarps + (kTma ? 1 : 2) * kLoaderWarps);
 };
-
-// The part of one group's sum for one tile that a CTA forms.
-struct Segment {
-    int g, n0, k0;
-    int p0, p1;        // positions (none: an empty group, whose sum is zero)
-    bool whole;        // all of the group's positions: written as it is
-    int part;          // else which of the CTA's two partial tiles
-};
-
-// Walks the segments of a CTA's units.  Whole warps.
-template <typename T, int BN>
-struct Walk {
-    const WeightArgs& a;
-    const WeightGroups<T>& gr;
-    int u, begin, end, last;
-    __device__ __forceinline__ Walk(const WeightArgs& args, const WeightGroups<T>& groups)
-        : a(args), gr(groups), u(blockIdx.x * args.per), begin(u), end(imin(u + args.per, args.units)), last(groups.slot(args.G)) {}
-    __device__ __forceinline__ bool next(Segment& s) {
-        while (u < end) {
-            const int t = u / a.slots, first = t * a.slots, slot = u - first, from = u;
-            if (slot >= last) {          // units of no group
-                u = first + a.slots;
-                continue;
-            }
-            s.g = gr.find(slot, a.G);
-            const int g0 = gr.slot(s.g), b = gr.start(s.g), e = gr.start(s.g + 1);
-            u = imin(end, first + gr.slot(s.g + 1));
-            s.n0 = t / a.ktiles * kTileM;
-            s.k0 = t % a.ktiles * BN;
-            s.p0 = (int)imin<int64_t>(b + (int64_t)(slot - g0) * kStageK<T>, e);
-            s.p1 = (int)imin<int64_t>(b + (int64_t)(u - first - g0) * kStageK<T>, e);
-            s.whole = s.p0 == b && s.p1 == e;
-            s.part = from == begin ? 0 : 1;
-            if (s.p0 < s.p1 || (b == e && slot == g0)) return true;   // else only units that count for writing
-        }
-        return false;
-    }
-};
-
-__device__ __forceinline__ int row_at(const WeightArgs& a, int p) {
-    if (!a.perm) return p;
-    const int r = __ldg(a.perm + p);
-    return (uint32_t)r < (uint32_t)a.M ? r : -1;
-}
 
 template <typename T, bool kTma, int BN>
 __global__ void __launch_bounds__(WeightShape<T, kTma, BN>::kThreads, 1)
@@ -146,7 +77,7 @@ weights_mma(const __grid_constant__ CUtensorMap dy_map, const __grid_constant__ 
         constexpr int kPer = kUnit / kLoaderWarps;
         auto row_of = [&](int p) {   // lane i (and 8 j + i) < 8: the row at position p + 8 w + i
             const int at = p + kPer * w + (lane & (kPer - 1));
-            return at < s.p1 ? row_at(a, at) : -1;
+            return at < s.p1 ? weight_row(a, at) : -1;
         };
         if constexpr (kTma) {
             // copies run kLag stages ahead of the arrivals that tell of them
@@ -339,44 +270,9 @@ weights_mma(const __grid_constant__ CUtensorMap dy_map, const __grid_constant__ 
     set.end();
 }
 
-// Block (x, y): the group and tile that CTA x + 1's range begins inside of, if
-// CTA x holds its first positions; rows y * kPartRows .. of the tile, 4
-// columns a thread.
-template <typename T, int BN>
-__global__ void __launch_bounds__(256) weights_join(const WeightArgs a) {
-    pdl_wait();
-    pdl_trigger();
-    const WeightGroups<T> gr{a.row_ptr, a.G, a.M, false};
-    const int cut = (blockIdx.x + 1) * a.per;
-    if (cut >= a.units) return;
-    const int t = cut / a.slots, slot = cut - t * a.slots;
-    if (slot >= gr.slot(a.G)) return;
-    const int g = gr.find(slot, a.G);
-    const int b = gr.start(g), e = gr.start(g + 1);
-    const int u0 = t * a.slots + gr.slot(g), u1 = u0 + (e - b + kStageK<T> - 1) / kStageK<T>;   // units with positions
-    if (u0 >= cut || u1 <= cut) return;             // the group is not cut here
-    const int first = u0 / a.per, last = (u1 - 1) / a.per;
-    if (first != (int)blockIdx.x) return;           // an earlier block adds it
-    const int n0 = t / a.ktiles * kTileM + blockIdx.y * kPartRows, k0 = t % a.ktiles * BN;
-    const int cols = imin(BN, a.K - k0), rows = imin(kPartRows, a.N - n0);
-    constexpr int64_t kTile = (int64_t)kTileM * BN;
-    for (int i = threadIdx.x; i < rows * (BN / 4); i += blockDim.x) {
-        const int r = i / (BN / 4), c = i % (BN / 4) * 4;
-        if (c >= cols) continue;
-        const float* at = a.partial + ((int64_t)blockIdx.y * kPartRows + r) * BN + c;
-        float4 sum = ld_ro4(at + ((int64_t)first * 2 + (u0 == first * a.per ? 0 : 1)) * kTile);
-#pragma unroll 8
-        for (int p = first + 1; p <= last; ++p) sum = f4_add(sum, ld_ro4(at + (int64_t)p * 2 * kTile));
-        T* out = static_cast<T*>(a.dw) + ((int64_t)g * a.N + n0 + r) * a.K + k0 + c;
-        const float v[4] = {sum.x, sum.y, sum.z, sum.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (c + j < cols) out[j] = from_f32<T>(v[j]);
-    }
-}
-
 // Tiles and ranges of a problem; the same on every device, so that the
-// workspace's size is too.
+// workspace's size is too.  One CTA for each of the 152 SMs; short rows take
+// little room, and four of theirs.
 constexpr int kCtas = 152;
 struct WeightPlan {
     int bn;
@@ -385,10 +281,11 @@ struct WeightPlan {
 };
 WeightPlan weight_plan(int32_t dtype, bool tma, int64_t M, int32_t K, int32_t N, int32_t G) {
     WeightPlan p;
-    p.bn = dtype == ZS_F32 ? 64 : K <= 32 ? 32 : K <= 64 ? 64 : (K + 127) / 128 % 2 || !tma ? 128 : 256;
+    p.bn = grouped_is_small(K, N) ? 32 : dtype == ZS_F32 ? 64 : K <= 32 ? 32 : K <= 64 ? 64 : (K + 127) / 128 % 2 || !tma ? 128 : 256;
     p.slots = M / (dtype == ZS_F32 ? kStageK<float> : kStageK<__half>) + (int64_t)G * kFlush;
     p.units = p.slots * ((N + kTileM - 1) / kTileM) * ((K + p.bn - 1) / p.bn);
-    p.per = (p.units + kCtas - 1) / kCtas;
+    const int most = grouped_is_small(K, N) ? 4 * kCtas : kCtas;
+    p.per = (p.units + most - 1) / most;
     p.ctas = p.per ? (int)((p.units + p.per - 1) / p.per) : 0;
     return p;
 }
@@ -458,6 +355,7 @@ zs_status grouped_weights(const char* fn, int32_t dtype, const void* dy, int64_t
     a.M = (int)M, a.G = G, a.N = N, a.K = K;
     a.ktiles = (K + p.bn - 1) / p.bn;
     a.slots = (int)p.slots, a.units = (int)p.units, a.per = (int)p.per;
+    if (grouped_is_small(K, N)) return grouped_small_weights(fn, dtype, a, p.ctas, s);
     switch (dtype) {
         case ZS_F32: return launch_weights<float, false>(fn, a, p, s);
         case ZS_BF16: return tma ? launch_weights<__nv_bfloat16, true>(fn, a, p, s)
