@@ -142,34 +142,20 @@ rows_mma(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUte
         bool have = (!kTma || a.perm) && next_product(a, gr, item, BN, t);
         int row = have ? row_of(t) : -1;
         if constexpr (kTma) {
-            // copies run kLag stages ahead of the arrivals that tell of them
-            constexpr int kLag = S - 1;
-            RingPos<S> told;
-            int ahead = 0;
+            Copies<S> copies;
             while (have && !is_dead(dead)) {
                 const bool more = next_product(a, gr, item, BN, u);
                 const int row_next = more ? row_of(u) : -1;
-                for (int k = 0; k < nk; ++k, pos.next()) {
-                    if (!bounded_wait(set.empty + 8 * pos.stage, pos.phase ^ 1, dead)) break;
-                    copy_rows<kTileM>(smem_u32(ring) + pos.stage * Sh::kStage, a.a, row, k * kBox, w, lane);
-                    copies_commit();
-                    if (++ahead > kLag) {
-                        copies_wait<kLag>();
-                        fence_async_smem();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(set.full + 8 * told.stage);
-                        told.next();
-                    }
+                for (int k = 0; k < nk; ++k) {
+                    if (!copies.acquire(set.full, set.empty, dead)) break;
+                    copy_rows<kTileM>(smem_u32(ring) + copies.next.stage * Sh::kStage, a.a, row, k * kBox, w, lane);
+                    copies.issued();
                 }
                 t = u;
                 row = row_next;
                 have = more;
             }
-            copies_wait<0>();
-            fence_async_smem();
-            __syncwarp();
-            for (int i = imin(ahead, kLag); i > 0; --i, told.next())
-                if (lane == 0) mbar_arrive(set.full + 8 * told.stage);
+            copies.finish(set.full);
         } else {
             // two groups of warps take the stages in turn; while one stage of a group is turned, its next is copied
             // (rows that are not aligned take the room of both)

@@ -167,7 +167,6 @@ zs_status rows_of(const char* fn, const SmallArgs& a, bool transposed, cudaStrea
 // numbers on their way in registers), 4 x 4 results a thread; four groups of
 // threads share the rows and add their sums at the end.
 constexpr int kHeld = 32, kShares = 4, kPer = kThreads / kShares;
-template <typename T>
 __global__ void __launch_bounds__(kThreads) small_weights(const WeightArgs a) {
     constexpr int kLoads = kHeld * kMost / kThreads;
     __shared__ __align__(16) float xs[kHeld][kStride], dys[kHeld][kStride];
@@ -175,13 +174,13 @@ __global__ void __launch_bounds__(kThreads) small_weights(const WeightArgs a) {
     __shared__ int rows[2][kHeld];
     pdl_wait();
     pdl_trigger();
-    const WeightGroups<T> gr{a.row_ptr, a.G, a.M, false};
-    Walk<T, kMost> walk(a, gr);
+    const WeightGroups<float> gr{a.row_ptr, a.G, a.M, false};
+    Walk<float, kMost> walk(a, gr);
     const int tx = threadIdx.x % 8, ty = threadIdx.x / 8 % 8, share = threadIdx.x / kPer;
     Segment s;
     while (walk.next(s)) {
         float acc[4][4] = {};
-        T xv[kLoads], dv[kLoads];
+        float xv[kLoads], dv[kLoads];
         auto number = [&](int p) {
             return threadIdx.x < kHeld && p + (int)threadIdx.x < s.p1 ? weight_row(a, p + threadIdx.x) : -1;
         };
@@ -189,8 +188,8 @@ __global__ void __launch_bounds__(kThreads) small_weights(const WeightArgs a) {
 #pragma unroll
             for (int j = 0; j < kLoads; ++j) {
                 const int i = threadIdx.x + j * kThreads, r = imax(rows[buf][i / kMost], 0), c = i % kMost;
-                xv[j] = static_cast<const T*>(a.x.p)[r * a.x.ld + imin(c, a.K - 1)];
-                dv[j] = static_cast<const T*>(a.dy.p)[r * a.dy.ld + imin(c, a.N - 1)];
+                xv[j] = static_cast<const float*>(a.x.p)[r * a.x.ld + imin(c, a.K - 1)];
+                dv[j] = static_cast<const float*>(a.dy.p)[r * a.dy.ld + imin(c, a.N - 1)];
             }
         };
         int buf = 0, ahead = number(s.p0);
@@ -206,8 +205,8 @@ __global__ void __launch_bounds__(kThreads) small_weights(const WeightArgs a) {
             for (int j = 0; j < kLoads; ++j) {
                 const int i = threadIdx.x + j * kThreads, r = i / kMost, c = i % kMost;
                 const bool in = rows[buf][r] >= 0;
-                xs[r][c] = in ? to_f32(xv[j]) : 0.f;
-                dys[r][c] = in ? to_f32(dv[j]) : 0.f;
+                xs[r][c] = in ? xv[j] : 0.f;
+                dys[r][c] = in ? dv[j] : 0.f;
             }
             __syncthreads();
             if (p + kHeld < s.p1) fetch(buf ^ 1);
@@ -244,28 +243,16 @@ __global__ void __launch_bounds__(kThreads) small_weights(const WeightArgs a) {
             for (int i = 0; i < 4; ++i) {
                 const int n = 4 * ty + i, k = 4 * tx;
                 if (n >= a.N) continue;
-                T* out = static_cast<T*>(a.dw) + ((int64_t)s.g * a.N + n) * a.K + k;
+                float* out = static_cast<float*>(a.dw) + ((int64_t)s.g * a.N + n) * a.K + k;
                 float* part = a.partial + (((int64_t)blockIdx.x * 2 + s.part) * kTileM + n) * kMost + k;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     if (k + j >= a.K) continue;
-                    if (s.whole) out[j] = from_f32<T>(acc[i][j]);
-                    else part[j] = acc[i][j];
+                    (s.whole ? out : part)[j] = acc[i][j];
                 }
             }
         }
     }
-}
-
-template <typename T>
-zs_status weights_of(const char* fn, const WeightArgs& a, int ctas, cudaStream_t s) {
-    launch(small_weights<T>, dim3(ctas), dim3(kThreads), 0, s, a);
-    if (zs_status st = check_launch(fn)) return st;
-    if (ctas > 1) {
-        launch(weights_join<T, kMost>, dim3(ctas - 1, kMost / kPartRows), dim3(256), 0, s, a);
-        return check_launch(fn);
-    }
-    return ZS_OK;
 }
 
 }  // namespace
@@ -286,12 +273,14 @@ zs_status grouped_small_rows(const char* fn, int32_t dtype, int which, const voi
     }
 }
 
-zs_status grouped_small_weights(const char* fn, int32_t dtype, const WeightArgs& a, int ctas, cudaStream_t s) {
-    switch (dtype) {
-        case ZS_F32: return weights_of<float>(fn, a, ctas, s);
-        case ZS_BF16: return weights_of<__nv_bfloat16>(fn, a, ctas, s);
-        default: return weights_of<__half>(fn, a, ctas, s);
+zs_status grouped_small_weights(const char* fn, const WeightArgs& a, int ctas, cudaStream_t s) {
+    launch(small_weights, dim3(ctas), dim3(kThreads), 0, s, a);
+    if (zs_status st = check_launch(fn)) return st;
+    if (ctas > 1) {
+        launch(weights_join<float, kMost>, dim3(ctas - 1, kMost / kPartRows), dim3(256), 0, s, a);
+        return check_launch(fn);
     }
+    return ZS_OK;
 }
 
 }  // namespace zs

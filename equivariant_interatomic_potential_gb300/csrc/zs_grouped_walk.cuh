@@ -124,7 +124,7 @@ __global__ void __launch_bounds__(256) weights_join(const WeightArgs a) {
         if (c + j < cols) out[j] = from_f32<T>(v[j]);
 }
 
-// The gradient where grouped_is_small() (zs_grouped_small.cu): one tile of 32 columns.
-zs_status grouped_small_weights(const char* fn, int32_t dtype, const WeightArgs& a, int ctas, cudaStream_t s);
+// The gradient in fp32 where grouped_is_small() (zs_grouped_small.cu): one tile of 32 columns.
+zs_status grouped_small_weights(const char* fn, const WeightArgs& a, int ctas, cudaStream_t s);
 
 }  // namespace zs

@@ -80,38 +80,24 @@ weights_mma(const __grid_constant__ CUtensorMap dy_map, const __grid_constant__ 
             return at < s.p1 ? weight_row(a, at) : -1;
         };
         if constexpr (kTma) {
-            // copies run kLag stages ahead of the arrivals that tell of them
-            constexpr int kLag = S - 1;
-            RingPos<S> told;
-            int ahead = 0;
+            Copies<S> copies;
             while (!is_dead(dead) && walk.next(s)) {
                 int row = row_of(s.p0);
-                for (int p = s.p0; p < s.p1; p += kUnit, pos.next()) {
+                for (int p = s.p0; p < s.p1; p += kUnit) {
                     const int mine = row;
                     row = row_of(p + kUnit);
-                    if (!bounded_wait(set.empty + 8 * pos.stage, pos.phase ^ 1, dead)) break;
-                    const uint32_t at = smem_u32(ring) + pos.stage * Sh::kStage;
+                    if (!copies.acquire(set.full, set.empty, dead)) break;
+                    const uint32_t at = smem_u32(ring) + copies.next.stage * Sh::kStage;
 #pragma unroll
                     for (int i = 0; i < 2; ++i)
                         if (s.n0 + i * kBoxMN < a.N) copy_rows<kUnit>(at + i * Sh::kBox, a.dy, mine, s.n0 + i * kBoxMN, w, lane);
 #pragma unroll
                     for (int i = 0; i < Sh::kBBoxes; ++i)
                         if (s.k0 + i * kBoxMN < a.K) copy_rows<kUnit>(at + Sh::kA + i * Sh::kBox, a.x, mine, s.k0 + i * kBoxMN, w, lane);
-                    copies_commit();
-                    if (++ahead > kLag) {
-                        copies_wait<kLag>();
-                        fence_async_smem();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(set.full + 8 * told.stage);
-                        told.next();
-                    }
+                    copies.issued();
                 }
             }
-            copies_wait<0>();
-            fence_async_smem();
-            __syncwarp();
-            for (int i = imin(ahead, kLag); i > 0; --i, told.next())
-                if (lane == 0) mbar_arrive(set.full + 8 * told.stage);
+            copies.finish(set.full);
         } else {
             // two groups of warps take the stages in turn; while one stage of a group is turned, its next is copied
             // (rows that are not aligned take the room of both)
@@ -275,16 +261,18 @@ weights_mma(const __grid_constant__ CUtensorMap dy_map, const __grid_constant__ 
 // little room, and four of theirs.
 constexpr int kCtas = 152;
 struct WeightPlan {
+    bool small;          // the CUDA cores form it (zs_grouped_small.cu)
     int bn;
     int64_t slots, units, per;
     int ctas;
 };
 WeightPlan weight_plan(int32_t dtype, bool tma, int64_t M, int32_t K, int32_t N, int32_t G) {
     WeightPlan p;
-    p.bn = grouped_is_small(K, N) ? 32 : dtype == ZS_F32 ? 64 : K <= 32 ? 32 : K <= 64 ? 64 : (K + 127) / 128 % 2 || !tma ? 128 : 256;
+    p.small = dtype == ZS_F32 && grouped_is_small(K, N);   // 16 bits: 19 us on the tensor cores, 25 without (65536 rows)
+    p.bn = p.small ? 32 : dtype == ZS_F32 ? 64 : K <= 32 ? 32 : K <= 64 ? 64 : (K + 127) / 128 % 2 || !tma ? 128 : 256;
     p.slots = M / (dtype == ZS_F32 ? kStageK<float> : kStageK<__half>) + (int64_t)G * kFlush;
     p.units = p.slots * ((N + kTileM - 1) / kTileM) * ((K + p.bn - 1) / p.bn);
-    const int most = grouped_is_small(K, N) ? 4 * kCtas : kCtas;
+    const int most = p.small ? 4 * kCtas : kCtas;
     p.per = (p.units + most - 1) / most;
     p.ctas = p.per ? (int)((p.units + p.per - 1) / p.per) : 0;
     return p;
@@ -355,7 +343,7 @@ zs_status grouped_weights(const char* fn, int32_t dtype, const void* dy, int64_t
     a.M = (int)M, a.G = G, a.N = N, a.K = K;
     a.ktiles = (K + p.bn - 1) / p.bn;
     a.slots = (int)p.slots, a.units = (int)p.units, a.per = (int)p.per;
-    if (grouped_is_small(K, N)) return grouped_small_weights(fn, dtype, a, p.ctas, s);
+    if (p.small) return grouped_small_weights(fn, a, p.ctas, s);
     switch (dtype) {
         case ZS_F32: return launch_weights<float, false>(fn, a, p, s);
         case ZS_BF16: return tma ? launch_weights<__nv_bfloat16, true>(fn, a, p, s)

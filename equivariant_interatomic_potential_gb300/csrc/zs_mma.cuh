@@ -88,6 +88,15 @@ __device__ __forceinline__ bool bounded_wait_one(uint32_t bar, uint32_t parity, 
 }
 __device__ __forceinline__ bool is_dead(volatile int* dead) { return __any_sync(0xffffffffu, *dead != 0); }
 
+// Whether the phase is over, without waiting.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+    return ok != 0;
+}
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" :: "r"(bar) : "memory");
 }
@@ -459,6 +468,45 @@ __device__ __forceinline__ void add_chunk(uint32_t from, int apart, float (&acc)
         for (int j = 0; j < 16; ++j) acc[at + j] += sum[j];
     }
 }
+
+// The copies of a loader warp that are on their way, told of (an arrival at the
+// stage's full barrier) as they land.
+template <int S>
+struct Copies {
+    RingPos<S> next, told;
+    int ahead = 0;      // stages copied and not told of
+    // Waits for the oldest stage and tells of it.
+    __device__ __forceinline__ void tell(uint32_t full) {
+        switch (--ahead) {   // as many newer ones may still be on their way
+            case 0: copies_wait<0>(); break;
+            case 1: copies_wait<1>(); break;
+            case 2: copies_wait<2>(); break;
+            case 3: copies_wait<3>(); break;
+            case 4: copies_wait<4>(); break;
+            case 5: copies_wait<5>(); break;
+            case 6: copies_wait<6>(); break;
+            default: copies_wait<7>(); break;
+        }
+        fence_async_smem();
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) mbar_arrive(full + 8 * told.stage);
+        told.next();
+    }
+    // The next stage is free; while it is not, older ones are told of.
+    __device__ __forceinline__ bool acquire(uint32_t full, uint32_t empty, volatile int* dead) {
+        const uint32_t bar = empty + 8 * next.stage, parity = next.phase ^ 1;
+        while (ahead > 0 && !__all_sync(0xffffffffu, mbar_test(bar, parity))) tell(full);
+        return bounded_wait(bar, parity, dead);
+    }
+    __device__ __forceinline__ void issued() {
+        copies_commit();
+        ++ahead;
+        next.next();
+    }
+    __device__ __forceinline__ void finish(uint32_t full) {
+        while (ahead > 0) tell(full);
+    }
+};
 
 // What every grouped kernel sets up: barriers, TMEM, the groups' starts.
 template <int S, uint32_t kTmemCols, int kTile, int kExtra>
