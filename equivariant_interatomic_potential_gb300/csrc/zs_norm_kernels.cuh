@@ -9,7 +9,7 @@ namespace zs {
 
 namespace {
 
-// CTAs an SM holds, which sets the registers a thread may take.
+// CTAs of kNormThreads an SM holds, which sets the registers a thread may take.
 template <int E>
 constexpr int kFwdCtas = E > 8 ? 2 : 3;
 template <int E>
@@ -91,7 +91,7 @@ __global__ void __launch_bounds__(kNormThreads, kFwdCtas<VEC * NV>) norm_fwd(con
             float z[E];
             ring.open(stage, 2, z, l);
 #pragma unroll
-            for (int i = 0; i < E; ++i) yv[i] = fmaf(sigmoid(z[i]) * pa[i], centred<kLayer>(v[i], hs.x) * hs.y, yv[i]);
+            for (int i = 0; i < E; ++i) yv[i] = fmaf(quick_sigmoid(z[i]) * pa[i], centred<kLayer>(v[i], hs.x) * hs.y, yv[i]);
         } else {
             const float q = s.gate_cols ? sigmoid(to_f32(gate)) : 1.f;
 #pragma unroll
@@ -166,7 +166,7 @@ __global__ void __launch_bounds__(kNormThreads, kBwdCtas<VEC * NV>) norm_bwd(con
         if constexpr (kGate) {
             ring.open(stage, 4, q, l);
 #pragma unroll
-            for (int i = 0; i < E; ++i) q[i] = sigmoid(q[i]);
+            for (int i = 0; i < E; ++i) q[i] = quick_sigmoid(q[i]);
         } else {
             q[0] = s.gate_cols ? sigmoid(to_f32(gate)) : 1.f;
         }
@@ -286,8 +286,9 @@ int start(const NormPlan& p, const NormArgs& a, cudaStream_t s) {
     if (kBackward && p.rows > 1) smem = imax(smem, p.rows * a.s.C * 4);
     constexpr int most = imax(per_thread * kNormThreads, kBackward ? VEC * NV * kNormThreads * 4 : 0);
     static_assert(most <= 224 * 1024, "the ring fits");
-    // as many CTAs as run at once
-    const int per_sm = imin(kBackward ? kBwdCtas<VEC * NV> : kFwdCtas<VEC * NV>, imax(1, 224 * 1024 / (smem + 4096)));
+    // as many CTAs as run at once: by their registers (threads), and by their shared memory
+    const int by_threads = (kBackward ? kBwdCtas<VEC * NV> : kFwdCtas<VEC * NV>) * kNormThreads / p.threads;
+    const int per_sm = imin(by_threads, imax(1, 224 * 1024 / (smem + 4096)));
     const int ctas = num_sms() * per_sm;
     const int groups = norm_groups(a.s.M, p.rows, (kBackward ? imin(kNormCtas, ctas) : ctas) / p.cluster);
     if (groups == 0) return 0;
