@@ -32,10 +32,16 @@ unsigned int take_timeouts_forward();
 unsigned int take_timeouts_backward();
 unsigned int take_timeouts_grouped_rows();
 unsigned int take_timeouts_grouped_weights();
+unsigned int take_timeouts_norm_f32();
+unsigned int take_timeouts_norm_bf16();
+unsigned int take_timeouts_norm_f16();
 cudaError_t set_timeout_flag_forward(unsigned int* flag);
 cudaError_t set_timeout_flag_backward(unsigned int* flag);
 cudaError_t set_timeout_flag_grouped_rows(unsigned int* flag);
 cudaError_t set_timeout_flag_grouped_weights(unsigned int* flag);
+cudaError_t set_timeout_flag_norm_f32(unsigned int* flag);
+cudaError_t set_timeout_flag_norm_bf16(unsigned int* flag);
+cudaError_t set_timeout_flag_norm_f16(unsigned int* flag);
 zs_status selftest_bounded_wait(uint32_t max_spins, cudaStream_t s);
 
 // The driver's cuCtxGetCurrent and cuCtxGetId, resolved once through the
@@ -78,7 +84,8 @@ extern "C" {
 zs_status zs_check_timeouts(void) {
     unsigned int sum = 0;
     for (auto take : {zs::take_timeouts_forward, zs::take_timeouts_backward, zs::take_timeouts_grouped_rows,
-                      zs::take_timeouts_grouped_weights}) {
+                      zs::take_timeouts_grouped_weights, zs::take_timeouts_norm_f32, zs::take_timeouts_norm_bf16,
+                      zs::take_timeouts_norm_f16}) {
         const unsigned int v = take();
         if (v == 0xffffffffu)
             return zs::fail(ZS_ERR_CUDA, "zs_check_timeouts: %s", cudaGetErrorString(cudaGetLastError()));
@@ -107,10 +114,11 @@ zs_status zs_set_timeout_flag(uint32_t* flag) {
             return zs::fail(ZS_ERR_INVALID_ARG, "zs_set_timeout_flag: the word is not 4-byte aligned");
     }
     unsigned int* f = reinterpret_cast<unsigned int*>(flag);
-    cudaError_t err = zs::set_timeout_flag_forward(f);
-    if (err == cudaSuccess) err = zs::set_timeout_flag_backward(f);
-    if (err == cudaSuccess) err = zs::set_timeout_flag_grouped_rows(f);
-    if (err == cudaSuccess) err = zs::set_timeout_flag_grouped_weights(f);
+    cudaError_t err = cudaSuccess;
+    for (auto set : {zs::set_timeout_flag_forward, zs::set_timeout_flag_backward, zs::set_timeout_flag_grouped_rows,
+                     zs::set_timeout_flag_grouped_weights, zs::set_timeout_flag_norm_f32, zs::set_timeout_flag_norm_bf16,
+                     zs::set_timeout_flag_norm_f16})
+        if (err == cudaSuccess) err = set(f);
     if (err != cudaSuccess) return zs::fail(ZS_ERR_CUDA, "zs_set_timeout_flag: %s", cudaGetErrorString(err));
     return ZS_OK;
 }

@@ -31,13 +31,15 @@
 
 #include <initializer_list>
 
+#include "zs_tma.cuh"
 #include "zs_types.cuh"
 
 namespace zs {
 
 constexpr int kNormMaxC = 8192;
 constexpr int kNormThreads = 256;     // of a CTA, at most
-constexpr int kNormWarps = kNormThreads / 32;
+constexpr int kNormWideThreads = 384; // of a CTA of the backward with 16 elements a thread: one CTA an SM, 168 registers
+constexpr int kNormWarps = kNormWideThreads / 32;
 constexpr int kNormCluster = 8;       // CTAs that share a row, at most
 constexpr int kNormCtas = 608;        // of the backward, at most: rows of the partial column sums
 
@@ -133,11 +135,10 @@ struct NormCols {
     }
 };
 
-// The rows on their way: kNormStages stages of NA operands, NV pieces each, in
-// shared memory; a piece of this thread lies `stride` (a slot for each thread
-// of the CTA) after the one before.
-constexpr int kNormStages = 4;
-template <typename T, int VEC, int NV, int NA, bool kEdges>
+// The rows on their way: S stages of NA operands, NV pieces each, in shared
+// memory; a piece of this thread lies `stride` (a slot for each thread of the
+// CTA) after the one before.
+template <typename T, int VEC, int NV, int NA, bool kEdges, int S>
 struct NormRing {
     using Co = NormCols<T, VEC, NV, kEdges>;
     static constexpr int kSlot = VEC == 1 ? 4 : 16;
@@ -150,7 +151,7 @@ struct NormRing {
         mine_s = (uint32_t)__cvta_generic_to_shared(mine);
         stride = blockDim.x * kSlot;
         // pieces outside the row are never copied: they stay zero
-        for (int i = 0; i < kNormStages * NA * NV; ++i) {
+        for (int i = 0; i < S * NA * NV; ++i) {
             if constexpr (VEC == 1) *reinterpret_cast<uint32_t*>(mine + i * stride) = 0;
             else *reinterpret_cast<uint4*>(mine + i * stride) = make_uint4(0, 0, 0, 0);
         }
@@ -175,8 +176,8 @@ struct NormRing {
         }
     }
     static __device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-    // All but the last kNormStages - 1 groups have landed.
-    static __device__ __forceinline__ void wait() { asm volatile("cp.async.wait_group %0;" :: "n"(kNormStages - 1) : "memory"); }
+    // All but the last S - 1 groups have landed.
+    static __device__ __forceinline__ void wait() { asm volatile("cp.async.wait_group %0;" :: "n"(S - 1) : "memory"); }
     static __device__ __forceinline__ void drain() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
     // The elements of operand a in a stage; a neighbour's count as zeros.
@@ -214,8 +215,18 @@ __device__ __forceinline__ void cluster_barrier() {
 // float4 for each warp of each CTA of the row, taken in turn, so that one
 // barrier a round is enough: who writes a round's slots again has passed the
 // barrier of the round between.  Every thread adds them in the same order.
+// Between the CTAs of a cluster the parts travel as asynchronous stores that
+// count on the receiver's mbarrier (a cluster barrier would also wait for the
+// rows' results to reach L2).
 struct NormSums {
     float4 red[2][kNormCluster * kNormWarps];
+    uint64_t bars[2];
+    // Thread 0, before the first barrier of the CTA and the cluster.
+    __device__ __forceinline__ void begin() {
+        mbar_init(smem_u32(&bars[0]), 1);
+        mbar_init(smem_u32(&bars[1]), 1);
+        mbar_fence_init();
+    }
 };
 template <int NQ>
 __device__ __forceinline__ void row_sum(float (&q)[NQ], const NormShape& s, NormSums& sums, int& round) {
@@ -228,7 +239,6 @@ __device__ __forceinline__ void row_sum(float (&q)[NQ], const NormShape& s, Norm
     if (s.tpr <= 32) return;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, per_row = s.tpr >> 5;
     float4* slot = sums.red[round & 1];
-    ++round;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
     float* ve = &v.x;
 #pragma unroll
@@ -242,15 +252,19 @@ __device__ __forceinline__ void row_sum(float (&q)[NQ], const NormShape& s, Norm
         first = 0;
         uint32_t rank;
         asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
-        if (lane < s.cluster) {   // lane i writes this warp's part to CTA i
-            const uint32_t mine = (uint32_t)__cvta_generic_to_shared(slot + rank * (blockDim.x >> 5) + warp);
-            uint32_t there;
-            asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(mine), "r"(lane));
-            asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};"
-                         :: "r"(there), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
+        const uint32_t bar = smem_u32(&sums.bars[round & 1]);
+        if (threadIdx.x == 0) mbar_arrive_expect_tx(bar, per_row * 16);
+        if (lane < s.cluster) {   // lane i sends this warp's part to CTA i
+            uint32_t there, bar_there;
+            asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(smem_u32(slot + rank * (blockDim.x >> 5) + warp)), "r"(lane));
+            asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(bar_there) : "r"(bar), "r"(lane));
+            asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];"
+                         :: "r"(there), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w), "r"(bar_there) : "memory");
         }
-        cluster_barrier();
+        mbar_wait(bar, (uint32_t)(round >> 1) & 1);
+        __syncwarp();
     }
+    ++round;
 #pragma unroll
     for (int i = 0; i < NQ; ++i) q[i] = 0.f;
     for (int w = 0; w < per_row; ++w) {
@@ -295,10 +309,11 @@ __device__ __forceinline__ float quick_sigmoid(float z) { return __fdividef(1.f,
 
 // How a row is spread: over as many threads as need nv pieces each, with the
 // largest nv up to `most` unless a smaller one leaves a fifth fewer slots empty.
+constexpr int norm_threads(int elements, bool backward) { return backward && elements > 8 ? kNormWideThreads : kNormThreads; }
 struct NormPlan {
     int nv, tpr, cluster, threads, rows;
 };
-inline NormPlan norm_plan(int32_t C, int vec, bool edges, int most) {
+inline NormPlan norm_plan(int32_t C, int vec, bool edges, int most, bool backward) {
     const int pieces = (C + (edges ? vec - 1 : 0) + vec - 1) / vec;   // a phase may add one
     NormPlan best = {};
     int least = 0;
@@ -306,7 +321,8 @@ inline NormPlan norm_plan(int32_t C, int vec, bool edges, int most) {
         NormPlan p;
         p.nv = nv;
         int t = (pieces + nv - 1) / nv;
-        p.cluster = (t + kNormThreads - 1) / kNormThreads;
+        const int threads = norm_threads(vec * nv, backward);
+        p.cluster = (t + threads - 1) / threads;
         if (p.cluster > kNormCluster) continue;
         if (t <= 32) {
             p.tpr = t <= 8 ? 8 : t <= 16 ? 16 : 32;
@@ -314,11 +330,11 @@ inline NormPlan norm_plan(int32_t C, int vec, bool edges, int most) {
             t = (t + p.cluster - 1) / p.cluster;
             p.tpr = p.cluster * ((t + 31) / 32 * 32);
         }
-        p.rows = p.cluster > 1 ? 1 : kNormThreads / p.tpr;
+        p.rows = p.cluster > 1 ? 1 : threads / p.tpr;
         p.threads = p.cluster > 1 ? p.tpr / p.cluster : p.rows * p.tpr;
         if (least == 0 || p.tpr * nv * 5 < least * 4) best = p, least = p.tpr * nv;
     }
-    return least || most >= 4 ? best : norm_plan(C, vec, edges, 2 * most);   // the row takes more pieces a thread
+    return least || most >= 4 ? best : norm_plan(C, vec, edges, 2 * most, backward);   // the row takes more pieces a thread
 }
 // Groups of rows (CTAs, or clusters) for M rows, `most` at most: a multiple of
 // 8 where a group takes several rounds, so that its phase stays.

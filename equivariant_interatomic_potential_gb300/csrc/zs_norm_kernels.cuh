@@ -9,11 +9,15 @@ namespace zs {
 
 namespace {
 
-// CTAs of kNormThreads an SM holds, which sets the registers a thread may take.
+// CTAs of norm_threads() an SM holds, which sets the registers a thread may
+// take, and stages of the rows on their way.
 template <int E>
 constexpr int kFwdCtas = E > 8 ? 2 : 3;
 template <int E>
 constexpr int kBwdCtas = E > 8 ? 1 : 2;
+constexpr int kFwdStages = 4;
+template <int E>
+constexpr int kBwdStages = E > 8 ? 3 : 4;
 
 // Mean (kLayer) and 1/root of a row's values: the mean first, then the
 // centred squares, both over the registers.  v is zero outside the row.
@@ -53,8 +57,10 @@ __global__ void __launch_bounds__(kNormThreads, kFwdCtas<VEC * NV>) norm_fwd(con
     const NormShape& s = a.s;
     const NormPlace at(s);
     NormLane l{s.tpr, at.lane, s.C, 0};
-    NormRing<T, VEC, NV, NA, kEdges> ring;
+    constexpr int S = kFwdStages;
+    NormRing<T, VEC, NV, NA, kEdges, S> ring;
     ring.init(smem);
+    if (threadIdx.x == 0) sums.begin();
     if (s.cluster > 1) cluster_barrier();   // every CTA of the row runs before another writes to it
     pdl_wait();
     pdl_trigger();
@@ -72,7 +78,7 @@ __global__ void __launch_bounds__(kNormThreads, kFwdCtas<VEC * NV>) norm_fwd(con
     auto gate_of = [&](int64_t row) {
         return !kGate && s.gate_cols && row < s.M ? static_cast<const T*>(a.gate.p)[row * a.gate.ld] : from_f32<T>(0.f);
     };
-    for (int i = 0; i < kNormStages - 1; ++i) issue(i);
+    for (int i = 0; i < S - 1; ++i) issue(i);
     T gate = gate_of(r);
     float pa[E], wr[E];
     Co::columns(pa, l, [&](int c) { return __ldg(a.scale + c) * __ldg(a.w_post + c); });
@@ -80,7 +86,7 @@ __global__ void __launch_bounds__(kNormThreads, kFwdCtas<VEC * NV>) norm_fwd(con
     int stage = 0;
     // every thread of the CTA goes round as often: the row sums may hold a barrier
     for (int64_t r0 = at.first; r0 < s.M; r0 += at.step, r += at.step) {
-        issue((stage + kNormStages - 1) % kNormStages);
+        issue((stage + S - 1) % S);
         const T gate_next = gate_of(r + at.step);
         ring.wait();
         float v[E], yv[E];
@@ -106,14 +112,14 @@ __global__ void __launch_bounds__(kNormThreads, kFwdCtas<VEC * NV>) norm_fwd(con
             if (a.stats_out && l.lane == 0) a.stats_out[r] = make_float4(hs.x, hs.y, ys.x, ys.y);
         }
         gate = gate_next;
-        stage = (stage + 1) % kNormStages;
+        stage = (stage + 1) % S;
     }
     ring.drain();
     if (s.cluster > 1) cluster_barrier();   // no CTA leaves while another may write to it
 }
 
 template <typename T, int VEC, int NV, bool kEdges, bool kGate, bool kLayer>
-__global__ void __launch_bounds__(kNormThreads, kBwdCtas<VEC * NV>) norm_bwd(const NormArgs a) {
+__global__ void __launch_bounds__(norm_threads(VEC * NV, true), kBwdCtas<VEC * NV>) norm_bwd(const NormArgs a) {
     using Co = NormCols<T, VEC, NV, kEdges>;
     constexpr int E = Co::E, NA = kGate ? 5 : 4;
     __shared__ NormSums sums;
@@ -122,8 +128,10 @@ __global__ void __launch_bounds__(kNormThreads, kBwdCtas<VEC * NV>) norm_bwd(con
     const NormShape& s = a.s;
     const NormPlace at(s);
     NormLane l{s.tpr, at.lane, s.C, 0};
-    NormRing<T, VEC, NV, NA, kEdges> ring;
+    constexpr int S = kBwdStages<E>;
+    NormRing<T, VEC, NV, NA, kEdges, S> ring;
     ring.init(smem);
+    if (threadIdx.x == 0) sums.begin();
     if (s.cluster > 1) cluster_barrier();   // every CTA of the row runs before another writes to it
     pdl_wait();
     pdl_trigger();
@@ -144,7 +152,7 @@ __global__ void __launch_bounds__(kNormThreads, kBwdCtas<VEC * NV>) norm_bwd(con
         return !kGate && s.gate_cols && row < s.M ? static_cast<const T*>(a.gate.p)[row * a.gate.ld] : from_f32<T>(0.f);
     };
     auto stats_of = [&](int64_t row) { return row < s.M ? __ldg(a.stats_in + row) : make_float4(0.f, 0.f, 0.f, 0.f); };
-    for (int i = 0; i < kNormStages - 1; ++i) issue(i);
+    for (int i = 0; i < S - 1; ++i) issue(i);
     T gate = gate_of(r);
     float4 st = stats_of(r);
     float pa[E], wr[E], sum_b[E], sum_pre[E];
@@ -155,7 +163,7 @@ __global__ void __launch_bounds__(kNormThreads, kBwdCtas<VEC * NV>) norm_bwd(con
     int stage = 0;
     // every thread of the CTA goes round as often: the row sums may hold a barrier
     for (int64_t r0 = at.first; r0 < s.M; r0 += at.step, r += at.step) {
-        issue((stage + kNormStages - 1) % kNormStages);
+        issue((stage + S - 1) % S);
         const T gate_next = gate_of(r + at.step);
         const float4 st_next = stats_of(r + at.step);
         const bool live = r < s.M;
@@ -223,7 +231,7 @@ __global__ void __launch_bounds__(kNormThreads, kBwdCtas<VEC * NV>) norm_bwd(con
         }
         gate = gate_next;
         st = st_next;
-        stage = (stage + 1) % kNormStages;
+        stage = (stage + 1) % S;
     }
     ring.drain();
     // the group's column sums: its rows' (which may be at other phases) added in order
@@ -281,13 +289,14 @@ __global__ void __launch_bounds__(kSumCols * kSumRows) norm_column_sums(const No
 template <typename T, int VEC, int NV, bool kEdges, bool kBackward, bool kGate, bool kLayer>
 int start(const NormPlan& p, const NormArgs& a, cudaStream_t s) {
     constexpr int NA = kBackward ? (kGate ? 5 : 4) : (kGate ? 3 : 2);
-    constexpr int per_thread = kNormStages * NA * NV * NormRing<T, VEC, NV, NA, kEdges>::kSlot;
+    constexpr int S = kBackward ? kBwdStages<VEC * NV> : kFwdStages, kThreads = norm_threads(VEC * NV, kBackward);
+    constexpr int per_thread = S * NA * NV * NormRing<T, VEC, NV, NA, kEdges, S>::kSlot;
     int smem = per_thread * p.threads;
     if (kBackward && p.rows > 1) smem = imax(smem, p.rows * a.s.C * 4);
-    constexpr int most = imax(per_thread * kNormThreads, kBackward ? VEC * NV * kNormThreads * 4 : 0);
+    constexpr int most = imax(per_thread * kThreads, kBackward ? VEC * NV * kThreads * 4 : 0);
     static_assert(most <= 224 * 1024, "the ring fits");
     // as many CTAs as run at once: by their registers (threads), and by their shared memory
-    const int by_threads = (kBackward ? kBwdCtas<VEC * NV> : kFwdCtas<VEC * NV>) * kNormThreads / p.threads;
+    const int by_threads = (kBackward ? kBwdCtas<VEC * NV> : kFwdCtas<VEC * NV>) * kThreads / p.threads;
     const int per_sm = imin(by_threads, imax(1, 224 * 1024 / (smem + 4096)));
     const int ctas = num_sms() * per_sm;
     const int groups = norm_groups(a.s.M, p.rows, (kBackward ? imin(kNormCtas, ctas) : ctas) / p.cluster);
@@ -333,8 +342,8 @@ zs_status dispatch(NormArgs& a, cudaStream_t s) {
     // that the backward, which holds more for each element, takes one where a warp then holds the row (65536 x 256 bf16
     // 57 against 70 us, 647170 x 128 fp32 406 against 418) and where the pieces at a row's ends take registers too
     // (4097 x 1031 fp16 48 against 58).
-    const int most = kBackward && (w.edges || C <= 32 * V) ? 1 : 2;
-    const NormPlan p = w.wide ? norm_plan(a.s.C, V, w.edges, most) : norm_plan(a.s.C, 1, false, 4);
+    const int most = kBackward && (w.edges ? C <= 256 * V : C <= 32 * V) ? 1 : 2;
+    const NormPlan p = w.wide ? norm_plan(a.s.C, V, w.edges, most, kBackward) : norm_plan(a.s.C, 1, false, 4, kBackward);
     a.s.tpr = p.tpr;
     a.s.cluster = p.cluster;
     if (!w.wide) {   // operands at different phases: element by element
