@@ -145,6 +145,7 @@ struct NormRing {
     unsigned char* mine;    // this thread's first slot
     uint32_t mine_s;        // its shared address
     uint32_t stride;
+    uint4 mask[kEdges ? NV : 1];
 
     __device__ __forceinline__ void init(unsigned char* smem) {
         mine = smem + threadIdx.x * kSlot;
@@ -180,8 +181,27 @@ struct NormRing {
     static __device__ __forceinline__ void wait() { asm volatile("cp.async.wait_group %0;" :: "n"(S - 1) : "memory"); }
     static __device__ __forceinline__ void drain() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
+    // Which bits of this thread's pieces are the row's (the phase is set).
+    __device__ __forceinline__ void cut(const NormLane& l) {
+        if constexpr (kEdges) {
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                const int c0 = Co::start(l, k);
+                uint32_t* m = &mask[k].x;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    if constexpr (sizeof(T) == 4) {
+                        m[j] = (unsigned)(c0 + j) < (unsigned)l.C ? 0xffffffffu : 0u;
+                    } else {
+                        m[j] = ((unsigned)(c0 + 2 * j) < (unsigned)l.C ? 0xffffu : 0u) |
+                               ((unsigned)(c0 + 2 * j + 1) < (unsigned)l.C ? 0xffff0000u : 0u);
+                    }
+                }
+            }
+        }
+    }
     // The elements of operand a in a stage; a neighbour's count as zeros.
-    __device__ __forceinline__ void open(int stage, int a, float (&f)[Co::E], const NormLane& l) const {
+    __device__ __forceinline__ void open(int stage, int a, float (&f)[Co::E]) const {
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             const unsigned char* slot = mine + ((stage * NA + a) * NV + k) * stride;
@@ -189,17 +209,11 @@ struct NormRing {
                 f[k] = to_f32(*reinterpret_cast<const T*>(slot));
             } else {
                 float q[VEC];
-                unpack<T>(*reinterpret_cast<const uint4*>(slot), q);
+                uint4 raw = *reinterpret_cast<const uint4*>(slot);
+                if constexpr (kEdges) raw = make_uint4(raw.x & mask[k].x, raw.y & mask[k].y, raw.z & mask[k].z, raw.w & mask[k].w);
+                unpack<T>(raw, q);
 #pragma unroll
                 for (int i = 0; i < VEC; ++i) f[k * VEC + i] = q[i];
-                if constexpr (kEdges) {
-                    const int c0 = Co::start(l, k);
-                    if (!Co::whole(l, c0)) {
-#pragma unroll
-                        for (int i = 0; i < VEC; ++i)
-                            f[k * VEC + i] = (unsigned)(c0 + i) < (unsigned)l.C ? f[k * VEC + i] : 0.f;
-                    }
-                }
             }
         }
     }
@@ -308,7 +322,7 @@ __device__ __forceinline__ float sigmoid(float z) { return __frcp_rn(1.f + expf(
 __device__ __forceinline__ float quick_sigmoid(float z) { return __fdividef(1.f, 1.f + __expf(-z)); }
 
 // How a row is spread: over as many threads as need nv pieces each, with the
-// largest nv up to `most` unless a smaller one leaves a fifth fewer slots empty.
+// largest nv up to `most` unless a smaller one takes a tenth fewer slots.
 constexpr int norm_threads(int elements, bool backward) { return backward && elements > 8 ? kNormWideThreads : kNormThreads; }
 struct NormPlan {
     int nv, tpr, cluster, threads, rows;
@@ -332,7 +346,7 @@ inline NormPlan norm_plan(int32_t C, int vec, bool edges, int most, bool backwar
         }
         p.rows = p.cluster > 1 ? 1 : threads / p.tpr;
         p.threads = p.cluster > 1 ? p.tpr / p.cluster : p.rows * p.tpr;
-        if (least == 0 || p.tpr * nv * 5 < least * 4) best = p, least = p.tpr * nv;
+        if (least == 0 || p.tpr * nv * 10 < least * 9) best = p, least = p.tpr * nv;
     }
     return least || most >= 4 ? best : norm_plan(C, vec, edges, 2 * most, backward);   // the row takes more pieces a thread
 }

@@ -66,6 +66,7 @@ __global__ void __launch_bounds__(kNormThreads, kFwdCtas<VEC * NV>) norm_fwd(con
     pdl_trigger();
     int64_t r = at.first + at.sub, ahead = r;
     if (kEdges) l.phase = (int)((reinterpret_cast<uintptr_t>(static_cast<const T*>(a.h.p) + r * a.h.ld) & 15u) / sizeof(T));
+    ring.cut(l);
     auto issue = [&](int stage) {
         if (ahead < s.M) {
             ring.issue(stage, 0, a.h, ahead, s.M, l);
@@ -90,12 +91,12 @@ __global__ void __launch_bounds__(kNormThreads, kFwdCtas<VEC * NV>) norm_fwd(con
         const T gate_next = gate_of(r + at.step);
         ring.wait();
         float v[E], yv[E];
-        ring.open(stage, 0, v, l);
+        ring.open(stage, 0, v);
         const float2 hs = row_stats<Co, kLayer>(v, s, l, sums, round);
-        ring.open(stage, 1, yv, l);
+        ring.open(stage, 1, yv);
         if constexpr (kGate) {
             float z[E];
-            ring.open(stage, 2, z, l);
+            ring.open(stage, 2, z);
 #pragma unroll
             for (int i = 0; i < E; ++i) yv[i] = fmaf(quick_sigmoid(z[i]) * pa[i], centred<kLayer>(v[i], hs.x) * hs.y, yv[i]);
         } else {
@@ -137,6 +138,7 @@ __global__ void __launch_bounds__(norm_threads(VEC * NV, true), kBwdCtas<VEC * N
     pdl_trigger();
     int64_t r = at.first + at.sub, ahead = r;
     if (kEdges) l.phase = (int)((reinterpret_cast<uintptr_t>(static_cast<const T*>(a.h.p) + r * a.h.ld) & 15u) / sizeof(T));
+    ring.cut(l);
     auto issue = [&](int stage) {
         if (ahead < s.M) {
             ring.issue(stage, 0, a.h, ahead, s.M, l);
@@ -169,10 +171,10 @@ __global__ void __launch_bounds__(norm_threads(VEC * NV, true), kBwdCtas<VEC * N
         const bool live = r < s.M;
         ring.wait();
         float nh[E], ny[E], q[kGate ? E : 1], d[E];
-        ring.open(stage, 0, nh, l);
-        ring.open(stage, 1, ny, l);
+        ring.open(stage, 0, nh);
+        ring.open(stage, 1, ny);
         if constexpr (kGate) {
-            ring.open(stage, 4, q, l);
+            ring.open(stage, 4, q);
 #pragma unroll
             for (int i = 0; i < E; ++i) q[i] = quick_sigmoid(q[i]);
         } else {
@@ -184,7 +186,7 @@ __global__ void __launch_bounds__(norm_threads(VEC * NV, true), kBwdCtas<VEC * N
             nh[i] = centred<kLayer>(nh[i], st.x) * st.y;
             ny[i] = centred<kLayer>(fmaf(gate_at(i) * pa[i], nh[i], ny[i]), st.z) * st.w;
         }
-        ring.open(stage, 2, d, l);
+        ring.open(stage, 2, d);
         if (!live) {   // a row that is not there adds nothing
 #pragma unroll
             for (int i = 0; i < E; ++i) d[i] = nh[i] = ny[i] = 0.f;
@@ -202,7 +204,7 @@ __global__ void __launch_bounds__(norm_threads(VEC * NV, true), kBwdCtas<VEC * N
         float dm = 0.f;
         if constexpr (kLayer) dm = m[1] * s.inv_c;
         float dx[E];
-        ring.open(stage, 3, dx, l);
+        ring.open(stage, 3, dx);
 #pragma unroll
         for (int i = 0; i < E; ++i) dx[i] = fmaf(st.w, fmaf(dn, ny[i], centred<kLayer>(d[i], dm)), dx[i]);
         if (live) Co::store(static_cast<T*>(a.out1) + r * s.C, dx, l);
@@ -260,7 +262,7 @@ __global__ void __launch_bounds__(norm_threads(VEC * NV, true), kBwdCtas<VEC * N
 
 // The gradients of the parameters from the groups' column sums, added in
 // order: kSumRows threads a column, then their sums in order.
-constexpr int kSumCols = 32, kSumRows = 16;
+constexpr int kSumCols = 32, kSumRows = 32;
 __global__ void __launch_bounds__(kSumCols * kSumRows) norm_column_sums(const NormArgs a, int groups) {
     __shared__ float part[kSumRows][kSumCols];
     const int j = threadIdx.x % kSumCols, k = threadIdx.x / kSumCols, C = a.s.C;
