@@ -11,6 +11,12 @@ and "Tests").  Here that operator is a ``torch.library`` custom op:
   num_nodes) -> (out, out_raw)``: the degree normalisation the pages apply
   after the operator (section "What", third bullet), fused: out[n] =
   node_scale[n] * the operator's sum, differentiable in node_scale too
+  ``zs_gie::grouped_matmul(x, w, row_ptr, perm) -> y``: each row times the
+  weights of its group (its species, or species and degree), the groups in a
+  CSR from ``build_csr``; differentiable in x and w
+  ``zs_gie::norm_gate_residual(h, x, gate, w_post, scale, w_pre, eps, kind) ->
+  (y, u, stats)``: the norms around a block with its gate, residual scale and
+  residual sum; differentiable in every tensor (``optim.AdamW`` steps them)
 
 ``zonal_scatter``'s backward is ``zs_gie::zonal_scatter_backward``, itself
 an operator without a derivative, so a second backward raises.  It takes the
@@ -26,6 +32,8 @@ memory, no synchronisation) and raises if a bounded wait of an earlier
 launch ran out.
 """
 from __future__ import annotations
+
+from typing import Optional
 
 import torch
 
@@ -174,3 +182,119 @@ def degree_normalised_scatter(coup: torch.Tensor, rad: torch.Tensor, dst: torch.
     """CSR of dst, then node_scale[n] * zonal scatter, differentiable in coup, rad and node_scale."""
     row_ptr, perm = build_csr(dst, num_nodes)
     return zonal_scatter_scaled(coup, rad, dst, row_ptr, perm, node_scale, num_nodes)[0]
+
+
+@torch.library.custom_op(f"{_NS}::grouped_matmul", mutates_args=())
+def grouped_matmul(x: torch.Tensor, w: torch.Tensor, row_ptr: torch.Tensor,
+                   perm: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """y[i] = w[g(i)] x[i]: x (M, K), w (G, N, K), the CSR (row_ptr, perm) of the rows' groups; y (M, N)."""
+    _cuda_only("grouped_matmul", x, w, row_ptr)
+    return zs.zs_grouped_matmul(x.contiguous(), w.contiguous(), row_ptr.contiguous(), perm)
+
+
+@grouped_matmul.register_fake
+def _(x, w, row_ptr, perm=None):
+    return x.new_empty((x.shape[0], w.shape[1]))
+
+
+@torch.library.custom_op(f"{_NS}::grouped_matmul_backward", mutates_args=())
+def grouped_matmul_backward(dy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, row_ptr: torch.Tensor,
+                            perm: Optional[torch.Tensor] = None) -> tuple[torch.Tensor, torch.Tensor]:
+    """(dx (M, K), dw (G, N, K)) for the cotangent dy (M, N)."""
+    _cuda_only("grouped_matmul_backward", dy, x, w, row_ptr)
+    return zs.zs_grouped_matmul_backward(dy.contiguous(), x.contiguous(), w.contiguous(), row_ptr.contiguous(), perm)
+
+
+@grouped_matmul_backward.register_fake
+def _(dy, x, w, row_ptr, perm=None):
+    return x.new_empty(x.shape), w.new_empty(w.shape)
+
+
+def _setup_context_grouped(ctx, inputs, output):
+    ctx.save_for_backward(*inputs[:3], *(t for t in inputs[3:] if t is not None))
+
+
+def _backward_grouped(ctx, dy):
+    x, w, row_ptr, *perm = ctx.saved_tensors
+    perm = perm[0] if perm else None
+    if ctx.needs_input_grad[0] and ctx.needs_input_grad[1]:
+        return (*grouped_matmul_backward(dy, x, w, row_ptr, perm), None, None)
+    if ctx.needs_input_grad[0]:   # fixed weights: the forces' path
+        return grouped_matmul_dx(dy, w, row_ptr, perm), None, None, None
+    return None, grouped_matmul_backward(dy, x, w, row_ptr, perm)[1], None, None
+
+
+@torch.library.custom_op(f"{_NS}::grouped_matmul_dx", mutates_args=())
+def grouped_matmul_dx(dy: torch.Tensor, w: torch.Tensor, row_ptr: torch.Tensor,
+                      perm: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """dx (M, K) alone, for the cotangent dy (M, N)."""
+    _cuda_only("grouped_matmul_dx", dy, w, row_ptr)
+    return zs.zs_grouped_matmul_dx(dy.contiguous(), w.contiguous(), row_ptr.contiguous(), perm)
+
+
+@grouped_matmul_dx.register_fake
+def _(dy, w, row_ptr, perm=None):
+    return dy.new_empty((dy.shape[0], w.shape[2]))
+
+
+grouped_matmul.register_autograd(_backward_grouped, setup_context=_setup_context_grouped)
+
+
+def species_linear(x: torch.Tensor, w: torch.Tensor, species: torch.Tensor) -> torch.Tensor:
+    """CSR of the rows' species (M,) int32, then y[i] = w[species[i]] x[i], differentiable in
+    x and w.  Rows whose species is outside [0, G) give zeros."""
+    row_ptr, perm = build_csr(species, w.shape[0])
+    return grouped_matmul(x, w, row_ptr, perm)
+
+
+@torch.library.custom_op(f"{_NS}::norm_gate_residual", mutates_args=())
+def norm_gate_residual(h: torch.Tensor, x: torch.Tensor, gate: Optional[torch.Tensor], w_post: torch.Tensor,
+                       scale: torch.Tensor, w_pre: torch.Tensor, eps: float = 1e-6,
+                       kind: str = "rms") -> tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """(y, u, stats): y = x + scale * sigmoid(gate) * (norm(h) * w_post), u = norm(y) * w_pre; stats (M, 4)
+    holds the rows' means and 1/roots and has no gradient."""
+    _cuda_only("norm_gate_residual", h, x, w_post, scale, w_pre)
+    return zs.zs_norm_gate_residual(h.contiguous(), x.contiguous(), None if gate is None else gate.contiguous(), w_post,
+                                    scale, w_pre, eps=eps, kind=kind)
+
+
+@norm_gate_residual.register_fake
+def _(h, x, gate, w_post, scale, w_pre, eps=1e-6, kind="rms"):
+    return h.new_empty(h.shape), h.new_empty(h.shape), h.new_empty((h.shape[0], 4), dtype=torch.float32)
+
+
+@torch.library.custom_op(f"{_NS}::norm_gate_residual_backward", mutates_args=())
+def norm_gate_residual_backward(
+        dy: torch.Tensor, du: torch.Tensor, h: torch.Tensor, x: torch.Tensor, gate: Optional[torch.Tensor],
+        w_post: torch.Tensor, scale: torch.Tensor, w_pre: torch.Tensor, stats: torch.Tensor, kind: str = "rms",
+) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor, torch.Tensor, torch.Tensor, torch.Tensor]:
+    """(dh, dx, dgate, dw_post, dscale, dw_pre) for the cotangents dy and du; dgate is empty without a gate."""
+    _cuda_only("norm_gate_residual_backward", dy, du, h, x, w_post, scale, w_pre, stats)
+    dh, dx, dgate, *sums = zs.zs_norm_gate_residual_backward(
+        dy.contiguous(), du.contiguous(), h.contiguous(), x.contiguous(), None if gate is None else gate.contiguous(), w_post,
+        scale, w_pre, stats, kind=kind)
+    return (dh, dx, h.new_empty(0) if dgate is None else dgate, *sums)
+
+
+@norm_gate_residual_backward.register_fake
+def _(dy, du, h, x, gate, w_post, scale, w_pre, stats, kind="rms"):
+    dgate = h.new_empty(0) if gate is None else gate.new_empty(gate.shape)
+    return (h.new_empty(h.shape), x.new_empty(x.shape), dgate, *(t.new_empty(t.shape) for t in (w_post, scale, w_pre)))
+
+
+def _setup_context_norm(ctx, inputs, output):
+    h, x, gate, w_post, scale, w_pre, eps, kind = inputs
+    ctx.mark_non_differentiable(output[2])
+    ctx.save_for_backward(h, x, w_post, scale, w_pre, output[2], *(() if gate is None else (gate,)))
+    ctx.kind = kind
+
+
+def _backward_norm(ctx, dy, du, _):
+    h, x, w_post, scale, w_pre, stats, *gate = ctx.saved_tensors
+    gate = gate[0] if gate else None
+    dh, dx, dgate, dw_post, dscale, dw_pre = norm_gate_residual_backward(dy, du, h, x, gate, w_post, scale, w_pre, stats,
+                                                                         ctx.kind)
+    return dh, dx, None if gate is None else dgate, dw_post, dscale, dw_pre, None, None
+
+
+norm_gate_residual.register_autograd(_backward_norm, setup_context=_setup_context_norm)
