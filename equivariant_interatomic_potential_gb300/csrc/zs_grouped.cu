@@ -56,6 +56,65 @@ zs_status check_ld(const char* fn, const char* what, int64_t ld, int64_t cols, i
     return ZS_OK;
 }
 
+// Rows of `cols` elements as whole 16-byte pieces.
+int64_t padded(int32_t dtype, int64_t cols) {
+    const int64_t per16 = 16 / dtype_bytes(dtype);
+    return (cols + per16 - 1) / per16 * per16;
+}
+bool pieces(int32_t dtype, const void* p, int64_t ld) { return aligned16(p) && ld % (16 / dtype_bytes(dtype)) == 0; }
+
+// Hands out a workspace's room for padded matrices.
+struct Padder {
+    Padding list[2] = {};
+    int n = 0;
+    char* room;
+    size_t left;
+    int32_t dtype;
+    // The matrix as it is, or (p and ld replaced) its place in the workspace where its rows are not whole pieces and it fits.
+    void lay_out(const void*& p, int64_t& ld, int64_t rows, int32_t cols) {
+        if (pieces(dtype, p, ld) || rows == 0) return;
+        const int64_t to = padded(dtype, cols);
+        const size_t bytes = align_up((size_t)rows * to * dtype_bytes(dtype), 256);
+        if (!room || bytes > left) return;
+        list[n++] = {p, ld, rows, cols, room};
+        p = room;
+        ld = to;
+        room += bytes;
+        left -= bytes;
+    }
+};
+
+// Fewer rows than this are not worth a copy.
+constexpr int64_t kPadRows = 256;
+size_t padded_bytes(int32_t dtype, int64_t rows, int32_t cols) {
+    return align_up((size_t)rows * padded(dtype, cols) * dtype_bytes(dtype), 256);
+}
+
+zs_status product(const char* fn, int which, int32_t dtype, const void* a, int64_t a_ld, const void* w, const int32_t* row_ptr,
+                  const int32_t* perm, int64_t M, int32_t K, int32_t N, int32_t G, void* out, int64_t out_ld, void* workspace,
+                  size_t workspace_bytes, zs_stream_t stream) {
+    const void* any = row_ptr;   // what is not read when a size is zero need not exist
+    if (zs_status st = check(fn, dtype, M, K, N, G, row_ptr, perm, {M ? a : any, M && G ? w : any, M ? out : any})) return st;
+    const int32_t in_cols = which ? N : K, out_cols = which ? K : N;
+    if (zs_status st = check_ld(fn, which ? "dy_ld" : "x_ld", a_ld, in_cols, M)) return st;
+    if (zs_status st = check_ld(fn, which ? "dx_ld" : "y_ld", out_ld, out_cols, M)) return st;
+    if (reinterpret_cast<uintptr_t>(workspace) & 255u)
+        return fail(ZS_ERR_INVALID_ARG, "%s: workspace is not 256-byte aligned", fn);
+    if (M == 0) return ZS_OK;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (M == 1) a_ld = in_cols;
+    if (grouped_is_few(dtype, which, M, N, G)) return grouped_few(fn, dtype, which, a, a_ld, w, K, row_ptr, perm, M, K, N, G, out, out_ld, s);
+    if (grouped_is_small(K, N)) return grouped_small_rows(fn, dtype, which, a, a_ld, w, row_ptr, perm, M, K, N, G, out, out_ld, s);
+    int64_t w_ld = K;
+    Padder pad{{}, 0, static_cast<char*>(workspace), workspace ? workspace_bytes : 0, dtype};
+    if (M >= kPadRows) {
+        pad.lay_out(w, w_ld, (int64_t)G * N, K);
+        pad.lay_out(a, a_ld, M, in_cols);
+        if (zs_status st = grouped_pad(fn, dtype, pad.list, s)) return st;
+    }
+    return grouped_rows(fn, dtype, a, a_ld, w, w_ld, row_ptr, perm, M, K, N, G, out, out_ld, which != 0, s);
+}
+
 }  // namespace
 
 }  // namespace zs
@@ -65,38 +124,47 @@ extern "C" {
 zs_status zs_grouped_matmul(int32_t dtype, const void* x, int64_t x_ld, const void* w, const int32_t* row_ptr,
                             const int32_t* perm, int64_t M, int32_t K, int32_t N, int32_t G, void* y, int64_t y_ld,
                             zs_stream_t stream) {
-    using namespace zs;
-    const char* fn = "zs_grouped_matmul";
-    const void* any = row_ptr;   // what is not read when a size is zero need not exist
-    if (zs_status st = check(fn, dtype, M, K, N, G, row_ptr, perm, {M ? x : any, M && G ? w : any, M ? y : any})) return st;
-    if (zs_status st = check_ld(fn, "x_ld", x_ld, K, M)) return st;
-    if (zs_status st = check_ld(fn, "y_ld", y_ld, N, M)) return st;
-    if (M == 0) return ZS_OK;
-    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (grouped_is_few(dtype, 0, M, N, G)) return grouped_few(fn, dtype, 0, x, x_ld, w, K, row_ptr, perm, M, K, N, G, y, y_ld, s);
-    if (grouped_is_small(K, N)) return grouped_small_rows(fn, dtype, 0, x, x_ld, w, row_ptr, perm, M, K, N, G, y, y_ld, s);
-    return grouped_rows(fn, dtype, x, M > 1 ? x_ld : K, w, row_ptr, perm, M, K, N, G, y, y_ld, false, s);
+    return zs::product("zs_grouped_matmul", 0, dtype, x, x_ld, w, row_ptr, perm, M, K, N, G, y, y_ld, nullptr, 0, stream);
 }
 
 zs_status zs_grouped_matmul_dx(int32_t dtype, const void* dy, int64_t dy_ld, const void* w, const int32_t* row_ptr,
                                const int32_t* perm, int64_t M, int32_t K, int32_t N, int32_t G, void* dx, int64_t dx_ld,
                                zs_stream_t stream) {
+    return zs::product("zs_grouped_matmul_dx", 1, dtype, dy, dy_ld, w, row_ptr, perm, M, K, N, G, dx, dx_ld, nullptr, 0, stream);
+}
+
+size_t zs_grouped_matmul_workspace_bytes(int32_t dtype, int64_t M, int32_t K, int32_t N, int32_t G) {
     using namespace zs;
-    const char* fn = "zs_grouped_matmul_dx";
-    const void* any = row_ptr;
-    if (zs_status st = check(fn, dtype, M, K, N, G, row_ptr, perm, {M ? dy : any, M && G ? w : any, M ? dx : any})) return st;
-    if (zs_status st = check_ld(fn, "dy_ld", dy_ld, N, M)) return st;
-    if (zs_status st = check_ld(fn, "dx_ld", dx_ld, K, M)) return st;
-    if (M == 0) return ZS_OK;
-    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (grouped_is_few(dtype, 1, M, N, G)) return grouped_few(fn, dtype, 1, dy, dy_ld, w, K, row_ptr, perm, M, K, N, G, dx, dx_ld, s);
-    if (grouped_is_small(K, N)) return grouped_small_rows(fn, dtype, 1, dy, dy_ld, w, row_ptr, perm, M, K, N, G, dx, dx_ld, s);
-    return grouped_rows(fn, dtype, dy, M > 1 ? dy_ld : N, w, row_ptr, perm, M, K, N, G, dx, dx_ld, true, s);
+    if (!known_dtype(dtype) || M < kPadRows || M >= (int64_t(1) << 31) || K < 1 || N < 1 || G < 1 || grouped_is_small(K, N)) return 0;
+    const bool k = padded(dtype, K) != K, n = padded(dtype, N) != N;
+    const size_t w = k ? padded_bytes(dtype, (int64_t)G * N, K) : 0;
+    return w + imax(k ? padded_bytes(dtype, M, K) : 0, n ? padded_bytes(dtype, M, N) : 0);
+}
+
+zs_status zs_grouped_matmul_ws(int32_t dtype, const void* x, int64_t x_ld, const void* w, const int32_t* row_ptr,
+                               const int32_t* perm, int64_t M, int32_t K, int32_t N, int32_t G, void* y, int64_t y_ld,
+                               void* workspace, size_t workspace_bytes, zs_stream_t stream) {
+    return zs::product("zs_grouped_matmul_ws", 0, dtype, x, x_ld, w, row_ptr, perm, M, K, N, G, y, y_ld, workspace,
+                       workspace_bytes, stream);
+}
+
+zs_status zs_grouped_matmul_dx_ws(int32_t dtype, const void* dy, int64_t dy_ld, const void* w, const int32_t* row_ptr,
+                                  const int32_t* perm, int64_t M, int32_t K, int32_t N, int32_t G, void* dx, int64_t dx_ld,
+                                  void* workspace, size_t workspace_bytes, zs_stream_t stream) {
+    return zs::product("zs_grouped_matmul_dx_ws", 1, dtype, dy, dy_ld, w, row_ptr, perm, M, K, N, G, dx, dx_ld, workspace,
+                       workspace_bytes, stream);
 }
 
 size_t zs_grouped_matmul_dw_workspace_bytes(int32_t dtype, int64_t M, int32_t K, int32_t N, int32_t G) {
     if (!zs::known_dtype(dtype) || M < 0 || M >= (int64_t(1) << 31) || K < 1 || N < 1 || G < 1) return 0;
-    return zs::grouped_is_few(dtype, 2, M, N, G) ? 0 : zs::grouped_weights_workspace(dtype, M, K, N, G);
+    using namespace zs;
+    if (grouped_is_few(dtype, 2, M, N, G)) return 0;
+    size_t bytes = grouped_weights_workspace(dtype, M, K, N, G);
+    if (M >= kPadRows && !grouped_is_small(K, N)) {
+        if (padded(dtype, K) != K) bytes += padded_bytes(dtype, M, K);
+        if (padded(dtype, N) != N) bytes += padded_bytes(dtype, M, N);
+    }
+    return bytes;
 }
 
 zs_status zs_grouped_matmul_dw(int32_t dtype, const void* dy, int64_t dy_ld, const void* x, int64_t x_ld,
@@ -117,8 +185,17 @@ zs_status zs_grouped_matmul_dw(int32_t dtype, const void* dy, int64_t dy_ld, con
     if (G == 0) return ZS_OK;
     if (grouped_is_few(dtype, 2, M, N, G))
         return grouped_few(fn, dtype, 2, dy, dy_ld, x, x_ld, row_ptr, perm, M, K, N, G, dw, K, reinterpret_cast<cudaStream_t>(stream));
-    return grouped_weights(fn, dtype, dy, M > 1 ? dy_ld : N, x, M > 1 ? x_ld : K, row_ptr, perm, M, K, N, G, dw, workspace,
-                           reinterpret_cast<cudaStream_t>(stream));
+    if (M == 1) dy_ld = N, x_ld = K;
+    // the partial sums first, then what is laid out anew
+    const size_t partial = grouped_weights_workspace(dtype, M, K, N, G);
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    Padder pad{{}, 0, static_cast<char*>(workspace) + partial, workspace ? workspace_bytes - partial : 0, dtype};
+    if (M >= kPadRows && !grouped_is_small(K, N)) {
+        pad.lay_out(x, x_ld, M, K);
+        pad.lay_out(dy, dy_ld, M, N);
+        if (zs_status st = grouped_pad(fn, dtype, pad.list, s)) return st;
+    }
+    return grouped_weights(fn, dtype, dy, dy_ld, x, x_ld, row_ptr, perm, M, K, N, G, dw, workspace, s);
 }
 
 }  // extern "C"

@@ -297,7 +297,7 @@ zs_status launch_rows(const char* fn, RowsArgs a, cudaStream_t s) {
         constexpr bool bf16 = std::is_same<T, __nv_bfloat16>::value;
         const int w_rows = kMN ? a.red : a.cols;
         if (!encode_boxes(&a_map, bf16, a.a.p, a.red, a.M, a.a.ld, 0, kTileM) ||
-            !encode_boxes(&w_map, bf16, a.w.p, a.w.ld, w_rows, a.w.ld, a.G, kMN ? kStageK<T> : BN))
+            !encode_boxes(&w_map, bf16, a.w.p, a.w.cols, w_rows, a.w.ld, a.G, kMN ? kStageK<T> : BN))
             return fail(ZS_ERR_CUDA, "%s: a tensor map was refused", fn);
     }
     a.ntiles = (a.cols + BN - 1) / BN;
@@ -333,8 +333,8 @@ zs_status rows_product(const char* fn, RowsArgs a, bool mn, bool aligned, cudaSt
 unsigned int take_timeouts_grouped_rows() { return take_timeouts_local(); }
 cudaError_t set_timeout_flag_grouped_rows(unsigned int* flag) { return set_timeout_flag_local(flag); }
 
-// rows x_ld apart, K the length of a weight row; transposed: the gradient.
-zs_status grouped_rows(const char* fn, int32_t dtype, const void* x, int64_t x_ld, const void* w, const int32_t* row_ptr,
+// rows x_ld apart, rows of K weights w_ld apart; transposed: the gradient.
+zs_status grouped_rows(const char* fn, int32_t dtype, const void* x, int64_t x_ld, const void* w, int64_t w_ld, const int32_t* row_ptr,
                        const int32_t* perm, int64_t M, int32_t K, int32_t N, int32_t G, void* out, int64_t out_ld,
                        bool transposed, cudaStream_t s) {
     const int es = dtype_bytes(dtype), per16 = 16 / es;
@@ -343,8 +343,8 @@ zs_status grouped_rows(const char* fn, int32_t dtype, const void* x, int64_t x_l
     a.red = transposed ? N : K;
     a.cols = transposed ? K : N;
     a.a = {x, x_ld, a.red, at(x, 16) && x_ld % per16 == 0};
-    a.w = {w, K, K, at(w, 16) && K % per16 == 0};
-    a.w_group = (int64_t)K * N;
+    a.w = {w, w_ld, K, at(w, 16) && w_ld % per16 == 0};
+    a.w_group = w_ld * N;
     a.row_ptr = row_ptr;
     a.perm = perm;
     a.out = out;

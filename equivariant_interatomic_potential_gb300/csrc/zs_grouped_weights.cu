@@ -321,7 +321,7 @@ size_t grouped_weights_workspace(int32_t dtype, int64_t M, int32_t K, int32_t N,
         const WeightPlan p = weight_plan(dtype, tma, M, K, N, G);
         if (p.ctas > 1 && !(tma && dtype == ZS_F32)) bytes = imax(bytes, (size_t)p.ctas * 2 * kTileM * p.bn * 4);
     }
-    return bytes;
+    return align_up(bytes, 256);
 }
 
 zs_status grouped_weights(const char* fn, int32_t dtype, const void* dy, int64_t dy_ld, const void* x, int64_t x_ld,

@@ -419,10 +419,22 @@ __device__ __forceinline__ void emit32(const float (&f)[32], int left, TO* row, 
             }
         } else {
             constexpr int kAtOnce = 32 / kCols;   // rows of a warp's store
-            for (int r0 = 0; r0 < 32; r0 += kAtOnce) {
-                const int r = r0 + lane / kCols, c = lane % kCols;
-                TO* dst = reinterpret_cast<TO*>(__shfl_sync(0xffffffffu, mine, r));
-                if (dst && c < here) dst[part * kCols + c] = *reinterpret_cast<const TO*>(stage + r * kStageRow + c * sizeof(TO));
+            constexpr int kBatch = 8;             // stores on their way at once: one after the other is latency alone
+            const int c = lane % kCols;
+            const bool inside = c < here;
+#pragma unroll 1
+            for (int r0 = 0; r0 < 32; r0 += kAtOnce * kBatch) {
+                TO v[kBatch];
+                TO* dst[kBatch];
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) {
+                    const int r = r0 + kAtOnce * i + lane / kCols;
+                    dst[i] = reinterpret_cast<TO*>(__shfl_sync(0xffffffffu, mine, r));
+                    v[i] = *reinterpret_cast<const TO*>(stage + r * kStageRow + c * sizeof(TO));
+                }
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i)
+                    if (dst[i] && inside) dst[i][part * kCols + c] = v[i];
             }
         }
     }

@@ -16,8 +16,9 @@
 
 namespace {
 
-decltype(&zs_grouped_matmul) f_matmul;
-decltype(&zs_grouped_matmul_dx) f_dx;
+decltype(&zs_grouped_matmul_ws) f_matmul;
+decltype(&zs_grouped_matmul_dx_ws) f_dx;
+decltype(&zs_grouped_matmul_workspace_bytes) f_matmul_bytes;
 decltype(&zs_grouped_matmul_dw_workspace_bytes) f_dw_bytes;
 decltype(&zs_grouped_matmul_dw) f_dw;
 decltype(&zs_norm_gate_residual) f_norm;
@@ -81,12 +82,15 @@ PyObject* matmul(PyObject*, PyObject* const* args, Py_ssize_t n) {
         if (d < 0 || !is_matrix(x, type, M, t ? N : K) || !is_array(row_ptr, at::kInt, G + 1) ||
             (args[3] != Py_None && !is_array(perm, at::kInt, M)) || (K | N | G) >> 31)
             return not_here();
-        at::Tensor out = make({M, t ? K : N}, *x, type);
+        at::Tensor out = make({M, t ? K : N}, *x, type), ws;
+        const size_t bytes = f_matmul_bytes(d, M, (int32_t)K, (int32_t)N, (int32_t)G);
+        if (bytes) ws = make({(int64_t)bytes}, *x, at::kByte);
         const int32_t* pp = perm ? static_cast<const int32_t*>(perm->const_data_ptr()) : nullptr;
         const int st = (t ? f_dx : f_matmul)(d, x->const_data_ptr(), t ? N : K, w->const_data_ptr(),
                                              static_cast<const int32_t*>(row_ptr->const_data_ptr()), pp, M, (int32_t)K, (int32_t)N,
-                                             (int32_t)G, out.mutable_data_ptr(), t ? K : N, stream());
-        if (st) return failed(t ? "zs_grouped_matmul_dx" : "zs_grouped_matmul", st);
+                                             (int32_t)G, out.mutable_data_ptr(), t ? K : N, bytes ? ws.mutable_data_ptr() : nullptr, bytes,
+                                             stream());
+        if (st) return failed(t ? "zs_grouped_matmul_dx_ws" : "zs_grouped_matmul_ws", st);
         return THPVariable_Wrap(std::move(out));
     });
 }
@@ -200,8 +204,9 @@ PyObject* bind(PyObject*, PyObject* args) {
         if (!v) PyErr_Format(PyExc_KeyError, "%s", name);
         return v ? PyLong_AsVoidPtr(v) : nullptr;
     };
-    f_matmul = reinterpret_cast<decltype(f_matmul)>(get("zs_grouped_matmul"));
-    f_dx = reinterpret_cast<decltype(f_dx)>(get("zs_grouped_matmul_dx"));
+    f_matmul = reinterpret_cast<decltype(f_matmul)>(get("zs_grouped_matmul_ws"));
+    f_dx = reinterpret_cast<decltype(f_dx)>(get("zs_grouped_matmul_dx_ws"));
+    f_matmul_bytes = reinterpret_cast<decltype(f_matmul_bytes)>(get("zs_grouped_matmul_workspace_bytes"));
     f_dw_bytes = reinterpret_cast<decltype(f_dw_bytes)>(get("zs_grouped_matmul_dw_workspace_bytes"));
     f_dw = reinterpret_cast<decltype(f_dw)>(get("zs_grouped_matmul_dw"));
     f_norm = reinterpret_cast<decltype(f_norm)>(get("zs_norm_gate_residual"));

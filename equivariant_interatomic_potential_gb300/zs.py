@@ -89,6 +89,11 @@ def load(build_if_missing: bool = True):
         lib.zs_grouped_matmul.argtypes = [I32, P, I64, P, P, P, I64, I32, I32, I32, P, I64, P]
         lib.zs_grouped_matmul_dx.restype = ctypes.c_int
         lib.zs_grouped_matmul_dx.argtypes = [I32, P, I64, P, P, P, I64, I32, I32, I32, P, I64, P]
+        lib.zs_grouped_matmul_workspace_bytes.restype = SZ
+        lib.zs_grouped_matmul_workspace_bytes.argtypes = [I32, I64, I32, I32, I32]
+        for fn in (lib.zs_grouped_matmul_ws, lib.zs_grouped_matmul_dx_ws):
+            fn.restype = ctypes.c_int
+            fn.argtypes = [I32, P, I64, P, P, P, I64, I32, I32, I32, P, I64, P, SZ, P]
         lib.zs_grouped_matmul_dw_workspace_bytes.restype = SZ
         lib.zs_grouped_matmul_dw_workspace_bytes.argtypes = [I32, I64, I32, I32, I32]
         lib.zs_grouped_matmul_dw.restype = ctypes.c_int
@@ -564,9 +569,13 @@ def zs_grouped_matmul(x: torch.Tensor, w: torch.Tensor, row_ptr: torch.Tensor, p
         out = torch.empty((M, N), dtype=dt, device=x.device)
     else:
         out_ld = _matrix(out, "out", dt, M, N)
-    st = load().zs_grouped_matmul(d, x.data_ptr(), x_ld, wp, rp, pp, M, K, N, G, out.data_ptr(), out_ld, _stream(stream))
+    lib = load()
+    wbytes = lib.zs_grouped_matmul_workspace_bytes(d, M, K, N, G)
+    workspace = _workspace(wbytes, w.device)
+    st = lib.zs_grouped_matmul_ws(d, x.data_ptr(), x_ld, wp, rp, pp, M, K, N, G, out.data_ptr(), out_ld, _ptr(workspace), wbytes,
+                                _stream(stream))
     if st:
-        _check("zs_grouped_matmul", st)
+        _check("zs_grouped_matmul_ws", st)
     return out
 
 
@@ -586,10 +595,13 @@ def zs_grouped_matmul_dx(dy: torch.Tensor, w: torch.Tensor, row_ptr: torch.Tenso
         out = torch.empty((M, K), dtype=dt, device=dy.device)
     else:
         out_ld = _matrix(out, "out", dt, M, K)
-    st = load().zs_grouped_matmul_dx(d, dy.data_ptr(), dy_ld, wp, rp, pp, M, K, N, G, out.data_ptr(), out_ld,
-                                     _stream(stream))
+    lib = load()
+    wbytes = lib.zs_grouped_matmul_workspace_bytes(d, M, K, N, G)
+    workspace = _workspace(wbytes, w.device)
+    st = lib.zs_grouped_matmul_dx_ws(d, dy.data_ptr(), dy_ld, wp, rp, pp, M, K, N, G, out.data_ptr(), out_ld, _ptr(workspace), wbytes,
+                                   _stream(stream))
     if st:
-        _check("zs_grouped_matmul_dx", st)
+        _check("zs_grouped_matmul_dx_ws", st)
     return out
 
 

@@ -365,6 +365,28 @@ ZS_API zs_status zs_grouped_matmul_dx(int32_t dtype, const void* dy, int64_t dy_
                                       void* dx, int64_t dx_ld, zs_stream_t stream);
 
 /*
+ * The two above with a workspace, in which rows that do not start on 16-byte
+ * boundaries (odd K or N, views at odd offsets) are laid out anew before the
+ * products: twice to four times as fast for such operands from a few hundred
+ * rows on.  Same results.
+ *   workspace  zs_grouped_matmul_workspace_bytes(dtype, M, K, N, G) bytes (0
+ *              where rows of K and of N elements are whole 16-byte pieces),
+ *              256-byte aligned; its contents need not start at zero.  A
+ *              smaller one, or NULL, is not used.
+ */
+ZS_API size_t zs_grouped_matmul_workspace_bytes(int32_t dtype, int64_t M, int32_t K, int32_t N, int32_t G);
+ZS_API zs_status zs_grouped_matmul_ws(int32_t dtype, const void* x, int64_t x_ld, const void* w,
+                                      const int32_t* row_ptr, const int32_t* perm,
+                                      int64_t M, int32_t K, int32_t N, int32_t G,
+                                      void* y, int64_t y_ld, void* workspace, size_t workspace_bytes,
+                                      zs_stream_t stream);
+ZS_API zs_status zs_grouped_matmul_dx_ws(int32_t dtype, const void* dy, int64_t dy_ld, const void* w,
+                                         const int32_t* row_ptr, const int32_t* perm,
+                                         int64_t M, int32_t K, int32_t N, int32_t G,
+                                         void* dx, int64_t dx_ld, void* workspace, size_t workspace_bytes,
+                                         zs_stream_t stream);
+
+/*
  * Gradient of zs_grouped_matmul in w:  dw[g] = sum over rows i of group g of
  * dy[i,:]^T x[i,:].
  *   dw (G, N, K)  contiguous, of the operands' type, fully written (a group

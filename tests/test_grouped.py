@@ -332,3 +332,56 @@ def test_binding_refusals():
         zs.zs_grouped_matmul(x[0], w, rp)
     with pytest.raises(ValueError, match="shape"):
         zs.zs_grouped_matmul(x, w[0], rp)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("K,N", [(41, 25), (217, 136), (136, 217), (7, 130), (1, 300), (263, 3)])
+@pytest.mark.parametrize("shift", [0, 1, 5])
+def test_rows_laid_out_anew(K, N, shift, dtype):
+    # whether a workspace has room for both operands, for one, or there is none, the results are the same sums
+    M, G = 777, 4
+    group, (x, w, dy), d = draw(M, K, N, G, dtype, K + N, "zipf", bad=0.05)
+    row_ptr, perm = (torch.from_numpy(a).cuda() for a in csr(group, G))
+    code, lib = {"f32": 0, "bf16": 1, "f16": 2}[dtype], zs.load()
+
+    def exact_end(a):   # views that end where their allocation does, rows `shift` elements wider
+        base = torch.full((a.numel() + (a.shape[0] - 1) * shift if a.dim() == 2 else a.numel(),), float("nan"),
+                          dtype=a.dtype, device="cuda")
+        view = base.as_strided(a.shape, (a.shape[1] + shift, 1)) if a.dim() == 2 else base.view(a.shape)
+        view.copy_(a.cuda())
+        return view
+
+    xv, dyv, wv = exact_end(x), exact_end(dy), exact_end(w)
+    need = lib.zs_grouped_matmul_workspace_bytes(code, M, K, N, G)
+    assert need % 256 == 0 and need > 0
+    ry, ay, rdx, adx, _, _ = grouped(d[0], d[1], group, d[2])
+    for room in (need, max(need // 2 // 256 * 256, 256), 0):
+        ws = torch.full((max(room, 256) + 256,), 0xFF, dtype=torch.uint8, device="cuda")
+        y = torch.full((M, N), 9.0, dtype=x.dtype, device="cuda")
+        dx = torch.full((M, K), 9.0, dtype=x.dtype, device="cuda")
+        for fn, a, ld, out, cols in ((lib.zs_grouped_matmul_ws, xv, K + shift, y, N),
+                                     (lib.zs_grouped_matmul_dx_ws, dyv, N + shift, dx, K)):
+            assert fn(code, a.data_ptr(), ld, wv.data_ptr(), row_ptr.data_ptr(), perm.data_ptr(), M, K, N, G,
+                      out.data_ptr(), cols, ws.data_ptr() if room else None, room,
+                      torch.cuda.current_stream().cuda_stream) == 0
+        torch.cuda.synchronize()
+        zs.zs_check_timeouts()
+        assert bool((ws[room:] == 0xFF).all())
+        close(y, ry, ay, dtype, "y")
+        close(dx, rdx, adx, dtype, "dx")
+
+
+def test_workspace_sizes_and_refusals():
+    lib = zs.load()
+    size = lib.zs_grouped_matmul_workspace_bytes
+    assert size(1, 5000, 64, 128, 3) == 0          # rows of whole 16-byte pieces
+    assert size(1, 5000, 17, 31, 3) == 0           # both at most 32: on other cores
+    assert size(9, 5000, 65, 128, 3) == 0 and size(1, -1, 65, 128, 3) == 0 and size(1, 5000, 0, 128, 3) == 0
+    up = lambda b: -(-b // 256) * 256  # noqa: E731
+    assert size(1, 5000, 65, 128, 3) == up(3 * 128 * 72 * 2) + up(5000 * 72 * 2)
+    assert size(0, 5000, 64, 129, 3) == up(5000 * 132 * 4)
+    for fn in (lib.zs_grouped_matmul_ws, lib.zs_grouped_matmul_dx_ws):
+        call = lambda ws, M: fn(1, FAKE, 65, FAKE, FAKE, FAKE, M, 65, 65, 3, FAKE, 65, ws, 1 << 30, None)  # noqa: E731
+        assert call(FAKE + 8, 300) == INVALID and b"aligned" in lib.zs_last_error()
+        assert call(FAKE, 0) == 0 and call(FAKE, -1) == INVALID
