@@ -172,9 +172,13 @@ __global__ void __launch_bounds__(kThreads) small_weights(const WeightArgs a) {
     __shared__ __align__(16) float xs[kHeld][kStride], dys[kHeld][kStride];
     __shared__ __align__(16) float sums[kPer * 16 * 2];
     __shared__ int rows[2][kHeld];
+    __shared__ int32_t starts[kGroupsHeld + 2];
     pdl_wait();
     pdl_trigger();
-    const WeightGroups<float> gr{a.row_ptr, a.G, a.M, false};
+    WeightGroups<float> gr;
+    gr.hold(a.row_ptr, a.G, a.M, starts);
+    __syncthreads();
+    if (threadIdx.x >= kThreads - 32) note_join<float>(a, gr);
     Walk<float, kMost> walk(a, gr);
     const int tx = threadIdx.x % 8, ty = threadIdx.x / 8 % 8, share = threadIdx.x / kPer;
     Segment s;

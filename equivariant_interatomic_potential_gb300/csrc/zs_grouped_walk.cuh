@@ -6,7 +6,10 @@
 // tiles all keep every SM busy.  (Each group also counts kFlush units for
 // writing its tile.)  A range cuts at most the group it starts in and the
 // group it ends in: those two sums go to the workspace in fp32, and a second
-// kernel adds, for each group that was cut, its CTAs' parts in order.
+// kernel adds, for each group that was cut, its CTAs' parts in order.  Which
+// ones they are the first kernel notes down (note_join): to find it anew in
+// each block of the second was a chain of loads that took it 5 us
+// more (45000 rows, 256 x 256 bf16 weights).
 #pragma once
 
 #include "zs_mma.cuh"
@@ -18,12 +21,21 @@ constexpr int kPartRows = 4;     // rows of a tile that one CTA of the second ke
 template <typename T>
 using WeightGroups = Groups<kStageK<T>, kFlush>;   // a unit's positions are a stage's
 
+// A group that is cut where a CTA's range ends and that starts in this range.
+struct JoinTile {
+    int g;        // -1: none
+    int tile;     // of the weights
+    int last;     // the CTA that holds its end
+    int part;     // which of the first CTA's partial tiles
+};
+
 struct WeightArgs {
     Matrix dy, x;
     const int32_t* row_ptr;
     const int32_t* perm;
     void* dw;
     float* partial;      // [CTA][2][128][BN]
+    JoinTile* joins;     // [CTA]
     bool dw_wide;
     int M, G, N, K;
     int ktiles;
@@ -75,24 +87,34 @@ __device__ __forceinline__ int weight_row(const WeightArgs& a, int p) {
     return (uint32_t)r < (uint32_t)a.M ? r : -1;
 }
 
-// Block (x, y): the group and tile that CTA x + 1's range begins inside of, if
-// CTA x holds its first positions; rows y * kPartRows .. of the tile, 4
-// columns a thread.
+// Notes down what is cut at the end of this CTA's range.  By a whole warp, which waits for nothing.
+template <typename T>
+__device__ __forceinline__ void note_join(const WeightArgs& a, const WeightGroups<T>& gr) {
+    JoinTile j = {-1, 0, 0, 0};
+    const int cut = (blockIdx.x + 1) * a.per;
+    if (cut < a.units) {
+        const int t = cut / a.slots, slot = cut - t * a.slots;
+        if (slot < gr.slot(a.G)) {
+            const int g = gr.find(slot, a.G);
+            const int b = gr.start(g), e = gr.start(g + 1);
+            const int u0 = t * a.slots + gr.slot(g), u1 = u0 + (e - b + kStageK<T> - 1) / kStageK<T>;   // units with positions
+            // it is cut here, and no earlier range holds positions of it
+            if (u0 < cut && u1 > cut && u0 / a.per == (int)blockIdx.x)
+                j = {g, t, (u1 - 1) / a.per, u0 != (int)blockIdx.x * a.per};
+        }
+    }
+    if ((threadIdx.x & 31) == 0 && blockIdx.x + 1 < gridDim.x) a.joins[blockIdx.x] = j;
+}
+
+// Block (x, y): the group whose first part CTA x formed, if it was cut; rows
+// y * kPartRows .. of its tile, 4 columns a thread.
 template <typename T, int BN>
 __global__ void __launch_bounds__(256) weights_join(const WeightArgs a) {
     pdl_wait();
     pdl_trigger();
-    const WeightGroups<T> gr{a.row_ptr, a.G, a.M, false};
-    const int cut = (blockIdx.x + 1) * a.per;
-    if (cut >= a.units) return;
-    const int t = cut / a.slots, slot = cut - t * a.slots;
-    if (slot >= gr.slot(a.G)) return;
-    const int g = gr.find(slot, a.G);
-    const int b = gr.start(g), e = gr.start(g + 1);
-    const int u0 = t * a.slots + gr.slot(g), u1 = u0 + (e - b + kStageK<T> - 1) / kStageK<T>;   // units with positions
-    if (u0 >= cut || u1 <= cut) return;             // the group is not cut here
-    const int first = u0 / a.per, last = (u1 - 1) / a.per;
-    if (first != (int)blockIdx.x) return;           // an earlier block adds it
+    const int4 note = __ldg(reinterpret_cast<const int4*>(a.joins) + blockIdx.x);
+    const int g = note.x, t = note.y, first = blockIdx.x, last = note.z, first_part = note.w;
+    if (g < 0) return;
     const int n0 = t / a.ktiles * kTileM + blockIdx.y * kPartRows, k0 = t % a.ktiles * BN;
     const int cols = imin(BN, a.K - k0), rows = imin(kPartRows, a.N - n0);
     constexpr int64_t kTile = (int64_t)kTileM * BN;
@@ -110,7 +132,7 @@ __global__ void __launch_bounds__(256) weights_join(const WeightArgs a) {
         const float* at = a.partial + ((int64_t)blockIdx.y * kPartRows + r) * BN + c;
 #pragma unroll 8
         for (int p = p0; p < p1; ++p)
-            sum = f4_add(sum, ld_ro4(at + ((int64_t)p * 2 + (p == first && u0 != first * a.per ? 1 : 0)) * kTile));
+            sum = f4_add(sum, ld_ro4(at + ((int64_t)p * 2 + (p == first ? first_part : 0)) * kTile));
     }
     sums[threadIdx.x] = sum;
     __syncthreads();

@@ -203,6 +203,8 @@ weights_mma(const __grid_constant__ CUtensorMap dy_map, const __grid_constant__ 
             __syncwarp();
         }
         if (is_dead(dead)) set.drain_products();
+    } else if (warp == 3) {
+        note_join<T>(a, set.groups);
     } else if (warp >= 4 && warp < 4 + 4 * Sh::kHalves) {
         const int q = warp & 3, half = (warp - 4) >> 2, r = 32 * q + lane;
         constexpr int kMine = BN / Sh::kHalves;
@@ -319,7 +321,7 @@ size_t grouped_weights_workspace(int32_t dtype, int64_t M, int32_t K, int32_t N,
     size_t bytes = 0;
     for (bool tma : {false, true}) {   // which one depends on the operands' alignment
         const WeightPlan p = weight_plan(dtype, tma, M, K, N, G);
-        if (p.ctas > 1 && !(tma && dtype == ZS_F32)) bytes = imax(bytes, (size_t)p.ctas * 2 * kTileM * p.bn * 4);
+        if (p.ctas > 1 && !(tma && dtype == ZS_F32)) bytes = imax(bytes, (size_t)p.ctas * (2 * kTileM * p.bn * 4 + sizeof(JoinTile)));
     }
     return align_up(bytes, 256);
 }
@@ -339,6 +341,7 @@ zs_status grouped_weights(const char* fn, int32_t dtype, const void* dy, int64_t
     a.perm = perm;
     a.dw = dw;
     a.partial = static_cast<float*>(workspace);
+    a.joins = reinterpret_cast<JoinTile*>(a.partial + (int64_t)p.ctas * 2 * kTileM * p.bn);
     a.dw_wide = at(dw, 16) && K % per16 == 0;
     a.M = (int)M, a.G = G, a.N = N, a.K = K;
     a.ktiles = (K + p.bn - 1) / p.bn;

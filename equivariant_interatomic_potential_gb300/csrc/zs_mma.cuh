@@ -64,9 +64,6 @@ __device__ __forceinline__ bool bounded_wait(uint32_t bar, uint32_t parity, vola
     bool ok = false;
     for (uint32_t i = 0; i < kMaxSpins && !ok; ++i) {
         ok = mbar_try_wait(bar, parity);
-#ifdef SLEEPNS
-        if (!ok) __nanosleep(SLEEPNS);
-#endif
         if (!ok && (i & 63) == 63 && *dead) break;
         if (!ok && i == kMaxSpins - 1) {
             note_timeout();
