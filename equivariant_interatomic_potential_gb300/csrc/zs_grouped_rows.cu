@@ -28,12 +28,17 @@ struct RowsArgs {
     int items, ntiles;
 };
 
-template <typename T, bool kTma, bool kMN, int BN>
+// kPair: two CTAs form a tile of 256 rows together, each with its own 128 rows
+// and half of the weights.
+template <typename T, bool kTma, bool kMN, int BN, bool kPair>
 struct RowsShape {
+    static_assert(!kPair || (kTma && BN == 256), "pairs form 256 x 256");
+    static constexpr int kTile = kPair ? 2 * kTileM : kTileM;
+    static constexpr int kMine = kPair ? BN / 2 : BN;   // columns whose weights this CTA holds
     static constexpr int P = kPlanes<T>, kBox = kStageK<T>;
     static constexpr uint32_t kA = box_bytes<kBox>(kTileM);
-    static constexpr int kBoxes = kMN ? (BN + kBoxMN - 1) / kBoxMN : 1;                       // of the right operand
-    static constexpr uint32_t kBoxB = kMN ? box_bytes<kBoxMN>(kBox) : box_bytes<kBox>(BN);
+    static constexpr int kBoxes = kMN ? (kMine + kBoxMN - 1) / kBoxMN : 1;                       // of the right operand
+    static constexpr uint32_t kBoxB = kMN ? box_bytes<kBoxMN>(kBox) : box_bytes<kBox>(kMine);
     static constexpr uint32_t kB = kBoxes * kBoxB;
     static constexpr uint32_t kStage = P * (kA + kB);
     static constexpr int kHalves = BN >= 64 ? 2 : 1;   // warps that share 32 rows of a tile
@@ -41,14 +46,14 @@ struct RowsShape {
     // what the loader warps copy into before they turn it: 16 bytes a part, two stages for each of the two groups (or
     // one of unaligned rows, 32 bytes a part)
     using PartsA = BoxParts<T, kTileM, kBox>;
-    using PartsB = BoxParts<T, kMN ? kBox : BN, kMN ? kBoxMN : kBox>;
+    using PartsB = BoxParts<T, kMN ? kBox : kMine, kMN ? kBoxMN : kBox>;
     static constexpr int kParts = PartsA::kSteps + kBoxes * PartsB::kSteps;
     static constexpr int kSlots = kTma ? 0 : 4 * kParts * 32 * kLoaderWarps * 16;
     static constexpr int kFixed = kSlots + kEpilogueWarps * kStageWarp + 1024 + 4608;   // staging, alignment, barriers and groups
     static constexpr int kFit = (kSmemMost - kFixed) / (int)kStage;
     static constexpr int S = kFit > 8 ? 8 : kFit;
     static_assert(kPlanes<T> == 1 || !kMN || BN == kBoxMN, "the planes of an MN-major operand follow each other");
-    static_assert(S >= 2 && Setup<S, kTmemCols, kTileM, 1>::kBytes <= 4608, "two stages at least");
+    static_assert(S >= 2 && Setup<S, kTmemCols, kTile, 1, kPair>::kBytes <= 4608, "two stages at least");
     static constexpr int kSmem = S * (int)kStage + kFixed;
     static constexpr int kThreads = 32 * (4 + kEpilogueWarps + (kTma ? 1 : 2) * kLoaderWarps);
 };
@@ -56,28 +61,31 @@ struct RowsShape {
 struct Item {
     int g, p0, p1, n0;
 };
-using RowGroups = Groups<kTileM, 1>;
+template <int kTile>
+using RowGroups = Groups<kTile, 1>;
 
-// The next tile of output with rows in it, from `item` on in steps of the grid.
-__device__ __forceinline__ bool next_item(const RowsArgs& a, const RowGroups& gr, int& item, int BN, Item& t) {
-    for (; item < a.items; item += gridDim.x) {
+// The next tile of output with rows in it, from `item` on in steps of `step`.
+template <int kTile>
+__device__ __forceinline__ bool next_item(const RowsArgs& a, const RowGroups<kTile>& gr, int& item, int step, int BN, Item& t) {
+    for (; item < a.items; item += step) {
         const int slot = item / a.ntiles;
         t.n0 = item % a.ntiles * BN;
         t.g = gr.find(slot, a.G + 1);
         const int b = gr.start(t.g), e = gr.start(t.g + 1);
-        const int64_t p0 = b + (int64_t)(slot - (b / kTileM + t.g)) * kTileM;
+        const int64_t p0 = b + (int64_t)(slot - (b / kTile + t.g)) * kTile;
         if (p0 < e) {
             t.p0 = (int)p0;
-            t.p1 = (int)imin<int64_t>(p0 + kTileM, e);
-            item += gridDim.x;
+            t.p1 = (int)imin<int64_t>(p0 + kTile, e);
+            item += step;
             return true;
         }
     }
     return false;
 }
 // The same without the rows of no group, which take no product.
-__device__ __forceinline__ bool next_product(const RowsArgs& a, const RowGroups& gr, int& item, int BN, Item& t) {
-    while (next_item(a, gr, item, BN, t))
+template <int kTile>
+__device__ __forceinline__ bool next_product(const RowsArgs& a, const RowGroups<kTile>& gr, int& item, int step, int BN, Item& t) {
+    while (next_item(a, gr, item, step, BN, t))
         if (t.g < a.G) return true;
     return false;
 }
@@ -88,41 +96,43 @@ __device__ __forceinline__ int row_at(const RowsArgs& a, int p) {
     return (uint32_t)r < (uint32_t)a.M ? r : -1;
 }
 
-template <typename T, bool kTma, bool kMN, int BN>
-__global__ void __launch_bounds__(RowsShape<T, kTma, kMN, BN>::kThreads, 1)
+template <typename T, bool kTma, bool kMN, int BN, bool kPair>
+__global__ void __launch_bounds__(RowsShape<T, kTma, kMN, BN, kPair>::kThreads, 1)
 rows_mma(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUtensorMap w_map, const RowsArgs a) {
-    using Sh = RowsShape<T, kTma, kMN, BN>;
+    using Sh = RowsShape<T, kTma, kMN, BN, kPair>;
     constexpr int S = Sh::S;
     extern __shared__ unsigned char raw[];
     unsigned char* ring = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
     unsigned char* slots = ring + S * Sh::kStage;
     unsigned char* staging = slots + Sh::kSlots;
-    Setup<S, Sh::kTmemCols, kTileM, 1> set;
+    Setup<S, Sh::kTmemCols, Sh::kTile, 1, kPair> set;
     set.begin(staging + kEpilogueWarps * kStageWarp, !kTma ? kLoaderWarps : a.perm ? 1 + kLoaderWarps : 1, 4 * Sh::kHalves, a.row_ptr, a.G, a.M);
-    const RowGroups& gr = set.groups;
+    const RowGroups<Sh::kTile>& gr = set.groups;
     volatile int* dead = set.dead;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     constexpr int kBox = Sh::kBox;
     const int nk = (a.red + kBox - 1) / kBox;
     constexpr int kPerChunk = kSums<T> > 1 ? kChunk / kBox : 1 << 30;   // stages between hand-overs to the epilogue
-    int item = blockIdx.x;
+    const int rank = kPair ? (int)cluster_rank() : 0, step = kPair ? gridDim.x / 2 : gridDim.x;
+    int item = kPair ? blockIdx.x / 2 : blockIdx.x;
     Item t;
 
     if (kTma && warp == 0) {
         RingPos<S> pos;
         int issued = 0;
-        while (!is_dead(dead) && next_product(a, gr, item, BN, t)) {
-            const int boxes = kMN ? (imin(BN, a.cols - t.n0) + kBoxMN - 1) / kBoxMN : 1;
+        while (!is_dead(dead) && next_product(a, gr, item, step, BN, t)) {
+            const int n0 = t.n0 + rank * Sh::kMine;
+            const int boxes = kMN ? imax(0, imin(Sh::kMine, a.cols - n0) + kBoxMN - 1) / kBoxMN : 1;
             const uint32_t bytes = (a.perm ? 0 : Sh::kA) + boxes * Sh::kBoxB;
             if (lane == 0) {
                 for (int k = 0; k < nk; ++k, ++issued, pos.next()) {
                     if (!bounded_wait_one(set.empty + 8 * pos.stage, pos.phase ^ 1, dead)) break;
                     const uint32_t bar = set.full + 8 * pos.stage, at = smem_u32(ring) + pos.stage * Sh::kStage, bt = at + Sh::kA;
                     mbar_arrive_expect_tx(bar, bytes);
-                    if (!a.perm) tma_2d(at, &a_map, k * kBox, t.p0, bar);
+                    if (!a.perm) tma_2d(at, &a_map, k * kBox, t.p0 + kTileM * rank, bar);
                     for (int i = 0; i < boxes; ++i) {
-                        if (kMN) tma_3d(bt + i * Sh::kBoxB, &w_map, t.n0 + i * kBoxMN, k * kBox, t.g, bar);
-                        else tma_3d(bt, &w_map, k * kBox, t.n0, t.g, bar);
+                        if (kMN) tma_3d(bt + i * Sh::kBoxB, &w_map, n0 + i * kBoxMN, k * kBox, t.g, bar);
+                        else tma_3d(bt, &w_map, k * kBox, n0, t.g, bar);
                     }
                 }
             }
@@ -130,21 +140,25 @@ rows_mma(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUte
         }
         issued = __shfl_sync(0xffffffffu, issued, 0);
         if (is_dead(dead)) set.drain_copies(issued);
+        if (kPair && lane == 0)   // the last arrivals from the first CTA's products
+            for (int i = 0; i < S; ++i, pos.next())
+                if (!bounded_wait_one<true>(set.empty + 8 * pos.stage, pos.phase ^ 1, dead)) break;
+        __syncwarp();
     } else if (warp >= 4 + kEpilogueWarps) {
         const int w = (warp - 4 - kEpilogueWarps) % kLoaderWarps;
         constexpr int kPerA = kTileM / kLoaderWarps;
         RingPos<S> pos;
         Item u;
         auto row_of = [&](const Item& x) {   // lane i (and 16 + i): the row of tile row kPerA w + i
-            const int p = x.p0 + kPerA * w + (lane & 15);
+            const int p = x.p0 + kTileM * rank + kPerA * w + (lane & 15);
             return p < x.p1 ? row_at(a, p) : -1;
         };
-        bool have = (!kTma || a.perm) && next_product(a, gr, item, BN, t);
+        bool have = (!kTma || a.perm) && next_product(a, gr, item, step, BN, t);
         int row = have ? row_of(t) : -1;
         if constexpr (kTma) {
             Copies<S> copies;
             while (have && !is_dead(dead)) {
-                const bool more = next_product(a, gr, item, BN, u);
+                const bool more = next_product(a, gr, item, step, BN, u);
                 const int row_next = more ? row_of(u) : -1;
                 for (int k = 0; k < nk; ++k) {
                     if (!copies.acquire(set.full, set.empty, dead)) break;
@@ -183,7 +197,7 @@ rows_mma(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUte
             };
             int n = 0, copied = 0;
             while (have && !is_dead(dead)) {
-                const bool more = next_product(a, gr, item, BN, u);
+                const bool more = next_product(a, gr, item, step, BN, u);
                 const int row_next = more ? row_of(u) : -1;
                 Matrix wm = a.w;
                 wm.p = static_cast<const T*>(wm.p) + t.g * a.w_group;
@@ -217,28 +231,37 @@ rows_mma(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUte
             copies_wait<0>();
             if (aligned && copied > 0 && !is_dead(dead)) turn_stage(mine + ((copied - 1) & 1) * Sh::kParts * kStride);
         }
-    } else if (warp == 1) {
+    } else if (warp == 1 && rank == 1) {
+        // tells the first CTA, which issues the products of both, of each full stage
         RingPos<S> pos;
-        int n = 0;
-        while (!is_dead(dead) && next_product(a, gr, item, BN, t)) {
+        while (!is_dead(dead) && next_product(a, gr, item, step, BN, t)) {
             if (lane == 0) {
                 for (int k = 0; k < nk; ++k, pos.next()) {
-                    const int buf = n & 1;
-                    if (k % kPerChunk == 0 && !bounded_wait_one(set.tempty + 8 * buf, ((n >> 1) & 1) ^ 1, dead)) break;
                     if (!bounded_wait_one(set.full + 8 * pos.stage, pos.phase, dead)) break;
-                    tc_fence_after();
-                    const uint32_t at = smem_u32(ring) + pos.stage * Sh::kStage;
-                    const int steps = (imin(kBox, a.red - k * kBox) + 15) / 16;
-                    issue_stage<T, false, kMN, BN>(set.tmem + buf * kSums<T> * BN, at, Sh::kA, 0, at + Sh::P * Sh::kA, Sh::kBoxB,
-                                                   steps, k % kPerChunk > 0);
-                    tc_commit(set.empty + 8 * pos.stage);
-                    if (k % kPerChunk == kPerChunk - 1 || k == nk - 1) {
-                        tc_commit(set.tfull + 8 * buf);
-                        ++n;
-                    }
+                    mbar_arrive_at(set.full + 8 * pos.stage, 0);
                 }
             }
             __syncwarp();
+        }
+    } else if (warp == 1) {
+        RingPos<S> pos;
+        int n = 0;
+        while (!is_dead(dead) && next_product(a, gr, item, step, BN, t)) {
+            for (int k = 0; k < nk; ++k, pos.next()) {
+                const int buf = n & 1;
+                if (k % kPerChunk == 0) bounded_wait_on<kPair>(set.tempty + 8 * buf, ((n >> 1) & 1) ^ 1, dead);
+                bounded_wait_on<kPair>(set.full + 8 * pos.stage, pos.phase, dead);
+                tc_fence_after();
+                const uint32_t at = smem_u32(ring) + pos.stage * Sh::kStage;
+                const int steps = (imin(kBox, a.red - k * kBox) + 15) / 16;
+                issue_stage<T, false, kMN, BN, kPair>(set.tmem + buf * kSums<T> * BN, at, Sh::kA, 0, at + Sh::P * Sh::kA, Sh::kBoxB,
+                                                      steps, k % kPerChunk > 0);
+                tc_commit<kPair>(set.empty + 8 * pos.stage);
+                if (k % kPerChunk == kPerChunk - 1 || k == nk - 1) {
+                    tc_commit<kPair>(set.tfull + 8 * buf);
+                    ++n;
+                }
+            }
         }
         if (is_dead(dead)) set.drain_products();
     } else if (warp >= 4 && warp < 4 + 4 * Sh::kHalves) {
@@ -246,8 +269,8 @@ rows_mma(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUte
         constexpr int kCols = BN / Sh::kHalves;
         unsigned char* stage = staging + (warp - 4) * kStageWarp;
         int n = 0;
-        while (!is_dead(dead) && next_item(a, gr, item, BN, t)) {
-            const int p = t.p0 + 32 * q + lane;
+        while (!is_dead(dead) && next_item(a, gr, item, step, BN, t)) {
+            const int p = t.p0 + kTileM * rank + 32 * q + lane;
             const int r = p < t.p1 ? row_at(a, p) : -1;
             T* row = r >= 0 ? static_cast<T*>(a.out) + r * a.out_ld + t.n0 : nullptr;
             const int c0 = half * kCols, c1 = imin(c0 + kCols, a.cols - t.n0);
@@ -263,7 +286,10 @@ rows_mma(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUte
                 store_tile<T>(lanes + buf * BN, c0, c1, row, a.out_wide, stage, lane);
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(set.tempty + 8 * buf);
+                if (lane == 0) {
+                    if (rank) mbar_arrive_at(set.tempty + 8 * buf, 0);
+                    else mbar_arrive(set.tempty + 8 * buf);
+                }
                 ++n;
             } else {
                 static_assert(kSums<T> == 1 || kCols == 32, "a warp's columns of an fp32 tile fit one register array");
@@ -289,33 +315,39 @@ rows_mma(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUte
     set.end();
 }
 
-template <typename T, bool kTma, bool kMN, int BN>
+template <typename T, bool kTma, bool kMN, int BN, bool kPair = false>
 zs_status launch_rows(const char* fn, RowsArgs a, cudaStream_t s) {
-    using Sh = RowsShape<T, kTma, kMN, BN>;
+    using Sh = RowsShape<T, kTma, kMN, BN, kPair>;
     CUtensorMap a_map = {}, w_map = {};
     if (kTma) {
         constexpr bool bf16 = std::is_same<T, __nv_bfloat16>::value;
         const int w_rows = kMN ? a.red : a.cols;
         if (!encode_boxes(&a_map, bf16, a.a.p, a.red, a.M, a.a.ld, 0, kTileM) ||
-            !encode_boxes(&w_map, bf16, a.w.p, a.w.cols, w_rows, a.w.ld, a.G, kMN ? kStageK<T> : BN))
+            !encode_boxes(&w_map, bf16, a.w.p, a.w.cols, w_rows, a.w.ld, a.G, kMN ? kStageK<T> : Sh::kMine))
             return fail(ZS_ERR_CUDA, "%s: a tensor map was refused", fn);
     }
     a.ntiles = (a.cols + BN - 1) / BN;
-    const int64_t items = ((int64_t)a.M / kTileM + a.G + 2) * a.ntiles;
+    const int64_t items = ((int64_t)a.M / Sh::kTile + a.G + 2) * a.ntiles;
     if (items >= (int64_t(1) << 31) - 65536) return fail(ZS_ERR_INVALID_ARG, "%s: %lld tiles", fn, (long long)items);
     a.items = (int)items;
+    constexpr auto kernel = rows_mma<T, kTma, kMN, BN, kPair>;
+    constexpr int kCtas = kPair ? 2 : 1;
     static std::atomic<uint64_t> done[kMaxDevices];
-    set_smem_limit_once(rows_mma<T, kTma, kMN, BN>, Sh::kSmem, done);
-    launch(rows_mma<T, kTma, kMN, BN>, dim3(imin(a.items, num_sms())), dim3(Sh::kThreads), Sh::kSmem, s, a_map, w_map, a);
+    set_smem_limit_once(kernel, Sh::kSmem, done);
+    launch_clusters(kCtas, kernel, dim3(kCtas * imin(a.items, num_sms() / kCtas)), dim3(Sh::kThreads), Sh::kSmem, s, a_map, w_map, a);
     return check_launch(fn);
 }
+
+// Rows of an average group from which on two CTAs share the weights of a tile.
+constexpr int kPairRows = 512;
 
 template <typename T, bool kTma, bool kMN>
 zs_status launch_rows(const char* fn, const RowsArgs& a, cudaStream_t s) {
     if constexpr (!kMN || sizeof(T) == 2)   // an MN-major plane of fp32 is a box wide
         if (a.cols <= 32) return launch_rows<T, kTma, kMN, 32>(fn, a, s);
     if constexpr (kTma)
-        if (a.cols > 64 && (a.cols + 127) / 128 % 2 == 0) return launch_rows<T, kTma, kMN, 256>(fn, a, s);
+        if (a.cols > 64 && (a.cols + 127) / 128 % 2 == 0)
+            return a.M >= kPairRows * (int64_t)a.G ? launch_rows<T, kTma, kMN, 256, true>(fn, a, s) : launch_rows<T, kTma, kMN, 256>(fn, a, s);
     if constexpr (sizeof(T) == 2)
         if (a.cols > 64) return launch_rows<T, kTma, kMN, 128>(fn, a, s);
     return launch_rows<T, kTma, kMN, 64>(fn, a, s);

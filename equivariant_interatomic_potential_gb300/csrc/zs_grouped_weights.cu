@@ -158,49 +158,39 @@ weights_mma(const __grid_constant__ CUtensorMap dy_map, const __grid_constant__ 
     } else if (warp == 1) {
         RingPos<S> pos;
         int n = 0;
-        // a stage's products, by lane 0
+        // a stage's products
         auto products = [&](int p) {
             const int buf = n & 1, since = (p - s.p0) % kPerChunk, steps = (imin(kUnit, s.p1 - p) + 15) / 16;
             const uint32_t at = smem_u32(ring) + pos.stage * Sh::kStage;
             tc_fence_after();
             issue_stage<T, true, true, BN>(set.tmem + buf * kSums<T> * BN, at, Sh::kA, Sh::kBox, at + Sh::P * Sh::kA, Sh::kBox,
                                            steps, since > 0);
-            tc_commit(set.empty + 8 * pos.stage);
+            tc_commit<false>(set.empty + 8 * pos.stage);
             if (since + kUnit >= kPerChunk || p + kUnit >= s.p1) {
-                tc_commit(set.tfull + 8 * buf);
+                tc_commit<false>(set.tfull + 8 * buf);
                 ++n;
             }
         };
         auto ready = [&](int p) {
             const int buf = n & 1;
-            return ((p - s.p0) % kPerChunk != 0 || bounded_wait_one(set.tempty + 8 * buf, ((n >> 1) & 1) ^ 1, dead)) &&
-                   bounded_wait_one(set.full + 8 * pos.stage, pos.phase, dead);
+            if ((p - s.p0) % kPerChunk == 0) bounded_wait_on(set.tempty + 8 * buf, ((n >> 1) & 1) ^ 1, dead);
+            bounded_wait_on(set.full + 8 * pos.stage, pos.phase, dead);
         };
         while (!is_dead(dead) && walk.next(s)) {
             // positions past the segment's end hold other rows where TMA brought them: they count as zeros
             const bool ragged = kTma && !a.perm && (s.p1 - s.p0) % 16 != 0;
-            int p = s.p0;
-            if (lane == 0)
-                for (; p < s.p1 && !(ragged && p + kUnit > s.p1) && ready(p); p += kUnit, pos.next()) products(p);
-            if (ragged) {
-                bool ok = true;
-                if (lane == 0) ok = p + kUnit > s.p1 && ready(p);
-                ok = __shfl_sync(0xffffffffu, ok, 0);
-                const int stage_now = __shfl_sync(0xffffffffu, pos.stage, 0);
-                if (ok) {
-                    const int rows = (s.p1 - s.p0) % kUnit, pieces = (((rows + 15) & ~15) - rows) * (kBoxMN / 8);
-                    unsigned char* at = ring + stage_now * Sh::kStage + rows * (kBoxMN * 2);
+            for (int p = s.p0; p < s.p1; p += kUnit, pos.next()) {
+                ready(p);
+                if (ragged && p + kUnit > s.p1) {
+                    const int rows = s.p1 - p, pieces = (((rows + 15) & ~15) - rows) * (kBoxMN / 8);
+                    unsigned char* at = ring + pos.stage * Sh::kStage + rows * (kBoxMN * 2);
                     for (int i = lane; i < pieces * (Sh::kABoxes + Sh::kBBoxes); i += 32)
                         *reinterpret_cast<uint4*>(at + i / pieces * Sh::kBox + i % pieces * 16) = make_uint4(0, 0, 0, 0);
                     fence_async_smem();
                     __syncwarp();
-                    if (lane == 0) {
-                        products(p);
-                        pos.next();
-                    }
                 }
+                products(p);
             }
-            __syncwarp();
         }
         if (is_dead(dead)) set.drain_products();
     } else if (warp == 3) {

@@ -58,6 +58,15 @@ __host__ __device__ constexpr uint32_t tmem_cols(int n) { return n <= 32 ? 32 : 
 
 // ---------------------------------------------------------------- barriers
 
+__device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+    return ok != 0;
+}
+
 // Whole warps.  dead: set by the first wait of the CTA that runs out; the
 // others give up soon after.  Every lane gets the same answer.
 __device__ __forceinline__ bool bounded_wait(uint32_t bar, uint32_t parity, volatile int* dead) {
@@ -74,14 +83,30 @@ __device__ __forceinline__ bool bounded_wait(uint32_t bar, uint32_t parity, vola
 }
 // One thread's wait, for the roles that issue: a vote at each stage would cost
 // them a tenth of the tensor cores' time.
+// kCluster: the other CTA of a pair arrives at this barrier too.
+template <bool kCluster = false>
 __device__ __forceinline__ bool bounded_wait_one(uint32_t bar, uint32_t parity, volatile int* dead) {
     for (uint32_t i = 0; i < kMaxSpins; ++i) {
-        if (mbar_try_wait(bar, parity)) return true;
+        if (kCluster ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)) return true;
         if ((i & 63) == 63 && *dead) return false;
     }
     note_timeout();
     *dead = 1;
     return false;
+}
+// A whole warp's wait without a vote: where it runs out the warp carries on
+// (outputs are then undefined), and finds the CTA dead later.
+template <bool kCluster = false>
+__device__ __forceinline__ void bounded_wait_on(uint32_t bar, uint32_t parity, volatile int* dead) {
+    for (uint32_t i = 0; i < kMaxSpins; ++i) {
+        if (kCluster ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)) break;
+        if ((i & 63) == 63 && *dead) break;
+        if (i == kMaxSpins - 1) {
+            note_timeout();
+            *dead = 1;
+        }
+    }
+    __syncwarp();
 }
 __device__ __forceinline__ bool is_dead(volatile int* dead) { return __any_sync(0xffffffffu, *dead != 0); }
 
@@ -97,6 +122,21 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" :: "r"(bar) : "memory");
 }
+// At the same barrier of CTA `rank` of the cluster.
+__device__ __forceinline__ void mbar_arrive_at(uint32_t bar, uint32_t rank) {
+    uint32_t there;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(bar), "r"(rank));
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" :: "r"(there) : "memory");
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void pair_barrier() {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 // A position in a ring of S stages.
@@ -111,22 +151,50 @@ struct RingPos {
 
 // ---------------------------------------------------------------- tcgen05
 
+// kPair: both CTAs of a cluster of two take part (a warp of each allocates and
+// frees; the first one's products are of both).
+template <bool kPair>
 __device__ __forceinline__ void tmem_alloc(uint32_t dst_smem, uint32_t cols) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" :: "r"(dst_smem), "r"(cols) : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    if constexpr (kPair) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" :: "r"(dst_smem), "r"(cols) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    } else {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" :: "r"(dst_smem), "r"(cols) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
 }
+template <bool kPair>
 __device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t cols) {
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(addr), "r"(cols) : "memory");
+    if constexpr (kPair) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" :: "r"(addr), "r"(cols) : "memory");
+    else asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(addr), "r"(cols) : "memory");
 }
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+// Products and their commits are issued by one lane that the warp elects, always
+// the same, with the warp in step: from inside a branch on the lane number each
+// instruction took 143 cycles to issue, more than a 128 x 256 product's 128.
+//
+// An arrival at the barrier (of a pair: at both CTAs') once the products issued so far are done.
+template <bool kPair>
 __device__ __forceinline__ void tc_commit(uint32_t bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" :: "r"(bar) : "memory");
+    if constexpr (kPair)
+        asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+                     "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}"
+                     :: "r"(bar), "h"((unsigned short)3) : "memory");
+    else
+        asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+                     "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" :: "r"(bar) : "memory");
 }
+template <bool kPair>
 __device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
-                 :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate) : "memory");
+    if constexpr (kPair)
+        asm volatile("{\n\t.reg .pred p, e;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                     "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+                     :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate) : "memory");
+    else
+        asm volatile("{\n\t.reg .pred p, e;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                     "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+                     :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate) : "memory");
 }
 // 32 columns of this warp's 32 TMEM lanes: lane l gets row l.
 __device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t (&r)[32]) {
@@ -167,32 +235,38 @@ __device__ __forceinline__ uint64_t box_desc(uint32_t addr, uint32_t lbo) {
 template <int kCols, bool kMN>
 constexpr uint32_t kDescStep = (kMN ? 16 * kCols * 2 : 32) >> 4;
 
-// Instruction descriptor: 16-bit operands, fp32 sums, 128 x n tile.
+// Instruction descriptor: 16-bit operands, fp32 sums, m x n tile.
 template <typename T>
-__device__ __forceinline__ uint32_t instr_desc(bool a_mn, bool b_mn, int n) {
+__device__ __forceinline__ uint32_t instr_desc(bool a_mn, bool b_mn, int n, int m = kTileM) {
     constexpr uint32_t type = sizeof(T) == 4 || std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;   // bf16 (planes too) or f16
     return (1u << 4) | (type << 7) | (type << 10) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16) |
-           ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kTileM >> 4) << 24);
+           ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
 
 // The products of one stage: `steps` times 16 summed-over elements, into a tile
 // of BN columns (fp32: three of them).  Planes of the left operand are a_plane
-// bytes apart, those of the right one follow each other.
-template <typename T, bool kAMN, bool kBMN, int BN>
+// bytes apart, those of the right one follow each other.  Of a pair, each CTA
+// holds 128 rows of the left operand and half the columns of the right one, at
+// the same addresses, and gets its rows' sums.
+template <typename T, bool kAMN, bool kBMN, int BN, bool kPair = false>
 __device__ __forceinline__ void issue_stage(uint32_t d, uint32_t a, uint32_t a_plane, uint32_t a_lbo, uint32_t b, uint32_t b_lbo,
                                             int steps, bool accumulate) {
     constexpr int kACols = kAMN ? kBoxMN : kStageK<T>, kBCols = kBMN ? kBoxMN : kStageK<T>;
     const uint64_t a0 = box_desc<kACols>(a, a_lbo), b0 = box_desc<kBCols>(b, b_lbo);
-    for (int k = 0; k < steps; ++k) {
+    constexpr int kMost = kStageK<T> / 16;
+#pragma unroll
+    for (int k = 0; k < kMost; ++k) {
+        if (k >= steps) break;
         const uint64_t ak = a0 + k * kDescStep<kACols, kAMN>, bk = b0 + k * kDescStep<kBCols, kBMN>;
         const bool more = accumulate || k > 0;
         if constexpr (kPlanes<T> == 1) {
-            tc_mma(d, ak, bk, instr_desc<T>(kAMN, kBMN, BN), more);
+            tc_mma<kPair>(d, ak, bk, instr_desc<T>(kAMN, kBMN, BN, kPair ? 2 * kTileM : kTileM), more);
         } else {
             const uint32_t ap = a_plane >> 4;
-            tc_mma(d, ak, bk, instr_desc<T>(kAMN, kBMN, 3 * BN), more);
-            tc_mma(d + BN, ak + ap, bk, instr_desc<T>(kAMN, kBMN, 2 * BN), true);
-            tc_mma(d + 2 * BN, ak + 2 * ap, bk, instr_desc<T>(kAMN, kBMN, BN), true);
+            static_assert(!kPair, "fp32 tiles are a CTA's own");
+            tc_mma<false>(d, ak, bk, instr_desc<T>(kAMN, kBMN, 3 * BN), more);
+            tc_mma<false>(d + BN, ak + ap, bk, instr_desc<T>(kAMN, kBMN, 2 * BN), true);
+            tc_mma<false>(d + 2 * BN, ak + 2 * ap, bk, instr_desc<T>(kAMN, kBMN, BN), true);
         }
     }
 }
@@ -517,8 +591,10 @@ struct Copies {
     }
 };
 
-// What every grouped kernel sets up: barriers, TMEM, the groups' starts.
-template <int S, uint32_t kTmemCols, int kTile, int kExtra>
+// What every grouped kernel sets up: barriers, TMEM, the groups' starts.  Of a
+// pair, the first CTA's full barriers count one arrival more (the other CTA's
+// stage is full) and its tempty barriers both CTAs' epilogue warps.
+template <int S, uint32_t kTmemCols, int kTile, int kExtra, bool kPair = false>
 struct Setup {
     static constexpr int kBytes = (2 * S + 7) * 8 + (kGroupsHeld + 2) * 4;
     uint32_t full, empty, tfull, tempty, done, tmem;
@@ -531,6 +607,7 @@ struct Setup {
         uint32_t* slot = reinterpret_cast<uint32_t*>(bars + 2 * S + 6);
         full = smem_u32(bars), empty = full + 8 * S, tfull = empty + 8 * S, tempty = tfull + 16, done = tempty + 16;
         if (threadIdx.x == 0) {
+            if (kPair && cluster_rank() == 0) ++full_count, epilogue_warps *= 2;
             for (int i = 0; i < S; ++i) {
                 mbar_init(full + 8 * i, full_count);
                 mbar_init(empty + 8 * i, 1);
@@ -546,17 +623,19 @@ struct Setup {
         pdl_wait();
         pdl_trigger();
         groups.hold(row_ptr, G, M, reinterpret_cast<int32_t*>(bars + 2 * S + 7));
-        if ((threadIdx.x >> 5) == 2) tmem_alloc(smem_u32(slot), kTmemCols);
+        if ((threadIdx.x >> 5) == 2) tmem_alloc<kPair>(smem_u32(slot), kTmemCols);
         tc_fence_before();
         __syncthreads();
+        if (kPair) pair_barrier();   // the other CTA's barriers are there
         tc_fence_after();
         tmem = *slot;
     }
     __device__ __forceinline__ void end() {
         tc_fence_before();
         __syncthreads();
+        if (kPair) pair_barrier();   // nothing reads, or arrives at, a CTA that has left
         tc_fence_after();
-        if ((threadIdx.x >> 5) == 2) tmem_free(tmem, kTmemCols);
+        if ((threadIdx.x >> 5) == 2) tmem_free<kPair>(tmem, kTmemCols);
     }
     // Where the CTA is dead: what was issued last on each stage has landed.
     __device__ __forceinline__ void drain_copies(int issued) const {
@@ -566,7 +645,7 @@ struct Setup {
         }
     }
     __device__ __forceinline__ void drain_products() const {
-        if ((threadIdx.x & 31) == 0) tc_commit(done);
+        tc_commit<kPair>(done);
         for (uint32_t i = 0; i < kDrainSpins && !mbar_try_wait(done, 0); ++i) {}
     }
 };

@@ -385,3 +385,18 @@ def test_workspace_sizes_and_refusals():
         call = lambda ws, M: fn(1, FAKE, 65, FAKE, FAKE, FAKE, M, 65, 65, 3, FAKE, 65, ws, 1 << 30, None)  # noqa: E731
         assert call(FAKE + 8, 300) == INVALID and b"aligned" in lib.zs_last_error()
         assert call(FAKE, 0) == 0 and call(FAKE, -1) == INVALID
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("M,K,N,G,sizes,ordered", [
+    (1500, 200, 256, 2, "uniform", False), (1100, 256, 136, 2, "uniform", True), (512, 64, 480, 1, "uniform", False),
+    (513, 16, 1000, 1, "one", True), (9000, 264, 232, 5, "zipf", False), (40000, 768, 256, 3, "one", False),
+    (7000, 1032, 984, 2, "zipf", True),
+])
+def test_tiles_of_two_ctas(M, K, N, G, sizes, ordered, dtype):
+    # many rows a group and more than 128 columns: rows off the tiles' ends, columns in one CTA's half alone
+    group, t, d = draw(M, K, N, G, dtype, M + N, sizes, bad=0.02 if not ordered else 0.0)
+    if ordered:
+        group = np.sort(group)
+    check_all(group, t, d, dtype, ordered=ordered)
