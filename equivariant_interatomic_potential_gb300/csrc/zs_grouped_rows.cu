@@ -106,11 +106,12 @@ rows_mma(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUte
     unsigned char* slots = ring + S * Sh::kStage;
     unsigned char* staging = slots + Sh::kSlots;
     Setup<S, Sh::kTmemCols, Sh::kTile, 1, kPair> set;
-    set.begin(staging + kEpilogueWarps * kStageWarp, !kTma ? kLoaderWarps : a.perm ? 1 + kLoaderWarps : 1, 4 * Sh::kHalves, a.row_ptr, a.G, a.M);
+    set.begin(staging + kEpilogueWarps * kStageWarp, !kTma ? kLoaderWarps : a.perm ? 1 + (kPair ? 2 : 1) * kLoaderWarps : 1, 4 * Sh::kHalves, a.row_ptr, a.G, a.M);
     const RowGroups<Sh::kTile>& gr = set.groups;
     volatile int* dead = set.dead;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     constexpr int kBox = Sh::kBox;
+    const uint32_t full = kPair ? in_first(set.full) : set.full;   // told to
     const int nk = (a.red + kBox - 1) / kBox;
     constexpr int kPerChunk = kSums<T> > 1 ? kChunk / kBox : 1 << 30;   // stages between hand-overs to the epilogue
     const int rank = kPair ? (int)cluster_rank() : 0, step = kPair ? gridDim.x / 2 : gridDim.x;
@@ -121,25 +122,27 @@ rows_mma(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUte
         RingPos<S> pos;
         int issued = 0;
         while (!is_dead(dead) && next_product(a, gr, item, step, BN, t)) {
-            const int n0 = t.n0 + rank * Sh::kMine;
-            const int boxes = kMN ? imax(0, imin(Sh::kMine, a.cols - n0) + kBoxMN - 1) / kBoxMN : 1;
-            const uint32_t bytes = (a.perm ? 0 : Sh::kA) + boxes * Sh::kBoxB;
+            auto boxes_from = [&](int n0) { return kMN ? imax(0, imin(Sh::kMine, a.cols - n0) + kBoxMN - 1) / kBoxMN : 1; };
+            const int n0 = t.n0 + rank * Sh::kMine, boxes = boxes_from(n0);
+            // of a pair, the first CTA's barrier counts both CTAs' bytes
+            const uint32_t bytes = (kPair ? 2 : 1) * (a.perm ? 0 : Sh::kA) + (boxes + (kPair ? boxes_from(t.n0 + Sh::kMine) : 0)) * Sh::kBoxB;
             if (lane == 0) {
                 for (int k = 0; k < nk; ++k, ++issued, pos.next()) {
                     if (!bounded_wait_one(set.empty + 8 * pos.stage, pos.phase ^ 1, dead)) break;
-                    const uint32_t bar = set.full + 8 * pos.stage, at = smem_u32(ring) + pos.stage * Sh::kStage, bt = at + Sh::kA;
-                    mbar_arrive_expect_tx(bar, bytes);
-                    if (!a.perm) tma_2d(at, &a_map, k * kBox, t.p0 + kTileM * rank, bar);
+                    const uint32_t at = smem_u32(ring) + pos.stage * Sh::kStage, bt = at + Sh::kA;
+                    const uint32_t bar = full + 8 * pos.stage;
+                    if (rank == 0) mbar_arrive_expect_tx(set.full + 8 * pos.stage, bytes);
+                    if (!a.perm) tma_2d<kPair>(at, &a_map, k * kBox, t.p0 + kTileM * rank, bar);
                     for (int i = 0; i < boxes; ++i) {
-                        if (kMN) tma_3d(bt + i * Sh::kBoxB, &w_map, n0 + i * kBoxMN, k * kBox, t.g, bar);
-                        else tma_3d(bt, &w_map, k * kBox, n0, t.g, bar);
+                        if (kMN) tma_3d<kPair>(bt + i * Sh::kBoxB, &w_map, n0 + i * kBoxMN, k * kBox, t.g, bar);
+                        else tma_3d<kPair>(bt, &w_map, k * kBox, n0, t.g, bar);
                     }
                 }
             }
             __syncwarp();
         }
         issued = __shfl_sync(0xffffffffu, issued, 0);
-        if (is_dead(dead)) set.drain_copies(issued);
+        if (is_dead(dead) && rank == 0) set.drain_copies(issued);
         if (kPair && lane == 0)   // the last arrivals from the first CTA's products
             for (int i = 0; i < S; ++i, pos.next())
                 if (!bounded_wait_one<true>(set.empty + 8 * pos.stage, pos.phase ^ 1, dead)) break;
@@ -156,12 +159,12 @@ rows_mma(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUte
         bool have = (!kTma || a.perm) && next_product(a, gr, item, step, BN, t);
         int row = have ? row_of(t) : -1;
         if constexpr (kTma) {
-            Copies<S> copies;
+            Copies<S, kPair> copies;
             while (have && !is_dead(dead)) {
                 const bool more = next_product(a, gr, item, step, BN, u);
                 const int row_next = more ? row_of(u) : -1;
                 for (int k = 0; k < nk; ++k) {
-                    if (!copies.acquire(set.full, set.empty, dead)) break;
+                    if (!copies.acquire(full, set.empty, dead)) break;
                     copy_rows<kTileM>(smem_u32(ring) + copies.next.stage * Sh::kStage, a.a, row, k * kBox, w, lane);
                     copies.issued();
                 }
@@ -169,7 +172,7 @@ rows_mma(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUte
                 row = row_next;
                 have = more;
             }
-            copies.finish(set.full);
+            copies.finish(full);
         } else {
             // two groups of warps take the stages in turn; while one stage of a group is turned, its next is copied
             // (rows that are not aligned take the room of both)
@@ -231,22 +234,11 @@ rows_mma(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUte
             copies_wait<0>();
             if (aligned && copied > 0 && !is_dead(dead)) turn_stage(mine + ((copied - 1) & 1) * Sh::kParts * kStride);
         }
-    } else if (warp == 1 && rank == 1) {
-        // tells the first CTA, which issues the products of both, of each full stage
-        RingPos<S> pos;
-        while (!is_dead(dead) && next_product(a, gr, item, step, BN, t)) {
-            if (lane == 0) {
-                for (int k = 0; k < nk; ++k, pos.next()) {
-                    if (!bounded_wait_one(set.full + 8 * pos.stage, pos.phase, dead)) break;
-                    mbar_arrive_at(set.full + 8 * pos.stage, 0);
-                }
-            }
-            __syncwarp();
-        }
-    } else if (warp == 1) {
+    } else if (warp == 1 && rank == 0) {   // of a pair, for both
         RingPos<S> pos;
         int n = 0;
-        while (!is_dead(dead) && next_product(a, gr, item, step, BN, t)) {
+        bool have = next_product(a, gr, item, step, BN, t);   // which tile it is does not matter here
+        while (have && !is_dead(dead)) {
             for (int k = 0; k < nk; ++k, pos.next()) {
                 const int buf = n & 1;
                 if (k % kPerChunk == 0) bounded_wait_on<kPair>(set.tempty + 8 * buf, ((n >> 1) & 1) ^ 1, dead);
@@ -255,8 +247,8 @@ rows_mma(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUte
                 const uint32_t at = smem_u32(ring) + pos.stage * Sh::kStage;
                 const int steps = (imin(kBox, a.red - k * kBox) + 15) / 16;
                 issue_stage<T, false, kMN, BN, kPair>(set.tmem + buf * kSums<T> * BN, at, Sh::kA, 0, at + Sh::P * Sh::kA, Sh::kBoxB,
-                                                      steps, k % kPerChunk > 0);
-                tc_commit<kPair>(set.empty + 8 * pos.stage);
+                                                      steps, k % kPerChunk > 0, set.empty + 8 * pos.stage);
+                if (k == 0) have = next_product(a, gr, item, step, BN, t);   // looked for while products run
                 if (k % kPerChunk == kPerChunk - 1 || k == nk - 1) {
                     tc_commit<kPair>(set.tfull + 8 * buf);
                     ++n;
@@ -287,7 +279,7 @@ rows_mma(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUte
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) {
-                    if (rank) mbar_arrive_at(set.tempty + 8 * buf, 0);
+                    if (kPair) mbar_arrive_there(in_first(set.tempty + 8 * buf));
                     else mbar_arrive(set.tempty + 8 * buf);
                 }
                 ++n;

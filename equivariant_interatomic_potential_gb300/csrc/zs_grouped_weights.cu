@@ -164,8 +164,7 @@ weights_mma(const __grid_constant__ CUtensorMap dy_map, const __grid_constant__ 
             const uint32_t at = smem_u32(ring) + pos.stage * Sh::kStage;
             tc_fence_after();
             issue_stage<T, true, true, BN>(set.tmem + buf * kSums<T> * BN, at, Sh::kA, Sh::kBox, at + Sh::P * Sh::kA, Sh::kBox,
-                                           steps, since > 0);
-            tc_commit<false>(set.empty + 8 * pos.stage);
+                                           steps, since > 0, set.empty + 8 * pos.stage);
             if (since + kUnit >= kPerChunk || p + kUnit >= s.p1) {
                 tc_commit<false>(set.tfull + 8 * buf);
                 ++n;

@@ -98,12 +98,15 @@ __device__ __forceinline__ bool bounded_wait_one(uint32_t bar, uint32_t parity, 
 // (outputs are then undefined), and finds the CTA dead later.
 template <bool kCluster = false>
 __device__ __forceinline__ void bounded_wait_on(uint32_t bar, uint32_t parity, volatile int* dead) {
-    for (uint32_t i = 0; i < kMaxSpins; ++i) {
-        if (kCluster ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)) break;
-        if ((i & 63) == 63 && *dead) break;
-        if (i == kMaxSpins - 1) {
-            note_timeout();
-            *dead = 1;
+    if (!(kCluster ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity))) {
+#pragma unroll 1
+        for (uint32_t i = 0; i < kMaxSpins; ++i) {
+            if (kCluster ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)) break;
+            if ((i & 63) == 63 && *dead) break;
+            if (i == kMaxSpins - 1) {
+                note_timeout();
+                *dead = 1;
+            }
         }
     }
     __syncwarp();
@@ -122,11 +125,17 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" :: "r"(bar) : "memory");
 }
-// At the same barrier of CTA `rank` of the cluster.
-__device__ __forceinline__ void mbar_arrive_at(uint32_t bar, uint32_t rank) {
+// The same address in the first CTA of the cluster.
+__device__ __forceinline__ uint32_t in_first(uint32_t at) {
     uint32_t there;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(bar), "r"(rank));
-    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" :: "r"(there) : "memory");
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(there) : "r"(at));
+    return there;
+}
+// At a barrier of the cluster.  (What is told of lies in this CTA's shared
+// memory, complete and fenced for the tensor cores before, or has been read from
+// TMEM; released to the whole cluster, each arrival took about 700 cycles.)
+__device__ __forceinline__ void mbar_arrive_there(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" :: "r"(bar) : "memory");
 }
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
@@ -196,6 +205,35 @@ __device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint3
                      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
                      :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate) : "memory");
 }
+// Four products one after the other, and an arrival at `bar` when they are done.
+template <bool kPair, uint32_t kStepA, uint32_t kStepB>
+__device__ __forceinline__ void tc_mma4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate, uint32_t bar) {
+    if constexpr (kPair)
+        asm volatile("{\n\t.reg .pred p, t, e;\n\t.reg .b64 a, b;\n\t"
+                     "elect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
+                     "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t"
+                     "add.s64 a, %1, %6;\n\tadd.s64 b, %2, %7;\n\t"
+                     "@e tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %3, t;\n\t"
+                     "add.s64 a, a, %6;\n\tadd.s64 b, b, %7;\n\t"
+                     "@e tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %3, t;\n\t"
+                     "add.s64 a, a, %6;\n\tadd.s64 b, b, %7;\n\t"
+                     "@e tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %3, t;\n\t"
+                     "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%5], %8;\n\t}"
+                     :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate), "r"(bar), "n"(kStepA), "n"(kStepB),
+                        "h"((unsigned short)3) : "memory");
+    else
+        asm volatile("{\n\t.reg .pred p, t, e;\n\t.reg .b64 a, b;\n\t"
+                     "elect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
+                     "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
+                     "add.s64 a, %1, %6;\n\tadd.s64 b, %2, %7;\n\t"
+                     "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+                     "add.s64 a, a, %6;\n\tadd.s64 b, b, %7;\n\t"
+                     "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+                     "add.s64 a, a, %6;\n\tadd.s64 b, b, %7;\n\t"
+                     "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+                     "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%5];\n\t}"
+                     :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate), "r"(bar), "n"(kStepA), "n"(kStepB) : "memory");
+}
 // 32 columns of this warp's 32 TMEM lanes: lane l gets row l.
 __device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t (&r)[32]) {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 "
@@ -244,42 +282,61 @@ __device__ __forceinline__ uint32_t instr_desc(bool a_mn, bool b_mn, int n, int 
 }
 
 // The products of one stage: `steps` times 16 summed-over elements, into a tile
-// of BN columns (fp32: three of them).  Planes of the left operand are a_plane
-// bytes apart, those of the right one follow each other.  Of a pair, each CTA
-// holds 128 rows of the left operand and half the columns of the right one, at
-// the same addresses, and gets its rows' sums.
+// of BN columns (fp32: three of them), and an arrival at `bar` when they are
+// done.  Planes of the left operand are a_plane bytes apart, those of the right
+// one follow each other.  Of a pair, each CTA holds 128 rows of the left operand
+// and half the columns of the right one, at the same addresses, and gets its
+// rows' sums.
 template <typename T, bool kAMN, bool kBMN, int BN, bool kPair = false>
 __device__ __forceinline__ void issue_stage(uint32_t d, uint32_t a, uint32_t a_plane, uint32_t a_lbo, uint32_t b, uint32_t b_lbo,
-                                            int steps, bool accumulate) {
+                                            int steps, bool accumulate, uint32_t bar) {
     constexpr int kACols = kAMN ? kBoxMN : kStageK<T>, kBCols = kBMN ? kBoxMN : kStageK<T>;
-    const uint64_t a0 = box_desc<kACols>(a, a_lbo), b0 = box_desc<kBCols>(b, b_lbo);
+    constexpr uint32_t kStepA = kDescStep<kACols, kAMN>, kStepB = kDescStep<kBCols, kBMN>;
     constexpr int kMost = kStageK<T> / 16;
+    const uint64_t a0 = box_desc<kACols>(a, a_lbo), b0 = box_desc<kBCols>(b, b_lbo);
+    if constexpr (kPlanes<T> == 1) {
+        static_assert(kMost == 4, "a whole stage's products in one block");
+        const uint32_t idesc = instr_desc<T>(kAMN, kBMN, BN, kPair ? 2 * kTileM : kTileM);
+        if (steps == kMost) {
+            tc_mma4<kPair, kStepA, kStepB>(d, a0, b0, idesc, accumulate, bar);
+            return;
+        }
+        for (int k = 0; k < steps; ++k) tc_mma<kPair>(d, a0 + k * kStepA, b0 + k * kStepB, idesc, accumulate || k > 0);
+    } else {
+        static_assert(!kPair, "fp32 tiles are a CTA's own");
 #pragma unroll
-    for (int k = 0; k < kMost; ++k) {
-        if (k >= steps) break;
-        const uint64_t ak = a0 + k * kDescStep<kACols, kAMN>, bk = b0 + k * kDescStep<kBCols, kBMN>;
-        const bool more = accumulate || k > 0;
-        if constexpr (kPlanes<T> == 1) {
-            tc_mma<kPair>(d, ak, bk, instr_desc<T>(kAMN, kBMN, BN, kPair ? 2 * kTileM : kTileM), more);
-        } else {
+        for (int k = 0; k < kMost; ++k) {
+            if (k >= steps) break;
+            const uint64_t ak = a0 + k * kStepA, bk = b0 + k * kStepB;
             const uint32_t ap = a_plane >> 4;
-            static_assert(!kPair, "fp32 tiles are a CTA's own");
-            tc_mma<false>(d, ak, bk, instr_desc<T>(kAMN, kBMN, 3 * BN), more);
+            tc_mma<false>(d, ak, bk, instr_desc<T>(kAMN, kBMN, 3 * BN), accumulate || k > 0);
             tc_mma<false>(d + BN, ak + ap, bk, instr_desc<T>(kAMN, kBMN, 2 * BN), true);
             tc_mma<false>(d + 2 * BN, ak + 2 * ap, bk, instr_desc<T>(kAMN, kBMN, BN), true);
         }
     }
+    tc_commit<kPair>(bar);
 }
 
 // ---------------------------------------------------------------- TMA
 
+// kPair: the barrier is the first CTA's.
+template <bool kPair = false>
 __device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
-    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
-                 :: "r"(dst), "l"(map), "r"(x), "r"(y), "r"(bar) : "memory");
+    if constexpr (kPair)
+        asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3}], [%4];"
+                     :: "r"(dst), "l"(map), "r"(x), "r"(y), "r"(bar) : "memory");
+    else
+        asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
+                     :: "r"(dst), "l"(map), "r"(x), "r"(y), "r"(bar) : "memory");
 }
+template <bool kPair = false>
 __device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
-    asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
-                 :: "r"(dst), "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar) : "memory");
+    if constexpr (kPair)
+        asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3, %4}], [%5];"
+                     :: "r"(dst), "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar) : "memory");
+    else
+        asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+                     :: "r"(dst), "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar) : "memory");
 }
 // ---------------------------------------------------------------- rows copied by warps
 
@@ -554,7 +611,8 @@ __device__ __forceinline__ void add_chunk(uint32_t from, int apart, float (&acc)
 
 // The copies of a loader warp that are on their way, told of (an arrival at the
 // stage's full barrier) as they land.
-template <int S>
+// kPair: the full barriers are the first CTA's.
+template <int S, bool kPair = false>
 struct Copies {
     RingPos<S> next, told;
     int ahead = 0;      // stages copied and not told of
@@ -572,7 +630,10 @@ struct Copies {
         }
         fence_async_smem();
         __syncwarp();
-        if ((threadIdx.x & 31) == 0) mbar_arrive(full + 8 * told.stage);
+        if ((threadIdx.x & 31) == 0) {
+            if (kPair) mbar_arrive_there(full + 8 * told.stage);
+            else mbar_arrive(full + 8 * told.stage);
+        }
         told.next();
     }
     // The next stage is free; while it is not, older ones are told of.
@@ -592,8 +653,8 @@ struct Copies {
 };
 
 // What every grouped kernel sets up: barriers, TMEM, the groups' starts.  Of a
-// pair, the first CTA's full barriers count one arrival more (the other CTA's
-// stage is full) and its tempty barriers both CTAs' epilogue warps.
+// pair, both CTAs' copies are told to the first CTA's full barriers and both
+// epilogues to its tempty barriers.
 template <int S, uint32_t kTmemCols, int kTile, int kExtra, bool kPair = false>
 struct Setup {
     static constexpr int kBytes = (2 * S + 7) * 8 + (kGroupsHeld + 2) * 4;
@@ -607,7 +668,7 @@ struct Setup {
         uint32_t* slot = reinterpret_cast<uint32_t*>(bars + 2 * S + 6);
         full = smem_u32(bars), empty = full + 8 * S, tfull = empty + 8 * S, tempty = tfull + 16, done = tempty + 16;
         if (threadIdx.x == 0) {
-            if (kPair && cluster_rank() == 0) ++full_count, epilogue_warps *= 2;
+            if (kPair) epilogue_warps *= 2;
             for (int i = 0; i < S; ++i) {
                 mbar_init(full + 8 * i, full_count);
                 mbar_init(empty + 8 * i, 1);
