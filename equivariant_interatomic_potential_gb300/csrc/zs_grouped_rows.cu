@@ -126,27 +126,22 @@ rows_mma(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUte
             const int n0 = t.n0 + rank * Sh::kMine, boxes = boxes_from(n0);
             // of a pair, the first CTA's barrier counts both CTAs' bytes
             const uint32_t bytes = (kPair ? 2 : 1) * (a.perm ? 0 : Sh::kA) + (boxes + (kPair ? boxes_from(t.n0 + Sh::kMine) : 0)) * Sh::kBoxB;
-            if (lane == 0) {
-                for (int k = 0; k < nk; ++k, ++issued, pos.next()) {
-                    if (!bounded_wait_one(set.empty + 8 * pos.stage, pos.phase ^ 1, dead)) break;
-                    const uint32_t at = smem_u32(ring) + pos.stage * Sh::kStage, bt = at + Sh::kA;
-                    const uint32_t bar = full + 8 * pos.stage;
-                    if (rank == 0) mbar_arrive_expect_tx(set.full + 8 * pos.stage, bytes);
-                    if (!a.perm) tma_2d<kPair>(at, &a_map, k * kBox, t.p0 + kTileM * rank, bar);
-                    for (int i = 0; i < boxes; ++i) {
-                        if (kMN) tma_3d<kPair>(bt + i * Sh::kBoxB, &w_map, n0 + i * kBoxMN, k * kBox, t.g, bar);
-                        else tma_3d<kPair>(bt, &w_map, k * kBox, n0, t.g, bar);
-                    }
+            for (int k = 0; k < nk; ++k, ++issued, pos.next()) {
+                bounded_wait_on(set.empty + 8 * pos.stage, pos.phase ^ 1, dead);
+                if (is_dead(dead)) break;
+                const uint32_t at = smem_u32(ring) + pos.stage * Sh::kStage, bt = at + Sh::kA;
+                const uint32_t bar = full + 8 * pos.stage;
+                if (rank == 0) expect_bytes(set.full + 8 * pos.stage, bytes);
+                if (!a.perm) tma_2d<kPair>(at, &a_map, k * kBox, t.p0 + kTileM * rank, bar);
+                for (int i = 0; i < boxes; ++i) {
+                    if (kMN) tma_3d<kPair>(bt + i * Sh::kBoxB, &w_map, n0 + i * kBoxMN, k * kBox, t.g, bar);
+                    else tma_3d<kPair>(bt, &w_map, k * kBox, n0, t.g, bar);
                 }
             }
-            __syncwarp();
         }
-        issued = __shfl_sync(0xffffffffu, issued, 0);
         if (is_dead(dead) && rank == 0) set.drain_copies(issued);
-        if (kPair && lane == 0)   // the last arrivals from the first CTA's products
-            for (int i = 0; i < S; ++i, pos.next())
-                if (!bounded_wait_one<true>(set.empty + 8 * pos.stage, pos.phase ^ 1, dead)) break;
-        __syncwarp();
+        if (kPair)   // the last arrivals from the first CTA's products
+            for (int i = 0; i < S; ++i, pos.next()) bounded_wait_on<true>(set.empty + 8 * pos.stage, pos.phase ^ 1, dead);
     } else if (warp >= 4 + kEpilogueWarps) {
         const int w = (warp - 4 - kEpilogueWarps) % kLoaderWarps;
         constexpr int kPerA = kTileM / kLoaderWarps;

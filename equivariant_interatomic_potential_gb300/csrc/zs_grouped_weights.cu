@@ -58,18 +58,15 @@ weights_mma(const __grid_constant__ CUtensorMap dy_map, const __grid_constant__ 
         while (!is_dead(dead) && walk.next(s)) {
             const int a_boxes = imin(2, (a.N - s.n0 + kBoxMN - 1) / kBoxMN);
             const int b_boxes = imin(Sh::kBBoxes, (a.K - s.k0 + kBoxMN - 1) / kBoxMN);
-            if (lane == 0) {
-                for (int p = s.p0; p < s.p1; p += kUnit, ++issued, pos.next()) {
-                    if (!bounded_wait_one(set.empty + 8 * pos.stage, pos.phase ^ 1, dead)) break;
-                    const uint32_t bar = set.full + 8 * pos.stage, at = smem_u32(ring) + pos.stage * Sh::kStage, bt = at + Sh::kA;
-                    mbar_arrive_expect_tx(bar, (a_boxes + b_boxes) * Sh::kBox);
-                    for (int i = 0; i < a_boxes; ++i) tma_2d(at + i * Sh::kBox, &dy_map, s.n0 + i * kBoxMN, p, bar);
-                    for (int i = 0; i < b_boxes; ++i) tma_2d(bt + i * Sh::kBox, &x_map, s.k0 + i * kBoxMN, p, bar);
-                }
+            for (int p = s.p0; p < s.p1; p += kUnit, ++issued, pos.next()) {
+                bounded_wait_on(set.empty + 8 * pos.stage, pos.phase ^ 1, dead);
+                if (is_dead(dead)) break;
+                const uint32_t bar = set.full + 8 * pos.stage, at = smem_u32(ring) + pos.stage * Sh::kStage, bt = at + Sh::kA;
+                expect_bytes(bar, (a_boxes + b_boxes) * Sh::kBox);
+                for (int i = 0; i < a_boxes; ++i) tma_2d(at + i * Sh::kBox, &dy_map, s.n0 + i * kBoxMN, p, bar);
+                for (int i = 0; i < b_boxes; ++i) tma_2d(bt + i * Sh::kBox, &x_map, s.k0 + i * kBoxMN, p, bar);
             }
-            __syncwarp();
         }
-        issued = __shfl_sync(0xffffffffu, issued, 0);
         if (is_dead(dead)) set.drain_copies(issued);
     } else if (warp >= 4 + kEpilogueWarps && (!kTma || a.perm)) {
         const int w = (warp - 4 - kEpilogueWarps) % kLoaderWarps;

@@ -81,21 +81,10 @@ __device__ __forceinline__ bool bounded_wait(uint32_t bar, uint32_t parity, vola
     }
     return __all_sync(0xffffffffu, ok);
 }
-// One thread's wait, for the roles that issue: a vote at each stage would cost
-// them a tenth of the tensor cores' time.
-// kCluster: the other CTA of a pair arrives at this barrier too.
-template <bool kCluster = false>
-__device__ __forceinline__ bool bounded_wait_one(uint32_t bar, uint32_t parity, volatile int* dead) {
-    for (uint32_t i = 0; i < kMaxSpins; ++i) {
-        if (kCluster ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)) return true;
-        if ((i & 63) == 63 && *dead) return false;
-    }
-    note_timeout();
-    *dead = 1;
-    return false;
-}
-// A whole warp's wait without a vote: where it runs out the warp carries on
-// (outputs are then undefined), and finds the CTA dead later.
+// The same without a vote, for the warps that issue copies and products: where
+// it runs out the warp carries on (outputs are then undefined) and finds the CTA
+// dead later.  A vote at each stage would cost them a tenth of the tensor cores'
+// time.  kCluster: the other CTA of a pair arrives at this barrier too.
 template <bool kCluster = false>
 __device__ __forceinline__ void bounded_wait_on(uint32_t bar, uint32_t parity, volatile int* dead) {
     if (!(kCluster ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity))) {
@@ -319,24 +308,32 @@ __device__ __forceinline__ void issue_stage(uint32_t d, uint32_t a, uint32_t a_p
 
 // ---------------------------------------------------------------- TMA
 
-// kPair: the barrier is the first CTA's.
+// By a warp in step, as the products are.  kPair: the barrier is the first CTA's.
 template <bool kPair = false>
 __device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
     if constexpr (kPair)
-        asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3}], [%4];"
-                     :: "r"(dst), "l"(map), "r"(x), "r"(y), "r"(bar) : "memory");
+        asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+                     "@e cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 "
+                     "[%0], [%1, {%2, %3}], [%4];\n\t}" :: "r"(dst), "l"(map), "r"(x), "r"(y), "r"(bar) : "memory");
     else
-        asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
-                     :: "r"(dst), "l"(map), "r"(x), "r"(y), "r"(bar) : "memory");
+        asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+                     "@e cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+                     "[%0], [%1, {%2, %3}], [%4];\n\t}" :: "r"(dst), "l"(map), "r"(x), "r"(y), "r"(bar) : "memory");
 }
 template <bool kPair = false>
 __device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
     if constexpr (kPair)
-        asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3, %4}], [%5];"
-                     :: "r"(dst), "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar) : "memory");
+        asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+                     "@e cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 "
+                     "[%0], [%1, {%2, %3, %4}], [%5];\n\t}" :: "r"(dst), "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar) : "memory");
     else
-        asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
-                     :: "r"(dst), "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar) : "memory");
+        asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+                     "@e cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+                     "[%0], [%1, {%2, %3, %4}], [%5];\n\t}" :: "r"(dst), "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar) : "memory");
+}
+__device__ __forceinline__ void expect_bytes(uint32_t bar, uint32_t bytes) {
+    asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+                 "@e mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" :: "r"(bar), "r"(bytes) : "memory");
 }
 // ---------------------------------------------------------------- rows copied by warps
 
