@@ -63,26 +63,36 @@ int64_t padded(int32_t dtype, int64_t cols) {
 }
 bool pieces(int32_t dtype, const void* p, int64_t ld) { return aligned16(p) && ld % (16 / dtype_bytes(dtype)) == 0; }
 
-// Hands out a workspace's room for padded matrices.
+// Hands out a workspace's room for matrices that are laid out anew.
 struct Padder {
     Padding list[2] = {};
     int n = 0;
     char* room;
     size_t left;
     int32_t dtype;
-    // The matrix as it is, or (p and ld replaced) its place in the workspace where its rows are not whole pieces and it fits.
-    void lay_out(const void*& p, int64_t& ld, int64_t rows, int32_t cols) {
-        if (pieces(dtype, p, ld) || rows == 0) return;
+    // p and ld replaced by a place in the workspace; false where it does not fit, or there is nothing to do.
+    bool lay_out(const void*& p, int64_t& ld, int64_t rows, int32_t cols, const int32_t* perm = nullptr) {
         const int64_t to = padded(dtype, cols);
         const size_t bytes = align_up((size_t)rows * to * dtype_bytes(dtype), 256);
-        if (!room || bytes > left) return;
-        list[n++] = {p, ld, rows, cols, room};
+        if (rows == 0 || !room || bytes > left) return false;
+        list[n++] = {p, ld, rows, cols, perm, room};
         p = room;
         ld = to;
         room += bytes;
         left -= bytes;
+        return true;
     }
 };
+
+// Gathered 16-bit rows are put in order first where enough tiles read them again, and TMA brings them from then on:
+// products of at least kOrderCols columns (32768 bf16 rows, 216 -> 1360: 53 us, 71 gathered by each tile; 512 -> 2048: 75 and
+// 94; 512 -> 1024: 50 and 50; 65536 rows, 256 -> 1024: 67 and 63), weight gradients of at least kOrderTiles tiles (2048 -> 512,
+// 32 tiles: 136 and 242 us; 256 -> 1024, 8 tiles: 111 and 113).  fp32 takes its rows through registers either way.
+constexpr int kOrderCols = 1280, kOrderTiles = 16;
+bool order_rows(int32_t dtype, int32_t cols) { return dtype != ZS_F32 && cols >= kOrderCols; }
+bool order_both(int32_t dtype, int32_t K, int32_t N) {
+    return dtype != ZS_F32 && (int64_t)((N + 127) / 128) * ((K + 255) / 256) >= kOrderTiles;
+}
 
 // Fewer rows than this are not worth a copy.
 constexpr int64_t kPadRows = 256;
@@ -106,13 +116,16 @@ zs_status product(const char* fn, int which, int32_t dtype, const void* a, int64
     if (grouped_is_few(dtype, which, M, N, G)) return grouped_few(fn, dtype, which, a, a_ld, w, K, row_ptr, perm, M, K, N, G, out, out_ld, s);
     if (grouped_is_small(K, N)) return grouped_small_rows(fn, dtype, which, a, a_ld, w, row_ptr, perm, M, K, N, G, out, out_ld, s);
     int64_t w_ld = K;
+    const int32_t* gather = perm;
     Padder pad{{}, 0, static_cast<char*>(workspace), workspace ? workspace_bytes : 0, dtype};
     if (M >= kPadRows) {
-        pad.lay_out(w, w_ld, (int64_t)G * N, K);
-        pad.lay_out(a, a_ld, M, in_cols);
+        if (!pieces(dtype, w, w_ld)) pad.lay_out(w, w_ld, (int64_t)G * N, K);
+        const int32_t* order = dtype == ZS_F32 ? nullptr : perm;
+        if ((!pieces(dtype, a, a_ld) || (order && order_rows(dtype, out_cols))) && pad.lay_out(a, a_ld, M, in_cols, order) && order)
+            gather = nullptr;
         if (zs_status st = grouped_pad(fn, dtype, pad.list, s)) return st;
     }
-    return grouped_rows(fn, dtype, a, a_ld, w, w_ld, row_ptr, perm, M, K, N, G, out, out_ld, which != 0, s);
+    return grouped_rows(fn, dtype, a, a_ld, w, w_ld, row_ptr, perm, gather, M, K, N, G, out, out_ld, which != 0, s);
 }
 
 }  // namespace
@@ -137,8 +150,8 @@ size_t zs_grouped_matmul_workspace_bytes(int32_t dtype, int64_t M, int32_t K, in
     using namespace zs;
     if (!known_dtype(dtype) || M < kPadRows || M >= (int64_t(1) << 31) || K < 1 || N < 1 || G < 1 || grouped_is_small(K, N)) return 0;
     const bool k = padded(dtype, K) != K, n = padded(dtype, N) != N;
-    const size_t w = k ? padded_bytes(dtype, (int64_t)G * N, K) : 0;
-    return w + imax(k ? padded_bytes(dtype, M, K) : 0, n ? padded_bytes(dtype, M, N) : 0);
+    return (k ? padded_bytes(dtype, (int64_t)G * N, K) : 0) +
+           imax(k || order_rows(dtype, N) ? padded_bytes(dtype, M, K) : 0, n || order_rows(dtype, K) ? padded_bytes(dtype, M, N) : 0);
 }
 
 zs_status zs_grouped_matmul_ws(int32_t dtype, const void* x, int64_t x_ld, const void* w, const int32_t* row_ptr,
@@ -159,12 +172,16 @@ size_t zs_grouped_matmul_dw_workspace_bytes(int32_t dtype, int64_t M, int32_t K,
     if (!zs::known_dtype(dtype) || M < 0 || M >= (int64_t(1) << 31) || K < 1 || N < 1 || G < 1) return 0;
     using namespace zs;
     if (grouped_is_few(dtype, 2, M, N, G)) return 0;
-    size_t bytes = grouped_weights_workspace(dtype, M, K, N, G);
-    if (M >= kPadRows && !grouped_is_small(K, N)) {
-        if (padded(dtype, K) != K) bytes += padded_bytes(dtype, M, K);
-        if (padded(dtype, N) != N) bytes += padded_bytes(dtype, M, N);
-    }
-    return bytes;
+    return grouped_weights_workspace(dtype, M, K, N, G);
+}
+
+size_t zs_grouped_matmul_dw_copy_bytes(int32_t dtype, int64_t M, int32_t K, int32_t N, int32_t G) {
+    using namespace zs;
+    if (!known_dtype(dtype) || M < kPadRows || M >= (int64_t(1) << 31) || K < 1 || N < 1 || G < 1 || grouped_is_small(K, N) ||
+        grouped_is_few(dtype, 2, M, N, G))
+        return 0;
+    const bool both = order_both(dtype, K, N);
+    return (both || padded(dtype, K) != K ? padded_bytes(dtype, M, K) : 0) + (both || padded(dtype, N) != N ? padded_bytes(dtype, M, N) : 0);
 }
 
 zs_status zs_grouped_matmul_dw(int32_t dtype, const void* dy, int64_t dy_ld, const void* x, int64_t x_ld,
@@ -186,13 +203,18 @@ zs_status zs_grouped_matmul_dw(int32_t dtype, const void* dy, int64_t dy_ld, con
     if (grouped_is_few(dtype, 2, M, N, G))
         return grouped_few(fn, dtype, 2, dy, dy_ld, x, x_ld, row_ptr, perm, M, K, N, G, dw, K, reinterpret_cast<cudaStream_t>(stream));
     if (M == 1) dy_ld = N, x_ld = K;
-    // the partial sums first, then what is laid out anew
-    const size_t partial = grouped_weights_workspace(dtype, M, K, N, G);
+    // the partial sums first, then what is laid out anew; in the groups' order only both operands at once
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    Padder pad{{}, 0, static_cast<char*>(workspace) + partial, workspace ? workspace_bytes - partial : 0, dtype};
+    Padder pad{{}, 0, static_cast<char*>(workspace) + need, workspace ? workspace_bytes - need : 0, dtype};
     if (M >= kPadRows && !grouped_is_small(K, N)) {
-        pad.lay_out(x, x_ld, M, K);
-        pad.lay_out(dy, dy_ld, M, N);
+        const bool x_off = !pieces(dtype, x, x_ld), dy_off = !pieces(dtype, dy, dy_ld);
+        if (perm && dtype != ZS_F32 && ((x_off && dy_off) || order_both(dtype, K, N)) && padded_bytes(dtype, M, K) + padded_bytes(dtype, M, N) <= pad.left &&
+            pad.lay_out(x, x_ld, M, K, perm) && pad.lay_out(dy, dy_ld, M, N, perm)) {
+            perm = nullptr;
+        } else {
+            if (x_off) pad.lay_out(x, x_ld, M, K);
+            if (dy_off) pad.lay_out(dy, dy_ld, M, N);
+        }
         if (zs_status st = grouped_pad(fn, dtype, pad.list, s)) return st;
     }
     return grouped_weights(fn, dtype, dy, dy_ld, x, x_ld, row_ptr, perm, M, K, N, G, dw, workspace, s);

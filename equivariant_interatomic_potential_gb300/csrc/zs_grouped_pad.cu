@@ -1,4 +1,5 @@
-// Rows that do not start on 16-byte boundaries, laid out anew so that they do.
+// Rows that do not start on 16-byte boundaries, or that a CSR gathers, laid out
+// anew: on such boundaries, and in the groups' order.
 //
 // The tensor-core products take their operands in 16-byte pieces.  Rows of an
 // odd number of elements can be brought into that form as they are loaded, but
@@ -18,6 +19,7 @@ namespace {
 struct PadMatrix {
     const char* src;
     char* dst;
+    const int32_t* perm;     // row of each position, or NULL: in order
     int64_t ld, rows;        // source rows in bytes
     int cols, pieces;        // bytes of a row, 16-byte pieces of a padded one
     int per_block;           // rows of a CTA
@@ -37,9 +39,9 @@ __device__ __forceinline__ uint4 unaligned_piece(const char* at, int left, const
     const int off = (int)(reinterpret_cast<uintptr_t>(at) & 15u);
     uint4 q = make_uint4(0, 0, 0, 0);
     uint32_t* qe = &q.x;
-    if (at - off + 32 <= end) {
+    if (at - off + (off ? 32 : 16) <= end) {
         const uint4* base = reinterpret_cast<const uint4*>(at - off);
-        const uint4 lo = __ldg(base), hi = __ldg(base + 1);
+        const uint4 lo = __ldg(base), hi = off ? __ldg(base + 1) : make_uint4(0, 0, 0, 0);
         const uint32_t u[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
         const int sh = 8 * (off & 3);
         uint32_t v[5], t[6];   // words (off / 4) .. + 4 of u
@@ -76,7 +78,6 @@ __global__ void __launch_bounds__(kThreads) pad_rows(const __grid_constant__ Pad
     const int64_t row0 = (blockIdx.x - (second ? a.blocks0 : 0)) * m.per_block;
     const int64_t here = m.rows - row0 < m.per_block ? m.rows - row0 : m.per_block;
     const int count = (int)here * m.pieces;
-    const char* src = m.src + row0 * m.ld;
     char* dst = m.dst + row0 * m.pieces * 16;
     const char* end = m.src + (m.rows - 1) * m.ld + m.cols;
     for (int p0 = threadIdx.x; p0 < count; p0 += kThreads * kPerThread) {
@@ -86,7 +87,10 @@ __global__ void __launch_bounds__(kThreads) pad_rows(const __grid_constant__ Pad
             const int p = p0 + i * kThreads;
             if (p >= count) break;
             const int r = m.pieces == 1 ? p : (int)__umulhi((uint32_t)p, m.inverse), c = (p - r * m.pieces) * 16;
-            q[i] = unaligned_piece<kEs>(src + r * m.ld + c, m.cols - c, end);
+            int64_t row = row0 + r;
+            if (m.perm) row = __ldg(m.perm + row);
+            q[i] = make_uint4(0, 0, 0, 0);
+            if ((uint64_t)row < (uint64_t)m.rows) q[i] = unaligned_piece<kEs>(m.src + row * m.ld + c, m.cols - c, end);
         }
 #pragma unroll
         for (int i = 0; i < kPerThread; ++i) {
@@ -107,6 +111,7 @@ zs_status grouped_pad(const char* fn, int32_t dtype, const Padding (&p)[2], cuda
         PadMatrix& m = a.m[i];
         m.src = static_cast<const char*>(p[i].src);
         m.dst = static_cast<char*>(p[i].dst);
+        m.perm = p[i].perm;
         m.ld = p[i].ld * es;
         m.rows = p[i].rows;
         m.cols = p[i].cols * es;

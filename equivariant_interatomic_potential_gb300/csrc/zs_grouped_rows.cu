@@ -19,7 +19,8 @@ struct RowsArgs {
     Matrix w;             // weights of group 0, rows w.ld apart
     int64_t w_group;      // elements of a group's weights
     const int32_t* row_ptr;
-    const int32_t* perm;
+    const int32_t* perm;  // the output rows
+    const int32_t* gather;   // the left operand's rows: perm, or NULL where they are in order
     void* out;
     int64_t out_ld;
     bool out_wide;
@@ -55,7 +56,7 @@ struct RowsShape {
     static_assert(kPlanes<T> == 1 || !kMN || BN == kBoxMN, "the planes of an MN-major operand follow each other");
     static_assert(S >= 2 && Setup<S, kTmemCols, kTile, 1, kPair>::kBytes <= 4608, "two stages at least");
     static constexpr int kSmem = S * (int)kStage + kFixed;
-    static constexpr int kThreads = 32 * (4 + kEpilogueWarps + (kTma ? 1 : 2) * kLoaderWarps);
+    static constexpr int kThreads = 32 * (4 + kEpilogueWarps + (kPair ? 0 : kTma ? 1 : 2) * kLoaderWarps);
 };
 
 struct Item {
@@ -90,10 +91,10 @@ __device__ __forceinline__ bool next_product(const RowsArgs& a, const RowGroups<
     return false;
 }
 
-__device__ __forceinline__ int row_at(const RowsArgs& a, int p) {
-    if (!a.perm) return p;
-    const int r = __ldg(a.perm + p);
-    return (uint32_t)r < (uint32_t)a.M ? r : -1;
+__device__ __forceinline__ int row_at(const int32_t* perm, int M, int p) {
+    if (!perm) return p;
+    const int r = __ldg(perm + p);
+    return (uint32_t)r < (uint32_t)M ? r : -1;
 }
 
 template <typename T, bool kTma, bool kMN, int BN, bool kPair>
@@ -106,7 +107,7 @@ rows_mma(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUte
     unsigned char* slots = ring + S * Sh::kStage;
     unsigned char* staging = slots + Sh::kSlots;
     Setup<S, Sh::kTmemCols, Sh::kTile, 1, kPair> set;
-    set.begin(staging + kEpilogueWarps * kStageWarp, !kTma ? kLoaderWarps : a.perm ? 1 + (kPair ? 2 : 1) * kLoaderWarps : 1, 4 * Sh::kHalves, a.row_ptr, a.G, a.M);
+    set.begin(staging + kEpilogueWarps * kStageWarp, !kTma ? kLoaderWarps : a.gather ? 1 + kLoaderWarps : 1, 4 * Sh::kHalves, a.row_ptr, a.G, a.M);
     const RowGroups<Sh::kTile>& gr = set.groups;
     volatile int* dead = set.dead;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -125,14 +126,14 @@ rows_mma(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUte
             auto boxes_from = [&](int n0) { return kMN ? imax(0, imin(Sh::kMine, a.cols - n0) + kBoxMN - 1) / kBoxMN : 1; };
             const int n0 = t.n0 + rank * Sh::kMine, boxes = boxes_from(n0);
             // of a pair, the first CTA's barrier counts both CTAs' bytes
-            const uint32_t bytes = (kPair ? 2 : 1) * (a.perm ? 0 : Sh::kA) + (boxes + (kPair ? boxes_from(t.n0 + Sh::kMine) : 0)) * Sh::kBoxB;
+            const uint32_t bytes = (kPair ? 2 : 1) * (a.gather ? 0 : Sh::kA) + (boxes + (kPair ? boxes_from(t.n0 + Sh::kMine) : 0)) * Sh::kBoxB;
             for (int k = 0; k < nk; ++k, ++issued, pos.next()) {
                 bounded_wait_on(set.empty + 8 * pos.stage, pos.phase ^ 1, dead);
                 if (is_dead(dead)) break;
                 const uint32_t at = smem_u32(ring) + pos.stage * Sh::kStage, bt = at + Sh::kA;
                 const uint32_t bar = full + 8 * pos.stage;
                 if (rank == 0) expect_bytes(set.full + 8 * pos.stage, bytes);
-                if (!a.perm) tma_2d<kPair>(at, &a_map, k * kBox, t.p0 + kTileM * rank, bar);
+                if (!a.gather) tma_2d<kPair>(at, &a_map, k * kBox, t.p0 + kTileM * rank, bar);
                 for (int i = 0; i < boxes; ++i) {
                     if (kMN) tma_3d<kPair>(bt + i * Sh::kBoxB, &w_map, n0 + i * kBoxMN, k * kBox, t.g, bar);
                     else tma_3d<kPair>(bt, &w_map, k * kBox, n0, t.g, bar);
@@ -142,24 +143,24 @@ rows_mma(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUte
         if (is_dead(dead) && rank == 0) set.drain_copies(issued);
         if (kPair)   // the last arrivals from the first CTA's products
             for (int i = 0; i < S; ++i, pos.next()) bounded_wait_on<true>(set.empty + 8 * pos.stage, pos.phase ^ 1, dead);
-    } else if (warp >= 4 + kEpilogueWarps) {
+    } else if (!kPair && warp >= 4 + kEpilogueWarps) {
         const int w = (warp - 4 - kEpilogueWarps) % kLoaderWarps;
         constexpr int kPerA = kTileM / kLoaderWarps;
         RingPos<S> pos;
         Item u;
         auto row_of = [&](const Item& x) {   // lane i (and 16 + i): the row of tile row kPerA w + i
-            const int p = x.p0 + kTileM * rank + kPerA * w + (lane & 15);
-            return p < x.p1 ? row_at(a, p) : -1;
+            const int p = x.p0 + kPerA * w + (lane & 15);
+            return p < x.p1 ? row_at(a.gather, a.M, p) : -1;
         };
-        bool have = (!kTma || a.perm) && next_product(a, gr, item, step, BN, t);
+        bool have = (!kTma || a.gather) && next_product(a, gr, item, step, BN, t);
         int row = have ? row_of(t) : -1;
         if constexpr (kTma) {
-            Copies<S, kPair> copies;
+            Copies<S> copies;
             while (have && !is_dead(dead)) {
                 const bool more = next_product(a, gr, item, step, BN, u);
                 const int row_next = more ? row_of(u) : -1;
                 for (int k = 0; k < nk; ++k) {
-                    if (!copies.acquire(full, set.empty, dead)) break;
+                    if (!copies.acquire(set.full, set.empty, dead)) break;
                     copy_rows<kTileM>(smem_u32(ring) + copies.next.stage * Sh::kStage, a.a, row, k * kBox, w, lane);
                     copies.issued();
                 }
@@ -167,7 +168,7 @@ rows_mma(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUte
                 row = row_next;
                 have = more;
             }
-            copies.finish(full);
+            copies.finish(set.full);
         } else {
             // two groups of warps take the stages in turn; while one stage of a group is turned, its next is copied
             // (rows that are not aligned take the room of both)
@@ -258,7 +259,7 @@ rows_mma(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUte
         int n = 0;
         while (!is_dead(dead) && next_item(a, gr, item, step, BN, t)) {
             const int p = t.p0 + kTileM * rank + 32 * q + lane;
-            const int r = p < t.p1 ? row_at(a, p) : -1;
+            const int r = p < t.p1 ? row_at(a.perm, a.M, p) : -1;
             T* row = r >= 0 ? static_cast<T*>(a.out) + r * a.out_ld + t.n0 : nullptr;
             const int c0 = half * kCols, c1 = imin(c0 + kCols, a.cols - t.n0);
             if (t.g == a.G) {
@@ -325,7 +326,11 @@ zs_status launch_rows(const char* fn, RowsArgs a, cudaStream_t s) {
     return check_launch(fn);
 }
 
-// Rows of an average group from which on two CTAs share the weights of a tile.
+// Rows of an average group from which on two CTAs form a tile of 256 rows, each
+// with half of its weights, where the rows are in order: 32768 bf16 rows, 1024 ->
+// 1024, 8 groups 52 us and 55 alone, 16 groups 52 and 61, 1024 -> 4096 170 and
+// 192.  Gathered rows are limited by the copies of their own (1024 -> 1024: 94 and
+// 83), short groups by tiles that are mostly empty (256 rows: 50 and 40).
 constexpr int kPairRows = 512;
 
 template <typename T, bool kTma, bool kMN>
@@ -334,7 +339,7 @@ zs_status launch_rows(const char* fn, const RowsArgs& a, cudaStream_t s) {
         if (a.cols <= 32) return launch_rows<T, kTma, kMN, 32>(fn, a, s);
     if constexpr (kTma)
         if (a.cols > 64 && (a.cols + 127) / 128 % 2 == 0)
-            return a.M >= kPairRows * (int64_t)a.G ? launch_rows<T, kTma, kMN, 256, true>(fn, a, s) : launch_rows<T, kTma, kMN, 256>(fn, a, s);
+            return !a.gather && a.M >= kPairRows * (int64_t)a.G ? launch_rows<T, kTma, kMN, 256, true>(fn, a, s) : launch_rows<T, kTma, kMN, 256>(fn, a, s);
     if constexpr (sizeof(T) == 2)
         if (a.cols > 64) return launch_rows<T, kTma, kMN, 128>(fn, a, s);
     return launch_rows<T, kTma, kMN, 64>(fn, a, s);
@@ -354,7 +359,7 @@ cudaError_t set_timeout_flag_grouped_rows(unsigned int* flag) { return set_timeo
 
 // rows x_ld apart, rows of K weights w_ld apart; transposed: the gradient.
 zs_status grouped_rows(const char* fn, int32_t dtype, const void* x, int64_t x_ld, const void* w, int64_t w_ld, const int32_t* row_ptr,
-                       const int32_t* perm, int64_t M, int32_t K, int32_t N, int32_t G, void* out, int64_t out_ld,
+                       const int32_t* perm, const int32_t* gather, int64_t M, int32_t K, int32_t N, int32_t G, void* out, int64_t out_ld,
                        bool transposed, cudaStream_t s) {
     const int es = dtype_bytes(dtype), per16 = 16 / es;
     auto at = [&](const void* p, int bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; };
@@ -366,6 +371,7 @@ zs_status grouped_rows(const char* fn, int32_t dtype, const void* x, int64_t x_l
     a.w_group = w_ld * N;
     a.row_ptr = row_ptr;
     a.perm = perm;
+    a.gather = gather;
     a.out = out;
     a.out_ld = out_ld;
     a.out_wide = at(out, 16) && out_ld % per16 == 0 && a.cols % per16 == 0;

@@ -120,9 +120,8 @@ __device__ __forceinline__ uint32_t in_first(uint32_t at) {
     asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(there) : "r"(at));
     return there;
 }
-// At a barrier of the cluster.  (What is told of lies in this CTA's shared
-// memory, complete and fenced for the tensor cores before, or has been read from
-// TMEM; released to the whole cluster, each arrival took about 700 cycles.)
+// At a barrier of the cluster.  (What is told of has been read from TMEM, nothing
+// written; released to the whole cluster, an arrival took about 700 cycles.)
 __device__ __forceinline__ void mbar_arrive_there(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" :: "r"(bar) : "memory");
 }
@@ -608,8 +607,7 @@ __device__ __forceinline__ void add_chunk(uint32_t from, int apart, float (&acc)
 
 // The copies of a loader warp that are on their way, told of (an arrival at the
 // stage's full barrier) as they land.
-// kPair: the full barriers are the first CTA's.
-template <int S, bool kPair = false>
+template <int S>
 struct Copies {
     RingPos<S> next, told;
     int ahead = 0;      // stages copied and not told of
@@ -627,10 +625,7 @@ struct Copies {
         }
         fence_async_smem();
         __syncwarp();
-        if ((threadIdx.x & 31) == 0) {
-            if (kPair) mbar_arrive_there(full + 8 * told.stage);
-            else mbar_arrive(full + 8 * told.stage);
-        }
+        if ((threadIdx.x & 31) == 0) mbar_arrive(full + 8 * told.stage);
         told.next();
     }
     // The next stage is free; while it is not, older ones are told of.

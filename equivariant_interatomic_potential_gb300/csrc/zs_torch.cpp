@@ -20,6 +20,7 @@ decltype(&zs_grouped_matmul_ws) f_matmul;
 decltype(&zs_grouped_matmul_dx_ws) f_dx;
 decltype(&zs_grouped_matmul_workspace_bytes) f_matmul_bytes;
 decltype(&zs_grouped_matmul_dw_workspace_bytes) f_dw_bytes;
+decltype(&zs_grouped_matmul_dw_copy_bytes) f_dw_copy;
 decltype(&zs_grouped_matmul_dw) f_dw;
 decltype(&zs_norm_gate_residual) f_norm;
 decltype(&zs_norm_gate_residual_backward_workspace_bytes) f_norm_bytes;
@@ -68,6 +69,9 @@ PyObject* guarded(F&& f) {
     }
 }
 
+// Whether rows of K or of N elements are not whole 16-byte pieces.
+bool odd(int d, int64_t K, int64_t N) { return (K | N) & (d == 0 ? 3 : 7); }
+
 // (rows, w, row_ptr, perm, transposed) -> y or dx
 PyObject* matmul(PyObject*, PyObject* const* args, Py_ssize_t n) {
     return guarded([&]() -> PyObject* {
@@ -83,7 +87,7 @@ PyObject* matmul(PyObject*, PyObject* const* args, Py_ssize_t n) {
             (args[3] != Py_None && !is_array(perm, at::kInt, M)) || (K | N | G) >> 31)
             return not_here();
         at::Tensor out = make({M, t ? K : N}, *x, type), ws;
-        const size_t bytes = f_matmul_bytes(d, M, (int32_t)K, (int32_t)N, (int32_t)G);
+        const size_t bytes = perm || odd(d, K, N) ? f_matmul_bytes(d, M, (int32_t)K, (int32_t)N, (int32_t)G) : 0;
         if (bytes) ws = make({(int64_t)bytes}, *x, at::kByte);
         const int32_t* pp = perm ? static_cast<const int32_t*>(perm->const_data_ptr()) : nullptr;
         const int st = (t ? f_dx : f_matmul)(d, x->const_data_ptr(), t ? N : K, w->const_data_ptr(),
@@ -109,7 +113,8 @@ PyObject* dw(PyObject*, PyObject* const* args, Py_ssize_t n) {
             (args[3] != Py_None && !is_array(perm, at::kInt, M)) || (K | N | G) >> 31)
             return not_here();
         at::Tensor out = make({G, N, K}, *x, type), ws;
-        const size_t bytes = f_dw_bytes(d, M, (int32_t)K, (int32_t)N, (int32_t)G);
+        const size_t bytes = f_dw_bytes(d, M, (int32_t)K, (int32_t)N, (int32_t)G) +
+                             (perm || odd(d, K, N) ? f_dw_copy(d, M, (int32_t)K, (int32_t)N, (int32_t)G) : 0);
         if (bytes) ws = make({(int64_t)bytes}, *x, at::kByte);
         const int32_t* pp = perm ? static_cast<const int32_t*>(perm->const_data_ptr()) : nullptr;
         const int st = f_dw(d, dy->const_data_ptr(), N, x->const_data_ptr(), K,
@@ -208,6 +213,7 @@ PyObject* bind(PyObject*, PyObject* args) {
     f_dx = reinterpret_cast<decltype(f_dx)>(get("zs_grouped_matmul_dx_ws"));
     f_matmul_bytes = reinterpret_cast<decltype(f_matmul_bytes)>(get("zs_grouped_matmul_workspace_bytes"));
     f_dw_bytes = reinterpret_cast<decltype(f_dw_bytes)>(get("zs_grouped_matmul_dw_workspace_bytes"));
+    f_dw_copy = reinterpret_cast<decltype(f_dw_copy)>(get("zs_grouped_matmul_dw_copy_bytes"));
     f_dw = reinterpret_cast<decltype(f_dw)>(get("zs_grouped_matmul_dw"));
     f_norm = reinterpret_cast<decltype(f_norm)>(get("zs_norm_gate_residual"));
     f_norm_bytes = reinterpret_cast<decltype(f_norm_bytes)>(get("zs_norm_gate_residual_backward_workspace_bytes"));

@@ -96,6 +96,8 @@ def load(build_if_missing: bool = True):
             fn.argtypes = [I32, P, I64, P, P, P, I64, I32, I32, I32, P, I64, P, SZ, P]
         lib.zs_grouped_matmul_dw_workspace_bytes.restype = SZ
         lib.zs_grouped_matmul_dw_workspace_bytes.argtypes = [I32, I64, I32, I32, I32]
+        lib.zs_grouped_matmul_dw_copy_bytes.restype = SZ
+        lib.zs_grouped_matmul_dw_copy_bytes.argtypes = [I32, I64, I32, I32, I32]
         lib.zs_grouped_matmul_dw.restype = ctypes.c_int
         lib.zs_grouped_matmul_dw.argtypes = [I32, P, I64, P, I64, P, P, I64, I32, I32, I32, P, P, SZ, P]
         lib.zs_norm_gate_residual.restype = ctypes.c_int
@@ -551,6 +553,11 @@ def _groups(w: torch.Tensor, row_ptr: torch.Tensor, perm: torch.Tensor | None, M
             None if perm is None else _array(perm, "perm", torch.int32, (M,)))
 
 
+def _copies(w, perm):
+    """Whether grouped products may lay out operands of weights like w anew."""
+    return perm is not None or ((w.shape[1] | w.shape[2]) * w.element_size()) % 16 != 0
+
+
 def zs_grouped_matmul(x: torch.Tensor, w: torch.Tensor, row_ptr: torch.Tensor, perm: torch.Tensor | None = None,
                       out=None, stream=None) -> torch.Tensor:
     """y[i] = w[g(i)] x[i] for rows grouped by the CSR (row_ptr, perm); perm None: rows
@@ -570,7 +577,7 @@ def zs_grouped_matmul(x: torch.Tensor, w: torch.Tensor, row_ptr: torch.Tensor, p
     else:
         out_ld = _matrix(out, "out", dt, M, N)
     lib = load()
-    wbytes = lib.zs_grouped_matmul_workspace_bytes(d, M, K, N, G)
+    wbytes = lib.zs_grouped_matmul_workspace_bytes(d, M, K, N, G) if _copies(w, perm) else 0
     workspace = _workspace(wbytes, w.device)
     st = lib.zs_grouped_matmul_ws(d, x.data_ptr(), x_ld, wp, rp, pp, M, K, N, G, out.data_ptr(), out_ld, _ptr(workspace), wbytes,
                                 _stream(stream))
@@ -596,7 +603,7 @@ def zs_grouped_matmul_dx(dy: torch.Tensor, w: torch.Tensor, row_ptr: torch.Tenso
     else:
         out_ld = _matrix(out, "out", dt, M, K)
     lib = load()
-    wbytes = lib.zs_grouped_matmul_workspace_bytes(d, M, K, N, G)
+    wbytes = lib.zs_grouped_matmul_workspace_bytes(d, M, K, N, G) if _copies(w, perm) else 0
     workspace = _workspace(wbytes, w.device)
     st = lib.zs_grouped_matmul_dx_ws(d, dy.data_ptr(), dy_ld, wp, rp, pp, M, K, N, G, out.data_ptr(), out_ld, _ptr(workspace), wbytes,
                                    _stream(stream))
@@ -631,6 +638,8 @@ def zs_grouped_matmul_dw(dy: torch.Tensor, x: torch.Tensor, row_ptr: torch.Tenso
     lib = load()
     if workspace is None:
         wbytes = lib.zs_grouped_matmul_dw_workspace_bytes(d, M, K, N, G)
+        if _copies(out, perm):
+            wbytes += lib.zs_grouped_matmul_dw_copy_bytes(d, M, K, N, G)
         if wbytes:
             workspace = torch.empty(wbytes, dtype=torch.uint8, device=dev)
     else:

@@ -366,13 +366,12 @@ ZS_API zs_status zs_grouped_matmul_dx(int32_t dtype, const void* dy, int64_t dy_
 
 /*
  * The two above with a workspace, in which rows that do not start on 16-byte
- * boundaries (odd K or N, views at odd offsets) are laid out anew before the
- * products: twice to four times as fast for such operands from a few hundred
- * rows on.  Same results.
- *   workspace  zs_grouped_matmul_workspace_bytes(dtype, M, K, N, G) bytes (0
- *              where rows of K and of N elements are whole 16-byte pieces),
- *              256-byte aligned; its contents need not start at zero.  A
- *              smaller one, or NULL, is not used.
+ * boundaries (odd K or N, views at odd offsets), and 16-bit rows that perm
+ * gathers for 1280 columns or more, are laid out anew before the products: up to
+ * four times as fast for the former from a few hundred rows on.  Same results.
+ *   workspace  zs_grouped_matmul_workspace_bytes(dtype, M, K, N, G) bytes,
+ *              256-byte aligned; its contents need not start at zero.  What
+ *              does not fit, or NULL, is not used.
  */
 ZS_API size_t zs_grouped_matmul_workspace_bytes(int32_t dtype, int64_t M, int32_t K, int32_t N, int32_t G);
 ZS_API zs_status zs_grouped_matmul_ws(int32_t dtype, const void* x, int64_t x_ld, const void* w,
@@ -392,9 +391,13 @@ ZS_API zs_status zs_grouped_matmul_dx_ws(int32_t dtype, const void* dy, int64_t 
  *   dw (G, N, K)  contiguous, of the operands' type, fully written (a group
  *                 without rows gets zeros)
  *   workspace     zs_grouped_matmul_dw_workspace_bytes(dtype, M, K, N, G)
- *                 bytes, 256-byte aligned; its contents need not start at zero
+ *                 bytes at least, 256-byte aligned; its contents need not start
+ *                 at zero.  Where it has zs_grouped_matmul_dw_copy_bytes() more,
+ *                 operands are laid out anew as above (for gathered rows: of 16
+ *                 tiles of 128 x 256 weights or more).
  */
 ZS_API size_t zs_grouped_matmul_dw_workspace_bytes(int32_t dtype, int64_t M, int32_t K, int32_t N, int32_t G);
+ZS_API size_t zs_grouped_matmul_dw_copy_bytes(int32_t dtype, int64_t M, int32_t K, int32_t N, int32_t G);
 ZS_API zs_status zs_grouped_matmul_dw(int32_t dtype, const void* dy, int64_t dy_ld, const void* x, int64_t x_ld,
                                       const int32_t* row_ptr, const int32_t* perm,
                                       int64_t M, int32_t K, int32_t N, int32_t G,

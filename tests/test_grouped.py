@@ -400,3 +400,25 @@ def test_tiles_of_two_ctas(M, K, N, G, sizes, ordered, dtype):
     if ordered:
         group = np.sort(group)
     check_all(group, t, d, dtype, ordered=ordered)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("M,K,N,G", [(900, 72, 1300, 5), (900, 1288, 136, 3), (700, 1031, 1029, 2), (1300, 520, 1024, 4), (256, 1024, 1320, 1)])
+def test_gathered_rows_put_in_order(M, K, N, G, dtype):
+    # rows of no group, and one row of values that are not finite, which reach nothing beyond it and its group
+    group, t, d = draw(M, K, N, G, dtype, M + K, "zipf", bad=0.1)
+    x, w, dy = (a.clone() for a in t)
+    sick = int(np.flatnonzero(group == 0)[0])
+    x[sick], dy[sick] = float("nan"), float("inf")
+    none = torch.from_numpy(group >= G)
+    x[none], dy[none] = float("nan"), float("nan")
+    y, dx, dw = run(group, G, x.cuda(), w.cuda(), dy.cuda())
+    ry, ay, rdx, adx, rdw, adw = grouped(d[0], d[1], group, d[2])
+    keep = np.arange(M) != sick
+    close(y[keep], ry[keep], ay[keep], dtype, "y")
+    close(dx[keep], rdx[keep], adx[keep], dtype, "dx")
+    close(dw[1:], rdw[1:], adw[1:], dtype, "dw")
+    assert not bool(torch.isfinite(y[sick]).any()) and not bool(torch.isfinite(dw[0]).any())
+    assert all(torch.equal(torch.nan_to_num(a), torch.nan_to_num(b))
+               for a, b in zip(run(group, G, x.cuda(), w.cuda(), dy.cuda()), (y, dx, dw)))
