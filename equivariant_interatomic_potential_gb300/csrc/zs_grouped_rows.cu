@@ -333,13 +333,27 @@ zs_status launch_rows(const char* fn, RowsArgs a, cudaStream_t s) {
 // 83), short groups by tiles that are mostly empty (256 rows: 50 and 40).
 constexpr int kPairRows = 512;
 
+// Whether tiles of 64 columns leave the SMs busier than wider ones: few tiles take few rounds, whose length is that of a
+// tile's copies and epilogue (about its columns and kTileCost more) as long as the sums are short.  2048 bf16 rows, 256 ->
+// 256: 6.6 us and 8.4; 1000 fp16 rows, 131 -> 131: 8.1 and 10.1; but 160 rows, sums of 3760, 784 columns: 77 and 64.
+constexpr int kTileCost = 96, kShortSum = 512;
+bool narrow_tiles(const RowsArgs& a, int bn) {
+    if (a.red > kShortSum) return false;
+    const int64_t rows = a.M / kTileM + imin(a.G, a.M);   // tiles of rows, at most
+    auto cost = [&](int n) { return (rows * ((a.cols + n - 1) / n) + num_sms() - 1) / num_sms() * (n + kTileCost); };
+    return 4 * cost(64) <= 3 * cost(bn);
+}
+
 template <typename T, bool kTma, bool kMN>
 zs_status launch_rows(const char* fn, const RowsArgs& a, cudaStream_t s) {
     if constexpr (!kMN || sizeof(T) == 2)   // an MN-major plane of fp32 is a box wide
         if (a.cols <= 32) return launch_rows<T, kTma, kMN, 32>(fn, a, s);
-    if constexpr (kTma)
-        if (a.cols > 64 && (a.cols + 127) / 128 % 2 == 0)
+    if constexpr (kTma) {
+        const bool even = (a.cols + 127) / 128 % 2 == 0;
+        if (a.cols > 64 && narrow_tiles(a, even ? 256 : 128)) return launch_rows<T, kTma, kMN, 64>(fn, a, s);
+        if (a.cols > 64 && even)
             return !a.gather && a.M >= kPairRows * (int64_t)a.G ? launch_rows<T, kTma, kMN, 256, true>(fn, a, s) : launch_rows<T, kTma, kMN, 256>(fn, a, s);
+    }
     if constexpr (sizeof(T) == 2)
         if (a.cols > 64) return launch_rows<T, kTma, kMN, 128>(fn, a, s);
     return launch_rows<T, kTma, kMN, 64>(fn, a, s);
