@@ -281,7 +281,7 @@ zs_status grouped_small_weights(const char* fn, const WeightArgs& a, int ctas, c
     launch(small_weights, dim3(ctas), dim3(kThreads), 0, s, a);
     if (zs_status st = check_launch(fn)) return st;
     if (ctas > 1) {
-        launch(weights_join<float, kMost>, dim3(ctas - 1, kMost / kPartRows), dim3(256), 0, s, a);
+        launch(weights_join<float, kMost>, dim3((a.cuts + kNotes - 1) / kNotes, kMost / kPartRows), dim3(256), 0, s, a);
         return check_launch(fn);
     }
     return ZS_OK;

@@ -9,7 +9,7 @@
 // kernel adds, for each group that was cut, its CTAs' parts in order.  Which
 // ones they are the first kernel notes down (note_join): to find it anew in
 // each block of the second was a chain of loads that took it 5 us
-// more (45000 rows, 256 x 256 bf16 weights).
+// more (32768 rows of 89 groups, 256 x 256 bf16 weights).
 #pragma once
 
 #include "zs_mma.cuh"
@@ -36,6 +36,7 @@ struct WeightArgs {
     void* dw;
     float* partial;      // [CTA][2][128][BN]
     JoinTile* joins;     // [CTA]
+    int cuts;            // ranges that end before the units do
     bool dw_wide;
     int M, G, N, K;
     int ktiles;
@@ -106,14 +107,11 @@ __device__ __forceinline__ void note_join(const WeightArgs& a, const WeightGroup
     if ((threadIdx.x & 31) == 0 && blockIdx.x + 1 < gridDim.x) a.joins[blockIdx.x] = j;
 }
 
-// Block (x, y): the group whose first part CTA x formed, if it was cut; rows
-// y * kPartRows .. of its tile, 4 columns a thread.
+// Adds the parts of a group that is cut, the first one formed by CTA `first`:
+// rows y * kPartRows .. of its tile, 4 columns a thread.
 template <typename T, int BN>
-__global__ void __launch_bounds__(256) weights_join(const WeightArgs a) {
-    pdl_wait();
-    pdl_trigger();
-    const int4 note = __ldg(reinterpret_cast<const int4*>(a.joins) + blockIdx.x);
-    const int g = note.x, t = note.y, first = blockIdx.x, last = note.z, first_part = note.w;
+__device__ __forceinline__ void join_tile(const WeightArgs& a, int4 note, int first) {
+    const int g = note.x, t = note.y, last = note.z, first_part = note.w;
     if (g < 0) return;
     const int n0 = t / a.ktiles * kTileM + blockIdx.y * kPartRows, k0 = t % a.ktiles * BN;
     const int cols = imin(BN, a.K - k0), rows = imin(kPartRows, a.N - n0);
@@ -136,14 +134,33 @@ __global__ void __launch_bounds__(256) weights_join(const WeightArgs a) {
     }
     sums[threadIdx.x] = sum;
     __syncthreads();
-    if (share > 0 || !in) return;
+    if (share == 0 && in) {
 #pragma unroll
-    for (int i = 1; i < kShares; ++i) sum = f4_add(sum, sums[i * kItems + item]);
-    T* out = static_cast<T*>(a.dw) + ((int64_t)g * a.N + n0 + r) * a.K + k0 + c;
-    const float v[4] = {sum.x, sum.y, sum.z, sum.w};
+        for (int i = 1; i < kShares; ++i) sum = f4_add(sum, sums[i * kItems + item]);
+        T* out = static_cast<T*>(a.dw) + ((int64_t)g * a.N + n0 + r) * a.K + k0 + c;
+        const float v[4] = {sum.x, sum.y, sum.z, sum.w};
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-        if (c + j < cols) out[j] = from_f32<T>(v[j]);
+        for (int j = 0; j < 4; ++j)
+            if (c + j < cols) out[j] = from_f32<T>(v[j]);
+    }
+    __syncthreads();   // sums
+}
+
+// Block (x, y): what was cut of which one of CTAs kNotes x .. formed the first
+// part (often nothing: a block that only looks and leaves takes its time too).
+constexpr int kNotes = 4;
+template <typename T, int BN>
+__global__ void __launch_bounds__(256) weights_join(const WeightArgs a) {
+    pdl_wait();
+    pdl_trigger();
+    int4 notes[kNotes];
+#pragma unroll
+    for (int i = 0; i < kNotes; ++i) {
+        const int x = blockIdx.x * kNotes + i;
+        notes[i] = x < a.cuts ? __ldg(reinterpret_cast<const int4*>(a.joins) + x) : make_int4(-1, 0, 0, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < kNotes; ++i) join_tile<T, BN>(a, notes[i], blockIdx.x * kNotes + i);
 }
 
 // The gradient in fp32 where grouped_is_small() (zs_grouped_small.cu): one tile of 32 columns.

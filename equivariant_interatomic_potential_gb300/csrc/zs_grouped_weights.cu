@@ -292,7 +292,7 @@ zs_status launch_weights(const char* fn, WeightArgs a, const WeightPlan& p, cuda
     launch(weights_mma<T, kTma, BN>, dim3(p.ctas), dim3(Sh::kThreads), Sh::kSmem, s, dy_map, x_map, a);
     if (zs_status st = check_launch(fn)) return st;
     if (p.ctas > 1) {
-        launch(weights_join<T, BN>, dim3(p.ctas - 1, kTileM / kPartRows), dim3(256), 0, s, a);
+        launch(weights_join<T, BN>, dim3((a.cuts + kNotes - 1) / kNotes, kTileM / kPartRows), dim3(256), 0, s, a);
         return check_launch(fn);
     }
     return ZS_OK;
@@ -338,6 +338,7 @@ zs_status grouped_weights(const char* fn, int32_t dtype, const void* dy, int64_t
     a.perm = perm;
     a.dw = dw;
     a.partial = static_cast<float*>(workspace);
+    a.cuts = p.ctas - 1;
     a.joins = reinterpret_cast<JoinTile*>(a.partial + (int64_t)p.ctas * 2 * kTileM * p.bn);
     a.dw_wide = at(dw, 16) && K % per16 == 0;
     a.M = (int)M, a.G = G, a.N = N, a.K = K;

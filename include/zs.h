@@ -343,11 +343,13 @@ typedef enum zs_dtype {
  *   x (M, K)         rows x_ld elements apart (x_ld >= K)
  *   w (G, N, K)      contiguous
  *   row_ptr (G+1,)   group g owns positions [row_ptr[g], row_ptr[g+1])
- *   perm (M,)        row at each position; NULL: position p is row p
+ *   perm (M,)        row at each position, each row once as zs_build_csr
+ *                    gives them; NULL: position p is row p
  *   y (M, N)         rows y_ld elements apart (y_ld >= N), fully written:
  *                    rows at positions >= row_ptr[G] (no group) are zeros
  * M < 2^31, any K >= 1, N >= 1, G >= 0.  Values outside a row's own group
- * never reach its result.
+ * never reach its result.  Sums are in fp32 in a fixed order for given sizes;
+ * an fp32 value that is not finite gives NaN in the results that it reaches.
  */
 ZS_API zs_status zs_grouped_matmul(int32_t dtype, const void* x, int64_t x_ld, const void* w,
                                    const int32_t* row_ptr, const int32_t* perm,
@@ -423,7 +425,7 @@ typedef enum zs_norm_kind {
  *   y, u (M, C)  contiguous, fully written
  *   stats (M, 4) fp32, may be NULL: mean and 1/root of h, then of y (means 0
  *                for ZS_NORM_RMS); what the backward reads; 16-byte aligned
- * 1 <= C <= 16384 (else ZS_ERR_UNSUPPORTED), eps >= 0.
+ * 1 <= C <= 8192 (else ZS_ERR_UNSUPPORTED), eps >= 0.
  */
 ZS_API zs_status zs_norm_gate_residual(int32_t dtype, int32_t kind, const void* h, int64_t h_ld,
                                        const void* x, int64_t x_ld, const void* gate, int64_t gate_ld,
