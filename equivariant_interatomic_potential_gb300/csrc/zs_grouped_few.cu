@@ -244,51 +244,64 @@ __global__ void __launch_bounds__(32 * kDxWarps) few_dx(const FewArgs a) {
     }
 }
 
-// dw: a warp takes four rows of dw, its lanes go along K; the rows of the group
-// pass by through shared memory.
-constexpr int kDwRows = 32, kHeld = 16;
+// dw: a warp takes eight rows of dw, its lanes go along K; the rows of the
+// group pass by through shared memory.
+constexpr int kDwWarpRows = 8, kDwRows = 8 * kDwWarpRows, kHeld = 8;
 template <typename T, int V>
-__global__ void __launch_bounds__(256) few_dw(const FewArgs a) {
+__global__ void __launch_bounds__(256) few_dw(const FewArgs a, bool x_wide) {
     constexpr int kCols = 32 * V;
     __shared__ __align__(16) float xs[kHeld][kCols];
-    __shared__ float dys[kHeld][kDwRows];
+    __shared__ __align__(16) float dys[kHeld][kDwRows];
+    __shared__ int rows[kHeld];
     pdl_wait();
     pdl_trigger();
     const int g = blockIdx.z, b = start(a, g), e = start(a, g + 1);
     const int k0 = blockIdx.x * kCols, n0 = blockIdx.y * kDwRows;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    __shared__ int rows[kHeld];
-    float acc[4][V] = {};
+    float acc[kDwWarpRows][V] = {};
     for (int p = b; p < e; p += kHeld) {
         __syncthreads();
         if (threadIdx.x < kHeld) rows[threadIdx.x] = row_at(a, p + threadIdx.x, e);
         __syncthreads();
         const int held = imin(kHeld, e - p);
+        if (V > 1 && x_wide) {
+            for (int i = threadIdx.x; i < held * 32; i += blockDim.x) {
+                const int row = rows[i / 32], k = k0 + i % 32 * V;
+                float f[V] = {};
+                if (row >= 0 && k < a.K) read<T, V>(static_cast<const T*>(a.b) + row * a.b_ld + k, f);
+#pragma unroll
+                for (int j = 0; j < V; ++j) xs[i / 32][i % 32 * V + j] = f[j];
+            }
+        } else {
 #pragma unroll 4
-        for (int i = threadIdx.x; i < held * kCols; i += blockDim.x) {
-            const int row = rows[i / kCols], k = k0 + i % kCols;
-            xs[i / kCols][i % kCols] = row >= 0 && k < a.K ? to_f32(static_cast<const T*>(a.b)[row * a.b_ld + k]) : 0.f;
+            for (int i = threadIdx.x; i < held * kCols; i += blockDim.x) {
+                const int row = rows[i / kCols], k = k0 + i % kCols;
+                xs[i / kCols][i % kCols] = row >= 0 && k < a.K ? to_f32(static_cast<const T*>(a.b)[row * a.b_ld + k]) : 0.f;
+            }
         }
+#pragma unroll 2
         for (int i = threadIdx.x; i < held * kDwRows; i += blockDim.x) {
             const int row = rows[i / kDwRows], n = n0 + i % kDwRows;
             dys[i / kDwRows][i % kDwRows] = row >= 0 && n < a.N ? to_f32(static_cast<const T*>(a.a)[row * a.a_ld + n]) : 0.f;
         }
         __syncthreads();
-        for (int r = 0; r < imin(kHeld, e - p); ++r) {
-            float x[V];
+        for (int r = 0; r < held; ++r) {
+            float x[V], d[kDwWarpRows];
 #pragma unroll
             for (int j = 0; j < V; ++j) x[j] = xs[r][lane * V + j];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < kDwWarpRows; ++i) d[i] = dys[r][kDwWarpRows * warp + i];
 #pragma unroll
-                for (int j = 0; j < V; ++j) acc[i][j] = fmaf(dys[r][4 * warp + i], x[j], acc[i][j]);
+            for (int i = 0; i < kDwWarpRows; ++i)
+#pragma unroll
+                for (int j = 0; j < V; ++j) acc[i][j] = fmaf(d[i], x[j], acc[i][j]);
         }
     }
     const int k = k0 + lane * V;
     if (k >= a.K) return;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int n = n0 + 4 * warp + i;
+    for (int i = 0; i < kDwWarpRows; ++i) {
+        const int n = n0 + kDwWarpRows * warp + i;
         if (n >= a.N) break;
         T* out = static_cast<T*>(a.out) + ((int64_t)g * a.N + n) * a.K + k;
         if constexpr (V == 1) out[0] = from_f32<T>(acc[i][0]);
@@ -319,7 +332,8 @@ zs_status launch_few(const char* fn, const FewArgs& a, int which, cudaStream_t s
         cfg.numAttrs = ctas > 1 ? 2 : 1;
         cudaLaunchKernelEx(&cfg, few_dx<T, V>, a);
     } else {
-        launch(few_dw<T, V>, dim3(up(a.K, 32 * V), up(a.N, kDwRows), a.G), dim3(256), 0, s, a);
+        launch(few_dw<T, V>, dim3(up(a.K, 32 * V), up(a.N, kDwRows), a.G), dim3(256), 0, s, a,
+               aligned16(a.b) && a.b_ld % kVec<T> == 0);
     }
     return check_launch(fn);
 }
