@@ -148,22 +148,23 @@ __global__ void __launch_bounds__(256) few_forward(const FewArgs a) {
     }
 }
 
-// dx: lanes go along K; the rows of w (the sum's elements) are shared by the
-// warps of a CTA, and by the CTAs of a cluster, which add their parts through
-// distributed shared memory.
+// dx: kLanes lanes go along K; the rows of w (the sum's elements) are shared by
+// the other lanes and the warps of a CTA, and by the CTAs of a cluster, which
+// add their parts through distributed shared memory.  Eight lanes (128 bytes of a
+// row) give four times the CTAs, for one or a few groups.
 constexpr int kDxWarps = 8, kDxCluster = 8;
 __device__ __forceinline__ void cluster_barrier() {
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-template <typename T, int V>
+template <typename T, int V, int kLanes>
 __global__ void __launch_bounds__(32 * kDxWarps) few_dx(const FewArgs a) {
-    constexpr int kCols = 32 * V;
+    constexpr int kCols = kLanes * V, kShares = kDxWarps * (32 / kLanes);   // columns; threads that share them
     __shared__ float dys[kFewRows * kFewChunk];
     __shared__ float sum[kFewRows][kCols];
     __shared__ int rows[kFewRows];
-    float* part = dys;   // [kDxWarps][kCols], once the sums are done
-    static_assert(kDxWarps * kCols <= kFewRows * kFewChunk, "the warps' parts fit");
+    float* part = dys;   // [kShares][kCols], once the sums are done
+    static_assert(kShares * kCols <= kFewRows * kFewChunk, "the parts fit");
     pdl_wait();
     pdl_trigger();
     const int ctas = gridDim.z, rank = blockIdx.z;
@@ -173,7 +174,7 @@ __global__ void __launch_bounds__(32 * kDxWarps) few_dx(const FewArgs a) {
         if (rank == 0) clear_rows<T>(a, b, e, c0, imin(c0 + kCols, a.K));
         return;
     }
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = c0 + lane * V;
+    const int share = threadIdx.x / kLanes, lane = threadIdx.x % kLanes, c = c0 + lane * V;
     const T* w = static_cast<const T*>(a.b) + (int64_t)g * a.N * a.K + c;
     const int per = (a.N + ctas - 1) / ctas, first = rank * per, last = imin(first + per, a.N);
     for (int p = b; p < e; p += kFewRows) {
@@ -189,14 +190,14 @@ __global__ void __launch_bounds__(32 * kDxWarps) few_dx(const FewArgs a) {
                 __syncthreads();
                 if (c < a.K) {
                     constexpr int kAtOnce = 8;   // rows of w on their way
-                    for (int i0 = warp; i0 < n; i0 += kDxWarps * kAtOnce) {
+                    for (int i0 = share; i0 < n; i0 += kShares * kAtOnce) {
                         float f[kAtOnce][V];
 #pragma unroll
                         for (int u = 0; u < kAtOnce; ++u)
-                            read<T, V>(w + (int64_t)(n0 + imin(i0 + u * kDxWarps, n - 1)) * a.K, f[u]);
+                            read<T, V>(w + (int64_t)(n0 + imin(i0 + u * kShares, n - 1)) * a.K, f[u]);
 #pragma unroll
                         for (int u = 0; u < kAtOnce; ++u) {
-                            const int i = i0 + u * kDxWarps;
+                            const int i = i0 + u * kShares;
                             if (i >= n) break;
 #pragma unroll
                             for (int r = 0; r < R; ++r)
@@ -210,12 +211,12 @@ __global__ void __launch_bounds__(32 * kDxWarps) few_dx(const FewArgs a) {
             for (int r = 0; r < R; ++r) {
                 __syncthreads();
 #pragma unroll
-                for (int j = 0; j < V; ++j) part[warp * kCols + lane * V + j] = acc[r][j];
+                for (int j = 0; j < V; ++j) part[share * kCols + lane * V + j] = acc[r][j];
                 __syncthreads();
                 for (int j = threadIdx.x; j < kCols; j += blockDim.x) {
                     float v = 0.f;
 #pragma unroll
-                    for (int i = 0; i < kDxWarps; ++i) v += part[i * kCols + j];
+                    for (int i = 0; i < kShares; ++i) v += part[i * kCols + j];
                     sum[r][j] = v;
                 }
             }
@@ -316,7 +317,8 @@ zs_status launch_few(const char* fn, const FewArgs& a, int which, cudaStream_t s
         launch(few_forward<T, V>, dim3(up(a.N, kFwdCols), a.G + 1), dim3(256), 0, s, a);
     } else if (which == 1) {
         // a cluster shares the sum where there are too few CTAs to read the weights with
-        const unsigned tiles = up(a.K, 32 * V);
+        const bool narrow = (int64_t)up(a.K, 32 * V) * a.G < 304;
+        const unsigned tiles = up(a.K, (narrow ? 8 : 32) * V);
         const unsigned ctas = (int64_t)tiles * a.G < 304 && a.N >= 256 ? kDxCluster : 1;
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(tiles, a.G + 1, ctas);
@@ -330,7 +332,7 @@ zs_status launch_few(const char* fn, const FewArgs& a, int which, cudaStream_t s
         attr[1].val.clusterDim.z = ctas;
         cfg.attrs = attr;
         cfg.numAttrs = ctas > 1 ? 2 : 1;
-        cudaLaunchKernelEx(&cfg, few_dx<T, V>, a);
+        cudaLaunchKernelEx(&cfg, narrow ? few_dx<T, V, 8> : few_dx<T, V, 32>, a);
     } else {
         launch(few_dw<T, V>, dim3(up(a.K, 32 * V), up(a.N, kDwRows), a.G), dim3(256), 0, s, a,
                aligned16(a.b) && a.b_ld % kVec<T> == 0);
