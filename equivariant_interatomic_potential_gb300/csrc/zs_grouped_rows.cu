@@ -107,7 +107,7 @@ rows_mma(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUte
     unsigned char* slots = ring + S * Sh::kStage;
     unsigned char* staging = slots + Sh::kSlots;
     Setup<S, Sh::kTmemCols, Sh::kTile, 1, kPair> set;
-    set.begin(staging + kEpilogueWarps * kStageWarp, !kTma ? kLoaderWarps : a.gather ? 1 + kLoaderWarps : 1, 4 * Sh::kHalves, a.row_ptr, a.G, a.M);
+    set.begin(staging + kEpilogueWarps * kStageWarp, !kTma ? kLoaderWarps : a.gather ? 1 + kCopyWarps : 1, 4 * Sh::kHalves, a.row_ptr, a.G, a.M);
     const RowGroups<Sh::kTile>& gr = set.groups;
     volatile int* dead = set.dead;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -145,23 +145,26 @@ rows_mma(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUte
             for (int i = 0; i < S; ++i, pos.next()) bounded_wait_on<true>(set.empty + 8 * pos.stage, pos.phase ^ 1, dead);
     } else if (!kPair && warp >= 4 + kEpilogueWarps) {
         const int w = (warp - 4 - kEpilogueWarps) % kLoaderWarps;
-        constexpr int kPerA = kTileM / kLoaderWarps;
+        constexpr int kPerA = kTileM / (kTma ? kCopyWarps : kLoaderWarps);
         RingPos<S> pos;
         Item u;
-        auto row_of = [&](const Item& x) {   // lane i (and 16 + i): the row of tile row kPerA w + i
-            const int p = x.p0 + kPerA * w + (lane & 15);
+        auto row_of = [&](const Item& x) {   // lane i (mod kPerA): the row of the warp's tile row i
+            const int p = x.p0 + kPerA * (kTma ? w % kCopyWarps : w) + lane % kPerA;
             return p < x.p1 ? row_at(a.gather, a.M, p) : -1;
         };
         bool have = (!kTma || a.gather) && next_product(a, gr, item, step, BN, t);
         int row = have ? row_of(t) : -1;
         if constexpr (kTma) {
-            Copies<S> copies;
+            const int turn = w / kCopyWarps, mine = w % kCopyWarps;
+            Copies<S> copies(turn);
+            int n = 0;
             while (have && !is_dead(dead)) {
                 const bool more = next_product(a, gr, item, step, BN, u);
                 const int row_next = more ? row_of(u) : -1;
                 for (int k = 0; k < nk; ++k) {
+                    if (n++ % kCopyGroups != turn) continue;
                     if (!copies.acquire(set.full, set.empty, dead)) break;
-                    copy_rows<kTileM>(smem_u32(ring) + copies.next.stage * Sh::kStage, a.a, row, k * kBox, w, lane);
+                    copy_rows<kTileM, kCopyWarps>(smem_u32(ring) + copies.stage() * Sh::kStage, a.a, row, k * kBox, mine, lane);
                     copies.issued();
                 }
                 t = u;

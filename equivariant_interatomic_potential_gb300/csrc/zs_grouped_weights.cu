@@ -45,7 +45,7 @@ weights_mma(const __grid_constant__ CUtensorMap dy_map, const __grid_constant__ 
     unsigned char* staging = slots + Sh::kSlots;
     constexpr int kUnit = Sh::kUnit;
     Setup<S, Sh::kTmemCols, kUnit, kFlush> set;
-    set.begin(staging + kEpilogueWarps * kStageWarp, kTma && !a.perm ? 1 : kLoaderWarps, 4 * Sh::kHalves, a.row_ptr, a.G, a.M);
+    set.begin(staging + kEpilogueWarps * kStageWarp, !kTma ? kLoaderWarps : a.perm ? kCopyWarps : 1, 4 * Sh::kHalves, a.row_ptr, a.G, a.M);
     volatile int* dead = set.dead;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     Walk<T, BN> walk(a, set.groups);
@@ -71,26 +71,29 @@ weights_mma(const __grid_constant__ CUtensorMap dy_map, const __grid_constant__ 
     } else if (warp >= 4 + kEpilogueWarps && (!kTma || a.perm)) {
         const int w = (warp - 4 - kEpilogueWarps) % kLoaderWarps;
         RingPos<S> pos;
-        constexpr int kPer = kUnit / kLoaderWarps;
-        auto row_of = [&](int p) {   // lane i (and 8 j + i) < 8: the row at position p + 8 w + i
-            const int at = p + kPer * w + (lane & (kPer - 1));
+        constexpr int kPer = kUnit / (kTma ? kCopyWarps : kLoaderWarps);
+        auto row_of = [&](int p) {   // lane i (mod kPer): the row at the warp's position i
+            const int at = p + kPer * (kTma ? w % kCopyWarps : w) + lane % kPer;
             return at < s.p1 ? weight_row(a, at) : -1;
         };
         if constexpr (kTma) {
-            Copies<S> copies;
+            const int turn = w / kCopyWarps, part = w % kCopyWarps;
+            Copies<S> copies(turn);
+            int n = 0;
             while (!is_dead(dead) && walk.next(s)) {
                 int row = row_of(s.p0);
                 for (int p = s.p0; p < s.p1; p += kUnit) {
                     const int mine = row;
                     row = row_of(p + kUnit);
+                    if (n++ % kCopyGroups != turn) continue;
                     if (!copies.acquire(set.full, set.empty, dead)) break;
-                    const uint32_t at = smem_u32(ring) + copies.next.stage * Sh::kStage;
+                    const uint32_t at = smem_u32(ring) + copies.stage() * Sh::kStage;
 #pragma unroll
                     for (int i = 0; i < 2; ++i)
-                        if (s.n0 + i * kBoxMN < a.N) copy_rows<kUnit>(at + i * Sh::kBox, a.dy, mine, s.n0 + i * kBoxMN, w, lane);
+                        if (s.n0 + i * kBoxMN < a.N) copy_rows<kUnit, kCopyWarps>(at + i * Sh::kBox, a.dy, mine, s.n0 + i * kBoxMN, part, lane);
 #pragma unroll
                     for (int i = 0; i < Sh::kBBoxes; ++i)
-                        if (s.k0 + i * kBoxMN < a.K) copy_rows<kUnit>(at + Sh::kA + i * Sh::kBox, a.x, mine, s.k0 + i * kBoxMN, w, lane);
+                        if (s.k0 + i * kBoxMN < a.K) copy_rows<kUnit, kCopyWarps>(at + Sh::kA + i * Sh::kBox, a.x, mine, s.k0 + i * kBoxMN, part, lane);
                     copies.issued();
                 }
             }

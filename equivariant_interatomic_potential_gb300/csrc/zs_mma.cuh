@@ -449,9 +449,9 @@ struct BoxParts {
 // copied straight to their places.  (TMA gathers four rows in about 40 cycles,
 // which is 12 bytes a cycle of an SM; this took 75 us where that took 104, for
 // 262144 rows of 256 channels.)
-template <int kRows>
+template <int kRows, int kWarps>
 __device__ __forceinline__ void copy_rows(uint32_t box, const Matrix& m, int rows, int c0, int w, int lane) {
-    constexpr int kPer = kRows / kLoaderWarps;
+    constexpr int kPer = kRows / kWarps;
     const int piece = lane & 7;
     const int c = c0 + 8 * piece;
 #pragma unroll
@@ -606,38 +606,39 @@ __device__ __forceinline__ void add_chunk(uint32_t from, int apart, float (&acc)
 }
 
 // The copies of a loader warp that are on their way, told of (an arrival at the
-// stage's full barrier) as they land.
+// stage's full barrier) as they land.  kCopyGroups groups of warps take the
+// stages in turn: waiting, fencing and telling of one stage is as long as the
+// products of one.
+constexpr int kCopyGroups = 2, kCopyWarps = kLoaderWarps / kCopyGroups;
 template <int S>
 struct Copies {
-    RingPos<S> next, told;
+    int next, told;     // stages, counted from the kernel's start
     int ahead = 0;      // stages copied and not told of
+    __device__ __forceinline__ explicit Copies(int group) : next(group), told(group) {}
+    __device__ __forceinline__ int stage() const { return next % S; }
     // Waits for the oldest stage and tells of it.
     __device__ __forceinline__ void tell(uint32_t full) {
         switch (--ahead) {   // as many newer ones may still be on their way
             case 0: copies_wait<0>(); break;
             case 1: copies_wait<1>(); break;
             case 2: copies_wait<2>(); break;
-            case 3: copies_wait<3>(); break;
-            case 4: copies_wait<4>(); break;
-            case 5: copies_wait<5>(); break;
-            case 6: copies_wait<6>(); break;
-            default: copies_wait<7>(); break;
+            default: copies_wait<3>(); break;
         }
         fence_async_smem();
         __syncwarp();
-        if ((threadIdx.x & 31) == 0) mbar_arrive(full + 8 * told.stage);
-        told.next();
+        if ((threadIdx.x & 31) == 0) mbar_arrive(full + 8 * (told % S));
+        told += kCopyGroups;
     }
     // The next stage is free; while it is not, older ones are told of.
     __device__ __forceinline__ bool acquire(uint32_t full, uint32_t empty, volatile int* dead) {
-        const uint32_t bar = empty + 8 * next.stage, parity = next.phase ^ 1;
+        const uint32_t bar = empty + 8 * stage(), parity = (uint32_t)(next / S & 1) ^ 1;
         while (ahead > 0 && !__all_sync(0xffffffffu, mbar_test(bar, parity))) tell(full);
         return bounded_wait(bar, parity, dead);
     }
     __device__ __forceinline__ void issued() {
         copies_commit();
         ++ahead;
-        next.next();
+        next += kCopyGroups;
     }
     __device__ __forceinline__ void finish(uint32_t full) {
         while (ahead > 0) tell(full);
