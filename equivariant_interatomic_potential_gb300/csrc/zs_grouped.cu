@@ -84,11 +84,11 @@ struct Padder {
     }
 };
 
-// Gathered 16-bit rows are put in order first where enough tiles read them again, and TMA brings them from then on:
-// products of at least kOrderCols columns (32768 bf16 rows, 216 -> 1360: 53 us, 71 gathered by each tile; 512 -> 2048: 75 and
-// 94; 512 -> 1024: 50 and 50; 65536 rows, 256 -> 1024: 67 and 63), weight gradients of at least kOrderTiles tiles (2048 -> 512,
-// 32 tiles: 136 and 242 us; 256 -> 1024, 8 tiles: 111 and 113).  fp32 takes its rows through registers either way.
-constexpr int kOrderCols = 1280, kOrderTiles = 16;
+// Gathered 16-bit rows are put in order first where many tiles read them again, and TMA brings them from then on (32768 bf16
+// rows, us so and gathered by each tile): products of at least kOrderCols columns (216 -> 1360: 55 and 66; 512 -> 2048: 74 and
+// 77; 1024 -> 4096: 200 and 238; but 256 -> 1024, 65536 rows: 67 and 58), weight gradients of at least kOrderTiles tiles
+// (1024 -> 4096, 128 tiles: 350 and 447; 2048 -> 512, 32 tiles: 137 and 128).  fp32 takes its rows through registers either way.
+constexpr int kOrderCols = 1280, kOrderTiles = 64;
 bool order_rows(int32_t dtype, int32_t cols) { return dtype != ZS_F32 && cols >= kOrderCols; }
 bool order_both(int32_t dtype, int32_t K, int32_t N) {
     return dtype != ZS_F32 && (int64_t)((N + 127) / 128) * ((K + 255) / 256) >= kOrderTiles;

@@ -351,13 +351,13 @@ zs_status few(const char* fn, const FewArgs& a, int which, cudaStream_t s) {
 }  // namespace
 
 // Measured against the tensor-core kernels (us, few / tensor): M = 1, 2048 -> 4096 bf16: y 6.5 / 34, dx 7.9 / 59, dw 5.8 / 12;
-// M = 16, 8 groups of 1024 -> 4096 bf16: 22 / 16, 44 / 42, 16 / 32; M = 64: 55 / 16, 82 / 42, 31 / 35; M = 16, one group of
-// 784 -> 3760 bf16: dx 22 / 40; M = 24, two groups of 256 -> 256: dx 12 / 6; M = 24, one group of 143 -> 1264 fp32: 9.9 / 13, 16 / 72, 6 / 9; M = 144, 57 groups of 1680 -> 264 fp32: 84 / 101, 69 / 94, 26 / 91, bf16:
-// 71 / 42, 67 / 19, 20 / 38; M = 512, 89 groups of 256 -> 256 fp32: 54 / 29, 79 / 30, 29 / 25, bf16 dw 34 / 15.
+// M = 8, 3 groups of 264 -> 2000 fp16: y 5.3 / 7.4, dx 6.8 / 23, dw 4.0 / 7.2; M = 16, 8 groups of 1024 -> 4096 bf16: 22 / 14,
+// 45 / 32, 16 / 32; M = 64: 55 / 15, 82 / 32, 31 / 33; M = 24, one group of 143 -> 1264 fp32: 9.9 / 13, 16 / 72, 6 / 9;
+// M = 144, 57 groups of 1680 -> 264 fp32: 84 / 106, 69 / 93, 26 / 91, bf16: 71 / 26, 67 / 15, 20 / 38; M = 512, 89 groups of
+// 256 -> 256 fp32: 54 / 30, 66 / 30, 29 / 25, bf16 dw 34 / 15.
 bool grouped_is_few(int32_t dtype, int which, int64_t M, int32_t N, int32_t G) {
     if (G >= 65535 || N > 65535 * kDwRows) return false;   // of a grid's sides
     if (which == 2) return M <= 32 || M <= 4 * (int64_t)G;
-    if (which == 1 && M <= 2 * kFewRows && N >= 1024) return true;
     return M <= kFewRows || (dtype == ZS_F32 && (M <= 4 * kFewRows || (M <= 256 && M <= 4 * (int64_t)G)));
 }
 

@@ -2,9 +2,14 @@
 // w transposed.  One persistent kernel: warp 0 brings tiles in by TMA, eight
 // more warps copy the rows of a CSR in with cp.async, or two groups of eight
 // read everything where neither can (fp32, which is cut into bf16 planes on
-// the way, and unaligned rows); warp 1
-// issues the products; warps 4 to 11 write finished tiles while the next one
-// is being summed.
+// the way, and unaligned rows); warp 1 issues the products (of a pair of CTAs,
+// the first one's those of both); warps 4 to 11 write finished tiles while the
+// next one is being summed.
+//
+// 32768 bf16 rows in order, 8 groups of 1024 -> 4096: 167 us (1.65 PFLOP/s) and
+// 184 transposed, the tensor cores 70 % active and the power limit reached; 89
+// groups of 256 -> 256, gathered: 19 us, of which the weights' copies take 10 and
+// the results' way out 4 (0.36 of the copy rate); fp32 at a sixth of the rate.
 #include <initializer_list>
 
 #include "zs_grouped.cuh"
@@ -145,36 +150,43 @@ rows_mma(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUte
             for (int i = 0; i < S; ++i, pos.next()) bounded_wait_on<true>(set.empty + 8 * pos.stage, pos.phase ^ 1, dead);
     } else if (!kPair && warp >= 4 + kEpilogueWarps) {
         const int w = (warp - 4 - kEpilogueWarps) % kLoaderWarps;
-        constexpr int kPerA = kTileM / (kTma ? kCopyWarps : kLoaderWarps);
-        RingPos<S> pos;
         Item u;
-        auto row_of = [&](const Item& x) {   // lane i (mod kPerA): the row of the warp's tile row i
-            const int p = x.p0 + kPerA * (kTma ? w % kCopyWarps : w) + lane % kPerA;
+        bool have = (!kTma || a.gather) && next_product(a, gr, item, step, BN, t);
+        auto row_of = [&](const Item& x, int i) {   // of the tile's row i
+            const int p = x.p0 + i;
             return p < x.p1 ? row_at(a.gather, a.M, p) : -1;
         };
-        bool have = (!kTma || a.gather) && next_product(a, gr, item, step, BN, t);
-        int row = have ? row_of(t) : -1;
         if constexpr (kTma) {
-            const int turn = w / kCopyWarps, mine = w % kCopyWarps;
+            constexpr int kPerA = kTileM / kCopyWarps, kPieces = kPerA / 32;   // rows of a warp; a lane holds one of each 32
+            const int turn = w / kCopyWarps, first = w % kCopyWarps * kPerA;
             Copies<S> copies(turn);
-            int n = 0;
+            int n = 0, row[kPieces], row_next[kPieces];
+#pragma unroll
+            for (int i = 0; i < kPieces; ++i) row[i] = have ? row_of(t, first + 32 * i + lane) : -1;
             while (have && !is_dead(dead)) {
                 const bool more = next_product(a, gr, item, step, BN, u);
-                const int row_next = more ? row_of(u) : -1;
+#pragma unroll
+                for (int i = 0; i < kPieces; ++i) row_next[i] = more ? row_of(u, first + 32 * i + lane) : -1;
                 for (int k = 0; k < nk; ++k) {
                     if (n++ % kCopyGroups != turn) continue;
                     if (!copies.acquire(set.full, set.empty, dead)) break;
-                    copy_rows<kTileM, kCopyWarps>(smem_u32(ring) + copies.stage() * Sh::kStage, a.a, row, k * kBox, mine, lane);
+                    const uint32_t at = smem_u32(ring) + copies.stage() * Sh::kStage;
+#pragma unroll
+                    for (int i = 0; i < kPieces; ++i) copy_rows<32>(at, a.a, row[i], k * kBox, first + 32 * i, lane);
                     copies.issued();
                 }
                 t = u;
-                row = row_next;
+#pragma unroll
+                for (int i = 0; i < kPieces; ++i) row[i] = row_next[i];
                 have = more;
             }
             copies.finish(set.full);
         } else {
             // two groups of warps take the stages in turn; while one stage of a group is turned, its next is copied
             // (rows that are not aligned take the room of both)
+            constexpr int kPerA = kTileM / kLoaderWarps;
+            auto lane_row = [&](const Item& x) { return row_of(x, kPerA * w + lane % kPerA); };
+            int row = have ? lane_row(t) : -1;
             const int turn = (warp - 4 - kEpilogueWarps) / kLoaderWarps;
             constexpr uint32_t kStride = 32 * kLoaderWarps * 16;
             const bool aligned = a.a.aligned && a.w.aligned;
@@ -200,7 +212,7 @@ rows_mma(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUte
             int n = 0, copied = 0;
             while (have && !is_dead(dead)) {
                 const bool more = next_product(a, gr, item, step, BN, u);
-                const int row_next = more ? row_of(u) : -1;
+                const int row_next = more ? lane_row(u) : -1;
                 Matrix wm = a.w;
                 wm.p = static_cast<const T*>(wm.p) + t.g * a.w_group;
                 for (int k = 0; k < nk; ++k) {
@@ -332,8 +344,8 @@ zs_status launch_rows(const char* fn, RowsArgs a, cudaStream_t s) {
 // Rows of an average group from which on two CTAs form a tile of 256 rows, each
 // with half of its weights, where the rows are in order: 32768 bf16 rows, 1024 ->
 // 1024, 8 groups 52 us and 55 alone, 16 groups 52 and 61, 1024 -> 4096 170 and
-// 192.  Gathered rows are limited by the copies of their own (1024 -> 1024: 94 and
-// 83), short groups by tiles that are mostly empty (256 rows: 50 and 40).
+// 192.  Gathered rows are limited by copies of their own (1024 -> 1024 94 and 83
+// when that was measured), short groups by tiles that are mostly empty (256 rows: 50 and 40).
 constexpr int kPairRows = 512;
 
 // Whether tiles of 64 columns leave the SMs busier than wider ones: few tiles take few rounds, whose length is that of a

@@ -445,18 +445,18 @@ struct BoxParts {
     }
 };
 
-// kRows rows of a box of 64 columns of a 16-bit matrix with aligned rows,
-// copied straight to their places.  (TMA gathers four rows in about 40 cycles,
+// kPer rows from row0 on of a box of 64 columns of a 16-bit matrix with aligned
+// rows, copied straight to their places; lane i holds the number of the i-th.  (TMA gathers four rows in about 40 cycles,
 // which is 12 bytes a cycle of an SM; this took 75 us where that took 104, for
 // 262144 rows of 256 channels.)
-template <int kRows, int kWarps>
-__device__ __forceinline__ void copy_rows(uint32_t box, const Matrix& m, int rows, int c0, int w, int lane) {
-    constexpr int kPer = kRows / kWarps;
+template <int kPer>
+__device__ __forceinline__ void copy_rows(uint32_t box, const Matrix& m, int rows, int c0, int row0, int lane) {
+    static_assert(kPer <= 32 && kPer % 4 == 0, "a lane holds a row's number");
     const int piece = lane & 7;
     const int c = c0 + 8 * piece;
 #pragma unroll
     for (int i = 0; i < kPer / 4; ++i) {
-        const int at = 4 * i + (lane >> 3), r = __shfl_sync(0xffffffffu, rows, at), row = kPer * w + at;
+        const int at = 4 * i + (lane >> 3), r = __shfl_sync(0xffffffffu, rows, at), row = row0 + at;
         const bool in = r >= 0 && c < m.cols;
         copy16(box + piece_at<64>(row, piece), static_cast<const uint16_t*>(m.p) + (in ? r * m.ld + c : 0),
                in ? imin(m.cols - c, 8) * 2 : 0);
@@ -607,9 +607,10 @@ __device__ __forceinline__ void add_chunk(uint32_t from, int apart, float (&acc)
 
 // The copies of a loader warp that are on their way, told of (an arrival at the
 // stage's full barrier) as they land.  kCopyGroups groups of warps take the
-// stages in turn: waiting, fencing and telling of one stage is as long as the
-// products of one.
-constexpr int kCopyGroups = 2, kCopyWarps = kLoaderWarps / kCopyGroups;
+// stages in turn: waiting, fencing and telling of one stage takes longer than its
+// products (32768 bf16 rows, 1024 -> 1024, us with one, two and four groups:
+// 83, 72 and 66).
+constexpr int kCopyGroups = 4, kCopyWarps = kLoaderWarps / kCopyGroups;
 template <int S>
 struct Copies {
     int next, told;     // stages, counted from the kernel's start

@@ -395,7 +395,7 @@ ZS_API zs_status zs_grouped_matmul_dx_ws(int32_t dtype, const void* dy, int64_t 
  *   workspace     zs_grouped_matmul_dw_workspace_bytes(dtype, M, K, N, G)
  *                 bytes at least, 256-byte aligned; its contents need not start
  *                 at zero.  Where it has zs_grouped_matmul_dw_copy_bytes() more,
- *                 operands are laid out anew as above (for gathered rows: of 16
+ *                 operands are laid out anew as above (for gathered rows: of 64
  *                 tiles of 128 x 256 weights or more).
  */
 ZS_API size_t zs_grouped_matmul_dw_workspace_bytes(int32_t dtype, int64_t M, int32_t K, int32_t N, int32_t G);

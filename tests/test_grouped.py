@@ -404,7 +404,7 @@ def test_tiles_of_two_ctas(M, K, N, G, sizes, ordered, dtype):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
-@pytest.mark.parametrize("M,K,N,G", [(900, 72, 1300, 5), (900, 1288, 136, 3), (700, 1031, 1029, 2), (1300, 520, 1024, 4), (256, 1024, 1320, 1)])
+@pytest.mark.parametrize("M,K,N,G", [(900, 72, 1300, 5), (900, 1288, 136, 3), (700, 1031, 1029, 2), (1300, 520, 1024, 4), (256, 1024, 1320, 1), (300, 2048, 1032, 2)])
 def test_gathered_rows_put_in_order(M, K, N, G, dtype):
     # rows of no group, and one row of values that are not finite, which reach nothing beyond it and its group
     group, t, d = draw(M, K, N, G, dtype, M + K, "zipf", bad=0.1)
