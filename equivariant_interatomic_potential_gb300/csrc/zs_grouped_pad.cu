@@ -4,9 +4,9 @@
 // The tensor-core products take their operands in 16-byte pieces.  Rows of an
 // odd number of elements can be brought into that form as they are loaded, but
 // then once for every tile that reads them; a copy costs one read and one
-// write.  (us with the copy and without, fp16: 32768 rows, 217 -> 1360: y 81 and
-// 192, dx 44 and 251, dw 83 and 226; 1000 rows, 131 -> 131: y 10.6 and 13.3; bf16,
-// 150000 rows, 41 -> 25: y 28.5 and 29.1, dw 41 and 38.  From 256 rows on it is
+// write.  (us with the copy and without, fp16: 32768 rows, 217 -> 1360: y 53 and
+// 192, dx 37 and 251, dw 56 and 226; 1000 rows, 131 -> 131: y 8 and 13; bf16,
+// 150000 rows, 41 -> 25: y 23 and 29, dw 27 and 38.  From 256 rows on it is
 // therefore always made.)  A thread makes a 16-byte piece out of the two aligned
 // ones that hold it, four at a time; 32768 rows of 1363 fp16, 180 MB, take 32 us.
 #include "zs_grouped.cuh"
