@@ -162,8 +162,11 @@ __device__ __forceinline__ bool aligned(const void* p, unsigned a) {
     return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0;
 }
 
+// 8-bit states take 88 instructions an element in long chains (roots, quotients, block maxima), so warps count for more than
+// the few values that spill: 30 M fp32 elements take 109 us with 4 CTAs an SM, 103 with 5, 102 with 6.  32-bit states wait for
+// memory, with more loads a warp on their way (200 M bf16: 628 us as the compiler likes, 714 with 5 CTAs).
 template <typename T, bool kEight, int N>
-__global__ void __launch_bounds__(kThreads) adamw_step(const __grid_constant__ Table<N> table, Consts c,
+__global__ void __launch_bounds__(kThreads, kEight ? 6 : 1) adamw_step(const __grid_constant__ Table<N> table, Consts c,
                                                        const float* __restrict__ grad_scale) {
     pdl_wait();
     pdl_trigger();
