@@ -168,6 +168,24 @@ def _stream(stream) -> int | None:
     return stream.cuda_stream
 
 
+def _on(stream, call, *args, **kw):
+    """call(...) with ``stream`` (a stream object or a handle) current, so that what the call
+    allocates is that stream's: no other stream is handed its workspace while the kernels
+    run.  The results may be used and dropped on the caller's stream too (once it has waited
+    for ``stream``)."""
+    handle = _stream(stream)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
+    caller = torch.cuda.current_stream()
+    with torch.cuda.stream(stream):
+        result = call(*args, **kw)
+    if caller.cuda_stream != handle:
+        for t in result if isinstance(result, tuple) else (result,):
+            if t is not None:
+                t.record_stream(caller)
+    return result
+
+
 def _need(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple):
     if t.device.type != "cuda":
         raise ValueError(f"{name} must be a CUDA tensor")
@@ -222,6 +240,8 @@ def _lmax(rad: torch.Tensor, lmax: int | None) -> int:
 def zs_build_csr(dst: torch.Tensor, N: int, row_ptr=None, perm=None, bad_dst_count=None,
                  workspace=None, stream=None):
     """Stable destination CSR.  Returns (row_ptr (N+1,), perm (E,), bad_dst_count (1,)) int32."""
+    if stream is not None:
+        return _on(stream, zs_build_csr, dst, N, row_ptr, perm, bad_dst_count, workspace)
     E = dst.shape[0]
     dev = dst.device
     _need(dst, "dst", torch.int32, (E,))
@@ -235,13 +255,15 @@ def zs_build_csr(dst: torch.Tensor, N: int, row_ptr=None, perm=None, bad_dst_cou
         workspace = _workspace(need, dev)
     wbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check("zs_build_csr", load().zs_build_csr(_ptr(dst), E, N, _ptr(row_ptr), _ptr(perm), _ptr(bad_dst_count),
-                                               _ptr(workspace), wbytes, _stream(stream)))
+                                               _ptr(workspace), wbytes, _stream(None)))
     return row_ptr, perm, bad_dst_count
 
 
 def zs_forward(coup: torch.Tensor, rad: torch.Tensor, row_ptr: torch.Tensor, perm: torch.Tensor, N: int,
                out=None, workspace=None, stream=None, lmax: int | None = None):
     """Forward zonal scatter.  Returns out (N, D, C) fp32; lmax defaults to rad.shape[1]."""
+    if stream is not None:
+        return _on(stream, zs_forward, coup, rad, row_ptr, perm, N, out, workspace, lmax=lmax)
     lmax = _lmax(rad, lmax)
     D, R = ladder(lmax)
     E = coup.shape[0]
@@ -257,7 +279,7 @@ def zs_forward(coup: torch.Tensor, rad: torch.Tensor, row_ptr: torch.Tensor, per
         workspace = _workspace(zs_forward_workspace_bytes(E, N, C, lmax), dev)
     wbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check("zs_forward", load().zs_forward(_ptr(coup), _ptr(rad), _ptr(row_ptr), _ptr(perm), E, N, C, lmax,
-                                           _ptr(out), _ptr(workspace), wbytes, _stream(stream)))
+                                           _ptr(out), _ptr(workspace), wbytes, _stream(None)))
     return out
 
 
@@ -265,6 +287,8 @@ def zs_forward_ld(coup: torch.Tensor, rad: torch.Tensor, row_ptr: torch.Tensor, 
                   out=None, workspace=None, stream=None, lmax: int | None = None):
     """zs_forward with coup a row-strided view (for example the m = 0 segment of a
     packed (E, 3D-2) Wigner band): coup[e] = coup.data_ptr() + e * coup.stride(0)."""
+    if stream is not None:
+        return _on(stream, zs_forward_ld, coup, rad, row_ptr, perm, N, out, workspace, lmax=lmax)
     lmax = _lmax(rad, lmax)
     D, R = ladder(lmax)
     E = coup.shape[0]
@@ -280,13 +304,15 @@ def zs_forward_ld(coup: torch.Tensor, rad: torch.Tensor, row_ptr: torch.Tensor, 
         workspace = _workspace(zs_forward_workspace_bytes(E, N, C, lmax), dev)
     wbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check("zs_forward_ld", load().zs_forward_ld(_ptr(coup), ld, _ptr(rad), _ptr(row_ptr), _ptr(perm), E, N, C, lmax,
-                                                 _ptr(out), _ptr(workspace), wbytes, _stream(stream)))
+                                                 _ptr(out), _ptr(workspace), wbytes, _stream(None)))
     return out
 
 
 def zs_backward_ld(g: torch.Tensor, coup: torch.Tensor, rad: torch.Tensor, dst: torch.Tensor, N: int,
                    d_coup: torch.Tensor, d_rad=None, stream=None, lmax: int | None = None):
     """zs_backward with coup and d_coup row-strided views (d_coup must be given)."""
+    if stream is not None:
+        return _on(stream, zs_backward_ld, g, coup, rad, dst, N, d_coup, d_rad, lmax=lmax)
     lmax = _lmax(rad, lmax)
     D, R = ladder(lmax)
     E = coup.shape[0]
@@ -300,7 +326,7 @@ def zs_backward_ld(g: torch.Tensor, coup: torch.Tensor, rad: torch.Tensor, dst: 
     d_rad = torch.empty((E, lmax, C), dtype=torch.float32, device=dev) if d_rad is None else d_rad
     _need(d_rad, "d_rad", torch.float32, (E, lmax, C))
     _check("zs_backward_ld", load().zs_backward_ld(_ptr(g), _ptr(coup), ld, _ptr(rad), _ptr(dst), E, N, C, lmax,
-                                                   _ptr(d_coup), dld, _ptr(d_rad), _stream(stream)))
+                                                   _ptr(d_coup), dld, _ptr(d_rad), _stream(None)))
     return d_coup, d_rad
 
 
@@ -309,6 +335,9 @@ def zs_forward_scaled(coup: torch.Tensor, rad: torch.Tensor, row_ptr: torch.Tens
                       workspace=None, stream=None, lmax: int | None = None):
     """Forward with the per-node factor fused in.  Returns (out, out_raw); out_raw is
     None when want_raw is False and none is given."""
+    if stream is not None:
+        return _on(stream, zs_forward_scaled, coup, rad, row_ptr, perm, node_scale, N, out, out_raw, want_raw,
+                   workspace, lmax=lmax)
     lmax = _lmax(rad, lmax)
     D, R = ladder(lmax)
     E = coup.shape[0]
@@ -330,7 +359,7 @@ def zs_forward_scaled(coup: torch.Tensor, rad: torch.Tensor, row_ptr: torch.Tens
     wbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check("zs_forward_scaled", load().zs_forward_scaled(_ptr(coup), _ptr(rad), _ptr(row_ptr), _ptr(perm),
                                                          _ptr(node_scale), E, N, C, lmax, _ptr(out), _ptr(out_raw),
-                                                         _ptr(workspace), wbytes, _stream(stream)))
+                                                         _ptr(workspace), wbytes, _stream(None)))
     return out, out_raw
 
 
@@ -339,6 +368,9 @@ def zs_backward_scaled(g: torch.Tensor, coup: torch.Tensor, rad: torch.Tensor, d
                        want_scale_grad: bool = True, stream=None, lmax: int | None = None):
     """Backward of zs_forward_scaled.  Returns (d_coup, d_rad, d_scale); d_scale is
     None unless out_raw is given (and want_scale_grad)."""
+    if stream is not None:
+        return _on(stream, zs_backward_scaled, g, coup, rad, dst, node_scale, N, out_raw, d_coup, d_rad, d_scale,
+                   want_scale_grad, lmax=lmax)
     lmax = _lmax(rad, lmax)
     D, R = ladder(lmax)
     E = coup.shape[0]
@@ -362,13 +394,15 @@ def zs_backward_scaled(g: torch.Tensor, coup: torch.Tensor, rad: torch.Tensor, d
     _check("zs_backward_scaled", load().zs_backward_scaled(_ptr(g), _ptr(coup), _ptr(rad), _ptr(dst),
                                                            _ptr(node_scale), _ptr(out_raw), E, N, C, lmax,
                                                            _ptr(d_coup), _ptr(d_rad), _ptr(d_scale),
-                                                           _stream(stream)))
+                                                           _stream(None)))
     return d_coup, d_rad, d_scale
 
 
 def zs_backward(g: torch.Tensor, coup: torch.Tensor, rad: torch.Tensor, dst: torch.Tensor, N: int,
                 d_coup=None, d_rad=None, stream=None, lmax: int | None = None):
     """Backward.  Returns (d_coup (E, R), d_rad (E, lmax, C)) fp32; lmax defaults to rad.shape[1]."""
+    if stream is not None:
+        return _on(stream, zs_backward, g, coup, rad, dst, N, d_coup, d_rad, lmax=lmax)
     lmax = _lmax(rad, lmax)
     D, R = ladder(lmax)
     E = coup.shape[0]
@@ -383,13 +417,15 @@ def zs_backward(g: torch.Tensor, coup: torch.Tensor, rad: torch.Tensor, dst: tor
     _need(d_coup, "d_coup", torch.float32, (E, R))
     _need(d_rad, "d_rad", torch.float32, (E, lmax, C))
     _check("zs_backward", load().zs_backward(_ptr(g), _ptr(coup), _ptr(rad), _ptr(dst), E, N, C, lmax,
-                                             _ptr(d_coup), _ptr(d_rad), _stream(stream)))
+                                             _ptr(d_coup), _ptr(d_rad), _stream(None)))
     return d_coup, d_rad
 
 
 def zs_backward_csr(g: torch.Tensor, coup: torch.Tensor, rad: torch.Tensor, row_ptr: torch.Tensor,
                     perm: torch.Tensor, N: int, d_coup=None, d_rad=None, stream=None, lmax: int | None = None):
     """Backward with edges visited in CSR order.  Returns (d_coup (E, R), d_rad (E, lmax, C)) fp32."""
+    if stream is not None:
+        return _on(stream, zs_backward_csr, g, coup, rad, row_ptr, perm, N, d_coup, d_rad, lmax=lmax)
     lmax = _lmax(rad, lmax)
     D, R = ladder(lmax)
     E = coup.shape[0]
@@ -405,7 +441,7 @@ def zs_backward_csr(g: torch.Tensor, coup: torch.Tensor, rad: torch.Tensor, row_
     _need(d_coup, "d_coup", torch.float32, (E, R))
     _need(d_rad, "d_rad", torch.float32, (E, lmax, C))
     _check("zs_backward_csr", load().zs_backward_csr(_ptr(g), _ptr(coup), _ptr(rad), _ptr(row_ptr), _ptr(perm),
-                                                     E, N, C, lmax, _ptr(d_coup), _ptr(d_rad), _stream(stream)))
+                                                     E, N, C, lmax, _ptr(d_coup), _ptr(d_rad), _stream(None)))
     return d_coup, d_rad
 
 
@@ -563,7 +599,9 @@ def zs_grouped_matmul(x: torch.Tensor, w: torch.Tensor, row_ptr: torch.Tensor, p
     """y[i] = w[g(i)] x[i] for rows grouped by the CSR (row_ptr, perm); perm None: rows
     are in group order already.  x (M, K) and w (G, N, K) float32, bfloat16 or
     float16; returns y (M, N).  x and out may be row-strided views."""
-    if out is None and stream is None:
+    if stream is not None:
+        return _on(stream, zs_grouped_matmul, x, w, row_ptr, perm, out)
+    if out is None:
         y = _fast.matmul(x, w, row_ptr, perm, False)
         if y is not NotImplemented:
             return y
@@ -580,7 +618,7 @@ def zs_grouped_matmul(x: torch.Tensor, w: torch.Tensor, row_ptr: torch.Tensor, p
     wbytes = lib.zs_grouped_matmul_workspace_bytes(d, M, K, N, G) if _copies(w, perm) else 0
     workspace = _workspace(wbytes, w.device)
     st = lib.zs_grouped_matmul_ws(d, x.data_ptr(), x_ld, wp, rp, pp, M, K, N, G, out.data_ptr(), out_ld, _ptr(workspace), wbytes,
-                                _stream(stream))
+                                _stream(None))
     if st:
         _check("zs_grouped_matmul_ws", st)
     return out
@@ -589,7 +627,9 @@ def zs_grouped_matmul(x: torch.Tensor, w: torch.Tensor, row_ptr: torch.Tensor, p
 def zs_grouped_matmul_dx(dy: torch.Tensor, w: torch.Tensor, row_ptr: torch.Tensor, perm: torch.Tensor | None = None,
                          out=None, stream=None) -> torch.Tensor:
     """dx[i] = w[g(i)]^T dy[i]: the gradient of zs_grouped_matmul in x, (M, K)."""
-    if out is None and stream is None:
+    if stream is not None:
+        return _on(stream, zs_grouped_matmul_dx, dy, w, row_ptr, perm, out)
+    if out is None:
         dx = _fast.matmul(dy, w, row_ptr, perm, True)
         if dx is not NotImplemented:
             return dx
@@ -606,7 +646,7 @@ def zs_grouped_matmul_dx(dy: torch.Tensor, w: torch.Tensor, row_ptr: torch.Tenso
     wbytes = lib.zs_grouped_matmul_workspace_bytes(d, M, K, N, G) if _copies(w, perm) else 0
     workspace = _workspace(wbytes, w.device)
     st = lib.zs_grouped_matmul_dx_ws(d, dy.data_ptr(), dy_ld, wp, rp, pp, M, K, N, G, out.data_ptr(), out_ld, _ptr(workspace), wbytes,
-                                   _stream(stream))
+                                   _stream(None))
     if st:
         _check("zs_grouped_matmul_dx_ws", st)
     return out
@@ -620,7 +660,9 @@ def zs_grouped_matmul_dw(dy: torch.Tensor, x: torch.Tensor, row_ptr: torch.Tenso
                          out=None, workspace=None, stream=None) -> torch.Tensor:
     """dw[g] = sum over the rows of group g of dy[i] x[i]^T: the gradient of
     zs_grouped_matmul in w, (G, N, K) with G = row_ptr.numel() - 1."""
-    if out is None and workspace is None and stream is None:
+    if stream is not None:
+        return _on(stream, zs_grouped_matmul_dw, dy, x, row_ptr, perm, out, workspace)
+    if out is None and workspace is None:
         dw = _fast.dw(dy, x, row_ptr, perm)
         if dw is not NotImplemented:
             return dw
@@ -645,7 +687,7 @@ def zs_grouped_matmul_dw(dy: torch.Tensor, x: torch.Tensor, row_ptr: torch.Tenso
     else:
         wbytes = workspace.numel() * workspace.element_size()
     st = lib.zs_grouped_matmul_dw(d, dy.data_ptr(), dy_ld, x.data_ptr(), x_ld, rp, pp, M, K, N, G, op, _ptr(workspace),
-                                  wbytes, _stream(stream))
+                                  wbytes, _stream(None))
     if st:
         _check("zs_grouped_matmul_dw", st)
     return out
@@ -654,8 +696,10 @@ def zs_grouped_matmul_dw(dy: torch.Tensor, x: torch.Tensor, row_ptr: torch.Tenso
 def zs_grouped_matmul_backward(dy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, row_ptr: torch.Tensor,
                                perm: torch.Tensor | None = None, stream=None):
     """Both gradients of zs_grouped_matmul: (dx (M, K), dw (G, N, K))."""
-    return (zs_grouped_matmul_dx(dy, w, row_ptr, perm, stream=stream),
-            zs_grouped_matmul_dw(dy, x, row_ptr, perm, stream=stream))
+    if stream is not None:
+        return _on(stream, zs_grouped_matmul_backward, dy, x, w, row_ptr, perm)
+    return (zs_grouped_matmul_dx(dy, w, row_ptr, perm),
+            zs_grouped_matmul_dw(dy, x, row_ptr, perm))
 
 
 def _norm_operands(h, x, gate, w_post, scale, w_pre, kind):
@@ -690,7 +734,9 @@ def zs_norm_gate_residual(h: torch.Tensor, x: torch.Tensor, gate: torch.Tensor |
     same, (M, 1), or None; w_post, scale, w_pre (C,) float32; kind "rms" or "layer".
     Returns (y, u, stats): stats (M, 4) float32 is what the backward reads (None
     when want_stats is False)."""
-    if stream is None and kind in NORM_KINDS:
+    if stream is not None:
+        return _on(stream, zs_norm_gate_residual, h, x, gate, w_post, scale, w_pre, eps, kind, want_stats)
+    if kind in NORM_KINDS:
         r = _fast.norm(h, x, gate, w_post, scale, w_pre, eps, NORM_KINDS[kind], want_stats)
         if r is not NotImplemented:
             return r
@@ -700,7 +746,7 @@ def zs_norm_gate_residual(h: torch.Tensor, x: torch.Tensor, gate: torch.Tensor |
     u = torch.empty((M, C), dtype=dt, device=dev)
     stats = torch.empty((M, 4), dtype=torch.float32, device=dev) if want_stats else None
     st = load().zs_norm_gate_residual(d, k, *args, eps, M, C, y.data_ptr(), u.data_ptr(),
-                                      stats.data_ptr() if want_stats else None, _stream(stream))
+                                      stats.data_ptr() if want_stats else None, _stream(None))
     if st:
         _check("zs_norm_gate_residual", st)
     return y, u, stats
@@ -711,7 +757,9 @@ def zs_norm_gate_residual_backward(dy: torch.Tensor | None, du: torch.Tensor | N
                                    w_pre: torch.Tensor, stats: torch.Tensor, kind: str = "rms", stream=None):
     """Gradients of zs_norm_gate_residual for the cotangents dy of y and du of u (None:
     zeros): (dh, dx, dgate, dw_post, dscale, dw_pre); dgate is None without a gate."""
-    if stream is None and kind in NORM_KINDS:
+    if stream is not None:
+        return _on(stream, zs_norm_gate_residual_backward, dy, du, h, x, gate, w_post, scale, w_pre, stats, kind)
+    if kind in NORM_KINDS:
         r = _fast.norm_backward(dy, du, h, x, gate, w_post, scale, w_pre, stats, NORM_KINDS[kind])
         if r is not NotImplemented:
             return r
@@ -730,7 +778,7 @@ def zs_norm_gate_residual_backward(dy: torch.Tensor | None, du: torch.Tensor | N
     st = lib.zs_norm_gate_residual_backward(
         d, k, None if dy is None else dy.data_ptr(), dy_ld, None if du is None else du.data_ptr(), du_ld, *args, stats_ptr,
         M, C, dh.data_ptr(), dx.data_ptr(), None if gate is None else dgate.data_ptr(), *(t.data_ptr() for t in sums),
-        _ptr(workspace), need, _stream(stream))
+        _ptr(workspace), need, _stream(None))
     if st:
         _check("zs_norm_gate_residual_backward", st)
     return dh, dx, dgate, *sums
