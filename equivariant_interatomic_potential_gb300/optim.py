@@ -53,7 +53,7 @@ class AdamW:
             new = [at[i] for i in group]
             if any(p.data_ptr() != self.params[i].data_ptr() for p, i in zip(plan.params, group)):
                 raise RuntimeError("a parameter has moved since the optimiser was built")
-            if any(a is not b for a, b in zip(new, plan.grads)):
+            if not plan.has_grads(new):   # by where they are: p.grad.data = other keeps the tensor
                 plan.set_grads(new)
 
     @torch.no_grad()

@@ -802,9 +802,10 @@ class AdamWPlan:
     32-bit states: exp_avg and exp_avg_sq float32 of the parameters' sizes.  8-bit
     states: torch.float8_e4m3fn of the parameters' sizes (exp_avg_sq holds the root of
     the second moment), with exp_avg_scale and exp_avg_sq_scale float32 of
-    ceil(numel / 256) elements each.  Every tensor is contiguous and is held by the
-    plan; ``zs_adamw_step`` updates them in place.  ``set_grads`` puts other gradient
-    tensors (of the same sizes) in place of the plan's."""
+    ceil(numel / 256) elements each.  Every tensor is contiguous; the plan is of the
+    memory that it has when the plan is made, which it holds, and ``zs_adamw_step``
+    updates that.  ``set_grads`` puts other gradients (of the same sizes) in place of the
+    plan's."""
 
     def __init__(self, params, grads, exp_avg, exp_avg_sq, exp_avg_scale=None, exp_avg_sq_scale=None):
         self.params, self.exp_avg, self.exp_avg_sq = list(params), list(exp_avg), list(exp_avg_sq)
@@ -835,6 +836,8 @@ class AdamWPlan:
                     self._one(lst[i], f"{name}[{i}]", torch.float32, (-(-p.numel() // ADAMW_BLOCK),))
                     setattr(e, name, _ptr(lst[i]))
         self._table_ptr = ctypes.addressof(self._table)
+        # a tensor's memory may be taken from it (t.data = other): it is held by itself
+        self._memory = [t.untyped_storage() for t in (*self.params, *self.exp_avg, *self.exp_avg_sq, *sum(self.scales, []))]
         self.set_grads(grads)
 
     def _one(self, t, name, dtype, shape):
@@ -851,6 +854,12 @@ class AdamWPlan:
         for i, g in enumerate(grads):
             self._table[i].grad = _ptr(g)
         self.grads = grads
+        self._grad_at = [g.data_ptr() for g in grads]
+        self._grad_memory = [g.untyped_storage() for g in grads]
+
+    def has_grads(self, grads) -> bool:
+        """Whether these tensors, where they are now, are the plan's gradients."""
+        return all(g.data_ptr() == at and g.shape == p.shape for g, at, p in zip(grads, self._grad_at, self.params))
 
 
 def zs_adamw_step(plan: AdamWPlan, step: int, lr: float, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,

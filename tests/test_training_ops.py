@@ -135,6 +135,47 @@ def test_optimiser_state_and_missing_gradients(bits):
         a.load_state_dict(AdamW(make()[:1], state_bits=bits).state_dict())
 
 
+def spoil(n):
+    """Takes freed blocks of n floats and overwrites them."""
+    return [torch.full((n,), 3.0, device="cuda") for _ in range(8)]
+
+
+@pytest.mark.gpu
+def test_optimiser_gradient_memory_replaced():
+    # p.grad stays the same tensor while its memory is another (p.grad.data = clipped): each step reads the present one
+    gen = torch.Generator(device="cuda").manual_seed(12)
+    rnd = lambda: torch.randn(5000, generator=gen, device="cuda")  # noqa: E731
+    p, q = torch.ones(5000, device="cuda"), torch.ones(5000, device="cuda").requires_grad_()
+    a, b = AdamW([p], lr=1e-2, weight_decay=0.1), torch.optim.AdamW([q], lr=1e-2, weight_decay=0.1)
+    p.grad = rnd()
+    for _ in range(4):
+        p.grad.data = rnd()
+        kept = spoil(5000)
+        q.grad = p.grad.clone()
+        a.step()
+        b.step()
+        del kept
+    # a gradient of another shape in the same place is refused, not read past its end
+    assert float((p - q).abs().max()) <= 1e-6 * float(q.detach().abs().max())
+    p.grad.data = p.grad.data[:100]
+    with pytest.raises(ValueError, match="shape"):
+        a.step()
+
+
+@pytest.mark.gpu
+def test_plan_holds_the_memory():
+    make = lambda: [torch.full((4000,), v, device="cuda") for v in (1.0, 0.5, 0.1, 0.2)]  # noqa: E731
+    want, mine = make(), make()
+    plans = [zs.AdamWPlan(*([t] for t in ts)) for ts in (want, mine)]
+    kept = mine[0].detach()
+    for t in mine:
+        t.data = torch.zeros(4000, device="cuda")
+    spoil(4000)
+    for plan in plans:
+        zs.zs_adamw_step(plan, 1, lr=1e-2)
+    assert torch.equal(kept, want[0]) and not bool(mine[0].any())
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("bits,dtype", [(32, torch.float32), (8, torch.float32), (8, torch.bfloat16)])
 def test_example_learns(bits, dtype):
