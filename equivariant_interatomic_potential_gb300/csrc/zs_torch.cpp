@@ -2,13 +2,14 @@
 //
 // The Python binding checks, allocates and marshals in Python, which takes
 // longer than the kernels of small calls run.  These functions do the same for
-// the ordinary case (contiguous CUDA tensors of the right types and shapes, the
-// current stream) and give NotImplemented for everything else, which the
+// the ordinary case (contiguous tensors of the current device, of the right types
+// and shapes, its current stream) and give NotImplemented for everything else, which the
 // binding then handles, refusals among it.  They call libzs through the
 // addresses that `bind` is given.
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -30,7 +31,7 @@ PyObject* on_error;   // binding's check(function name, status): raises
 const at::Tensor* plain(PyObject* o) {
     if (!THPVariable_CheckExact(o)) return nullptr;
     const at::Tensor& t = THPVariable_Unpack(o);
-    return t.is_cuda() && t.is_contiguous() ? &t : nullptr;
+    return t.is_cuda() && t.get_device() == c10::cuda::current_device() && t.is_contiguous() ? &t : nullptr;
 }
 // -1: not a type of the training operators
 int dtype_of(const at::Tensor& t) {

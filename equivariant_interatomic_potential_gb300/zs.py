@@ -168,6 +168,28 @@ def _stream(stream) -> int | None:
     return stream.cuda_stream
 
 
+def _current_device() -> int:
+    return torch.cuda.current_device() if _raw_device is None else _raw_device()
+
+
+def _one_device(operands, device=None) -> int:
+    """The index of the device that every CUDA tensor among the operands is on, which is
+    that of ``device`` (a stream's) where it is given."""
+    on = {t.get_device() for t in operands if isinstance(t, torch.Tensor) and t.is_cuda}
+    if device is not None:
+        on.add(device.index)
+    if len(on) > 1:
+        names = " and ".join(f"cuda:{i}" for i in sorted(on))
+        raise ValueError(f"the operands{'' if device is None else ' and the stream'} must be on one device, got {names}")
+    return on.pop() if on else -1
+
+
+def _elsewhere(*operands):
+    """The device of the operands where it is not the current one, which a call then enters."""
+    device = _one_device(operands)
+    return device if device >= 0 and device != _current_device() else None
+
+
 def _on(stream, call, *args, **kw):
     """call(...) with ``stream`` (a stream object or a handle) current, so that what the call
     allocates is that stream's: no other stream is handed its workspace while the kernels
@@ -176,6 +198,7 @@ def _on(stream, call, *args, **kw):
     handle = _stream(stream)
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
+    _one_device((*args, *kw.values()), stream.device)
     caller = torch.cuda.current_stream()
     with torch.cuda.stream(stream):
         result = call(*args, **kw)
@@ -605,6 +628,10 @@ def zs_grouped_matmul(x: torch.Tensor, w: torch.Tensor, row_ptr: torch.Tensor, p
         y = _fast.matmul(x, w, row_ptr, perm, False)
         if y is not NotImplemented:
             return y
+    device = _elsewhere(x, w, row_ptr, perm, out)
+    if device is not None:
+        with torch.cuda.device(device):
+            return zs_grouped_matmul(x, w, row_ptr, perm, out)
     M, _ = _rows(x, "x")
     d, G, N, K, wp, rp, pp = _groups(w, row_ptr, perm, M)
     dt = w.dtype
@@ -633,6 +660,10 @@ def zs_grouped_matmul_dx(dy: torch.Tensor, w: torch.Tensor, row_ptr: torch.Tenso
         dx = _fast.matmul(dy, w, row_ptr, perm, True)
         if dx is not NotImplemented:
             return dx
+    device = _elsewhere(dy, w, row_ptr, perm, out)
+    if device is not None:
+        with torch.cuda.device(device):
+            return zs_grouped_matmul_dx(dy, w, row_ptr, perm, out)
     M, _ = _rows(dy, "dy")
     d, G, N, K, wp, rp, pp = _groups(w, row_ptr, perm, M)
     dt = w.dtype
@@ -666,6 +697,10 @@ def zs_grouped_matmul_dw(dy: torch.Tensor, x: torch.Tensor, row_ptr: torch.Tenso
         dw = _fast.dw(dy, x, row_ptr, perm)
         if dw is not NotImplemented:
             return dw
+    device = _elsewhere(dy, x, row_ptr, perm, out, workspace)
+    if device is not None:
+        with torch.cuda.device(device):
+            return zs_grouped_matmul_dw(dy, x, row_ptr, perm, out, workspace)
     M, K = _rows(x, "x")
     _, N = _rows(dy, "dy")
     G = row_ptr.numel() - 1
@@ -740,6 +775,10 @@ def zs_norm_gate_residual(h: torch.Tensor, x: torch.Tensor, gate: torch.Tensor |
         r = _fast.norm(h, x, gate, w_post, scale, w_pre, eps, NORM_KINDS[kind], want_stats)
         if r is not NotImplemented:
             return r
+    device = _elsewhere(h, x, gate, w_post, scale, w_pre)
+    if device is not None:
+        with torch.cuda.device(device):
+            return zs_norm_gate_residual(h, x, gate, w_post, scale, w_pre, eps, kind, want_stats)
     d, k, M, C, args = _norm_operands(h, x, gate, w_post, scale, w_pre, kind)
     dt, dev = h.dtype, h.device
     y = torch.empty((M, C), dtype=dt, device=dev)
@@ -763,6 +802,10 @@ def zs_norm_gate_residual_backward(dy: torch.Tensor | None, du: torch.Tensor | N
         r = _fast.norm_backward(dy, du, h, x, gate, w_post, scale, w_pre, stats, NORM_KINDS[kind])
         if r is not NotImplemented:
             return r
+    device = _elsewhere(dy, du, h, x, gate, w_post, scale, w_pre, stats)
+    if device is not None:
+        with torch.cuda.device(device):
+            return zs_norm_gate_residual_backward(dy, du, h, x, gate, w_post, scale, w_pre, stats, kind)
     d, k, M, C, args = _norm_operands(h, x, gate, w_post, scale, w_pre, kind)
     dt, dev, f32 = h.dtype, h.device, torch.float32
     dy_ld = 0 if dy is None else _matrix(dy, "dy", dt, M, C)
@@ -871,6 +914,11 @@ def zs_adamw_step(plan: AdamWPlan, step: int, lr: float, beta1: float = 0.9, bet
         if grad_scale.numel() != 1 or grad_scale.dtype != torch.float32 or grad_scale.device != plan.device:
             raise ValueError(f"grad_scale must be one float32 element on {plan.device}")
         scale_ptr = grad_scale.data_ptr()
+    if isinstance(stream, torch.cuda.Stream):
+        _one_device((plan.params[0],), stream.device)
+    if plan.device.index != _current_device():   # a launch is the current device's
+        with torch.cuda.device(plan.device):
+            return zs_adamw_step(plan, step, lr, beta1, beta2, eps, weight_decay, grad_scale, stream)
     hyper = _AdamWHyper(lr, beta1, beta2, eps, weight_decay, step)
     st = load().zs_adamw_step(plan._table_ptr, len(plan.params), plan.dtype, plan.state_bits, ctypes.addressof(hyper),
                               scale_ptr, _stream(stream))
