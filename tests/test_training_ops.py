@@ -135,6 +135,31 @@ def test_optimiser_state_and_missing_gradients(bits):
         a.load_state_dict(AdamW(make()[:1], state_bits=bits).state_dict())
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("missing", [lambda t, i: i == 1 and t < 30, lambda t, i: (t + i) % 3 == 0,
+                                     lambda t, i: i > 0 and t % 7 != i], ids=["late", "in_turn", "seldom"])
+def test_optimiser_skipped_steps_against_torch(missing):
+    # a parameter that misses steps has the bias correction of its own steps; tolerance as above, for 40 steps
+    gen = torch.Generator(device="cuda").manual_seed(7)
+    shapes = [(300, 7), (64,), (1000,)]
+    mine = [torch.randn(s, generator=gen, device="cuda") for s in shapes]
+    theirs = [p.clone().requires_grad_() for p in mine]
+    a = AdamW(mine, lr=1e-2, weight_decay=0.1)
+    b = torch.optim.AdamW(theirs, lr=1e-2, weight_decay=0.1)
+    for t in range(40):
+        for i, (p, q) in enumerate(zip(mine, theirs)):
+            g = torch.randn(p.shape, generator=gen, device="cuda")
+            p.grad, q.grad = (None, None) if missing(t, i) else (g, g.clone())
+        if t == 25:    # the counts travel with the state
+            state = a.state_dict()
+            a = AdamW(mine, lr=1e-2, weight_decay=0.1)
+            a.load_state_dict(state)
+        a.step()
+        b.step()
+        for p, q in zip(mine, theirs):
+            assert float((p - q.detach()).abs().max()) <= 4e-6 * float(q.detach().abs().max()), t
+
+
 def spoil(n):
     """Takes freed blocks of n floats and overwrites them."""
     return [torch.full((n,), 3.0, device="cuda") for _ in range(8)]
