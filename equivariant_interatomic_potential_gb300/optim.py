@@ -1,91 +1,140 @@
-"""AdamW over libzs: one launch for all tensors of a type, states in 32 or 8 bits."""
+"""AdamW over libzs: one launch for the tensors of a type, states in 32 or 8 bits."""
 from __future__ import annotations
+
+from itertools import chain
 
 import torch
 
 from . import zs
 
+_HYPER = ("lr", "betas", "eps", "weight_decay")
 
-class AdamW:
+
+def _of_groups(name: str) -> property:
+    """A hyper-parameter of the first group; setting it sets every group's."""
+    def put(self, value):
+        for group in self.param_groups:
+            group[name] = value
+
+    return property(lambda self: self.param_groups[0][name], put)
+
+
+class AdamW(torch.optim.Optimizer):
     """AdamW (decoupled weight decay, bias correction) over CUDA parameters.
 
-    params: tensors, each contiguous, float32, bfloat16 or float16, on one device;
-    every call of ``step`` uses their ``.grad`` (a missing one counts as skipped: the
-    parameter and its states stay, and its bias correction counts its own steps).  One
-    launch for the parameters of a type that have had as many steps.  state_bits 32
-    keeps both moments in float32, 8 as float8_e4m3fn codes with a scale for each 256
-    elements (the second one as its root): 2.06 bytes a parameter instead of 8.
+    params: tensors, or groups of them with options of their own, each contiguous,
+    float32, bfloat16 or float16, on one device; every call of ``step`` uses their
+    ``.grad`` (a missing one counts as skipped: the parameter and its states stay, and
+    its bias correction counts its own steps).  One launch for the parameters of a type
+    that share their options and have had as many steps.  state_bits 32 keeps both
+    moments in float32, 8 as float8_e4m3fn codes with a scale for each 256 elements (the
+    second one as its root): 2.06 bytes a parameter instead of 8.
     """
 
     def __init__(self, params, lr: float = 1e-3, betas: tuple[float, float] = (0.9, 0.999), eps: float = 1e-8,
                  weight_decay: float = 0.01, state_bits: int = 32):
-        self.params = list(params)
-        if not self.params:
+        params = list(params)
+        if not params:
             raise ValueError("AdamW needs at least one parameter")
-        if state_bits not in (8, 32):
-            raise ValueError(f"state_bits must be 8 or 32, got {state_bits}")
-        self.lr, self.betas, self.eps, self.weight_decay, self.state_bits = lr, betas, eps, weight_decay, state_bits
-        self.steps = [0] * len(self.params)   # that each parameter has had
-        dtype = torch.float32 if state_bits == 32 else torch.float8_e4m3fn
-        self.state = []
-        for p in self.params:
-            s = {k: torch.zeros(p.shape, dtype=torch.float32, device=p.device).to(dtype) for k in ("exp_avg", "exp_avg_sq")}
-            if state_bits == 8:
-                blocks = -(-p.numel() // zs.ADAMW_BLOCK)
-                s |= {k: torch.zeros(blocks, device=p.device) for k in ("exp_avg_scale", "exp_avg_sq_scale")}
-            self.state.append(s)
-        self._plans: list[tuple[list[int], zs.AdamWPlan]] = []
+        self._plans: dict[tuple, zs.AdamWPlan] = {}
+        super().__init__(params, dict(lr=lr, betas=betas, eps=eps, weight_decay=weight_decay, state_bits=state_bits))
 
-    def _plan(self, live: list[int], grads: list[torch.Tensor]):
-        """Plans over the parameters with gradients, one for each type and number of steps; kept while the sets stay."""
-        groups: dict[tuple, list[int]] = {}
-        for i in live:
-            groups.setdefault((self.params[i].dtype, self.steps[i]), []).append(i)
-        kept = {tuple(group): plan for group, plan in self._plans}
-        at = dict(zip(live, grads))
-        self._plans = []
-        for group in groups.values():
-            new, plan = [at[i] for i in group], kept.get(tuple(group))
-            if plan is None:
-                scales = [[self.state[i][k] for i in group] for k in ("exp_avg_scale", "exp_avg_sq_scale")] \
-                    if self.state_bits == 8 else [None, None]
-                plan = zs.AdamWPlan([self.params[i].detach() for i in group], new,
-                                    *([self.state[i][k] for i in group] for k in ("exp_avg", "exp_avg_sq")), *scales)
-            elif any(p.data_ptr() != self.params[i].data_ptr() for p, i in zip(plan.params, group)):
-                raise RuntimeError("a parameter has moved since the optimiser was built")
-            elif not plan.has_grads(new):   # by where they are: p.grad.data = other keeps the tensor
-                plan.set_grads(new)
-            self._plans.append((group, plan))
+    lr, betas, eps, weight_decay = map(_of_groups, _HYPER)
+
+    def __setstate__(self, state):
+        super().__setstate__(state)
+        self._plans = {}
+
+    def add_param_group(self, param_group: dict) -> None:
+        bits = param_group.get("state_bits", self.defaults["state_bits"])
+        if bits not in (8, 32):
+            raise ValueError(f"state_bits must be 8 or 32, got {bits}")
+        super().add_param_group(param_group)
+        dtype = torch.float32 if bits == 32 else torch.float8_e4m3fn
+        for p in self.param_groups[-1]["params"]:
+            s = self.state[p]
+            s["step"] = 0
+            for k in ("exp_avg", "exp_avg_sq"):
+                s[k] = torch.zeros(p.shape, dtype=torch.float32, device=p.device).to(dtype)
+                if bits == 8:
+                    s[k + "_scale"] = torch.zeros(-(-p.numel() // zs.ADAMW_BLOCK), device=p.device)
+
+    def _plan(self, params: list[torch.Tensor], states: list[dict], grads: list[torch.Tensor], bits: int) -> zs.AdamWPlan:
+        """The plan over these tensors; kept from the last step where they are the same."""
+        plan = self._plans.get(tuple(map(id, params)))
+        if plan is None or any(s["exp_avg"] is not m or s["exp_avg_sq"] is not v
+                               for s, m, v in zip(states, plan.exp_avg, plan.exp_avg_sq)):
+            names = ("exp_avg", "exp_avg_sq") + (("exp_avg_scale", "exp_avg_sq_scale") if bits == 8 else ())
+            return zs.AdamWPlan([p.detach() for p in params], grads, *([s[k] for s in states] for k in names))
+        if not plan.has_params(params):
+            raise RuntimeError("a parameter has moved since the optimiser was built")
+        if not plan.has_grads(grads):   # by where they are: p.grad.data = other keeps the tensor
+            plan.set_grads(grads)
+        return plan
 
     @torch.no_grad()
-    def step(self, grad_scale: torch.Tensor | None = None) -> None:
-        """One step; grad_scale: one float32 element on the device that multiplies every gradient."""
-        live = [i for i, p in enumerate(self.params) if p.grad is not None]
-        if not live:
-            return
-        self._plan(live, [self.params[i].grad.contiguous() for i in live])
-        for group, plan in self._plans:
-            zs.zs_adamw_step(plan, self.steps[group[0]] + 1, lr=self.lr, beta1=self.betas[0], beta2=self.betas[1], eps=self.eps,
-                             weight_decay=self.weight_decay, grad_scale=grad_scale)
-            for i in group:
-                self.steps[i] += 1
-            torch.autograd.graph.increment_version([self.params[i] for i in group])
+    def step(self, closure=None, grad_scale: torch.Tensor | None = None):
+        """One step.  closure: evaluates the loss again, which is returned.  grad_scale: one
+        float32 element on the device that multiplies every gradient (also taken in the
+        closure's place)."""
+        loss = None
+        if isinstance(closure, torch.Tensor):
+            closure, grad_scale = None, closure
+        if closure is not None:
+            with torch.enable_grad():
+                loss = closure()
+        # parameters, states and gradients of each set of options, type and number of steps
+        alike: dict[tuple, tuple[list, list, list]] = {}
+        for group in self.param_groups:
+            options = (float(group["lr"]), *map(float, group["betas"]), group["eps"], group["weight_decay"], group["state_bits"])
+            last = into = None
+            for p in group["params"]:
+                g = p.grad
+                if g is None:
+                    continue
+                s = self.state[p]
+                kind = (p.dtype, s["step"])
+                if kind != last:
+                    last, into = kind, alike.setdefault((options, *kind), ([], [], []))
+                into[0].append(p)
+                into[1].append(s)
+                into[2].append(g if g.is_contiguous() else g.contiguous())
+        plans = {}
+        for (options, _, steps), (params, states, grads) in alike.items():
+            lr, beta1, beta2, eps, decay, bits = options
+            plan = plans[tuple(map(id, params))] = self._plan(params, states, grads, bits)
+            zs.zs_adamw_step(plan, steps + 1, lr=lr, beta1=beta1, beta2=beta2, eps=eps, weight_decay=decay, grad_scale=grad_scale)
+            for s in states:
+                s["step"] = steps + 1
+            torch.autograd.graph.increment_version(params)
+        self._plans = plans
+        return loss
 
-    def zero_grad(self, set_to_none: bool = True) -> None:
-        for p in self.params:
-            if p.grad is not None:
-                p.grad = None if set_to_none else p.grad.zero_()
-
-    def state_dict(self) -> dict:
-        return {"steps": list(self.steps), "state_bits": self.state_bits, "state": [{k: v.clone() for k, v in s.items()} for s in self.state]}
-
-    def load_state_dict(self, d: dict) -> None:
-        if d["state_bits"] != self.state_bits or len(d["state"]) != len(self.state):
-            raise ValueError("the state is of another optimiser: other bits or another number of parameters")
-        for mine, theirs in zip(self.state, d["state"]):
-            for k, v in mine.items():
-                if theirs[k].shape != v.shape:
-                    raise ValueError(f"{k} has shape {tuple(theirs[k].shape)}, the parameter needs {tuple(v.shape)}")
-                v.copy_(theirs[k])
-        steps = d["steps"]   # one number where every parameter has had as many
-        self.steps = [steps] * len(self.params) if isinstance(steps, int) else list(steps)
+    def load_state_dict(self, state_dict: dict) -> None:
+        d = dict(state_dict)
+        mine, params = self.state, list(chain.from_iterable(g["params"] for g in self.param_groups))
+        if "steps" in d:   # the form without groups
+            steps = d["steps"] if isinstance(d["steps"], list) else [d["steps"]] * len(d["state"])
+            if len(steps) != len(params):
+                raise ValueError(f"the state is of {len(steps)} parameters, the optimiser of {len(params)}")
+            groups = self.state_dict()["param_groups"]
+            for g in groups:
+                g["state_bits"] = d["state_bits"]
+            d = {"state": {i: {**s, "step": n} for i, (s, n) in enumerate(zip(d["state"], steps))}, "param_groups": groups}
+        bits = [(g["state_bits"], h.get("state_bits", 32)) for g, h in zip(self.param_groups, d["param_groups"])]
+        if any(a != b for a, b in bits):
+            raise ValueError("the state is of an optimiser with other state_bits")
+        theirs = [d["state"].get(i, {}) for i in chain.from_iterable(g["params"] for g in d["param_groups"])]
+        for p, s in zip(params, theirs):
+            for k, v in mine[p].items():
+                if s and k != "step" and s[k].shape != v.shape:
+                    raise ValueError(f"{k} has shape {tuple(s[k].shape)}, the parameter needs {tuple(v.shape)}")
+        # the groups are the base class's to check and take over; it would cast the states to the parameters' types
+        super().load_state_dict({**d, "state": {}, "param_groups": [{"state_bits": 32, **g} for g in d["param_groups"]]})
+        self.state = mine
+        for p, s in zip(params, theirs):
+            for k, v in mine[p].items():
+                if k == "step":
+                    mine[p][k] = int(s.get(k, 0))
+                else:
+                    v.copy_(s[k]) if s else v.zero_()

@@ -879,11 +879,14 @@ class AdamWPlan:
                     self._one(lst[i], f"{name}[{i}]", torch.float32, (-(-p.numel() // ADAMW_BLOCK),))
                     setattr(e, name, _ptr(lst[i]))
         self._table_ptr = ctypes.addressof(self._table)
+        self._shapes, self._param_at = [p.shape for p in self.params], [p.data_ptr() for p in self.params]
         # a tensor's memory may be taken from it (t.data = other): it is held by itself
         self._memory = [t.untyped_storage() for t in (*self.params, *self.exp_avg, *self.exp_avg_sq, *sum(self.scales, []))]
         self.set_grads(grads)
 
     def _one(self, t, name, dtype, shape):
+        if t.dtype is dtype and t.shape == shape and t.get_device() == self.device.index and t.is_contiguous():
+            return
         _need(t, name, dtype, tuple(shape))
         if t.device != self.device:
             raise ValueError(f"{name} is on {t.device}, the plan on {self.device}")
@@ -892,17 +895,21 @@ class AdamWPlan:
         grads = list(grads)
         if len(grads) != len(self.params):
             raise ValueError(f"grads has {len(grads)} tensors, params {len(self.params)}")
-        for i, (g, p) in enumerate(zip(grads, self.params)):
-            self._one(g, f"grads[{i}]", p.dtype, p.shape)
-        for i, g in enumerate(grads):
-            self._table[i].grad = _ptr(g)
-        self.grads = grads
-        self._grad_at = [g.data_ptr() for g in grads]
+        dtype = self.params[0].dtype
+        for i, (g, shape) in enumerate(zip(grads, self._shapes)):
+            self._one(g, f"grads[{i}]", dtype, shape)
+        self.grads, self._grad_at = grads, [g.data_ptr() for g in grads]
+        for i, at in enumerate(self._grad_at):
+            self._table[i].grad = at or None
         self._grad_memory = [g.untyped_storage() for g in grads]
 
     def has_grads(self, grads) -> bool:
         """Whether these tensors, where they are now, are the plan's gradients."""
-        return all(g.data_ptr() == at and g.shape == p.shape for g, at, p in zip(grads, self._grad_at, self.params))
+        return [g.data_ptr() for g in grads] == self._grad_at and [g.shape for g in grads] == self._shapes
+
+    def has_params(self, params) -> bool:
+        """Whether these tensors, where they are now, are the plan's parameters."""
+        return [p.data_ptr() for p in params] == self._param_at
 
 
 def zs_adamw_step(plan: AdamWPlan, step: int, lr: float, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,

@@ -160,6 +160,81 @@ def test_optimiser_skipped_steps_against_torch(missing):
             assert float((p - q.detach()).abs().max()) <= 4e-6 * float(q.detach().abs().max()), t
 
 
+def test_optimiser_is_one_of_torchs(tmp_path):
+    # groups with options of their own, schedulers, hooks, and states that are kept as they are (on the CPU: no step)
+    p, q = torch.zeros(300), torch.zeros(33, dtype=torch.bfloat16)
+    opt = AdamW([{"params": [p], "weight_decay": 0.0}, {"params": [q], "state_bits": 8}], lr=0.5, betas=(0.8, 0.9))
+    assert isinstance(opt, torch.optim.Optimizer) and opt.lr == 0.5 and opt.betas == (0.8, 0.9)
+    torch.optim.lr_scheduler.StepLR(opt, 1)
+    opt.lr = 0.25
+    assert [g["lr"] for g in opt.param_groups] == [0.25, 0.25] and [g["weight_decay"] for g in opt.param_groups] == [0.0, 0.01]
+    for s in opt.state.values():   # values that the parameters' types could not hold
+        for k, v in s.items():
+            if k != "step":
+                v.copy_(torch.rand(v.shape) + 0.1)
+        s["step"] = 7
+    torch.save(opt.state_dict(), tmp_path / "state")
+    other = AdamW([{"params": [p.clone()]}, {"params": [q.clone()], "state_bits": 8}])
+    other.load_state_dict(torch.load(tmp_path / "state"))
+    assert other.lr == 0.25 and other.param_groups[0]["weight_decay"] == 0.0 and other.betas == (0.8, 0.9)
+    for a, b in zip(opt.state.values(), other.state.values()):
+        assert a.keys() == b.keys() and a["step"] == b["step"] == 7
+        assert all(a[k].dtype == b[k].dtype and torch.equal(a[k].float(), b[k].float()) for k in a if k != "step")
+    with pytest.raises(ValueError, match="state_bits"):
+        AdamW([{"params": [p]}, {"params": [q]}]).load_state_dict(opt.state_dict())
+    with pytest.raises(ValueError, match="shape"):
+        AdamW([{"params": [p[:5]]}, {"params": [q], "state_bits": 8}]).load_state_dict(opt.state_dict())
+    with pytest.raises(ValueError, match="state_bits must be"):
+        opt.add_param_group({"params": [torch.zeros(3)], "state_bits": 4})
+
+
+def test_optimiser_loads_the_form_without_groups():
+    state = [{"exp_avg": torch.full((5,), 0.5), "exp_avg_sq": torch.full((5,), 0.25)},
+             {"exp_avg": torch.full((2,), 0.1), "exp_avg_sq": torch.full((2,), 0.2)}]
+    for steps in (11, [11, 4]):
+        opt = AdamW([torch.zeros(5), torch.zeros(2)], lr=0.3)
+        opt.load_state_dict({"steps": steps, "state_bits": 32, "state": state})
+        a, b = opt.state.values()
+        assert a["step"] == 11 and b["step"] == (11 if steps == 11 else 4) and opt.lr == 0.3
+        assert torch.equal(a["exp_avg"], state[0]["exp_avg"]) and torch.equal(b["exp_avg_sq"], state[1]["exp_avg_sq"])
+        with pytest.raises(ValueError, match="state_bits"):
+            opt.load_state_dict({"steps": steps, "state_bits": 8, "state": state})
+        with pytest.raises(ValueError, match="parameters"):
+            opt.load_state_dict({"steps": steps if steps == 11 else [3], "state_bits": 32, "state": state[:1]})
+
+
+@pytest.mark.gpu
+def test_optimiser_groups_and_schedule_against_torch():
+    # groups, a scheduler of rates and betas, a closure, and torch's own state taken over half way
+    gen = torch.Generator(device="cuda").manual_seed(8)
+    first = [torch.randn(s, generator=gen, device="cuda") for s in ((300, 7), (64,), (1000,))]
+
+    def build(cls, values):
+        ps = [v.clone().requires_grad_() for v in values]
+        opt = cls([{"params": ps[:1], "weight_decay": 0.0, "eps": 1e-6}, {"params": ps[1:], "lr": 3e-3}], lr=1e-2, weight_decay=0.1)
+        return ps, opt, torch.optim.lr_scheduler.OneCycleLR(opt, max_lr=[2e-2, 1e-2], total_steps=40)
+
+    (mine, a, sa), (theirs, b, sb) = build(AdamW, first), build(torch.optim.AdamW, first)
+    for t in range(30):
+        if t == 15:
+            state = b.state_dict()
+            a.load_state_dict(state)
+        for p, q in zip(mine, theirs):
+            p.grad = torch.randn(p.shape, generator=gen, device="cuda")
+            q.grad = p.grad.clone()
+        assert float(a.step(lambda: torch.tensor(5.0))) == 5.0
+        b.step()
+        sa.step()
+        sb.step()
+        for p, q in zip(mine, theirs):
+            assert float((p - q).abs().max()) <= 3e-6 * float(q.detach().abs().max()), t
+    scale = torch.full((1,), 0.0, device="cuda")
+    a.lr = 0.0
+    before = [p.detach().clone() for p in mine]
+    a.step(scale)   # in the closure's place
+    assert all(torch.equal(p, q) for p, q in zip(mine, before))
+
+
 def spoil(n):
     """Takes freed blocks of n floats and overwrites them."""
     return [torch.full((n,), 3.0, device="cuda") for _ in range(8)]
