@@ -37,6 +37,20 @@ struct Consts {
     float beta1, omb1, beta2, omb2, eps, decay, step_size, rbc2;
 };
 
+// What the random bits of 8-bit codes are formed from: a key of the seed and
+// the step, and the chunks of the list before this table.
+struct Dither {
+    uint32_t lo, hi;
+    int64_t base;
+};
+
+// States in 32 bits, in 8 rounded to nearest, and in 8 rounded at random: up
+// with the probability of the distance to the code below, so that a state's
+// expectation is its value.  To nearest, a root that a step changes by less
+// than half a code (with beta2 = 0.999 every one but the block's largest, which
+// the scale follows) never moves again.
+enum States { kFull, kNearest, kRandom };
+
 constexpr float kE4m3Max = 448.f;
 constexpr float kE4m3Tiny = 0.001953125f;   // 2^-9
 constexpr float kScaleMin = 1e-30f;
@@ -121,10 +135,26 @@ __device__ __forceinline__ float max_or_nan(float a, float b) {
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
     return r;
 }
+// 32 random bits of element c of the list: multiply-xorshift rounds, the key
+// in their midst too, so that no two steps' bits are the same ones reordered.
+__device__ __forceinline__ uint32_t random_bits(uint32_t c, uint32_t lo, uint32_t hi) {
+    uint32_t x = c ^ lo;
+    x = (x ^ (x >> 16)) * 0x7feb352du;
+    x = ((x ^ (x >> 15)) + hi) * 0x846ca68bu;
+    return x ^ (x >> 16);
+}
+// |q| <= 448 or a little above -> the e4m3 value below or above it, by 16 random
+// bits.  The last 20 of its 23 bits go, with 2^-6 added first where the codes
+// stand 2^-9 apart whatever the exponent.  What is a code stays one.
+__device__ __forceinline__ float round_at_random(float q, uint32_t bits16) {
+    const float a = fabsf(q), off = a < 0.015625f ? 0.015625f : 0.f;
+    const uint32_t t = (__float_as_uint(__fadd_rn(a, off)) + (bits16 << 4) + 8u) & 0xfff00000u;
+    return copysignf(__fadd_rn(__uint_as_float(t), -off), q);
+}
 // The codes of a block (a warp's values, zero past its end) and its scale.
 // Blocks of finite values, all but every one, take no care of others.
-template <bool kRoot>
-__device__ __forceinline__ uint2 encode(const float (&f)[kPer], float& scale) {
+template <bool kRoot, bool kAtRandom>
+__device__ __forceinline__ uint2 encode(const float (&f)[kPer], float& scale, const uint32_t (&bits)[kPer]) {
     float top = 0.f;
 #pragma unroll
     for (int j = 0; j < kPer; ++j) top = max_or_nan(top, fabsf(f[j]));
@@ -150,6 +180,7 @@ __device__ __forceinline__ uint2 encode(const float (&f)[kPer], float& scale) {
         for (int k = 0; k < 2; ++k) {
             const float x = f[j + k];
             qe[k] = __fmul_rn(x, inv);
+            if (kAtRandom) qe[k] = round_at_random(qe[k], kRoot ? bits[j + k] >> 16 : bits[j + k] & 0xffffu);
             if (kRoot && x > 0.f) qe[k] = fmaxf(qe[k], least);
             if (!fine && !finite(x)) qe[k] = __int_as_float(0x7fc00000);
         }
@@ -163,11 +194,11 @@ __device__ __forceinline__ bool aligned(const void* p, unsigned a) {
 }
 
 // 8-bit states take 88 instructions an element in long chains (roots, quotients, block maxima), so warps count for more than
-// the few values that spill: 30 M fp32 elements take 109 us with 4 CTAs an SM, 103 with 5, 102 with 6.  32-bit states wait for
+// the few values that spill: 30 M fp32 elements take 109 us with 4 CTAs an SM, 103 with 5, 102 with 6, and 12 more rounded at random.  32-bit states wait for
 // memory, with more loads a warp on their way (200 M bf16: 628 us as the compiler likes, 714 with 5 CTAs).
-template <typename T, bool kEight, int N>
-__global__ void __launch_bounds__(kThreads, kEight ? 6 : 1) adamw_step(const __grid_constant__ Table<N> table, Consts c,
-                                                       const float* __restrict__ grad_scale) {
+template <typename T, States kStates, int N>
+__global__ void __launch_bounds__(kThreads, kStates == kFull ? 1 : 6)
+adamw_step(const __grid_constant__ Table<N> table, Consts c, const float* __restrict__ grad_scale, Dither d) {
     pdl_wait();
     pdl_trigger();
     const int chunk = blockIdx.x;
@@ -188,7 +219,7 @@ __global__ void __launch_bounds__(kThreads, kEight ? 6 : 1) adamw_step(const __g
     load(grad, i, n, aligned(grad, 16), g);
     const bool pw = aligned(param, 16);
     load(param, i, n, pw, p);
-    if constexpr (!kEight) {
+    if constexpr (kStates == kFull) {
         float* ma = static_cast<float*>(t.exp_avg);
         float* va = static_cast<float*>(t.exp_avg_sq);
         const bool mw = aligned(ma, 16), vw = aligned(va, 16);
@@ -217,9 +248,16 @@ __global__ void __launch_bounds__(kThreads, kEight ? 6 : 1) adamw_step(const __g
             update(p[j], gj, m[j], second_moment(__fmul_rn(r[j], r[j]), gj, c), r[j], c);
         }
         store(param, i, n, pw, p);
+        uint32_t bits[kPer] = {};
+        if constexpr (kStates == kRandom) {
+            const int64_t at = (d.base + chunk) * kChunk + threadIdx.x * kPer;
+            const uint32_t lo = d.lo + (uint32_t)(at >> 32) * 0x9e3779b9u;
+#pragma unroll
+            for (int j = 0; j < kPer; ++j) bits[j] = random_bits((uint32_t)at + j, lo, d.hi);
+        }
         float ms, rs;
-        store_codes(ma, i, n, mw, encode<false>(m, ms));
-        store_codes(va, i, n, vw, encode<true>(r, rs));
+        store_codes(ma, i, n, mw, encode<false, kStates == kRandom>(m, ms, bits));
+        store_codes(va, i, n, vw, encode<true, kStates == kRandom>(r, rs, bits));
         if ((threadIdx.x & 31) == 0) {
             t.exp_avg_scale[b] = ms;
             t.exp_avg_sq_scale[b] = rs;
@@ -227,17 +265,17 @@ __global__ void __launch_bounds__(kThreads, kEight ? 6 : 1) adamw_step(const __g
     }
 }
 
-template <typename T, bool kEight, int N>
-zs_status launch_table(const Table<N>& table, const Consts& c, const float* grad_scale, cudaStream_t s) {
+template <typename T, States kStates, int N>
+zs_status launch_table(const Table<N>& table, const Consts& c, const float* grad_scale, const Dither& d, cudaStream_t s) {
     const int chunks = table.first[table.count];
     if (chunks == 0) return ZS_OK;
-    launch(adamw_step<T, kEight, N>, dim3(chunks), dim3(kThreads), 0, s, table, c, grad_scale);
+    launch(adamw_step<T, kStates, N>, dim3(chunks), dim3(kThreads), 0, s, table, c, grad_scale, d);
     return check_launch("zs_adamw_step");
 }
 
 // Cuts the list into tables: kTableMax tensors, or 2^30 chunks, each.
-template <typename T, bool kEight, int N>
-zs_status step_with(const zs_adamw_tensor* tensors, int32_t count, const Consts& c, const float* grad_scale,
+template <typename T, States kStates, int N>
+zs_status step_with(const zs_adamw_tensor* tensors, int32_t count, const Consts& c, const float* grad_scale, Dither d,
                     cudaStream_t s) {
     Table<N> table;
     table.count = 0;
@@ -248,9 +286,10 @@ zs_status step_with(const zs_adamw_tensor* tensors, int32_t count, const Consts&
         const int64_t k = (n + kChunk - 1) / kChunk;
         if (table.count == N || chunks + k > (int64_t(1) << 30)) {
             table.first[table.count] = (int32_t)chunks;
-            const zs_status st = launch_table<T, kEight>(table, c, grad_scale, s);
+            const zs_status st = launch_table<T, kStates>(table, c, grad_scale, d, s);
             if (st != ZS_OK) return st;
             table.count = 0;
+            d.base += chunks;
             chunks = 0;
         }
         table.t[table.count] = tensors[i];
@@ -258,24 +297,29 @@ zs_status step_with(const zs_adamw_tensor* tensors, int32_t count, const Consts&
         chunks += k;
     }
     table.first[table.count] = (int32_t)chunks;
-    return launch_table<T, kEight>(table, c, grad_scale, s);
+    return launch_table<T, kStates>(table, c, grad_scale, d, s);
 }
 
-template <typename T, bool kEight>
-zs_status step(const zs_adamw_tensor* tensors, int32_t count, const Consts& c, const float* grad_scale,
+template <typename T, States kStates>
+zs_status step(const zs_adamw_tensor* tensors, int32_t count, const Consts& c, const float* grad_scale, const Dither& d,
                cudaStream_t s) {
-    if (count <= kTableShort) return step_with<T, kEight, kTableShort>(tensors, count, c, grad_scale, s);
-    return step_with<T, kEight, kTableMax>(tensors, count, c, grad_scale, s);
+    if (count <= kTableShort) return step_with<T, kStates, kTableShort>(tensors, count, c, grad_scale, d, s);
+    return step_with<T, kStates, kTableMax>(tensors, count, c, grad_scale, d, s);
 }
 
-}  // namespace
+template <typename T>
+zs_status step(States states, const zs_adamw_tensor* tensors, int32_t count, const Consts& c, const float* grad_scale,
+               const Dither& d, cudaStream_t s) {
+    switch (states) {
+        case kFull: return step<T, kFull>(tensors, count, c, grad_scale, d, s);
+        case kNearest: return step<T, kNearest>(tensors, count, c, grad_scale, d, s);
+        default: return step<T, kRandom>(tensors, count, c, grad_scale, d, s);
+    }
+}
 
-}  // namespace zs
-
-extern "C" zs_status zs_adamw_step(const zs_adamw_tensor* tensors, int32_t count, int32_t dtype, int32_t state_bits,
-                                   const zs_adamw_hyper* hyper, const float* grad_scale, zs_stream_t stream) {
-    using namespace zs;
-    const char* fn = "zs_adamw_step";
+// seed: NULL rounds to nearest.
+zs_status adamw(const char* fn, const zs_adamw_tensor* tensors, int32_t count, int32_t dtype, int32_t state_bits,
+                const zs_adamw_hyper* hyper, const uint64_t* seed, const float* grad_scale, zs_stream_t stream) {
     if (!known_dtype(dtype)) return fail(ZS_ERR_UNSUPPORTED, "%s: dtype %d is not a zs_dtype", fn, dtype);
     if (state_bits != 32 && state_bits != 8)
         return fail(ZS_ERR_UNSUPPORTED, "%s: states have 32 or 8 bits, not %d", fn, state_bits);
@@ -310,13 +354,35 @@ extern "C" zs_status zs_adamw_step(const zs_adamw_tensor* tensors, int32_t count
     c.step_size = (float)(h.lr / (1.0 - pow(h.beta1, (double)h.step)));
     c.rbc2 = (float)(1.0 / sqrt(1.0 - pow(h.beta2, (double)h.step)));
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const bool eight = state_bits == 8;
+    const States states = state_bits == 32 ? kFull : seed ? kRandom : kNearest;
+    Dither d = {};
+    if (seed) {
+        uint64_t key = *seed ^ ((uint64_t)h.step * 0x9e3779b97f4a7c15ull);
+        for (int i = 0; i < 2; ++i) key = (key ^ (key >> 32)) * 0xd6e8feb86659fd93ull;
+        key ^= key >> 32;
+        d.lo = (uint32_t)key, d.hi = (uint32_t)(key >> 32);
+    }
     switch (dtype) {
-        case ZS_F32: return eight ? step<float, true>(tensors, count, c, grad_scale, s)
-                                  : step<float, false>(tensors, count, c, grad_scale, s);
-        case ZS_BF16: return eight ? step<__nv_bfloat16, true>(tensors, count, c, grad_scale, s)
-                                   : step<__nv_bfloat16, false>(tensors, count, c, grad_scale, s);
-        default: return eight ? step<__half, true>(tensors, count, c, grad_scale, s)
-                              : step<__half, false>(tensors, count, c, grad_scale, s);
+        case ZS_F32: return step<float>(states, tensors, count, c, grad_scale, d, s);
+        case ZS_BF16: return step<__nv_bfloat16>(states, tensors, count, c, grad_scale, d, s);
+        default: return step<__half>(states, tensors, count, c, grad_scale, d, s);
     }
 }
+
+}  // namespace
+
+}  // namespace zs
+
+extern "C" {
+
+zs_status zs_adamw_step(const zs_adamw_tensor* tensors, int32_t count, int32_t dtype, int32_t state_bits,
+                        const zs_adamw_hyper* hyper, const float* grad_scale, zs_stream_t stream) {
+    return zs::adamw("zs_adamw_step", tensors, count, dtype, state_bits, hyper, nullptr, grad_scale, stream);
+}
+
+zs_status zs_adamw_step_seeded(const zs_adamw_tensor* tensors, int32_t count, int32_t dtype, int32_t state_bits,
+                               const zs_adamw_hyper* hyper, uint64_t seed, const float* grad_scale, zs_stream_t stream) {
+    return zs::adamw("zs_adamw_step_seeded", tensors, count, dtype, state_bits, hyper, &seed, grad_scale, stream);
+}
+
+}  // extern "C"

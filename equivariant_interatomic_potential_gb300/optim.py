@@ -32,12 +32,12 @@ class AdamW(torch.optim.Optimizer):
     """
 
     def __init__(self, params, lr: float = 1e-3, betas: tuple[float, float] = (0.9, 0.999), eps: float = 1e-8,
-                 weight_decay: float = 0.01, state_bits: int = 32):
+                 weight_decay: float = 0.01, state_bits: int = 32, seed: int = 0):
         params = list(params)
         if not params:
             raise ValueError("AdamW needs at least one parameter")
         self._plans: dict[tuple, zs.AdamWPlan] = {}
-        super().__init__(params, dict(lr=lr, betas=betas, eps=eps, weight_decay=weight_decay, state_bits=state_bits))
+        super().__init__(params, dict(lr=lr, betas=betas, eps=eps, weight_decay=weight_decay, state_bits=state_bits, seed=seed))
 
     lr, betas, eps, weight_decay = map(_of_groups, _HYPER)
 
@@ -86,7 +86,8 @@ class AdamW(torch.optim.Optimizer):
         # parameters, states and gradients of each set of options, type and number of steps
         alike: dict[tuple, tuple[list, list, list]] = {}
         for group in self.param_groups:
-            options = (float(group["lr"]), *map(float, group["betas"]), group["eps"], group["weight_decay"], group["state_bits"])
+            options = (float(group["lr"]), *map(float, group["betas"]), group["eps"], group["weight_decay"],
+                       group["state_bits"], group["seed"])
             last = into = None
             for p in group["params"]:
                 g = p.grad
@@ -101,9 +102,11 @@ class AdamW(torch.optim.Optimizer):
                 into[2].append(g if g.is_contiguous() else g.contiguous())
         plans = {}
         for (options, _, steps), (params, states, grads) in alike.items():
-            lr, beta1, beta2, eps, decay, bits = options
-            plan = plans[tuple(map(id, params))] = self._plan(params, states, grads, bits)
-            zs.zs_adamw_step(plan, steps + 1, lr=lr, beta1=beta1, beta2=beta2, eps=eps, weight_decay=decay, grad_scale=grad_scale)
+            lr, beta1, beta2, eps, decay, bits, seed = options
+            plan = self._plan(params, states, grads, bits)
+            zs.zs_adamw_step(plan, steps + 1, lr=lr, beta1=beta1, beta2=beta2, eps=eps, weight_decay=decay, grad_scale=grad_scale,
+                             seed=seed + len(plans))   # each launch has random bits of its own
+            plans[tuple(map(id, params))] = plan
             for s in states:
                 s["step"] = steps + 1
             torch.autograd.graph.increment_version(params)
@@ -130,7 +133,7 @@ class AdamW(torch.optim.Optimizer):
                 if s and k != "step" and s[k].shape != v.shape:
                     raise ValueError(f"{k} has shape {tuple(s[k].shape)}, the parameter needs {tuple(v.shape)}")
         # the groups are the base class's to check and take over; it would cast the states to the parameters' types
-        super().load_state_dict({**d, "state": {}, "param_groups": [{"state_bits": 32, **g} for g in d["param_groups"]]})
+        super().load_state_dict({**d, "state": {}, "param_groups": [{"state_bits": 32, "seed": 0, **g} for g in d["param_groups"]]})
         self.state = mine
         for p, s in zip(params, theirs):
             for k, v in mine[p].items():

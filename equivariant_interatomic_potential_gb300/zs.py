@@ -109,6 +109,8 @@ def load(build_if_missing: bool = True):
                                                        I64, I32, P, P, P, P, P, P, P, SZ, P]
         lib.zs_adamw_step.restype = ctypes.c_int
         lib.zs_adamw_step.argtypes = [P, I32, I32, I32, P, P, P]
+        lib.zs_adamw_step_seeded.restype = ctypes.c_int
+        lib.zs_adamw_step_seeded.argtypes = [P, I32, I32, I32, P, ctypes.c_uint64, P, P]
         _lib = lib
         return lib
 
@@ -913,9 +915,13 @@ class AdamWPlan:
 
 
 def zs_adamw_step(plan: AdamWPlan, step: int, lr: float, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,
-                  weight_decay: float = 0.01, grad_scale: torch.Tensor | None = None, stream=None) -> None:
+                  weight_decay: float = 0.01, grad_scale: torch.Tensor | None = None, stream=None,
+                  seed: int | None = None) -> None:
     """One AdamW step (number ``step``, from 1) over the plan's tensors, in place.
-    grad_scale: one float32 element on the device that multiplies every gradient."""
+    grad_scale: one float32 element on the device that multiplies every gradient.
+    8-bit states are rounded to nearest, which leaves a second moment where it is when
+    it shrinks slowly, or with a ``seed`` at random by bits that follow from it and the
+    step, as a training run needs them."""
     scale_ptr = None
     if grad_scale is not None:
         if grad_scale.numel() != 1 or grad_scale.dtype != torch.float32 or grad_scale.device != plan.device:
@@ -925,9 +931,12 @@ def zs_adamw_step(plan: AdamWPlan, step: int, lr: float, beta1: float = 0.9, bet
         _one_device((plan.params[0],), stream.device)
     if plan.device.index != _current_device():   # a launch is the current device's
         with torch.cuda.device(plan.device):
-            return zs_adamw_step(plan, step, lr, beta1, beta2, eps, weight_decay, grad_scale, stream)
+            return zs_adamw_step(plan, step, lr, beta1, beta2, eps, weight_decay, grad_scale, stream, seed)
     hyper = _AdamWHyper(lr, beta1, beta2, eps, weight_decay, step)
-    st = load().zs_adamw_step(plan._table_ptr, len(plan.params), plan.dtype, plan.state_bits, ctypes.addressof(hyper),
-                              scale_ptr, _stream(stream))
+    head = (plan._table_ptr, len(plan.params), plan.dtype, plan.state_bits, ctypes.addressof(hyper))
+    if seed is None:
+        st = load().zs_adamw_step(*head, scale_ptr, _stream(stream))
+    else:
+        st = load().zs_adamw_step_seeded(*head, seed & (1 << 64) - 1, scale_ptr, _stream(stream))
     if st:
         _check("zs_adamw_step", st)
