@@ -316,10 +316,30 @@ struct NormPlace {
 
 // A gate of a whole row.
 __device__ __forceinline__ float sigmoid(float z) { return __frcp_rn(1.f + expf(-z)); }
-// A gate of one element: known to about |z| 2^-24 of itself at z < 0 and better
+// A gate of one element.  In 16 bits (half an ulp 2^-12 or more of what the
+// result is rounded to) known to about |z| 2^-24 of itself at z < 0 and better
 // at z > 0, in a quarter of the instructions (4097 x 1031 fp16: forward 25 ->
-// 19 us, backward 38 -> 34).
-__device__ __forceinline__ float quick_sigmoid(float z) { return __fdividef(1.f, 1.f + __expf(-z)); }
+// 19 us, backward 38 -> 34).  In fp32 -z log2(e) is formed in two parts, of
+// which the second one multiplies the power of two by 1 + part ln(2), so that
+// the error stays at a few ulps whatever z (65536 x 512 fp32: forward 120 us,
+// backward 208; one part 121 and 208, with the functions of a row's gate 138
+// and 252).  Beyond +-100, where the gate is 1 or 0, z does not grow: infinities.
+template <typename T>
+__device__ __forceinline__ float element_sigmoid(float z) {
+    if constexpr (sizeof(T) == 4) {
+        constexpr float kLog2E = 1.4426950408889634f, kRest = 1.4426950408889634 - (double)kLog2E;
+        float e, q;
+        asm("min.NaN.f32 %0, %1, %2;" : "=f"(z) : "f"(z), "f"(100.f));
+        asm("max.NaN.f32 %0, %1, %2;" : "=f"(z) : "f"(z), "f"(-100.f));
+        const float t = -z * kLog2E, rest = fmaf(-z, kRest, fmaf(-z, kLog2E, -t));
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
+        e *= fmaf(rest, 0.6931471805599453f, 1.f);
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(q) : "f"(1.f + e));
+        return q;
+    } else {
+        return __fdividef(1.f, 1.f + __expf(-z));
+    }
+}
 
 // How a row is spread: over as many threads as need nv pieces each, with the
 // largest nv up to `most` unless a smaller one takes a tenth fewer slots.

@@ -98,7 +98,7 @@ __global__ void __launch_bounds__(kNormThreads, kFwdCtas<VEC * NV>) norm_fwd(con
             float z[E];
             ring.open(stage, 2, z);
 #pragma unroll
-            for (int i = 0; i < E; ++i) yv[i] = fmaf(quick_sigmoid(z[i]) * pa[i], centred<kLayer>(v[i], hs.x) * hs.y, yv[i]);
+            for (int i = 0; i < E; ++i) yv[i] = fmaf(element_sigmoid<T>(z[i]) * pa[i], centred<kLayer>(v[i], hs.x) * hs.y, yv[i]);
         } else {
             const float q = s.gate_cols ? sigmoid(to_f32(gate)) : 1.f;
 #pragma unroll
@@ -176,7 +176,7 @@ __global__ void __launch_bounds__(norm_threads(VEC * NV, true), kBwdCtas<VEC * N
         if constexpr (kGate) {
             ring.open(stage, 4, q);
 #pragma unroll
-            for (int i = 0; i < E; ++i) q[i] = quick_sigmoid(q[i]);
+            for (int i = 0; i < E; ++i) q[i] = element_sigmoid<T>(q[i]);
         } else {
             q[0] = s.gate_cols ? sigmoid(to_f32(gate)) : 1.f;
         }

@@ -240,3 +240,17 @@ def test_binding_refusals():
         zs.zs_norm_gate_residual(h, h, None, w, w, w, kind="batch")
     with pytest.raises(ValueError, match="matrix"):
         zs.zs_norm_gate_residual(w, h, None, w, w, w)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("gate", ["full", "row"])
+def test_gates_in_32_bits(gate):
+    # With x = 0 and h = 1, y is the gate.  An exponential known to 2 ulps, a sum, a reciprocal, a root known to 2 and
+    # three products: 2^-20 of the result, for gates far below zero too.
+    C = 96
+    z = torch.linspace(-80.0, 20.0, 64 * C).reshape(64, C)
+    z = z if gate == "full" else z[:, :1].contiguous()
+    ones, zeros, vec = torch.ones(64, C), torch.zeros(64, C), torch.ones(C)
+    y, _, _ = zs.zs_norm_gate_residual(*cuda([ones, zeros, z, vec, vec, vec]), eps=0.0)
+    want = 1.0 / (1.0 + np.exp(-f64(z)))
+    assert (np.abs(f64(y) - want) <= 2.0 ** -20 * want).all()
