@@ -422,3 +422,51 @@ def test_gathered_rows_put_in_order(M, K, N, G, dtype):
     assert not bool(torch.isfinite(y[sick]).any()) and not bool(torch.isfinite(dw[0]).any())
     assert all(torch.equal(torch.nan_to_num(a), torch.nan_to_num(b))
                for a, b in zip(run(group, G, x.cuda(), w.cuda(), dy.cuda()), (y, dx, dw)))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("K,N", [(64, 96), (65, 131)])
+def test_fp32_products_of_one_term(K, N):
+    """fp32 on the tensor cores, sums of one term that is not zero: what is left of the
+    three planes of 8 bits.  Planes rounded to nearest leave at most 2^-8 and 2^-17 of a
+    value in [1, 2), so the products left out are below 2^-24 of the term, of either sign;
+    the joining of the three partial sums rounds twice, the second time once at most."""
+    M, rng = 700, np.random.default_rng(3)
+
+    def some(*shape):
+        bits = rng.integers(0x3f800000, 0x40000000, shape, dtype=np.uint32)
+        hard = np.array([0x3f80ffff, 0x3f807f40, 0x3f837bbe, 0x3f8590c0, 0x3fffffff, 0x3f817fff], np.uint32)
+        return np.where(rng.random(shape) < 0.3, rng.choice(hard, shape), bits).view(np.float32)
+
+    def check(got, want, what):
+        err = np.abs(f64(got) - want) / np.where(want == 0, 1, want)
+        assert err.max() <= 2.2 * 2.0 ** -24, f"{what}: {err.max() * 2 ** 24:.2f} x 2^-24"
+
+    one = lambda a: np.where(np.arange(a.shape[1]) == rng.integers(0, a.shape[1], (len(a), 1)), a, 0)  # noqa: E731
+    x, dy, w = one(some(M, K)), one(some(M, N)), some(1, N, K)
+    row_ptr = torch.tensor([0, M], dtype=torch.int32, device="cuda")
+    up = lambda a: torch.from_numpy(a.astype(np.float32)).cuda()  # noqa: E731
+    d = lambda a: a.astype(np.float64)  # noqa: E731
+    check(zs.zs_grouped_matmul(up(x), up(w), row_ptr), d(x) @ d(w[0]).T, "y")
+    check(zs.zs_grouped_matmul_dx(up(dy), up(w), row_ptr), d(dy) @ d(w[0]), "dx")
+    x, dy = some(M, K), some(M, N)
+    x[np.arange(M) != 333] = 0
+    check(zs.zs_grouped_matmul_dw(up(dy), up(x), row_ptr)[0], d(dy).T @ d(x), "dw")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("K,N", [(64, 96), (65, 131)])
+def test_fp32_largest_values(K, N):
+    # values that bf16 would round to infinity are cut off instead; an infinity and a NaN still reach only their rows
+    M, top = 700, float(np.finfo(np.float32).max)
+    x, w = torch.zeros(M, K), torch.zeros(1, N, K)
+    x[:, 3], x[:, 5], w[0, :, 3] = top, -top, 0.75
+    x[7, 3], x[9, 2], x[11, 3] = float("inf"), float("nan"), top / 2
+    row_ptr = torch.tensor([0, M], dtype=torch.int32, device="cuda")
+    y = zs.zs_grouped_matmul(x.cuda(), w.cuda(), row_ptr).cpu()
+    want = torch.full((M, N), 0.75 * top)
+    want[11] = 0.375 * top
+    keep = torch.ones(M, dtype=torch.bool)
+    keep[[7, 9]] = False
+    assert bool(((y - want)[keep].abs() <= 2.0 ** -22 * want[keep]).all())
+    assert not bool(torch.isfinite(y[~keep]).any())
