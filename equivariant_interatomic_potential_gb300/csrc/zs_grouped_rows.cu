@@ -119,7 +119,7 @@ rows_mma(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUte
     constexpr int kBox = Sh::kBox;
     const uint32_t full = kPair ? in_first(set.full) : set.full;   // told to
     const int nk = (a.red + kBox - 1) / kBox;
-    constexpr int kPerChunk = kSums<T> > 1 ? kChunk / kBox : 1 << 30;   // stages between hand-overs to the epilogue
+    constexpr int kPerChunk = (kSums<T> > 1 ? kChunk : kLongSum) / kBox;   // stages between hand-overs to the epilogue
     const int rank = kPair ? (int)cluster_rank() : 0, step = kPair ? gridDim.x / 2 : gridDim.x;
     int item = kPair ? blockIdx.x / 2 : blockIdx.x;
     Item t;
@@ -247,12 +247,13 @@ rows_mma(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUte
         }
     } else if (warp == 1 && rank == 0) {   // of a pair, for both
         RingPos<S> pos;
-        int n = 0;
+        Buffers<T> bufs;
+        int n = 0;   // of chunks (fp32), or tiles
         bool have = next_product(a, gr, item, step, BN, t);   // which tile it is does not matter here
         while (have && !is_dead(dead)) {
             for (int k = 0; k < nk; ++k, pos.next()) {
-                const int buf = n & 1;
-                if (k % kPerChunk == 0) bounded_wait_on<kPair>(set.tempty + 8 * buf, ((n >> 1) & 1) ^ 1, dead);
+                const int buf = (kSums<T> > 1 || k < kPerChunk ? n : n + 1) & 1;
+                if (k % kPerChunk == 0) bounded_wait_on<kPair>(set.tempty + 8 * buf, bufs.of(buf, n) ^ 1, dead);
                 bounded_wait_on<kPair>(set.full + 8 * pos.stage, pos.phase, dead);
                 tc_fence_after();
                 const uint32_t at = smem_u32(ring) + pos.stage * Sh::kStage;
@@ -262,7 +263,8 @@ rows_mma(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUte
                 if (k == 0) have = next_product(a, gr, item, step, BN, t);   // looked for while products run
                 if (k % kPerChunk == kPerChunk - 1 || k == nk - 1) {
                     tc_commit<kPair>(set.tfull + 8 * buf);
-                    ++n;
+                    bufs.used(buf);
+                    if (kSums<T> > 1 || k == nk - 1) ++n;
                 }
             }
         }
@@ -271,7 +273,22 @@ rows_mma(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUte
         const int q = warp & 3, half = (warp - 4) >> 2;
         constexpr int kCols = BN / Sh::kHalves;
         unsigned char* stage = staging + (warp - 4) * kStageWarp;
+        Buffers<T> bufs;
         int n = 0;
+        auto ready = [&](int buf) {
+            if (!bounded_wait(set.tfull + 8 * buf, bufs.of(buf, n), dead)) return false;
+            bufs.used(buf);
+            tc_fence_after();
+            return true;
+        };
+        auto release = [&](int buf) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if (kPair) mbar_arrive_there(in_first(set.tempty + 8 * buf));
+                else mbar_arrive(set.tempty + 8 * buf);
+            }
+        };
         while (!is_dead(dead) && next_item(a, gr, item, step, BN, t)) {
             const int p = t.p0 + kTileM * rank + 32 * q + lane;
             const int r = p < t.p1 ? row_at(a.perm, a.M, p) : -1;
@@ -283,16 +300,16 @@ rows_mma(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUte
             }
             const uint32_t lanes = set.tmem + ((uint32_t)(32 * q) << 16);
             if constexpr (kSums<T> == 1) {
-                const int buf = n & 1;
-                if (!bounded_wait(set.tfull + 8 * buf, (n >> 1) & 1, dead)) break;
-                tc_fence_after();
-                store_tile<T>(lanes + buf * BN, c0, c1, row, a.out_wide, stage, lane);
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    if (kPair) mbar_arrive_there(in_first(set.tempty + 8 * buf));
-                    else mbar_arrive(set.tempty + 8 * buf);
+                const int buf = n & 1, other = buf ^ 1;
+                if (!ready(buf)) break;
+                bool ok = true;
+                for (int k = kPerChunk; k < nk && (ok = ready(other)); k += kPerChunk) {
+                    add_tile(lanes + buf * BN, lanes + other * BN, c0, c0 + kCols);
+                    release(other);
                 }
+                if (!ok) break;
+                store_tile<T>(lanes + buf * BN, c0, c1, row, a.out_wide, stage, lane);
+                release(buf);
                 ++n;
             } else {
                 static_assert(kSums<T> == 1 || kCols == 32, "a warp's columns of an fp32 tile fit one register array");
@@ -302,13 +319,10 @@ rows_mma(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUte
                 bool ok = true;
                 for (int k = 0; k < nk; k += kPerChunk, ++n) {
                     const int buf = n & 1;
-                    if (!(ok = bounded_wait(set.tfull + 8 * buf, (n >> 1) & 1, dead))) break;
-                    tc_fence_after();
+                    if (!(ok = ready(buf))) break;
                     const uint32_t from = lanes + buf * kSums<T> * BN + c0;
                     add_chunk(from, BN, acc);
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(set.tempty + 8 * buf);
+                    release(buf);
                 }
                 if (!ok) break;
                 if (c0 < c1) emit32<T>(acc, c1 - c0, row ? row + c0 : nullptr, a.out_wide, stage, lane);

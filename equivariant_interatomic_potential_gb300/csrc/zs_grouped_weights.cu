@@ -54,7 +54,7 @@ weights_mma(const __grid_constant__ CUtensorMap dy_map, const __grid_constant__ 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     Walk<T, BN> walk(a, set.groups);
     Segment s;
-    constexpr int kPerChunk = kSums<T> > 1 ? kChunk : 1 << 30;   // positions between hand-overs to the epilogue
+    constexpr int kPerChunk = kSums<T> > 1 ? kChunk : kLongSum;   // positions between hand-overs to the epilogue
 
     if (kTma && warp == 0 && !a.perm) {
         RingPos<S> pos;
@@ -160,22 +160,25 @@ weights_mma(const __grid_constant__ CUtensorMap dy_map, const __grid_constant__ 
         }
     } else if (warp == 1) {
         RingPos<S> pos;
-        int n = 0;
+        Buffers<T> bufs;
+        int n = 0;   // of chunks (fp32), or segments
+        auto buffer_of = [&](int p) { return (kSums<T> > 1 || p - s.p0 < kPerChunk ? n : n + 1) & 1; };
         // a stage's products
         auto products = [&](int p) {
-            const int buf = n & 1, since = (p - s.p0) % kPerChunk, steps = (imin(kUnit, s.p1 - p) + 15) / 16;
+            const int buf = buffer_of(p), since = (p - s.p0) % kPerChunk, steps = (imin(kUnit, s.p1 - p) + 15) / 16;
             const uint32_t at = smem_u32(ring) + pos.stage * Sh::kStage;
             tc_fence_after();
             issue_stage<T, true, true, BN>(set.tmem + buf * kSums<T> * BN, at, Sh::kA, Sh::kBox, at + Sh::P * Sh::kA, Sh::kBox,
                                            steps, since > 0, set.empty + 8 * pos.stage);
             if (since + kUnit >= kPerChunk || p + kUnit >= s.p1) {
                 tc_commit<false>(set.tfull + 8 * buf);
-                ++n;
+                bufs.used(buf);
+                if (kSums<T> > 1 || p + kUnit >= s.p1) ++n;
             }
         };
         auto ready = [&](int p) {
-            const int buf = n & 1;
-            if ((p - s.p0) % kPerChunk == 0) bounded_wait_on(set.tempty + 8 * buf, ((n >> 1) & 1) ^ 1, dead);
+            const int buf = buffer_of(p);
+            if ((p - s.p0) % kPerChunk == 0) bounded_wait_on(set.tempty + 8 * buf, bufs.of(buf, n) ^ 1, dead);
             bounded_wait_on(set.full + 8 * pos.stage, pos.phase, dead);
         };
         while (!is_dead(dead) && walk.next(s)) {
@@ -202,7 +205,19 @@ weights_mma(const __grid_constant__ CUtensorMap dy_map, const __grid_constant__ 
         constexpr int kMine = BN / Sh::kHalves;
         unsigned char* stage = staging + (warp - 4) * kStageWarp;
         const uint32_t lanes = set.tmem + ((uint32_t)(32 * q) << 16);
+        Buffers<T> bufs;
         int n = 0;
+        auto ready = [&](int buf) {
+            if (!bounded_wait(set.tfull + 8 * buf, bufs.of(buf, n), dead)) return false;
+            bufs.used(buf);
+            tc_fence_after();
+            return true;
+        };
+        auto release = [&](int buf) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(set.tempty + 8 * buf);
+        };
         while (!is_dead(dead) && walk.next(s)) {
             const bool some = s.p0 < s.p1, mine = s.n0 + r < a.N;
             const int c0 = half * kMine, c1 = imin(c0 + kMine, a.K - s.k0);
@@ -210,18 +225,18 @@ weights_mma(const __grid_constant__ CUtensorMap dy_map, const __grid_constant__ 
             float* part = mine ? a.partial + (((int64_t)blockIdx.x * 2 + s.part) * kTileM + r) * BN : nullptr;
             const int c1_part = imin((c1 + 3) / 4 * 4, c0 + kMine);   // whole pieces of a partial tile's rows
             if constexpr (kSums<T> == 1) {
-                const int buf = n & 1;
-                if (some) {
-                    if (!bounded_wait(set.tfull + 8 * buf, (n >> 1) & 1, dead)) break;
-                    tc_fence_after();
+                const int buf = n & 1, other = buf ^ 1;
+                bool ok = !some || ready(buf);
+                for (int done = kPerChunk; done < s.p1 - s.p0 && (ok = ok && ready(other)); done += kPerChunk) {
+                    add_tile(lanes + buf * BN, lanes + other * BN, c0, c0 + kMine);
+                    release(other);
                 }
+                if (!ok) break;
                 const uint32_t from = some ? lanes + buf * BN : kNoTile;
                 if (s.whole) store_tile<T>(from, c0, c1, row, a.dw_wide, stage, lane);
                 else store_tile<float>(from, c0, c1_part, part, true, stage, lane);
                 if (some) {
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(set.tempty + 8 * buf);
+                    release(buf);
                     ++n;
                 }
             } else {
@@ -232,13 +247,10 @@ weights_mma(const __grid_constant__ CUtensorMap dy_map, const __grid_constant__ 
                 bool ok = true;
                 for (int p = s.p0; p < s.p1; p += kPerChunk, ++n) {
                     const int buf = n & 1;
-                    if (!(ok = bounded_wait(set.tfull + 8 * buf, (n >> 1) & 1, dead))) break;
-                    tc_fence_after();
+                    if (!(ok = ready(buf))) break;
                     const uint32_t from = lanes + buf * kSums<T> * BN + c0;
                     add_chunk(from, BN, acc);
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(set.tempty + 8 * buf);
+                    release(buf);
                 }
                 if (!ok) break;
                 if (c0 >= c1) continue;

@@ -52,6 +52,11 @@ constexpr uint32_t kDrainSpins = 1u << 16;
 constexpr int kEpilogueWarps = 8;              // two for each 32 TMEM lanes
 constexpr int kLoaderWarps = 8;                // of each of the two groups that take stages in turn
 constexpr int kChunk = 128;                    // elements summed in TMEM at a time for fp32 operands
+// Of 16-bit operands.  512 additions that truncate leave a sum of one sign up to
+// 2^-14 low (5e-5 as measured), an eighth of half an ulp of fp16; a sum of 65536
+// in one piece came out 4.3e-4 low, of 262144 1.7e-3.  Longer sums pass to the
+// epilogue every kLongSum elements, which adds them up in TMEM.
+constexpr int kLongSum = 8192;
 template <typename T>
 constexpr int kPlanes = sizeof(T) == 4 ? 3 : 1;
 template <typename T>
@@ -242,6 +247,13 @@ __device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t (&r)[16]) {
                    "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
                  : "r"(addr) : "memory");
 }
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 "
+                 "[%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
+                 :: "r"(addr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+                    "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]) : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
 // Where 16-byte piece c of row r sits in a box.
@@ -589,6 +601,34 @@ __device__ __forceinline__ void store_tile(uint32_t tmem, int c0, int c1, TO* ro
         emit32<TO>(f, imin(32, c1 - c), row ? row + c : nullptr, wide, stage, lane);
     }
 }
+
+// Columns [c0, c1) of the tile at `to` += those at `from`, rounded to nearest.
+__device__ __forceinline__ void add_tile(uint32_t to, uint32_t from, int c0, int c1) {
+#pragma unroll 1
+    for (int c = c0; c < c1; c += 16) {
+        uint32_t a[16], b[16];
+        tmem_ld16(to + c, a);
+        tmem_ld16(from + c, b);
+        tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) a[i] = __float_as_uint(__uint_as_float(a[i]) + __uint_as_float(b[i]));
+        tmem_st16(to + c, a);
+    }
+    tmem_st_wait();
+}
+
+// The two buffers of a tile's sums in TMEM, as both sides go through them: the
+// parity of the barriers of each one's fill.  fp32 operands take them in turn, a
+// chunk each.  A 16-bit tile starts in the one that the tile before did not, and
+// the other one takes what comes after kLongSum elements, over and over.
+template <typename T>
+struct Buffers {
+    uint32_t parity = 0;   // bit b: of buffer b
+    __device__ __forceinline__ uint32_t of(int b, int n) const { return (kSums<T> > 1 ? n >> 1 : parity >> b) & 1; }
+    __device__ __forceinline__ void used(int b) {
+        if (kSums<T> == 1) parity ^= 1u << b;
+    }
+};
 
 // acc += the three sums, `apart` columns from each other, of 32 columns of an
 // fp32 product's chunk, the smallest first; 16 columns at a time, for the

@@ -470,3 +470,76 @@ def test_fp32_largest_values(K, N):
     keep[[7, 9]] = False
     assert bool(((y - want)[keep].abs() <= 2.0 ** -22 * want[keep]).all())
     assert not bool(torch.isfinite(y[~keep]).any())
+
+
+def spread(*shape, gen, dtype):
+    """Values of one sign whose roundings go either way."""
+    return (torch.rand(shape, generator=gen, device="cuda") * 0.1 + 0.05).to(dtype)
+
+
+def low(got, want):
+    """The mean relative error over as many elements as average their roundings out."""
+    err = (got.double() - want) / want
+    assert float(err.abs().max()) <= 2.0 ** -7
+    return abs(float(err.mean()))
+
+
+LOW = 1e-4   # 512 additions, each up to an ulp of fp32 low: 2^-14, and what is left of the roundings' mean
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("M,K,N,gathered", [(1024, 65536, 1024, False), (1024, 65528, 1024, True), (600, 40000, 100, True),
+                                            (200, 32769, 136, True), (1024, 8200, 1024, False)])
+def test_long_sums_over_columns(M, K, N, gathered, dtype):
+    # sums of 16-bit products of one sign, much longer than the tensor cores' truncating additions bear
+    gen = torch.Generator(device="cuda").manual_seed(K)
+    x, w, dy = (spread(*s, gen=gen, dtype=TORCH[dtype]) for s in ((M, K), (1, N, K), (M, K)))
+    w.mul_((torch.rand(1, N, 1, generator=gen, device="cuda") + 1).to(w.dtype))
+    row_ptr = torch.tensor([0, M], dtype=torch.int32, device="cuda")
+    perm = torch.randperm(M, generator=gen, device="cuda").int() if gathered else None
+    y = zs.zs_grouped_matmul(x, w, row_ptr, perm)
+    wt = w.transpose(1, 2).contiguous()      # (1, K, N): dx of rows of K sums over K
+    dx = zs.zs_grouped_matmul_dx(dy, wt, row_ptr, perm)
+    torch.cuda.synchronize()
+    zs.zs_check_timeouts()
+    assert low(y, x.double() @ w[0].double().T) <= LOW
+    assert low(dx, dy.double() @ w[0].double().T) <= LOW
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("M,K,N,gathered", [(65536, 2560, 2048, False), (100000, 2560, 2048, True), (70001, 1283, 2048, True)])
+def test_long_sums_over_rows(M, K, N, gathered, dtype):
+    # the weight gradient of one group of many rows, for as many tiles as SMs and more: a CTA sums a whole tile
+    gen = torch.Generator(device="cuda").manual_seed(M)
+    x, dy = (spread(*s, gen=gen, dtype=TORCH[dtype]) for s in ((M, K), (M, N)))
+    dy.mul_((torch.rand(1, N, generator=gen, device="cuda") + 1).to(dy.dtype))
+    row_ptr = torch.tensor([0, M], dtype=torch.int32, device="cuda")
+    perm = torch.randperm(M, generator=gen, device="cuda").int() if gathered else None
+    dw = zs.zs_grouped_matmul_dw(dy, x, row_ptr, perm)[0]
+    torch.cuda.synchronize()
+    zs.zs_check_timeouts()
+    assert low(dw[:, :200], dy.double().T @ x[:, :200].double()) <= LOW
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M", [8191, 8192, 8193, 16384, 16400, 24577])
+def test_sums_about_the_long_ones(M):
+    # several groups, whole and cut ones, their sums one chunk, one row more, or several chunks long
+    rng = np.random.default_rng(M)
+    group = np.concatenate([np.zeros(M, int), np.full(500, 1), np.full(9000, 2)])
+    rows, K, N = len(group), 264, 1100
+    x, xd = held(rng.standard_normal((rows, K)), "bf16")
+    dy, dyd = held(rng.standard_normal((rows, N)), "bf16")
+    row_ptr = torch.from_numpy(csr(group, 4)[0]).cuda()
+    perm = rng.permutation(rows)
+    for pm in (None, torch.from_numpy(perm.astype(np.int32)).cuda()):
+        at = (lambda t: t.cuda()) if pm is None else (lambda t: t[torch.from_numpy(np.argsort(perm))].cuda())
+        dw = zs.zs_grouped_matmul_dw(at(dy), at(x), row_ptr, pm)
+        torch.cuda.synchronize()
+        zs.zs_check_timeouts()
+        for g in range(3):
+            r = group == g
+            close(dw[g], dyd[r].T @ xd[r], np.abs(dyd[r]).T @ np.abs(xd[r]), "bf16", f"dw[{g}]")
+        assert not bool(dw[3].any())
