@@ -52,11 +52,13 @@ constexpr uint32_t kDrainSpins = 1u << 16;
 constexpr int kEpilogueWarps = 8;              // two for each 32 TMEM lanes
 constexpr int kLoaderWarps = 8;                // of each of the two groups that take stages in turn
 constexpr int kChunk = 128;                    // elements summed in TMEM at a time for fp32 operands
-// Of 16-bit operands.  512 additions that truncate leave a sum of one sign up to
-// 2^-14 low (5e-5 as measured), an eighth of half an ulp of fp16; a sum of 65536
-// in one piece came out 4.3e-4 low, of 262144 1.7e-3.  Longer sums pass to the
-// epilogue every kLongSum elements, which adds them up in TMEM.
-constexpr int kLongSum = 8192;
+// Of 16-bit operands.  128 additions that truncate leave a sum of one sign up to
+// 2^-16 low (1.3e-5 as measured), a thirtieth of half an ulp of fp16; a sum of
+// 65536 in one piece came out 4.3e-4 low, of 262144 1.7e-3.  Longer sums pass to
+// the epilogue every kLongSum elements, which adds them up in TMEM (32768 rows,
+// 1024 -> 4096 bf16, us of dx and dw with 8192: 185 and 237; 2048: 186 and 242;
+// 1024: 191 and 248).
+constexpr int kLongSum = 2048;
 template <typename T>
 constexpr int kPlanes = sizeof(T) == 4 ? 3 : 1;
 template <typename T>

@@ -484,7 +484,7 @@ def low(got, want):
     return abs(float(err.mean()))
 
 
-LOW = 1e-4   # 512 additions, each up to an ulp of fp32 low: 2^-14, and what is left of the roundings' mean
+LOW = 1e-4   # each of 128 additions is up to an ulp of fp32 low, 2^-16 in all; and what is left of the roundings' mean
 
 
 @pytest.mark.gpu
