@@ -34,10 +34,13 @@ bool encode_boxes(CUtensorMap* map, bool bf16, const void* p, int64_t cols, int6
 
 namespace {
 
+// Rows and columns a tile or a chunk past the last one are still numbers of 32 bits.
+constexpr int64_t kMostSide = (int64_t(1) << 31) - (1 << 16);
+
 zs_status check(const char* fn, int32_t dtype, int64_t M, int32_t K, int32_t N, int32_t G, const int32_t* row_ptr,
                 const int32_t* perm, std::initializer_list<const void*> arrays) {
     if (!known_dtype(dtype)) return fail(ZS_ERR_UNSUPPORTED, "%s: dtype %d is not a zs_dtype", fn, dtype);
-    if (M < 0 || M >= (int64_t(1) << 31) || K < 1 || N < 1 || G < 0)
+    if (M < 0 || M > kMostSide || K < 1 || K > kMostSide || N < 1 || N > kMostSide || G < 0)
         return fail(ZS_ERR_INVALID_ARG, "%s: M=%lld K=%d N=%d G=%d", fn, (long long)M, K, N, G);
     if (!row_ptr) return fail(ZS_ERR_INVALID_ARG, "%s: row_ptr is NULL", fn);
     if ((reinterpret_cast<uintptr_t>(row_ptr) | reinterpret_cast<uintptr_t>(perm)) & 3)
@@ -148,7 +151,7 @@ zs_status zs_grouped_matmul_dx(int32_t dtype, const void* dy, int64_t dy_ld, con
 
 size_t zs_grouped_matmul_workspace_bytes(int32_t dtype, int64_t M, int32_t K, int32_t N, int32_t G) {
     using namespace zs;
-    if (!known_dtype(dtype) || M < kPadRows || M >= (int64_t(1) << 31) || K < 1 || N < 1 || G < 1 || grouped_is_small(K, N)) return 0;
+    if (!known_dtype(dtype) || M < kPadRows || M > kMostSide || K < 1 || N < 1 || G < 1 || grouped_is_small(K, N)) return 0;
     const bool k = padded(dtype, K) != K, n = padded(dtype, N) != N;
     return (k ? padded_bytes(dtype, (int64_t)G * N, K) : 0) +
            imax(k || order_rows(dtype, N) ? padded_bytes(dtype, M, K) : 0, n || order_rows(dtype, K) ? padded_bytes(dtype, M, N) : 0);
@@ -169,7 +172,7 @@ zs_status zs_grouped_matmul_dx_ws(int32_t dtype, const void* dy, int64_t dy_ld, 
 }
 
 size_t zs_grouped_matmul_dw_workspace_bytes(int32_t dtype, int64_t M, int32_t K, int32_t N, int32_t G) {
-    if (!zs::known_dtype(dtype) || M < 0 || M >= (int64_t(1) << 31) || K < 1 || N < 1 || G < 1) return 0;
+    if (!zs::known_dtype(dtype) || M < 0 || M > kMostSide || K < 1 || N < 1 || G < 1) return 0;
     using namespace zs;
     if (grouped_is_few(dtype, 2, M, N, G)) return 0;
     return grouped_weights_workspace(dtype, M, K, N, G);
@@ -177,7 +180,7 @@ size_t zs_grouped_matmul_dw_workspace_bytes(int32_t dtype, int64_t M, int32_t K,
 
 size_t zs_grouped_matmul_dw_copy_bytes(int32_t dtype, int64_t M, int32_t K, int32_t N, int32_t G) {
     using namespace zs;
-    if (!known_dtype(dtype) || M < kPadRows || M >= (int64_t(1) << 31) || K < 1 || N < 1 || G < 1 || grouped_is_small(K, N) ||
+    if (!known_dtype(dtype) || M < kPadRows || M > kMostSide || K < 1 || N < 1 || G < 1 || grouped_is_small(K, N) ||
         grouped_is_few(dtype, 2, M, N, G))
         return 0;
     const bool both = order_both(dtype, K, N);

@@ -348,7 +348,7 @@ zs_status grouped_weights(const char* fn, int32_t dtype, const void* dy, int64_t
     auto at = [&](const void* p, int bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; };
     const bool tma = dtype != ZS_F32 && at(dy, 16) && dy_ld % per16 == 0 && at(x, 16) && x_ld % per16 == 0 && M > 0;
     const WeightPlan p = weight_plan(dtype, tma, M, K, N, G);
-    if (p.units >= (int64_t(1) << 31) - (1 << 24)) return fail(ZS_ERR_INVALID_ARG, "%s: %lld units", fn, (long long)p.units);
+    if (p.units + p.per >= int64_t(1) << 31) return fail(ZS_ERR_INVALID_ARG, "%s: %lld units", fn, (long long)p.units);
     WeightArgs a = {};
     a.dy = {dy, dy_ld, N, at(dy, 16) && dy_ld % per16 == 0};
     a.x = {x, x_ld, K, at(x, 16) && x_ld % per16 == 0};

@@ -347,8 +347,8 @@ typedef enum zs_dtype {
  *                    gives them; NULL: position p is row p
  *   y (M, N)         rows y_ld elements apart (y_ld >= N), fully written:
  *                    rows at positions >= row_ptr[G] (no group) are zeros
- * M < 2^31, any K >= 1, N >= 1, G >= 0.  Values outside a row's own group
- * never reach its result.  Sums are in fp32 in a fixed order for given sizes;
+ * M, K and N up to 2^31 - 2^16, K >= 1, N >= 1, G >= 0.  Values outside a
+ * row's own group never reach its result.  Sums are in fp32 in a fixed order for given sizes;
  * an fp32 value that is not finite gives NaN in the results that it reaches.
  */
 ZS_API zs_status zs_grouped_matmul(int32_t dtype, const void* x, int64_t x_ld, const void* w,

@@ -321,6 +321,24 @@ def test_argument_checks():
     assert lib.zs_grouped_matmul_dw_workspace_bytes(9, 10, 32, 48, 3) == 0
 
 
+def test_sizes_past_32_bits_refused():
+    # positions, columns and units of work a tile or a range past the last one have to stay below 2^31; all of these
+    # are refused before anything is launched
+    lib, most = zs.load(), (1 << 31) - (1 << 16)
+
+    def product(fn, M=10, K=32, N=48):
+        return fn(1, FAKE, max(K, N), FAKE, FAKE, None, M, K, N, 1, FAKE, max(K, N), None)
+
+    def dw(M=10, K=32, N=48):
+        return lib.zs_grouped_matmul_dw(1, FAKE, N, FAKE, K, FAKE, None, M, K, N, 1, FAKE, FAKE, 1 << 40, None)
+
+    for side in ("M", "K", "N"):
+        for call in (lambda **kw: product(lib.zs_grouped_matmul, **kw), lambda **kw: product(lib.zs_grouped_matmul_dx, **kw), dw):
+            assert call(**{side: most + 1}) == INVALID and call(**{side: (1 << 31) - 1}) == INVALID, side
+    # 24601 tiles of 86610 units: fewer than 2^31 - 2^24 of them, but the last range of 17322000 would end past 2^31
+    assert dw(M=64 * 86608, K=337 * 256, N=73 * 128) == INVALID and b"units" in lib.zs_last_error()
+
+
 def test_binding_refusals():
     x, w = torch.zeros(4, 8), torch.zeros(2, 6, 8)
     rp = torch.zeros(3, dtype=torch.int32)
