@@ -172,7 +172,7 @@ zs_status zs_grouped_matmul_dx_ws(int32_t dtype, const void* dy, int64_t dy_ld, 
 }
 
 size_t zs_grouped_matmul_dw_workspace_bytes(int32_t dtype, int64_t M, int32_t K, int32_t N, int32_t G) {
-    if (!zs::known_dtype(dtype) || M < 0 || M > kMostSide || K < 1 || N < 1 || G < 1) return 0;
+    if (!zs::known_dtype(dtype) || M < 0 || M > zs::kMostSide || K < 1 || N < 1 || G < 1) return 0;
     using namespace zs;
     if (grouped_is_few(dtype, 2, M, N, G)) return 0;
     return grouped_weights_workspace(dtype, M, K, N, G);
