@@ -109,6 +109,8 @@ zs_status grouped_pad(const char* fn, int32_t dtype, const Padding (&p)[2], cuda
     int64_t blocks[2];
     for (int i = 0; i < 2; ++i) {
         PadMatrix& m = a.m[i];
+        blocks[i] = 0;
+        if (p[i].rows == 0) continue;
         m.src = static_cast<const char*>(p[i].src);
         m.dst = static_cast<char*>(p[i].dst);
         m.perm = p[i].perm;
@@ -116,7 +118,7 @@ zs_status grouped_pad(const char* fn, int32_t dtype, const Padding (&p)[2], cuda
         m.rows = p[i].rows;
         m.cols = p[i].cols * es;
         m.pieces = (m.cols + 15) / 16;
-        m.per_block = imax(1, kThreads * kPerThread / imax(1, m.pieces));
+        m.per_block = imax(1, kThreads * kPerThread / m.pieces);
         // exact for p < 1024: p pieces < 2^32
         m.inverse = m.per_block > 1 ? (uint32_t)(((uint64_t(1) << 32) + m.pieces - 1) / m.pieces) : 0;
         blocks[i] = (m.rows + m.per_block - 1) / m.per_block;

@@ -335,8 +335,15 @@ def test_sizes_past_32_bits_refused():
     for side in ("M", "K", "N"):
         for call in (lambda **kw: product(lib.zs_grouped_matmul, **kw), lambda **kw: product(lib.zs_grouped_matmul_dx, **kw), dw):
             assert call(**{side: most + 1}) == INVALID and call(**{side: (1 << 31) - 1}) == INVALID, side
-    # 24601 tiles of 86610 units: fewer than 2^31 - 2^24 of them, but the last range of 17322000 would end past 2^31
-    assert dw(M=64 * 86608, K=337 * 256, N=73 * 128) == INVALID and b"units" in lib.zs_last_error()
+    # 24601 tiles of 87202 units: fewer than 2^31 of them, but not with one range more
+    assert dw(M=64 * 87200, K=337 * 256, N=73 * 128) == INVALID and b"units" in lib.zs_last_error()
+
+
+def test_nothing_to_lay_out():
+    # operands of whole 16-byte pieces, and a size that is refused after the laying out was looked at, before any
+    # launch: on the way the host divided by the zero pieces of the matrix that is not there, which x86 traps
+    assert zs.load().zs_grouped_matmul_dw(1, FAKE, 9344, FAKE, 86272, FAKE, None, 64 * 87200, 86272, 9344, 1, FAKE, FAKE,
+                                          1 << 40, None) == INVALID
 
 
 def test_binding_refusals():
