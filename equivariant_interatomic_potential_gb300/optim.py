@@ -76,7 +76,10 @@ class AdamW(torch.optim.Optimizer):
     def step(self, closure=None, grad_scale: torch.Tensor | None = None):
         """One step.  closure: evaluates the loss again, which is returned.  grad_scale: one
         float32 element on the device that multiplies every gradient (also taken in the
-        closure's place)."""
+        closure's place).  Not while a graph is captured: the step's number, rates and
+        addresses would be those of the capture in every replay."""
+        if torch.cuda.is_current_stream_capturing():
+            raise RuntimeError("an optimiser step cannot be captured: its number, rates and addresses would stay those of the capture")
         loss = None
         if isinstance(closure, torch.Tensor):
             closure, grad_scale = None, closure

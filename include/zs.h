@@ -498,7 +498,8 @@ typedef struct zs_adamw_hyper {
  *   grad_scale   (1,) fp32 on the device, may be NULL (1): the reciprocal of a
  *                loss scale, a clipping factor
  * The arrays of one call must not overlap.  Tensors of any element alignment;
- * 16-byte aligned ones take wide loads.
+ * 16-byte aligned ones take wide loads.  Captured in a graph, a call replays with
+ * the step, the rates and the addresses of its capture.
  * Rounded to nearest, a code moves only where a step changes its value by more
  * than half the distance to the next code, about 3 to 6 %: with beta2 = 0.999 no
  * root ever falls against the largest of its block, and a first moment may

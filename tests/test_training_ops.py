@@ -235,6 +235,24 @@ def test_optimiser_groups_and_schedule_against_torch():
     assert all(torch.equal(p, q) for p, q in zip(mine, before))
 
 
+@pytest.mark.gpu
+@pytest.mark.filterwarnings("ignore:The CUDA Graph is empty")
+def test_optimiser_step_is_not_captured():
+    p = torch.ones(100, device="cuda")
+    p.grad = torch.ones(100, device="cuda")
+    opt = AdamW([p])
+    opt.step()
+    before, s = p.clone(), torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s), torch.cuda.graph(torch.cuda.CUDAGraph(), stream=s):
+        with pytest.raises(RuntimeError, match="captured"):
+            opt.step()
+    torch.cuda.synchronize()
+    assert torch.equal(p, before) and opt.state[p]["step"] == 1
+    opt.step()
+    assert not torch.equal(p, before)
+
+
 def spoil(n):
     """Takes freed blocks of n floats and overwrites them."""
     return [torch.full((n,), 3.0, device="cuda") for _ in range(8)]
