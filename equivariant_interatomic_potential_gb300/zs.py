@@ -12,6 +12,7 @@ import importlib.util
 import os
 import re
 import threading
+import warnings
 
 import torch
 
@@ -116,17 +117,27 @@ def load(build_if_missing: bool = True):
 
 
 class _Fast:
-    """zs_torch.so, the short way for ordinary operands; loaded on first use."""
+    """zs_torch, the short way for ordinary operands; built if need be and loaded on first
+    use.  Where that fails, every call is left to the binding."""
+
+    NAMES = ("matmul", "dw", "norm", "norm_backward")
 
     def __getattr__(self, name):
+        if name not in self.NAMES:
+            raise AttributeError(name)
         lib = load()
-        spec = importlib.util.spec_from_file_location("zs_torch", _build.EXT)
-        ext = importlib.util.module_from_spec(spec)
-        spec.loader.exec_module(ext)
-        names = [n for n in declared_functions() if n.startswith(("zs_grouped", "zs_norm"))]
-        ext.bind({n: ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names}, _check)
-        for n in ("matmul", "dw", "norm", "norm_backward"):
-            setattr(self, n, getattr(ext, n))
+        try:
+            spec = importlib.util.spec_from_file_location("zs_torch", _build.build_ext())
+            ext = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(ext)
+            names = [n for n in declared_functions() if n.startswith(("zs_grouped", "zs_norm"))]
+            ext.bind({n: ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names}, _check)
+            calls = {n: getattr(ext, n) for n in self.NAMES}
+        except Exception as e:
+            warnings.warn(f"zs_torch cannot be used, calls of the training operators take longer on the host: {e}")
+            calls = dict.fromkeys(self.NAMES, lambda *operands: NotImplemented)
+        for n, call in calls.items():
+            setattr(self, n, call)
         return getattr(self, name)
 
 
