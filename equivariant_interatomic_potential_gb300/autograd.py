@@ -219,9 +219,9 @@ def _backward_grouped(ctx, dy):
     perm = perm[0] if perm else None
     if ctx.needs_input_grad[0] and ctx.needs_input_grad[1]:
         return (*grouped_matmul_backward(dy, x, w, row_ptr, perm), None, None)
-    if ctx.needs_input_grad[0]:   # fixed weights: the forces' path
-        return grouped_matmul_dx(dy, w, row_ptr, perm), None, None, None
-    return None, grouped_matmul_backward(dy, x, w, row_ptr, perm)[1], None, None
+    dx = grouped_matmul_dx(dy, w, row_ptr, perm) if ctx.needs_input_grad[0] else None   # fixed weights: the forces' path
+    dw = grouped_matmul_dw(dy, x, row_ptr, perm) if ctx.needs_input_grad[1] else None
+    return dx, dw, None, None
 
 
 @torch.library.custom_op(f"{_NS}::grouped_matmul_dx", mutates_args=())
@@ -235,6 +235,19 @@ def grouped_matmul_dx(dy: torch.Tensor, w: torch.Tensor, row_ptr: torch.Tensor,
 @grouped_matmul_dx.register_fake
 def _(dy, w, row_ptr, perm=None):
     return dy.new_empty((dy.shape[0], w.shape[2]))
+
+
+@torch.library.custom_op(f"{_NS}::grouped_matmul_dw", mutates_args=())
+def grouped_matmul_dw(dy: torch.Tensor, x: torch.Tensor, row_ptr: torch.Tensor,
+                      perm: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """dw (G, N, K) alone, for the cotangent dy (M, N)."""
+    _cuda_only("grouped_matmul_dw", dy, x, row_ptr)
+    return zs.zs_grouped_matmul_dw(dy.contiguous(), x.contiguous(), row_ptr.contiguous(), perm)
+
+
+@grouped_matmul_dw.register_fake
+def _(dy, x, row_ptr, perm=None):
+    return dy.new_empty((row_ptr.shape[0] - 1, dy.shape[1], x.shape[1]))
 
 
 grouped_matmul.register_autograd(_backward_grouped, setup_context=_setup_context_grouped)

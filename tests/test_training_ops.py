@@ -65,6 +65,19 @@ def test_grouped_autograd(needs):
     assert torch.equal(wr.grad, dw) if needs[1] else wr.grad is None
 
 
+def test_gradients_nobody_asked_for_are_not_formed(monkeypatch):
+    # traced with fake tensors: which operators the backward calls
+    def backward_of(needs):
+        x, w = (torch.randn(s, requires_grad=n) for s, n in zip(((7, 8), (3, 5, 8)), needs))
+        f = lambda x, w: torch.autograd.grad(ag.species_linear(x, w, torch.zeros(7, dtype=torch.int32)).sum(),  # noqa: E731
+                                             [t for t in (x, w) if t.requires_grad])
+        nodes = make_fx(f, tracing_mode="fake")(x, w).graph.nodes
+        return sorted(str(n.target) for n in nodes if "grouped_matmul_" in str(n.target))
+
+    dx, dw, both = (f"zs_gie.grouped_matmul_{n}.default" for n in ("dx", "dw", "backward"))
+    assert backward_of((True, False)) == [dx] and backward_of((False, True)) == [dw] and backward_of((True, True)) == [both]
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("gate", ["full", "row", "none"])
 def test_norm_autograd(gate):
