@@ -253,6 +253,47 @@ def _(dy, x, row_ptr, perm=None):
 grouped_matmul.register_autograd(_backward_grouped, setup_context=_setup_context_grouped)
 
 
+# The gradients are products of the same kind, linear in each operand, so that their own gradients are too (a potential
+# trained on its forces differentiates them).
+
+def _backward_grouped_dx(ctx, a):   # of dx = w^T dy, for the cotangent a (M, K)
+    dy, w, row_ptr, *perm = ctx.saved_tensors
+    perm = perm[0] if perm else None
+    return (grouped_matmul(a, w, row_ptr, perm) if ctx.needs_input_grad[0] else None,
+            grouped_matmul_dw(dy, a, row_ptr, perm) if ctx.needs_input_grad[1] else None, None, None)
+
+
+def _backward_grouped_dw(ctx, b):   # of dw = sum dy x^T, for the cotangent b (G, N, K)
+    dy, x, row_ptr, *perm = ctx.saved_tensors
+    perm = perm[0] if perm else None
+    return (grouped_matmul(x, b, row_ptr, perm) if ctx.needs_input_grad[0] else None,
+            grouped_matmul_dx(dy, b, row_ptr, perm) if ctx.needs_input_grad[1] else None, None, None)
+
+
+def _setup_context_grouped_backward(ctx, inputs, output):
+    ctx.set_materialize_grads(False)
+    ctx.save_for_backward(*inputs[:4], *(t for t in inputs[4:] if t is not None))
+
+
+def _backward_grouped_backward(ctx, a, b):   # of both, for the cotangents a of dx and b of dw (None: zeros)
+    dy, x, w, row_ptr, *perm = ctx.saved_tensors
+    perm = perm[0] if perm else None
+    g_dy = g_x = g_w = None
+    if ctx.needs_input_grad[0]:
+        parts = [grouped_matmul(r, v, row_ptr, perm) for r, v in ((a, w), (x, b)) if r is not None and v is not None]
+        g_dy = sum(parts[1:], parts[0]) if parts else None
+    if ctx.needs_input_grad[1] and b is not None:
+        g_x = grouped_matmul_dx(dy, b, row_ptr, perm)
+    if ctx.needs_input_grad[2] and a is not None:
+        g_w = grouped_matmul_dw(dy, a, row_ptr, perm)
+    return g_dy, g_x, g_w, None, None
+
+
+grouped_matmul_dx.register_autograd(_backward_grouped_dx, setup_context=_setup_context_grouped)
+grouped_matmul_dw.register_autograd(_backward_grouped_dw, setup_context=_setup_context_grouped)
+grouped_matmul_backward.register_autograd(_backward_grouped_backward, setup_context=_setup_context_grouped_backward)
+
+
 def species_linear(x: torch.Tensor, w: torch.Tensor, species: torch.Tensor) -> torch.Tensor:
     """CSR of the rows' species (M,) int32, then y[i] = w[species[i]] x[i], differentiable in
     x and w.  Rows whose species is outside [0, G) give zeros."""

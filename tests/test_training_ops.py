@@ -79,6 +79,35 @@ def test_gradients_nobody_asked_for_are_not_formed(monkeypatch):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("gathered", [False, True])
+@pytest.mark.parametrize("needs", [(True, True), (True, False), (False, True)])
+def test_grouped_second_derivatives(needs, gathered):
+    """A loss of an energy and its gradients (the forces' loss), against the same in 64 bits from plain products.
+    Each result is a sum of at most three chains of products: 1e-5 of the magnitude of its largest element."""
+    gen = torch.Generator(device="cuda").manual_seed(9)
+    M, K, N, G = 300, 48, 40, 4
+    rnd = lambda *s: torch.randn(s, generator=gen, device="cuda")  # noqa: E731
+    group = torch.randint(0, G, (M,), generator=gen, device="cuda")
+    group = group if gathered else group.sort()[0]
+    row_ptr, perm = (torch.from_numpy(a).cuda() for a in csr(group.cpu().numpy(), G))
+    values = rnd(M, K), rnd(G, N, K) * K ** -0.5, rnd(M, N), rnd(M, K), rnd(G, N, K)
+
+    def grads(dtype):
+        x, w, c, a, b = (v.to(dtype) for v in values)
+        x.requires_grad_(needs[0]), w.requires_grad_(needs[1])
+        y = ag.grouped_matmul(x, w, row_ptr, perm if gathered else None) if dtype == torch.float32 else \
+            torch.einsum("mnk,mk->mn", w[group], x)
+        energy = (torch.tanh(y) * c).sum()       # not linear: the cotangent of y wants a gradient too
+        at = [t for t in (x, w) if t.requires_grad]
+        first = torch.autograd.grad(energy, at, create_graph=True)
+        loss = energy + sum((g.square() * (a if g.dim() == 2 else b)).sum() for g in first)
+        return torch.autograd.grad(loss, at)
+
+    for got, want in zip(grads(torch.float32), grads(torch.float64)):
+        assert float((got - want).abs().max()) <= 1e-5 * float(want.abs().max())
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("gate", ["full", "row", "none"])
 def test_norm_autograd(gate):
     M, C = 200, 96
