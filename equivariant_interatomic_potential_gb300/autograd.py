@@ -319,13 +319,14 @@ def _(h, x, gate, w_post, scale, w_pre, eps=1e-6, kind="rms"):
 
 @torch.library.custom_op(f"{_NS}::norm_gate_residual_backward", mutates_args=())
 def norm_gate_residual_backward(
-        dy: torch.Tensor, du: torch.Tensor, h: torch.Tensor, x: torch.Tensor, gate: Optional[torch.Tensor],
+        dy: Optional[torch.Tensor], du: Optional[torch.Tensor], h: torch.Tensor, x: torch.Tensor, gate: Optional[torch.Tensor],
         w_post: torch.Tensor, scale: torch.Tensor, w_pre: torch.Tensor, stats: torch.Tensor, kind: str = "rms",
 ) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor, torch.Tensor, torch.Tensor, torch.Tensor]:
-    """(dh, dx, dgate, dw_post, dscale, dw_pre) for the cotangents dy and du; dgate is empty without a gate."""
-    _cuda_only("norm_gate_residual_backward", dy, du, h, x, w_post, scale, w_pre, stats)
+    """(dh, dx, dgate, dw_post, dscale, dw_pre) for the cotangents dy and du (None: zeros); dgate is empty
+    without a gate."""
+    _cuda_only("norm_gate_residual_backward", *(t for t in (dy, du) if t is not None), h, x, w_post, scale, w_pre, stats)
     dh, dx, dgate, *sums = zs.zs_norm_gate_residual_backward(
-        dy.contiguous(), du.contiguous(), h.contiguous(), x.contiguous(), None if gate is None else gate.contiguous(), w_post,
+        *(None if t is None else t.contiguous() for t in (dy, du)), h.contiguous(), x.contiguous(), None if gate is None else gate.contiguous(), w_post,
         scale, w_pre, stats, kind=kind)
     return (dh, dx, h.new_empty(0) if dgate is None else dgate, *sums)
 
@@ -338,12 +339,15 @@ def _(dy, du, h, x, gate, w_post, scale, w_pre, stats, kind="rms"):
 
 def _setup_context_norm(ctx, inputs, output):
     h, x, gate, w_post, scale, w_pre, eps, kind = inputs
+    ctx.set_materialize_grads(False)   # a cotangent that is not there is not read
     ctx.mark_non_differentiable(output[2])
     ctx.save_for_backward(h, x, w_post, scale, w_pre, output[2], *(() if gate is None else (gate,)))
     ctx.kind = kind
 
 
 def _backward_norm(ctx, dy, du, _):
+    if dy is None and du is None:
+        return (None,) * 8
     h, x, w_post, scale, w_pre, stats, *gate = ctx.saved_tensors
     gate = gate[0] if gate else None
     dh, dx, dgate, dw_post, dscale, dw_pre = norm_gate_residual_backward(dy, du, h, x, gate, w_post, scale, w_pre, stats,

@@ -124,6 +124,35 @@ def test_norm_autograd(gate):
         assert (leaf is None) == (g is None) and (g is None or torch.equal(leaf.grad, g))
 
 
+@pytest.mark.parametrize("which", ["y", "u"])
+def test_cotangents_that_are_not_there(which):
+    # traced with fake tensors: no matrix of zeros in a cotangent's place
+    def f(h, x, vec):
+        y, u, _ = ag.norm_gate_residual(h, x, None, vec, vec, vec)
+        return torch.autograd.grad((y if which == "y" else u).sum(), (h, x, vec))
+
+    h, x, vec = (torch.randn(s, requires_grad=True) for s in ((7, 8), (7, 8), (8,)))
+    nodes = list(make_fx(f, tracing_mode="fake")(h, x, vec).graph.nodes)
+    call, = [n for n in nodes if "norm_gate_residual_backward" in str(n.target)]
+    assert (call.args[0] is None, call.args[1] is None) == (which == "u", which == "y")
+    assert not any("zeros" in str(n.target) for n in nodes)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("which", ["y", "u"])
+def test_norm_autograd_of_one_output(which):
+    M, C = 300, 96
+    gen = torch.Generator(device="cuda").manual_seed(14)
+    rnd = lambda *s: torch.randn(s, generator=gen, device="cuda")  # noqa: E731
+    ops, d = [rnd(M, C), rnd(M, C), rnd(M, C), rnd(C), rnd(C), rnd(C)], rnd(M, C)
+    leaves = [t.clone().requires_grad_() for t in ops]
+    y, u, _ = ag.norm_gate_residual(*leaves)
+    (y if which == "y" else u).backward(d)
+    stats = zs.zs_norm_gate_residual(*ops)[2]
+    want = zs.zs_norm_gate_residual_backward(d if which == "y" else None, d if which == "u" else None, *ops, stats)
+    assert all(torch.equal(leaf.grad, g) for leaf, g in zip(leaves, want))
+
+
 @pytest.mark.gpu
 def test_optimiser_against_torch():
     # fp32 rounding of a few operations a step: 1e-6 of the parameters' size after five
