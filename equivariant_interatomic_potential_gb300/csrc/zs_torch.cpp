@@ -11,6 +11,7 @@
 #include <ATen/ATen.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include "zs.h"
@@ -59,13 +60,13 @@ PyObject* failed(const char* fn, int status) {
     if (!PyErr_Occurred()) PyErr_Format(PyExc_RuntimeError, "%s -> %d", fn, status);
     return nullptr;
 }
-// C++ exceptions (an allocation that fails) as Python ones
+// C++ exceptions as the Python ones that torch makes of them (an allocation that fails: torch.OutOfMemoryError)
 template <typename F>
 PyObject* guarded(F&& f) {
     try {
         return f();
-    } catch (const std::exception& e) {
-        PyErr_SetString(PyExc_RuntimeError, e.what());
+    } catch (const std::exception&) {
+        torch::translate_exception_to_python(std::current_exception());
         return nullptr;
     }
 }

@@ -57,3 +57,15 @@ def test_results_without_the_extension(no_extension, monkeypatch):
         without = everything()
     monkeypatch.undo()
     assert all(torch.equal(a, b) for a, b in zip(without, everything()))
+
+
+@pytest.mark.gpu
+def test_allocations_that_fail():
+    # results of 4 TB, refused by the allocator: the same exception from the extension and from the binding
+    n = 1 << 20
+    x, w = torch.zeros(n, 1, device="cuda"), torch.zeros(1, n, 1, device="cuda")
+    row_ptr = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    for call in (lambda **kw: zs.zs_grouped_matmul(x, w, row_ptr, **kw), lambda **kw: zs.zs_grouped_matmul_dw(x.view(1, n), x.view(1, n), row_ptr, **kw)):
+        for kw in ({}, {"stream": torch.cuda.Stream()}):
+            with pytest.raises(torch.OutOfMemoryError):
+                call(**kw)
