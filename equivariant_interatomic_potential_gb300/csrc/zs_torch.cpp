@@ -154,7 +154,8 @@ PyObject* norm(PyObject*, PyObject* const* args, Py_ssize_t n) {
         NormOperands o;
         if (n != 9 || !PyFloat_CheckExact(args[6]) || !o.read(args)) return not_here();
         at::Tensor y = make({o.M, o.C}, *o.h, o.h->scalar_type()), u = make({o.M, o.C}, *o.h, o.h->scalar_type()), stats;
-        const bool want = args[8] == Py_True;
+        const int want = PyObject_IsTrue(args[8]);
+        if (want < 0) return nullptr;
         if (want) stats = make({o.M, 4}, *o.h, at::kFloat);
         const int st = f_norm(o.d, (int)PyLong_AsLong(args[7]), o.h->const_data_ptr(), o.C, o.x->const_data_ptr(), o.C, o.gate_ptr(),
                               o.gate_cols, (int32_t)o.gate_cols, floats(o.w_post), floats(o.scale), floats(o.w_pre),

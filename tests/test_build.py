@@ -69,3 +69,13 @@ def test_allocations_that_fail():
         for kw in ({}, {"stream": torch.cuda.Stream()}):
             with pytest.raises(torch.OutOfMemoryError):
                 call(**kw)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("short", [True, False], ids=["extension", "binding"])
+@pytest.mark.parametrize("want", [True, 1, "yes", False, 0, None])
+def test_any_truth_value_asks_for_statistics(want, short, monkeypatch):
+    if not short:
+        monkeypatch.setattr(zs, "_fast", type("None", (), {"norm": staticmethod(lambda *a: NotImplemented)}))
+    t, v = torch.ones(4, 8, device="cuda"), torch.ones(8, device="cuda")
+    assert (zs.zs_norm_gate_residual(t, t, None, v, v, v, want_stats=want)[2] is not None) == bool(want)
