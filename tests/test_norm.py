@@ -254,3 +254,20 @@ def test_gates_in_32_bits(gate):
     y, _, _ = zs.zs_norm_gate_residual(*cuda([ones, zeros, z, vec, vec, vec]), eps=0.0)
     want = 1.0 / (1.0 + np.exp(-f64(z)))
     assert (np.abs(f64(y) - want) <= 2.0 ** -20 * want).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("M,C", [(70, 700), (33, 2048), (9, 4100), (5, 8191), (2, 8192)])
+def test_operands_at_different_phases(M, C, dtype):
+    # each operand starts at another element offset, so that rows go element by element, over clusters where they are wide
+    for kind, gate in (("rms", "full"), ("layer", "row")):
+        t, d, ct, cd = draw(M, C, gate, dtype, C + M)
+
+        def at(a, shift):
+            base = torch.full((a.numel() + 8,), float("nan"), dtype=a.dtype, device="cuda")
+            view = base[shift:shift + a.numel()].view(a.shape)
+            view.copy_(a.cuda())
+            return view
+
+        check([at(a, i + 1) for i, a in enumerate(t[:3])] + t[3:], d, [at(a, i + 4) for i, a in enumerate(ct)], cd, dtype, kind)
