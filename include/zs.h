@@ -348,8 +348,12 @@ typedef enum zs_dtype {
  *   y (M, N)         rows y_ld elements apart (y_ld >= N), fully written:
  *                    rows at positions >= row_ptr[G] (no group) are zeros
  * M, K and N up to 2^31 - 2^16, K >= 1, N >= 1, G >= 0.  Values outside a
- * row's own group never reach its result.  Sums are in fp32 in a fixed order for given sizes;
- * an fp32 value that is not finite gives NaN in the results that it reaches.
+ * row's own group never reach its result.  Sums are in fp32, in a fixed order
+ * for given sizes.  Those of the tensor cores, whose additions truncate, come out
+ * up to 2^-16 of their terms' magnitudes low for 16-bit operands and about 2^-22
+ * for fp32 ones, each of whose terms is known to 2^-24.  An fp32 value that is
+ * not finite makes the results that it reaches not finite: NaN, or the infinity
+ * that the sum is.
  */
 ZS_API zs_status zs_grouped_matmul(int32_t dtype, const void* x, int64_t x_ld, const void* w,
                                    const int32_t* row_ptr, const int32_t* perm,
