@@ -205,6 +205,10 @@ __global__ void __launch_bounds__(norm_threads(VEC * NV, true), kBwdCtas<VEC * N
         if constexpr (kLayer) dm = m[1] * s.inv_c;
         float dx[E];
         ring.open(stage, 3, dx);
+        if (!live) {   // an infinity of the row that its slots held before would leave NaN
+#pragma unroll
+            for (int i = 0; i < E; ++i) dx[i] = 0.f;
+        }
 #pragma unroll
         for (int i = 0; i < E; ++i) dx[i] = fmaf(st.w, fmaf(dn, ny[i], centred<kLayer>(d[i], dm)), dx[i]);
         if (live) Co::store(static_cast<T*>(a.out1) + r * s.C, dx, l);

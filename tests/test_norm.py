@@ -271,3 +271,23 @@ def test_operands_at_different_phases(M, C, dtype):
             return view
 
         check([at(a, i + 1) for i, a in enumerate(t[:3])] + t[3:], d, [at(a, i + 4) for i, a in enumerate(ct)], cd, dtype, kind)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("gate", ["full", "none"])
+def test_infinite_cotangents_stay_infinite(gate):
+    """dy of +infinity in one column, whose norm(h) are all positive: its sums over the rows
+    are +-infinity by the formula, however many rows the last round of the grid lacks.  A
+    row's slots are taken again every few rounds, so there are several of them."""
+    for M in (20000, 40000, 61003):
+        t, _, (dy, du), _ = draw(M, 32, gate, "f32", 3)
+        t[0][:, 5] = t[0][:, 5].abs() + 0.1
+        dy[:, 5] = float("inf")
+        du.zero_()
+        t = cuda(t)
+        stats = zs.zs_norm_gate_residual(*t, eps=EPS)[2]
+        dw_post, dscale = zs.zs_norm_gate_residual_backward(dy.cuda(), du.cuda(), *t, stats)[3:5]
+        assert float(dw_post[5]) == float("inf") * float(t[4][5].sign()), M
+        assert float(dscale[5]) == float("inf") * float(t[3][5].sign()), M
+        keep = torch.arange(32, device="cuda") != 5
+        assert bool(torch.isfinite(dw_post[keep]).all())
