@@ -50,8 +50,12 @@ class AdamW(torch.optim.Optimizer):
         if bits not in (8, 32):
             raise ValueError(f"state_bits must be 8 or 32, got {bits}")
         super().add_param_group(param_group)
+        params = self.param_groups[-1]["params"]
+        if len(set(params)) != len(params):
+            self.param_groups.pop()
+            raise ValueError("a parameter is given twice")
         dtype = torch.float32 if bits == 32 else torch.float8_e4m3fn
-        for p in self.param_groups[-1]["params"]:
+        for p in params:
             s = self.state[p]
             s["step"] = 0
             for k in ("exp_avg", "exp_avg_sq"):

@@ -893,6 +893,10 @@ class AdamWPlan:
                     setattr(e, name, _ptr(lst[i]))
         self._table_ptr = ctypes.addressof(self._table)
         self._shapes, self._param_at = [p.shape for p in self.params], [p.data_ptr() for p in self.params]
+        written = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size())
+                         for t in (*self.params, *self.exp_avg, *self.exp_avg_sq, *sum(self.scales, [])) if t.numel() and t.data_ptr())
+        if any(end > start for (_, end), (start, _) in zip(written, written[1:])):
+            raise ValueError("parameters and states must not overlap, nor be given twice")
         # a tensor's memory may be taken from it (t.data = other): it is held by itself
         self._memory = [t.untyped_storage() for t in (*self.params, *self.exp_avg, *self.exp_avg_sq, *sum(self.scales, []))]
         self.set_grads(grads)

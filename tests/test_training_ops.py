@@ -351,6 +351,32 @@ def test_optimiser_gradient_memory_replaced():
         a.step()
 
 
+@pytest.mark.filterwarnings("ignore:optimizer contains a parameter group with duplicate")
+def test_parameters_given_twice():
+    # threads of one launch would read and write them at the same time
+    p, q = torch.zeros(5), torch.zeros(3)
+    with pytest.raises(ValueError, match="twice"):
+        AdamW([p, q, p])
+    opt = AdamW([p])
+    with pytest.raises(ValueError, match="twice"):
+        opt.add_param_group({"params": [q, q]})
+    with pytest.raises(ValueError):
+        opt.add_param_group({"params": [p]})
+    assert len(opt.param_groups) == 1
+
+
+@pytest.mark.gpu
+def test_plan_of_overlapping_memory():
+    a = torch.zeros(1000, device="cuda")
+    make = lambda n, k=1: [torch.zeros(n, device="cuda") for _ in range(k)]  # noqa: E731
+    with pytest.raises(ValueError, match="overlap"):
+        zs.AdamWPlan([a[:600], a[599:]], [*make(600), *make(401)], [*make(600), *make(401)], [*make(600), *make(401)])
+    m = make(600)
+    with pytest.raises(ValueError, match="overlap"):
+        zs.AdamWPlan([a[:600]], make(600), m, m)
+    zs.AdamWPlan([a[:600], a[600:]], [*make(600), *make(400)], [*make(600), *make(400)], [*make(600), *make(400)])
+
+
 @pytest.mark.gpu
 def test_plan_holds_the_memory():
     make = lambda: [torch.full((4000,), v, device="cuda") for v in (1.0, 0.5, 0.1, 0.2)]  # noqa: E731
