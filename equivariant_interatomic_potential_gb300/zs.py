@@ -874,6 +874,7 @@ class AdamWPlan:
         self.scales = [] if exp_avg_scale is None else [list(exp_avg_scale), list(exp_avg_sq_scale)]
         self.dtype = _dtype(self.params[0], "params[0]")
         self.device = self.params[0].device
+        self._index = self.device.index
         self._table = (_AdamWTensor * n)()
         state_dtype = torch.float32 if self.state_bits == 32 else torch.float8_e4m3fn
         for lst, name in ((self.exp_avg, "exp_avg"), (self.exp_avg_sq, "exp_avg_sq"),
@@ -902,7 +903,7 @@ class AdamWPlan:
         self.set_grads(grads)
 
     def _one(self, t, name, dtype, shape):
-        if t.dtype is dtype and t.shape == shape and t.get_device() == self.device.index and t.is_contiguous():
+        if t.dtype is dtype and t.shape == shape and t.get_device() == self._index and t.is_contiguous():
             return
         _need(t, name, dtype, tuple(shape))
         if t.device != self.device:
@@ -942,16 +943,17 @@ def zs_adamw_step(plan: AdamWPlan, step: int, lr: float, beta1: float = 0.9, bet
         if grad_scale.numel() != 1 or grad_scale.dtype != torch.float32 or grad_scale.device != plan.device:
             raise ValueError(f"grad_scale must be one float32 element on {plan.device}")
         scale_ptr = grad_scale.data_ptr()
-    if isinstance(stream, torch.cuda.Stream):
+    if stream is not None and isinstance(stream, torch.cuda.Stream):
         _one_device((plan.params[0],), stream.device)
-    if plan.device.index != _current_device():   # a launch is the current device's
+    if plan._index != _current_device():   # a launch is the current device's
         with torch.cuda.device(plan.device):
             return zs_adamw_step(plan, step, lr, beta1, beta2, eps, weight_decay, grad_scale, stream, seed)
     hyper = _AdamWHyper(lr, beta1, beta2, eps, weight_decay, step)
-    head = (plan._table_ptr, len(plan.params), plan.dtype, plan.state_bits, ctypes.addressof(hyper))
     if seed is None:
-        st = load().zs_adamw_step(*head, scale_ptr, _stream(stream))
+        st = load().zs_adamw_step(plan._table_ptr, len(plan.params), plan.dtype, plan.state_bits, ctypes.addressof(hyper),
+                                  scale_ptr, _stream(stream))
     else:
-        st = load().zs_adamw_step_seeded(*head, seed & (1 << 64) - 1, scale_ptr, _stream(stream))
+        st = load().zs_adamw_step_seeded(plan._table_ptr, len(plan.params), plan.dtype, plan.state_bits,
+                                         ctypes.addressof(hyper), seed & (1 << 64) - 1, scale_ptr, _stream(stream))
     if st:
         _check("zs_adamw_step", st)
