@@ -248,12 +248,14 @@ rows_mma(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUte
     } else if (warp == 1 && rank == 0) {   // of a pair, for both
         RingPos<S> pos;
         Buffers<T> bufs;
-        int n = 0;   // of chunks (fp32), or tiles
+        int n = 0, buf = 0;   // n of chunks (fp32), or tiles
         bool have = next_product(a, gr, item, step, BN, t);   // which tile it is does not matter here
         while (have && !is_dead(dead)) {
             for (int k = 0; k < nk; ++k, pos.next()) {
-                const int buf = (kSums<T> > 1 || k < kPerChunk ? n : n + 1) & 1;
-                if (k % kPerChunk == 0) bounded_wait_on<kPair>(set.tempty + 8 * buf, bufs.of(buf, n) ^ 1, dead);
+                if (k % kPerChunk == 0) {
+                    buf = (kSums<T> > 1 || k == 0 ? n : n + 1) & 1;
+                    bounded_wait_on<kPair>(set.tempty + 8 * buf, bufs.of(buf, n) ^ 1, dead);
+                }
                 bounded_wait_on<kPair>(set.full + 8 * pos.stage, pos.phase, dead);
                 tc_fence_after();
                 const uint32_t at = smem_u32(ring) + pos.stage * Sh::kStage;

@@ -161,11 +161,10 @@ weights_mma(const __grid_constant__ CUtensorMap dy_map, const __grid_constant__ 
     } else if (warp == 1) {
         RingPos<S> pos;
         Buffers<T> bufs;
-        int n = 0;   // of chunks (fp32), or segments
-        auto buffer_of = [&](int p) { return (kSums<T> > 1 || p - s.p0 < kPerChunk ? n : n + 1) & 1; };
+        int n = 0, buf = 0;   // n of chunks (fp32), or segments
         // a stage's products
         auto products = [&](int p) {
-            const int buf = buffer_of(p), since = (p - s.p0) % kPerChunk, steps = (imin(kUnit, s.p1 - p) + 15) / 16;
+            const int since = (p - s.p0) % kPerChunk, steps = (imin(kUnit, s.p1 - p) + 15) / 16;
             const uint32_t at = smem_u32(ring) + pos.stage * Sh::kStage;
             tc_fence_after();
             issue_stage<T, true, true, BN>(set.tmem + buf * kSums<T> * BN, at, Sh::kA, Sh::kBox, at + Sh::P * Sh::kA, Sh::kBox,
@@ -177,8 +176,10 @@ weights_mma(const __grid_constant__ CUtensorMap dy_map, const __grid_constant__ 
             }
         };
         auto ready = [&](int p) {
-            const int buf = buffer_of(p);
-            if ((p - s.p0) % kPerChunk == 0) bounded_wait_on(set.tempty + 8 * buf, bufs.of(buf, n) ^ 1, dead);
+            if ((p - s.p0) % kPerChunk == 0) {
+                buf = (kSums<T> > 1 || p == s.p0 ? n : n + 1) & 1;
+                bounded_wait_on(set.tempty + 8 * buf, bufs.of(buf, n) ^ 1, dead);
+            }
             bounded_wait_on(set.full + 8 * pos.stage, pos.phase, dead);
         };
         while (!is_dead(dead) && walk.next(s)) {
