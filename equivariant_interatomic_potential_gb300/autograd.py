@@ -1,4 +1,4 @@
-"""PyTorch operators over libzs, with first-order autograd.
+"""PyTorch operators over libzs, with autograd (first-order but for the grouped products).
 
 The pull request "fused Triton zonal scatter for the GIE head" (deepmd-kit)
 puts the zonal scatter behind a differentiable operator whose backward is
@@ -13,7 +13,7 @@ and "Tests").  Here that operator is a ``torch.library`` custom op:
   node_scale[n] * the operator's sum, differentiable in node_scale too
   ``zs_gie::grouped_matmul(x, w, row_ptr, perm) -> y``: each row times the
   weights of its group (its species, or species and degree), the groups in a
-  CSR from ``build_csr``; differentiable in x and w
+  CSR from ``build_csr``; differentiable in x and w, its gradients again
   ``zs_gie::norm_gate_residual(h, x, gate, w_post, scale, w_pre, eps, kind) ->
   (y, u, stats)``: the norms around a block with its gate, residual scale and
   residual sum; differentiable in every tensor (``optim.AdamW`` steps them)

@@ -6,8 +6,8 @@
 // the first one's those of both); warps 4 to 11 write finished tiles while the
 // next one is being summed.
 //
-// 32768 bf16 rows in order, 8 groups of 1024 -> 4096: 167 us (1.65 PFLOP/s) and
-// 184 transposed, the tensor cores 70 % active and the power limit reached; 89
+// 32768 bf16 rows in order, 8 groups of 1024 -> 4096: 170 us (1.62 PFLOP/s) and
+// 189 transposed, the tensor cores 70 % active and the power limit reached; 89
 // groups of 256 -> 256, gathered: 19 us, of which the weights' copies take 10 and
 // the results' way out 4 (0.36 of the copy rate); fp32 at a sixth of the rate.
 #include <initializer_list>

@@ -4,7 +4,7 @@
 // Both operands have the summed-over direction across their memory rows
 // (MN-major boxes); zs_grouped_walk.cuh says how the work is shared out.
 //
-// 32768 bf16 rows in order, 8 groups of 1024 -> 4096: 233 us (1.18 PFLOP/s), of
+// 32768 bf16 rows in order, 8 groups of 1024 -> 4096: 238 us (1.16 PFLOP/s), of
 // which the copies alone take 214 (48 KB a stage, six boxes); 89 groups of 256 ->
 // 256, gathered: 30 us with the joining kernel, bound by the partial tiles.
 #include <initializer_list>

@@ -2,8 +2,10 @@
 
 Every entry point has the name of the C function it calls.  Tensors must be
 CUDA tensors of the documented dtype and shape; outputs and workspaces are
-allocated with torch when not given.  All compute runs in libzs's kernels;
-there is no fallback, and a missing or unbuildable library raises.
+allocated with torch when not given.  A call runs on the current stream, or on
+``stream`` (an object or a handle) as if that one were current: it has to be
+ordered after the work that makes the operands.  All compute runs in libzs's
+kernels; there is no fallback, and a missing or unbuildable library raises.
 """
 from __future__ import annotations
 
