@@ -120,6 +120,12 @@ class AdamW(torch.optim.Optimizer):
         self._plans = plans
         return loss
 
+    def state_dict(self) -> dict:
+        """The base class's form, with copies of the states: later steps leave it as it is."""
+        d = super().state_dict()
+        d["state"] = {i: {k: v.clone() if isinstance(v, torch.Tensor) else v for k, v in s.items()} for i, s in d["state"].items()}
+        return d
+
     def load_state_dict(self, state_dict: dict) -> None:
         d = dict(state_dict)
         mine, params = self.state, list(chain.from_iterable(g["params"] for g in self.param_groups))
@@ -127,7 +133,7 @@ class AdamW(torch.optim.Optimizer):
             steps = d["steps"] if isinstance(d["steps"], list) else [d["steps"]] * len(d["state"])
             if len(steps) != len(params):
                 raise ValueError(f"the state is of {len(steps)} parameters, the optimiser of {len(params)}")
-            groups = self.state_dict()["param_groups"]
+            groups = super().state_dict()["param_groups"]
             for g in groups:
                 g["state_bits"] = d["state_bits"]
             d = {"state": {i: {**s, "step": n} for i, (s, n) in enumerate(zip(d["state"], steps))}, "param_groups": groups}

@@ -259,6 +259,17 @@ def test_optimiser_is_one_of_torchs(tmp_path):
         opt.add_param_group({"params": [torch.zeros(3)], "state_bits": 4})
 
 
+def test_optimiser_state_dict_is_a_snapshot():
+    opt = AdamW([torch.zeros(5)])
+    d = opt.state_dict()
+    for s in opt.state.values():
+        s["step"] = 3
+        s["exp_avg"].fill_(1.0)
+    assert d["state"][0]["step"] == 0 and not bool(d["state"][0]["exp_avg"].any())
+    opt.load_state_dict(d)
+    assert opt.state[opt.param_groups[0]["params"][0]]["step"] == 0
+
+
 def test_optimiser_loads_the_form_without_groups():
     state = [{"exp_avg": torch.full((5,), 0.5), "exp_avg_sq": torch.full((5,), 0.25)},
              {"exp_avg": torch.full((2,), 0.1), "exp_avg_sq": torch.full((2,), 0.2)}]
