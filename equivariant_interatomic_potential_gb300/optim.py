@@ -107,17 +107,15 @@ class AdamW(torch.optim.Optimizer):
                 into[0].append(p)
                 into[1].append(s)
                 into[2].append(g if g.is_contiguous() else g.contiguous())
-        plans = {}
-        for (options, _, steps), (params, states, grads) in alike.items():
-            lr, beta1, beta2, eps, decay, bits, seed = options
-            plan = self._plan(params, states, grads, bits)
-            zs.zs_adamw_step(plan, steps + 1, lr=lr, beta1=beta1, beta2=beta2, eps=eps, weight_decay=decay, grad_scale=grad_scale,
-                             seed=seed + len(plans))   # each launch has random bits of its own
-            plans[tuple(map(id, params))] = plan
+        plans = {tuple(map(id, params)): self._plan(params, states, grads, options[5])
+                 for (options, _, _), (params, states, grads) in alike.items()}   # what is refused is, before any launch
+        self._plans = plans
+        for i, (((lr, beta1, beta2, eps, decay, _, seed), _, steps), (params, states, _)) in enumerate(alike.items()):
+            zs.zs_adamw_step(plans[tuple(map(id, params))], steps + 1, lr=lr, beta1=beta1, beta2=beta2, eps=eps,
+                             weight_decay=decay, grad_scale=grad_scale, seed=seed + i)   # each launch has random bits of its own
             for s in states:
                 s["step"] = steps + 1
             torch.autograd.graph.increment_version(params)
-        self._plans = plans
         return loss
 
     def state_dict(self) -> dict:

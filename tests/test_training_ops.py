@@ -362,6 +362,24 @@ def test_optimiser_gradient_memory_replaced():
         a.step()
 
 
+@pytest.mark.gpu
+def test_optimiser_refuses_before_it_steps():
+    # one gradient of a wrong shape: no parameter moves, of whatever launch
+    p, q = torch.ones(50, device="cuda"), torch.ones(60, device="cuda", dtype=torch.bfloat16)
+    opt = AdamW([p, q])
+    p.grad, q.grad = torch.ones_like(p), torch.ones_like(q)
+    opt.step()
+    before = p.clone(), q.clone()
+    q.grad.data = torch.ones(30, device="cuda", dtype=torch.bfloat16)
+    for _ in range(2):
+        with pytest.raises(ValueError, match="shape"):
+            opt.step()
+    assert torch.equal(p, before[0]) and torch.equal(q, before[1]) and opt.state[p]["step"] == opt.state[q]["step"] == 1
+    q.grad = torch.ones_like(q)
+    opt.step()
+    assert not torch.equal(p, before[0]) and opt.state[p]["step"] == opt.state[q]["step"] == 2
+
+
 @pytest.mark.filterwarnings("ignore:optimizer contains a parameter group with duplicate")
 def test_parameters_given_twice():
     # threads of one launch would read and write them at the same time
