@@ -283,7 +283,7 @@ WeightPlan weight_plan(int32_t dtype, bool tma, int64_t M, int32_t K, int32_t N,
     const int most = p.small ? 4 * kCtas : kCtas;
     p.per = (p.units + most - 1) / most;
     // Where tiles share an operand that L2 does not hold, ranges that start at the same positions of their tiles read it
-    // from memory once: 32768 x 4096 and 32768 x 1024 bf16, 128 tiles, take 234 us on 128 SMs so and 270 on all 152 with
+    // from memory once: 32768 x 4096 and 32768 x 1024 bf16, 128 tiles, take 250 us on 128 SMs so and 272 on all 152 with
     // equal ranges.  Where it does not matter, fewer SMs do: 32768 x 1360 and 32768 x 216 79 and 74 us.
     const int64_t ntiles = (N + kTileM - 1) / kTileM, ktiles = (K + p.bn - 1) / p.bn, tiles = ntiles * ktiles;
     const int64_t row = dtype_bytes(dtype) * imax(ktiles > 1 ? (int64_t)N : 0, ntiles > 1 ? (int64_t)K : 0);
