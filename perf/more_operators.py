@@ -270,13 +270,13 @@ def _plain_route(s):
         choice = choice + s["bias"].double()
     choice = torch.where(z == -math.inf, -math.inf, choice)
     if s["top_groups"] < s["groups"]:
-        best = choice.view(M, s["groups"], -1).sort(2, descending=True, stable=True)[0][:, :, :s["group_top"]]
+        best = choice.view(M, s["groups"], -1).sort(dim=2, descending=True, stable=True)[0][:, :, :s["group_top"]]
         value = torch.where(best[:, :, 0] == -math.inf, -math.inf, torch.where(best == -math.inf, 0.0, best).sum(2))
-        kept = value.sort(1, descending=True, stable=True)[1][:, :s["top_groups"]]
+        kept = value.sort(dim=1, descending=True, stable=True)[1][:, :s["top_groups"]]
         mask = torch.zeros(M, s["groups"], dtype=torch.bool, device="cuda")
         mask[torch.arange(M, device="cuda")[:, None], kept] = True
         choice = torch.where(mask.repeat_interleave(E // s["groups"], 1), choice, -math.inf)
-    value, at = choice.sort(1, descending=True, stable=True)
+    value, at = choice.sort(dim=1, descending=True, stable=True)
     at, none = at[:, :k], value[:, :k] == -math.inf
     p = _scores(z.float(), s["score"])
     chosen = torch.where(none, 0.0, torch.gather(p, 1, at))
