@@ -27,6 +27,15 @@ decltype(&zs_grouped_matmul_dw) f_dw;
 decltype(&zs_norm_gate_residual) f_norm;
 decltype(&zs_norm_gate_residual_backward_workspace_bytes) f_norm_bytes;
 decltype(&zs_norm_gate_residual_backward) f_norm_backward;
+decltype(&zs_embedding) f_embedding;
+decltype(&zs_embedding_backward_workspace_bytes) f_embedding_bytes;
+decltype(&zs_embedding_backward) f_embedding_backward;
+decltype(&zs_route) f_route;
+decltype(&zs_route_backward) f_route_backward;
+decltype(&zs_dispatch) f_dispatch;
+decltype(&zs_combine) f_combine;
+decltype(&zs_combine_backward) f_combine_backward;
+decltype(&zs_dropout) f_dropout;
 PyObject* on_error;   // binding's check(function name, status): raises
 
 const at::Tensor* plain(PyObject* o) {
@@ -203,6 +212,183 @@ PyObject* norm_backward(PyObject*, PyObject* const* args, Py_ssize_t n) {
     });
 }
 
+// Numbers as they are ordinarily given; false for others and for those out of range.
+bool number(PyObject* o, int64_t lo, int64_t hi, int64_t& v) {
+    if (!PyLong_CheckExact(o)) return false;
+    int over = 0;
+    v = PyLong_AsLongLongAndOverflow(o, &over);
+    return !over && v >= lo && v <= hi;
+}
+bool number(PyObject* o, double& v) {
+    if (!PyFloat_CheckExact(o)) return false;
+    v = PyFloat_AS_DOUBLE(o);
+    return true;
+}
+const int32_t* ints(const at::Tensor* t) { return t ? static_cast<const int32_t*>(t->const_data_ptr()) : nullptr; }
+int32_t* ints(at::Tensor& t) { return static_cast<int32_t*>(t.mutable_data_ptr()); }
+PyObject* pair(at::Tensor&& a, at::Tensor&& b) {
+    PyObject* r = PyTuple_New(2);
+    if (!r) return nullptr;
+    PyTuple_SET_ITEM(r, 0, THPVariable_Wrap(std::move(a)));
+    PyTuple_SET_ITEM(r, 1, THPVariable_Wrap(std::move(b)));
+    return r;
+}
+
+// (w, ids, scale) -> y
+PyObject* embedding(PyObject*, PyObject* const* args, Py_ssize_t n) {
+    return guarded([&]() -> PyObject* {
+        double scale;
+        if (n != 3 || !number(args[2], scale)) return not_here();
+        const at::Tensor *w = plain(args[0]), *ids = plain(args[1]);
+        if (!w || !ids || w->dim() != 2 || ids->dim() != 1 || (w->size(0) | w->size(1)) >> 31) return not_here();
+        const int64_t M = ids->size(0), V = w->size(0), C = w->size(1);
+        const int d = dtype_of(*w);
+        if (d < 0 || !is_array(ids, at::kInt, M)) return not_here();
+        at::Tensor y = make({M, C}, *w, w->scalar_type());
+        const int st = f_embedding(d, w->const_data_ptr(), C, ints(ids), M, (int32_t)V, (int32_t)C, (float)scale, y.mutable_data_ptr(), C,
+                                   stream());
+        return st ? failed("zs_embedding", st) : THPVariable_Wrap(std::move(y));
+    });
+}
+
+// (dy, row_ptr, perm, scale) -> dw
+PyObject* embedding_backward(PyObject*, PyObject* const* args, Py_ssize_t n) {
+    return guarded([&]() -> PyObject* {
+        double scale;
+        if (n != 4 || !number(args[3], scale)) return not_here();
+        const at::Tensor *dy = plain(args[0]), *row_ptr = plain(args[1]), *perm = plain(args[2]);
+        if (!dy || !row_ptr || dy->dim() != 2 || dy->size(1) >> 31) return not_here();
+        const int64_t M = dy->size(0), C = dy->size(1), V = row_ptr->numel() - 1;
+        const int d = dtype_of(*dy);
+        if (d < 0 || V < 0 || V >> 31 || !is_array(row_ptr, at::kInt, V + 1) || !is_array(perm, at::kInt, M)) return not_here();
+        at::Tensor dw = make({V, C}, *dy, dy->scalar_type()), ws;
+        const size_t bytes = f_embedding_bytes(d, M, (int32_t)V, (int32_t)C);
+        if (bytes) ws = make({(int64_t)bytes}, *dy, at::kByte);
+        const int st = f_embedding_backward(d, dy->const_data_ptr(), C, ints(row_ptr), ints(perm), M, (int32_t)V, (int32_t)C, (float)scale,
+                                            dw.mutable_data_ptr(), bytes ? ws.mutable_data_ptr() : nullptr, bytes, stream());
+        return st ? failed("zs_embedding_backward", st) : THPVariable_Wrap(std::move(dw));
+    });
+}
+
+// (logits, k, bias, score, groups, top_groups, group_top, renormalise, scale) -> (ids, weights)
+PyObject* route(PyObject*, PyObject* const* args, Py_ssize_t n) {
+    return guarded([&]() -> PyObject* {
+        int64_t k, score, groups, top_groups, group_top;
+        double scale;
+        if (n != 9 || !number(args[1], 1, 1 << 20, k) || !number(args[3], 0, 1, score) || !number(args[4], 1, 1 << 20, groups) ||
+            !number(args[5], 1, 1 << 20, top_groups) || !number(args[6], 1, 2, group_top) || !number(args[8], scale))
+            return not_here();
+        const at::Tensor *z = plain(args[0]), *bias = args[2] == Py_None ? nullptr : plain(args[2]);
+        if (!z || z->dim() != 2 || z->size(1) >> 20) return not_here();
+        const int64_t M = z->size(0), E = z->size(1);
+        const int d = dtype_of(*z), renormalise = PyObject_IsTrue(args[7]);
+        if (renormalise < 0) return nullptr;
+        if (d < 0 || k > E || (args[2] != Py_None && !is_array(bias, at::kFloat, E))) return not_here();
+        at::Tensor ids = make({M, k}, *z, at::kInt), weights = make({M, k}, *z, at::kFloat);
+        const int st = f_route(d, (int32_t)score, z->const_data_ptr(), E, bias ? floats(bias) : nullptr, M, (int32_t)E, (int32_t)k,
+                               (int32_t)groups, (int32_t)top_groups, (int32_t)group_top, renormalise, (float)scale, ints(ids),
+                               floats(weights), stream());
+        return st ? failed("zs_route", st) : pair(std::move(ids), std::move(weights));
+    });
+}
+
+// (dweights, logits, ids, score, renormalise, scale) -> dlogits
+PyObject* route_backward(PyObject*, PyObject* const* args, Py_ssize_t n) {
+    return guarded([&]() -> PyObject* {
+        int64_t score;
+        double scale;
+        if (n != 6 || !number(args[3], 0, 1, score) || !number(args[5], scale)) return not_here();
+        const at::Tensor *g = plain(args[0]), *z = plain(args[1]), *ids = plain(args[2]);
+        if (!g || !z || !ids || z->dim() != 2 || ids->dim() != 2 || z->size(1) >> 20) return not_here();
+        const int64_t M = z->size(0), E = z->size(1), k = ids->size(1);
+        const int d = dtype_of(*z), renormalise = PyObject_IsTrue(args[4]);
+        if (renormalise < 0) return nullptr;
+        if (d < 0 || k < 1 || k > E || !is_matrix(ids, at::kInt, M, k) || !is_matrix(g, at::kFloat, M, k)) return not_here();
+        at::Tensor dz = make({M, E}, *z, z->scalar_type());
+        const int st = f_route_backward(d, (int32_t)score, floats(g), z->const_data_ptr(), E, ints(ids), M, (int32_t)E, (int32_t)k,
+                                        renormalise, (float)scale, dz.mutable_data_ptr(), stream());
+        return st ? failed("zs_route_backward", st) : THPVariable_Wrap(std::move(dz));
+    });
+}
+
+// (x, row_ptr, perm, k) -> (xs, slot)
+PyObject* dispatch(PyObject*, PyObject* const* args, Py_ssize_t n) {
+    return guarded([&]() -> PyObject* {
+        int64_t k;
+        if (n != 4 || !number(args[3], 1, INT32_MAX, k)) return not_here();
+        const at::Tensor *x = plain(args[0]), *row_ptr = plain(args[1]), *perm = plain(args[2]);
+        if (!x || !row_ptr || x->dim() != 2 || (x->size(0) | x->size(1)) >> 31) return not_here();
+        const int64_t M = x->size(0), C = x->size(1), G = row_ptr->numel() - 1, R = M * k;
+        const int d = dtype_of(*x);
+        if (d < 0 || G < 0 || G >> 31 || R >> 31 || !is_array(row_ptr, at::kInt, G + 1) || !is_array(perm, at::kInt, R)) return not_here();
+        at::Tensor xs = make({R, C}, *x, x->scalar_type()), slot = make({M, k}, *x, at::kInt);
+        const int st = f_dispatch(d, x->const_data_ptr(), C, ints(row_ptr), ints(perm), M, (int32_t)k, (int32_t)G, (int32_t)C,
+                                  xs.mutable_data_ptr(), ints(slot), stream());
+        return st ? failed("zs_dispatch", st) : pair(std::move(xs), std::move(slot));
+    });
+}
+
+// (h, slot, weights) -> y
+PyObject* combine(PyObject*, PyObject* const* args, Py_ssize_t n) {
+    return guarded([&]() -> PyObject* {
+        if (n != 3) return not_here();
+        const at::Tensor *h = plain(args[0]), *slot = plain(args[1]), *weights = args[2] == Py_None ? nullptr : plain(args[2]);
+        if (!h || !slot || h->dim() != 2 || slot->dim() != 2 || slot->scalar_type() != at::kInt || slot->size(1) < 1 ||
+            (h->size(0) | h->size(1) | slot->size(1)) >> 31)
+            return not_here();
+        const int64_t M = slot->size(0), k = slot->size(1), R = h->size(0), C = h->size(1);
+        const int d = dtype_of(*h);
+        if (d < 0 || (args[2] != Py_None && !is_matrix(weights, at::kFloat, M, k))) return not_here();
+        at::Tensor y = make({M, C}, *h, h->scalar_type());
+        const int st = f_combine(d, h->const_data_ptr(), C, ints(slot), weights ? floats(weights) : nullptr, M, (int32_t)k, R, (int32_t)C,
+                                 y.mutable_data_ptr(), C, stream());
+        return st ? failed("zs_combine", st) : THPVariable_Wrap(std::move(y));
+    });
+}
+
+// (dy, h, slot, weights, row_ptr) -> (dh, dweights)
+PyObject* combine_backward(PyObject*, PyObject* const* args, Py_ssize_t n) {
+    return guarded([&]() -> PyObject* {
+        if (n != 5) return not_here();
+        const at::Tensor *dy = plain(args[0]), *h = plain(args[1]), *slot = plain(args[2]), *weights = plain(args[3]), *row_ptr = plain(args[4]);
+        if (!dy || !h || !slot || !row_ptr || h->dim() != 2 || slot->dim() != 2 || (slot->size(0) | slot->size(1) | h->size(1)) >> 31)
+            return not_here();
+        const int64_t M = slot->size(0), k = slot->size(1), R = M * k, C = h->size(1), G = row_ptr->numel() - 1;
+        const at::ScalarType type = h->scalar_type();
+        const int d = dtype_of(*h);
+        if (d < 0 || k < 1 || G < 0 || G >> 31 || !is_matrix(h, type, R, C) || !is_matrix(dy, type, M, C) || !is_matrix(slot, at::kInt, M, k) ||
+            !is_matrix(weights, at::kFloat, M, k) || !is_array(row_ptr, at::kInt, G + 1))
+            return not_here();
+        at::Tensor dh = make({R, C}, *h, type), dweights = make({M, k}, *h, at::kFloat);
+        const int st = f_combine_backward(d, dy->const_data_ptr(), C, h->const_data_ptr(), C, ints(slot), floats(weights), ints(row_ptr), M,
+                                          (int32_t)k, (int32_t)G, (int32_t)C, dh.mutable_data_ptr(), floats(dweights), stream());
+        return st ? failed("zs_combine_backward", st) : pair(std::move(dh), std::move(dweights));
+    });
+}
+
+// (h, p, seed, call, step, residual) -> y
+PyObject* dropout(PyObject*, PyObject* const* args, Py_ssize_t n) {
+    return guarded([&]() -> PyObject* {
+        double p;
+        int64_t seed, call, step = 0;
+        if (n != 6 || !number(args[1], p) || !number(args[2], 0, INT64_MAX, seed) || !number(args[3], 0, UINT32_MAX, call)) return not_here();
+        const at::Tensor *h = plain(args[0]), *r = args[5] == Py_None ? nullptr : plain(args[5]), *count = nullptr;
+        if (!number(args[4], INT64_MIN, INT64_MAX, step)) {
+            count = plain(args[4]);
+            if (!count || count->scalar_type() != at::kLong || count->numel() != 1) return not_here();
+        }
+        if (!h || h->dim() != 2 || h->size(1) < 1 || (h->size(0) | h->size(1)) >> 31) return not_here();
+        const int64_t M = h->size(0), C = h->size(1);
+        const int d = dtype_of(*h);
+        if (d < 0 || (args[5] != Py_None && !is_matrix(r, h->scalar_type(), M, C))) return not_here();
+        at::Tensor y = make({M, C}, *h, h->scalar_type());
+        const int st = f_dropout(d, h->const_data_ptr(), C, r ? r->const_data_ptr() : nullptr, C, M, (int32_t)C, p, (uint64_t)seed,
+                                 (uint32_t)call, step, count ? static_cast<const int64_t*>(count->const_data_ptr()) : nullptr,
+                                 y.mutable_data_ptr(), C, stream());
+        return st ? failed("zs_dropout", st) : THPVariable_Wrap(std::move(y));
+    });
+}
+
 // ({function name: address}, check)
 PyObject* bind(PyObject*, PyObject* args) {
     PyObject *table, *check;
@@ -221,6 +407,15 @@ PyObject* bind(PyObject*, PyObject* args) {
     f_norm = reinterpret_cast<decltype(f_norm)>(get("zs_norm_gate_residual"));
     f_norm_bytes = reinterpret_cast<decltype(f_norm_bytes)>(get("zs_norm_gate_residual_backward_workspace_bytes"));
     f_norm_backward = reinterpret_cast<decltype(f_norm_backward)>(get("zs_norm_gate_residual_backward"));
+    f_embedding = reinterpret_cast<decltype(f_embedding)>(get("zs_embedding"));
+    f_embedding_bytes = reinterpret_cast<decltype(f_embedding_bytes)>(get("zs_embedding_backward_workspace_bytes"));
+    f_embedding_backward = reinterpret_cast<decltype(f_embedding_backward)>(get("zs_embedding_backward"));
+    f_route = reinterpret_cast<decltype(f_route)>(get("zs_route"));
+    f_route_backward = reinterpret_cast<decltype(f_route_backward)>(get("zs_route_backward"));
+    f_dispatch = reinterpret_cast<decltype(f_dispatch)>(get("zs_dispatch"));
+    f_combine = reinterpret_cast<decltype(f_combine)>(get("zs_combine"));
+    f_combine_backward = reinterpret_cast<decltype(f_combine_backward)>(get("zs_combine_backward"));
+    f_dropout = reinterpret_cast<decltype(f_dropout)>(get("zs_dropout"));
     if (PyErr_Occurred()) return nullptr;
     Py_XSETREF(on_error, Py_NewRef(check));
     Py_RETURN_NONE;
@@ -235,6 +430,14 @@ PyMethodDef methods[] = {
     {"dw", fast<dw>(), METH_FASTCALL, nullptr},
     {"norm", fast<norm>(), METH_FASTCALL, nullptr},
     {"norm_backward", fast<norm_backward>(), METH_FASTCALL, nullptr},
+    {"embedding", fast<embedding>(), METH_FASTCALL, nullptr},
+    {"embedding_backward", fast<embedding_backward>(), METH_FASTCALL, nullptr},
+    {"route", fast<route>(), METH_FASTCALL, nullptr},
+    {"route_backward", fast<route_backward>(), METH_FASTCALL, nullptr},
+    {"dispatch", fast<dispatch>(), METH_FASTCALL, nullptr},
+    {"combine", fast<combine>(), METH_FASTCALL, nullptr},
+    {"combine_backward", fast<combine_backward>(), METH_FASTCALL, nullptr},
+    {"dropout", fast<dropout>(), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "zs_torch", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import importlib.util
+import operator
 import os
 import re
 import threading
@@ -114,6 +115,25 @@ def load(build_if_missing: bool = True):
         lib.zs_adamw_step.argtypes = [P, I32, I32, I32, P, P, P]
         lib.zs_adamw_step_seeded.restype = ctypes.c_int
         lib.zs_adamw_step_seeded.argtypes = [P, I32, I32, I32, P, ctypes.c_uint64, P, P]
+        U32, U64 = ctypes.c_uint32, ctypes.c_uint64
+        lib.zs_embedding.restype = ctypes.c_int
+        lib.zs_embedding.argtypes = [I32, P, I64, P, I64, I32, I32, F32, P, I64, P]
+        lib.zs_embedding_backward_workspace_bytes.restype = SZ
+        lib.zs_embedding_backward_workspace_bytes.argtypes = [I32, I64, I32, I32]
+        lib.zs_embedding_backward.restype = ctypes.c_int
+        lib.zs_embedding_backward.argtypes = [I32, P, I64, P, P, I64, I32, I32, F32, P, P, SZ, P]
+        lib.zs_route.restype = ctypes.c_int
+        lib.zs_route.argtypes = [I32, I32, P, I64, P, I64, I32, I32, I32, I32, I32, I32, F32, P, P, P]
+        lib.zs_route_backward.restype = ctypes.c_int
+        lib.zs_route_backward.argtypes = [I32, I32, P, P, I64, P, I64, I32, I32, I32, F32, P, P]
+        lib.zs_dispatch.restype = ctypes.c_int
+        lib.zs_dispatch.argtypes = [I32, P, I64, P, P, I64, I32, I32, I32, P, P, P]
+        lib.zs_combine.restype = ctypes.c_int
+        lib.zs_combine.argtypes = [I32, P, I64, P, P, I64, I32, I64, I32, P, I64, P]
+        lib.zs_combine_backward.restype = ctypes.c_int
+        lib.zs_combine_backward.argtypes = [I32, P, I64, P, I64, P, P, P, I64, I32, I32, I32, P, P, P]
+        lib.zs_dropout.restype = ctypes.c_int
+        lib.zs_dropout.argtypes = [I32, P, I64, P, I64, I64, I32, ctypes.c_double, U64, U32, I64, P, P, I64, P]
         _lib = lib
         return lib
 
@@ -122,7 +142,9 @@ class _Fast:
     """zs_torch, the short way for ordinary operands; built if need be and loaded on first
     use.  Where that fails, every call is left to the binding."""
 
-    NAMES = ("matmul", "dw", "norm", "norm_backward")
+    NAMES = ("matmul", "dw", "norm", "norm_backward", "embedding", "embedding_backward", "route", "route_backward", "dispatch",
+             "combine", "combine_backward", "dropout")
+    LIBRARY = ("zs_grouped", "zs_norm", "zs_embedding", "zs_route", "zs_dispatch", "zs_combine", "zs_dropout")
 
     def __getattr__(self, name):
         if name not in self.NAMES:
@@ -132,7 +154,7 @@ class _Fast:
             spec = importlib.util.spec_from_file_location("zs_torch", _build.build_ext())
             ext = importlib.util.module_from_spec(spec)
             spec.loader.exec_module(ext)
-            names = [n for n in declared_functions() if n.startswith(("zs_grouped", "zs_norm"))]
+            names = [n for n in declared_functions() if n.startswith(self.LIBRARY)]
             ext.bind({n: ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names}, _check)
             calls = {n: getattr(ext, n) for n in self.NAMES}
         except Exception as e:
@@ -959,3 +981,276 @@ def zs_adamw_step(plan: AdamWPlan, step: int, lr: float, beta1: float = 0.9, bet
                                          ctypes.addressof(hyper), seed & (1 << 64) - 1, scale_ptr, _stream(stream))
     if st:
         _check("zs_adamw_step", st)
+
+
+# ---------------------------------------------------------------------------
+# A block whose rows go to several experts: embedding, routing, the way to the
+# experts' grouped products and back, dropout.
+
+SCORE_KINDS = {"softmax": 0, "sigmoid": 1}
+
+
+def _int(value, name: str, lo: int, hi: int) -> int:
+    """An integer in [lo, hi]: what the C call's argument can hold."""
+    value = operator.index(value)
+    if not lo <= value <= hi:
+        raise ValueError(f"{name} must be in [{lo}, {hi}], got {value}")
+    return value
+
+
+_I32, _U32 = (1 << 31) - 1, (1 << 32) - 1
+
+
+def zs_embedding(w: torch.Tensor, ids: torch.Tensor, scale: float = 1.0, stream=None) -> torch.Tensor:
+    """y[i] = scale * w[ids[i]]: w (V, C) float32, bfloat16 or float16 (a row-strided view
+    allowed), ids (M,) int32; rows of ids outside [0, V) are zeros.  Returns y (M, C)."""
+    if stream is not None:
+        return _on(stream, zs_embedding, w, ids, scale)
+    y = _fast.embedding(w, ids, scale)
+    if y is not NotImplemented:
+        return y
+    device = _elsewhere(w, ids)
+    if device is not None:
+        with torch.cuda.device(device):
+            return zs_embedding(w, ids, scale)
+    V, C = _rows(w, "w")
+    d, M = _dtype(w, "w"), ids.numel()
+    ld = _matrix(w, "w", w.dtype, V, C)
+    ip = _array(ids, "ids", torch.int32, (M,))
+    y = torch.empty((M, C), dtype=w.dtype, device=w.device)
+    st = load().zs_embedding(d, _ptr(w), ld, ip, M, _int(V, "V", 0, _I32), _int(C, "C", 0, _I32), scale, _ptr(y), C, _stream(None))
+    if st:
+        _check("zs_embedding", st)
+    return y
+
+
+def zs_embedding_backward(dy: torch.Tensor, row_ptr: torch.Tensor, perm: torch.Tensor, scale: float = 1.0,
+                          stream=None) -> torch.Tensor:
+    """dw[v] = scale * the sum of dy over the rows that hold v: the gradient of zs_embedding in
+    w, (V, C) of dy's type, from the CSR (row_ptr (V+1,), perm (M,)) of zs_build_csr(ids, V)."""
+    if stream is not None:
+        return _on(stream, zs_embedding_backward, dy, row_ptr, perm, scale)
+    dw = _fast.embedding_backward(dy, row_ptr, perm, scale)
+    if dw is not NotImplemented:
+        return dw
+    device = _elsewhere(dy, row_ptr, perm)
+    if device is not None:
+        with torch.cuda.device(device):
+            return zs_embedding_backward(dy, row_ptr, perm, scale)
+    M, C = _rows(dy, "dy")
+    d, V = _dtype(dy, "dy"), row_ptr.numel() - 1
+    _int(V, "V = row_ptr.numel() - 1", 0, _I32), _int(C, "C", 0, _I32)
+    ld = _matrix(dy, "dy", dy.dtype, M, C)
+    rp, pp = _array(row_ptr, "row_ptr", torch.int32, (V + 1,)), _array(perm, "perm", torch.int32, (M,))
+    dw = torch.empty((V, C), dtype=dy.dtype, device=dy.device)
+    lib = load()
+    need = lib.zs_embedding_backward_workspace_bytes(d, M, V, C)
+    workspace = _workspace(need, dy.device)
+    st = lib.zs_embedding_backward(d, _ptr(dy), ld, rp, pp, M, V, C, scale, _ptr(dw), _ptr(workspace), need, _stream(None))
+    if st:
+        _check("zs_embedding_backward", st)
+    return dw
+
+
+def _score(score: str) -> int:
+    kind = SCORE_KINDS.get(score)
+    if kind is None:
+        raise ValueError(f"score must be one of {sorted(SCORE_KINDS)}, got {score!r}")
+    return kind
+
+
+def zs_route(logits: torch.Tensor, k: int, bias: torch.Tensor | None = None, score: str = "softmax", groups: int = 1,
+             top_groups: int | None = None, group_top: int = 1, renormalise: bool = True, scale: float = 1.0, stream=None):
+    """The k experts of each row with the largest score + bias among its best groups of
+    experts, and their weights.
+
+    logits (M, E) float32, bfloat16 or float16 (a row-strided view allowed; -inf closes an
+    expert to a row), bias (E,) float32 or None (it counts for the choice alone), score
+    "softmax" or "sigmoid".  The experts are in ``groups`` groups in a row; a group's value is
+    the sum of its ``group_top`` (1 or 2) largest score + bias, and only the ``top_groups``
+    groups with the largest values are open (None: all).  Returns (ids (M, k) int32, weights
+    (M, k) float32): ids in descending order, equal ones by index, -1 behind the last open
+    expert; weights scale * score, of scores divided by their sum over the row's choices with
+    ``renormalise``."""
+    if stream is not None:
+        return _on(stream, zs_route, logits, k, bias, score, groups, top_groups, group_top, renormalise, scale)
+    if score in SCORE_KINDS:
+        r = _fast.route(logits, k, bias, SCORE_KINDS[score], groups, groups if top_groups is None else top_groups, group_top,
+                        renormalise, scale)
+        if r is not NotImplemented:
+            return r
+    device = _elsewhere(logits, bias)
+    if device is not None:
+        with torch.cuda.device(device):
+            return zs_route(logits, k, bias, score, groups, top_groups, group_top, renormalise, scale)
+    kind = _score(score)
+    M, E = _rows(logits, "logits")
+    d = _dtype(logits, "logits")
+    ld = _matrix(logits, "logits", logits.dtype, M, E)
+    bp = None if bias is None else _array(bias, "bias", torch.float32, (E,))
+    k, groups = _int(k, "k", 1, E), _int(groups, "groups", 1, _I32)
+    top_groups = groups if top_groups is None else _int(top_groups, "top_groups", 1, _I32)
+    ids = torch.empty((M, k), dtype=torch.int32, device=logits.device)
+    weights = torch.empty((M, k), dtype=torch.float32, device=logits.device)
+    st = load().zs_route(d, kind, _ptr(logits), ld, bp, M, _int(E, "E", 0, _I32), k, groups, top_groups,
+                         _int(group_top, "group_top", 1, 2), bool(renormalise), scale, _ptr(ids), _ptr(weights), _stream(None))
+    if st:
+        _check("zs_route", st)
+    return ids, weights
+
+
+def zs_route_backward(dweights: torch.Tensor, logits: torch.Tensor, ids: torch.Tensor, score: str = "softmax",
+                      renormalise: bool = True, scale: float = 1.0, stream=None) -> torch.Tensor:
+    """The gradient of zs_route's weights in the logits, the choice ``ids`` held fixed:
+    dlogits (M, E) of the logits' type for the cotangent dweights (M, k) float32."""
+    if stream is not None:
+        return _on(stream, zs_route_backward, dweights, logits, ids, score, renormalise, scale)
+    if score in SCORE_KINDS:
+        r = _fast.route_backward(dweights, logits, ids, SCORE_KINDS[score], renormalise, scale)
+        if r is not NotImplemented:
+            return r
+    device = _elsewhere(dweights, logits, ids)
+    if device is not None:
+        with torch.cuda.device(device):
+            return zs_route_backward(dweights, logits, ids, score, renormalise, scale)
+    kind = _score(score)
+    M, E = _rows(logits, "logits")
+    _, k = _rows(ids, "ids")
+    d = _dtype(logits, "logits")
+    ld = _matrix(logits, "logits", logits.dtype, M, E)
+    ip, gp = _array(ids, "ids", torch.int32, (M, k)), _array(dweights, "dweights", torch.float32, (M, k))
+    dlogits = torch.empty((M, E), dtype=logits.dtype, device=logits.device)
+    st = load().zs_route_backward(d, kind, gp, _ptr(logits), ld, ip, M, _int(E, "E", 0, _I32), k, bool(renormalise), scale,
+                                  _ptr(dlogits), _stream(None))
+    if st:
+        _check("zs_route_backward", st)
+    return dlogits
+
+
+def zs_dispatch(x: torch.Tensor, row_ptr: torch.Tensor, perm: torch.Tensor, k: int, stream=None):
+    """Rows to their experts: with (row_ptr (G+1,), perm (M*k,)) the CSR zs_build_csr gives for the
+    flattened ids (M, k) of zs_route, xs[p] = x[perm[p] // k] (zeros from position row_ptr[G]),
+    in the order of zs_grouped_matmul without a perm, and slot[perm[p]] = p (-1 without a group).
+    x (M, C) float32, bfloat16 or float16 (a row-strided view allowed).  Returns (xs (M*k, C),
+    slot (M, k) int32)."""
+    if stream is not None:
+        return _on(stream, zs_dispatch, x, row_ptr, perm, k)
+    r = _fast.dispatch(x, row_ptr, perm, k)
+    if r is not NotImplemented:
+        return r
+    device = _elsewhere(x, row_ptr, perm)
+    if device is not None:
+        with torch.cuda.device(device):
+            return zs_dispatch(x, row_ptr, perm, k)
+    M, C = _rows(x, "x")
+    d, k, G = _dtype(x, "x"), _int(k, "k", 1, _I32), row_ptr.numel() - 1
+    ld = _matrix(x, "x", x.dtype, M, C)
+    rp, pp = _array(row_ptr, "row_ptr", torch.int32, (G + 1,)), _array(perm, "perm", torch.int32, (M * k,))
+    xs = torch.empty((M * k, C), dtype=x.dtype, device=x.device)
+    slot = torch.empty((M, k), dtype=torch.int32, device=x.device)
+    st = load().zs_dispatch(d, _ptr(x), ld, rp, pp, M, k, _int(G, "G = row_ptr.numel() - 1", 0, _I32), _int(C, "C", 0, _I32), _ptr(xs),
+                            _ptr(slot), _stream(None))
+    if st:
+        _check("zs_dispatch", st)
+    return xs, slot
+
+
+def zs_combine(h: torch.Tensor, slot: torch.Tensor, weights: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """And back: y[i] = the sum over j of weights[i, j] * h[slot[i, j]]; slots outside [0, R) add
+    nothing.  h (R, C) float32, bfloat16 or float16 (a row-strided view allowed), slot (M, k)
+    int32, weights (M, k) float32.  Without weights it is the gradient of zs_dispatch in x."""
+    if stream is not None:
+        return _on(stream, zs_combine, h, slot, weights)
+    y = _fast.combine(h, slot, weights)
+    if y is not NotImplemented:
+        return y
+    device = _elsewhere(h, slot, weights)
+    if device is not None:
+        with torch.cuda.device(device):
+            return zs_combine(h, slot, weights)
+    R, C = _rows(h, "h")
+    M, k = _rows(slot, "slot")
+    d = _dtype(h, "h")
+    ld = _matrix(h, "h", h.dtype, R, C)
+    sp = _array(slot, "slot", torch.int32, (M, k))
+    wp = None if weights is None else _array(weights, "weights", torch.float32, (M, k))
+    y = torch.empty((M, C), dtype=h.dtype, device=h.device)
+    st = load().zs_combine(d, _ptr(h), ld, sp, wp, M, _int(k, "k", 1, _I32), R, _int(C, "C", 0, _I32), _ptr(y), C, _stream(None))
+    if st:
+        _check("zs_combine", st)
+    return y
+
+
+def zs_combine_backward(dy: torch.Tensor, h: torch.Tensor, slot: torch.Tensor, weights: torch.Tensor, row_ptr: torch.Tensor,
+                        stream=None):
+    """Gradients of zs_combine with weights, for the slots and the CSR's row_ptr of zs_dispatch:
+    (dh (M*k, C), zeros from position row_ptr[G]; dweights (M, k) float32, 0 without a slot)."""
+    if stream is not None:
+        return _on(stream, zs_combine_backward, dy, h, slot, weights, row_ptr)
+    r = _fast.combine_backward(dy, h, slot, weights, row_ptr)
+    if r is not NotImplemented:
+        return r
+    device = _elsewhere(dy, h, slot, weights, row_ptr)
+    if device is not None:
+        with torch.cuda.device(device):
+            return zs_combine_backward(dy, h, slot, weights, row_ptr)
+    _, C = _rows(h, "h")
+    M, k = _rows(slot, "slot")
+    d, dt, G = _dtype(h, "h"), h.dtype, row_ptr.numel() - 1
+    h_ld = _matrix(h, "h", dt, M * k, C)
+    dy_ld = _matrix(dy, "dy", dt, M, C)
+    sp, wp = _array(slot, "slot", torch.int32, (M, k)), _array(weights, "weights", torch.float32, (M, k))
+    rp = _array(row_ptr, "row_ptr", torch.int32, (G + 1,))
+    dh = torch.empty((M * k, C), dtype=dt, device=h.device)
+    dweights = torch.empty((M, k), dtype=torch.float32, device=h.device)
+    st = load().zs_combine_backward(d, _ptr(dy), dy_ld, _ptr(h), h_ld, sp, wp, rp, M, _int(k, "k", 1, _I32),
+                                    _int(G, "G = row_ptr.numel() - 1", 0, _I32), _int(C, "C", 0, _I32), _ptr(dh), _ptr(dweights),
+                                    _stream(None))
+    if st:
+        _check("zs_combine_backward", st)
+    return dh, dweights
+
+
+def zs_dropout(h: torch.Tensor, p: float, seed: int, call: int = 0, step: int | torch.Tensor = 0,
+               residual: torch.Tensor | None = None, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """residual + dropout(h): elements are dropped with probability p (to 1 / 65536), the others
+    divided by 1 - p.  The mask follows from the elements' numbers in their order, the seed (64
+    bits), ``call`` (32 bits: which of a step's dropouts this is) and ``step``: a number, or one
+    int64 element on the device, which a captured call reads at each replay.  It is drawn again
+    where it is needed: the gradient in h is zs_dropout(dy, p, seed, call, step).
+
+    h float32, bfloat16 or float16, of any shape where it is contiguous, or a matrix with
+    contiguous rows; residual and out like h (out may be h or residual)."""
+    if stream is not None:
+        return _on(stream, zs_dropout, h, p, seed, call, step, residual, out)
+    if out is None:
+        y = _fast.dropout(h, p, seed, call, step, residual)
+        if y is not NotImplemented:
+            return y
+    device = _elsewhere(h, residual, out, step)
+    if device is not None:
+        with torch.cuda.device(device):
+            return zs_dropout(h, p, seed, call, step, residual, out)
+    d, shape = _dtype(h, "h"), h.shape
+    if out is None:
+        out = torch.empty(shape, dtype=h.dtype, device=h.device)
+    given = {"h": h, "residual": residual, "out": out}
+    if h.dim() == 2:
+        M, C = shape
+        at = {n: (None, 0) if t is None else (_ptr(t), _matrix(t, n, h.dtype, M, C)) for n, t in given.items()}
+    else:
+        C = int(shape[-1]) if h.dim() else 1
+        M = h.numel() // C if C else 0
+        at = {n: (None, 0) if t is None else (_array(t, n, h.dtype, shape) or None, C) for n, t in given.items()}
+    call, step_ptr = _int(call, "call", 0, _U32), None
+    if isinstance(step, torch.Tensor):
+        if not step.is_cuda or step.dtype != torch.int64 or step.numel() != 1:
+            raise ValueError("step must be a number or one int64 element on the device")
+        step_ptr, step = step.data_ptr(), 0
+    if M * C == 0:
+        return out
+    st = load().zs_dropout(d, *at["h"], *at["residual"], M, _int(C, "C", 0, _I32), p, operator.index(seed) & (1 << 64) - 1, call,
+                           _int(step, "step", -1 << 63, (1 << 63) - 1), step_ptr, *at["out"], _stream(None))
+    if st:
+        _check("zs_dropout", st)
+    return out

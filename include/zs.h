@@ -534,6 +534,146 @@ ZS_API zs_status zs_adamw_step_seeded(const zs_adamw_tensor* tensors, int32_t co
                                       const zs_adamw_hyper* hyper, uint64_t seed, const float* grad_scale,
                                       zs_stream_t stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * Operators of a block whose rows go to several experts: the embedding the
+ * rows start from, the choice of their experts, their way to the experts'
+ * grouped products and back, and dropout on the way to the residual stream.
+ * The conventions of the training operators hold.
+ */
+
+/*
+ * Embedding: y[i,:] = scale * w[ids[i],:], rounded once.
+ *   dtype     zs_dtype of w and y
+ *   w (V, C)  rows w_ld elements apart
+ *   ids (M,)  int32; rows of ids outside [0, V) are zeros
+ *   scale     finite
+ *   y (M, C)  rows y_ld elements apart, fully written
+ * M, V and C up to 2^31 - 2^16, C >= 1; M = 0 and V = 0 are valid.
+ */
+ZS_API zs_status zs_embedding(int32_t dtype, const void* w, int64_t w_ld, const int32_t* ids,
+                              int64_t M, int32_t V, int32_t C, float scale,
+                              void* y, int64_t y_ld, zs_stream_t stream);
+
+/*
+ * Gradient of zs_embedding in w:  dw[v,:] = scale * sum of dy[i,:] over the
+ * rows i with ids[i] = v, from the CSR (row_ptr (V+1), perm (M)) that
+ * zs_build_csr gives for the ids.
+ *   dy (M, C)  rows dy_ld elements apart; rows of no id are not used
+ *   dw (V, C)  contiguous, of dy's type, fully written (zeros for ids that no
+ *              row has)
+ *   workspace  zs_embedding_backward_workspace_bytes(dtype, M, V, C) bytes,
+ *              256-byte aligned
+ * Sums are in fp32, in an order that follows from the sizes.
+ */
+ZS_API size_t zs_embedding_backward_workspace_bytes(int32_t dtype, int64_t M, int32_t V, int32_t C);
+ZS_API zs_status zs_embedding_backward(int32_t dtype, const void* dy, int64_t dy_ld, const int32_t* row_ptr,
+                                       const int32_t* perm, int64_t M, int32_t V, int32_t C, float scale,
+                                       void* dw, void* workspace, size_t workspace_bytes, zs_stream_t stream);
+
+/* Scores of a row of logits z: exp(z_e) over the sum of them, or 1 / (1 + exp(-z_e)). */
+typedef enum zs_score_kind {
+    ZS_SCORE_SOFTMAX = 0,
+    ZS_SCORE_SIGMOID = 1
+} zs_score_kind;
+
+/*
+ * Routing: for each row of logits the k experts with the largest score + bias,
+ * and their weights.  The E experts are in `groups` groups of E / groups in a
+ * row; a group's value is the sum of its group_top largest score + bias, and
+ * only the experts of the top_groups groups with the largest values are open.
+ *   dtype           zs_dtype of the logits
+ *   logits (M, E)   rows logits_ld elements apart; an expert whose logit is
+ *                   -infinity is closed to the row
+ *   bias (E,)       fp32, may be NULL: for the choice alone, not in the weights
+ *   ids (M, k)      int32: in descending order of score + bias, equal ones by
+ *                   their index; -1 behind the last open expert
+ *   weights (M, k)  fp32: scale * score, the scores divided by their sum over
+ *                   the row's choices where renormalise is not 0; 0 where the
+ *                   id is -1
+ * The choice is that of scores and sums in 64 bits (among logits alone, where
+ * there is neither a bias nor a choice of groups: they sort like their scores);
+ * NaN counts as the largest value, and an expert whose bias is -infinity is
+ * closed.  1 <= k <= E, scale finite.  ZS_ERR_UNSUPPORTED for E above 1024, k
+ * above 32, groups above 32, and where E / groups times the next power of two
+ * of groups is above 1024.
+ */
+ZS_API zs_status zs_route(int32_t dtype, int32_t score, const void* logits, int64_t logits_ld, const float* bias,
+                          int64_t M, int32_t E, int32_t k, int32_t groups, int32_t top_groups, int32_t group_top,
+                          int32_t renormalise, float scale, int32_t* ids, float* weights, zs_stream_t stream);
+
+/*
+ * Gradient of zs_route's weights in the logits, the choice held fixed.
+ *   dweights (M, k)  fp32 cotangent of the weights
+ *   ids (M, k)       the forward's; ids outside [0, E) add nothing
+ *   dlogits (M, E)   contiguous, of the logits' type, fully written
+ */
+ZS_API zs_status zs_route_backward(int32_t dtype, int32_t score, const float* dweights, const void* logits,
+                                   int64_t logits_ld, const int32_t* ids, int64_t M, int32_t E, int32_t k,
+                                   int32_t renormalise, float scale, void* dlogits, zs_stream_t stream);
+
+/*
+ * Rows to their experts: an assignment a = i * k + j is row i's choice j, and
+ * (row_ptr (G+1), perm (M*k)) the CSR that zs_build_csr gives for the ids of the
+ * assignments.
+ *   xs[p,:] = x[perm[p] / k,:]      for positions p < row_ptr[G], zeros behind
+ *   slot[perm[p]] = p               -1 for assignments of no group
+ * so that xs is in the order of zs_grouped_matmul without a perm.
+ *   x (M, C)      rows x_ld elements apart
+ *   xs (M*k, C)   contiguous, fully written
+ *   slot (M, k)   int32, fully written
+ * M * k and C up to 2^31 - 2^16, k >= 1.
+ */
+ZS_API zs_status zs_dispatch(int32_t dtype, const void* x, int64_t x_ld, const int32_t* row_ptr, const int32_t* perm,
+                             int64_t M, int32_t k, int32_t G, int32_t C, void* xs, int32_t* slot, zs_stream_t stream);
+
+/*
+ * And back:  y[i,:] = sum over j of weights[i,j] * h[slot[i,j],:], in the order
+ * of j, rounded once; slots outside [0, R) add nothing.  Without weights (NULL)
+ * it is the gradient of zs_dispatch: dx[i,:] = sum over j of dxs[slot[i,j],:].
+ *   h (R, C)        rows h_ld elements apart
+ *   weights (M, k)  fp32, may be NULL (1)
+ *   y (M, C)        rows y_ld elements apart, fully written
+ */
+ZS_API zs_status zs_combine(int32_t dtype, const void* h, int64_t h_ld, const int32_t* slot, const float* weights,
+                            int64_t M, int32_t k, int64_t R, int32_t C, void* y, int64_t y_ld, zs_stream_t stream);
+
+/*
+ * Gradients of zs_combine for slots as zs_dispatch gives them (each position
+ * below row_ptr[G] once):
+ *   dh[slot[i,j],:] = weights[i,j] * dy[i,:]      zeros from position row_ptr[G]
+ *   dweights[i,j] = sum over c of dy[i,c] * h[slot[i,j],c]   0 without a slot
+ *   dy (M, C), h (M*k, C)  rows dy_ld, h_ld elements apart
+ *   dh (M*k, C)            contiguous, fully written
+ *   dweights (M, k)        fp32, fully written
+ */
+ZS_API zs_status zs_combine_backward(int32_t dtype, const void* dy, int64_t dy_ld, const void* h, int64_t h_ld,
+                                     const int32_t* slot, const float* weights, const int32_t* row_ptr,
+                                     int64_t M, int32_t k, int32_t G, int32_t C,
+                                     void* dh, float* dweights, zs_stream_t stream);
+
+/*
+ * Dropout:  y = residual + (kept ? h * 65536 / (65536 - limit) : 0), rounded
+ * once, limit = 65536 p rounded to an integer.  Element (i, c), e = i * C + c, is
+ * kept where its 16 random bits are not below limit: half e % 2 (the low one
+ * first) of word (e % 8) / 2 of Philox 4x32 with 10 rounds (Salmon, Moraes,
+ * Dror, Shaw 2011), counter (low and high half of e / 8, call, low half of the
+ * step), key (low and high half of seed).  The mask follows from these numbers,
+ * whatever the strides: the gradient in h is the same call on the cotangent,
+ * without a residual.
+ *   h, residual, y (M, C)  rows h_ld, residual_ld, y_ld elements apart;
+ *                          residual may be NULL (0); y may be h or residual
+ *   p        in [0, 1]; what is dropped counts as 0 whatever it holds
+ *   call     which of a step's dropouts this is
+ *   step     which step, plus *step_at where step_at is not NULL: a count on
+ *            the device, read when the kernel runs, so that a captured call
+ *            draws another mask at each replay
+ * M * C below 2^41.
+ */
+ZS_API zs_status zs_dropout(int32_t dtype, const void* h, int64_t h_ld, const void* residual, int64_t residual_ld,
+                            int64_t M, int32_t C, double p, uint64_t seed, uint32_t call, int64_t step,
+                            const int64_t* step_at, void* y, int64_t y_ld, zs_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
