@@ -1,32 +1,40 @@
 // Routing of rows to experts, and the gradient of the logits.
 //
-// A warp takes a row.  Its lanes hold the experts in ascending order, those of
-// a group of experts in neighbouring lanes, so that the lowest lane among equal
-// ones has the lowest index.  Scores become unsigned keys that sort like them
-// (0: closed), and k rounds of a warp maximum pick the experts.
+// A warp takes a row.  Its lanes hold up to V experts each in ascending order,
+// those of a group of experts in neighbouring lanes, so that the lowest lane
+// among equal ones has the lowest index.  Values become unsigned keys that sort
+// like them (0: closed), the last bits of a key the expert's place in its lane.
+// A lane sorts its keys by a network of minima and maxima and lays them down in
+// shared memory; then k rounds of a warp maximum over the lanes' first keys pick
+// the experts, and the lane that a round took from moves on to its next key.
 //
 // The choice is that of the scores in 64 bits.  Without a bias and groups it
-// goes by the logits themselves, which sort like their scores.  Otherwise scores
-// are formed in 32 bits, with a bound of their error; where two neighbours of
-// the choice lie closer than that (and are not of one logit and bias), the row is
-// done again in 64 bits.  Weights are formed in 32 bits, relative to the largest
-// chosen logit where they are renormalised, so that they never are 0 / 0.
+// goes by the logits themselves, which sort like their scores.  Keys hold values
+// to a bound that is known (the place's bits, and the error of scores, which are
+// formed in 32 bits); where two neighbours of the choice lie closer than that
+// (and are not of one logit and bias), the row is done again in 64 bits: about
+// one row in a thousand of ordinary ones.  Weights are formed in 32 bits,
+// relative to the largest chosen logit where they are renormalised, so that they
+// never are 0 / 0.
 //
-// What bounds it: instructions, k rounds of about 3 E / 32 of them a row.
+// What bounds it: instructions, a few hundred a row.
 #include "zs_types.cuh"
 
 namespace zs {
 namespace {
 
 constexpr int kRouteMaxE = 1024, kRouteMaxK = 32, kRouteMaxGroups = 32;
-constexpr int kRouteWarps = 8;
+constexpr int kRouteWarps = 4;
 constexpr unsigned kAll = 0xffffffffu;
 
 struct RouteShape {
     int64_t M, ld;
     int32_t E, k, groups, per, top_groups, group_top;
-    int32_t lanes, each;    // lanes of a group, experts of a lane
+    int32_t lanes, each;    // lanes of a group (a power of two), experts of a lane
+    int32_t lane_bits;      // log2 of lanes
+    int32_t width;          // the least power of two that holds k
     bool sigmoid, renormalise;
+    bool wide, wide_bias;   // a lane's logits and biases are whole 16-byte pieces
     float scale;
 };
 
@@ -66,24 +74,37 @@ __device__ __forceinline__ F from_key(typename KeyOf<F>::U k) {
     return KeyOf<F>::value(k & top ? k & ~top : ~k);
 }
 
+// 2^x and 1 / x by one instruction each (2 ulps and 1, numbers below the normal ones as 0).
+__device__ __forceinline__ float exp2_quick(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float reciprocal_quick(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+constexpr float kLog2e = 1.44269504088896341f;
+
 template <typename F>
 __device__ __forceinline__ F sum_of_warp(F v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
     return v;
 }
-__device__ __forceinline__ float max_of_warp(float v) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, o));
-    return v;
+__device__ __forceinline__ float max_of_warp(float v) {   // NaN are passed over
+    float m;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
+    return m;
 }
 
 // A lane's experts.
 struct Lane {
     int group, first, count;
     __device__ __forceinline__ Lane(const RouteShape& s, int lane) {
-        group = lane / s.lanes;
-        const int at = (lane - group * s.lanes) * s.each;
+        group = lane >> s.lane_bits;
+        const int at = (lane & (s.lanes - 1)) * s.each;
         first = group * s.per + at;
         count = group < s.groups ? imax(imin(s.per - at, s.each), 0) : 0;
     }
@@ -92,130 +113,389 @@ struct Lane {
 template <typename T>
 __device__ __forceinline__ float logit(const T* row, int e) { return to_f32(__ldg(row + e)); }
 
-// Keeps the keys of the best groups, zeroes the others.  Returns whether the last group in and the first one out are
-// closer than their scores are known, each to `error` and the rounding of its sum.
-template <typename F, int V>
-__device__ __forceinline__ bool keep_groups(const RouteShape& s, const Lane& l, typename KeyOf<F>::U (&key)[V], F error) {
-    using U = typename KeyOf<F>::U;
-    U first = 0, second = 0;
+// A lane's keys, the largest first: Batcher's merge exchange sort, V a power of two.
+template <int V>
+__device__ __forceinline__ void sort_keys(uint32_t (&key)[V]) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const U k = key[i];
-        second = k > first ? first : (k > second ? k : second);
-        first = k > first ? k : first;
-    }
+    for (int p = 1; p < V; p *= 2)
+#pragma unroll
+        for (int k = p; k >= 1; k /= 2)
+#pragma unroll
+            for (int j = k % p; j <= V - 1 - k; j += 2 * k)
+#pragma unroll
+                for (int i = 0; i < k; ++i)
+                    if (i + j + k < V && (i + j) / (2 * p) == (i + j + k) / (2 * p)) {
+                        const uint32_t a = key[i + j], b = key[i + j + k];
+                        key[i + j] = max(a, b);
+                        key[i + j + k] = min(a, b);
+                    }
+}
+
+// The two largest keys of a lane's group, from those of its lanes.
+template <typename U>
+__device__ __forceinline__ void two_of_group(const RouteShape& s, U& first, U& second) {
     for (int o = 1; o < s.lanes; o <<= 1) {
         const U a = __shfl_xor_sync(kAll, first, o), b = __shfl_xor_sync(kAll, second, o);
-        second = a > first ? (b > first ? b : first) : (a > second ? a : second);
-        first = a > first ? a : first;
+        second = max(min(a, first), a > first ? b : second);
+        first = max(a, first);
     }
-    U value = 0;
-    F size = 0;   // of what the sum is formed of
-    if (first) {
+}
+// Whether a lane's group is among the best, by its two largest keys, and in `close` whether the last group in and the
+// first one out are closer than known: each score to `error`, each value to `relative` of itself.
+template <typename F>
+__device__ __forceinline__ bool group_kept(const RouteShape& s, const Lane& l, typename KeyOf<F>::U first, typename KeyOf<F>::U second,
+                                           F error, F relative, bool& close) {
+    using U = typename KeyOf<F>::U;
+    U left = 0, last = 0;
+    F size = 0, last_size = 0;   // of what a sum is formed of
+    if (first && l.group < s.groups) {
         F v = from_key<F>(first);
         size = fabs(v);
-        if (first == ~(U)0 || (s.group_top == 2 && second == ~(U)0)) {
-            v = (F)NAN;
-        } else if (s.group_top == 2 && second) {
+        if (s.group_top == 2 && second) {
             const F w = from_key<F>(second);
             v += w;
             size += fabs(w);
         }
-        value = to_key<F>(v);
-        if (!value) value = 1;
+        left = to_key<F>(v);
+        if (!left) left = 1;
     }
-    int ahead = 0;
-    for (int g = 0; g < s.groups; ++g) {
-        const U other = __shfl_sync(kAll, value, g * s.lanes);
-        ahead += other > value || (other == value && g < l.group);
+    // rounds: the lowest group of the largest value is kept; the one behind the last is only looked at
+    bool kept = false;
+    for (int r = 0;; ++r) {
+        const U top = KeyOf<F>::max_of_warp(left);
+        if (top == 0) break;
+        const int winner = __ffs(__ballot_sync(kAll, left == top)) - 1;
+        const F winner_size = __shfl_sync(kAll, size, winner);
+        if (r == s.top_groups) {
+            close = from_key<F>(last) - from_key<F>(top) <= 4 * error + relative * (last_size + winner_size);
+            break;
+        }
+        last = top;
+        last_size = winner_size;
+        if (l.group == winner >> s.lane_bits) kept = true, left = 0;
     }
-    const bool kept = l.group < s.groups && ahead < s.top_groups;
-    const bool last = kept && ahead == s.top_groups - 1, next = l.group < s.groups && ahead == s.top_groups;
-    const unsigned in = __ballot_sync(kAll, last), out = __ballot_sync(kAll, next);
-    bool close = false;
-    if (in && out) {
-        const int p = __ffs(in) - 1, q = __ffs(out) - 1;
-        const U a = __shfl_sync(kAll, value, p), b = __shfl_sync(kAll, value, q);
-        const F sizes = __shfl_sync(kAll, size, p) + __shfl_sync(kAll, size, q);
-        close = a && b && from_key<F>(a) - from_key<F>(b) <= 4 * error + (F)0x1p-22 * sizes;
-    }
-    if (!kept)
-#pragma unroll
-        for (int i = 0; i < V; ++i) key[i] = 0;
-    return close;
+    return kept;
 }
 
-// The largest key of the warp, taken out: its expert in `e` (of the lowest index), the key returned (0: none left).
-template <typename F, int V>
-__device__ __forceinline__ typename KeyOf<F>::U take(const Lane& l, int lane, typename KeyOf<F>::U (&key)[V], int& e) {
-    using U = typename KeyOf<F>::U;
-    U best = key[0];
-#pragma unroll
-    for (int i = 1; i < V; ++i) best = key[i] > best ? key[i] : best;
-    const U top = KeyOf<F>::max_of_warp(best);
-    if (top == 0) return 0;
-    const int winner = __ffs(__ballot_sync(kAll, best == top)) - 1;
-    int at = 0;
-#pragma unroll
-    for (int i = V - 1; i >= 0; --i) at = key[i] == top ? i : at;
-    if (lane == winner)
-#pragma unroll
-        for (int i = 0; i < V; ++i) key[i] = i == at ? 0 : key[i];
-    e = __shfl_sync(kAll, l.first + at, winner);
-    return top;
+// What the choice goes by, in 64 bits: -infinity where it is closed.  `top` and `sum` for a softmax with a bias.
+template <bool kScored>
+__device__ __forceinline__ double score_in_64_bits(const RouteShape& s, double z, double top, double sum, const float* __restrict__ bias,
+                                                   int e) {
+    if (!kScored || z == -INFINITY) return z;
+    const double a = s.sigmoid ? 1.0 / (1.0 + exp(-z)) : exp(z - top) / sum;
+    return bias ? a + (double)__ldg(bias + e) : a;
 }
 
 // The row's choice in 64 bits: the expert of choice `lane` (or -1).
-template <typename T, int V>
+template <typename T, int V, bool kScored>
 __device__ __noinline__ int choose_in_64_bits(const RouteShape& s, int lane, const T* __restrict__ row, const float* __restrict__ bias) {
+    using U = unsigned long long;
     const Lane l(s, lane);
-    double z[V], top = -INFINITY;
-    for (int i = 0; i < V; ++i) {
-        z[i] = i < l.count ? (double)logit(row, l.first + i) : -INFINITY;
-        top = z[i] > top ? z[i] : top;
-    }
-    double sum = 0.0;
-    if (!s.sigmoid) {
+    U key[V];
+    double top = -INFINITY, sum = 0.0;
+    if (kScored && !s.sigmoid) {
+#pragma unroll 1
+        for (int i = 0; i < l.count; ++i) top = fmax(top, (double)logit(row, l.first + i));
         for (int o = 16; o > 0; o >>= 1) top = fmax(top, __shfl_xor_sync(kAll, top, o));
-        for (int i = 0; i < V; ++i)
-            if (i < l.count && top != -INFINITY) sum += exp(z[i] - top);
+#pragma unroll 1
+        for (int i = 0; i < l.count; ++i) {
+            const float z = logit(row, l.first + i);
+            if (z != -INFINITY) sum += exp((double)z - top);
+        }
         sum = sum_of_warp(sum);
     }
-    unsigned long long key[V];
+#pragma unroll 1
     for (int i = 0; i < V; ++i) {
         key[i] = 0;
-        if (i >= l.count || z[i] == -INFINITY) continue;
-        const double score = s.sigmoid ? 1.0 / (1.0 + exp(-z[i])) : exp(z[i] - top) / sum;
-        key[i] = to_key<double>(score + (bias ? (double)__ldg(bias + l.first + i) : 0.0));
+        if (i < l.count) key[i] = to_key<double>(score_in_64_bits<kScored>(s, logit(row, l.first + i), top, sum, bias, l.first + i));
     }
-    if (s.top_groups < s.groups) keep_groups<double, V>(s, l, key, 0.0);
+    if (s.top_groups < s.groups) {
+        U first = 0, second = 0;
+        for (int i = 0; i < V; ++i) {
+            const U k = key[i];
+            second = k > first ? first : (k > second ? k : second);
+            first = k > first ? k : first;
+        }
+        bool close;
+        two_of_group(s, first, second);
+        if (!group_kept<double>(s, l, first, second, 0.0, 0.0, close))
+            for (int i = 0; i < V; ++i) key[i] = 0;
+    }
     int mine = -1;
+#pragma unroll 1
     for (int r = 0; r < s.k; ++r) {
-        int e = -1;
-        if (take<double, V>(l, lane, key, e) == 0) break;
+        U best = 0;
+        int at = 0;
+        for (int i = 0; i < V; ++i) {
+            at = key[i] > best ? i : at;
+            best = key[i] > best ? key[i] : best;
+        }
+        const U top_key = KeyOf<double>::max_of_warp(best);
+        if (top_key == 0) break;
+        const int winner = __ffs(__ballot_sync(kAll, best == top_key)) - 1;
+        if (lane == winner) key[at] = 0;
+        const int e = __shfl_sync(kAll, l.first + at, winner);
         if (lane == r) mine = e;
     }
     return mine;
 }
 
-// Shares of the chosen logits z (lanes with `held`) among themselves: softmax, or sigmoids over their sum.
-__device__ __forceinline__ float renormalised(bool sigmoid, bool held, float z) {
-    const float top = max_of_warp(held ? z : -INFINITY);
+// A lane's V neighbours: 16 bytes at a time where `wide`, closed ones behind `count`.
+template <typename T, int V>
+__device__ __forceinline__ void load_lane(const T* p, int count, bool wide, float none, float (&z)[V]) {
+    constexpr int N = kVec<T>;
+    if constexpr (V % N == 0) {
+        if (wide) {
+#pragma unroll
+            for (int q = 0; q < V / N; ++q) {
+                float f[N];
+                unpack<T>(count > 0 ? __ldg(reinterpret_cast<const uint4*>(p) + q) : make_uint4(0, 0, 0, 0), f);
+#pragma unroll
+                for (int i = 0; i < N; ++i) z[q * N + i] = count > 0 ? f[i] : none;
+            }
+            return;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) z[i] = i < count ? to_f32(__ldg(p + i)) : none;
+}
+
+// Shares of the chosen logits z (lanes with `held`) among those of `width` lanes: softmax, or sigmoids over their sum.
+__device__ __forceinline__ float renormalised(bool sigmoid, bool held, float z, int width) {
+    float top = held ? z : -INFINITY;
+    for (int o = width >> 1; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
     float t = 0.f;
     if (held) {
-        if (sigmoid) t = expf(fminf(z, 0.f) - fminf(top, 0.f)) / (1.f + expf(-fabsf(z)));
+        if (sigmoid) t = __fdividef(expf(fminf(z, 0.f) - fminf(top, 0.f)), 1.f + expf(-fabsf(z)));
         else t = expf(z - top);
         if (z != z) t = z;
     }
-    const float sum = sum_of_warp(t);
-    return held ? t / sum : 0.f;
+    float sum = t;
+    for (int o = width >> 1; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
+    return held ? __fdividef(t, sum) : 0.f;
 }
-__device__ __forceinline__ float sigmoid_of(float z) { return 1.f / (1.f + expf(-z)); }
+__device__ __forceinline__ float sigmoid_of(float z) { return __fdividef(1.f, 1.f + expf(-z)); }
+
+// What one row's rounds leave: how many they were, what its scores are relative to, and how far 32 bits know them.
+struct Picked {
+    int n;
+    float top, sum;   // a softmax's largest logit and sum, where it is formed
+    float error;      // of a score, beside its rounding
+    bool odd;         // NaN (of a lane's own)
+    bool close;       // groups whose choice 32 bits do not tell
+};
+
+// A warp's place in shared memory: its lanes' sorted keys, and what its rounds took (a key, and its lane).
+template <int V>
+struct RouteSpace {
+    uint32_t list[V + 1][32];
+    uint2 taken[kRouteMaxK + 1];   // the choices, and the one behind
+};
+
+constexpr uint32_t kOpen = 0x00800000u;                   // the key of the lowest finite value
+template <int V> constexpr uint32_t kPlace = V - 1;       // a key's bits for the place in its lane, the last one 0
+template <int V> constexpr float kRelative = V * 0x1p-23f + 0x1p-22f;   // what the place's bits and a sum's rounding take
+// Keys of 16-bit logits are exact: they leave the place's bits clear.
+template <typename T, bool kScored> constexpr bool kExact = !kScored && sizeof(T) == 2;
+
+__device__ __forceinline__ uint32_t open_key(float v) {   // NaN apart
+    const uint32_t b = __float_as_uint(v);
+    return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+}
+template <int V>
+__device__ __forceinline__ int expert_of(const RouteShape& s, uint2 t) {
+    return (int)((t.y >> s.lane_bits) * s.per + (t.y & (s.lanes - 1)) * s.each + (kPlace<V> - (t.x & kPlace<V>)));
+}
+// Whether the values of two keys, the second one behind the first, are closer than they are known.
+template <int V>
+__device__ __forceinline__ bool near_keys(uint32_t a, uint32_t b, float error) {
+    const float p = from_key<float>(a & ~kPlace<V>), q = from_key<float>(b & ~kPlace<V>);
+    return p - q <= 2.f * error + kRelative<V> * (fabsf(p) + fabsf(q)) + V * 0x1p-148f;
+}
+
+// The rounds of a row with the logits z, up to `rounds`, and up to `most` while keys are near the one of the last choice;
+// among the groups of the mask `groups`, where it is not 0.
+template <typename T, int V, bool kScored>
+__device__ __forceinline__ Picked pick(const RouteShape& s, const Lane& l, int lane, const float (&z)[V], const float* __restrict__ bias,
+                                       RouteSpace<V>& space, int rounds, int most, unsigned groups = 0,
+                                       uint32_t* largest = nullptr) {
+    Picked p = {0, 0.f, 1.f, 0.f, false, false};
+    const bool whole = !s.sigmoid && (kScored || !s.renormalise);   // scores over all experts are wanted
+    float a[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) a[i] = z[i];
+    if (whole) {
+        float top = z[0];
+#pragma unroll
+        for (int i = 1; i < V; ++i) top = fmaxf(top, z[i]);
+        p.top = max_of_warp(top);
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const float e = z[i] == -INFINITY ? 0.f : s.renormalise ? exp2_quick((z[i] - p.top) * kLog2e) : expf(z[i] - p.top);
+            if (kScored) a[i] = e;
+            sum += e;
+        }
+        p.sum = sum_of_warp(sum);
+    }
+    if (kScored) {
+        // exp(x) is known to 2 ulps and x log2(e) to 2 |x| 2^-24: times the exponential, or a sigmoid's slope, below 1.1 ulps
+        // of 1 more.  A sigmoid's sum and quotient add 1.5 ulps of it; a sum of exponentials, up to 2^-19 of it off, is that
+        // of all scores.
+        const float inv = s.sigmoid ? 1.f : reciprocal_quick(fmaxf(p.sum, 1.f));   // 1 and more, but where all are closed
+        p.error = s.sigmoid ? 0x1p-21f : 0x1p-18f * inv;
+        float b[V];
+        if (bias) load_lane<float, V>(bias + l.first, l.count, s.wide_bias, 0.f, b);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            a[i] = s.sigmoid ? reciprocal_quick(1.f + exp2_quick(z[i] * -kLog2e)) : a[i] * inv;
+            if (bias) a[i] += b[i];
+        }
+    }
+    uint32_t key[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        p.odd = p.odd || a[i] != a[i];
+        if (kScored) a[i] = z[i] == -INFINITY ? -INFINITY : a[i];
+        key[i] = (open_key(kScored ? a[i] : a[i] + 0.f) & ~kPlace<V>) | (kPlace<V> - i);   // -0 is 0
+    }
+    sort_keys(key);
+    uint32_t head = key[0];
+    if (largest) *largest = head;
+    if (kScored && s.top_groups < s.groups) {
+        if (groups) {
+            if (!(groups >> l.group & 1)) head = 0;
+        } else {
+            uint32_t first = key[0] & ~kPlace<V>, second = V > 1 ? key[V > 1] & ~kPlace<V> : 0;
+            if (first < kOpen) first = 0;
+            if (second < kOpen) second = 0;
+            two_of_group(s, first, second);
+            bool close = false;
+            if (!group_kept<float>(s, l, first, second, p.error, kRelative<V>, close)) head = 0;
+            p.close = close;
+        }
+    }
+#pragma unroll
+    for (int i = 1; i < V; ++i) space.list[i][lane] = key[i];
+    space.list[V][lane] = 0;
+    const uint32_t* next = &space.list[1][lane];
+    uint32_t least = kOpen, before = 0;
+    for (; p.n < most; ++p.n) {
+        const uint32_t top_key = __reduce_max_sync(kAll, head & ~kPlace<V>);
+        if (top_key < least) break;
+        if (p.n >= rounds && !near_keys<V>(before, top_key, p.error)) break;
+        if (p.n == s.k - 1) before = top_key;
+        const unsigned of = __ballot_sync(kAll, (head & ~kPlace<V>) == top_key);
+        if (lane == __ffs(of) - 1) {   // the lowest lane notes its key and moves on
+            space.taken[p.n] = make_uint2(head, lane);
+            head = *next;
+            next += 32;
+        }
+    }
+    return p;
+}
+
+// The groups of a row whose choice 32 bits do not tell, as a mask: the elements of each that may be among its two
+// largest, in 64 bits, a lane each; then a lane for each group.  0 where they are too many.  `keys` are a lane's sorted
+// ones, which pick left in `space` (the first one is given).
+template <typename T, int V>
+__device__ __forceinline__ unsigned groups_in_64_bits(const RouteShape& s, const Lane& l, int lane, const T* __restrict__ row,
+                                                      const float* __restrict__ bias, RouteSpace<V>& space, uint32_t head, float error) {
+    uint32_t first = head & ~kPlace<V>, second = V > 1 ? space.list[1][lane] & ~kPlace<V> : 0;
+    if (first < kOpen) first = 0;
+    if (second < kOpen) second = 0;
+    two_of_group(s, first, second);
+    const uint32_t of = s.group_top == 2 ? second : first;   // what a group's candidates are near to, or above
+    int n = 0;
+    for (int i = 0; i < V; ++i) {
+        const uint32_t key = i == 0 ? head : space.list[i][lane];
+        const bool in = l.group < s.groups && key >= kOpen && ((key & ~kPlace<V>) >= of || near_keys<V>(of, key, error));
+        const unsigned all = __ballot_sync(kAll, in);
+        const int at = n + __popc(all & ((1u << lane) - 1));
+        if (in && at < 32) space.taken[at] = make_uint2(key, lane);
+        n += __popc(all);
+    }
+    __syncwarp();
+    if (n > 32) return 0;
+    const int e = lane < n ? expert_of<V>(s, space.taken[lane]) : 0, group = e / s.per;
+    // a softmax's sums sort like those of its exponentials
+    double a = 0.0, top = 0.0;
+    if (lane < n) a = logit(row, e);
+    if (!s.sigmoid) {
+        top = lane < n ? a : -INFINITY;
+        for (int o = 16; o > 0; o >>= 1) top = fmax(top, __shfl_xor_sync(kAll, top, o));
+    }
+    if (lane < n) a = score_in_64_bits<true>(s, a, top, 1.0, bias, e);
+    double one = -INFINITY, two = -INFINITY;   // the two largest of group `lane`
+    for (int j = 0; j < n; ++j) {
+        const double other = __shfl_sync(kAll, a, j);
+        if (__shfl_sync(kAll, group, j) != lane) continue;
+        two = other > one ? one : fmax(two, other);
+        one = fmax(one, other);
+    }
+    const double value = s.group_top == 2 && two != -INFINITY ? one + two : one;
+    int ahead = 0;
+    for (int g = 0; g < s.groups; ++g) {
+        const double other = __shfl_sync(kAll, value, g);
+        ahead += other > value || (other == value && g < lane);
+    }
+    __syncwarp();
+    return __ballot_sync(kAll, lane < s.groups && ahead < s.top_groups);
+}
+
+// A row whose choice 32 bits do not tell: all that may be among its k largest, in 64 bits, a lane each, put in order by
+// how many are ahead.  Where that is not enough (NaN, a softmax with a bias, too many) the whole row in 64 bits.
+template <typename T, int V, bool kScored>
+__device__ __noinline__ int choose_again(const RouteShape& s, int lane, const T* __restrict__ row, const float* __restrict__ bias,
+                                         RouteSpace<V>& space) {
+    const Lane l(s, lane);
+    bool far = kScored && !s.sigmoid && bias;
+    unsigned groups = 0;
+    uint2* taken = space.taken;
+    for (int again = 0; !far && again < 2; ++again) {
+        float z[V];
+        load_lane<T, V>(row + l.first, l.count, s.wide, -INFINITY, z);
+        __syncwarp();
+        uint32_t head;
+        const Picked p = pick<T, V, kScored>(s, l, lane, z, bias, space, s.k, kRouteMaxK + 1, groups, &head);
+        __syncwarp();
+        far = __any_sync(kAll, p.odd);
+        if (far) break;
+        if (kScored && p.close) {
+            groups = groups_in_64_bits<T, V>(s, l, lane, row, bias, space, head, p.error);
+            far = groups == 0;
+            continue;
+        }
+        far = p.n > kRouteMaxK;
+        if (far) break;
+        const int e = lane < p.n ? expert_of<V>(s, taken[lane]) : 0;
+        double a = 0.0;
+        if (lane < p.n) {   // a softmax's scores sort like its logits
+            a = logit(row, e);
+            if (kScored && s.sigmoid) a = score_in_64_bits<kScored>(s, a, 0.0, 0.0, bias, e);
+        }
+        int ahead = 0;
+        for (int j = 0; j < p.n; ++j) {
+            const double other = __shfl_sync(kAll, a, j);
+            const int f = __shfl_sync(kAll, e, j);
+            ahead += other > a || (other == a && f < e);
+        }
+        __syncwarp();
+        if (lane < p.n) taken[ahead].x = e;
+        __syncwarp();
+        const int mine = lane < imin(p.n, s.k) ? (int)taken[lane].x : -1;
+        __syncwarp();
+        return mine;
+    }
+    return choose_in_64_bits<T, V, kScored>(s, lane, row, bias);
+}
 
 template <typename T, int V, bool kScored>
-__global__ void __launch_bounds__(kRouteWarps * 32) route_rows(RouteShape s, const T* __restrict__ logits, const float* __restrict__ bias,
-                                                               int32_t* __restrict__ ids, float* __restrict__ weights) {
+__global__ void __launch_bounds__(kRouteWarps * 32, V <= 8 ? 12 : V <= 16 ? 8 : 4) route_rows(
+    RouteShape s, const T* __restrict__ logits, const float* __restrict__ bias, int32_t* __restrict__ ids, float* __restrict__ weights) {
+    __shared__ RouteSpace<V> spaces[kRouteWarps];
     const int lane = threadIdx.x & 31;
+    RouteSpace<V>& space = spaces[threadIdx.x >> 5];
     const int64_t r0 = (int64_t)blockIdx.x * kRouteWarps + (threadIdx.x >> 5);
     pdl_wait();
     pdl_trigger();
@@ -223,102 +503,77 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_rows(RouteShape s, con
     const T* row = logits + r0 * s.ld;
     const Lane l(s, lane);
     float z[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) z[i] = i < l.count ? logit(row, l.first + i) : -INFINITY;
-    float top = 0.f, sum = 1.f;
-    const bool whole = !s.sigmoid && (kScored || !s.renormalise);   // scores over all experts are wanted
-    if (whole) {
-        top = z[0];
-#pragma unroll
-        for (int i = 1; i < V; ++i) top = fmaxf(top, z[i]);
-        top = max_of_warp(top);
-    }
-    float e[V];
-    if (whole) {
-        sum = 0.f;
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            e[i] = z[i] == -INFINITY ? 0.f : expf(z[i] - top);
-            sum += e[i];
+    load_lane<T, V>(row + l.first, l.count, s.wide, -INFINITY, z);
+    const int rounds = kExact<T, kScored> ? s.k : s.k + 1;
+    const Picked p = pick<T, V, kScored>(s, l, lane, z, bias, space, rounds, rounds);
+    __syncwarp();
+    int id = -1;
+    bool again = p.odd || p.close;
+    if (lane < imin(p.n, s.k)) {
+        const uint2 t = space.taken[lane];
+        id = expert_of<V>(s, t);
+        if (!kExact<T, kScored> && lane + 1 < p.n) {
+            const uint2 u = space.taken[lane + 1];
+            if (near_keys<V>(t.x, u.x, p.error)) {
+                const int e = expert_of<V>(s, u);   // two of one logit and bias are in their order
+                again = again || !(logit(row, id) == logit(row, e) && (!bias || __ldg(bias + id) == __ldg(bias + e)));
+            }
         }
-        sum = sum_of_warp(sum);
     }
-    uint32_t key[V];
-    float error = 0.f;   // of a score, beside its rounding
-    bool close = false;
-    if (kScored) {
-        const float inv = 1.f / sum;
-        // sigmoids: an exponential, a sum and a quotient; softmax: the difference to the largest logit is known to
-        // 2^-24 of itself, and an exponential above zero has no difference beyond 104
-        error = s.sigmoid ? 0x1p-20f : 0x1p-17f * inv;
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const float score = s.sigmoid ? sigmoid_of(z[i]) : e[i] * inv;
-            key[i] = z[i] == -INFINITY ? 0 : to_key(score + (bias && i < l.count ? __ldg(bias + l.first + i) : 0.f));
-        }
-        if (s.top_groups < s.groups) close = keep_groups<float, V>(s, l, key, error);
-    } else {
-#pragma unroll
-        for (int i = 0; i < V; ++i) key[i] = to_key(z[i]);
-    }
-    int mine = -1, before = -1;
-    float last = 0.f;
-    for (int r = 0; r < (kScored ? s.k + 1 : s.k); ++r) {
-        int at = -1;
-        const uint32_t best = take<float, V>(l, lane, key, at);
-        if (best == 0) break;
-        if (kScored) {
-            const float a = from_key<float>(best);
-            if (r > 0 && last - a <= 2.f * error + 0x1p-22f * (fabsf(last) + fabsf(a)) &&
-                !(logit(row, before) == logit(row, at) && (!bias || __ldg(bias + before) == __ldg(bias + at))))
-                close = true;
-            last = a;
-            before = at;
-        }
-        if (lane == r && r < s.k) mine = at;
-    }
-    if (kScored && close) mine = choose_in_64_bits<T, V>(s, lane, row, bias);
-    const bool held = mine >= 0;
-    const float zc = held ? logit(row, mine) : -INFINITY;
+    if (__any_sync(kAll, again)) id = choose_again<T, V, kScored>(s, lane, row, bias, space);
+    const bool held = id >= 0;
+    const float zc = held ? logit(row, id) : -INFINITY;
     float w;
-    if (s.renormalise) w = renormalised(s.sigmoid, held, zc);
-    else w = !held ? 0.f : s.sigmoid ? sigmoid_of(zc) : expf(zc - top) / sum;
+    if (s.renormalise) w = renormalised(s.sigmoid, held, zc, s.width);
+    else w = !held ? 0.f : s.sigmoid ? sigmoid_of(zc) : __fdividef(expf(zc - p.top), p.sum);
     if (lane < s.k) {
-        ids[r0 * s.k + lane] = mine;
-        weights[r0 * s.k + lane] = held ? w * s.scale : 0.f;
+        const int64_t at = r0 * s.k + lane;
+        ids[at] = id;
+        weights[at] = held ? w * s.scale : 0.f;
     }
 }
 
-template <typename T>
+// Gradients by expert gather in shared memory; a lane writes V neighbours of the row.  kWhole: softmax over all experts,
+// whose every logit has a gradient.
+template <typename T, int V, bool kWhole>
 __global__ void __launch_bounds__(kRouteWarps * 32) route_rows_backward(RouteShape s, const float* __restrict__ dweights,
                                                                         const T* __restrict__ logits, const int32_t* __restrict__ ids,
                                                                         T* __restrict__ dlogits) {
-    extern __shared__ float buffers[];
+    __shared__ __align__(16) float buffers[kRouteWarps][32 * V];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t r0 = (int64_t)blockIdx.x * kRouteWarps + warp;
-    float* g = buffers + warp * s.E;   // gradients by expert
+    float* g = buffers[warp];
     pdl_wait();
     pdl_trigger();
     if (r0 >= s.M) return;
     const T* row = logits + r0 * s.ld;
-    for (int i = lane; i < s.E; i += 32) g[i] = 0.f;
+    const int first = lane * V, count = imax(imin(s.E - first, V), 0);
+    float e[V];
+    if (kWhole) load_lane<T, V>(row + first, count, s.wide, -INFINITY, e);
+#pragma unroll
+    for (int i = 0; i < V; ++i) g[i * 32 + lane] = 0.f;
     const int id = lane < s.k ? __ldg(ids + r0 * s.k + lane) : -1;
     const bool held = (uint32_t)id < (uint32_t)s.E;
     const float z = held ? logit(row, id) : -INFINITY;
     const float d = held ? __ldg(dweights + r0 * s.k + lane) * s.scale : 0.f;
-    const bool whole = !s.sigmoid && !s.renormalise;
-    float top = -INFINITY, sum = 0.f, mean = 0.f, own = d;
-    if (whole) {
-        for (int i = lane; i < s.E; i += 32) top = fmaxf(top, logit(row, i));
+    float mean = 0.f, own = d;
+    if (kWhole) {
+        float top = e[0], sum = 0.f;
+#pragma unroll
+        for (int i = 1; i < V; ++i) top = fmaxf(top, e[i]);
         top = max_of_warp(top);
-        for (int i = lane; i < s.E; i += 32) {
-            const float v = logit(row, i);
-            sum += v == -INFINITY ? 0.f : expf(v - top);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            e[i] = e[i] == -INFINITY ? 0.f : expf(e[i] - top);
+            sum += e[i];
         }
         sum = sum_of_warp(sum);
-        mean = sum_of_warp(held ? d * (expf(z - top) / sum) : 0.f);
+        const float inv = 1.f / sum;   // no open expert: 0 times infinity is never asked for
+        mean = sum_of_warp(held && z != -INFINITY ? d * (expf(z - top) * inv) : 0.f);
+#pragma unroll
+        for (int i = 0; i < V; ++i) e[i] = e[i] == 0.f ? 0.f : e[i] * inv;
     } else if (s.renormalise) {
-        const float share = renormalised(s.sigmoid, held, z);
+        const float share = renormalised(s.sigmoid, held, z, s.width);
         const float all = sum_of_warp(held ? share * d : 0.f);
         own = share * (d - all);
         if (s.sigmoid) own *= sigmoid_of(-z);
@@ -326,32 +581,85 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_rows_backward(RouteSha
         own = d * sigmoid_of(z) * sigmoid_of(-z);
     }
     __syncwarp();
-    for (int j = 0; j < s.k; ++j) {   // one after another: an expert may be named twice
-        if (lane == j && held) g[id] += own;
-        __syncwarp();
-    }
-    T* out = dlogits + r0 * s.E;
-    for (int i = lane; i < s.E; i += 32) {
-        float v = g[i];
-        if (whole) {
-            const float zi = logit(row, i);
-            v = zi == -INFINITY ? 0.f : expf(zi - top) / sum * (v - mean);
+    // an expert that is named twice: its lanes find another one's number there, and add one after another
+    if (held) g[id] = __int_as_float(lane);
+    __syncwarp();
+    const bool twice = __any_sync(kAll, held && __float_as_int(g[id]) != lane);
+    __syncwarp();
+    if (held) g[id] = twice ? 0.f : own;
+    __syncwarp();
+    if (twice)
+        for (int j = 0; j < s.k; ++j) {
+            if (lane == j && held) g[id] += own;
+            __syncwarp();
         }
-        out[i] = from_f32<T>(v);
+    T* out = dlogits + r0 * s.E + first;
+    float v[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        v[i] = g[first + i];
+        if (kWhole) v[i] = e[i] == 0.f ? 0.f : e[i] * (v[i] - mean);
     }
+    constexpr int N = kVec<T>;
+    if constexpr (V % N == 0) {
+        if (s.wide) {
+            if (count > 0)
+#pragma unroll
+                for (int q = 0; q < V / N; ++q) {
+                    float f[N];
+#pragma unroll
+                    for (int i = 0; i < N; ++i) f[i] = v[q * N + i];
+                    st_piece(out + q * N, pack<T>(f));
+                }
+            return;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+        if (i < count) out[i] = from_f32<T>(v[i]);
+}
+
+// The least power of two of experts in a lane that holds `each`.
+inline int lane_size(int each) {
+    int v = 1;
+    while (v < each) v *= 2;
+    return v;
+}
+// Whether lanes that hold V experts (each, or none: `first` experts of a lane are multiples of V) read whole 16-byte pieces.
+inline bool wide_lanes(const void* p, int64_t ld, int bytes, int V, int per, int each) {
+    return each == V && per % V == 0 && V * bytes % 16 == 0 && aligned16(p) && ld * bytes % 16 == 0;
 }
 
 template <typename T, bool kScored>
 zs_status route_launch(const RouteShape& s, const void* logits, const float* bias, int32_t* ids, float* weights, cudaStream_t stream) {
     const dim3 grid((unsigned)((s.M + kRouteWarps - 1) / kRouteWarps)), block(kRouteWarps * 32);
     const T* z = static_cast<const T*>(logits);
-    if (s.each <= 1) launch(route_rows<T, 1, kScored>, grid, block, 0, stream, s, z, bias, ids, weights);
-    else if (s.each <= 2) launch(route_rows<T, 2, kScored>, grid, block, 0, stream, s, z, bias, ids, weights);
-    else if (s.each <= 4) launch(route_rows<T, 4, kScored>, grid, block, 0, stream, s, z, bias, ids, weights);
-    else if (s.each <= 8) launch(route_rows<T, 8, kScored>, grid, block, 0, stream, s, z, bias, ids, weights);
-    else if (s.each <= 16) launch(route_rows<T, 16, kScored>, grid, block, 0, stream, s, z, bias, ids, weights);
-    else launch(route_rows<T, 32, kScored>, grid, block, 0, stream, s, z, bias, ids, weights);
+    switch (lane_size(s.each)) {
+        case 1: launch(route_rows<T, 1, kScored>, grid, block, 0, stream, s, z, bias, ids, weights); break;
+        case 2: launch(route_rows<T, 2, kScored>, grid, block, 0, stream, s, z, bias, ids, weights); break;
+        case 4: launch(route_rows<T, 4, kScored>, grid, block, 0, stream, s, z, bias, ids, weights); break;
+        case 8: launch(route_rows<T, 8, kScored>, grid, block, 0, stream, s, z, bias, ids, weights); break;
+        case 16: launch(route_rows<T, 16, kScored>, grid, block, 0, stream, s, z, bias, ids, weights); break;
+        default: launch(route_rows<T, 32, kScored>, grid, block, 0, stream, s, z, bias, ids, weights); break;
+    }
     return check_launch("route");
+}
+
+template <typename T, bool kWhole>
+zs_status route_backward_launch(const RouteShape& s, const float* dweights, const void* logits, const int32_t* ids, void* dlogits,
+                                cudaStream_t stream) {
+    const dim3 grid((unsigned)((s.M + kRouteWarps - 1) / kRouteWarps)), block(kRouteWarps * 32);
+    const T* z = static_cast<const T*>(logits);
+    T* dz = static_cast<T*>(dlogits);
+    switch (lane_size(s.each)) {
+        case 1: launch(route_rows_backward<T, 1, kWhole>, grid, block, 0, stream, s, dweights, z, ids, dz); break;
+        case 2: launch(route_rows_backward<T, 2, kWhole>, grid, block, 0, stream, s, dweights, z, ids, dz); break;
+        case 4: launch(route_rows_backward<T, 4, kWhole>, grid, block, 0, stream, s, dweights, z, ids, dz); break;
+        case 8: launch(route_rows_backward<T, 8, kWhole>, grid, block, 0, stream, s, dweights, z, ids, dz); break;
+        case 16: launch(route_rows_backward<T, 16, kWhole>, grid, block, 0, stream, s, dweights, z, ids, dz); break;
+        default: launch(route_rows_backward<T, 32, kWhole>, grid, block, 0, stream, s, dweights, z, ids, dz); break;
+    }
+    return check_launch("route gradient");
 }
 
 zs_status check(const char* fn, int32_t dtype, int32_t score, const void* logits, int64_t ld, int64_t M, int32_t E, int32_t k, float scale,
@@ -369,6 +677,8 @@ zs_status check(const char* fn, int32_t dtype, int32_t score, const void* logits
         return fail(ZS_ERR_INVALID_ARG, "%s: logits is not aligned to its elements", fn);
     if (M > 1 && ld < E) return fail(ZS_ERR_INVALID_ARG, "%s: a row stride of logits, %lld, is below E=%d", fn, (long long)ld, E);
     s.M = M, s.ld = ld, s.E = E, s.k = k, s.scale = scale;
+    s.width = 1;
+    while (s.width < k) s.width *= 2;
     s.sigmoid = score == ZS_SCORE_SIGMOID;
     return ZS_OK;
 }
@@ -403,11 +713,15 @@ zs_status zs_route(int32_t dtype, int32_t score, const void* logits, int64_t log
     int slots = 1;
     while (slots < s.groups) slots *= 2;
     s.lanes = 32 / slots;
+    while ((1 << s.lane_bits) < s.lanes) ++s.lane_bits;
     s.each = (s.per + s.lanes - 1) / s.lanes;
     if (s.each > kRouteMaxE / 32)
         return fail(ZS_ERR_UNSUPPORTED, "%s: %d groups of %d experts do not fit 32 lanes of %d", fn, s.groups, s.per, kRouteMaxE / 32);
     if (M == 0) return ZS_OK;
     const bool scored = bias || s.groups > 1;
+    const int V = lane_size(s.each);
+    s.wide = wide_lanes(logits, M > 1 ? logits_ld : E, dtype_bytes(dtype), V, s.per, s.each);
+    s.wide_bias = wide_lanes(bias, 0, 4, V, s.per, s.each);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     auto go = [&](auto t) {
         using T = decltype(t);
@@ -429,17 +743,17 @@ zs_status zs_route_backward(int32_t dtype, int32_t score, const float* dweights,
         return fail(ZS_ERR_INVALID_ARG, "%s: dweights, ids or dlogits is not aligned to its elements", fn);
     if (M == 0) return ZS_OK;
     s.renormalise = renormalise != 0;
-    const dim3 grid((unsigned)((M + kRouteWarps - 1) / kRouteWarps)), block(kRouteWarps * 32);
-    const size_t smem = (size_t)kRouteWarps * E * sizeof(float);
+    s.each = lane_size((E + 31) / 32);
+    s.wide = wide_lanes(logits, M > 1 ? logits_ld : E, dtype_bytes(dtype), s.each, E, s.each) &&
+             wide_lanes(dlogits, E, dtype_bytes(dtype), s.each, E, s.each);
+    const bool whole = !s.sigmoid && !s.renormalise;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     auto go = [&](auto t) {
         using T = decltype(t);
-        launch(route_rows_backward<T>, grid, block, smem, st, s, dweights, static_cast<const T*>(logits), ids, static_cast<T*>(dlogits));
+        return whole ? route_backward_launch<T, true>(s, dweights, logits, ids, dlogits, st)
+                     : route_backward_launch<T, false>(s, dweights, logits, ids, dlogits, st);
     };
-    if (dtype == ZS_F32) go(float());
-    else if (dtype == ZS_BF16) go(__nv_bfloat16());
-    else go(__half());
-    return check_launch("route gradient");
+    return dtype == ZS_F32 ? go(float()) : dtype == ZS_BF16 ? go(__nv_bfloat16()) : go(__half());
 }
 
 }  // extern "C"

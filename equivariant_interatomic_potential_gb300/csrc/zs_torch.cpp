@@ -27,6 +27,8 @@ decltype(&zs_grouped_matmul_dw) f_dw;
 decltype(&zs_norm_gate_residual) f_norm;
 decltype(&zs_norm_gate_residual_backward_workspace_bytes) f_norm_bytes;
 decltype(&zs_norm_gate_residual_backward) f_norm_backward;
+decltype(&zs_build_csr_workspace_bytes) f_csr_bytes;
+decltype(&zs_build_csr) f_csr;
 decltype(&zs_embedding) f_embedding;
 decltype(&zs_embedding_backward_workspace_bytes) f_embedding_bytes;
 decltype(&zs_embedding_backward) f_embedding_backward;
@@ -234,6 +236,29 @@ PyObject* pair(at::Tensor&& a, at::Tensor&& b) {
     return r;
 }
 
+// (dst, N) -> (row_ptr, perm, bad_dst_count)
+PyObject* csr(PyObject*, PyObject* const* args, Py_ssize_t n) {
+    return guarded([&]() -> PyObject* {
+        int64_t N;
+        if (n != 2 || !number(args[1], 0, INT32_MAX, N)) return not_here();
+        const at::Tensor* dst = plain(args[0]);
+        if (!dst || dst->dim() != 1 || !is_array(dst, at::kInt, dst->size(0))) return not_here();
+        const int64_t E = dst->size(0);
+        at::Tensor row_ptr = make({N + 1}, *dst, at::kInt), perm = make({E}, *dst, at::kInt), bad = make({1}, *dst, at::kInt), ws;
+        const size_t bytes = f_csr_bytes(E, (int32_t)N);
+        if (bytes) ws = make({(int64_t)bytes}, *dst, at::kByte);
+        const int st = f_csr(E ? ints(dst) : nullptr, E, (int32_t)N, ints(row_ptr), E ? ints(perm) : nullptr, ints(bad),
+                             bytes ? ws.mutable_data_ptr() : nullptr, bytes, stream());
+        if (st) return failed("zs_build_csr", st);
+        PyObject* r = PyTuple_New(3);
+        if (!r) return nullptr;
+        PyTuple_SET_ITEM(r, 0, THPVariable_Wrap(std::move(row_ptr)));
+        PyTuple_SET_ITEM(r, 1, THPVariable_Wrap(std::move(perm)));
+        PyTuple_SET_ITEM(r, 2, THPVariable_Wrap(std::move(bad)));
+        return r;
+    });
+}
+
 // (w, ids, scale) -> y
 PyObject* embedding(PyObject*, PyObject* const* args, Py_ssize_t n) {
     return guarded([&]() -> PyObject* {
@@ -407,6 +432,8 @@ PyObject* bind(PyObject*, PyObject* args) {
     f_norm = reinterpret_cast<decltype(f_norm)>(get("zs_norm_gate_residual"));
     f_norm_bytes = reinterpret_cast<decltype(f_norm_bytes)>(get("zs_norm_gate_residual_backward_workspace_bytes"));
     f_norm_backward = reinterpret_cast<decltype(f_norm_backward)>(get("zs_norm_gate_residual_backward"));
+    f_csr_bytes = reinterpret_cast<decltype(f_csr_bytes)>(get("zs_build_csr_workspace_bytes"));
+    f_csr = reinterpret_cast<decltype(f_csr)>(get("zs_build_csr"));
     f_embedding = reinterpret_cast<decltype(f_embedding)>(get("zs_embedding"));
     f_embedding_bytes = reinterpret_cast<decltype(f_embedding_bytes)>(get("zs_embedding_backward_workspace_bytes"));
     f_embedding_backward = reinterpret_cast<decltype(f_embedding_backward)>(get("zs_embedding_backward"));
@@ -430,6 +457,7 @@ PyMethodDef methods[] = {
     {"dw", fast<dw>(), METH_FASTCALL, nullptr},
     {"norm", fast<norm>(), METH_FASTCALL, nullptr},
     {"norm_backward", fast<norm_backward>(), METH_FASTCALL, nullptr},
+    {"csr", fast<csr>(), METH_FASTCALL, nullptr},
     {"embedding", fast<embedding>(), METH_FASTCALL, nullptr},
     {"embedding_backward", fast<embedding_backward>(), METH_FASTCALL, nullptr},
     {"route", fast<route>(), METH_FASTCALL, nullptr},

@@ -142,9 +142,9 @@ class _Fast:
     """zs_torch, the short way for ordinary operands; built if need be and loaded on first
     use.  Where that fails, every call is left to the binding."""
 
-    NAMES = ("matmul", "dw", "norm", "norm_backward", "embedding", "embedding_backward", "route", "route_backward", "dispatch",
+    NAMES = ("matmul", "dw", "norm", "norm_backward", "csr", "embedding", "embedding_backward", "route", "route_backward", "dispatch",
              "combine", "combine_backward", "dropout")
-    LIBRARY = ("zs_grouped", "zs_norm", "zs_embedding", "zs_route", "zs_dispatch", "zs_combine", "zs_dropout")
+    LIBRARY = ("zs_build_csr", "zs_grouped", "zs_norm", "zs_embedding", "zs_route", "zs_dispatch", "zs_combine", "zs_dropout")
 
     def __getattr__(self, name):
         if name not in self.NAMES:
@@ -302,6 +302,10 @@ def zs_build_csr(dst: torch.Tensor, N: int, row_ptr=None, perm=None, bad_dst_cou
     """Stable destination CSR.  Returns (row_ptr (N+1,), perm (E,), bad_dst_count (1,)) int32."""
     if stream is not None:
         return _on(stream, zs_build_csr, dst, N, row_ptr, perm, bad_dst_count, workspace)
+    if row_ptr is None and perm is None and bad_dst_count is None and workspace is None:
+        r = _fast.csr(dst, N)
+        if r is not NotImplemented:
+            return r
     E = dst.shape[0]
     dev = dst.device
     _need(dst, "dst", torch.int32, (E,))
