@@ -64,7 +64,8 @@ __device__ __forceinline__ unsigned lanemask_lt() {
     return m;
 }
 
-template <bool kFirst>
+// kByTile: the counts of a tile together, for csr_downsweep<.., kScan>.
+template <bool kFirst, int kItems, bool kByTile>
 __global__ void __launch_bounds__(kCsrThreads)
 csr_upsweep(const int32_t* __restrict__ keys_in, int64_t E, int32_t N, int shift,
             int32_t* __restrict__ hist, int T) {
@@ -76,18 +77,18 @@ csr_upsweep(const int32_t* __restrict__ keys_in, int64_t E, int32_t N, int shift
     __syncthreads();
     // counts do not depend on the order of the increments; the tile's keys
     // are all loaded before the first increment (one round trip, not eight)
-    const int64_t base = (int64_t)blockIdx.x * kTile;
-    int dig[kTile / kCsrThreads];
+    const int64_t base = (int64_t)blockIdx.x * (kItems * kCsrThreads);
+    int dig[kItems];
 #pragma unroll
-    for (int u = 0; u < kTile / kCsrThreads; ++u) {
+    for (int u = 0; u < kItems; ++u) {
         const int64_t idx = base + u * kCsrThreads + tid;
         dig[u] = idx < E ? (key_of(keys_in, idx, N, kFirst) >> shift) & (kRadix - 1) : -1;
     }
 #pragma unroll
-    for (int u = 0; u < kTile / kCsrThreads; ++u)
+    for (int u = 0; u < kItems; ++u)
         if (dig[u] >= 0) atomicAdd(&cnt[dig[u]], 1);
     __syncthreads();
-    hist[(int64_t)tid * T + blockIdx.x] = cnt[tid];
+    hist[kByTile ? (int64_t)blockIdx.x * kRadix + tid : (int64_t)tid * T + blockIdx.x] = cnt[tid];
 }
 
 // One CTA per row: exclusive scan of hist[d, 0..T) in place, total to tot[d].
@@ -141,7 +142,9 @@ csr_scan(int32_t* __restrict__ hist, int T, int32_t* __restrict__ tot) {
     if (tid == 0) tot[blockIdx.x] = carry;
 }
 
-template <bool kFirst>
+// kScan: hist holds the tiles' counts as csr_upsweep<.., kByTile> left them (few
+// tiles), which every CTA adds up itself.
+template <bool kFirst, int kItems, bool kScan>
 __global__ void __launch_bounds__(kCsrThreads)
 csr_downsweep(const int32_t* __restrict__ keys_in, const int32_t* __restrict__ vals_in,
               int64_t E, int32_t N, int shift,
@@ -150,17 +153,29 @@ csr_downsweep(const int32_t* __restrict__ keys_in, const int32_t* __restrict__ v
     __shared__ int cnt[kCsrWarps][kRadix];
     __shared__ int wsum[kCsrWarps];
     __shared__ int dbase[kRadix];
-    __shared__ int32_t skey[kTile], sval[kTile];
+    constexpr int kTileKeys = kItems * kCsrThreads;
+    __shared__ int32_t skey[kTileKeys], sval[kTileKeys];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     for (int i = tid; i < kCsrWarps * kRadix; i += kCsrThreads) (&cnt[0][0])[i] = 0;
     pdl_wait();
     pdl_trigger();
 
     // this tile's offset within each digit, loaded now beside the totals
-    const int hv = hist[(int64_t)tid * T + blockIdx.x];
+    int hv = 0, total = 0;
+    if (kScan) {
+#pragma unroll 16
+        for (int t = 0; t < T; ++t) {
+            const int c = hist[(int64_t)t * kRadix + tid];
+            hv += t < (int)blockIdx.x ? c : 0;
+            total += c;
+        }
+    } else {
+        hv = hist[(int64_t)tid * T + blockIdx.x];
+        total = tot[tid];
+    }
     // Exclusive scan of the 256 digit totals (kCsrThreads == kRadix).
     {
-        const int v = tot[tid];
+        const int v = total;
         int incl = v;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
@@ -175,14 +190,14 @@ csr_downsweep(const int32_t* __restrict__ keys_in, const int32_t* __restrict__ v
     }
     __syncthreads();
 
-    const int64_t base = (int64_t)blockIdx.x * kTile + (int64_t)warp * kCsrItems * 32;
-    int32_t key[kCsrItems], val[kCsrItems];
-    int rank[kCsrItems], dig[kCsrItems];
+    const int64_t base = (int64_t)blockIdx.x * kTileKeys + (int64_t)warp * kItems * 32;
+    int32_t key[kItems], val[kItems];
+    int rank[kItems], dig[kItems];
     const unsigned lt = lanemask_lt();
     // every item's key and value are loaded before the ranking starts (its
     // warp synchronisations would otherwise hold each load back to its round)
 #pragma unroll
-    for (int i = 0; i < kCsrItems; ++i) {
+    for (int i = 0; i < kItems; ++i) {
         const int64_t idx = base + i * 32 + lane;
         const bool valid = idx < E;
         key[i] = valid ? key_of(keys_in, idx, N, kFirst) : 0;
@@ -190,7 +205,7 @@ csr_downsweep(const int32_t* __restrict__ keys_in, const int32_t* __restrict__ v
         dig[i] = valid ? ((key[i] >> shift) & (kRadix - 1)) : kRadix;
     }
 #pragma unroll
-    for (int i = 0; i < kCsrItems; ++i) {
+    for (int i = 0; i < kItems; ++i) {
         const bool valid = dig[i] < kRadix;
         const unsigned peers = digit_peers(dig[i] & (kRadix - 1), valid);
         rank[i] = valid ? cnt[warp][dig[i]] + __popc(peers & lt) : 0;
@@ -230,7 +245,7 @@ csr_downsweep(const int32_t* __restrict__ keys_in, const int32_t* __restrict__ v
     __syncthreads();
     // stage the tile in digit order, then write each digit's run contiguously
 #pragma unroll
-    for (int i = 0; i < kCsrItems; ++i) {
+    for (int i = 0; i < kItems; ++i) {
         if (dig[i] < kRadix) {
             const int slot = cnt[warp][dig[i]] + rank[i];
             skey[slot] = key[i];
@@ -238,7 +253,7 @@ csr_downsweep(const int32_t* __restrict__ keys_in, const int32_t* __restrict__ v
         }
     }
     __syncthreads();
-    const int n_in_tile = (int)imin<int64_t>(kTile, E - (int64_t)blockIdx.x * kTile);
+    const int n_in_tile = (int)imin<int64_t>(kTileKeys, E - (int64_t)blockIdx.x * kTileKeys);
     for (int slot = tid; slot < n_in_tile; slot += kCsrThreads) {
         const int32_t k = skey[slot];
         const int pos = dbase[(k >> shift) & (kRadix - 1)] + slot;
@@ -249,19 +264,18 @@ csr_downsweep(const int32_t* __restrict__ keys_in, const int32_t* __restrict__ v
 
 // row_ptr from sorted keys: position j is the first of every node in
 // (key[j-1], key[j]]; the count of keys equal to N (invalid) is E - row_ptr[N].
-// Each thread looks at kRowPtrPer consecutive positions.
-constexpr int kRowPtrPer = 4;
-
+// Each thread looks at kPer consecutive positions.
+template <int kPer>
 __global__ void __launch_bounds__(256)
 csr_row_ptr(const int32_t* __restrict__ sorted, int64_t E, int32_t N,
             int32_t* __restrict__ row_ptr, int32_t* __restrict__ bad) {
-    const int64_t j0 = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) * kRowPtrPer;
+    const int64_t j0 = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) * kPer;
     pdl_wait();
     pdl_trigger();
     if (j0 > E) return;
     int64_t kprev = j0 > 0 ? (int64_t)__ldg(sorted + j0 - 1) : -1;
 #pragma unroll
-    for (int i = 0; i < kRowPtrPer; ++i) {
+    for (int i = 0; i < kPer; ++i) {
         const int64_t j = j0 + i;
         if (j > E) break;
         const int64_t kcur = j < E ? (int64_t)__ldg(sorted + j) : (int64_t)N + 1;
@@ -631,6 +645,20 @@ csr_count_single(const int32_t* __restrict__ dst, int64_t E, int32_t N, int roun
     }
 }
 
+// Both passes over at most kFewTiles tiles of 256 * kItems keys: dst by its low digit to (k0, v0), these by their high
+// one to (k1, perm).
+constexpr int kFewTiles = 64;
+template <int kItems>
+void sort_twice(const int32_t* dst, int64_t E, int32_t N, int32_t* k0, int32_t* v0, int32_t* k1, int32_t* perm, int32_t* hist,
+                cudaStream_t s) {
+    const int T = (int)((E + kItems * kCsrThreads - 1) / (kItems * kCsrThreads));
+    const int32_t *none = nullptr, *counts = hist, *kin = k0, *vin = v0;
+    launch(csr_upsweep<true, kItems, true>, T, kCsrThreads, 0, s, dst, E, N, 0, hist, T);
+    launch(csr_downsweep<true, kItems, true>, T, kCsrThreads, 0, s, dst, none, E, N, 0, counts, none, T, k0, v0);
+    launch(csr_upsweep<false, kItems, true>, T, kCsrThreads, 0, s, kin, E, N, 8, hist, T);
+    launch(csr_downsweep<false, kItems, true>, T, kCsrThreads, 0, s, kin, vin, E, N, 8, counts, none, T, k1, perm);
+}
+
 struct CsrPlan {
     bool counting = false;
     int T = 0;
@@ -724,24 +752,37 @@ extern "C" zs_status zs_build_csr(const int32_t* dst, int64_t E, int32_t N,
     if (E > 0) {
         int32_t* hist = reinterpret_cast<int32_t*>(ws + p.off_hist);
         int32_t* tot = reinterpret_cast<int32_t*>(ws + p.off_tot);
+        int32_t *k0 = reinterpret_cast<int32_t*>(ws + p.off_k[0]), *v0 = reinterpret_cast<int32_t*>(ws + p.off_v[0]);
+        int32_t *k1 = reinterpret_cast<int32_t*>(ws + p.off_k[1]), *v1 = reinterpret_cast<int32_t*>(ws + p.off_v[1]);
+        if (p.passes == 2 && E <= (int64_t)kFewTiles * kTile) {
+            // Two passes over few keys: tiles so small that most SMs have one, and no kernel that scans their counts.  Those
+            // lie where a third pass would put its values, and behind: 4 bytes a key, up to the next 1024.
+            if (E <= kFewTiles * 256) sort_twice<1>(dst, E, N, k0, v0, k1, perm, v1, s);
+            else if (E <= kFewTiles * 512) sort_twice<2>(dst, E, N, k0, v0, k1, perm, v1, s);
+            else if (E <= kFewTiles * 1024) sort_twice<4>(dst, E, N, k0, v0, k1, perm, v1, s);
+            else sort_twice<8>(dst, E, N, k0, v0, k1, perm, v1, s);
+            launch(csr_row_ptr<1>, (unsigned)((E + 1 + 255) / 256), 256, 0, s, (const int32_t*)k1, E, N, row_ptr, bad_dst_count);
+            return check_launch("zs_build_csr");
+        }
         const int32_t* kin = dst;
         const int32_t* vin = nullptr;
         for (int pass = 0; pass < p.passes; ++pass) {
             const bool first = pass == 0, last = pass == p.passes - 1;
             const int shift = 8 * pass;
-            int32_t* kout = reinterpret_cast<int32_t*>(ws + p.off_k[pass & 1]);
-            int32_t* vout = last ? perm : reinterpret_cast<int32_t*>(ws + p.off_v[pass & 1]);
-            if (first) launch(csr_upsweep<true>, p.T, kCsrThreads, 0, s, kin, E, N, shift, hist, p.T);
-            else launch(csr_upsweep<false>, p.T, kCsrThreads, 0, s, kin, E, N, shift, hist, p.T);
+            int32_t* kout = pass & 1 ? k1 : k0;
+            int32_t* vout = last ? perm : pass & 1 ? v1 : v0;
+            if (first) launch(csr_upsweep<true, kCsrItems, false>, p.T, kCsrThreads, 0, s, kin, E, N, shift, hist, p.T);
+            else launch(csr_upsweep<false, kCsrItems, false>, p.T, kCsrThreads, 0, s, kin, E, N, shift, hist, p.T);
             launch(csr_scan, kRadix, kCsrThreads, 0, s, hist, p.T, tot);
-            if (first) launch(csr_downsweep<true>, p.T, kCsrThreads, 0, s, kin, vin, E, N, shift, (const int32_t*)hist, (const int32_t*)tot, p.T, kout, vout);
-            else launch(csr_downsweep<false>, p.T, kCsrThreads, 0, s, kin, vin, E, N, shift, (const int32_t*)hist, (const int32_t*)tot, p.T, kout, vout);
+            if (first) launch(csr_downsweep<true, kCsrItems, false>, p.T, kCsrThreads, 0, s, kin, vin, E, N, shift, (const int32_t*)hist, (const int32_t*)tot, p.T, kout, vout);
+            else launch(csr_downsweep<false, kCsrItems, false>, p.T, kCsrThreads, 0, s, kin, vin, E, N, shift, (const int32_t*)hist, (const int32_t*)tot, p.T, kout, vout);
             kin = kout;
             vin = vout;
         }
         sorted = kin;
     }
-    const int64_t threads = (E + 1 + kRowPtrPer - 1) / kRowPtrPer;
-    launch(csr_row_ptr, (unsigned)((threads + 255) / 256), 256, 0, s, sorted, E, N, row_ptr, bad_dst_count);
+    constexpr int kPer = 4;
+    const int64_t threads = (E + 1 + kPer - 1) / kPer;
+    launch(csr_row_ptr<kPer>, (unsigned)((threads + 255) / 256), 256, 0, s, sorted, E, N, row_ptr, bad_dst_count);
     return check_launch("zs_build_csr");
 }

@@ -16,28 +16,29 @@
 // its threads is added up in shared memory.  What is cut between CTAs goes to
 // the workspace in fp32 and is added up by a second kernel in the CTAs' order.
 // All sums are in fp32 and in an order that follows from the sizes.
+
 #include "zs_rows.cuh"
 
 namespace zs {
 namespace {
 
 struct IdSource {
-    static constexpr bool kScaled = true;
+    static constexpr bool kScaled = true, kAgain = true;   // rows are read again: they may stay in L1
     const int32_t* ids;
     int32_t V;
-    __device__ __forceinline__ int64_t row(int64_t i, bool) const {
+    __device__ __forceinline__ int32_t row(int32_t i, bool) const {
         const int32_t v = __ldg(ids + i);
         return (uint32_t)v < (uint32_t)V ? v : -1;
     }
 };
 
-template <typename T, int VEC>
+template <typename T, bool kWhole>
 zs_status embed_forward(const void* w, int64_t w_ld, int32_t V, const int32_t* ids, int64_t M, int32_t C, float scale, void* y,
                         int64_t y_ld, cudaStream_t s) {
-    constexpr int U = VEC == 1 ? 8 : 2;
-    const MoveShape shape = move_shape(M, C / VEC, U);
-    launch(move_rows<T, VEC, U, IdSource>, dim3(shape.ctas_x, shape.ctas_y), dim3(kMoveThreads), 0, s, shape, IdSource{ids, V},
-           static_cast<const T*>(w), w_ld, scale, static_cast<T*>(y), y_ld);
+    constexpr int U = 4;
+    const MoveShape shape = move_shape(M, Row<T, kWhole>::pieces(C), C, U);
+    launch(move_rows<T, kWhole, U, IdSource>, dim3(shape.ctas_x, shape.ctas_y), dim3(kMoveThreads), 0, s, shape, IdSource{ids, V},
+           Rows<T>(w, V, w_ld, C), scale, static_cast<T*>(y), y_ld);
     return check_launch("embedding");
 }
 
@@ -46,7 +47,7 @@ zs_status embed_forward(const void* w, int64_t w_ld, int32_t V, const int32_t* i
 constexpr int kSumThreads = 256;
 constexpr int kSumBatch = 8;         // rows of dy in flight for a thread
 constexpr int kSumItems = 4096;      // most items of a CTA (staged in shared memory)
-constexpr int kSumCtas = 6;          // CTAs an SM that the shares are made for
+constexpr int kSumCtas = 2;          // CTAs an SM that the shares are made for: as many as run at once
 
 struct SumShape {
     int64_t M, items;                // items: M + V
@@ -64,7 +65,7 @@ inline SumShape sum_shape(int64_t M, int32_t V, int32_t C, int vec) {
     s.V = V;
     s.C = C;
     s.items = M + V;
-    s.P = C / vec;
+    s.P = (C + vec - 1) / vec;
     s.cols = imin(s.P, kSumThreads);
     s.units = kSumThreads / s.cols;
     s.ctas_y = (s.P + s.cols - 1) / s.cols;
@@ -81,43 +82,49 @@ struct SumNote {
     int32_t row, first;
 };
 
-// Rows that end before item d of the merged list: how many v have row_ptr[v + 1] + v < d.  Whole warp.
-__device__ __forceinline__ int rows_before(const int32_t* row_ptr, int32_t V, int64_t d, int lane) {
-    int lo = 0, hi = V;
-    while (lo < hi) {
-        const int step = ((hi - lo) + 31) >> 5;
-        const int64_t at = (int64_t)lo + (int64_t)lane * step;
-        const bool ge = at >= hi || (int64_t)__ldg(row_ptr + at + 1) + at >= d;
+// Rows that end before item d of the merged list: how many v have row_ptr[v + 1] + v < d.  By `kSumThreads / 2` threads,
+// the two halves of the CTA with a d each: rounds of as many samples at even distances, two of them for 16000 rows.
+__device__ __forceinline__ int rows_before(const int32_t* row_ptr, int32_t V, int64_t d, int (*first)[kSumThreads / 64]) {
+    constexpr int N = kSumThreads / 2;
+    const int t = threadIdx.x % N, half = threadIdx.x / N, lane = threadIdx.x & 31;
+    int64_t lo = 0, hi = V;
+    while (__syncthreads_or(lo < hi)) {
+        const int64_t step = (hi - lo + N - 1) / N, at = lo + t * step;
+        const bool ge = lo < hi && (at >= hi || (int64_t)__ldg(row_ptr + at + 1) + at >= d);
         const unsigned m = __ballot_sync(0xffffffffu, ge);
-        if (m == 0) {
-            lo += 31 * step + 1;
-        } else {
-            const int f = __ffs(m) - 1;
-            hi = (int)imin<int64_t>((int64_t)lo + (int64_t)f * step, hi);
-            if (f > 0) lo += (f - 1) * step + 1;
-        }
+        if (lane == 0) first[half][t >> 5] = m ? (t & ~31) + __ffs(m) - 1 : N;   // the first sample that is not before d
+        __syncthreads();
+        if (lo >= hi) continue;
+        int f = N;
+#pragma unroll
+        for (int w = 0; w < N / 32; ++w) f = imin(f, first[half][w]);
+        hi = imin(lo + f * step, hi);
+        if (f > 0) lo += (f - 1) * step + 1;
+        if (lo > hi) lo = hi;
     }
-    return lo;
+    return (int)lo;
 }
 
-template <typename T, int VEC>
-__global__ void __launch_bounds__(kSumThreads) sum_rows(SumShape s, const T* __restrict__ dy, int64_t dy_ld,
+template <typename T, bool kWhole>
+__global__ void __launch_bounds__(kSumThreads, 2) sum_rows(SumShape s, Rows<T> dy,
                                                         const int32_t* __restrict__ row_ptr, const int32_t* __restrict__ perm,
                                                         float scale, T* __restrict__ dw, float* __restrict__ head,
                                                         float* __restrict__ tail, SumNote* __restrict__ notes) {
-    using R = Row<T, VEC>;
+    using R = Row<T, kWhole>;
+    constexpr int VEC = R::N;
     __shared__ int32_t staged[kSumItems + 8];        // row_ptr[v0 .. v1 + 1], then perm[j0 .. j1)
     __shared__ int32_t bound[2];
     __shared__ int32_t unit_row[kSumThreads + 1];    // rows that end before each unit
     __shared__ float open[kSumThreads * VEC];        // sums of rows that a unit leaves open
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    __shared__ int samples[2][kSumThreads / 64];
+    const int tid = threadIdx.x;
     const int64_t share = (int64_t)s.units * s.per_unit;
     const int64_t d0 = blockIdx.x * share, d1 = imin(d0 + share, s.items);
     pdl_wait();
     pdl_trigger();
-    if (warp < 2) {
-        const int v = rows_before(row_ptr, s.V, warp ? d1 : d0, lane);
-        if (lane == 0) bound[warp] = v;
+    {
+        const int v = rows_before(row_ptr, s.V, tid < kSumThreads / 2 ? d0 : d1, samples);
+        if (tid % (kSumThreads / 2) == 0) bound[tid / (kSumThreads / 2)] = v;
     }
     __syncthreads();
     const int v0 = bound[0], v1 = bound[1];
@@ -144,7 +151,7 @@ __global__ void __launch_bounds__(kSumThreads) sum_rows(SumShape s, const T* __r
     __syncthreads();
 
     const int unit = (int)s.by_cols.quotient((uint32_t)tid), col = tid - unit * s.cols;
-    const int64_t c = (int64_t)blockIdx.y * s.cols + col;
+    const int64_t c = (int64_t)blockIdx.y * s.cols + col, e = c * VEC;
     const bool live = unit < s.units && c < s.P;
     float acc[VEC] = {};
     bool cut = false;                 // the unit closes a row that others have begun
@@ -169,31 +176,37 @@ __global__ void __launch_bounds__(kSumThreads) sum_rows(SumShape s, const T* __r
                 float f[VEC];
 #pragma unroll
                 for (int i = 0; i < VEC; ++i) f[i] = acc[i] * scale;
-                R::store(dw + (int64_t)(v0 + r) * s.C, c, R::rounded(f));
+                R::template store<true>(dw + (int64_t)(v0 + r) * s.C, e, s.C, pack<T>(f));
             }
 #pragma unroll
             for (int i = 0; i < VEC; ++i) acc[i] = 0.f;
             ++r;
         };
-        for (; p < p_end; p += kSumBatch) {
-            typename R::Raw v[kSumBatch];
+        auto load = [&](uint4(&v)[kSumBatch], int p) {
 #pragma unroll
             for (int u = 0; u < kSumBatch; ++u) {
                 v[u] = R::zero();
                 if (p + u < p_end) {
                     const int32_t i = sperm[p + u];
-                    if ((uint64_t)(int64_t)i < (uint64_t)s.M) v[u] = R::load_once(dy + (int64_t)i * dy_ld, c);
+                    if ((uint64_t)(int64_t)i < (uint64_t)s.M) v[u] = R::template load<false>(dy, i, e, s.C);
                 }
             }
+        };
+        uint4 v[kSumBatch], next[kSumBatch];
+        load(v, p);
+        for (; p < p_end; p += kSumBatch) {
+            load(next, p + kSumBatch);
 #pragma unroll
             for (int u = 0; u < kSumBatch; ++u) {
                 if (p + u >= p_end) break;
                 while (r < r_end && j0 + p + u >= (int64_t)staged[r + 1]) close();
                 float f[VEC];
-                R::floats(v[u], f);
+                unpack<T>(v[u], f);
 #pragma unroll
                 for (int i = 0; i < VEC; ++i) acc[i] += f[i];
             }
+#pragma unroll
+            for (int u = 0; u < kSumBatch; ++u) v[u] = next[u];
         }
         while (r < r_end) close();
 #pragma unroll
@@ -212,7 +225,8 @@ __global__ void __launch_bounds__(kSumThreads) sum_rows(SumShape s, const T* __r
 #pragma unroll
             for (int i = 0; i < VEC; ++i) sum[i] += open[(q * s.cols + col) * VEC + i];
     };
-    const int64_t at = (int64_t)blockIdx.x * s.C + c * VEC;
+    const int64_t at = (int64_t)blockIdx.x * s.C + e;
+    const int width = kWhole ? VEC : (int)imin<int64_t>(VEC, s.C - e);   // of the piece
     if (cut) {
         float sum[VEC];
         earlier(begun_row, sum);
@@ -221,10 +235,11 @@ __global__ void __launch_bounds__(kSumThreads) sum_rows(SumShape s, const T* __r
         if ((int64_t)staged[begun_row] + v0 + begun_row >= d0) {   // begun in this CTA
 #pragma unroll
             for (int i = 0; i < VEC; ++i) sum[i] *= scale;
-            R::store(dw + (int64_t)(v0 + begun_row) * s.C, c, R::rounded(sum));
+            R::template store<true>(dw + (int64_t)(v0 + begun_row) * s.C, e, s.C, pack<T>(sum));
         } else {
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) head[at + i] = sum[i];
+            for (int i = 0; i < VEC; ++i)
+                if (i < width) head[at + i] = sum[i];
         }
     }
     if (unit == s.units - 1) {
@@ -235,8 +250,10 @@ __global__ void __launch_bounds__(kSumThreads) sum_rows(SumShape s, const T* __r
 #pragma unroll
             for (int i = 0; i < VEC; ++i) acc[i] += sum[i];
         }
+        if ((int64_t)staged[r] + v0 + r < d1)   // the row goes on in the next CTA
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) tail[at + i] = acc[i];
+            for (int i = 0; i < VEC; ++i)
+                if (i < width) tail[at + i] = acc[i];
     }
     if (tid == 0 && blockIdx.y == 0) {
         // the row that is open at the CTA's start, if it was begun before and ends here
@@ -246,42 +263,56 @@ __global__ void __launch_bounds__(kSumThreads) sum_rows(SumShape s, const T* __r
     }
 }
 
-// A CTA for each CTA that closes a row which others have begun: the parts in
-// their order, by slices of threads and the slices in theirs.
-template <typename T>
-__global__ void __launch_bounds__(kSumThreads) join_rows(int32_t C, int cols, float scale, const float* __restrict__ head,
+// For each CTA that closes a row which others have begun: the parts in their order, by slices of threads, the slices in
+// theirs.  W floats at a time where rows of C are whole vectors of them.
+constexpr int kJoinColumns = 256;
+template <typename T, int W>
+__global__ void __launch_bounds__(kSumThreads) join_rows(int32_t C, float scale, const float* __restrict__ head,
                                                          const float* __restrict__ tail, const SumNote* __restrict__ notes,
                                                          T* __restrict__ dw) {
-    __shared__ float part[kSumThreads];
+    using Vec = typename std::conditional<W == 4, float4, float>::type;
+    __shared__ Vec part[kSumThreads];
     pdl_wait();
     pdl_trigger();
     const SumNote note = notes[blockIdx.x];
     if (note.row < 0) return;
+    const int64_t c0 = (int64_t)blockIdx.y * kJoinColumns;
+    const int cols = (int)imin<int64_t>(kJoinColumns, C - c0) / W;       // vectors of this CTA
     const int slices = kSumThreads / cols, slice = threadIdx.x / cols, col = threadIdx.x - slice * cols;
     const int last = blockIdx.x, n = last - note.first;   // tails of the CTAs [first, last), then the head of the last
     const int each = (n + slices - 1) / slices;
-    for (int64_t c = (int64_t)blockIdx.y * cols + col; c - col < C; c += (int64_t)gridDim.y * cols) {
-        float sum = 0.f;
-        if (slice < slices && c < C) {
-            const int a = note.first + imin(slice * each, n), b = note.first + imin((slice + 1) * each, n);
-            int q = a;
-            for (; q + kSumBatch <= b; q += kSumBatch) {
-                float v[kSumBatch];
+    auto at = [&](const float* p, int64_t q) { return reinterpret_cast<const Vec*>(p + q * C + c0)[col]; };
+    auto add = [](Vec& a, Vec b) {
+        if constexpr (W == 4) a = f4_add(a, b);
+        else a += b;
+    };
+    Vec sum = {};
+    if (slice < slices) {
+        int q = note.first + imin(slice * each, n);
+        const int end = note.first + imin((slice + 1) * each, n);
+        for (; q + kSumBatch <= end; q += kSumBatch) {
+            Vec v[kSumBatch];
 #pragma unroll
-                for (int u = 0; u < kSumBatch; ++u) v[u] = tail[(int64_t)(q + u) * C + c];
+            for (int u = 0; u < kSumBatch; ++u) v[u] = at(tail, q + u);
 #pragma unroll
-                for (int u = 0; u < kSumBatch; ++u) sum += v[u];
-            }
-            for (; q < b; ++q) sum += tail[(int64_t)q * C + c];
+            for (int u = 0; u < kSumBatch; ++u) add(sum, v[u]);
         }
+        for (; q < end; ++q) add(sum, at(tail, q));
+    }
+    if (n > 1) {
         part[threadIdx.x] = sum;
         __syncthreads();
-        if (slice == 0 && c < C) {
-            for (int k = 1; k < slices; ++k) sum += part[k * cols + col];
-            sum += head[(int64_t)last * C + c];
-            dw[(int64_t)note.row * C + c] = from_f32<T>(sum * scale);
-        }
-        __syncthreads();
+    }
+    if (slice > 0) return;
+    for (int k = 1; k < imin(slices, n); ++k) add(sum, part[k * cols + col]);
+    add(sum, at(head, last));
+    T* out = dw + (int64_t)note.row * C + c0 + col * W;
+    if constexpr (W == 4) {
+        const float f[4] = {sum.x, sum.y, sum.z, sum.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) out[i] = from_f32<T>(f[i] * scale);
+    } else {
+        *out = from_f32<T>(sum * scale);
     }
 }
 
@@ -289,22 +320,22 @@ size_t sum_workspace(const SumShape& s) {
     return 2 * align_up((size_t)s.ctas * s.C * 4, 256) + align_up((size_t)s.ctas * sizeof(SumNote), 256);
 }
 
-template <typename T, int VEC>
+template <typename T, bool kWhole>
 zs_status embed_backward(const void* dy, int64_t dy_ld, const int32_t* row_ptr, const int32_t* perm, int64_t M, int32_t V, int32_t C,
                          float scale, void* dw, void* workspace, cudaStream_t stream) {
-    const SumShape s = sum_shape(M, V, C, VEC);
+    const SumShape s = sum_shape(M, V, C, kVec<T>);
     float* head = static_cast<float*>(workspace);
     const size_t each = align_up((size_t)s.ctas * C * 4, 256);
     float* tail = reinterpret_cast<float*>(static_cast<char*>(workspace) + each);
     SumNote* notes = reinterpret_cast<SumNote*>(static_cast<char*>(workspace) + 2 * each);
-    launch(sum_rows<T, VEC>, dim3(s.ctas, s.ctas_y), dim3(kSumThreads), 0, stream, s, static_cast<const T*>(dy), dy_ld, row_ptr, perm,
-           scale, static_cast<T*>(dw), head, tail, notes);
+    launch(sum_rows<T, kWhole>, dim3(s.ctas, s.ctas_y), dim3(kSumThreads), 0, stream, s, Rows<T>(dy, M, dy_ld, C), row_ptr, perm, scale,
+            static_cast<T*>(dw), head, tail, notes);
     if (zs_status st = check_launch("embedding gradient")) return st;
     if (s.ctas > 1) {
-        const int cols = imin(C, 32);
-        const int32_t ctas_y = (int32_t)imin<int64_t>(64, (C + cols - 1) / cols);
-        launch(join_rows<T>, dim3(s.ctas, ctas_y), dim3(kSumThreads), 0, stream, C, cols, scale, (const float*)head, (const float*)tail,
-               (const SumNote*)notes, static_cast<T*>(dw));
+        const dim3 grid(s.ctas, (C + kJoinColumns - 1) / kJoinColumns);
+        auto join = C % 4 ? join_rows<T, 1> : join_rows<T, 4>;
+        launch(join, grid, dim3(kSumThreads), 0, stream, C, scale, (const float*)head, (const float*)tail, (const SumNote*)notes,
+               static_cast<T*>(dw));
         return check_launch("embedding gradient (join)");
     }
     return ZS_OK;
@@ -342,9 +373,7 @@ zs_status zs_embedding(int32_t dtype, const void* w, int64_t w_ld, const int32_t
 size_t zs_embedding_backward_workspace_bytes(int32_t dtype, int64_t M, int32_t V, int32_t C) {
     using namespace zs;
     if (!known_dtype(dtype) || M < 0 || V < 1 || C < 1 || M > kMaxRows || V > kMaxRows || C > kMaxRows) return 0;
-    const int vec = 16 / dtype_bytes(dtype);
-    const size_t elements = sum_workspace(sum_shape(M, V, C, 1));
-    return C % vec ? elements : imax(elements, sum_workspace(sum_shape(M, V, C, vec)));
+    return sum_workspace(sum_shape(M, V, C, 16 / dtype_bytes(dtype)));
 }
 
 zs_status zs_embedding_backward(int32_t dtype, const void* dy, int64_t dy_ld, const int32_t* row_ptr, const int32_t* perm, int64_t M,

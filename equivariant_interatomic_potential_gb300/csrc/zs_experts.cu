@@ -15,92 +15,162 @@ namespace {
 constexpr int kChoices = 8;   // rows that a thread has in flight
 
 struct AssignmentSource {
-    static constexpr bool kScaled = false;
+    static constexpr bool kScaled = false, kAgain = false;
     const int32_t *row_ptr, *perm;
     int32_t G, R;             // R assignments
     FastDiv by_k;
     int32_t* slot;
-    __device__ __forceinline__ int64_t row(int64_t p, bool first) const {
+    __device__ __forceinline__ int32_t row(int32_t p, bool first) const {
         const int32_t a = __ldg(perm + p);
         if ((uint32_t)a >= (uint32_t)R) return -1;
         const bool held = p < __ldg(row_ptr + G);
-        if (first) slot[a] = held ? (int32_t)p : -1;
-        return held ? (int64_t)by_k.quotient((uint32_t)a) : -1;
+        if (first) slot[a] = held ? p : -1;
+        return held ? (int32_t)by_k.quotient((uint32_t)a) : -1;
     }
 };
 
-template <typename T, int VEC>
+// slot alone, from perm.
+__global__ void __launch_bounds__(kMoveThreads) invert(int32_t R, const int32_t* __restrict__ end, const int32_t* __restrict__ perm,
+                                                       int32_t* __restrict__ slot) {
+    pdl_wait();
+    pdl_trigger();
+    const int64_t p = (int64_t)blockIdx.x * kMoveThreads + threadIdx.x;
+    if (p >= R) return;
+    const int32_t a = __ldg(perm + p);
+    if ((uint32_t)a < (uint32_t)R) slot[a] = p < __ldg(end) ? (int32_t)p : -1;
+}
+
+// Zeros in the rows of the result from row_ptr[G] on.
+template <typename R, typename T>
+__device__ __forceinline__ void clear_rows_behind(const int32_t* __restrict__ end, int32_t rows, T* to, int64_t ld, int32_t P, int32_t C) {
+    if (blockIdx.y != 0) return;
+    for (int64_t p = (int64_t)imax(__ldg(end), 0) + blockIdx.x; p < rows; p += gridDim.x)
+        for (int c = threadIdx.x; c < P; c += blockDim.x) R::template store<true>(to + p * ld, R::column(to + p * ld, c), C, R::zero());
+}
+
+// Each row of x to its slots: x is read once, whatever k.
+template <typename T, bool kWhole>
+__global__ void __launch_bounds__(kMoveThreads) spread_rows(MoveShape s, int32_t k, int32_t R, Rows<T> x,
+                                                            const int32_t* __restrict__ slot, const int32_t* __restrict__ end,
+                                                            T* __restrict__ xs) {
+    using Rw = Row<T, kWhole>;
+    pdl_wait();
+    pdl_trigger();
+    for_pieces<1>(s, [&](const int32_t(&row)[1], const int32_t(&piece)[1]) {
+        if (row[0] < 0) return;
+        const int32_t* at = slot + (int64_t)row[0] * k;
+        uint4 v = Rw::zero();
+        if (kWhole) v = Rw::template load<false>(x, row[0], (int64_t)piece[0] * Rw::N, s.C);
+        for (int j0 = 0; j0 < k; j0 += kChoices) {
+            int32_t p[kChoices];
+#pragma unroll
+            for (int j = 0; j < kChoices; ++j) p[j] = j0 + j < k ? __ldg(at + j0 + j) : -1;
+#pragma unroll
+            for (int j = 0; j < kChoices; ++j) {
+                if ((uint32_t)p[j] >= (uint32_t)R) continue;
+                T* to = xs + (int64_t)p[j] * s.C;
+                const int64_t e = Rw::column(to, piece[0]);
+                if (!kWhole) v = Rw::template load<true>(x, row[0], e, s.C);   // to each slot's phase, from L1
+                Rw::template store<true>(to, e, s.C, v);
+            }
+        }
+    });
+    clear_rows_behind<Rw>(end, R, xs, s.C, s.P, s.C);
+}
+
+template <typename T, bool kWhole>
 zs_status dispatch(const void* x, int64_t x_ld, const int32_t* row_ptr, const int32_t* perm, int32_t R, int32_t k, int32_t G, int32_t C,
                    void* xs, int32_t* slot, cudaStream_t s) {
-    constexpr int U = VEC == 1 ? 8 : 4;
-    const MoveShape shape = move_shape(R, C / VEC, U);
-    launch(move_rows<T, VEC, U, AssignmentSource>, dim3(shape.ctas_x, shape.ctas_y), dim3(kMoveThreads), 0, s, shape,
-           AssignmentSource{row_ptr, perm, G, R, FastDiv((uint32_t)k), slot}, static_cast<const T*>(x), x_ld, 1.f, static_cast<T*>(xs),
-           (int64_t)C);
+    using Rw = Row<T, kWhole>;
+    const Rows<T> from(x, R / k, x_ld, C);
+    T* to = static_cast<T*>(xs);
+    // One kernel that reads a row of x for each of xs; from 8 MB of xs on two, the second of which reads x once (8 choices
+    // of 1024 bf16: 1 MB 1.8 against 2.9 us, 8 MB 3.8 and 3.8, 64 MB 14.6 and 11.3, 512 MB 156 and 93).
+    if (k > 1 && (int64_t)R * C * (int64_t)sizeof(T) >= 8 << 20) {
+        launch(invert, dim3((R + kMoveThreads - 1) / kMoveThreads), dim3(kMoveThreads), 0, s, R, row_ptr + G, perm, slot);
+        const MoveShape shape = move_shape(R / k, Rw::pieces(C), C, 1);
+        launch(spread_rows<T, kWhole>, dim3(shape.ctas_x, shape.ctas_y), dim3(kMoveThreads), 0, s, shape, k, R, from,
+               (const int32_t*)slot, row_ptr + G, to);
+    } else {
+        constexpr int U = 4;
+        const MoveShape shape = move_shape(R, Rw::pieces(C), C, U);
+        launch(move_rows<T, kWhole, U, AssignmentSource>, dim3(shape.ctas_x, shape.ctas_y), dim3(kMoveThreads), 0, s, shape,
+               AssignmentSource{row_ptr, perm, G, R, FastDiv((uint32_t)k), slot}, from, 1.f, to, (int64_t)C);
+    }
     return check_launch("dispatch");
 }
 
-template <typename T, int VEC>
-__global__ void __launch_bounds__(kMoveThreads) combine_rows(MoveShape s, int32_t k, int32_t R, const T* __restrict__ h, int64_t h_ld,
+// U pieces of a thread at a time and KJ choices of each: eight loads in flight.
+template <typename T, bool kWhole, int KJ>
+__global__ void __launch_bounds__(kMoveThreads) combine_rows(MoveShape s, int32_t k, int32_t R, Rows<T> h,
                                                              const int32_t* __restrict__ slot, const float* __restrict__ weights,
                                                              T* __restrict__ y, int64_t y_ld) {
-    using Rw = Row<T, VEC>;
+    using Rw = Row<T, kWhole>;
+    constexpr int U = kChoices / KJ, N = Rw::N;
     pdl_wait();
     pdl_trigger();
-    const int64_t r0 = (int64_t)blockIdx.x * s.rows;
-    const int n = (int)imin<int64_t>(s.rows, s.M - r0) * s.tile;
-    for (int64_t c0 = (int64_t)blockIdx.y * s.tile; c0 < s.P; c0 += (int64_t)gridDim.y * s.tile) {
-        const int cols = (int)imin<int64_t>(s.tile, s.P - c0);
-        for (int t = threadIdx.x; t < n; t += kMoveThreads) {
-            const int row = (int)s.per_row.quotient((uint32_t)t), col = t - row * s.tile;
-            if (col >= cols) continue;
-            const int32_t* at = slot + (r0 + row) * k;
-            float sum[VEC] = {};
-            for (int j0 = 0; j0 < k; j0 += kChoices) {
-                typename Rw::Raw v[kChoices];
-                float w[kChoices];
-                bool held[kChoices];
+    for_pieces<U>(s, [&](const int32_t(&row)[U], const int32_t(&piece)[U]) {
+        float sum[U][N] = {};
+        for (int j0 = 0; j0 < k; j0 += KJ) {
+            uint4 v[U][KJ];
+            float w[U][KJ];
+            bool held[U][KJ];
 #pragma unroll
-                for (int j = 0; j < kChoices; ++j) {
-                    held[j] = false;
-                    if (j0 + j >= k) continue;
-                    const int32_t p = __ldg(at + j0 + j);
-                    held[j] = (uint32_t)p < (uint32_t)R;
-                    if (!held[j]) continue;
-                    v[j] = Rw::load_once(h + p * h_ld, c0 + col);
-                    w[j] = weights ? __ldg(weights + (r0 + row) * k + j0 + j) : 1.f;
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int j = 0; j < KJ; ++j) {
+                    held[u][j] = false;
+                    if (row[u] < 0 || j0 + j >= k) continue;
+                    const int64_t a = (int64_t)row[u] * k + j0 + j;
+                    const int32_t p = __ldg(slot + a);
+                    held[u][j] = (uint32_t)p < (uint32_t)R;
+                    if (!held[u][j]) continue;
+                    v[u][j] = Rw::template load<false>(h, p, Rw::column(y + (int64_t)row[u] * y_ld, piece[u]), s.C);
+                    w[u][j] = weights ? __ldg(weights + a) : 1.f;
                 }
 #pragma unroll
-                for (int j = 0; j < kChoices; ++j) {
-                    if (!held[j]) continue;
-                    float f[VEC];
-                    Rw::floats(v[j], f);
+            for (int u = 0; u < U; ++u)
 #pragma unroll
-                    for (int i = 0; i < VEC; ++i) sum[i] = fmaf(w[j], f[i], sum[i]);
+                for (int j = 0; j < KJ; ++j) {
+                    if (!held[u][j]) continue;
+                    float f[N];
+                    unpack<T>(v[u][j], f);
+#pragma unroll
+                    for (int i = 0; i < N; ++i) sum[u][i] = fmaf(w[u][j], f[i], sum[u][i]);
                 }
-            }
-            Rw::store(y + (r0 + row) * y_ld, c0 + col, Rw::rounded(sum));
         }
-    }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (row[u] < 0) continue;
+            T* to = y + (int64_t)row[u] * y_ld;
+            Rw::template store<false>(to, Rw::column(to, piece[u]), s.C, pack<T>(sum[u]));
+        }
+    });
 }
 
-template <typename T, int VEC>
+template <typename T, bool kWhole>
 zs_status combine(const void* h, int64_t h_ld, const int32_t* slot, const float* weights, int64_t M, int32_t k, int32_t R, int32_t C,
                   void* y, int64_t y_ld, cudaStream_t s) {
-    const MoveShape shape = move_shape(M, C / VEC, 1);
-    launch(combine_rows<T, VEC>, dim3(shape.ctas_x, shape.ctas_y), dim3(kMoveThreads), 0, s, shape, k, R, static_cast<const T*>(h), h_ld,
-           slot, weights, static_cast<T*>(y), y_ld);
+    auto go = [&](auto choices) {
+        constexpr int KJ = decltype(choices)::value;
+        const MoveShape shape = move_shape(M, Row<T, kWhole>::pieces(C), C, kChoices / KJ);
+        launch(combine_rows<T, kWhole, KJ>, dim3(shape.ctas_x, shape.ctas_y), dim3(kMoveThreads), 0, s, shape, k, R,
+               Rows<T>(h, R, h_ld, C), slot, weights, static_cast<T*>(y), y_ld);
+    };
+    if (k <= 2) go(std::integral_constant<int, 2>());
+    else if (k <= 4) go(std::integral_constant<int, 4>());
+    else go(std::integral_constant<int, kChoices>());
     return check_launch("combine");
 }
 
 // `lanes` threads (a power of two) for a row i of dy, which they read once for its k choices.
 constexpr int kBackThreads = 256;
-template <typename T, int VEC>
+template <typename T, bool kWhole>
 __global__ void __launch_bounds__(kBackThreads) combine_rows_backward(
-    int64_t M, int32_t k, int32_t R, int32_t P, int lanes, const T* __restrict__ dy, int64_t dy_ld, const T* __restrict__ h,
-    int64_t h_ld, const int32_t* __restrict__ slot, const float* __restrict__ weights, const int32_t* __restrict__ end,
-    T* __restrict__ dh, int64_t dh_ld, float* __restrict__ dweights) {
-    using Rw = Row<T, VEC>;
+    int64_t M, int32_t k, int32_t R, int32_t P, int32_t C, int lanes, Rows<T> dy, Rows<T> h, const int32_t* __restrict__ slot, const float* __restrict__ weights, const int32_t* __restrict__ end,
+    T* __restrict__ dh, float* __restrict__ dweights) {
+    using Rw = Row<T, kWhole>;
+    constexpr int N = Rw::N;
     __shared__ float part[kBackThreads / 32][kChoices];
     pdl_wait();
     pdl_trigger();
@@ -122,24 +192,30 @@ __global__ void __launch_bounds__(kBackThreads) combine_rows_backward(
         }
         if (live) {
             for (int c = lane; c < P; c += lanes) {
-                typename Rw::Raw v[kChoices];
-                const typename Rw::Raw raw = Rw::load(dy + i * dy_ld, c);
+                uint4 v[kChoices];
+                float g[N];
+                if (kWhole) Rw::template load_floats<true>(dy, i, (int64_t)c * N, C, g);
 #pragma unroll
                 for (int j = 0; j < kChoices; ++j)
-                    if (at[j] >= 0) v[j] = Rw::load_once(h + at[j] * h_ld, c);
-                float g[VEC];
-                Rw::floats(raw, g);
+                    if (kWhole && at[j] >= 0) v[j] = Rw::template load<false>(h, at[j], (int64_t)c * N, C);
 #pragma unroll
                 for (int j = 0; j < kChoices; ++j) {
                     if (at[j] < 0) continue;
-                    float f[VEC], d[VEC];
-                    Rw::floats(v[j], f);
+                    T* to = dh + (int64_t)at[j] * C;
+                    const int64_t e = Rw::column(to, c);
+                    float f[N], d[N];
+                    if (kWhole) {
+                        unpack<T>(v[j], f);
+                    } else {   // to each slot's phase, dy from L1
+                        Rw::template load_floats<false>(h, at[j], e, C, f);
+                        Rw::template load_floats<true>(dy, i, e, C, g);
+                    }
 #pragma unroll
-                    for (int q = 0; q < VEC; ++q) {
+                    for (int q = 0; q < N; ++q) {
                         dot[j] = fmaf(g[q], f[q], dot[j]);
                         d[q] = w[j] * g[q];
                     }
-                    Rw::store(dh + at[j] * dh_ld, c, Rw::rounded(d));
+                    Rw::template store<true>(to, e, C, pack<T>(d));
                 }
             }
         }
@@ -163,23 +239,20 @@ __global__ void __launch_bounds__(kBackThreads) combine_rows_backward(
             for (int j = 0; j < kChoices; ++j)
                 if (j0 + j < k) dweights[i * k + j0 + j] = at[j] >= 0 ? dot[j] : 0.f;
     }
-    // rows of dh behind the last group's
-    for (int64_t p = (int64_t)imax(__ldg(end), 0) + blockIdx.x; p < R; p += gridDim.x)
-        for (int c = threadIdx.x; c < P; c += kBackThreads) Rw::store(dh + p * dh_ld, c, Rw::zero());
+    clear_rows_behind<Rw>(end, R, dh, C, P, C);
 }
 
-template <typename T, int VEC>
+template <typename T, bool kWhole>
 zs_status combine_backward(const void* dy, int64_t dy_ld, const void* h, int64_t h_ld, const int32_t* slot, const float* weights,
                            const int32_t* end, int64_t M, int32_t k, int32_t C, void* dh, float* dweights, cudaStream_t s) {
-    const int32_t P = C / VEC;
+    const int32_t P = Row<T, kWhole>::pieces(C);
     // enough threads a row that no one takes more than one piece, or so many that every SM has work
     int lanes = 1;
     while (lanes < 32 && lanes < P) lanes *= 2;
     while (lanes < kBackThreads && lanes < P && M * lanes < (int64_t)num_sms() * 1024) lanes *= 2;
     const int64_t rows = kBackThreads / lanes;
-    launch(combine_rows_backward<T, VEC>, dim3((unsigned)((M + rows - 1) / rows)), dim3(kBackThreads), 0, s, M, k, (int32_t)(M * k), P,
-           lanes, static_cast<const T*>(dy), dy_ld, static_cast<const T*>(h), h_ld, slot, weights, end, static_cast<T*>(dh), (int64_t)C,
-           dweights);
+    launch(combine_rows_backward<T, kWhole>, dim3((unsigned)((M + rows - 1) / rows)), dim3(kBackThreads), 0, s, M, k, (int32_t)(M * k), P,
+           C, lanes, Rows<T>(dy, M, dy_ld, C), Rows<T>(h, M * k, h_ld, C), slot, weights, end, static_cast<T*>(dh), dweights);
     return check_launch("combine gradient");
 }
 

@@ -1,10 +1,14 @@
 // Rows in pieces: what the operators that move rows (embedding, experts'
 // exchange) share.
 //
-// A row of C elements is P pieces of VEC elements: 16 bytes where every base
-// and row stride is on 16-byte boundaries, single elements elsewhere.  Pieces
-// of several rows are numbered together, so that a CTA's threads are all busy
-// whatever the width.
+// A row is written in aligned pieces of 16 bytes.  Where every base and row
+// stride is on 16-byte boundaries and the width is whole pieces (kWhole), those
+// are the row's own.  Elsewhere (odd widths, views at odd offsets) each row of
+// the result has its own phase: its first and last piece are written element by
+// element, and a piece is read from another row's phase as two aligned 16-byte
+// words that are shifted together (fp16 rows of 301, 64 MB: 94 us by elements,
+// see zs_experts.cu for what is left of it).  Pieces of several rows are numbered
+// together, so that a CTA's threads are all busy whatever the width.
 #pragma once
 
 #include <initializer_list>
@@ -24,35 +28,89 @@ struct FastDiv {
     __device__ __forceinline__ uint32_t quotient(uint32_t n) const { return (__umulhi(n, mul) + n) >> shift; }
 };
 
-template <typename T, int VEC>
+__device__ __forceinline__ uint4 ld_cached(const void* p) { return __ldg(static_cast<const uint4*>(p)); }
+__device__ __forceinline__ void st_once(void* p, uint4 v) {   // data that nothing reads again soon
+    asm volatile("st.global.cs.v4.u32 [%0], {%1,%2,%3,%4};" :: "l"(p), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+// The 16 bytes at offset o (0 < o < 16) of two words in a row.
+__device__ __forceinline__ uint4 shifted(uint4 a, uint4 b, int o) {
+    uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    if (o & 8) {
+#pragma unroll
+        for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+    }
+    if (o & 4) {
+#pragma unroll
+        for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+    }
+    const int s = 8 * (o & 3);
+    return make_uint4(__funnelshift_r(w[0], w[1], s), __funnelshift_r(w[1], w[2], s), __funnelshift_r(w[2], w[3], s),
+                      __funnelshift_r(w[3], w[4], s));
+}
+
+// A matrix that is read: rows ld apart, all of it in [p, end).
+template <typename T>
+struct Rows {
+    const T *p, *end;
+    int64_t ld;
+    Rows(const void* p_, int64_t rows, int64_t ld_, int32_t C)
+        : p(static_cast<const T*>(p_)), end(p + (rows > 0 ? (rows - 1) * ld_ + C : 0)), ld(ld_) {}
+};
+
+// Pieces of rows of C elements.  kCached: rows that are read again soon.
+template <typename T, bool kWhole>
 struct Row {
-    static_assert(VEC == kVec<T> || VEC == 1, "16-byte pieces or elements");
-    using Raw = typename std::conditional<VEC == 1, T, uint4>::type;
-    static __device__ __forceinline__ Raw load(const T* row, int64_t piece) {
-        if constexpr (VEC == 1) return __ldg(row + piece);
-        else return __ldg(reinterpret_cast<const uint4*>(row) + piece);
+    static constexpr int N = kVec<T>;   // elements of a piece
+
+    // Pieces that cover a row, whatever its phase.
+    static int32_t pieces(int32_t C) { return kWhole ? C / N : (int32_t)(((int64_t)C + 2 * N - 2) / N); }
+    // The column of the first element of piece c of a row of the result at `to`: below 0 where the row starts inside it.
+    static __device__ __forceinline__ int64_t column(const T* to, int32_t c) {
+        return (int64_t)c * N - (kWhole ? 0 : (int64_t)((reinterpret_cast<uintptr_t>(to) & 15u) / sizeof(T)));
     }
-    // Data that is read once.
-    static __device__ __forceinline__ Raw load_once(const T* row, int64_t piece) {
-        if constexpr (VEC == 1) return __ldg(row + piece);
-        else return ld_piece(row + piece * VEC);
+    // Columns [e, e + N) of a row of m; of those outside the row, whatever lies there (but nothing outside m is read).
+    template <bool kCached>
+    static __device__ __forceinline__ uint4 load(const Rows<T>& m, int64_t i, int64_t e, int32_t C) {
+        const T* row = m.p + i * m.ld;
+        if constexpr (kWhole) {
+            return kCached ? ld_cached(row + e) : ld_piece(row + e);
+        } else {
+            const int o = (int)(reinterpret_cast<uintptr_t>(row + e) & 15u), back = o / (int)sizeof(T);
+            const T *first = row + (e - back), *second = first + N;   // the aligned words that hold them
+            const bool a = e - back + N > 0 && e - back < C, b = o && e - back + 2 * N > 0 && e - back + N < C;
+            if ((a && (first < m.p || first + N > m.end)) || (b && (second < m.p || second + N > m.end))) {
+                Piece<T> v;   // at the ends of m
+#pragma unroll 1
+                for (int q = 0; q < N; ++q) v.e[q] = e + q >= 0 && e + q < C ? __ldg(row + e + q) : from_f32<T>(0.f);
+                return v.raw;
+            }
+            const uint4 v = a ? ld_cached(first) : zero();
+            return o ? shifted(v, b ? ld_cached(second) : zero(), o) : v;
+        }
     }
-    static __device__ __forceinline__ Raw zero() {
-        if constexpr (VEC == 1) return from_f32<T>(0.f);
-        else return make_uint4(0, 0, 0, 0);
+    // The same, zeros outside the row.
+    template <bool kCached>
+    static __device__ __forceinline__ void load_floats(const Rows<T>& m, int64_t i, int64_t e, int32_t C, float (&f)[N]) {
+        unpack<T>(load<kCached>(m, i, e, C), f);
+        if (!kWhole && (e < 0 || e + N > C))
+#pragma unroll
+            for (int q = 0; q < N; ++q) f[q] = e + q >= 0 && e + q < C ? f[q] : 0.f;
     }
-    static __device__ __forceinline__ void store(T* row, int64_t piece, Raw v) {
-        if constexpr (VEC == 1) row[piece] = v;
-        else st_piece(row + piece * VEC, v);
+    // Columns [e, e + N) of a row of the result, as far as they are in it.
+    template <bool kOnce>
+    static __device__ __forceinline__ void store(T* row, int64_t e, int32_t C, uint4 v) {
+        if (kWhole || (e >= 0 && e + N <= C && aligned16(row + e))) {
+            if (kOnce) st_once(row + e, v);
+            else st_piece(row + e, v);
+        } else {
+            Piece<T> p;
+            p.raw = v;
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                if (e + i >= 0 && e + i < C) row[e + i] = p.e[i];
+        }
     }
-    static __device__ __forceinline__ void floats(Raw v, float (&f)[VEC]) {
-        if constexpr (VEC == 1) f[0] = to_f32(v);
-        else unpack<T>(v, f);
-    }
-    static __device__ __forceinline__ Raw rounded(const float (&f)[VEC]) {
-        if constexpr (VEC == 1) return from_f32<T>(f[0]);
-        else return pack<T>(f);
-    }
+    static __device__ __forceinline__ uint4 zero() { return make_uint4(0, 0, 0, 0); }
 };
 
 // Whether rows of C elements at these bases and strides (in elements) are whole 16-byte pieces.
@@ -68,11 +126,11 @@ inline bool whole_pieces(int32_t dtype, int32_t C, std::initializer_list<RowsAt>
     return true;
 }
 
-// Calls f with the element type and the elements of a piece as template arguments: f<T, VEC>(args...).
-#define ZS_ROWS_DISPATCH(F, dtype, whole, ...)                                                      \
-    ((dtype) == ZS_F32    ? ((whole) ? F<float, 4>(__VA_ARGS__) : F<float, 1>(__VA_ARGS__))         \
-     : (dtype) == ZS_BF16 ? ((whole) ? F<__nv_bfloat16, 8>(__VA_ARGS__) : F<__nv_bfloat16, 1>(__VA_ARGS__)) \
-                          : ((whole) ? F<__half, 8>(__VA_ARGS__) : F<__half, 1>(__VA_ARGS__)))
+// Calls F with the element type and whether rows are whole pieces as template arguments.
+#define ZS_ROWS_DISPATCH(F, dtype, whole, ...)                                                                            \
+    ((dtype) == ZS_F32    ? ((whole) ? F<float, true>(__VA_ARGS__) : F<float, false>(__VA_ARGS__))                        \
+     : (dtype) == ZS_BF16 ? ((whole) ? F<__nv_bfloat16, true>(__VA_ARGS__) : F<__nv_bfloat16, false>(__VA_ARGS__))        \
+                          : ((whole) ? F<__half, true>(__VA_ARGS__) : F<__half, false>(__VA_ARGS__)))
 
 // Checks that the entry points of these operators share.
 inline zs_status check_rows(const char* fn, const char* name, int32_t dtype, const void* p, int64_t ld, int64_t rows, int32_t C) {
@@ -89,24 +147,24 @@ inline zs_status check_words(const char* fn, const char* name, const void* p, in
 }
 constexpr int64_t kMaxRows = ((int64_t)1 << 31) - (1 << 16);   // rows and columns of one call
 
-// Rows copied from where `Source` says, times a factor.  A CTA takes `rows`
-// rows of P pieces, or where a row is wider than its tile, a tile of a row.
+// Work on rows of pieces.  A CTA takes `rows` rows of P pieces, or where a row is wider than its tile, a tile of a row.
 constexpr int kMoveThreads = 256;
 
 struct MoveShape {
     int64_t M;
-    int32_t P, rows, tile;   // pieces of a row, rows of a CTA, pieces of a CTA's part of a row
-    FastDiv per_row;         // by the pieces of a CTA's part of a row
+    int32_t P, C, rows, tile;   // pieces and elements of a row, rows of a CTA, pieces of a CTA's part of a row
+    FastDiv per_row;            // by the pieces of a CTA's part of a row
     int32_t ctas_x, ctas_y;
 };
 
 // Threads take up to `each` pieces; fewer where that leaves SMs without a CTA.
-inline MoveShape move_shape(int64_t M, int32_t P, int each) {
+inline MoveShape move_shape(int64_t M, int32_t P, int32_t C, int each) {
     MoveShape s = {};
     int64_t tile = (int64_t)kMoveThreads * each;
     while (tile > kMoveThreads && M * P < tile * num_sms()) tile /= 2;
     s.M = M;
     s.P = P;
+    s.C = C;
     s.tile = (int32_t)imin<int64_t>(P, tile);
     s.rows = (int32_t)imax<int64_t>(1, tile / P);
     s.per_row = FastDiv((uint32_t)s.tile);
@@ -115,47 +173,58 @@ inline MoveShape move_shape(int64_t M, int32_t P, int each) {
     return s;
 }
 
-template <typename T, int VEC, int U, typename Source>
-__global__ void __launch_bounds__(kMoveThreads) move_rows(MoveShape s, Source src, const T* __restrict__ x, int64_t x_ld, float factor,
-                                                          T* __restrict__ y, int64_t y_ld) {
-    using R = Row<T, VEC>;
-    pdl_wait();
-    pdl_trigger();
+// Calls f(rows, pieces) for this CTA's pieces, up to U of a thread at a time: row -1 where there is none.
+template <int U, typename F>
+__device__ __forceinline__ void for_pieces(const MoveShape& s, F&& f) {
     const int64_t r0 = (int64_t)blockIdx.x * s.rows;
-    const int rows = (int)imin<int64_t>(s.rows, s.M - r0);
+    const int n = (int)imin<int64_t>(s.rows, s.M - r0) * s.tile;
     for (int64_t c0 = (int64_t)blockIdx.y * s.tile; c0 < s.P; c0 += (int64_t)gridDim.y * s.tile) {
         const int cols = (int)imin<int64_t>(s.tile, s.P - c0);
-        const int n = rows * s.tile;
         for (int t0 = threadIdx.x; t0 < n; t0 += U * kMoveThreads) {
-            typename R::Raw v[U];
-            int row[U], col[U];
+            int32_t row[U], piece[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int t = t0 + u * kMoveThreads;
-                row[u] = (int)s.per_row.quotient((uint32_t)t);
-                col[u] = t - row[u] * s.tile;
-                v[u] = R::zero();
-                if (t < n && col[u] < cols) {
-                    const int64_t from = src.row(r0 + row[u], c0 + col[u] == 0);
-                    if (from >= 0) v[u] = R::load(x + from * x_ld, c0 + col[u]);
-                } else {
-                    row[u] = -1;
-                }
+                const int q = (int)s.per_row.quotient((uint32_t)t), col = t - q * s.tile;
+                row[u] = t < n && col < cols ? (int32_t)(r0 + q) : -1;
+                piece[u] = (int32_t)(c0 + col);
             }
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                if (row[u] < 0) continue;
-                if (Source::kScaled) {
-                    float f[VEC];
-                    R::floats(v[u], f);
-#pragma unroll
-                    for (int i = 0; i < VEC; ++i) f[i] *= factor;
-                    v[u] = R::rounded(f);
-                }
-                R::store(y + (r0 + row[u]) * y_ld, c0 + col[u], v[u]);
-            }
+            f(row, piece);
         }
     }
+}
+
+// Rows copied from where `Source` says, times a factor.
+template <typename T, bool kWhole, int U, typename Source>
+__global__ void __launch_bounds__(kMoveThreads) move_rows(MoveShape s, Source src, Rows<T> x, float factor, T* __restrict__ y,
+                                                          int64_t y_ld) {
+    using R = Row<T, kWhole>;
+    pdl_wait();
+    pdl_trigger();
+    for_pieces<U>(s, [&](const int32_t(&row)[U], const int32_t(&piece)[U]) {
+        uint4 v[U];
+        int32_t from[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) from[u] = row[u] >= 0 ? src.row(row[u], piece[u] == 0) : -1;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            v[u] = R::zero();
+            if (from[u] >= 0) v[u] = R::template load<Source::kAgain>(x, from[u], R::column(y + (int64_t)row[u] * y_ld, piece[u]), s.C);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (row[u] < 0) continue;
+            if (Source::kScaled) {
+                float f[R::N];
+                unpack<T>(v[u], f);
+#pragma unroll
+                for (int i = 0; i < R::N; ++i) f[i] *= factor;
+                v[u] = pack<T>(f);
+            }
+            T* to = y + (int64_t)row[u] * y_ld;
+            R::template store<true>(to, R::column(to, piece[u]), s.C, v[u]);
+        }
+    });
 }
 
 }  // namespace zs
