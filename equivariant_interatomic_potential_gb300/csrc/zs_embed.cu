@@ -151,7 +151,8 @@ __global__ void __launch_bounds__(kSumThreads, 2) sum_rows(SumShape s, Rows<T> d
     __syncthreads();
 
     const int unit = (int)s.by_cols.quotient((uint32_t)tid), col = tid - unit * s.cols;
-    const int64_t c = (int64_t)blockIdx.y * s.cols + col, e = c * VEC;
+    const int64_t c = (int64_t)blockIdx.y * s.cols + col;
+    const int32_t e = (int32_t)imin<int64_t>(c * VEC, s.C);
     const bool live = unit < s.units && c < s.P;
     float acc[VEC] = {};
     bool cut = false;                 // the unit closes a row that others have begun
@@ -226,7 +227,7 @@ __global__ void __launch_bounds__(kSumThreads, 2) sum_rows(SumShape s, Rows<T> d
             for (int i = 0; i < VEC; ++i) sum[i] += open[(q * s.cols + col) * VEC + i];
     };
     const int64_t at = (int64_t)blockIdx.x * s.C + e;
-    const int width = kWhole ? VEC : (int)imin<int64_t>(VEC, s.C - e);   // of the piece
+    const int width = kWhole ? VEC : imin(VEC, s.C - e);   // of the piece
     if (cut) {
         float sum[VEC];
         earlier(begun_row, sum);

@@ -60,7 +60,7 @@ __global__ void __launch_bounds__(kMoveThreads) spread_rows(MoveShape s, int32_t
         if (row[0] < 0) return;
         const int32_t* at = slot + (int64_t)row[0] * k;
         uint4 v = Rw::zero();
-        if (kWhole) v = Rw::template load<false>(x, row[0], (int64_t)piece[0] * Rw::N, s.C);
+        if (kWhole) v = Rw::template load<false>(x, row[0], piece[0] * Rw::N, s.C);
         for (int j0 = 0; j0 < k; j0 += kChoices) {
             int32_t p[kChoices];
 #pragma unroll
@@ -69,7 +69,7 @@ __global__ void __launch_bounds__(kMoveThreads) spread_rows(MoveShape s, int32_t
             for (int j = 0; j < kChoices; ++j) {
                 if ((uint32_t)p[j] >= (uint32_t)R) continue;
                 T* to = xs + (int64_t)p[j] * s.C;
-                const int64_t e = Rw::column(to, piece[0]);
+                const int32_t e = Rw::column(to, piece[0]);
                 if (!kWhole) v = Rw::template load<true>(x, row[0], e, s.C);   // to each slot's phase, from L1
                 Rw::template store<true>(to, e, s.C, v);
             }
@@ -100,13 +100,16 @@ zs_status dispatch(const void* x, int64_t x_ld, const int32_t* row_ptr, const in
     return check_launch("dispatch");
 }
 
-// U pieces of a thread at a time and KJ choices of each: eight loads in flight.
-template <typename T, bool kWhole, int KJ>
-__global__ void __launch_bounds__(kMoveThreads) combine_rows(MoveShape s, int32_t k, int32_t R, Rows<T> h,
-                                                             const int32_t* __restrict__ slot, const float* __restrict__ weights,
-                                                             T* __restrict__ y, int64_t y_ld) {
+// U pieces of a thread at a time and KJ choices of each: four or eight loads in flight and four or five CTAs an SM.  More
+// loads and fewer CTAs are slower (8 choices of 1024 bf16, 32768 rows: 106 us at 3 CTAs, 97 at 4; 2 choices of 256, 256 MB:
+// 8 loads at 3 CTAs 111, 4 at 5 84), staging slots in shared memory too (115 to 188): the read of rows in any order is the
+// limit, 0.93 of the copy rate.
+template <typename T, bool kWhole, int KJ, int U>
+__global__ void __launch_bounds__(kMoveThreads, (KJ == kChoices ? 4 : 5) - !kWhole) combine_rows(
+    MoveShape s, int32_t k, int32_t R, Rows<T> h, const int32_t* __restrict__ slot, const float* __restrict__ weights, T* __restrict__ y,
+    int64_t y_ld) {
     using Rw = Row<T, kWhole>;
-    constexpr int U = kChoices / KJ, N = Rw::N;
+    constexpr int N = Rw::N;
     pdl_wait();
     pdl_trigger();
     for_pieces<U>(s, [&](const int32_t(&row)[U], const int32_t(&piece)[U]) {
@@ -151,37 +154,38 @@ __global__ void __launch_bounds__(kMoveThreads) combine_rows(MoveShape s, int32_
 template <typename T, bool kWhole>
 zs_status combine(const void* h, int64_t h_ld, const int32_t* slot, const float* weights, int64_t M, int32_t k, int32_t R, int32_t C,
                   void* y, int64_t y_ld, cudaStream_t s) {
-    auto go = [&](auto choices) {
-        constexpr int KJ = decltype(choices)::value;
-        const MoveShape shape = move_shape(M, Row<T, kWhole>::pieces(C), C, kChoices / KJ);
-        launch(combine_rows<T, kWhole, KJ>, dim3(shape.ctas_x, shape.ctas_y), dim3(kMoveThreads), 0, s, shape, k, R,
+    auto go = [&](auto choices, auto pieces) {
+        constexpr int KJ = decltype(choices)::value, U = decltype(pieces)::value;
+        const MoveShape shape = move_shape(M, Row<T, kWhole>::pieces(C), C, U);
+        launch(combine_rows<T, kWhole, KJ, U>, dim3(shape.ctas_x, shape.ctas_y), dim3(kMoveThreads), 0, s, shape, k, R,
                Rows<T>(h, R, h_ld, C), slot, weights, static_cast<T*>(y), y_ld);
     };
-    if (k <= 2) go(std::integral_constant<int, 2>());
-    else if (k <= 4) go(std::integral_constant<int, 4>());
-    else go(std::integral_constant<int, kChoices>());
+    using std::integral_constant;
+    if (k <= 2) go(integral_constant<int, 2>(), integral_constant<int, kWhole ? 2 : 1>());
+    else if (k <= 4) go(integral_constant<int, 4>(), integral_constant<int, 1>());
+    else go(integral_constant<int, kChoices>(), integral_constant<int, 1>());
     return check_launch("combine");
 }
 
 // `lanes` threads (a power of two) for a row i of dy, which they read once for its k choices.
 constexpr int kBackThreads = 256;
-template <typename T, bool kWhole>
-__global__ void __launch_bounds__(kBackThreads) combine_rows_backward(
+template <typename T, bool kWhole, int KJ>
+__global__ void __launch_bounds__(kBackThreads, kWhole ? 3 : 2) combine_rows_backward(
     int64_t M, int32_t k, int32_t R, int32_t P, int32_t C, int lanes, Rows<T> dy, Rows<T> h, const int32_t* __restrict__ slot, const float* __restrict__ weights, const int32_t* __restrict__ end,
     T* __restrict__ dh, float* __restrict__ dweights) {
     using Rw = Row<T, kWhole>;
-    constexpr int N = Rw::N;
-    __shared__ float part[kBackThreads / 32][kChoices];
+    constexpr int N = Rw::N, kBatch = kWhole ? KJ : 4;
+    __shared__ float part[kBackThreads / 32][KJ];
     pdl_wait();
     pdl_trigger();
     const int group = threadIdx.x / lanes, lane = threadIdx.x - group * lanes;
     const int64_t i = (int64_t)blockIdx.x * (kBackThreads / lanes) + group;
     const bool live = i < M;
-    for (int j0 = 0; j0 < k; j0 += kChoices) {
-        float dot[kChoices] = {}, w[kChoices];
-        int32_t at[kChoices];
+    for (int j0 = 0; j0 < k; j0 += KJ) {
+        float dot[KJ] = {}, w[KJ];
+        int32_t at[KJ];
 #pragma unroll
-        for (int j = 0; j < kChoices; ++j) {
+        for (int j = 0; j < KJ; ++j) {
             at[j] = -1;
             w[j] = 0.f;
             if (!live || j0 + j >= k) continue;
@@ -192,51 +196,54 @@ __global__ void __launch_bounds__(kBackThreads) combine_rows_backward(
         }
         if (live) {
             for (int c = lane; c < P; c += lanes) {
-                uint4 v[kChoices];
                 float g[N];
-                if (kWhole) Rw::template load_floats<true>(dy, i, (int64_t)c * N, C, g);
+                if (kWhole) Rw::template load_floats<true>(dy, i, c * N, C, g);
 #pragma unroll
-                for (int j = 0; j < kChoices; ++j)
-                    if (kWhole && at[j] >= 0) v[j] = Rw::template load<false>(h, at[j], (int64_t)c * N, C);
+                for (int b = 0; b < KJ; b += kBatch) {
+                    uint4 v[kBatch], d[kBatch];   // of h, and where phases differ of dy in each slot's phase, from L1
 #pragma unroll
-                for (int j = 0; j < kChoices; ++j) {
-                    if (at[j] < 0) continue;
-                    T* to = dh + (int64_t)at[j] * C;
-                    const int64_t e = Rw::column(to, c);
-                    float f[N], d[N];
-                    if (kWhole) {
-                        unpack<T>(v[j], f);
-                    } else {   // to each slot's phase, dy from L1
-                        Rw::template load_floats<false>(h, at[j], e, C, f);
-                        Rw::template load_floats<true>(dy, i, e, C, g);
+                    for (int j = 0; j < kBatch; ++j) {
+                        if (at[b + j] < 0) continue;
+                        const int32_t e = Rw::column(dh + (int64_t)at[b + j] * C, c);
+                        v[j] = Rw::template load<false>(h, at[b + j], e, C);
+                        if (!kWhole) d[j] = Rw::template load<true>(dy, i, e, C);
                     }
 #pragma unroll
-                    for (int q = 0; q < N; ++q) {
-                        dot[j] = fmaf(g[q], f[q], dot[j]);
-                        d[q] = w[j] * g[q];
+                    for (int j = 0; j < kBatch; ++j) {
+                        if (at[b + j] < 0) continue;
+                        T* to = dh + (int64_t)at[b + j] * C;
+                        const int32_t e = Rw::column(to, c);
+                        float f[N], scaled[N];
+                        Rw::floats(v[j], e, C, f);
+                        if (!kWhole) Rw::floats(d[j], e, C, g);
+#pragma unroll
+                        for (int q = 0; q < N; ++q) {
+                            dot[b + j] = fmaf(g[q], f[q], dot[b + j]);
+                            scaled[q] = w[b + j] * g[q];
+                        }
+                        Rw::template store<true>(to, e, C, pack<T>(scaled));
                     }
-                    Rw::template store<true>(to, e, C, pack<T>(d));
                 }
             }
         }
 #pragma unroll
-        for (int j = 0; j < kChoices; ++j)
+        for (int j = 0; j < KJ; ++j)
             for (int o = imin(lanes, 32) >> 1; o > 0; o >>= 1) dot[j] += __shfl_xor_sync(0xffffffffu, dot[j], o);
         if (lanes > 32) {
             const int warp = threadIdx.x >> 5;
             if ((threadIdx.x & 31) == 0)
 #pragma unroll
-                for (int j = 0; j < kChoices; ++j) part[warp][j] = dot[j];
+                for (int j = 0; j < KJ; ++j) part[warp][j] = dot[j];
             __syncthreads();
             if (lane == 0)
 #pragma unroll
-                for (int j = 0; j < kChoices; ++j)
+                for (int j = 0; j < KJ; ++j)
                     for (int q = 1; q < lanes / 32; ++q) dot[j] += part[warp + q][j];
             __syncthreads();
         }
         if (live && lane == 0)
 #pragma unroll
-            for (int j = 0; j < kChoices; ++j)
+            for (int j = 0; j < KJ; ++j)
                 if (j0 + j < k) dweights[i * k + j0 + j] = at[j] >= 0 ? dot[j] : 0.f;
     }
     clear_rows_behind<Rw>(end, R, dh, C, P, C);
@@ -251,7 +258,8 @@ zs_status combine_backward(const void* dy, int64_t dy_ld, const void* h, int64_t
     while (lanes < 32 && lanes < P) lanes *= 2;
     while (lanes < kBackThreads && lanes < P && M * lanes < (int64_t)num_sms() * 1024) lanes *= 2;
     const int64_t rows = kBackThreads / lanes;
-    launch(combine_rows_backward<T, kWhole>, dim3((unsigned)((M + rows - 1) / rows)), dim3(kBackThreads), 0, s, M, k, (int32_t)(M * k), P,
+    auto kernel = k <= 4 ? combine_rows_backward<T, kWhole, 4> : combine_rows_backward<T, kWhole, kChoices>;
+    launch(kernel, dim3((unsigned)((M + rows - 1) / rows)), dim3(kBackThreads), 0, s, M, k, (int32_t)(M * k), P,
            C, lanes, Rows<T>(dy, M, dy_ld, C), Rows<T>(h, M * k, h_ld, C), slot, weights, end, static_cast<T*>(dh), dweights);
     return check_launch("combine gradient");
 }

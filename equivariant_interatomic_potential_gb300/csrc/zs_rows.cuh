@@ -65,12 +65,12 @@ struct Row {
     // Pieces that cover a row, whatever its phase.
     static int32_t pieces(int32_t C) { return kWhole ? C / N : (int32_t)(((int64_t)C + 2 * N - 2) / N); }
     // The column of the first element of piece c of a row of the result at `to`: below 0 where the row starts inside it.
-    static __device__ __forceinline__ int64_t column(const T* to, int32_t c) {
-        return (int64_t)c * N - (kWhole ? 0 : (int64_t)((reinterpret_cast<uintptr_t>(to) & 15u) / sizeof(T)));
+    static __device__ __forceinline__ int32_t column(const T* to, int32_t c) {
+        return c * N - (kWhole ? 0 : (int32_t)((uint32_t)reinterpret_cast<uintptr_t>(to) & 15u) / (int32_t)sizeof(T));
     }
     // Columns [e, e + N) of a row of m; of those outside the row, whatever lies there (but nothing outside m is read).
     template <bool kCached>
-    static __device__ __forceinline__ uint4 load(const Rows<T>& m, int64_t i, int64_t e, int32_t C) {
+    static __device__ __forceinline__ uint4 load(const Rows<T>& m, int64_t i, int32_t e, int32_t C) {
         const T* row = m.p + i * m.ld;
         if constexpr (kWhole) {
             return kCached ? ld_cached(row + e) : ld_piece(row + e);
@@ -88,17 +88,20 @@ struct Row {
             return o ? shifted(v, b ? ld_cached(second) : zero(), o) : v;
         }
     }
-    // The same, zeros outside the row.
-    template <bool kCached>
-    static __device__ __forceinline__ void load_floats(const Rows<T>& m, int64_t i, int64_t e, int32_t C, float (&f)[N]) {
-        unpack<T>(load<kCached>(m, i, e, C), f);
+    // Their values, zeros outside the row.
+    static __device__ __forceinline__ void floats(uint4 v, int32_t e, int32_t C, float (&f)[N]) {
+        unpack<T>(v, f);
         if (!kWhole && (e < 0 || e + N > C))
 #pragma unroll
             for (int q = 0; q < N; ++q) f[q] = e + q >= 0 && e + q < C ? f[q] : 0.f;
     }
+    template <bool kCached>
+    static __device__ __forceinline__ void load_floats(const Rows<T>& m, int64_t i, int32_t e, int32_t C, float (&f)[N]) {
+        floats(load<kCached>(m, i, e, C), e, C, f);
+    }
     // Columns [e, e + N) of a row of the result, as far as they are in it.
     template <bool kOnce>
-    static __device__ __forceinline__ void store(T* row, int64_t e, int32_t C, uint4 v) {
+    static __device__ __forceinline__ void store(T* row, int32_t e, int32_t C, uint4 v) {
         if (kWhole || (e >= 0 && e + N <= C && aligned16(row + e))) {
             if (kOnce) st_once(row + e, v);
             else st_piece(row + e, v);
