@@ -45,9 +45,9 @@ zs_status embed_forward(const void* w, int64_t w_ld, int32_t V, const int32_t* i
 // ------------------------------------------------------------------ gradient
 
 constexpr int kSumThreads = 256;
-constexpr int kSumBatch = 8;         // rows of dy in flight for a thread
+constexpr int kSumBatch = 6;         // rows of dy in flight for a thread
 constexpr int kSumItems = 4096;      // most items of a CTA (staged in shared memory)
-constexpr int kSumCtas = 2;          // CTAs an SM that the shares are made for: as many as run at once
+constexpr int kSumCtas = 3;          // CTAs an SM that the shares are made for: as many as run at once
 
 struct SumShape {
     int64_t M, items;                // items: M + V
@@ -106,7 +106,7 @@ __device__ __forceinline__ int rows_before(const int32_t* row_ptr, int32_t V, in
 }
 
 template <typename T, bool kWhole>
-__global__ void __launch_bounds__(kSumThreads, 2) sum_rows(SumShape s, Rows<T> dy,
+__global__ void __launch_bounds__(kSumThreads, kSumCtas) sum_rows(SumShape s, Rows<T> dy,
                                                         const int32_t* __restrict__ row_ptr, const int32_t* __restrict__ perm,
                                                         float scale, T* __restrict__ dw, float* __restrict__ head,
                                                         float* __restrict__ tail, SumNote* __restrict__ notes) {
