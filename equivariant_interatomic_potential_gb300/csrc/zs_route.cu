@@ -140,43 +140,6 @@ __device__ __forceinline__ void two_of_group(const RouteShape& s, U& first, U& s
         first = max(a, first);
     }
 }
-// Whether a lane's group is among the best, by its two largest keys, and in `close` whether the last group in and the
-// first one out are closer than known: each score to `error`, each value to `relative` of itself.
-template <typename F>
-__device__ __forceinline__ bool group_kept(const RouteShape& s, const Lane& l, typename KeyOf<F>::U first, typename KeyOf<F>::U second,
-                                           F error, F relative, bool& close) {
-    using U = typename KeyOf<F>::U;
-    U left = 0, last = 0;
-    F size = 0, last_size = 0;   // of what a sum is formed of
-    if (first && l.group < s.groups) {
-        F v = from_key<F>(first);
-        size = fabs(v);
-        if (s.group_top == 2 && second) {
-            const F w = from_key<F>(second);
-            v += w;
-            size += fabs(w);
-        }
-        left = to_key<F>(v);
-        if (!left) left = 1;
-    }
-    // rounds: the lowest group of the largest value is kept; the one behind the last is only looked at
-    bool kept = false;
-    for (int r = 0;; ++r) {
-        const U top = KeyOf<F>::max_of_warp(left);
-        if (top == 0) break;
-        const int winner = __ffs(__ballot_sync(kAll, left == top)) - 1;
-        const F winner_size = __shfl_sync(kAll, size, winner);
-        if (r == s.top_groups) {
-            close = from_key<F>(last) - from_key<F>(top) <= 4 * error + relative * (last_size + winner_size);
-            break;
-        }
-        last = top;
-        last_size = winner_size;
-        if (l.group == winner >> s.lane_bits) kept = true, left = 0;
-    }
-    return kept;
-}
-
 // What the choice goes by, in 64 bits: -infinity where it is closed.  `top` and `sum` for a softmax with a bias.
 template <bool kScored>
 __device__ __forceinline__ double score_in_64_bits(const RouteShape& s, double z, double top, double sum, const float* __restrict__ bias,
@@ -184,6 +147,26 @@ __device__ __forceinline__ double score_in_64_bits(const RouteShape& s, double z
     if (!kScored || z == -INFINITY) return z;
     const double a = s.sigmoid ? 1.0 / (1.0 + exp(-z)) : exp(z - top) / sum;
     return bias ? a + (double)__ldg(bias + e) : a;
+}
+
+// Whether a lane's group is among the best, by the values that the lanes of `speaks` hold of theirs: NaN above all, equal
+// ones by their number.
+__device__ __forceinline__ bool group_in_64_bits(const RouteShape& s, int group, bool speaks, double value) {
+    unsigned speakers = __ballot_sync(kAll, speaks && group < s.groups);
+    const unsigned long long mine = to_key<double>(value);
+    unsigned long long own = 0;
+    for (unsigned m = speakers; m; m &= m - 1) {   // each lane's group's own value
+        const int j = __ffs(m) - 1;
+        const unsigned long long v = __shfl_sync(kAll, mine, j);
+        if (__shfl_sync(kAll, group, j) == group) own = v;
+    }
+    int ahead = 0;
+    for (unsigned m = speakers; m; m &= m - 1) {
+        const int j = __ffs(m) - 1, g = __shfl_sync(kAll, group, j);
+        const unsigned long long v = __shfl_sync(kAll, mine, j);
+        ahead += v > own || (v == own && g < group);
+    }
+    return group < s.groups && ahead < s.top_groups;
 }
 
 // The row's choice in 64 bits: the expert of choice `lane` (or -1).
@@ -216,9 +199,10 @@ __device__ __noinline__ int choose_in_64_bits(const RouteShape& s, int lane, con
             second = k > first ? first : (k > second ? k : second);
             first = k > first ? k : first;
         }
-        bool close;
         two_of_group(s, first, second);
-        if (!group_kept<double>(s, l, first, second, 0.0, 0.0, close))
+        double value = -INFINITY;
+        if (first) value = from_key<double>(first) + (s.group_top == 2 && second ? from_key<double>(second) : 0.0);
+        if (!group_in_64_bits(s, l.group, l.group << s.lane_bits == lane, value))
             for (int i = 0; i < V; ++i) key[i] = 0;
     }
     int mine = -1;
@@ -276,23 +260,7 @@ __device__ __forceinline__ float renormalised(bool sigmoid, bool held, float z, 
 }
 __device__ __forceinline__ float sigmoid_of(float z) { return __fdividef(1.f, 1.f + expf(-z)); }
 
-// What one row's rounds leave: how many they were, what its scores are relative to, and how far 32 bits know them.
-struct Picked {
-    int n;
-    float top, sum;   // a softmax's largest logit and sum, where it is formed
-    float error;      // of a score, beside its rounding
-    bool odd;         // NaN (of a lane's own)
-    bool close;       // groups whose choice 32 bits do not tell
-};
-
-// A warp's place in shared memory: its lanes' sorted keys, and what its rounds took (a key, and its lane).
-template <int V>
-struct RouteSpace {
-    uint32_t list[V + 1][32];
-    uint2 taken[kRouteMaxK + 1];   // the choices, and the one behind
-};
-
-constexpr uint32_t kOpen = 0x00800000u;                   // the key of the lowest finite value
+constexpr uint32_t kOpen = 0x00800000u;                   // the key of the lowest finite value: below are closed ones
 template <int V> constexpr uint32_t kPlace = V - 1;       // a key's bits for the place in its lane, the last one 0
 template <int V> constexpr float kRelative = V * 0x1p-23f + 0x1p-22f;   // what the place's bits and a sum's rounding take
 // Keys of 16-bit logits are exact: they leave the place's bits clear.
@@ -302,6 +270,14 @@ __device__ __forceinline__ uint32_t open_key(float v) {   // NaN apart
     const uint32_t b = __float_as_uint(v);
     return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
 }
+
+// A warp's place in shared memory: its lanes' sorted keys (behind the first ones, and 0 behind the last), and what its
+// rounds took (a key, and its lane).
+template <int V>
+struct RouteSpace {
+    uint32_t list[V + 1][32];
+    uint2 taken[kRouteMaxK + 1];
+};
 template <int V>
 __device__ __forceinline__ int expert_of(const RouteShape& s, uint2 t) {
     return (int)((t.y >> s.lane_bits) * s.per + (t.y & (s.lanes - 1)) * s.each + (kPlace<V> - (t.x & kPlace<V>)));
@@ -313,94 +289,12 @@ __device__ __forceinline__ bool near_keys(uint32_t a, uint32_t b, float error) {
     return p - q <= 2.f * error + kRelative<V> * (fabsf(p) + fabsf(q)) + V * 0x1p-148f;
 }
 
-// The rounds of a row with the logits z, up to `rounds`, and up to `most` while keys are near the one of the last choice;
-// among the groups of the mask `groups`, where it is not 0.
-template <typename T, int V, bool kScored>
-__device__ __forceinline__ Picked pick(const RouteShape& s, const Lane& l, int lane, const float (&z)[V], const float* __restrict__ bias,
-                                       RouteSpace<V>& space, int rounds, int most, unsigned groups = 0,
-                                       uint32_t* largest = nullptr) {
-    Picked p = {0, 0.f, 1.f, 0.f, false, false};
-    const bool whole = !s.sigmoid && (kScored || !s.renormalise);   // scores over all experts are wanted
-    float a[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) a[i] = z[i];
-    if (whole) {
-        float top = z[0];
-#pragma unroll
-        for (int i = 1; i < V; ++i) top = fmaxf(top, z[i]);
-        p.top = max_of_warp(top);
-        float sum = 0.f;
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const float e = z[i] == -INFINITY ? 0.f : s.renormalise ? exp2_quick((z[i] - p.top) * kLog2e) : expf(z[i] - p.top);
-            if (kScored) a[i] = e;
-            sum += e;
-        }
-        p.sum = sum_of_warp(sum);
-    }
-    if (kScored) {
-        // exp(x) is known to 2 ulps and x log2(e) to 2 |x| 2^-24: times the exponential, or a sigmoid's slope, below 1.1 ulps
-        // of 1 more.  A sigmoid's sum and quotient add 1.5 ulps of it; a sum of exponentials, up to 2^-19 of it off, is that
-        // of all scores.
-        const float inv = s.sigmoid ? 1.f : reciprocal_quick(fmaxf(p.sum, 1.f));   // 1 and more, but where all are closed
-        p.error = s.sigmoid ? 0x1p-21f : 0x1p-18f * inv;
-        float b[V];
-        if (bias) load_lane<float, V>(bias + l.first, l.count, s.wide_bias, 0.f, b);
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            a[i] = s.sigmoid ? reciprocal_quick(1.f + exp2_quick(z[i] * -kLog2e)) : a[i] * inv;
-            if (bias) a[i] += b[i];
-        }
-    }
-    uint32_t key[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-        p.odd = p.odd || a[i] != a[i];
-        if (kScored) a[i] = z[i] == -INFINITY ? -INFINITY : a[i];
-        key[i] = (open_key(kScored ? a[i] : a[i] + 0.f) & ~kPlace<V>) | (kPlace<V> - i);   // -0 is 0
-    }
-    sort_keys(key);
-    uint32_t head = key[0];
-    if (largest) *largest = head;
-    if (kScored && s.top_groups < s.groups) {
-        if (groups) {
-            if (!(groups >> l.group & 1)) head = 0;
-        } else {
-            uint32_t first = key[0] & ~kPlace<V>, second = V > 1 ? key[V > 1] & ~kPlace<V> : 0;
-            if (first < kOpen) first = 0;
-            if (second < kOpen) second = 0;
-            two_of_group(s, first, second);
-            bool close = false;
-            if (!group_kept<float>(s, l, first, second, p.error, kRelative<V>, close)) head = 0;
-            p.close = close;
-        }
-    }
-#pragma unroll
-    for (int i = 1; i < V; ++i) space.list[i][lane] = key[i];
-    space.list[V][lane] = 0;
-    const uint32_t* next = &space.list[1][lane];
-    uint32_t least = kOpen, before = 0;
-    for (; p.n < most; ++p.n) {
-        const uint32_t top_key = __reduce_max_sync(kAll, head & ~kPlace<V>);
-        if (top_key < least) break;
-        if (p.n >= rounds && !near_keys<V>(before, top_key, p.error)) break;
-        if (p.n == s.k - 1) before = top_key;
-        const unsigned of = __ballot_sync(kAll, (head & ~kPlace<V>) == top_key);
-        if (lane == __ffs(of) - 1) {   // the lowest lane notes its key and moves on
-            space.taken[p.n] = make_uint2(head, lane);
-            head = *next;
-            next += 32;
-        }
-    }
-    return p;
-}
-
 // The groups of a row whose choice 32 bits do not tell, as a mask: the elements of each that may be among its two
-// largest, in 64 bits, a lane each; then a lane for each group.  0 where they are too many.  `keys` are a lane's sorted
-// ones, which pick left in `space` (the first one is given).
+// largest, in 64 bits, a lane each.  0 where they are too many.  `head` is a lane's first key.
 template <typename T, int V>
-__device__ __forceinline__ unsigned groups_in_64_bits(const RouteShape& s, const Lane& l, int lane, const T* __restrict__ row,
-                                                      const float* __restrict__ bias, RouteSpace<V>& space, uint32_t head, float error) {
+__device__ __noinline__ unsigned groups_in_64_bits(const RouteShape& s, int lane, const T* __restrict__ row, const float* __restrict__ bias,
+                                                   RouteSpace<V>& space, uint32_t head, float error) {
+    const Lane l(s, lane);
     uint32_t first = head & ~kPlace<V>, second = V > 1 ? space.list[1][lane] & ~kPlace<V> : 0;
     if (first < kOpen) first = 0;
     if (second < kOpen) second = 0;
@@ -411,18 +305,17 @@ __device__ __forceinline__ unsigned groups_in_64_bits(const RouteShape& s, const
         const uint32_t key = i == 0 ? head : space.list[i][lane];
         const bool in = l.group < s.groups && key >= kOpen && ((key & ~kPlace<V>) >= of || near_keys<V>(of, key, error));
         const unsigned all = __ballot_sync(kAll, in);
+        if (!all) break;   // a lane's keys descend
         const int at = n + __popc(all & ((1u << lane) - 1));
         if (in && at < 32) space.taken[at] = make_uint2(key, lane);
         n += __popc(all);
     }
     __syncwarp();
     if (n > 32) return 0;
-    const int e = lane < n ? expert_of<V>(s, space.taken[lane]) : 0, group = e / s.per;
-    // a softmax's sums sort like those of its exponentials
-    double a = 0.0, top = 0.0;
-    if (lane < n) a = logit(row, e);
-    if (!s.sigmoid) {
-        top = lane < n ? a : -INFINITY;
+    const int e = lane < n ? expert_of<V>(s, space.taken[lane]) : 0, group = lane < n ? e / s.per : -1;
+    double a = lane < n ? (double)logit(row, e) : -INFINITY, top = 0.0;
+    if (!s.sigmoid) {   // sums of a softmax's scores sort like those of its exponentials
+        top = a;
         for (int o = 16; o > 0; o >>= 1) top = fmax(top, __shfl_xor_sync(kAll, top, o));
     }
     if (lane < n) a = score_in_64_bits<true>(s, a, top, 1.0, bias, e);
@@ -434,60 +327,33 @@ __device__ __forceinline__ unsigned groups_in_64_bits(const RouteShape& s, const
         one = fmax(one, other);
     }
     const double value = s.group_top == 2 && two != -INFINITY ? one + two : one;
-    int ahead = 0;
-    for (int g = 0; g < s.groups; ++g) {
-        const double other = __shfl_sync(kAll, value, g);
-        ahead += other > value || (other == value && g < lane);
-    }
+    const unsigned mask = __ballot_sync(kAll, group_in_64_bits(s, lane, lane < s.groups, value));
     __syncwarp();
-    return __ballot_sync(kAll, lane < s.groups && ahead < s.top_groups);
+    return mask;
 }
 
-// A row whose choice 32 bits do not tell: all that may be among its k largest, in 64 bits, a lane each, put in order by
-// how many are ahead.  Where that is not enough (NaN, a softmax with a bias, too many) the whole row in 64 bits.
+// The order of the n candidates that the rounds took, by their scores in 64 bits (or by logits, which sort like a
+// softmax's scores without a bias): a lane each, by how many are ahead.  The expert of choice `lane` (or -1).
 template <typename T, int V, bool kScored>
-__device__ __noinline__ int choose_again(const RouteShape& s, int lane, const T* __restrict__ row, const float* __restrict__ bias,
-                                         RouteSpace<V>& space) {
-    const Lane l(s, lane);
-    bool far = kScored && !s.sigmoid && bias;
-    unsigned groups = 0;
-    uint2* taken = space.taken;
-    for (int again = 0; !far && again < 2; ++again) {
-        float z[V];
-        load_lane<T, V>(row + l.first, l.count, s.wide, -INFINITY, z);
-        __syncwarp();
-        uint32_t head;
-        const Picked p = pick<T, V, kScored>(s, l, lane, z, bias, space, s.k, kRouteMaxK + 1, groups, &head);
-        __syncwarp();
-        far = __any_sync(kAll, p.odd);
-        if (far) break;
-        if (kScored && p.close) {
-            groups = groups_in_64_bits<T, V>(s, l, lane, row, bias, space, head, p.error);
-            far = groups == 0;
-            continue;
-        }
-        far = p.n > kRouteMaxK;
-        if (far) break;
-        const int e = lane < p.n ? expert_of<V>(s, taken[lane]) : 0;
-        double a = 0.0;
-        if (lane < p.n) {   // a softmax's scores sort like its logits
-            a = logit(row, e);
-            if (kScored && s.sigmoid) a = score_in_64_bits<kScored>(s, a, 0.0, 0.0, bias, e);
-        }
-        int ahead = 0;
-        for (int j = 0; j < p.n; ++j) {
-            const double other = __shfl_sync(kAll, a, j);
-            const int f = __shfl_sync(kAll, e, j);
-            ahead += other > a || (other == a && f < e);
-        }
-        __syncwarp();
-        if (lane < p.n) taken[ahead].x = e;
-        __syncwarp();
-        const int mine = lane < imin(p.n, s.k) ? (int)taken[lane].x : -1;
-        __syncwarp();
-        return mine;
+__device__ __noinline__ int order_in_64_bits(const RouteShape& s, int lane, const T* __restrict__ row, const float* __restrict__ bias,
+                                             RouteSpace<V>& space, int n) {
+    const bool open = lane < n;
+    const int e = open ? expert_of<V>(s, space.taken[lane]) : -1;
+    double a = -INFINITY;
+    if (open) {
+        a = logit(row, e);
+        if (kScored && s.sigmoid) a = score_in_64_bits<kScored>(s, a, 0.0, 0.0, bias, e);
     }
-    return choose_in_64_bits<T, V, kScored>(s, lane, row, bias);
+    int ahead = 0;
+    for (int j = 0; j < n; ++j) {
+        const double other = __shfl_sync(kAll, a, j);
+        const int f = __shfl_sync(kAll, e, j);
+        ahead += other > a || (other == a && f < e);
+    }
+    __syncwarp();
+    if (open) space.taken[ahead].x = e;
+    __syncwarp();
+    return lane < imin(n, s.k) ? (int)space.taken[lane].x : -1;
 }
 
 template <typename T, int V, bool kScored>
@@ -502,34 +368,144 @@ __global__ void __launch_bounds__(kRouteWarps * 32, V <= 8 ? 12 : V <= 16 ? 8 : 
     if (r0 >= s.M) return;
     const T* row = logits + r0 * s.ld;
     const Lane l(s, lane);
-    float z[V];
-    load_lane<T, V>(row + l.first, l.count, s.wide, -INFINITY, z);
-    const int rounds = kExact<T, kScored> ? s.k : s.k + 1;
-    const Picked p = pick<T, V, kScored>(s, l, lane, z, bias, space, rounds, rounds);
-    __syncwarp();
-    int id = -1;
-    bool again = p.odd || p.close;
-    if (lane < imin(p.n, s.k)) {
-        const uint2 t = space.taken[lane];
-        id = expert_of<V>(s, t);
-        if (!kExact<T, kScored> && lane + 1 < p.n) {
-            const uint2 u = space.taken[lane + 1];
-            if (near_keys<V>(t.x, u.x, p.error)) {
-                const int e = expert_of<V>(s, u);   // two of one logit and bias are in their order
-                again = again || !(logit(row, id) == logit(row, e) && (!bias || __ldg(bias + id) == __ldg(bias + e)));
-            }
+    float a[V];
+    load_lane<T, V>(row + l.first, l.count, s.wide, -INFINITY, a);
+
+    const bool whole = !s.sigmoid && (kScored || !s.renormalise);   // a softmax's scores over all experts are wanted
+    float top = 0.f, sum = 1.f, error = 0.f;                        // error: of a score, beside its rounding
+    bool odd = false;
+    uint32_t closed = 0;                                            // the lane's closed experts, by their bits
+    if (kScored)
+#pragma unroll
+        for (int i = 0; i < V; ++i) closed |= (a[i] == -INFINITY ? 1u : 0u) << i;
+    if (whole) {
+        top = a[0];
+#pragma unroll
+        for (int i = 1; i < V; ++i) top = fmaxf(top, a[i]);
+        top = max_of_warp(top);
+        sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const float e = a[i] == -INFINITY ? 0.f : s.renormalise ? exp2_quick((a[i] - top) * kLog2e) : expf(a[i] - top);
+            if (kScored) a[i] = e;
+            sum += e;
+        }
+        sum = sum_of_warp(sum);
+    }
+    if (kScored) {
+        // exp(x) is known to 2 ulps and x log2(e) to 2 |x| 2^-24: times the exponential, or a sigmoid's slope, below 1.1 ulps
+        // of 1 more.  A sigmoid's sum and quotient add 1.5 ulps of it; a sum of exponentials, up to 2^-19 of it off, is that
+        // of all scores.
+        const float inv = s.sigmoid ? 1.f : reciprocal_quick(fmaxf(sum, 1.f));   // 1 and more, but where all are closed
+        error = s.sigmoid ? 0x1p-21f : 0x1p-18f * inv;
+        float b[V];
+        if (bias) load_lane<float, V>(bias + l.first, l.count, s.wide_bias, 0.f, b);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            a[i] = s.sigmoid ? reciprocal_quick(1.f + exp2_quick(a[i] * -kLog2e)) : a[i] * inv;
+            if (bias) a[i] += b[i];
         }
     }
-    if (__any_sync(kAll, again)) id = choose_again<T, V, kScored>(s, lane, row, bias, space);
+    // keys, sorted: the first one here, the others in shared memory
+    uint32_t key[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        odd = odd || a[i] != a[i];
+        if (kScored) a[i] = closed >> i & 1u ? -INFINITY : a[i];
+        key[i] = (open_key(kScored ? a[i] : a[i] + 0.f) & ~kPlace<V>) | (kPlace<V> - i);   // -0 is 0
+    }
+    sort_keys(key);
+    uint32_t head = key[0];
+#pragma unroll
+    for (int i = 1; i < V; ++i) space.list[i][lane] = key[i];
+    space.list[V][lane] = 0;
+
+    if (kScored && s.top_groups < s.groups) {
+        uint32_t first = head & ~kPlace<V>, second = V > 1 ? key[V > 1] & ~kPlace<V> : 0;
+        if (first < kOpen) first = 0;
+        if (second < kOpen) second = 0;
+        two_of_group(s, first, second);
+        // a group's value, the last bits its number, so that no two are alike and the lower one of equal ones is ahead
+        const uint32_t number = 32 / s.lanes - 1;
+        const float p = from_key<float>(first), q = s.group_top == 2 && second ? from_key<float>(second) : 0.f;
+        uint32_t left = first && l.group < s.groups ? (open_key(p + q + 0.f) & ~number) | (number - l.group) : 0, last = 0;
+        const float sizes = __uint_as_float(__reduce_max_sync(kAll, left ? __float_as_uint(fabsf(p) + fabsf(q)) : 0));
+        bool kept = false;
+        for (int r = 0; r < s.top_groups; ++r) {
+            last = __reduce_max_sync(kAll, left);
+            kept = kept || left == last;
+            left = left == last ? 0 : left;
+        }
+        const uint32_t out = __reduce_max_sync(kAll, left);
+        if (out && from_key<float>(last & ~number) - from_key<float>(out & ~number) <=
+                       4.f * error + 2.f * (kRelative<V> + (number + 1) * 0x1p-23f) * sizes) {
+            const unsigned mask = !s.sigmoid && bias ? 0 : groups_in_64_bits<T, V>(s, lane, row, bias, space, head, error);
+            odd = odd || mask == 0;
+            if (mask) kept = mask >> l.group & 1u;
+        }
+        if (!kept) head = 0;
+    }
+
+    // Rounds: the lowest lane of the largest key notes it and moves on, at most V times (its list ends in 0, which no round
+    // takes).  Closed keys are behind the open ones.  Then all that are near the last one may have to change places with it.
+    const uint32_t below = (1u << lane) - 1;
+    uint32_t last = 0, taken = (uint32_t)__cvta_generic_to_shared(space.taken), next = (uint32_t)__cvta_generic_to_shared(&space.list[1][lane]);
+    int n = 0;
+    auto round = [&](uint32_t best, uint32_t most) {   // predicated: a branch costs as much as the round
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t.reg .b32 of;\n\t"
+            "setp.eq.u32 p, %3, %4;\n\t"
+            "vote.sync.ballot.b32 of, p, 0xffffffff;\n\t"
+            "and.b32 of, of, %5;\n\t"
+            "setp.eq.and.u32 p, of, 0, p;\n\t"
+            "@p st.shared.v2.u32 [%2], {%0, %6};\n\t"
+            "@p ld.shared.u32 %0, [%1];\n\t"
+            "@p add.u32 %1, %1, 128;\n\t}"
+            : "+r"(head), "+r"(next)
+            : "r"(taken), "r"(best), "r"(most), "r"(below), "r"(lane)
+            : "memory");
+        taken += sizeof(uint2);
+    };
+#pragma unroll 1
+    for (; n < s.k; ++n) {
+        const uint32_t best = head & ~kPlace<V>, most = __reduce_max_sync(kAll, best);
+        if (most < kOpen) break;
+        last = most;
+        round(best, most);
+    }
+    if (!kExact<T, kScored> && n == s.k)
+        for (; n <= kRouteMaxK; ++n) {
+            const uint32_t best = head & ~kPlace<V>, most = __reduce_max_sync(kAll, best);
+            if (most < kOpen || !near_keys<V>(last, most, error)) break;
+            round(best, most);
+        }
+    __syncwarp();
+    int id = -1;
+    bool near = false;
+    if (lane < imin(n, s.k)) id = expert_of<V>(s, space.taken[lane]);
+    if (!kExact<T, kScored> && lane + 1 < n) {
+        const uint2 t = space.taken[lane], u = space.taken[lane + 1];
+        if (near_keys<V>(t.x, u.x, error)) {
+            const int e = expert_of<V>(s, t), f = expert_of<V>(s, u);   // two of one logit and bias are in their order
+            near = !(logit(row, e) == logit(row, f) && (!bias || __ldg(bias + e) == __ldg(bias + f)));
+        }
+    }
+    bool far = __any_sync(kAll, odd);
+    if (!kExact<T, kScored> && !far && __any_sync(kAll, near)) {
+        far = n > kRouteMaxK || (kScored && !s.sigmoid && bias);
+        if (!far) id = order_in_64_bits<T, V, kScored>(s, lane, row, bias, space, n);
+    }
+    if (far) id = choose_in_64_bits<T, V, kScored>(s, lane, row, bias);
+
     const bool held = id >= 0;
     const float zc = held ? logit(row, id) : -INFINITY;
     float w;
     if (s.renormalise) w = renormalised(s.sigmoid, held, zc, s.width);
-    else w = !held ? 0.f : s.sigmoid ? sigmoid_of(zc) : __fdividef(expf(zc - p.top), p.sum);
+    else w = !held ? 0.f : s.sigmoid ? sigmoid_of(zc) : __fdividef(expf(zc - top), sum);
     if (lane < s.k) {
-        const int64_t at = r0 * s.k + lane;
-        ids[at] = id;
-        weights[at] = held ? w * s.scale : 0.f;
+        const int64_t to = r0 * s.k + lane;
+        ids[to] = id;
+        weights[to] = held ? w * s.scale : 0.f;
     }
 }
 
