@@ -17,6 +17,12 @@ and "Tests").  Here that operator is a ``torch.library`` custom op:
   ``zs_gie::norm_gate_residual(h, x, gate, w_post, scale, w_pre, eps, kind) ->
   (y, u, stats)``: the norms around a block with its gate, residual scale and
   residual sum; differentiable in every tensor (``optim.AdamW`` steps them)
+  ``zs_gie::embedding(w, ids, scale) -> y``, ``zs_gie::route(logits, k, bias, ...)
+  -> (ids, weights)``, ``zs_gie::dispatch(x, row_ptr, perm, k) -> (xs, slot)``,
+  ``zs_gie::combine(h, slot, weights, row_ptr, perm) -> y`` and ``zs_gie::dropout(h,
+  p, seed, call, step, step_at, residual) -> y``: a block whose rows go to several
+  experts (``expert_block`` runs them together).  ``route`` and a weighted ``combine``
+  are differentiable once, the others, which are linear, as often as wanted
 
 ``zonal_scatter``'s backward is ``zs_gie::zonal_scatter_backward``, itself
 an operator without a derivative, so a second backward raises.  It takes the
@@ -356,3 +362,222 @@ def _backward_norm(ctx, dy, du, _):
 
 
 norm_gate_residual.register_autograd(_backward_norm, setup_context=_setup_context_norm)
+
+
+# ---------------------------------------------------------------------------
+# A block whose rows go to several experts.
+
+@torch.library.custom_op(f"{_NS}::embedding", mutates_args=())
+def embedding(w: torch.Tensor, ids: torch.Tensor, scale: float = 1.0) -> torch.Tensor:
+    """y[i] = scale * w[ids[i]]: w (V, C), ids (M,) int32 (zeros for ids outside [0, V)); y (M, C)."""
+    _cuda_only("embedding", w, ids)
+    return zs.zs_embedding(w.contiguous(), ids.contiguous(), scale)
+
+
+@embedding.register_fake
+def _(w, ids, scale=1.0):
+    return w.new_empty((ids.shape[0], w.shape[1]))
+
+
+@torch.library.custom_op(f"{_NS}::embedding_backward", mutates_args=())
+def embedding_backward(dy: torch.Tensor, ids: torch.Tensor, num: int, scale: float = 1.0) -> torch.Tensor:
+    """dw (num, C) for the cotangent dy (M, C): the CSR of the ids, then the sums of its rows."""
+    _cuda_only("embedding_backward", dy, ids)
+    row_ptr, perm, _ = zs.zs_build_csr(ids.contiguous(), num)
+    return zs.zs_embedding_backward(dy.contiguous(), row_ptr, perm, scale)
+
+
+@embedding_backward.register_fake
+def _(dy, ids, num, scale=1.0):
+    return dy.new_empty((num, dy.shape[1]))
+
+
+def _setup_context_embedding(ctx, inputs, output):
+    w, ids, ctx.scale = inputs
+    ctx.num = w.shape[0]
+    ctx.save_for_backward(ids)
+
+
+def _backward_embedding(ctx, dy):
+    return embedding_backward(dy, ctx.saved_tensors[0], ctx.num, ctx.scale), None, None
+
+
+def _setup_context_embedding_backward(ctx, inputs, output):
+    _, ids, _, ctx.scale = inputs
+    ctx.save_for_backward(ids)
+
+
+def _backward_embedding_backward(ctx, a):   # linear in dy
+    return embedding(a, ctx.saved_tensors[0], ctx.scale), None, None, None
+
+
+embedding.register_autograd(_backward_embedding, setup_context=_setup_context_embedding)
+embedding_backward.register_autograd(_backward_embedding_backward, setup_context=_setup_context_embedding_backward)
+
+
+@torch.library.custom_op(f"{_NS}::route", mutates_args=())
+def route(logits: torch.Tensor, k: int, bias: Optional[torch.Tensor] = None, score: str = "softmax", groups: int = 1,
+          top_groups: Optional[int] = None, group_top: int = 1, renormalise: bool = True,
+          scale: float = 1.0) -> tuple[torch.Tensor, torch.Tensor]:
+    """(ids (M, k) int32, weights (M, k) float32): the k experts of each row with the largest score + bias
+    among its best groups, and their weights, differentiable in the logits with the choice held fixed."""
+    _cuda_only("route", logits)
+    return zs.zs_route(logits.contiguous(), k, bias, score, groups, top_groups, group_top, renormalise, scale)
+
+
+@route.register_fake
+def _(logits, k, bias=None, score="softmax", groups=1, top_groups=None, group_top=1, renormalise=True, scale=1.0):
+    shape = (logits.shape[0], k)
+    return logits.new_empty(shape, dtype=torch.int32), logits.new_empty(shape, dtype=torch.float32)
+
+
+@torch.library.custom_op(f"{_NS}::route_backward", mutates_args=())
+def route_backward(dweights: torch.Tensor, logits: torch.Tensor, ids: torch.Tensor, score: str = "softmax",
+                   renormalise: bool = True, scale: float = 1.0) -> torch.Tensor:
+    """dlogits (M, E) for the cotangent dweights (M, k)."""
+    _cuda_only("route_backward", dweights, logits, ids)
+    return zs.zs_route_backward(dweights.contiguous(), logits.contiguous(), ids.contiguous(), score, renormalise, scale)
+
+
+@route_backward.register_fake
+def _(dweights, logits, ids, score="softmax", renormalise=True, scale=1.0):
+    return logits.new_empty(logits.shape)
+
+
+def _setup_context_route(ctx, inputs, output):
+    logits, _, _, ctx.score, _, _, _, ctx.renormalise, ctx.scale = inputs
+    ctx.mark_non_differentiable(output[0])
+    ctx.set_materialize_grads(False)
+    ctx.save_for_backward(logits, output[0])
+
+
+def _backward_route(ctx, _, dweights):
+    grad = None
+    if dweights is not None:
+        logits, ids = ctx.saved_tensors
+        grad = route_backward(dweights, logits, ids, ctx.score, ctx.renormalise, ctx.scale)
+    return (grad,) + (None,) * 8
+
+
+route.register_autograd(_backward_route, setup_context=_setup_context_route)
+
+
+@torch.library.custom_op(f"{_NS}::dispatch", mutates_args=())
+def dispatch(x: torch.Tensor, row_ptr: torch.Tensor, perm: torch.Tensor, k: int) -> tuple[torch.Tensor, torch.Tensor]:
+    """(xs (M k, C), slot (M, k)): the rows in the order of their experts, from the CSR of the flattened ids."""
+    _cuda_only("dispatch", x, row_ptr, perm)
+    return zs.zs_dispatch(x.contiguous(), row_ptr.contiguous(), perm.contiguous(), k)
+
+
+@dispatch.register_fake
+def _(x, row_ptr, perm, k):
+    return x.new_empty((x.shape[0] * k, x.shape[1])), x.new_empty((x.shape[0], k), dtype=torch.int32)
+
+
+@torch.library.custom_op(f"{_NS}::combine", mutates_args=())
+def combine(h: torch.Tensor, slot: torch.Tensor, weights: Optional[torch.Tensor], row_ptr: torch.Tensor,
+            perm: torch.Tensor) -> torch.Tensor:
+    """y (M, C): the sum over j of weights[i, j] h[slot[i, j]] (weights None: 1), for the CSR that dispatch was given."""
+    _cuda_only("combine", h, slot)
+    return zs.zs_combine(h.contiguous(), slot.contiguous(), None if weights is None else weights.contiguous())
+
+
+@combine.register_fake
+def _(h, slot, weights, row_ptr, perm):
+    return h.new_empty((slot.shape[0], h.shape[1]))
+
+
+@torch.library.custom_op(f"{_NS}::combine_backward", mutates_args=())
+def combine_backward(dy: torch.Tensor, h: torch.Tensor, slot: torch.Tensor, weights: torch.Tensor,
+                     row_ptr: torch.Tensor) -> tuple[torch.Tensor, torch.Tensor]:
+    """(dh (M k, C), dweights (M, k)) for the cotangent dy (M, C)."""
+    _cuda_only("combine_backward", dy, h, slot, weights, row_ptr)
+    return zs.zs_combine_backward(dy.contiguous(), h.contiguous(), slot.contiguous(), weights.contiguous(), row_ptr.contiguous())
+
+
+@combine_backward.register_fake
+def _(dy, h, slot, weights, row_ptr):
+    return h.new_empty(h.shape), weights.new_empty(weights.shape)
+
+
+def _setup_context_dispatch(ctx, inputs, output):
+    _, row_ptr, perm, _ = inputs
+    ctx.mark_non_differentiable(output[1])
+    ctx.set_materialize_grads(False)
+    ctx.save_for_backward(output[1], row_ptr, perm)
+
+
+def _backward_dispatch(ctx, dxs, _):
+    if dxs is None:
+        return (None,) * 4
+    slot, row_ptr, perm = ctx.saved_tensors
+    return combine(dxs, slot, None, row_ptr, perm), None, None, None
+
+
+def _setup_context_combine(ctx, inputs, output):
+    h, slot, weights, row_ptr, perm = inputs
+    ctx.weighted = weights is not None
+    ctx.save_for_backward(slot, row_ptr, perm, *((h, weights) if ctx.weighted else ()))
+
+
+def _backward_combine(ctx, dy):
+    slot, row_ptr, perm, *rest = ctx.saved_tensors
+    if not ctx.weighted:
+        return dispatch(dy, row_ptr, perm, slot.shape[1])[0], None, None, None, None
+    dh, dweights = combine_backward(dy, rest[0], slot, rest[1], row_ptr)
+    return dh, None, dweights, None, None
+
+
+dispatch.register_autograd(_backward_dispatch, setup_context=_setup_context_dispatch)
+combine.register_autograd(_backward_combine, setup_context=_setup_context_combine)
+
+
+@torch.library.custom_op(f"{_NS}::dropout", mutates_args=())
+def dropout(h: torch.Tensor, p: float, seed: int, call: int = 0, step: int = 0, step_at: Optional[torch.Tensor] = None,
+            residual: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """residual + dropout(h), by the counters (call, step): step a number, or with ``step_at`` one int64 element on
+    the device (step is 0 then), which may move on once the backward pass has run."""
+    _cuda_only("dropout", h)
+    if step_at is not None and step != 0:
+        raise ValueError("step and step_at are given")
+    return zs.zs_dropout(h.contiguous(), p, seed, call, step if step_at is None else step_at,
+                         None if residual is None else residual.contiguous())
+
+
+@dropout.register_fake
+def _(h, p, seed, call=0, step=0, step_at=None, residual=None):
+    return h.new_empty(h.shape)
+
+
+def _setup_context_dropout(ctx, inputs, output):
+    _, *ctx.counters, step_at, residual = inputs
+    ctx.residual = residual is not None
+    ctx.save_for_backward(*(() if step_at is None else (step_at,)))
+
+
+def _backward_dropout(ctx, dy):
+    step_at = ctx.saved_tensors[0] if ctx.saved_tensors else None
+    dh = dropout(dy, *ctx.counters, step_at) if ctx.needs_input_grad[0] else None
+    return dh, None, None, None, None, None, dy if ctx.residual else None
+
+
+dropout.register_autograd(_backward_dropout, setup_context=_setup_context_dropout)
+
+
+def species_embedding(species: torch.Tensor, w: torch.Tensor, scale: float = 1.0) -> torch.Tensor:
+    """y[i] = scale * w[species[i]], differentiable in w.  Rows whose species is outside [0, V) are zeros."""
+    return embedding(w, species, scale)
+
+
+def expert_block(x: torch.Tensor, logits: torch.Tensor, w_in: torch.Tensor, w_out: torch.Tensor, k: int,
+                 bias: Optional[torch.Tensor] = None, score: str = "softmax", groups: int = 1, top_groups: Optional[int] = None,
+                 group_top: int = 1, renormalise: bool = True, scale: float = 1.0,
+                 activation=torch.nn.functional.silu) -> torch.Tensor:
+    """A layer of experts: y[i] = the sum over the row's k experts e, by their weights, of
+    w_out[e] activation(w_in[e] x[i]).  x (M, C), logits (M, E), w_in (E, H, C), w_out (E, N, H); y (M, N),
+    differentiable in x, the logits and both weights."""
+    ids, weights = route(logits, k, bias, score, groups, top_groups, group_top, renormalise, scale)
+    row_ptr, perm = build_csr(ids.view(-1), w_in.shape[0])
+    xs, slot = dispatch(x, row_ptr, perm, k)
+    h = grouped_matmul(activation(grouped_matmul(xs, w_in, row_ptr)), w_out, row_ptr)
+    return combine(h, slot, weights, row_ptr, perm)
