@@ -2,7 +2,8 @@
 // CSR of the ids.
 //
 // Forward: y[i] = scale * w[ids[i]], one pass that writes M C elements and
-// reads the rows it needs (move_rows).
+// reads the rows it needs (move_rows).  Bound by what it writes: 647170 rows of
+// 96 floats of a table of 3 MB in 43 us, 5.8 TB/s.
 //
 // Gradient: dw[v] = scale * sum of dy[perm[j]] over the positions j of CSR row
 // v.  A row of dw is written once and a row of dy read once, both C elements,
@@ -12,11 +13,15 @@
 // and however many rows of the table have none.  A CTA takes one share of the
 // list and up to 256 pieces of the columns: it stages its part of row_ptr and
 // perm in shared memory, its threads (a share of the CTA's items and a piece
-// each) walk their items with eight loads in flight, and what is cut between
-// its threads is added up in shared memory.  What is cut between CTAs goes to
-// the workspace in fp32 and is added up by a second kernel in the CTAs' order.
-// All sums are in fp32 and in an order that follows from the sizes.
-
+// each) walk their items, six rows on their way while six are added, and what is
+// cut between its threads is added up in shared memory.  What is cut between
+// CTAs goes to the workspace in fp32 and is added up by a second kernel in the
+// CTAs' order.  All sums are in fp32 and in an order that follows from the sizes
+// and the ids.  As many CTAs as run at once: the search for a share's first row
+// and the staging take about 5 us, in which nothing else runs (24 CTAs an SM: 67
+// instead of 47 us).  Both kernels, 647170 rows of 96 floats, skewed over 7921
+// ids: 47 us, 5.4 TB/s; 16384 rows of 1024 bf16 and a table of 50021: 33 us, 4.2
+// TB/s, of which the join is about 4.
 #include "zs_rows.cuh"
 
 namespace zs {
@@ -45,7 +50,7 @@ zs_status embed_forward(const void* w, int64_t w_ld, int32_t V, const int32_t* i
 // ------------------------------------------------------------------ gradient
 
 constexpr int kSumThreads = 256;
-constexpr int kSumBatch = 6;         // rows of dy in flight for a thread
+constexpr int kSumBatch = 6;         // rows of dy that a thread loads at a time
 constexpr int kSumItems = 4096;      // most items of a CTA (staged in shared memory)
 constexpr int kSumCtas = 3;          // CTAs an SM that the shares are made for: as many as run at once
 
@@ -106,10 +111,10 @@ __device__ __forceinline__ int rows_before(const int32_t* row_ptr, int32_t V, in
 }
 
 template <typename T, bool kWhole>
-__global__ void __launch_bounds__(kSumThreads, kSumCtas) sum_rows(SumShape s, Rows<T> dy,
-                                                        const int32_t* __restrict__ row_ptr, const int32_t* __restrict__ perm,
-                                                        float scale, T* __restrict__ dw, float* __restrict__ head,
-                                                        float* __restrict__ tail, SumNote* __restrict__ notes) {
+__global__ void __launch_bounds__(kSumThreads, kSumCtas) sum_rows(SumShape s, Rows<T> dy, const int32_t* __restrict__ row_ptr,
+                                                                  const int32_t* __restrict__ perm, float scale, T* __restrict__ dw,
+                                                                  float* __restrict__ head, float* __restrict__ tail,
+                                                                  SumNote* __restrict__ notes) {
     using R = Row<T, kWhole>;
     constexpr int VEC = R::N;
     __shared__ int32_t staged[kSumItems + 8];        // row_ptr[v0 .. v1 + 1], then perm[j0 .. j1)

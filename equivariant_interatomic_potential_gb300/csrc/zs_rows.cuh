@@ -6,9 +6,9 @@
 // are the row's own.  Elsewhere (odd widths, views at odd offsets) each row of
 // the result has its own phase: its first and last piece are written element by
 // element, and a piece is read from another row's phase as two aligned 16-byte
-// words that are shifted together (fp16 rows of 301, 64 MB: 94 us by elements,
-// see zs_experts.cu for what is left of it).  Pieces of several rows are numbered
-// together, so that a CTA's threads are all busy whatever the width.
+// words that are shifted together (fp16 rows of 301 dispatched, 64 MB: 94 us
+// element by element, 35 so).  Pieces of several rows are numbered together, so
+// that a CTA's threads are all busy whatever the width.
 #pragma once
 
 #include <initializer_list>
