@@ -51,6 +51,7 @@ zs_status embed_forward(const void* w, int64_t w_ld, int32_t V, const int32_t* i
 
 constexpr int kSumThreads = 256;
 constexpr int kSumBatch = 6;         // rows of dy that a thread loads at a time
+constexpr int kSumMaxC = 1 << 23;    // columns (of the grids)
 constexpr int kSumItems = 4096;      // most items of a CTA (staged in shared memory)
 constexpr int kSumCtas = 3;          // CTAs an SM that the shares are made for: as many as run at once
 
@@ -378,7 +379,7 @@ zs_status zs_embedding(int32_t dtype, const void* w, int64_t w_ld, const int32_t
 
 size_t zs_embedding_backward_workspace_bytes(int32_t dtype, int64_t M, int32_t V, int32_t C) {
     using namespace zs;
-    if (!known_dtype(dtype) || M < 0 || V < 1 || C < 1 || M > kMaxRows || V > kMaxRows || C > kMaxRows) return 0;
+    if (!known_dtype(dtype) || M < 0 || V < 1 || C < 1 || M > kMaxRows || V > kMaxRows || C > kSumMaxC) return 0;
     return sum_workspace(sum_shape(M, V, C, 16 / dtype_bytes(dtype)));
 }
 
@@ -388,6 +389,7 @@ zs_status zs_embedding_backward(int32_t dtype, const void* dy, int64_t dy_ld, co
     using namespace zs;
     const char* fn = "zs_embedding_backward";
     if (zs_status st = check(fn, dtype, M, V, C, scale)) return st;
+    if (C > kSumMaxC) return fail(ZS_ERR_UNSUPPORTED, "%s: C=%d is above %d", fn, C, kSumMaxC);
     if (V == 0) return ZS_OK;
     if (zs_status st = check_rows(fn, "dy", dtype, dy, dy_ld, M, C)) return st;
     if (zs_status st = check_rows(fn, "dw", dtype, dw, C, V, C)) return st;

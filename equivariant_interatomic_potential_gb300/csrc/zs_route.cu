@@ -21,8 +21,8 @@
 //
 // What bounds it: instructions.  A row of 256 experts takes about 320 and 25 for
 // each choice, sigmoids and a bias 140 more, groups 160: 32768 rows, 8 choices, 4
-// of 8 groups: 33 us where the bytes are 5.  At 24 warps of 40 registers an SM
-// and more it issues in three of four cycles.  An unsorted lane (rounds that look
+// of 8 groups: 33 us where the bytes are 5.  With 48 warps of 40 registers an SM
+// it issues in three of four cycles.  An unsorted lane (rounds that look
 // at all V keys) took 77 us, several rows a warp 45 (too few CTAs to even out).
 #include "zs_types.cuh"
 
@@ -155,24 +155,17 @@ __device__ __forceinline__ double score_in_64_bits(const RouteShape& s, double z
     return bias ? a + (double)__ldg(bias + e) : a;
 }
 
-// Whether a lane's group is among the best, by the values that the lanes of `speaks` hold of theirs: NaN above all, equal
-// ones by their number.
-__device__ __forceinline__ bool group_in_64_bits(const RouteShape& s, int group, bool speaks, double value) {
-    unsigned speakers = __ballot_sync(kAll, speaks && group < s.groups);
-    const unsigned long long mine = to_key<double>(value);
-    unsigned long long own = 0;
-    for (unsigned m = speakers; m; m &= m - 1) {   // each lane's group's own value
-        const int j = __ffs(m) - 1;
-        const unsigned long long v = __shfl_sync(kAll, mine, j);
-        if (__shfl_sync(kAll, group, j) == group) own = v;
-    }
+// The `need` groups of the mask `groups` with the largest values, as a mask: lane g holds group g's.  NaN are above all,
+// equal ones go by their number.
+__device__ __forceinline__ unsigned best_groups(unsigned groups, int need, int lane, double value) {
+    const unsigned long long own = to_key<double>(value);
     int ahead = 0;
-    for (unsigned m = speakers; m; m &= m - 1) {
-        const int j = __ffs(m) - 1, g = __shfl_sync(kAll, group, j);
-        const unsigned long long v = __shfl_sync(kAll, mine, j);
-        ahead += v > own || (v == own && g < group);
+    for (unsigned m = groups; m; m &= m - 1) {
+        const int g = __ffs(m) - 1;
+        const unsigned long long v = __shfl_sync(kAll, own, g);
+        ahead += v > own || (v == own && g < lane);
     }
-    return group < s.groups && ahead < s.top_groups;
+    return __ballot_sync(kAll, (groups >> lane & 1u) && ahead < need);
 }
 
 // The row's choice in 64 bits: the expert of choice `lane` (or -1).
@@ -208,7 +201,9 @@ __device__ __noinline__ int choose_in_64_bits(const RouteShape& s, int lane, con
         two_of_group(s, first, second);
         double value = -INFINITY;
         if (first) value = from_key<double>(first) + (s.group_top == 2 && second ? from_key<double>(second) : 0.0);
-        if (!group_in_64_bits(s, l.group, l.group << s.lane_bits == lane, value))
+        value = __shfl_sync(kAll, value, (lane << s.lane_bits) & 31);   // lane g: group g's
+        const unsigned kept = best_groups(s.groups == 32 ? kAll : (1u << s.groups) - 1, s.top_groups, lane, value);
+        if (!(kept >> l.group & 1u))
             for (int i = 0; i < V; ++i) key[i] = 0;
     }
     int mine = -1;
@@ -295,29 +290,41 @@ __device__ __forceinline__ bool near_keys(uint32_t a, uint32_t b, float error) {
     return p - q <= 2.f * error + kRelative<V> * (fabsf(p) + fabsf(q)) + V * 0x1p-148f;
 }
 
-// The groups of a row whose choice 32 bits do not tell, as a mask: the elements of each that may be among its two
-// largest, in 64 bits, a lane each.  0 where they are too many.  `head` is a lane's first key.
+// Of the groups of the mask `border`, between which 32 bits do not tell, the `need` best as a mask: the elements of each
+// that may be among its two largest, in 64 bits, a lane each; groups of nothing but one logit and bias (a router that has
+// learnt nothing) by their numbers.  0 where there are too many, or a softmax has a bias.  `head` is a lane's first key.
 template <typename T, int V>
-__device__ __noinline__ unsigned groups_in_64_bits(const RouteShape& s, int lane, const T* __restrict__ row, const float* __restrict__ bias,
-                                                   RouteSpace<V>& space, uint32_t head, float error) {
+__device__ __noinline__ unsigned border_groups(const RouteShape& s, int lane, const T* __restrict__ row, const float* __restrict__ bias,
+                                               RouteSpace<V>& space, uint32_t head, float error, unsigned border, int need) {
     const Lane l(s, lane);
     uint32_t first = head & ~kPlace<V>, second = V > 1 ? space.list[1][lane] & ~kPlace<V> : 0;
     if (first < kOpen) first = 0;
     if (second < kOpen) second = 0;
     two_of_group(s, first, second);
     const uint32_t of = s.group_top == 2 ? second : first;   // what a group's candidates are near to, or above
-    int n = 0;
+    int n = 0, mine = 0;                                     // candidates, and how many are this lane's first keys
     for (int i = 0; i < V; ++i) {
         const uint32_t key = i == 0 ? head : space.list[i][lane];
-        const bool in = l.group < s.groups && key >= kOpen && ((key & ~kPlace<V>) >= of || near_keys<V>(of, key, error));
+        const bool in = (border >> l.group & 1u) && key >= kOpen && ((key & ~kPlace<V>) >= of || near_keys<V>(of, key, error));
         const unsigned all = __ballot_sync(kAll, in);
         if (!all) break;   // a lane's keys descend
         const int at = n + __popc(all & ((1u << lane) - 1));
         if (in && at < 32) space.taken[at] = make_uint2(key, lane);
+        mine += in;
         n += __popc(all);
     }
     __syncwarp();
-    if (n > 32) return 0;
+    if (n > 32 || (!s.sigmoid && bias)) {
+        const int e = expert_of<V>(s, space.taken[0]);
+        const float z = logit(row, e), b = bias ? __ldg(bias + e) : 0.f;
+        bool alike = true;
+        for (int i = 0; i < mine; ++i) {
+            const int f = expert_of<V>(s, make_uint2(i == 0 ? head : space.list[i][lane], lane));
+            alike = alike && logit(row, f) == z && (!bias || __ldg(bias + f) == b);
+        }
+        __syncwarp();
+        return __all_sync(kAll, alike) ? best_groups(border, need, lane, 0.0) : 0;
+    }
     const int e = lane < n ? expert_of<V>(s, space.taken[lane]) : 0, group = lane < n ? e / s.per : -1;
     double a = lane < n ? (double)logit(row, e) : -INFINITY, top = 0.0;
     if (!s.sigmoid) {   // sums of a softmax's scores sort like those of its exponentials
@@ -332,24 +339,18 @@ __device__ __noinline__ unsigned groups_in_64_bits(const RouteShape& s, int lane
         two = other > one ? one : fmax(two, other);
         one = fmax(one, other);
     }
-    const double value = s.group_top == 2 && two != -INFINITY ? one + two : one;
-    const unsigned mask = __ballot_sync(kAll, group_in_64_bits(s, lane, lane < s.groups, value));
     __syncwarp();
-    return mask;
+    return best_groups(border, need, lane, s.group_top == 2 && two != -INFINITY ? one + two : one);
 }
 
-// The order of the n candidates that the rounds took, by their scores in 64 bits (or by logits, which sort like a
-// softmax's scores without a bias): a lane each, by how many are ahead.  The expert of choice `lane` (or -1).
+// The order of the n candidates that the rounds took, by what the choice goes by in 64 bits (a softmax's scores, without a
+// bias, by their exponentials): a lane each, by how many are ahead.  The expert of choice `lane` (or -1).
 template <typename T, int V, bool kScored>
 __device__ __noinline__ int order_in_64_bits(const RouteShape& s, int lane, const T* __restrict__ row, const float* __restrict__ bias,
-                                             RouteSpace<V>& space, int n) {
+                                             RouteSpace<V>& space, int n, float top) {
     const bool open = lane < n;
     const int e = open ? expert_of<V>(s, space.taken[lane]) : -1;
-    double a = -INFINITY;
-    if (open) {
-        a = logit(row, e);
-        if (kScored && s.sigmoid) a = score_in_64_bits<kScored>(s, a, 0.0, 0.0, bias, e);
-    }
+    const double a = open ? score_in_64_bits<kScored>(s, logit(row, e), top, 1.0, bias, e) : -INFINITY;
     int ahead = 0;
     for (int j = 0; j < n; ++j) {
         const double other = __shfl_sync(kAll, a, j);
@@ -434,8 +435,9 @@ __global__ void __launch_bounds__(kRouteWarps * 32, V <= 8 ? 12 : V <= 16 ? 8 : 
         // a group's value, the last bits its number, so that no two are alike and the lower one of equal ones is ahead
         const uint32_t number = 32 / s.lanes - 1;
         const float p = from_key<float>(first), q = s.group_top == 2 && second ? from_key<float>(second) : 0.f;
-        uint32_t left = first && l.group < s.groups ? (open_key(p + q + 0.f) & ~number) | (number - l.group) : 0, last = 0;
-        const float sizes = __uint_as_float(__reduce_max_sync(kAll, left ? __float_as_uint(fabsf(p) + fabsf(q)) : 0));
+        const uint32_t value = first && l.group < s.groups ? (open_key(p + q + 0.f) & ~number) | (number - l.group) : 0;
+        const float sizes = __uint_as_float(__reduce_max_sync(kAll, value ? __float_as_uint(fabsf(p) + fabsf(q)) : 0));
+        uint32_t left = value, last = 0;
         bool kept = false;
         for (int r = 0; r < s.top_groups; ++r) {
             last = __reduce_max_sync(kAll, left);
@@ -443,11 +445,21 @@ __global__ void __launch_bounds__(kRouteWarps * 32, V <= 8 ? 12 : V <= 16 ? 8 : 
             left = left == last ? 0 : left;
         }
         const uint32_t out = __reduce_max_sync(kAll, left);
-        if (out && from_key<float>(last & ~number) - from_key<float>(out & ~number) <=
-                       4.f * error + 2.f * (kRelative<V> + (number + 1) * 0x1p-23f) * sizes) {
-            const unsigned mask = !s.sigmoid && bias ? 0 : groups_in_64_bits<T, V>(s, lane, row, bias, space, head, error);
+        const float in_value = from_key<float>(last & ~number), out_value = from_key<float>(out & ~number);
+        const float known = 4.f * error + 2.f * (kRelative<V> + (number + 1) * 0x1p-23f) * sizes;
+        if (out && in_value - out_value <= known) {
+            // those that are above all that are out, or below all that are in, stay where they are
+            const float v = from_key<float>(value & ~number);
+            const bool speaks = value && lane == l.group << s.lane_bits;
+            const bool at_border = speaks && !(v > out_value + known) && !(v < in_value - known);
+            unsigned border = 0, sure = 0;   // by the groups' numbers
+            for (int g = 0; g < s.groups; ++g) {
+                border |= (unsigned)__shfl_sync(kAll, (int)at_border, g << s.lane_bits) << g;
+                sure |= (unsigned)__shfl_sync(kAll, (int)(kept && speaks && !at_border), g << s.lane_bits) << g;
+            }
+            const unsigned mask = border_groups<T, V>(s, lane, row, bias, space, head, error, border, s.top_groups - __popc(sure));
             odd = odd || mask == 0;
-            if (mask) kept = mask >> l.group & 1u;
+            if (mask) kept = (mask | sure) >> l.group & 1u;
         }
         if (!kept) head = 0;
     }
@@ -499,7 +511,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32, V <= 8 ? 12 : V <= 16 ? 8 : 
     bool far = __any_sync(kAll, odd);
     if (!kExact<T, kScored> && !far && __any_sync(kAll, near)) {
         far = n > kRouteMaxK || (kScored && !s.sigmoid && bias);
-        if (!far) id = order_in_64_bits<T, V, kScored>(s, lane, row, bias, space, n);
+        if (!far) id = order_in_64_bits<T, V, kScored>(s, lane, row, bias, space, n, top);
     }
     if (far) id = choose_in_64_bits<T, V, kScored>(s, lane, row, bias);
 

@@ -564,7 +564,8 @@ ZS_API zs_status zs_embedding(int32_t dtype, const void* w, int64_t w_ld, const 
  *              row has)
  *   workspace  zs_embedding_backward_workspace_bytes(dtype, M, V, C) bytes,
  *              256-byte aligned
- * Sums are in fp32, in an order that follows from the sizes.
+ * Sums are in fp32, in an order that follows from the sizes and the CSR.
+ * ZS_ERR_UNSUPPORTED for C above 2^23.
  */
 ZS_API size_t zs_embedding_backward_workspace_bytes(int32_t dtype, int64_t M, int32_t V, int32_t C);
 ZS_API zs_status zs_embedding_backward(int32_t dtype, const void* dy, int64_t dy_ld, const int32_t* row_ptr,

@@ -188,7 +188,7 @@ def test_argument_checks():
         return lib.zs_embedding_backward(a["dtype"], a["w"], a["ld"], a["ids"], a["ids"], a["M"], a["V"], a["C"], a["scale"], a["y"], a["ws"],
                                          a["bytes"], None)
 
-    assert bwd(dtype=-1) == UNSUPPORTED
+    assert bwd(dtype=-1) == UNSUPPORTED and bwd(C=(1 << 23) + 1, ld=1 << 24) == UNSUPPORTED
     for kw in (dict(M=-1), dict(C=-4), dict(w=None), dict(ids=None), dict(y=None), dict(ld=3), dict(ws=None), dict(bytes=need - 1),
                dict(ws=FAKE + 8), dict(y=FAKE + 2), dict(scale=float("nan"))):
         assert bwd(**kw) == INVALID, kw

@@ -115,6 +115,28 @@ def test_scores_closer_than_32_bits(score):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,k,groups,top_groups", [(256, 8, 8, 4), (1024, 8, 32, 5), (96, 4, 32, 4), (40, 3, 20, 9)])
+def test_groups_that_are_alike(score, E, k, groups, top_groups):
+    """Rows of one logit (a router that has learnt nothing), with a few that stand out, and groups that are alike but for
+    one logit's last bit: the border goes by the groups' numbers, or by what only 64 bits tell."""
+    rng = np.random.default_rng(16)
+    M, per = 64, E // groups
+    z = np.zeros((M, E), np.float32)
+    for i in range(M):
+        stand_out = rng.permutation(groups)[: i % top_groups]
+        z[i, stand_out * per] = 1.0                                            # some groups are in for sure
+        if i % 3 == 0:
+            z[i] += np.tile((np.arange(per) * 0.01).astype(np.float32), groups)     # groups alike, experts not
+        if i % 5 == 0:
+            at = rng.permutation(groups)[: groups // 2] * per + per - 1
+            z[i, at] = np.nextafter(z[i, at], np.float32(2))
+    for bias in (None, np.zeros(E, np.float32), np.tile((rng.standard_normal(per) * 0.01).astype(np.float32), groups)):
+        for group_top in (1, 2):
+            check(torch.from_numpy(z).cuda(), z.astype(np.float64), k, bias, score, groups, top_groups, group_top, True, 1.0, "f32", rng)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("renormalise", [True, False])
 def test_far_logits(renormalise):
     # logits whose scores leave fp32's range: renormalised weights are ratios all the same
