@@ -9,6 +9,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -61,7 +62,7 @@ bool is_matrix(const at::Tensor* t, at::ScalarType type, int64_t rows, int64_t c
     return t && t->scalar_type() == type && t->dim() == 2 && t->size(0) == rows && t->size(1) == cols;
 }
 at::Tensor make(at::IntArrayRef shape, const at::Tensor& like, at::ScalarType type) {
-    return at::empty(shape, like.options().dtype(type));
+    return at::Tensor(at::detail::empty_cuda(shape, type, like.device(), std::nullopt));   // half the time of at::empty
 }
 zs_stream_t stream() { return reinterpret_cast<zs_stream_t>(c10::cuda::getCurrentCUDAStream().stream()); }
 PyObject* not_here() { Py_RETURN_NOTIMPLEMENTED; }
