@@ -350,9 +350,43 @@ __device__ __forceinline__ int32_t clamp_key(int32_t k, int32_t N) { return (uin
 // are found by claim and verify: every lane writes its lane id into bits
 // 10..14 of its key's counter (count < 1024 stays in bits 0..9), reads the
 // slot back, and lanes that lost the claim are grouped with the winner by
-// one ballot per contested key.  Uncontested rounds cost no ballot loop.
+// one ballot per contested key.  Uncontested rounds cost no ballot loop.  Of
+// few keys (species, experts) most lanes are contested: there the lanes of a key
+// are found by one ballot for each of its bits instead (up to kFewKeyBits of
+// them; 4096 edges, 89 skewed keys: the whole build 7.8 -> 6.4 us; with nine, 256
+// keys, no gain).
+constexpr int kFewKeyBits = 8;
+__device__ __forceinline__ void rank_few_keys(uint32_t* packed, uint16_t* wcnt, int rounds, int n, int32_t N, int warp, int lane) {
+    const unsigned lt = lanemask_lt();
+    const int TW = rounds * 32, bits = 32 - __clz(N);
+    for (int r = 0; r < rounds; ++r) {
+        const int i = warp * TW + r * 32 + lane;
+        const bool valid = i < n;
+        const int key = valid ? clamp_key((int32_t)packed[i], N) : 0;
+        unsigned peers = __ballot_sync(0xffffffffu, valid);
+#pragma unroll
+        for (int b = 0; b < kFewKeyBits; ++b) {
+            if (b >= bits) break;
+            const bool bit = (key >> b) & 1;
+            const unsigned bal = __ballot_sync(0xffffffffu, bit);
+            peers &= bit ? bal : ~bal;
+        }
+        const uint32_t before = valid ? wcnt[key] : 0u;
+        __syncwarp();
+        if (valid) {
+            if ((peers & lt) == 0) wcnt[key] = (uint16_t)(before + __popc(peers));
+            packed[i] = ((uint32_t)key << 16) | (before + __popc(peers & lt));
+        }
+        __syncwarp();
+    }
+}
+
 __device__ __forceinline__ void rank_in_warp(uint32_t* packed, uint16_t* wcnt, int rounds, int n, int32_t N, int warp,
                                              int lane) {
+    if (N >> kFewKeyBits == 0) {
+        rank_few_keys(packed, wcnt, rounds, n, N, warp, lane);
+        return;
+    }
     const unsigned lt = lanemask_lt();
     const int TW = rounds * 32;
     for (int r = 0; r < rounds; ++r) {
@@ -597,7 +631,7 @@ csr_count_scatter(const int32_t* __restrict__ dst, const uint16_t* __restrict__ 
 // path in one CTA and one launch -- csr_count_rank's ranking and counts, then
 // csr_count_scatter's node bases and scatter, the counts staying in shared
 // memory (with one tile, every edge's offset within its key is its rank).
-constexpr int kSingleMaxEdges = kCntMaxRounds * kCntThreads;
+constexpr int kSingleMaxEdges = 8 * kCntThreads;   // 4096: 6.4 to 7.8 us; 8192 edges took 9.4 to 15, 6 in three launches
 inline int count_single_smem(int nkeys, int rounds) {
     return count_rank_smem(nkeys, rounds) + 2 * count_pairs(nkeys) * 4;
 }
