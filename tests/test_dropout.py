@@ -53,6 +53,18 @@ def test_against_the_formula(M, C, dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_many_elements(dtype):
+    # more blocks than a thread each has room for, the last one short
+    M, C = 3001, 2049
+    rng = np.random.default_rng(5)
+    (h, hd), (r, rd) = (held(rng.standard_normal((M, C)), dtype) for _ in range(2))
+    h, r = h.cuda(), r.cuda()
+    check(zs.zs_dropout(h, 0.1, 99, 1, 2), hd, None, 0.1, 99, 1, 2, dtype)
+    check(zs.zs_dropout(h, 0.1, 99, 1, 2, residual=r, out=h), hd, rd, 0.1, 99, 1, 2, dtype)
+
+
+@pytest.mark.gpu
 def test_other_seeds_and_signs():
     h = torch.ones(64, 64, device="cuda")
     for seed in (-1, 2 ** 64 - 1, 1 << 63):

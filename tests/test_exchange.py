@@ -74,6 +74,14 @@ def test_there_and_back(M, k, E, C, dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("M,k,E,C", [(3000, 8, 64, 256), (5001, 2, 16, 600), (9000, 4, 300, 129)])
+def test_more_than_the_small_calls(M, k, E, C, dtype):
+    # rows of xs of 8 MB and more: x is read once for all of a row's choices
+    check(*draw(M, k, E, C, dtype, M, 0.1), dtype)
+
+
+@pytest.mark.gpu
 def test_no_rows():
     none = torch.zeros(0, dtype=torch.int32, device="cuda")
     row_ptr, perm, _ = zs.zs_build_csr(none, 4)

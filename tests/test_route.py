@@ -186,6 +186,11 @@ def test_nan_is_the_largest(bias):
     z[6, 1] = float("inf")
     ids, w = zs.zs_route(z, 5, b, "sigmoid", renormalise=False)
     assert int(ids[6, 0]) == 1 and float(w[6, 0]) == 1.0
+    half = torch.randn(9, 40, device="cuda").bfloat16()    # 16-bit logits, whose keys are exact
+    half[3, 17], half[5] = float("nan"), float("nan")
+    ids, w = zs.zs_route(half, 5, b, "sigmoid")
+    assert int(ids[3, 0]) == 17 and ids[5].tolist() == [0, 1, 2, 3, 4] and bool(torch.isnan(w[[3, 5]]).all())
+    assert not bool(torch.isnan(w[[0, 1, 2, 4, 6, 7, 8]]).any())
     for score in ("softmax", "sigmoid"):           # ids stay those of experts, each once
         ids, _ = zs.zs_route(z, 5, b, score, 4, 2, 2)
         assert bool(((ids >= 0) & (ids < 40)).all()) and all(len(set(r)) == 5 for r in ids.tolist())
