@@ -134,6 +134,7 @@ __global__ void __launch_bounds__(kSumThreads, kSumCtas) sum_rows(SumShape s, Ro
     const int64_t d0 = blockIdx.x * share, d1 = imin(d0 + share, s.items);
     pdl_wait();
     pdl_trigger();
+    const int32_t held = __ldg(row_ptr + s.V);       // positions of some id: those behind are not read
     if (gridDim.x == 1) {
         if (tid == 0) bound[0] = 0, bound[1] = s.V;
     } else {
@@ -146,7 +147,7 @@ __global__ void __launch_bounds__(kSumThreads, kSumCtas) sum_rows(SumShape s, Ro
     // v1 - v0 rows end here and one more may be open: v1 - v0 + 2 bounds, and j1 - j0 positions, together at most the
     // share and two (and no more than fits, whatever row_ptr holds)
     const int rows = imax(imin(v1 - v0, kSumItems), 0), bounds = rows + 2;
-    const int count = (int)imin<int64_t>(j1 - j0, kSumItems + 8 - bounds);
+    const int count = (int)imax<int64_t>(imin<int64_t>(imin<int64_t>(j1, held) - j0, kSumItems + 8 - bounds), 0);
     for (int i = tid; i < bounds; i += kSumThreads) staged[i] = v0 + i <= s.V ? __ldg(row_ptr + v0 + i) : (int32_t)s.M;
     int32_t* sperm = staged + bounds;
     for (int i = tid; i < count; i += kSumThreads) sperm[i] = __ldg(perm + j0 + i);
