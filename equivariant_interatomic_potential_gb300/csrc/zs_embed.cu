@@ -192,7 +192,7 @@ __global__ void __launch_bounds__(kSumThreads, kSumCtas) sum_rows(SumShape s, Ro
                 float f[VEC];
 #pragma unroll
                 for (int i = 0; i < VEC; ++i) f[i] = acc[i] * scale;
-                R::template store<true>(dw + (int64_t)(v0 + r) * s.C, e, s.C, pack<T>(f));
+                R::template store<true, false>(dw + (int64_t)(v0 + r) * s.C, e, s.C, pack<T>(f));
             }
 #pragma unroll
             for (int i = 0; i < VEC; ++i) acc[i] = 0.f;
@@ -250,7 +250,7 @@ __global__ void __launch_bounds__(kSumThreads, kSumCtas) sum_rows(SumShape s, Ro
         if ((int64_t)staged[begun_row] + v0 + begun_row >= d0) {   // begun in this CTA
 #pragma unroll
             for (int i = 0; i < VEC; ++i) sum[i] *= scale;
-            R::template store<true>(dw + (int64_t)(v0 + begun_row) * s.C, e, s.C, pack<T>(sum));
+            R::template store<true, false>(dw + (int64_t)(v0 + begun_row) * s.C, e, s.C, pack<T>(sum));
         } else {
 #pragma unroll
             for (int i = 0; i < VEC; ++i)

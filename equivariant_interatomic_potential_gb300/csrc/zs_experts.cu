@@ -101,12 +101,12 @@ zs_status dispatch(const void* x, int64_t x_ld, const int32_t* row_ptr, const in
     return check_launch("dispatch");
 }
 
-// U pieces of a thread at a time and KJ choices of each: four or eight loads in flight and four or five CTAs an SM.  More
+// U pieces of a thread at a time and KJ choices of each: four or eight loads in flight and three to five CTAs an SM.  More
 // loads and fewer CTAs are slower (8 choices of 1024 bf16, 32768 rows: 106 us at 3 CTAs, 97 at 4; 2 choices of 256, 256 MB:
 // 8 loads at 3 CTAs 111, 4 at 5 84), staging slots in shared memory too (115 to 188): the read of rows in any order is the
 // limit, 0.93 of the copy rate.
 template <typename T, bool kWhole, int KJ, int U>
-__global__ void __launch_bounds__(kMoveThreads, (KJ == kChoices ? 4 : 5) - !kWhole) combine_rows(
+__global__ void __launch_bounds__(kMoveThreads, KJ == kChoices ? (kWhole ? 4 : 3) : 5) combine_rows(
     MoveShape s, int32_t k, int32_t R, Rows<T> h, const int32_t* __restrict__ slot, const float* __restrict__ weights, T* __restrict__ y,
     int64_t y_ld) {
     using Rw = Row<T, kWhole>;
@@ -168,22 +168,41 @@ zs_status combine(const void* h, int64_t h_ld, const int32_t* slot, const float*
     return check_launch("combine");
 }
 
-// `lanes` threads (a power of two) for a row i of dy, which they read once for its k choices: their rows of h in flight
-// together, the products with dy in fp32 registers until the row's end.  Where phases differ, dy is shifted to each slot's
-// (from L1), fewer rows at a time and more CTAs an SM (fp16, 3 choices of 301, 256 MB: 515 us at 4 rows and 2 CTAs, 378 at
-// 1 and 5).  Whole pieces: memory, 32768 rows, 8 choices of 1024 bf16: 176 us, 0.95 of the copy rate.
+// The sums of the `lanes` threads (a power of two) of a row, at its first one.
 constexpr int kBackThreads = 256;
-template <typename T, bool kWhole, int KJ>
-__global__ void __launch_bounds__(kBackThreads, kWhole ? 3 : KJ == kChoices ? 4 : 5) combine_rows_backward(
-    int64_t M, int32_t k, int32_t R, int32_t P, int32_t C, int lanes, Rows<T> dy, Rows<T> h, const int32_t* __restrict__ slot,
+template <int KJ>
+__device__ __forceinline__ void sum_of_row(float (&dot)[KJ], int lanes, int lane, float (*part)[KJ]) {
+#pragma unroll
+    for (int j = 0; j < KJ; ++j)
+        for (int o = imin(lanes, 32) >> 1; o > 0; o >>= 1) dot[j] += __shfl_xor_sync(0xffffffffu, dot[j], o);
+    if (lanes > 32) {
+        const int warp = threadIdx.x >> 5;
+        if ((threadIdx.x & 31) == 0)
+#pragma unroll
+            for (int j = 0; j < KJ; ++j) part[warp][j] = dot[j];
+        __syncthreads();
+        if (lane == 0)
+#pragma unroll
+            for (int j = 0; j < KJ; ++j)
+                for (int q = 1; q < lanes / 32; ++q) dot[j] += part[warp + q][j];
+        __syncthreads();
+    }
+}
+
+// `lanes` threads for a row i of dy, which they read once for its k choices: their rows of h in flight together, the
+// products with dy in fp32 registers until the row's end.  Memory: 32768 rows, 8 choices of 1024 bf16: 176 us, 0.95 of the
+// copy rate.
+template <typename T, int KJ>
+__global__ void __launch_bounds__(kBackThreads, 3) combine_rows_backward(
+    int64_t M, int32_t k, int32_t R, int32_t P, int32_t C, int lane_bits, Rows<T> dy, Rows<T> h, const int32_t* __restrict__ slot,
     const float* __restrict__ weights, const int32_t* __restrict__ end, T* __restrict__ dh, float* __restrict__ dweights) {
-    using Rw = Row<T, kWhole>;
-    constexpr int N = Rw::N, kBatch = kWhole ? KJ : KJ == kChoices ? 2 : 1;
+    using Rw = Row<T, true>;
+    constexpr int N = Rw::N;
     __shared__ float part[kBackThreads / 32][KJ];
     pdl_wait();
     pdl_trigger();
-    const int group = threadIdx.x / lanes, lane = threadIdx.x - group * lanes;
-    const int64_t i = (int64_t)blockIdx.x * (kBackThreads / lanes) + group;
+    const int lanes = 1 << lane_bits, lane = threadIdx.x & (lanes - 1);
+    const int64_t i = (int64_t)blockIdx.x * (kBackThreads >> lane_bits) + (threadIdx.x >> lane_bits);
     const bool live = i < M;
     for (int j0 = 0; j0 < k; j0 += KJ) {
         float dot[KJ] = {}, w[KJ];
@@ -201,50 +220,26 @@ __global__ void __launch_bounds__(kBackThreads, kWhole ? 3 : KJ == kChoices ? 4 
         if (live) {
             for (int c = lane; c < P; c += lanes) {
                 float g[N];
-                if (kWhole) Rw::template load_floats<true>(dy, i, c * N, C, g);
+                Rw::template load_floats<true>(dy, i, c * N, C, g);
+                uint4 v[KJ];
 #pragma unroll
-                for (int b = 0; b < KJ; b += kBatch) {
-                    uint4 v[kBatch], d[kBatch];   // of h, and where phases differ of dy in each slot's phase, from L1
+                for (int j = 0; j < KJ; ++j)
+                    if (at[j] >= 0) v[j] = Rw::template load<false>(h, at[j], c * N, C);
 #pragma unroll
-                    for (int j = 0; j < kBatch; ++j) {
-                        if (at[b + j] < 0) continue;
-                        const int32_t e = Rw::column(dh + (int64_t)at[b + j] * C, c);
-                        v[j] = Rw::template load<false>(h, at[b + j], e, C);
-                        if (!kWhole) d[j] = Rw::template load<true>(dy, i, e, C);
+                for (int j = 0; j < KJ; ++j) {
+                    if (at[j] < 0) continue;
+                    float f[N], scaled[N];
+                    unpack<T>(v[j], f);
+#pragma unroll
+                    for (int q = 0; q < N; ++q) {
+                        dot[j] = fmaf(g[q], f[q], dot[j]);
+                        scaled[q] = w[j] * g[q];
                     }
-#pragma unroll
-                    for (int j = 0; j < kBatch; ++j) {
-                        if (at[b + j] < 0) continue;
-                        T* to = dh + (int64_t)at[b + j] * C;
-                        const int32_t e = Rw::column(to, c);
-                        float f[N], scaled[N];
-                        Rw::floats(v[j], e, C, f);
-                        if (!kWhole) Rw::floats(d[j], e, C, g);
-#pragma unroll
-                        for (int q = 0; q < N; ++q) {
-                            dot[b + j] = fmaf(g[q], f[q], dot[b + j]);
-                            scaled[q] = w[b + j] * g[q];
-                        }
-                        Rw::template store<true>(to, e, C, pack<T>(scaled));
-                    }
+                    Rw::template store<true>(dh + (int64_t)at[j] * C, c * N, C, pack<T>(scaled));
                 }
             }
         }
-#pragma unroll
-        for (int j = 0; j < KJ; ++j)
-            for (int o = imin(lanes, 32) >> 1; o > 0; o >>= 1) dot[j] += __shfl_xor_sync(0xffffffffu, dot[j], o);
-        if (lanes > 32) {
-            const int warp = threadIdx.x >> 5;
-            if ((threadIdx.x & 31) == 0)
-#pragma unroll
-                for (int j = 0; j < KJ; ++j) part[warp][j] = dot[j];
-            __syncthreads();
-            if (lane == 0)
-#pragma unroll
-                for (int j = 0; j < KJ; ++j)
-                    for (int q = 1; q < lanes / 32; ++q) dot[j] += part[warp + q][j];
-            __syncthreads();
-        }
+        sum_of_row(dot, lanes, lane, part);
         if (live && lane == 0)
 #pragma unroll
             for (int j = 0; j < KJ; ++j)
@@ -253,18 +248,81 @@ __global__ void __launch_bounds__(kBackThreads, kWhole ? 3 : KJ == kChoices ? 4 
     clear_rows_behind<Rw>(end, R, dh, C, P, C);
 }
 
+// The same where rows have phases of their own: dy is shifted to each slot's (from L1), so that nothing is gained by a
+// thread that takes a piece of all choices.  The threads go through the pieces of all choices instead (`chunk` pieces of a
+// row at a time, all of it but for the widest rows), and no more of them idle than the last round leaves: fp16, 3 choices
+// of 301, 256 MB: 208 us, where a thread for a piece of all choices took 378; two pieces of a thread at a time no less.
+// What bounds it is issue slots.
+template <typename T, int KJ>
+__global__ void __launch_bounds__(kBackThreads, KJ == kChoices ? 4 : 5) combine_rows_backward_any(
+    int64_t M, int32_t k, int32_t R, int32_t P, int32_t C, int lane_bits, int32_t chunk, FastDiv by_chunk, Rows<T> dy, Rows<T> h,
+    const int32_t* __restrict__ slot, const float* __restrict__ weights, const int32_t* __restrict__ end, T* __restrict__ dh,
+    float* __restrict__ dweights) {
+    using Rw = Row<T, false>;
+    constexpr int N = Rw::N;
+    __shared__ float part[kBackThreads / 32][KJ];
+    pdl_wait();
+    pdl_trigger();
+    const int lanes = 1 << lane_bits, lane = threadIdx.x & (lanes - 1);
+    const int64_t i = (int64_t)blockIdx.x * (kBackThreads >> lane_bits) + (threadIdx.x >> lane_bits);
+    const bool live = i < M;
+    for (int j0 = 0; j0 < k; j0 += KJ) {
+        float dot[KJ] = {};
+        const int64_t a = i * k + j0;
+        const int items = live ? imin(KJ, k - j0) * chunk : 0;
+        for (int64_t c0 = 0; c0 < P; c0 += chunk)
+            for (int t = lane; t < items; t += lanes) {
+                const int j = (int)by_chunk.quotient((uint32_t)t);
+                const int64_t c = c0 + (t - j * chunk);
+                const int32_t p = c < P ? __ldg(slot + a + j) : -1;
+                if ((uint32_t)p >= (uint32_t)R) continue;
+                T* to = dh + (int64_t)p * C;
+                const int32_t e = Rw::column(to, (int32_t)c);
+                const uint4 v = Rw::template load<false>(h, p, e, C), d = Rw::template load<true>(dy, i, e, C);
+                const float w = __ldg(weights + a + j);
+                float f[N], g[N], product = 0.f;
+                Rw::floats(v, e, C, f);
+                Rw::floats(d, e, C, g);
+#pragma unroll
+                for (int q = 0; q < N; ++q) {
+                    product = fmaf(g[q], f[q], product);
+                    g[q] *= w;
+                }
+                Rw::template store<true>(to, e, C, pack<T>(g));
+#pragma unroll
+                for (int q = 0; q < KJ; ++q) dot[q] += q == j ? product : 0.f;
+            }
+        sum_of_row(dot, lanes, lane, part);
+        if (live && lane == 0)
+#pragma unroll
+            for (int q = 0; q < KJ; ++q)   // 0 without a slot
+                if (j0 + q < k) dweights[a + q] = dot[q];
+    }
+    clear_rows_behind<Rw>(end, R, dh, C, P, C);
+}
+
 template <typename T, bool kWhole>
 zs_status combine_backward(const void* dy, int64_t dy_ld, const void* h, int64_t h_ld, const int32_t* slot, const float* weights,
                            const int32_t* end, int64_t M, int32_t k, int32_t C, void* dh, float* dweights, cudaStream_t s) {
-    const int32_t P = Row<T, kWhole>::pieces(C);
+    const int32_t P = Row<T, kWhole>::pieces(C), chunk = imin(P, 1 << 20);
+    const int KJ = k <= 4 ? 4 : kChoices;
+    const int64_t items = kWhole ? P : (int64_t)chunk * imin(k, KJ);
     // enough threads a row that no one takes more than one piece, or so many that every SM has work
-    int lanes = 1;
-    while (lanes < 32 && lanes < P) lanes *= 2;
-    while (lanes < kBackThreads && lanes < P && M * lanes < (int64_t)num_sms() * 1024) lanes *= 2;
-    const int64_t rows = kBackThreads / lanes;
-    auto kernel = k <= 4 ? combine_rows_backward<T, kWhole, 4> : combine_rows_backward<T, kWhole, kChoices>;
-    launch(kernel, dim3((unsigned)((M + rows - 1) / rows)), dim3(kBackThreads), 0, s, M, k, (int32_t)(M * k), P,
-           C, lanes, Rows<T>(dy, M, dy_ld, C), Rows<T>(h, M * k, h_ld, C), slot, weights, end, static_cast<T*>(dh), dweights);
+    int lane_bits = 0;
+    while (lane_bits < 5 && 1 << lane_bits < items) ++lane_bits;
+    while (1 << lane_bits < kBackThreads && 1 << lane_bits < items && M << lane_bits < (int64_t)num_sms() * 512) ++lane_bits;
+    const int64_t rows = kBackThreads >> lane_bits;
+    const dim3 grid((unsigned)((M + rows - 1) / rows)), block(kBackThreads);
+    const int32_t R = (int32_t)(M * k);
+    const Rows<T> g(dy, M, dy_ld, C), v(h, R, h_ld, C);
+    T* to = static_cast<T*>(dh);
+    if constexpr (kWhole) {
+        auto kernel = KJ == 4 ? combine_rows_backward<T, 4> : combine_rows_backward<T, kChoices>;
+        launch(kernel, grid, block, 0, s, M, k, R, P, C, lane_bits, g, v, slot, weights, end, to, dweights);
+    } else {
+        auto kernel = KJ == 4 ? combine_rows_backward_any<T, 4> : combine_rows_backward_any<T, kChoices>;
+        launch(kernel, grid, block, 0, s, M, k, R, P, C, lane_bits, chunk, FastDiv((uint32_t)chunk), g, v, slot, weights, end, to, dweights);
+    }
     return check_launch("combine gradient");
 }
 

@@ -7,7 +7,7 @@
 // the result has its own phase: its first and last piece are written element by
 // element, and a piece is read from another row's phase as two aligned 16-byte
 // words that are shifted together (fp16 rows of 301 dispatched, 64 MB: 94 us
-// element by element, 35 so).  Pieces of several rows are numbered together, so
+// element by element, 26 so).  Pieces of several rows are numbered together, so
 // that a CTA's threads are all busy whatever the width.
 #pragma once
 
@@ -48,13 +48,19 @@ __device__ __forceinline__ uint4 shifted(uint4 a, uint4 b, int o) {
                       __funnelshift_r(w[3], w[4], s));
 }
 
-// A matrix that is read: rows ld apart, all of it in [p, end).
+// A matrix that is read: rows ld apart, all of it in [p, end).  Around `inner` rows from row `margin` on there are three
+// pieces and more of it on both sides.
 template <typename T>
 struct Rows {
     const T *p, *end;
     int64_t ld;
+    int32_t margin;
+    uint32_t inner;
     Rows(const void* p_, int64_t rows, int64_t ld_, int32_t C)
-        : p(static_cast<const T*>(p_)), end(p + (rows > 0 ? (rows - 1) * ld_ + C : 0)), ld(ld_) {}
+        : p(static_cast<const T*>(p_)), end(p + (rows > 0 ? (rows - 1) * ld_ + C : 0)), ld(ld_) {
+        margin = (int32_t)((3 * kVec<T> + (int64_t)C - 1) / C);   // a row takes C and more
+        inner = rows > 2 * (int64_t)margin ? (uint32_t)(rows - 2 * margin) : 0u;
+    }
 };
 
 // Pieces of rows of C elements.  kCached: rows that are read again soon.
@@ -68,6 +74,10 @@ struct Row {
     static __device__ __forceinline__ int32_t column(const T* to, int32_t c) {
         return c * N - (kWhole ? 0 : (int32_t)((uint32_t)reinterpret_cast<uintptr_t>(to) & 15u) / (int32_t)sizeof(T));
     }
+    // Which of the columns [e, e + N) are in the row, as bits.
+    static __device__ __forceinline__ uint32_t inside(int32_t e, int32_t C) {
+        return ((1u << imin(imax(C - e, 0), N)) - 1u) & (~0u << imax(-e, 0));
+    }
     // Columns [e, e + N) of a row of m; of those outside the row, whatever lies there (but nothing outside m is read).
     template <bool kCached>
     static __device__ __forceinline__ uint4 load(const Rows<T>& m, int64_t i, int32_t e, int32_t C) {
@@ -77,6 +87,10 @@ struct Row {
         } else {
             const int o = (int)(reinterpret_cast<uintptr_t>(row + e) & 15u), back = o / (int)sizeof(T);
             const T *first = row + (e - back), *second = first + N;   // the aligned words that hold them
+            if ((uint32_t)((int32_t)i - m.margin) < m.inner) {
+                const uint4 v = ld_cached(first);
+                return o ? shifted(v, ld_cached(second), o) : v;
+            }
             const bool a = e - back + N > 0 && e - back < C, b = o && e - back + 2 * N > 0 && e - back + N < C;
             if ((a && (first < m.p || first + N > m.end)) || (b && (second < m.p || second + N > m.end))) {
                 Piece<T> v;   // at the ends of m
@@ -91,26 +105,29 @@ struct Row {
     // Their values, zeros outside the row.
     static __device__ __forceinline__ void floats(uint4 v, int32_t e, int32_t C, float (&f)[N]) {
         unpack<T>(v, f);
-        if (!kWhole && (e < 0 || e + N > C))
+        if (!kWhole && (e < 0 || e + N > C)) {
+            const uint32_t in = inside(e, C);
 #pragma unroll
-            for (int q = 0; q < N; ++q) f[q] = e + q >= 0 && e + q < C ? f[q] : 0.f;
+            for (int q = 0; q < N; ++q) f[q] = in >> q & 1u ? f[q] : 0.f;
+        }
     }
     template <bool kCached>
     static __device__ __forceinline__ void load_floats(const Rows<T>& m, int64_t i, int32_t e, int32_t C, float (&f)[N]) {
         floats(load<kCached>(m, i, e, C), e, C, f);
     }
-    // Columns [e, e + N) of a row of the result, as far as they are in it.
-    template <bool kOnce>
+    // Columns [e, e + N) of a row of the result, as far as they are in it.  kInPhase: e is a column(), on a 16-byte boundary.
+    template <bool kOnce, bool kInPhase = true>
     static __device__ __forceinline__ void store(T* row, int32_t e, int32_t C, uint4 v) {
-        if (kWhole || (e >= 0 && e + N <= C && aligned16(row + e))) {
+        if (kWhole || (e >= 0 && e + N <= C && (kInPhase || aligned16(row + e)))) {
             if (kOnce) st_once(row + e, v);
             else st_piece(row + e, v);
         } else {
+            const uint32_t in = inside(e, C);
             Piece<T> p;
             p.raw = v;
 #pragma unroll
-            for (int i = 0; i < N; ++i)
-                if (e + i >= 0 && e + i < C) row[e + i] = p.e[i];
+            for (int q = 0; q < N; ++q)
+                if (in >> q & 1u) row[e + q] = p.e[q];
         }
     }
     static __device__ __forceinline__ uint4 zero() { return make_uint4(0, 0, 0, 0); }
