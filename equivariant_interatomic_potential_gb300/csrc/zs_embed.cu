@@ -41,7 +41,7 @@ template <typename T, bool kWhole>
 zs_status embed_forward(const void* w, int64_t w_ld, int32_t V, const int32_t* ids, int64_t M, int32_t C, float scale, void* y,
                         int64_t y_ld, cudaStream_t s) {
     constexpr int U = 4;
-    const MoveShape shape = move_shape(M, Row<T, kWhole>::pieces(C), C, U);
+    const MoveShape shape = move_rows_shape<T, kWhole>(M, C, U);
     launch(move_rows<T, kWhole, U, IdSource>, dim3(shape.ctas_x, shape.ctas_y), dim3(kMoveThreads), 0, s, shape, IdSource{ids, V},
            Rows<T>(w, V, w_ld, C), scale, static_cast<T*>(y), y_ld);
     return check_launch("embedding");
@@ -122,8 +122,9 @@ __global__ void __launch_bounds__(kSumThreads, kSumCtas) sum_rows(SumShape s, Ro
                                                                   const int32_t* __restrict__ perm, float scale, T* __restrict__ dw,
                                                                   float* __restrict__ head, float* __restrict__ tail,
                                                                   SumNote* __restrict__ notes) {
-    using R = Row<T, kWhole>;
-    constexpr int VEC = R::N;
+    using R = Row<T, kWhole, sizeof(T) == 4>;
+    // rows at a time; of words that are shifted one (and the next ones' in flight): 16384 of 50021, 1023 bf16: 47 us, two 59
+    constexpr int VEC = R::N, kBatch = R::kOnePhase ? kSumBatch : 1;
     __shared__ int32_t staged[kSumItems + 8];        // row_ptr[v0 .. v1 + 1], then perm[j0 .. j1)
     __shared__ int32_t bound[2];
     __shared__ int32_t unit_row[kSumThreads + 1];    // rows that end before each unit
@@ -167,7 +168,8 @@ __global__ void __launch_bounds__(kSumThreads, kSumCtas) sum_rows(SumShape s, Ro
 
     const int unit = (int)s.by_cols.quotient((uint32_t)tid), col = tid - unit * s.cols;
     const int64_t c = (int64_t)blockIdx.y * s.cols + col;
-    const int32_t e = (int32_t)imin<int64_t>(c * VEC, s.C);
+    const int32_t e = (int32_t)imin<int64_t>(R::kStrided ? c : c * VEC, s.C);
+    auto column = [&](int64_t c, int i) { return R::kStrided ? c + (int64_t)i * s.P : c * VEC + i; };   // element i of piece c
     const bool live = unit < s.units && c < s.P;
     float acc[VEC] = {};
     bool cut = false;                 // the unit closes a row that others have begun
@@ -189,40 +191,44 @@ __global__ void __launch_bounds__(kSumThreads, kSumCtas) sum_rows(SumShape s, Ro
 #pragma unroll
                 for (int i = 0; i < VEC; ++i) begun[i] = acc[i];
             } else {
+                // a row of nothing but zeros in its own phase, in which it may have a piece more
+                T* to = dw + (int64_t)(v0 + r) * s.C;
+                const bool empty = !kWhole && !R::kStrided && staged[r] == staged[r + 1];
                 float f[VEC];
 #pragma unroll
                 for (int i = 0; i < VEC; ++i) f[i] = acc[i] * scale;
-                R::template store<true, false>(dw + (int64_t)(v0 + r) * s.C, e, s.C, pack<T>(f));
+                R::template store<true, false>(to, empty ? R::column(to, (int32_t)c) : e, s.C, pack<T>(f));
+                if (empty && c == s.P - 1) R::template store<true>(to, R::column(to, s.P), s.C, R::zero());
             }
 #pragma unroll
             for (int i = 0; i < VEC; ++i) acc[i] = 0.f;
             ++r;
         };
-        auto load = [&](uint4(&v)[kSumBatch], int p) {
+        auto load = [&](typename R::Loaded(&v)[kBatch], int p) {
 #pragma unroll
-            for (int u = 0; u < kSumBatch; ++u) {
-                v[u] = R::zero();
+            for (int u = 0; u < kBatch; ++u) {
+                v[u] = {};
                 if (p + u < p_end) {
                     const int32_t i = sperm[p + u];
                     if ((uint64_t)(int64_t)i < (uint64_t)s.M) v[u] = R::template load<false>(dy, i, e, s.C);
                 }
             }
         };
-        uint4 v[kSumBatch], next[kSumBatch];
+        typename R::Loaded v[kBatch], next[kBatch];
         load(v, p);
-        for (; p < p_end; p += kSumBatch) {
-            load(next, p + kSumBatch);
+        for (; p < p_end; p += kBatch) {
+            load(next, p + kBatch);
 #pragma unroll
-            for (int u = 0; u < kSumBatch; ++u) {
+            for (int u = 0; u < kBatch; ++u) {
                 if (p + u >= p_end) break;
                 while (r < r_end && j0 + p + u >= (int64_t)staged[r + 1]) close();
                 float f[VEC];
-                unpack<T>(v[u], f);
+                unpack<T>(R::join(v[u]), f);
 #pragma unroll
                 for (int i = 0; i < VEC; ++i) acc[i] += f[i];
             }
 #pragma unroll
-            for (int u = 0; u < kSumBatch; ++u) v[u] = next[u];
+            for (int u = 0; u < kBatch; ++u) v[u] = next[u];
         }
         while (r < r_end) close();
 #pragma unroll
@@ -240,8 +246,7 @@ __global__ void __launch_bounds__(kSumThreads, kSumCtas) sum_rows(SumShape s, Ro
 #pragma unroll
             for (int i = 0; i < VEC; ++i) sum[i] += open[(q * s.cols + col) * VEC + i];
     };
-    const int64_t at = (int64_t)blockIdx.x * s.C + e;
-    const int width = kWhole ? VEC : imin(VEC, s.C - e);   // of the piece
+    const int64_t at = (int64_t)blockIdx.x * s.C;
     if (live && cut) {
         float sum[VEC];
         earlier(begun_row, sum);
@@ -254,7 +259,7 @@ __global__ void __launch_bounds__(kSumThreads, kSumCtas) sum_rows(SumShape s, Ro
         } else {
 #pragma unroll
             for (int i = 0; i < VEC; ++i)
-                if (i < width) head[at + i] = sum[i];
+                if (kWhole || column(c, i) < s.C) head[at + column(c, i)] = sum[i];
         }
     }
     if (live && unit == s.units - 1) {
@@ -268,7 +273,7 @@ __global__ void __launch_bounds__(kSumThreads, kSumCtas) sum_rows(SumShape s, Ro
         if ((int64_t)staged[r] + v0 + r < d1)   // the row goes on in the next CTA
 #pragma unroll
             for (int i = 0; i < VEC; ++i)
-                if (i < width) tail[at + i] = acc[i];
+                if (kWhole || column(c, i) < s.C) tail[at + column(c, i)] = acc[i];
     }
     // the row that is open at the CTA's start, if it was begun before and ends here
     const int64_t begin = (int64_t)staged[0] + v0;
@@ -281,8 +286,11 @@ __global__ void __launch_bounds__(kSumThreads, kSumCtas) sum_rows(SumShape s, Ro
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     if (!closes) return;
-    const int64_t c0 = (int64_t)blockIdx.y * s.cols * VEC, c1 = imin<int64_t>(c0 + s.cols * VEC, s.C);
-    for (int64_t q = c0 + tid; q < c1; q += kSumThreads) {
+    const int64_t c0 = (int64_t)blockIdx.y * s.cols;
+    for (int t = tid; t < s.cols * VEC; t += kSumThreads) {
+        const int i = R::kStrided ? (int)s.by_cols.quotient((uint32_t)t) : t % VEC;
+        const int64_t piece = c0 + (R::kStrided ? t - i * s.cols : t / VEC), q = column(piece, i);
+        if (piece >= s.P || q >= s.C) continue;
         float sum = 0.f;
         for (int b = first; b < (int)blockIdx.x; ++b) sum += __ldcg(tail + (int64_t)b * s.C + q);
         sum += __ldcg(head + (int64_t)blockIdx.x * s.C + q);

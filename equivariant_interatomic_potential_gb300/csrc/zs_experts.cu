@@ -61,7 +61,7 @@ __global__ void __launch_bounds__(kMoveThreads) spread_rows(MoveShape s, int32_t
         if (row[0] < 0) return;
         const int32_t* at = slot + (int64_t)row[0] * k;
         uint4 v = Rw::zero();
-        if (kWhole) v = Rw::template load<false>(x, row[0], piece[0] * Rw::N, s.C);
+        if (kWhole) v = Rw::join(Rw::template load<false>(x, row[0], piece[0] * Rw::N, s.C));
         for (int j0 = 0; j0 < k; j0 += kChoices) {
             int32_t p[kChoices];
 #pragma unroll
@@ -71,7 +71,7 @@ __global__ void __launch_bounds__(kMoveThreads) spread_rows(MoveShape s, int32_t
                 if ((uint32_t)p[j] >= (uint32_t)R) continue;
                 T* to = xs + (int64_t)p[j] * s.C;
                 const int32_t e = Rw::column(to, piece[0]);
-                if (!kWhole) v = Rw::template load<true>(x, row[0], e, s.C);   // to each slot's phase, from L1
+                if (!kWhole) v = Rw::template join<true>(Rw::template load<true>(x, row[0], e, s.C));   // to each slot's phase, from L1
                 Rw::template store<true>(to, e, s.C, v);
             }
         }
@@ -94,19 +94,20 @@ zs_status dispatch(const void* x, int64_t x_ld, const int32_t* row_ptr, const in
                (const int32_t*)slot, row_ptr + G, to);
     } else {
         constexpr int U = 4;
-        const MoveShape shape = move_shape(R, Rw::pieces(C), C, U);
+        const MoveShape shape = move_rows_shape<T, kWhole>(R, C, U);
         launch(move_rows<T, kWhole, U, AssignmentSource>, dim3(shape.ctas_x, shape.ctas_y), dim3(kMoveThreads), 0, s, shape,
                AssignmentSource{row_ptr, perm, G, R, FastDiv((uint32_t)k), slot}, from, 1.f, to, (int64_t)C);
     }
     return check_launch("dispatch");
 }
 
-// U pieces of a thread at a time and KJ choices of each: four or eight loads in flight and three to five CTAs an SM.  More
+// U pieces of a thread at a time and KJ choices of each: four or eight loads in flight and four or five CTAs an SM.  More
 // loads and fewer CTAs are slower (8 choices of 1024 bf16, 32768 rows: 106 us at 3 CTAs, 97 at 4; 2 choices of 256, 256 MB:
 // 8 loads at 3 CTAs 111, 4 at 5 84), staging slots in shared memory too (115 to 188): the read of rows in any order is the
-// limit, 0.93 of the copy rate.
+// limit, 0.93 of the copy rate.  Where rows have phases of their own a load is of two words, and two choices at a time are
+// the most that five CTAs' registers hold (8 choices of 301 fp16, 256 MB: 79 us; four at four CTAs 87, eight at three 90).
 template <typename T, bool kWhole, int KJ, int U>
-__global__ void __launch_bounds__(kMoveThreads, KJ == kChoices ? (kWhole ? 4 : 3) : 5) combine_rows(
+__global__ void __launch_bounds__(kMoveThreads, KJ == kChoices ? 4 : 5) combine_rows(
     MoveShape s, int32_t k, int32_t R, Rows<T> h, const int32_t* __restrict__ slot, const float* __restrict__ weights, T* __restrict__ y,
     int64_t y_ld) {
     using Rw = Row<T, kWhole>;
@@ -116,7 +117,7 @@ __global__ void __launch_bounds__(kMoveThreads, KJ == kChoices ? (kWhole ? 4 : 3
     for_pieces<U>(s, [&](const int32_t(&row)[U], const int32_t(&piece)[U]) {
         float sum[U][N] = {};
         for (int j0 = 0; j0 < k; j0 += KJ) {
-            uint4 v[U][KJ];
+            typename Rw::Loaded v[U][KJ];
             float w[U][KJ];
             bool held[U][KJ];
 #pragma unroll
@@ -138,7 +139,7 @@ __global__ void __launch_bounds__(kMoveThreads, KJ == kChoices ? (kWhole ? 4 : 3
                 for (int j = 0; j < KJ; ++j) {
                     if (!held[u][j]) continue;
                     float f[N];
-                    unpack<T>(v[u][j], f);
+                    unpack<T>(Rw::join(v[u][j]), f);
 #pragma unroll
                     for (int i = 0; i < N; ++i) sum[u][i] = fmaf(w[u][j], f[i], sum[u][i]);
                 }
@@ -162,9 +163,11 @@ zs_status combine(const void* h, int64_t h_ld, const int32_t* slot, const float*
                Rows<T>(h, R, h_ld, C), slot, weights, static_cast<T*>(y), y_ld);
     };
     using std::integral_constant;
-    if (k <= 2) go(integral_constant<int, 2>(), integral_constant<int, kWhole ? 2 : 1>());
-    else if (k <= 4) go(integral_constant<int, 4>(), integral_constant<int, 1>());
-    else go(integral_constant<int, kChoices>(), integral_constant<int, 1>());
+    if (k <= 2 || !kWhole) go(integral_constant<int, 2>(), integral_constant<int, kWhole ? 2 : 1>());
+    else if constexpr (kWhole) {
+        if (k <= 4) go(integral_constant<int, 4>(), integral_constant<int, 1>());
+        else go(integral_constant<int, kChoices>(), integral_constant<int, 1>());
+    }
     return check_launch("combine");
 }
 
@@ -192,11 +195,11 @@ __device__ __forceinline__ void sum_of_row(float (&dot)[KJ], int lanes, int lane
 // `lanes` threads for a row i of dy, which they read once for its k choices: their rows of h in flight together, the
 // products with dy in fp32 registers until the row's end.  Memory: 32768 rows, 8 choices of 1024 bf16: 176 us, 0.95 of the
 // copy rate.
-template <typename T, int KJ>
+template <typename T, bool kWhole, int KJ>
 __global__ void __launch_bounds__(kBackThreads, 3) combine_rows_backward(
     int64_t M, int32_t k, int32_t R, int32_t P, int32_t C, int lane_bits, Rows<T> dy, Rows<T> h, const int32_t* __restrict__ slot,
     const float* __restrict__ weights, const int32_t* __restrict__ end, T* __restrict__ dh, float* __restrict__ dweights) {
-    using Rw = Row<T, true>;
+    using Rw = Row<T, kWhole, sizeof(T) == 4>;
     constexpr int N = Rw::N;
     __shared__ float part[kBackThreads / 32][KJ];
     pdl_wait();
@@ -219,12 +222,13 @@ __global__ void __launch_bounds__(kBackThreads, 3) combine_rows_backward(
         }
         if (live) {
             for (int c = lane; c < P; c += lanes) {
+                const int32_t e = Rw::column(dh, c);
                 float g[N];
-                Rw::template load_floats<true>(dy, i, c * N, C, g);
+                unpack<T>(Rw::join(Rw::template load<true>(dy, i, e, C)), g);
                 uint4 v[KJ];
 #pragma unroll
                 for (int j = 0; j < KJ; ++j)
-                    if (at[j] >= 0) v[j] = Rw::template load<false>(h, at[j], c * N, C);
+                    if (at[j] >= 0) v[j] = Rw::join(Rw::template load<false>(h, at[j], e, C));
 #pragma unroll
                 for (int j = 0; j < KJ; ++j) {
                     if (at[j] < 0) continue;
@@ -235,7 +239,7 @@ __global__ void __launch_bounds__(kBackThreads, 3) combine_rows_backward(
                         dot[j] = fmaf(g[q], f[q], dot[j]);
                         scaled[q] = w[j] * g[q];
                     }
-                    Rw::template store<true>(dh + (int64_t)at[j] * C, c * N, C, pack<T>(scaled));
+                    Rw::template store<true>(dh + (int64_t)at[j] * C, e, C, pack<T>(scaled));
                 }
             }
         }
@@ -278,11 +282,11 @@ __global__ void __launch_bounds__(kBackThreads, KJ == kChoices ? 4 : 5) combine_
                 if ((uint32_t)p >= (uint32_t)R) continue;
                 T* to = dh + (int64_t)p * C;
                 const int32_t e = Rw::column(to, (int32_t)c);
-                const uint4 v = Rw::template load<false>(h, p, e, C), d = Rw::template load<true>(dy, i, e, C);
+                const typename Rw::Loaded v = Rw::template load<false>(h, p, e, C), d = Rw::template load<true>(dy, i, e, C);
                 const float w = __ldg(weights + a + j);
                 float f[N], g[N], product = 0.f;
-                Rw::floats(v, e, C, f);
-                Rw::floats(d, e, C, g);
+                Rw::floats(Rw::template join<true>(v), e, C, f);
+                Rw::floats(Rw::join(d), e, C, g);
 #pragma unroll
                 for (int q = 0; q < N; ++q) {
                     product = fmaf(g[q], f[q], product);
@@ -304,9 +308,10 @@ __global__ void __launch_bounds__(kBackThreads, KJ == kChoices ? 4 : 5) combine_
 template <typename T, bool kWhole>
 zs_status combine_backward(const void* dy, int64_t dy_ld, const void* h, int64_t h_ld, const int32_t* slot, const float* weights,
                            const int32_t* end, int64_t M, int32_t k, int32_t C, void* dh, float* dweights, cudaStream_t s) {
-    const int32_t P = Row<T, kWhole>::pieces(C), chunk = imin(P, 1 << 20);
+    using Rw = Row<T, kWhole, sizeof(T) == 4>;
+    const int32_t P = Rw::pieces(C), chunk = imin(P, 1 << 20);
     const int KJ = k <= 4 ? 4 : kChoices;
-    const int64_t items = kWhole ? P : (int64_t)chunk * imin(k, KJ);
+    const int64_t items = Rw::kOnePhase ? P : (int64_t)chunk * imin(k, KJ);
     // enough threads a row that no one takes more than one piece, or so many that every SM has work
     int lane_bits = 0;
     while (lane_bits < 5 && 1 << lane_bits < items) ++lane_bits;
@@ -316,8 +321,8 @@ zs_status combine_backward(const void* dy, int64_t dy_ld, const void* h, int64_t
     const int32_t R = (int32_t)(M * k);
     const Rows<T> g(dy, M, dy_ld, C), v(h, R, h_ld, C);
     T* to = static_cast<T*>(dh);
-    if constexpr (kWhole) {
-        auto kernel = KJ == 4 ? combine_rows_backward<T, 4> : combine_rows_backward<T, kChoices>;
+    if constexpr (Rw::kOnePhase) {
+        auto kernel = KJ == 4 ? combine_rows_backward<T, kWhole, 4> : combine_rows_backward<T, kWhole, kChoices>;
         launch(kernel, grid, block, 0, s, M, k, R, P, C, lane_bits, g, v, slot, weights, end, to, dweights);
     } else {
         auto kernel = KJ == 4 ? combine_rows_backward_any<T, 4> : combine_rows_backward_any<T, kChoices>;

@@ -7,7 +7,7 @@
 // the result has its own phase: its first and last piece are written element by
 // element, and a piece is read from another row's phase as two aligned 16-byte
 // words that are shifted together (fp16 rows of 301 dispatched, 64 MB: 94 us
-// element by element, 26 so).  Pieces of several rows are numbered together, so
+// element by element, 25 so).  Pieces of several rows are numbered together, so
 // that a CTA's threads are all busy whatever the width.
 #pragma once
 
@@ -32,7 +32,8 @@ __device__ __forceinline__ uint4 ld_cached(const void* p) { return __ldg(static_
 __device__ __forceinline__ void st_once(void* p, uint4 v) {   // data that nothing reads again soon
     asm volatile("st.global.cs.v4.u32 [%0], {%1,%2,%3,%4};" :: "l"(p), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
-// The 16 bytes at offset o (0 < o < 16) of two words in a row.
+// The 16 bytes at offset o (below 16, whole elements) of two words in a row.
+template <typename T>
 __device__ __forceinline__ uint4 shifted(uint4 a, uint4 b, int o) {
     uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
     if (o & 8) {
@@ -43,7 +44,8 @@ __device__ __forceinline__ uint4 shifted(uint4 a, uint4 b, int o) {
 #pragma unroll
         for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
     }
-    const int s = 8 * (o & 3);
+    if constexpr (sizeof(T) == 4) return make_uint4(w[0], w[1], w[2], w[3]);
+    const int s = 8 * (o & 2);
     return make_uint4(__funnelshift_r(w[0], w[1], s), __funnelshift_r(w[1], w[2], s), __funnelshift_r(w[2], w[3], s),
                       __funnelshift_r(w[3], w[4], s));
 }
@@ -63,64 +65,118 @@ struct Rows {
     }
 };
 
-// Pieces of rows of C elements.  kCached: rows that are read again soon.
-template <typename T, bool kWhole>
+// Pieces of rows of C elements.  kCached: rows that are read again soon.  kLane: rows of fp32 that are not whole pieces, read
+// and written element by element: of P pieces, piece c has the columns c, c + P, c + 2 P, ... in all rows.  It takes fewer
+// instructions than two words that are shifted, but more traffic, of 128 bytes that lie across two lines: it is taken where
+// instructions are the limit (647170 x 95 looked up 65 us against 78, their gradient 84 against 108; but 256 MB, dispatched
+// to 8 slots at a time, 73 against 53, and combined 97 against 76).
+template <typename T, bool kWhole, bool kLane = false>
 struct Row {
-    static constexpr int N = kVec<T>;   // elements of a piece
+    static constexpr int N = kVec<T>;                       // elements of a piece
+    static constexpr bool kStrided = !kWhole && kLane;
+    static constexpr bool kOnePhase = kWhole || kStrided;   // a piece has the same columns in all rows
 
     // Pieces that cover a row, whatever its phase.
-    static int32_t pieces(int32_t C) { return kWhole ? C / N : (int32_t)(((int64_t)C + 2 * N - 2) / N); }
+    static __host__ __device__ __forceinline__ int32_t pieces(int32_t C) {
+        return kWhole ? C / N : (int32_t)(((int64_t)C + (kStrided ? N - 1 : 2 * N - 2)) / N);
+    }
     // The column of the first element of piece c of a row of the result at `to`: below 0 where the row starts inside it.
     static __device__ __forceinline__ int32_t column(const T* to, int32_t c) {
+        if (kStrided) return c;
         return c * N - (kWhole ? 0 : (int32_t)((uint32_t)reinterpret_cast<uintptr_t>(to) & 15u) / (int32_t)sizeof(T));
     }
     // Which of the columns [e, e + N) are in the row, as bits.
     static __device__ __forceinline__ uint32_t inside(int32_t e, int32_t C) {
         return ((1u << imin(imax(C - e, 0), N)) - 1u) & (~0u << imax(-e, 0));
     }
-    // Columns [e, e + N) of a row of m; of those outside the row, whatever lies there (but nothing outside m is read).
+    // The piece of a row of m at column e, in flight: the aligned words that hold it, and the offset in these.  Nothing waits
+    // for the words before join(), so that a thread's loads are all on their way together.
+    struct Loaded {
+        uint4 a, b;
+        int o;
+    };
     template <bool kCached>
-    static __device__ __forceinline__ uint4 load(const Rows<T>& m, int64_t i, int32_t e, int32_t C) {
+    static __device__ __forceinline__ Loaded load(const Rows<T>& m, int32_t i, int32_t e, int32_t C) {
         const T* row = m.p + i * m.ld;
+        Loaded v;
         if constexpr (kWhole) {
-            return kCached ? ld_cached(row + e) : ld_piece(row + e);
+            v.a = kCached ? ld_cached(row + e) : ld_piece(row + e);
+        } else if constexpr (kStrided) {
+            static_assert(sizeof(T) == 4, "32-bit elements");
+            uint32_t w[N];
+#pragma unroll
+            for (int q = 0; q < N; ++q) {
+                const int64_t at = e + (int64_t)q * pieces(C);
+                w[q] = at < C ? __ldg(reinterpret_cast<const uint32_t*>(row) + at) : 0u;
+            }
+            v.a = make_uint4(w[0], w[1], w[2], w[3]);
         } else {
-            const int o = (int)(reinterpret_cast<uintptr_t>(row + e) & 15u), back = o / (int)sizeof(T);
-            const T *first = row + (e - back), *second = first + N;   // the aligned words that hold them
-            if ((uint32_t)((int32_t)i - m.margin) < m.inner) {
-                const uint4 v = ld_cached(first);
-                return o ? shifted(v, ld_cached(second), o) : v;
-            }
-            const bool a = e - back + N > 0 && e - back < C, b = o && e - back + 2 * N > 0 && e - back + N < C;
-            if ((a && (first < m.p || first + N > m.end)) || (b && (second < m.p || second + N > m.end))) {
-                Piece<T> v;   // at the ends of m
+            v.o = (int)(reinterpret_cast<uintptr_t>(row + e) & 15u);
+            v.b = zero();
+            if ((uint32_t)(i - m.margin) < m.inner) {
+                const T* first = row + (e - v.o / (int)sizeof(T));
+                v.a = ld_cached(first);
+                if (v.o) v.b = ld_cached(first + N);
+            } else {   // near the ends of m, where a word may reach out of it: element by element
+                constexpr int kBits = 8 * sizeof(T);
+                v.o = 0;
+                v.a = zero();
 #pragma unroll 1
-                for (int q = 0; q < N; ++q) v.e[q] = e + q >= 0 && e + q < C ? __ldg(row + e + q) : from_f32<T>(0.f);
-                return v.raw;
+                for (int q = N - 1; q >= 0; --q) {
+                    Piece<T> one;
+                    one.raw = zero();
+                    if (e + q >= 0 && e + q < C) one.e[0] = __ldg(row + e + q);
+                    v.a.w = __funnelshift_lc(v.a.z, v.a.w, kBits);
+                    v.a.z = __funnelshift_lc(v.a.y, v.a.z, kBits);
+                    v.a.y = __funnelshift_lc(v.a.x, v.a.y, kBits);
+                    v.a.x = __funnelshift_lc(0, v.a.x, kBits) | one.raw.x;
+                }
             }
-            const uint4 v = a ? ld_cached(first) : zero();
-            return o ? shifted(v, b ? ld_cached(second) : zero(), o) : v;
         }
+        return v;
+    }
+    // Its elements; those outside the row hold anything.  kOften: rows of the same phase are frequent, which need no shift.
+    template <bool kOften = false>
+    static __device__ __forceinline__ uint4 join(const Loaded& v) {
+        if constexpr (kWhole || kStrided) return v.a;
+        else if constexpr (kOften) return v.o ? shifted<T>(v.a, v.b, v.o) : v.a;
+        else return shifted<T>(v.a, v.b, v.o);
     }
     // Their values, zeros outside the row.
     static __device__ __forceinline__ void floats(uint4 v, int32_t e, int32_t C, float (&f)[N]) {
         unpack<T>(v, f);
-        if (!kWhole && (e < 0 || e + N > C)) {
+        if (!kWhole && !kStrided && (e < 0 || e + N > C)) {
             const uint32_t in = inside(e, C);
 #pragma unroll
             for (int q = 0; q < N; ++q) f[q] = in >> q & 1u ? f[q] : 0.f;
         }
     }
-    template <bool kCached>
-    static __device__ __forceinline__ void load_floats(const Rows<T>& m, int64_t i, int32_t e, int32_t C, float (&f)[N]) {
-        floats(load<kCached>(m, i, e, C), e, C, f);
-    }
-    // Columns [e, e + N) of a row of the result, as far as they are in it.  kInPhase: e is a column(), on a 16-byte boundary.
+    // The piece of a row of the result at column e, as far as it is in it.  kInPhase: e is a column(), on a 16-byte boundary.
     template <bool kOnce, bool kInPhase = true>
     static __device__ __forceinline__ void store(T* row, int32_t e, int32_t C, uint4 v) {
-        if (kWhole || (e >= 0 && e + N <= C && (kInPhase || aligned16(row + e)))) {
+        if constexpr (kStrided) {
+            const uint32_t w[N] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int q = 0; q < N; ++q) {
+                const int64_t at = e + (int64_t)q * pieces(C);
+                if (at < C) reinterpret_cast<uint32_t*>(row)[at] = w[q];
+            }
+        } else if (kWhole || (e >= 0 && e + N <= C && (kInPhase || aligned16(row + e)))) {
             if (kOnce) st_once(row + e, v);
             else st_piece(row + e, v);
+        } else if (!kInPhase && sizeof(T) == 2 && e >= 0 && e + N <= C) {   // two elements at a time where they are on a boundary
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+            if (reinterpret_cast<uintptr_t>(row + e) & 2u) {
+                Piece<T> p;
+                p.raw = v;
+                row[e] = p.e[0];
+#pragma unroll
+                for (int q = 0; q < 3; ++q) *reinterpret_cast<uint32_t*>(row + e + 1 + 2 * q) = __funnelshift_r(w[q], w[q + 1], 16);
+                row[e + N - 1] = p.e[N - 1];
+            } else {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) *reinterpret_cast<uint32_t*>(row + e + 2 * q) = w[q];
+            }
         } else {
             const uint32_t in = inside(e, C);
             Piece<T> p;
@@ -218,33 +274,38 @@ __device__ __forceinline__ void for_pieces(const MoveShape& s, F&& f) {
 template <typename T, bool kWhole, int U, typename Source>
 __global__ void __launch_bounds__(kMoveThreads) move_rows(MoveShape s, Source src, Rows<T> x, float factor, T* __restrict__ y,
                                                           int64_t y_ld) {
-    using R = Row<T, kWhole>;
+    using R = Row<T, kWhole, sizeof(T) == 4>;
     pdl_wait();
     pdl_trigger();
     for_pieces<U>(s, [&](const int32_t(&row)[U], const int32_t(&piece)[U]) {
-        uint4 v[U];
+        typename R::Loaded in[U];
         int32_t from[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) from[u] = row[u] >= 0 ? src.row(row[u], piece[u] == 0) : -1;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            v[u] = R::zero();
-            if (from[u] >= 0) v[u] = R::template load<Source::kAgain>(x, from[u], R::column(y + (int64_t)row[u] * y_ld, piece[u]), s.C);
+            in[u] = {};
+            if (from[u] >= 0) in[u] = R::template load<Source::kAgain>(x, from[u], R::column(y + (int64_t)row[u] * y_ld, piece[u]), s.C);
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             if (row[u] < 0) continue;
+            uint4 v = R::join(in[u]);
             if (Source::kScaled) {
                 float f[R::N];
-                unpack<T>(v[u], f);
+                unpack<T>(v, f);
 #pragma unroll
                 for (int i = 0; i < R::N; ++i) f[i] *= factor;
-                v[u] = pack<T>(f);
+                v = pack<T>(f);
             }
             T* to = y + (int64_t)row[u] * y_ld;
-            R::template store<true>(to, R::column(to, piece[u]), s.C, v[u]);
+            R::template store<true>(to, R::column(to, piece[u]), s.C, v);
         }
     });
+}
+template <typename T, bool kWhole>
+inline MoveShape move_rows_shape(int64_t M, int32_t C, int U) {
+    return move_shape(M, Row<T, kWhole, sizeof(T) == 4>::pieces(C), C, U);
 }
 
 }  // namespace zs
