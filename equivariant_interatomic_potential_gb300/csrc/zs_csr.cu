@@ -264,28 +264,82 @@ csr_downsweep(const int32_t* __restrict__ keys_in, const int32_t* __restrict__ v
 
 // row_ptr from sorted keys: position j is the first of every node in
 // (key[j-1], key[j]]; the count of keys equal to N (invalid) is E - row_ptr[N].
-// Each thread looks at kPer consecutive positions.
-template <int kPer>
+// A thread looks at kRowPtrPer consecutive positions and writes the few nodes
+// between two keys; where they are many, the lanes of its warp write them
+// together (one key of 50021: 332 us by one thread).
+constexpr int kRowPtrPer = 4, kRowPtrFew = 16;
+
 __global__ void __launch_bounds__(256)
 csr_row_ptr(const int32_t* __restrict__ sorted, int64_t E, int32_t N,
             int32_t* __restrict__ row_ptr, int32_t* __restrict__ bad) {
-    const int64_t j0 = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) * kPer;
+    const int64_t j0 = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) * kRowPtrPer;
+    const int lane = threadIdx.x & 31;
     pdl_wait();
     pdl_trigger();
-    if (j0 > E) return;
-    int64_t kprev = j0 > 0 ? (int64_t)__ldg(sorted + j0 - 1) : -1;
+    int64_t kprev = j0 > 0 && j0 <= E ? (int64_t)__ldg(sorted + j0 - 1) : -1;
+    int64_t kcur[kRowPtrPer];
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
+    for (int i = 0; i < kRowPtrPer; ++i) kcur[i] = j0 + i < E ? (int64_t)__ldg(sorted + j0 + i) : (int64_t)N + 1;
+#pragma unroll
+    for (int i = 0; i < kRowPtrPer; ++i) {
         const int64_t j = j0 + i;
-        if (j > E) break;
-        const int64_t kcur = j < E ? (int64_t)__ldg(sorted + j) : (int64_t)N + 1;
-        const int64_t hi = kcur < (int64_t)N ? kcur : (int64_t)N;
-        for (int64_t n = kprev + 1; n <= hi; ++n) {
-            row_ptr[n] = (int32_t)j;
-            if (n == N && bad) *bad = (int32_t)(E - j);
+        const int64_t lo = kprev + 1, hi = j <= E ? imin(kcur[i], (int64_t)N) : -1;   // nodes [lo, hi]
+        if (hi == N && lo <= hi && bad) *bad = (int32_t)(E - j);
+        const bool many = hi - lo >= kRowPtrFew;
+        if (!many)
+            for (int64_t n = lo; n <= hi; ++n) row_ptr[n] = (int32_t)j;
+        for (unsigned m = __ballot_sync(0xffffffffu, many); m; m &= m - 1) {
+            const int src = __ffs(m) - 1;
+            const int64_t from = __shfl_sync(0xffffffffu, lo, src), to = __shfl_sync(0xffffffffu, hi, src);
+            const int at = __shfl_sync(0xffffffffu, (int)j, src);
+            for (int64_t n = from + lane; n <= to; n += 32) row_ptr[n] = at;
         }
-        kprev = kcur;
+        kprev = kcur[i];
     }
+}
+
+// The same where nodes are many more than keys: for each node the first key that
+// is not below it.  A CTA finds where the keys of its 256 nodes lie with as many
+// probes at a time (two rounds for 65536 keys), then each thread its node's in
+// there, three probes at a time.
+struct Found {
+    uint32_t lo, hi;   // the place is in [lo, hi]
+    // after `below` of probes at lo + (i + 1) step - 1 were below the key
+    __device__ __forceinline__ void narrow(uint32_t step, uint32_t below, uint32_t probes) {
+        if (below < probes) hi = imin(hi, lo + (below + 1) * step - 1);
+        lo += below * step;
+    }
+};
+constexpr int kRowPtrNodes = 256;
+
+__global__ void __launch_bounds__(kRowPtrNodes)
+csr_row_ptr_of_few(const int32_t* __restrict__ sorted, int32_t E, int32_t N, int32_t* __restrict__ row_ptr, int32_t* __restrict__ bad) {
+    const int64_t v0 = (int64_t)blockIdx.x * kRowPtrNodes, v = v0 + threadIdx.x;
+    pdl_wait();
+    pdl_trigger();
+    Found first = {0, (uint32_t)E}, last = first;
+    while (first.lo < first.hi || last.lo < last.hi) {
+        const uint32_t p = (first.hi - first.lo + kRowPtrNodes - 1) / kRowPtrNodes, q = (last.hi - last.lo + kRowPtrNodes - 1) / kRowPtrNodes;
+        const uint32_t a = first.lo + (threadIdx.x + 1) * p - 1, b = last.lo + (threadIdx.x + 1) * q - 1;
+        const int before = p && a < first.hi && __ldg(sorted + a) < v0;
+        const int upto = q && b < last.hi && __ldg(sorted + b) < v0 + kRowPtrNodes;
+        first.narrow(p, (uint32_t)__syncthreads_count(before), kRowPtrNodes);
+        last.narrow(q, (uint32_t)__syncthreads_count(upto), kRowPtrNodes);
+    }
+    if (v > N) return;
+    Found at = {first.lo, last.lo};
+    while (at.lo < at.hi) {
+        const uint32_t step = (at.hi - at.lo + 3) / 4;
+        uint32_t below = 0;
+#pragma unroll
+        for (uint32_t i = 0; i < 3; ++i) {
+            const uint32_t p = at.lo + (i + 1) * step - 1;
+            below += p < at.hi && __ldg(sorted + p) < v;
+        }
+        at.narrow(step, below, 3);
+    }
+    row_ptr[v] = (int32_t)at.lo;
+    if (v == N && bad) *bad = E - (int32_t)at.lo;
 }
 
 // ---------------------------------------------------------------------------
@@ -679,18 +733,30 @@ csr_count_single(const int32_t* __restrict__ dst, int64_t E, int32_t N, int roun
     }
 }
 
-// Both passes over at most kFewTiles tiles of 256 * kItems keys: dst by its low digit to (k0, v0), these by their high
-// one to (k1, perm).
+// All passes over at most kFewTiles tiles of 256 * kItems keys, so small that most SMs have one, and no kernel that scans
+// their counts.  These (1 KB a tile, at most 4 bytes a key but for kItems = 1) lie in `hist` if they are one tile's, else where
+// the pass leaves an array free: the last one that of the values it would write, of several the ones before it perm; of two
+// both v[1], which has room behind it for the up to 1 KB that kItems = 1 takes more.  Returns the sorted keys.
 constexpr int kFewTiles = 64;
 template <int kItems>
-void sort_twice(const int32_t* dst, int64_t E, int32_t N, int32_t* k0, int32_t* v0, int32_t* k1, int32_t* perm, int32_t* hist,
-                cudaStream_t s) {
+const int32_t* sort_few(int passes, const int32_t* dst, int64_t E, int32_t N, int32_t* const (&k)[2], int32_t* const (&v)[2], int32_t* perm,
+                        int32_t* hist, cudaStream_t s) {
     const int T = (int)((E + kItems * kCsrThreads - 1) / (kItems * kCsrThreads));
-    const int32_t *none = nullptr, *counts = hist, *kin = k0, *vin = v0;
-    launch(csr_upsweep<true, kItems, true>, T, kCsrThreads, 0, s, dst, E, N, 0, hist, T);
-    launch(csr_downsweep<true, kItems, true>, T, kCsrThreads, 0, s, dst, none, E, N, 0, counts, none, T, k0, v0);
-    launch(csr_upsweep<false, kItems, true>, T, kCsrThreads, 0, s, kin, E, N, 8, hist, T);
-    launch(csr_downsweep<false, kItems, true>, T, kCsrThreads, 0, s, kin, vin, E, N, 8, counts, none, T, k1, perm);
+    const int32_t* none = nullptr;
+    for (int pass = 0; pass < passes; ++pass) {
+        int32_t* counted = T == 1 ? hist : passes == 2 ? v[1] : pass == passes - 1 ? v[pass & 1] : perm;
+        const int32_t* counts = counted;
+        const int32_t *kin = k[1 - (pass & 1)], *vin = v[1 - (pass & 1)];
+        int32_t *kout = k[pass & 1], *vout = pass == passes - 1 ? perm : v[pass & 1];
+        if (pass == 0) {
+            launch(csr_upsweep<true, kItems, true>, T, kCsrThreads, 0, s, dst, E, N, 0, counted, T);
+            launch(csr_downsweep<true, kItems, true>, T, kCsrThreads, 0, s, dst, none, E, N, 0, counts, none, T, kout, vout);
+        } else {
+            launch(csr_upsweep<false, kItems, true>, T, kCsrThreads, 0, s, kin, E, N, 8 * pass, counted, T);
+            launch(csr_downsweep<false, kItems, true>, T, kCsrThreads, 0, s, kin, vin, E, N, 8 * pass, counts, none, T, kout, vout);
+        }
+    }
+    return k[(passes - 1) & 1];
 }
 
 struct CsrPlan {
@@ -786,37 +852,40 @@ extern "C" zs_status zs_build_csr(const int32_t* dst, int64_t E, int32_t N,
     if (E > 0) {
         int32_t* hist = reinterpret_cast<int32_t*>(ws + p.off_hist);
         int32_t* tot = reinterpret_cast<int32_t*>(ws + p.off_tot);
-        int32_t *k0 = reinterpret_cast<int32_t*>(ws + p.off_k[0]), *v0 = reinterpret_cast<int32_t*>(ws + p.off_v[0]);
-        int32_t *k1 = reinterpret_cast<int32_t*>(ws + p.off_k[1]), *v1 = reinterpret_cast<int32_t*>(ws + p.off_v[1]);
-        if (p.passes == 2 && E <= (int64_t)kFewTiles * kTile) {
-            // Two passes over few keys: tiles so small that most SMs have one, and no kernel that scans their counts.  Those
-            // lie where a third pass would put its values, and behind: 4 bytes a key, up to the next 1024.
-            if (E <= kFewTiles * 256) sort_twice<1>(dst, E, N, k0, v0, k1, perm, v1, s);
-            else if (E <= kFewTiles * 512) sort_twice<2>(dst, E, N, k0, v0, k1, perm, v1, s);
-            else if (E <= kFewTiles * 1024) sort_twice<4>(dst, E, N, k0, v0, k1, perm, v1, s);
-            else sort_twice<8>(dst, E, N, k0, v0, k1, perm, v1, s);
-            launch(csr_row_ptr<1>, (unsigned)((E + 1 + 255) / 256), 256, 0, s, (const int32_t*)k1, E, N, row_ptr, bad_dst_count);
-            return check_launch("zs_build_csr");
+        int32_t* const k[2] = {reinterpret_cast<int32_t*>(ws + p.off_k[0]), reinterpret_cast<int32_t*>(ws + p.off_k[1])};
+        int32_t* const v[2] = {reinterpret_cast<int32_t*>(ws + p.off_v[0]), reinterpret_cast<int32_t*>(ws + p.off_v[1])};
+        if (p.passes > 1 && E <= (int64_t)kFewTiles * kTile) {
+            if (E <= kFewTiles * 256 && p.passes == 2) sorted = sort_few<1>(p.passes, dst, E, N, k, v, perm, hist, s);
+            else if (E <= kFewTiles * 512) sorted = sort_few<2>(p.passes, dst, E, N, k, v, perm, hist, s);
+            else if (E <= kFewTiles * 1024) sorted = sort_few<4>(p.passes, dst, E, N, k, v, perm, hist, s);
+            else sorted = sort_few<8>(p.passes, dst, E, N, k, v, perm, hist, s);
+        } else {
+            const int32_t* kin = dst;
+            const int32_t* vin = nullptr;
+            for (int pass = 0; pass < p.passes; ++pass) {
+                const bool first = pass == 0, last = pass == p.passes - 1;
+                const int shift = 8 * pass;
+                int32_t* kout = k[pass & 1];
+                int32_t* vout = last ? perm : v[pass & 1];
+                if (first) launch(csr_upsweep<true, kCsrItems, false>, p.T, kCsrThreads, 0, s, kin, E, N, shift, hist, p.T);
+                else launch(csr_upsweep<false, kCsrItems, false>, p.T, kCsrThreads, 0, s, kin, E, N, shift, hist, p.T);
+                launch(csr_scan, kRadix, kCsrThreads, 0, s, hist, p.T, tot);
+                if (first) launch(csr_downsweep<true, kCsrItems, false>, p.T, kCsrThreads, 0, s, kin, vin, E, N, shift, (const int32_t*)hist, (const int32_t*)tot, p.T, kout, vout);
+                else launch(csr_downsweep<false, kCsrItems, false>, p.T, kCsrThreads, 0, s, kin, vin, E, N, shift, (const int32_t*)hist, (const int32_t*)tot, p.T, kout, vout);
+                kin = kout;
+                vin = vout;
+            }
+            sorted = kin;
         }
-        const int32_t* kin = dst;
-        const int32_t* vin = nullptr;
-        for (int pass = 0; pass < p.passes; ++pass) {
-            const bool first = pass == 0, last = pass == p.passes - 1;
-            const int shift = 8 * pass;
-            int32_t* kout = pass & 1 ? k1 : k0;
-            int32_t* vout = last ? perm : pass & 1 ? v1 : v0;
-            if (first) launch(csr_upsweep<true, kCsrItems, false>, p.T, kCsrThreads, 0, s, kin, E, N, shift, hist, p.T);
-            else launch(csr_upsweep<false, kCsrItems, false>, p.T, kCsrThreads, 0, s, kin, E, N, shift, hist, p.T);
-            launch(csr_scan, kRadix, kCsrThreads, 0, s, hist, p.T, tot);
-            if (first) launch(csr_downsweep<true, kCsrItems, false>, p.T, kCsrThreads, 0, s, kin, vin, E, N, shift, (const int32_t*)hist, (const int32_t*)tot, p.T, kout, vout);
-            else launch(csr_downsweep<false, kCsrItems, false>, p.T, kCsrThreads, 0, s, kin, vin, E, N, shift, (const int32_t*)hist, (const int32_t*)tot, p.T, kout, vout);
-            kin = kout;
-            vin = vout;
-        }
-        sorted = kin;
     }
-    constexpr int kPer = 4;
-    const int64_t threads = (E + 1 + kPer - 1) / kPer;
-    launch(csr_row_ptr<kPer>, (unsigned)((threads + 255) / 256), 256, 0, s, sorted, E, N, row_ptr, bad_dst_count);
+    // From two keys a node on by the keys' positions, else by the nodes (the whole build, positions against nodes: 647170 keys
+    // of 7921 32 us and 33, 65536 of 50021 14.4 and 15.2; but 16384 skewed ones of 50021 24 and 13, 173 of 50021 33 and 7).
+    if (E >= 2 * (int64_t)N) {
+        const int64_t threads = (E + 1 + kRowPtrPer - 1) / kRowPtrPer;
+        launch(csr_row_ptr, (unsigned)((threads + 255) / 256), 256, 0, s, sorted, E, N, row_ptr, bad_dst_count);
+    } else {
+        launch(csr_row_ptr_of_few, (unsigned)(((int64_t)N + kRowPtrNodes) / kRowPtrNodes), kRowPtrNodes, 0, s, sorted, (int32_t)E, N, row_ptr,
+               bad_dst_count);
+    }
     return check_launch("zs_build_csr");
 }

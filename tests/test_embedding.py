@@ -220,3 +220,22 @@ def test_refusals_on_the_device():
         zs.zs_embedding(torch.zeros(8, 4, device="cuda").T, ids)
     with pytest.raises(ValueError, match="perm"):
         zs.zs_embedding_backward(w, ids, ids)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("E,N", [(1, 50021), (173, 32624), (257, 200000), (16384, 50021), (200000, 70000), (131073, 66000), (140001, 70000), (513, 65536), (300, 1 << 24),
+                                 (40000, (1 << 24) + 3), (131072, 100000)])
+@pytest.mark.parametrize("kind", ["uniform", "skewed", "one", "last", "outside"])
+def test_order_of_ids_with_gaps(E, N, kind):
+    # row_ptr is exact however far apart the ids are: few ids of many, all of one, and none
+    u = torch.rand(E, device="cuda", dtype=torch.float64)
+    ids = {"uniform": u * N, "skewed": u**9 * N, "one": torch.full_like(u, N // 3), "last": torch.full_like(u, N - 1),
+           "outside": torch.where(u < 0.3, -1.0, N + 5.0)}[kind].floor().int()
+    row_ptr, perm, bad = zs.zs_build_csr(ids, N)
+    held = (ids >= 0) & (ids < N)
+    count = torch.bincount(ids[held].long(), minlength=N)
+    want = torch.cat([count.new_zeros(1), count.cumsum(0)])
+    assert torch.equal(row_ptr.long(), want)
+    assert int(bad) == int((~held).sum())
+    order = torch.where(held, ids, N).long().sort(stable=True)[1]
+    assert torch.equal(perm.long(), order)
