@@ -163,11 +163,16 @@ csr_downsweep(const int32_t* __restrict__ keys_in, const int32_t* __restrict__ v
     // this tile's offset within each digit, loaded now beside the totals
     int hv = 0, total = 0;
     if (kScan) {
-#pragma unroll 16
-        for (int t = 0; t < T; ++t) {
-            const int c = hist[(int64_t)t * kRadix + tid];
-            hv += t < (int)blockIdx.x ? c : 0;
-            total += c;
+        constexpr int kAtOnce = 16;   // loads in flight, the last ones too
+        for (int t0 = 0; t0 < T; t0 += kAtOnce) {
+            int c[kAtOnce];
+#pragma unroll
+            for (int u = 0; u < kAtOnce; ++u) c[u] = t0 + u < T ? hist[(int64_t)(t0 + u) * kRadix + tid] : 0;
+#pragma unroll
+            for (int u = 0; u < kAtOnce; ++u) {
+                hv += t0 + u < (int)blockIdx.x ? c[u] : 0;
+                total += c[u];
+            }
         }
     } else {
         hv = hist[(int64_t)tid * T + blockIdx.x];

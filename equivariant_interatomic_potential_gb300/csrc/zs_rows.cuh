@@ -113,11 +113,11 @@ struct Row {
         } else {
             v.o = (int)(reinterpret_cast<uintptr_t>(row + e) & 15u);
             v.b = zero();
-            if ((uint32_t)(i - m.margin) < m.inner) {
+            if ((uint32_t)(i - m.margin) < m.inner || (e >= N && e + 2 * N <= C)) {
                 const T* first = row + (e - v.o / (int)sizeof(T));
                 v.a = ld_cached(first);
                 if (v.o) v.b = ld_cached(first + N);
-            } else {   // near the ends of m, where a word may reach out of it: element by element
+            } else {   // at the ends of rows near those of m, where a word may reach out of it: element by element
                 constexpr int kBits = 8 * sizeof(T);
                 v.o = 0;
                 v.a = zero();
