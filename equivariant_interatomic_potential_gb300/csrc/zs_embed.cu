@@ -76,9 +76,15 @@ inline SumShape sum_shape(int64_t M, int32_t V, int32_t C, int vec) {
     s.C = C;
     s.items = M + V;
     s.P = (C + vec - 1) / vec;
-    s.cols = imin(s.P, kSumThreads);
-    s.units = kSumThreads / s.cols;
-    s.ctas_y = (s.P + s.cols - 1) / s.cols;
+    // Columns are cut so that few threads idle: of 256, P of them in each of as many units as fit.  Up to four CTAs a row more
+    // than the least are tried, until five threads of six have work (132 pieces: one CTA has 132 at work, of three each 220).
+    const int least = (s.P + kSumThreads - 1) / kSumThreads;
+    int64_t best = 0;
+    for (int y = least; y <= imin(least + 4, s.P) && best < (int64_t)kSumThreads * 5 / 6 * 1000; ++y) {
+        const int cols = (s.P + y - 1) / y, units = kSumThreads / cols;
+        const int64_t busy = (int64_t)s.P * units * 1000 / y;   // threads of a CTA, on average, in thousandths
+        if (busy > best) best = busy, s.cols = cols, s.units = units, s.ctas_y = y;
+    }
     const int64_t few = (s.items + kSumCluster * s.units - 1) / (kSumCluster * s.units);
     s.cluster = few <= imin(kSumFew, kSumItems / s.units);
     const int64_t target = imax<int64_t>(1, (int64_t)num_sms() * kSumCtas / s.ctas_y);
@@ -300,9 +306,9 @@ __global__ void __launch_bounds__(kSumThreads, kSumCtas) sum_rows(SumShape s, Ro
 
 // For each CTA that closes a row which others have begun: the parts in their order, by slices of threads, the slices in
 // theirs.  W floats at a time where rows of C are whole vectors of them.
-constexpr int kJoinColumns = 256;
+constexpr int kJoinBatch = 8;
 template <typename T, int W>
-__global__ void __launch_bounds__(kSumThreads) join_rows(int32_t C, float scale, const float* __restrict__ head,
+__global__ void __launch_bounds__(kSumThreads) join_rows(int32_t C, int32_t wide, float scale, const float* __restrict__ head,
                                                          const float* __restrict__ tail, const SumNote* __restrict__ notes,
                                                          T* __restrict__ dw) {
     using Vec = typename std::conditional<W == 4, float4, float>::type;
@@ -311,8 +317,8 @@ __global__ void __launch_bounds__(kSumThreads) join_rows(int32_t C, float scale,
     pdl_trigger();
     const SumNote note = notes[blockIdx.x];
     if (note.row < 0) return;
-    const int64_t c0 = (int64_t)blockIdx.y * kJoinColumns;
-    const int cols = (int)imin<int64_t>(kJoinColumns, C - c0) / W;       // vectors of this CTA
+    const int64_t c0 = (int64_t)blockIdx.y * wide;
+    const int cols = (int)imin<int64_t>(wide, C - c0) / W;       // vectors of this CTA
     const int slices = kSumThreads / cols, slice = threadIdx.x / cols, col = threadIdx.x - slice * cols;
     const int last = blockIdx.x, n = last - note.first;   // tails of the CTAs [first, last), then the head of the last
     const int each = (n + slices - 1) / slices;
@@ -325,14 +331,13 @@ __global__ void __launch_bounds__(kSumThreads) join_rows(int32_t C, float scale,
     if (slice < slices) {
         int q = note.first + imin(slice * each, n);
         const int end = note.first + imin((slice + 1) * each, n);
-        for (; q + kSumBatch <= end; q += kSumBatch) {
-            Vec v[kSumBatch];
+        for (; q < end; q += kJoinBatch) {
+            Vec v[kJoinBatch];
 #pragma unroll
-            for (int u = 0; u < kSumBatch; ++u) v[u] = at(tail, q + u);
+            for (int u = 0; u < kJoinBatch; ++u) v[u] = q + u < end ? at(tail, q + u) : Vec{};
 #pragma unroll
-            for (int u = 0; u < kSumBatch; ++u) add(sum, v[u]);
+            for (int u = 0; u < kJoinBatch; ++u) add(sum, v[u]);
         }
-        for (; q < end; ++q) add(sum, at(tail, q));
     }
     if (n > 1) {
         part[threadIdx.x] = sum;
@@ -370,9 +375,13 @@ zs_status embed_backward(const void* dy, int64_t dy_ld, const int32_t* row_ptr, 
     else launch(sum_rows<T, kWhole, false>, grid, block, 0, stream, s, rows, row_ptr, perm, scale, to, head, tail, notes);
     if (zs_status st = check_launch("embedding gradient")) return st;
     if (!s.cluster && s.ctas > 1) {
-        const dim3 columns(s.ctas, (C + kJoinColumns - 1) / kJoinColumns);
+        // as few columns a CTA as its threads are slices of many parts (11841 rows of one id, 256 bf16: 256 columns 17 us, 64
+        // 11), while those without a row do not take longer to start (16384 of 50021, 1024 bf16: 64 columns 39, 256 34)
+        int wide = 64;
+        while (wide < 256 && (int64_t)s.ctas * ((C + wide - 1) / wide) > 2048) wide *= 2;
+        const dim3 columns(s.ctas, (C + wide - 1) / wide);
         auto join = C % 4 ? join_rows<T, 1> : join_rows<T, 4>;
-        launch(join, columns, block, 0, stream, C, scale, (const float*)head, (const float*)tail, (const SumNote*)notes, to);
+        launch(join, columns, block, 0, stream, C, wide, scale, (const float*)head, (const float*)tail, (const SumNote*)notes, to);
         return check_launch("embedding gradient (join)");
     }
     return ZS_OK;
