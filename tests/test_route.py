@@ -316,3 +316,67 @@ def test_refusals_on_the_device():
     ids = torch.zeros(4, 2, dtype=torch.int32, device="cuda")
     with pytest.raises(ValueError, match="dweights"):
         zs.zs_route_backward(torch.zeros(4, 3, device="cuda"), z, ids)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("E,k", [(1, 1), (2, 1), (3, 3), (4, 2), (8, 2), (8, 8), (13, 4), (16, 16), (17, 4)])
+def test_many_rows_of_few_experts(E, k, dtype):
+    # closed experts, ties, NaN, rows at strides and views off 16-byte boundaries among them
+    rng = np.random.default_rng(E + 7 * k)
+    M = 4099
+    a = rng.standard_normal((M, E)) * 1.5
+    a[rng.random((M, E)) < np.linspace(0, 0.5, M)[:, None]] = -np.inf
+    a[-1] = -np.inf
+    a[5:400] = rng.integers(0, 3, (395, E))
+    z, zd = held(a, dtype)
+    z = z.cuda()
+    for score, biased, renormalise in itertools.product(("softmax", "sigmoid"), (False, True), (False, True)):
+        bias = (rng.standard_normal(E) * 0.2).astype(np.float32) if biased else None
+        ids, w, dz = check(z, zd, k, bias, score, 1, 1, 1, renormalise, 2.5, dtype, rng)
+        assert bool((ids[-1] == -1).all()) and not bool(w[-1].any()) and not bool(dz[-1].any())
+        wide = torch.full((M, E + 3), float("nan"), dtype=z.dtype, device="cuda")
+        wide[:, 1:1 + E] = z
+        view = wide[:, 1:1 + E]
+        how = dict(score=score, renormalise=renormalise, scale=2.5)
+        again = zs.zs_route(view, k, None if bias is None else torch.from_numpy(bias).cuda(), **how)
+        assert torch.equal(again[0], ids) and torch.equal(again[1], w)
+        g = torch.ones_like(w)
+        assert torch.equal(zs.zs_route_backward(g, view, ids, **how), zs.zs_route_backward(g, z, ids, **how))
+        # a row of NaN is its own affair, and so is one of infinity
+        bad = z.clone()
+        bad[77] = float("nan")
+        bad[78, 0] = float("inf")
+        got, gw = zs.zs_route(bad, k, None if bias is None else torch.from_numpy(bias).cuda(), **how)
+        keep = torch.ones(M, dtype=torch.bool, device="cuda")
+        keep[77:79] = False
+        assert torch.equal(got[keep], ids[keep]) and torch.equal(gw[keep], w[keep])
+        assert got[77].tolist() == list(range(k)) and bool(torch.isnan(gw[77]).all())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_few_experts_closer_than_32_bits(score):
+    # as above, a thread's row: rows that 64 bits have to tell, beside others that they need not
+    rng = np.random.default_rng(17)
+    M, E, k = 4200, 12, 5
+    z = rng.standard_normal((M, E)).astype(np.float32)
+    z[::3] = z[0]
+    s = ref.scores(z[:1].astype(np.float64), score)
+    bias = (0.5 - s[0]).astype(np.float32)
+    ids, _ = zs.zs_route(torch.from_numpy(z).cuda(), k, torch.from_numpy(bias).cuda(), score)
+    a = ref.scores(z.astype(np.float64), score) + bias.astype(np.float64)
+    assert np.array_equal(ids.cpu().numpy(), np.argsort(-a, axis=1, kind="stable")[:, :k])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("renormalise", [True, False])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_few_experts_named_twice(score, renormalise):
+    # the gradient of ids that hold an expert twice, or none: cotangents of the same expert add up, as for few rows
+    torch.manual_seed(3)
+    z, g = torch.randn(4100, 8, device="cuda"), torch.randn(4100, 3, device="cuda")
+    ids = torch.randint(-1, 8, (4100, 3), device="cuda", dtype=torch.int32)
+    many = zs.zs_route_backward(g, z, ids, score, renormalise)
+    few = torch.cat([zs.zs_route_backward(g[i:i + 100], z[i:i + 100], ids[i:i + 100], score, renormalise) for i in range(0, 4100, 100)])
+    assert bool(((many - few).abs() <= 2.0 ** -18 * (1 + g.abs().sum(1, keepdim=True))).all())
