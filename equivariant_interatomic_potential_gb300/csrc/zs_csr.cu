@@ -690,7 +690,7 @@ csr_count_scatter(const int32_t* __restrict__ dst, const uint16_t* __restrict__ 
 // path in one CTA and one launch -- csr_count_rank's ranking and counts, then
 // csr_count_scatter's node bases and scatter, the counts staying in shared
 // memory (with one tile, every edge's offset within its key is its rank).
-constexpr int kSingleMaxEdges = 8 * kCntThreads;   // 4096: 6.4 to 7.8 us; 8192 edges took 9.4 to 15, 6 in three launches
+constexpr int kSingleMaxEdges = 8 * kCntThreads;   // 4096: 6.4 to 8.3 us; 8192 edges took 9.4 to 15, 6 in three launches
 inline int count_single_smem(int nkeys, int rounds) {
     return count_rank_smem(nkeys, rounds) + 2 * count_pairs(nkeys) * 4;
 }
@@ -736,6 +736,71 @@ csr_count_single(const int32_t* __restrict__ dst, int64_t E, int32_t N, int roun
         const uint32_t p = packed[i];
         perm[ktot[p >> 16] + (int32_t)(p & 0xffffu)] = i;
     }
+}
+
+// The same by a cluster of kGroupCtas CTAs, a tile each: what the others counted
+// is read from their shared memory, so that no counts go through global memory
+// and no second kernel waits for them (89 keys: 4096 edges 3.8 us, one CTA 7.1;
+// 8192 4.2 and 12291 5.4, three launches 6.5 and 6.2; 1000 as long as one CTA).
+constexpr int kGroupCtas = 8, kGroupMinEdges = 1024, kGroupMaxKeys = 1024, kGroupMaxRounds = 4;
+inline int count_group_smem(int nkeys, int rounds) { return count_rank_smem(nkeys, rounds) + 6 * count_pairs(nkeys) * 4; }
+
+__global__ void __launch_bounds__(kCntThreads, 1)
+csr_count_group(const int32_t* __restrict__ dst, int64_t E, int32_t N, int rounds,
+                int32_t* __restrict__ perm, int32_t* __restrict__ row_ptr, int32_t* __restrict__ bad) {
+    extern __shared__ uint32_t cnt_words[];
+    __shared__ int32_t wsum[kCntWarps];
+    const int nkeys = N + 1;
+    const int npairs = count_pairs(nkeys);
+    uint16_t* cnt = reinterpret_cast<uint16_t*>(cnt_words);
+    uint32_t* packed = cnt_words + kCntWarps * npairs;                           // [TS]: key << 16 | rank
+    int32_t* mine = reinterpret_cast<int32_t*>(packed + rounds * kCntThreads);   // [2 * npairs]: this tile's counts
+    int32_t* tot = mine + 2 * npairs;                                            // all tiles'
+    int32_t* base = tot + 2 * npairs;                                            // those of the tiles before, then positions
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int TW = rounds * 32;
+    const int tbase = (int)blockIdx.x * rounds * kCntThreads;
+    const int n = imax(imin(rounds * kCntThreads, (int)E - tbase), 0);
+    pdl_wait();
+    pdl_trigger();
+    copy_ints(reinterpret_cast<int32_t*>(packed), dst + (n > 0 ? tbase : 0), n, tid, kCntThreads);
+    for (int i = tid; i < kCntWarps * npairs / 4; i += kCntThreads) reinterpret_cast<uint4*>(cnt_words)[i] = make_uint4(0u, 0u, 0u, 0u);
+    cp_async_wait_all();
+    __syncthreads();
+    rank_in_warp(packed, cnt + 2 * warp * npairs, rounds, n, N, warp, lane);
+    __syncthreads();
+    for (int q = tid; q < npairs; q += kCntThreads) {
+        const uint32_t run = prefix_over_warps(cnt_words, npairs, q);
+        mine[2 * q] = (int32_t)(run & 0xffffu);
+        mine[2 * q + 1] = (int32_t)(run >> 16);
+    }
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    for (int k = tid; k < nkeys; k += kCntThreads) {
+        const uint32_t at = static_cast<uint32_t>(__cvta_generic_to_shared(mine + k));
+        int32_t c[kGroupCtas], all = 0, before = 0;
+#pragma unroll
+        for (int r = 0; r < kGroupCtas; ++r)
+            asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %1, %2;\n\tld.shared::cluster.s32 %0, [a];\n\t}"
+                         : "=r"(c[r]) : "r"(at), "r"(r) : "memory");
+#pragma unroll
+        for (int r = 0; r < kGroupCtas; ++r) {
+            all += c[r];
+            before += r < (int)blockIdx.x ? c[r] : 0;
+        }
+        tot[k] = all;
+        base[k] = before;
+    }
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");   // no CTA ends before all have read
+    __syncthreads();
+    key_bases(tot, base, base, nkeys, N, wsum, blockIdx.x == 0 ? row_ptr : nullptr, bad);
+    __syncthreads();
+#pragma unroll 4
+    for (int i = tid; i < n; i += kCntThreads) {
+        const uint32_t p = packed[i];
+        perm[base[p >> 16] + (int32_t)((p & 0xffffu) + cnt[2 * (i / TW) * npairs + (p >> 16)])] = tbase + i;
+    }
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 // All passes over at most kFewTiles tiles of 256 * kItems keys, so small that most SMs have one, and no kernel that scans
@@ -832,6 +897,14 @@ extern "C" zs_status zs_build_csr(const int32_t* dst, int64_t E, int32_t N,
         int32_t* M = reinterpret_cast<int32_t*>(ws + p.off_hist);
         int32_t* tot = reinterpret_cast<int32_t*>(ws + p.off_tot);
         uint16_t* rank = reinterpret_cast<uint16_t*>(ws + p.off_rank);
+        if (E > kGroupMinEdges && E <= kGroupCtas * kGroupMaxRounds * kCntThreads && N < kGroupMaxKeys) {
+            static std::atomic<uint64_t> group_smem_set[kMaxDevices];
+            set_smem_limit_once(csr_count_group, count_group_smem(kGroupMaxKeys, kGroupMaxRounds), group_smem_set);
+            const int rounds = (int)((E + kGroupCtas * kCntThreads - 1) / (kGroupCtas * kCntThreads));
+            launch_clusters(kGroupCtas, csr_count_group, kGroupCtas, kCntThreads, count_group_smem(N + 1, rounds), s, dst, E, N, rounds, perm,
+                            row_ptr, bad_dst_count);
+            return check_launch("zs_build_csr");
+        }
         if (E <= kSingleMaxEdges) {
             static std::atomic<uint64_t> single_smem_set[kMaxDevices];
             set_smem_limit_once(csr_count_single, count_single_smem(kCntMaxKeys, kCntMaxRounds), single_smem_set);
