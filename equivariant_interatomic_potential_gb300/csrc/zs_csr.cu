@@ -9,7 +9,8 @@
 //
 // Counting path (N + 1 <= kCntMaxKeys, every bench-sized graph but the
 // largest): one pass, three launches with no inter-CTA waiting (one launch of
-// one CTA, count_single, for up to kSingleMaxEdges edges):
+// one CTA, count_single, for up to kSingleMaxEdges edges; of up to kGroupMaxKeys
+// keys one of a cluster, count_group, from 1024 to 16384 edges):
 //   count_rank    -- per tile of edges, each edge's stable rank among the
 //                    tile's edges of the same node (warp match + per-warp
 //                    running counts in shared memory, then a prefix over
@@ -24,7 +25,8 @@
 //   downsweep -- per tile, stable rank of every key among equal digits
 //                (warp ballots + per-warp running counts), staged in shared
 //                memory in digit order and written out run by run
-// and a final pass that reads the sorted keys to write row_ptr.
+// and a final pass that reads the sorted keys to write row_ptr.  Up to a million
+// keys a pass takes two launches (sort_few): the downsweep adds up the counts.
 #include "zs_common.cuh"
 
 namespace zs {
@@ -91,6 +93,50 @@ csr_upsweep(const int32_t* __restrict__ keys_in, int64_t E, int32_t N, int shift
     hist[kByTile ? (int64_t)blockIdx.x * kRadix + tid : (int64_t)tid * T + blockIdx.x] = cnt[tid];
 }
 
+// The counts of kTileGroup tiles, a cluster's, in place of each tile's: those of the tiles before it in the group to `before`,
+// a tile's together, and the group's to `groups`.  A CTA adds up 32 digits, which it reads from the others' shared memory.
+constexpr int kTileGroup = 8;
+template <bool kFirst, int kItems>
+__global__ void __launch_bounds__(kCsrThreads)
+csr_upsweep_group(const int32_t* __restrict__ keys_in, int64_t E, int32_t N, int shift, int32_t* __restrict__ before,
+                  int32_t* __restrict__ groups) {
+    __shared__ int cnt[kRadix];
+    const int tid = threadIdx.x;
+    cnt[tid] = 0;
+    pdl_wait();
+    pdl_trigger();
+    __syncthreads();
+    const int64_t base = (int64_t)blockIdx.x * (kItems * kCsrThreads);
+    int dig[kItems];
+#pragma unroll
+    for (int u = 0; u < kItems; ++u) {
+        const int64_t idx = base + u * kCsrThreads + tid;
+        dig[u] = idx < E ? (key_of(keys_in, idx, N, kFirst) >> shift) & (kRadix - 1) : -1;
+    }
+#pragma unroll
+    for (int u = 0; u < kItems; ++u)
+        if (dig[u] >= 0) atomicAdd(&cnt[dig[u]], 1);
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    if (tid < kRadix / kTileGroup) {
+        const int group = blockIdx.x / kTileGroup, d = (blockIdx.x % kTileGroup) * (kRadix / kTileGroup) + tid;
+        const uint32_t at = static_cast<uint32_t>(__cvta_generic_to_shared(cnt + d));
+        int c[kTileGroup], run = 0;
+#pragma unroll
+        for (int r = 0; r < kTileGroup; ++r)
+            asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %1, %2;\n\tld.shared::cluster.s32 %0, [a];\n\t}"
+                         : "=r"(c[r]) : "r"(at), "r"(r) : "memory");
+#pragma unroll
+        for (int r = 0; r < kTileGroup; ++r) {
+            before[(int64_t)(group * kTileGroup + r) * kRadix + d] = run;
+            run += c[r];
+        }
+        groups[(int64_t)group * kRadix + d] = run;
+    }
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");   // no CTA ends before all have read
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
 // One CTA per row: exclusive scan of hist[d, 0..T) in place, total to tot[d].
 // Thread i takes the consecutive entries [i * per, (i + 1) * per), all loaded
 // before they are added (a row is one round trip of loads, not one per
@@ -142,9 +188,11 @@ csr_scan(int32_t* __restrict__ hist, int T, int32_t* __restrict__ tot) {
     if (tid == 0) tot[blockIdx.x] = carry;
 }
 
-// kScan: hist holds the tiles' counts as csr_upsweep<.., kByTile> left them (few
-// tiles), which every CTA adds up itself.
-template <bool kFirst, int kItems, bool kScan>
+// kScan 0: hist and tot of csr_scan.  1: hist holds the T tiles' counts as
+// csr_upsweep<.., kByTile> left them (few tiles), which every CTA adds up itself.
+// 2: those of T groups of tiles, and tot what is before each tile in its group,
+// as csr_upsweep_group left them.
+template <bool kFirst, int kItems, int kScan>
 __global__ void __launch_bounds__(kCsrThreads)
 csr_downsweep(const int32_t* __restrict__ keys_in, const int32_t* __restrict__ vals_in,
               int64_t E, int32_t N, int shift,
@@ -160,8 +208,22 @@ csr_downsweep(const int32_t* __restrict__ keys_in, const int32_t* __restrict__ v
     pdl_wait();
     pdl_trigger();
 
+    const int64_t base = (int64_t)blockIdx.x * kTileKeys + (int64_t)warp * kItems * 32;
+    int32_t key[kItems], val[kItems];
+    int rank[kItems], dig[kItems];
+    const unsigned lt = lanemask_lt();
+    // every item's key and value are on their way before the digits' places are
+    // added up and the ranking starts (whose synchronisations would hold them back)
+#pragma unroll
+    for (int i = 0; i < kItems; ++i) {
+        const int64_t idx = base + i * 32 + lane;
+        const bool valid = idx < E;
+        key[i] = valid ? key_of(keys_in, idx, N, kFirst) : 0;
+        val[i] = valid ? (kFirst ? (int32_t)idx : __ldg(vals_in + idx)) : 0;
+        dig[i] = valid ? ((key[i] >> shift) & (kRadix - 1)) : kRadix;
+    }
     // this tile's offset within each digit, loaded now beside the totals
-    int hv = 0, total = 0;
+    int hv = kScan == 2 ? tot[(int64_t)blockIdx.x * kRadix + tid] : 0, total = 0;
     if (kScan) {
         constexpr int kAtOnce = 16;   // loads in flight, the last ones too
         for (int t0 = 0; t0 < T; t0 += kAtOnce) {
@@ -170,7 +232,7 @@ csr_downsweep(const int32_t* __restrict__ keys_in, const int32_t* __restrict__ v
             for (int u = 0; u < kAtOnce; ++u) c[u] = t0 + u < T ? hist[(int64_t)(t0 + u) * kRadix + tid] : 0;
 #pragma unroll
             for (int u = 0; u < kAtOnce; ++u) {
-                hv += t0 + u < (int)blockIdx.x ? c[u] : 0;
+                hv += t0 + u < (int)blockIdx.x / (kScan == 2 ? kTileGroup : 1) ? c[u] : 0;
                 total += c[u];
             }
         }
@@ -195,20 +257,6 @@ csr_downsweep(const int32_t* __restrict__ keys_in, const int32_t* __restrict__ v
     }
     __syncthreads();
 
-    const int64_t base = (int64_t)blockIdx.x * kTileKeys + (int64_t)warp * kItems * 32;
-    int32_t key[kItems], val[kItems];
-    int rank[kItems], dig[kItems];
-    const unsigned lt = lanemask_lt();
-    // every item's key and value are loaded before the ranking starts (its
-    // warp synchronisations would otherwise hold each load back to its round)
-#pragma unroll
-    for (int i = 0; i < kItems; ++i) {
-        const int64_t idx = base + i * 32 + lane;
-        const bool valid = idx < E;
-        key[i] = valid ? key_of(keys_in, idx, N, kFirst) : 0;
-        val[i] = valid ? (kFirst ? (int32_t)idx : __ldg(vals_in + idx)) : 0;
-        dig[i] = valid ? ((key[i] >> shift) & (kRadix - 1)) : kRadix;
-    }
 #pragma unroll
     for (int i = 0; i < kItems; ++i) {
         const bool valid = dig[i] < kRadix;
@@ -803,28 +851,35 @@ csr_count_group(const int32_t* __restrict__ dst, int64_t E, int32_t N, int round
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// All passes over at most kFewTiles tiles of 256 * kItems keys, so small that most SMs have one, and no kernel that scans
-// their counts.  These (1 KB a tile, at most 4 bytes a key but for kItems = 1) lie in `hist` if they are one tile's, else where
-// the pass leaves an array free: the last one that of the values it would write, of several the ones before it perm; of two
-// both v[1], which has room behind it for the up to 1 KB that kItems = 1 takes more.  Returns the sorted keys.
+// All passes over tiles of 256 * kItems keys, at most kFewTiles of them (so small that most SMs have one) or of groups of them
+// (kGroups), and no kernel that scans their counts (262144 keys of 7921: 21 us, 30 with one).  These (1 KB a tile, at most 4
+// bytes a key but for kItems = 1) lie in `hist` if they are one tile's, else where the pass leaves an array free: the last one
+// that of the values it would write, of several the ones before it perm; of two both v[1], which has room behind it for the up
+// to 1 KB that kItems = 1 takes more.  Returns the sorted keys.
 constexpr int kFewTiles = 64;
-template <int kItems>
+template <int kItems, bool kGroups = false>
 const int32_t* sort_few(int passes, const int32_t* dst, int64_t E, int32_t N, int32_t* const (&k)[2], int32_t* const (&v)[2], int32_t* perm,
                         int32_t* hist, cudaStream_t s) {
-    const int T = (int)((E + kItems * kCsrThreads - 1) / (kItems * kCsrThreads));
+    const int T = (int)((E + kItems * kCsrThreads - 1) / (kItems * kCsrThreads)), G = (T + kTileGroup - 1) / kTileGroup;
     const int32_t* none = nullptr;
+    auto pass_of = [&](auto first, int pass, const int32_t* kin, const int32_t* vin, int32_t* kout, int32_t* vout, int32_t* counted) {
+        constexpr bool kFirst = decltype(first)::value;
+        if constexpr (kGroups) {
+            int32_t* groups = counted + (int64_t)G * kTileGroup * kRadix;
+            launch_clusters(kTileGroup, csr_upsweep_group<kFirst, kItems>, G * kTileGroup, kCsrThreads, 0, s, kin, E, N, 8 * pass, counted, groups);
+            launch(csr_downsweep<kFirst, kItems, 2>, T, kCsrThreads, 0, s, kin, vin, E, N, 8 * pass, (const int32_t*)groups,
+                   (const int32_t*)counted, G, kout, vout);
+        } else {
+            launch(csr_upsweep<kFirst, kItems, true>, T, kCsrThreads, 0, s, kin, E, N, 8 * pass, counted, T);
+            launch(csr_downsweep<kFirst, kItems, 1>, T, kCsrThreads, 0, s, kin, vin, E, N, 8 * pass, (const int32_t*)counted, none, T, kout,
+                   vout);
+        }
+    };
     for (int pass = 0; pass < passes; ++pass) {
         int32_t* counted = T == 1 ? hist : passes == 2 ? v[1] : pass == passes - 1 ? v[pass & 1] : perm;
-        const int32_t* counts = counted;
-        const int32_t *kin = k[1 - (pass & 1)], *vin = v[1 - (pass & 1)];
         int32_t *kout = k[pass & 1], *vout = pass == passes - 1 ? perm : v[pass & 1];
-        if (pass == 0) {
-            launch(csr_upsweep<true, kItems, true>, T, kCsrThreads, 0, s, dst, E, N, 0, counted, T);
-            launch(csr_downsweep<true, kItems, true>, T, kCsrThreads, 0, s, dst, none, E, N, 0, counts, none, T, kout, vout);
-        } else {
-            launch(csr_upsweep<false, kItems, true>, T, kCsrThreads, 0, s, kin, E, N, 8 * pass, counted, T);
-            launch(csr_downsweep<false, kItems, true>, T, kCsrThreads, 0, s, kin, vin, E, N, 8 * pass, counts, none, T, kout, vout);
-        }
+        if (pass == 0) pass_of(std::true_type(), 0, dst, none, kout, vout, counted);
+        else pass_of(std::false_type(), pass, k[1 - (pass & 1)], v[1 - (pass & 1)], kout, vout, counted);
     }
     return k[(passes - 1) & 1];
 }
@@ -937,6 +992,11 @@ extern "C" zs_status zs_build_csr(const int32_t* dst, int64_t E, int32_t N,
             else if (E <= kFewTiles * 512) sorted = sort_few<2>(p.passes, dst, E, N, k, v, perm, hist, s);
             else if (E <= kFewTiles * 1024) sorted = sort_few<4>(p.passes, dst, E, N, k, v, perm, hist, s);
             else sorted = sort_few<8>(p.passes, dst, E, N, k, v, perm, hist, s);
+        } else if (p.passes > 1 && E <= (int64_t)kFewTiles * kTileGroup * kTile) {
+            // twice as large tiles where they are about one for each SM (of 7921: 400000 keys 23.8 us with 8 a thread, 23.3 with
+            // 16; 647170 31.5 and 29.5, 800000 32.8 and 30.4; 1048576 32.9 and 34.6)
+            if (E > 256 * (int64_t)kTile && E <= 400 * (int64_t)kTile) sorted = sort_few<2 * kCsrItems, true>(p.passes, dst, E, N, k, v, perm, hist, s);
+            else sorted = sort_few<kCsrItems, true>(p.passes, dst, E, N, k, v, perm, hist, s);
         } else {
             const int32_t* kin = dst;
             const int32_t* vin = nullptr;
@@ -948,8 +1008,8 @@ extern "C" zs_status zs_build_csr(const int32_t* dst, int64_t E, int32_t N,
                 if (first) launch(csr_upsweep<true, kCsrItems, false>, p.T, kCsrThreads, 0, s, kin, E, N, shift, hist, p.T);
                 else launch(csr_upsweep<false, kCsrItems, false>, p.T, kCsrThreads, 0, s, kin, E, N, shift, hist, p.T);
                 launch(csr_scan, kRadix, kCsrThreads, 0, s, hist, p.T, tot);
-                if (first) launch(csr_downsweep<true, kCsrItems, false>, p.T, kCsrThreads, 0, s, kin, vin, E, N, shift, (const int32_t*)hist, (const int32_t*)tot, p.T, kout, vout);
-                else launch(csr_downsweep<false, kCsrItems, false>, p.T, kCsrThreads, 0, s, kin, vin, E, N, shift, (const int32_t*)hist, (const int32_t*)tot, p.T, kout, vout);
+                if (first) launch(csr_downsweep<true, kCsrItems, 0>, p.T, kCsrThreads, 0, s, kin, vin, E, N, shift, (const int32_t*)hist, (const int32_t*)tot, p.T, kout, vout);
+                else launch(csr_downsweep<false, kCsrItems, 0>, p.T, kCsrThreads, 0, s, kin, vin, E, N, shift, (const int32_t*)hist, (const int32_t*)tot, p.T, kout, vout);
                 kin = kout;
                 vin = vout;
             }
@@ -957,7 +1017,7 @@ extern "C" zs_status zs_build_csr(const int32_t* dst, int64_t E, int32_t N,
         }
     }
     // From two keys a node on by the keys' positions, else by the nodes (the whole build, positions against nodes: 647170 keys
-    // of 7921 32 us and 33, 65536 of 50021 14.4 and 15.2; but 16384 skewed ones of 50021 24 and 13, 173 of 50021 33 and 7).
+    // of 7921 30 us and 31, 65536 of 50021 14.4 and 15.2; but 16384 skewed ones of 50021 24 and 13, 173 of 50021 33 and 7).
     if (E >= 2 * (int64_t)N) {
         const int64_t threads = (E + 1 + kRowPtrPer - 1) / kRowPtrPer;
         launch(csr_row_ptr, (unsigned)((threads + 255) / 256), 256, 0, s, sorted, E, N, row_ptr, bad_dst_count);

@@ -223,8 +223,9 @@ def test_refusals_on_the_device():
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("E,N", [(1, 50021), (173, 32624), (257, 200000), (16384, 50021), (200000, 70000), (131073, 66000), (140001, 70000), (513, 65536), (300, 1 << 24),
-                                 (40000, (1 << 24) + 3), (131072, 100000)])
+@pytest.mark.parametrize("E,N", [(1, 50021), (173, 32624), (257, 200000), (16384, 50021), (200000, 70000), (131073, 66000), (140001, 70000),
+                                 (513, 65536), (300, 1 << 24), (40000, (1 << 24) + 3), (131072, 100000), (262145, 30000), (600001, 70000),
+                                 (819201, 9000), (1048577, 6000), (1025, 1023), (5000, 37), (16384, 900), (12289, 1), (4097, 1024)])
 @pytest.mark.parametrize("kind", ["uniform", "skewed", "one", "last", "outside"])
 def test_order_of_ids_with_gaps(E, N, kind):
     # row_ptr is exact however far apart the ids are: few ids of many, all of one, and none
