@@ -1,6 +1,7 @@
 // Routing of rows to experts, and the gradient of the logits.
 //
-// A warp takes a row.  Its lanes hold up to V experts each in ascending order,
+// A warp takes a row (a thread where experts are few and rows many, see
+// route_rows_of_few).  Its lanes hold up to V experts each in ascending order,
 // those of a group of experts in neighbouring lanes, so that the lowest lane
 // among equal ones has the lowest index.  Values become unsigned keys that sort
 // like them (0: closed), the last bits of a key the expert's place in its lane.
