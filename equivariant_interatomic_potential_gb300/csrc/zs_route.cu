@@ -251,6 +251,9 @@ __device__ __forceinline__ void load_lane(const T* p, int count, bool wide, floa
     for (int i = 0; i < V; ++i) z[i] = i < count ? to_f32(__ldg(p + i)) : none;
 }
 
+// t / sum: exactly 1 for the only one, whose gradient then is 0.
+__device__ __forceinline__ float share_of(float t, float sum) { return t == sum ? 1.f : __fdividef(t, sum); }
+
 // Shares of the chosen logits z (lanes with `held`) among those of `width` lanes: softmax, or sigmoids over their sum.
 __device__ __forceinline__ float renormalised(bool sigmoid, bool held, float z, int width) {
     float top = held ? z : -INFINITY;
@@ -263,7 +266,7 @@ __device__ __forceinline__ float renormalised(bool sigmoid, bool held, float z, 
     }
     float sum = t;
     for (int o = width >> 1; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
-    return held ? __fdividef(t, sum) : 0.f;
+    return held ? share_of(t, sum) : 0.f;
 }
 __device__ __forceinline__ float sigmoid_of(float z) { return __fdividef(1.f, 1.f + expf(-z)); }
 
@@ -618,7 +621,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_rows_of_few(RouteShape
                 float w = 0.f;
                 if (j < n) {
                     const float z = logit(row, chosen(j));
-                    w = s.scale * (s.renormalise ? __fdividef(part(z), all) : s.sigmoid ? sigmoid_of(z) : __fdividef(expf(z - top), sum));
+                    w = s.scale * (s.renormalise ? share_of(part(z), all) : s.sigmoid ? sigmoid_of(z) : __fdividef(expf(z - top), sum));
                 }
                 ids[r0 * s.k + j] = j < n ? chosen(j) : -1;
                 weights[r0 * s.k + j] = w;
@@ -655,7 +658,7 @@ __global__ void __launch_bounds__(kBackWarps<V> * 32) route_rows_backward(RouteS
     const int id = lane < s.k ? __ldg(ids + r0 * s.k + lane) : -1;
     const bool held = (uint32_t)id < (uint32_t)s.E;
     const float z = held ? logit(row, id) : -INFINITY;
-    const float d = held ? __ldg(dweights + r0 * s.k + lane) * s.scale : 0.f;
+    const float d = held ? __fmul_rn(__ldg(dweights + r0 * s.k + lane), s.scale) : 0.f;   // rounded: the mean of one is itself
     float mean = 0.f, own = d;
     if (kWhole) {
         float top = e[0], sum = 0.f;
@@ -720,7 +723,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_rows_backward_of_few(R
 #pragma unroll 1
         for (int j = 0; j < s.k; ++j) {
             const int id = __ldg(ids + r0 * s.k + j);
-            if ((uint32_t)id < (uint32_t)s.E) f(id, logit(row, id), __ldg(dweights + r0 * s.k + j) * s.scale);
+            if ((uint32_t)id < (uint32_t)s.E) f(id, logit(row, id), __fmul_rn(__ldg(dweights + r0 * s.k + j), s.scale));   // rounded: the mean of one is itself
         }
     };
     auto give = [&](int id, float v) {
@@ -750,9 +753,9 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_rows_backward_of_few(R
         };
         of_choices([&](int, float at, float) { first = fmaxf(first, at); });
         of_choices([&](int, float at, float) { sum += part(at); });
-        of_choices([&](int, float at, float d) { mean += __fdividef(part(at), sum) * d; });
+        of_choices([&](int, float at, float d) { mean += share_of(part(at), sum) * d; });
         of_choices([&](int id, float at, float d) {
-            const float own = __fdividef(part(at), sum) * (d - mean);
+            const float own = share_of(part(at), sum) * (d - mean);
             give(id, s.sigmoid ? own * sigmoid_of(-at) : own);
         });
     } else {

@@ -380,3 +380,20 @@ def test_few_experts_named_twice(score, renormalise):
     many = zs.zs_route_backward(g, z, ids, score, renormalise)
     few = torch.cat([zs.zs_route_backward(g[i:i + 100], z[i:i + 100], ids[i:i + 100], score, renormalise) for i in range(0, 4100, 100)])
     assert bool(((many - few).abs() <= 2.0 ** -18 * (1 + g.abs().sum(1, keepdim=True))).all())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("M,E", [(15, 13), (5000, 13), (300, 64), (70, 1000)])
+def test_only_choice(M, E, score, dtype):
+    # the renormalised weight of the only choice is 1, whatever its score, and the logits have no gradient: exactly
+    z = (torch.randn(M, E, device="cuda", generator=torch.Generator(device="cuda").manual_seed(2)) * 3).to(dtype)
+    ids, w = zs.zs_route(z, 1, score=score, scale=2.5)
+    assert bool((w == 2.5).all())
+    g = torch.randn(M, 1, device="cuda")
+    assert not bool(zs.zs_route_backward(g, z, ids, score, True, 2.5).any())
+    z[:, 1:] = -float("inf")                       # and of the only one that is open
+    ids, w = zs.zs_route(z, 4, score=score, scale=2.5)
+    assert bool((w[:, 0] == 2.5).all()) and not bool(w[:, 1:].any())
+    assert not bool(zs.zs_route_backward(torch.randn(M, 4, device="cuda"), z, ids, score, True, 2.5).any())
