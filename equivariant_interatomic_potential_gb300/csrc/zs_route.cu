@@ -301,7 +301,8 @@ __device__ __forceinline__ bool near_keys(uint32_t a, uint32_t b, float error) {
 
 // Of the groups of the mask `border`, between which 32 bits do not tell, the `need` best as a mask: the elements of each
 // that may be among its two largest, in 64 bits, a lane each; groups of nothing but one logit and bias (a router that has
-// learnt nothing) by their numbers.  0 where there are too many, or a softmax has a bias.  `head` is a lane's first key.
+// learnt nothing), and all of one or all of two terms, by their numbers.  0 where there are too many, or a softmax has a
+// bias.  `head` is a lane's first key.
 template <typename T, int V>
 __device__ __noinline__ unsigned border_groups(const RouteShape& s, int lane, const T* __restrict__ row, const float* __restrict__ bias,
                                                RouteSpace<V>& space, uint32_t head, float error, unsigned border, int need) {
@@ -326,7 +327,10 @@ __device__ __noinline__ unsigned border_groups(const RouteShape& s, int lane, co
     if (n > 32 || (!s.sigmoid && bias)) {
         const int e = expert_of<V>(s, space.taken[0]);
         const float z = logit(row, e), b = bias ? __ldg(bias + e) : 0.f;
-        bool alike = true;
+        // one term against two of the same score are not alike, and may be as near to each other as the score is to 0
+        const bool in = border >> l.group & 1u, alone = s.group_top == 2 && second == 0;
+        const unsigned of_one = __ballot_sync(kAll, in && alone), of_two = __ballot_sync(kAll, in && !alone);
+        bool alike = !of_one || !of_two;
         for (int i = 0; i < mine; ++i) {
             const int f = expert_of<V>(s, make_uint2(i == 0 ? head : space.list[i][lane], lane));
             alike = alike && logit(row, f) == z && (!bias || __ldg(bias + f) == b);

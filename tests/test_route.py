@@ -397,3 +397,38 @@ def test_only_choice(M, E, score, dtype):
     ids, w = zs.zs_route(z, 4, score=score, scale=2.5)
     assert bool((w[:, 0] == 2.5).all()) and not bool(w[:, 1:].any())
     assert not bool(zs.zs_route_backward(torch.randn(M, 4, device="cuda"), z, ids, score, True, 2.5).any())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("group_top", [1, 2])
+@pytest.mark.parametrize("E,k,groups,top_groups", [(8, 3, 4, 2), (64, 6, 8, 3), (256, 8, 8, 4), (96, 4, 32, 6)])
+def test_groups_of_one_small_score_with_few_open(E, k, groups, top_groups, group_top):
+    """Scores that are alike and so small that 32 bits do not tell one from the sum of two: a group with a single open
+    expert is behind those with two.  Beside them closed groups and such that are in for sure."""
+    rng = np.random.default_rng(E + group_top)
+    M, per = 96, E // groups
+    z = np.zeros((M, groups, per), np.float32)
+    for i in range(M):
+        open_one = rng.permutation(groups)[: 1 + i % (groups - 1)]
+        for g in open_one:
+            z[i, g, rng.permutation(per)[1:]] = -np.inf
+        if i % 4 == 1:
+            z[i, rng.integers(groups)] = -np.inf
+    low, high = z.copy(), z.copy()
+    low[np.isfinite(z)] = -30.0                                  # a sigmoid of 2^-43
+    for i in range(M):
+        high[i, i % groups] = 20.0                               # the others' softmax is below 2^-28
+    some = (rng.standard_normal(E) * 0.01).astype(np.float32)
+    for score, a in (("softmax", high), ("sigmoid", low)):
+        a = a.reshape(M, E)
+        for bias in (None, np.zeros(E, np.float32), some):
+            for renormalise in (True, False):
+                check(torch.from_numpy(a).cuda(), a.astype(np.float64), k, bias, score, groups, top_groups, group_top, renormalise, 1.0,
+                      "f32", rng)
+
+
+@pytest.mark.gpu
+def test_a_single_open_expert_against_two():
+    z = torch.tensor([[20.0, 20.0, 0.0, -float("inf"), 0.0, 0.0, 0.0, 0.0]], device="cuda")
+    ids, _ = zs.zs_route(z, 3, torch.zeros(8, device="cuda"), "softmax", 4, 2, 2)
+    assert ids.tolist() == [[0, 1, 4]]
