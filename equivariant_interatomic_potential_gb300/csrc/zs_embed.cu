@@ -136,6 +136,7 @@ __global__ void __launch_bounds__(kSumThreads, kSumCtas) sum_rows(SumShape s, Ro
     __shared__ int32_t unit_row[kSumThreads + 1];    // rows that end before each unit
     __shared__ float open[kSumThreads * VEC];        // sums of rows that a unit leaves open
     __shared__ int samples[2][kSumThreads / 64];
+    __shared__ int32_t begun_by;                     // the CTA that began the row which ends here and was begun before, or -1
     const int tid = threadIdx.x;
     const int64_t share = (int64_t)s.units * s.per_unit;
     const int64_t d0 = blockIdx.x * share, d1 = imin(d0 + share, s.items);
@@ -159,6 +160,10 @@ __global__ void __launch_bounds__(kSumThreads, kSumCtas) sum_rows(SumShape s, Ro
     int32_t* sperm = staged + bounds;
     for (int i = tid; i < count; i += kSumThreads) sperm[i] = __ldg(perm + j0 + i);
     __syncthreads();
+    if (tid == 0) {                                  // items are below 2^32
+        const int64_t begin = (int64_t)staged[0] + v0;
+        begun_by = rows > 0 && begin < d0 ? (int32_t)((uint32_t)imax<int64_t>(begin, 0) / (uint32_t)share) : -1;
+    }
     // where each unit starts: rows that end before it
     for (int i = tid; i <= s.units; i += kSumThreads) {
         const int64_t d = imin(d0 + (int64_t)i * s.per_unit, d1);
@@ -252,6 +257,9 @@ __global__ void __launch_bounds__(kSumThreads, kSumCtas) sum_rows(SumShape s, Ro
 #pragma unroll
             for (int i = 0; i < VEC; ++i) sum[i] += open[(q * s.cols + col) * VEC + i];
     };
+    // Without the ways that Row::store takes by a row's phase: with these, behind the threads of a warp that had gone all of
+    // them (its rows at a phase of 0, then odd, then even ones, and their last pieces) the last pieces' threads went on with
+    // values that were not theirs, and left out or misplaced parts of the row that is joined below (7 of 137000 gradients).
     const int64_t at = (int64_t)blockIdx.x * s.C;
     if (live && cut) {
         float sum[VEC];
@@ -261,7 +269,14 @@ __global__ void __launch_bounds__(kSumThreads, kSumCtas) sum_rows(SumShape s, Ro
         if ((int64_t)staged[begun_row] + v0 + begun_row >= d0) {   // begun in this CTA
 #pragma unroll
             for (int i = 0; i < VEC; ++i) sum[i] *= scale;
-            R::template store<true, false>(dw + (int64_t)(v0 + begun_row) * s.C, e, s.C, pack<T>(sum));
+            T* to = dw + (int64_t)(v0 + begun_row) * s.C;
+            if constexpr (kWhole) {
+                R::template store<true>(to, e, s.C, pack<T>(sum));
+            } else {   // a store for each element: few rows are cut
+#pragma unroll
+                for (int i = 0; i < VEC; ++i)
+                    if (column(c, i) < s.C) to[column(c, i)] = from_f32<T>(sum[i]);
+            }
         } else {
 #pragma unroll
             for (int i = 0; i < VEC; ++i)
@@ -281,17 +296,14 @@ __global__ void __launch_bounds__(kSumThreads, kSumCtas) sum_rows(SumShape s, Ro
             for (int i = 0; i < VEC; ++i)
                 if (kWhole || column(c, i) < s.C) tail[at + column(c, i)] = acc[i];
     }
-    // the row that is open at the CTA's start, if it was begun before and ends here
-    const int64_t begin = (int64_t)staged[0] + v0;
-    const bool closes = rows > 0 && begin < d0;
-    const int first = closes ? (int)imax<int64_t>(begin / share, 0) : 0;
+    const int first = begun_by;
     if (!kCluster) {
-        if (tid == 0 && blockIdx.y == 0) notes[blockIdx.x] = SumNote{closes ? v0 : -1, first};
+        if (tid == 0 && blockIdx.y == 0) notes[blockIdx.x] = SumNote{first < 0 ? -1 : v0, imax(first, 0)};
         return;
     }
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-    if (!closes) return;
+    if (first < 0) return;
     const int64_t c0 = (int64_t)blockIdx.y * s.cols;
     for (int t = tid; t < s.cols * VEC; t += kSumThreads) {
         const int i = R::kStrided ? (int)s.by_cols.quotient((uint32_t)t) : t % VEC;
