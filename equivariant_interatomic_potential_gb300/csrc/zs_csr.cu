@@ -116,8 +116,7 @@ csr_upsweep_group(const int32_t* __restrict__ keys_in, int64_t E, int32_t N, int
 #pragma unroll
     for (int u = 0; u < kItems; ++u)
         if (dig[u] >= 0) atomicAdd(&cnt[dig[u]], 1);
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    cluster_barrier();
     if (tid < kRadix / kTileGroup) {
         const int group = blockIdx.x / kTileGroup, d = (blockIdx.x % kTileGroup) * (kRadix / kTileGroup) + tid;
         const uint32_t at = static_cast<uint32_t>(__cvta_generic_to_shared(cnt + d));
@@ -133,8 +132,7 @@ csr_upsweep_group(const int32_t* __restrict__ keys_in, int64_t E, int32_t N, int
         }
         groups[(int64_t)group * kRadix + d] = run;
     }
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");   // no CTA ends before all have read
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    cluster_barrier();   // no CTA ends before all have read
 }
 
 // One CTA per row: exclusive scan of hist[d, 0..T) in place, total to tot[d].
@@ -822,8 +820,7 @@ csr_count_group(const int32_t* __restrict__ dst, int64_t E, int32_t N, int round
         mine[2 * q] = (int32_t)(run & 0xffffu);
         mine[2 * q + 1] = (int32_t)(run >> 16);
     }
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    cluster_barrier();
     for (int k = tid; k < nkeys; k += kCntThreads) {
         const uint32_t at = static_cast<uint32_t>(__cvta_generic_to_shared(mine + k));
         int32_t c[kGroupCtas], all = 0, before = 0;
@@ -839,7 +836,7 @@ csr_count_group(const int32_t* __restrict__ dst, int64_t E, int32_t N, int round
         tot[k] = all;
         base[k] = before;
     }
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");   // no CTA ends before all have read
+    cluster_arrive();   // no CTA ends before all have read
     __syncthreads();
     key_bases(tot, base, base, nkeys, N, wsum, blockIdx.x == 0 ? row_ptr : nullptr, bad);
     __syncthreads();
@@ -848,7 +845,7 @@ csr_count_group(const int32_t* __restrict__ dst, int64_t E, int32_t N, int round
         const uint32_t p = packed[i];
         perm[base[p >> 16] + (int32_t)((p & 0xffffu) + cnt[2 * (i / TW) * npairs + (p >> 16)])] = tbase + i;
     }
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    cluster_wait();
 }
 
 // All passes over tiles of 256 * kItems keys, at most kFewTiles of them (so small that most SMs have one) or of groups of them

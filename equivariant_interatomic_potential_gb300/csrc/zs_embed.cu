@@ -301,8 +301,7 @@ __global__ void __launch_bounds__(kSumThreads, kSumCtas) sum_rows(SumShape s, Ro
         if (tid == 0 && blockIdx.y == 0) notes[blockIdx.x] = SumNote{first < 0 ? -1 : v0, imax(first, 0)};
         return;
     }
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    cluster_barrier();
     if (first < 0) return;
     const int64_t c0 = (int64_t)blockIdx.y * s.cols;
     for (int t = tid; t < s.cols * VEC; t += kSumThreads) {

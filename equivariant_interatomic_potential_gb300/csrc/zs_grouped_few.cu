@@ -153,10 +153,6 @@ __global__ void __launch_bounds__(256) few_forward(const FewArgs a) {
 // add their parts through distributed shared memory.  Eight lanes (128 bytes of a
 // row) give four times the CTAs, for one or a few groups.
 constexpr int kDxWarps = 8, kDxCluster = 8;
-__device__ __forceinline__ void cluster_barrier() {
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
 template <typename T, int V, int kLanes>
 __global__ void __launch_bounds__(32 * kDxWarps) few_dx(const FewArgs a) {
     constexpr int kCols = kLanes * V, kShares = kDxWarps * (32 / kLanes);   // columns; threads that share them

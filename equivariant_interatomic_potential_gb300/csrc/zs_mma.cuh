@@ -139,10 +139,6 @@ __device__ __forceinline__ uint32_t cluster_rank() {
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
     return r;
 }
-__device__ __forceinline__ void pair_barrier() {
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 // A position in a ring of S stages.
@@ -728,14 +724,14 @@ struct Setup {
         if ((threadIdx.x >> 5) == 2) tmem_alloc<kPair>(smem_u32(slot), kTmemCols);
         tc_fence_before();
         __syncthreads();
-        if (kPair) pair_barrier();   // the other CTA's barriers are there
+        if (kPair) cluster_barrier();   // the other CTA's barriers are there
         tc_fence_after();
         tmem = *slot;
     }
     __device__ __forceinline__ void end() {
         tc_fence_before();
         __syncthreads();
-        if (kPair) pair_barrier();   // nothing reads, or arrives at, a CTA that has left
+        if (kPair) cluster_barrier();   // nothing reads, or arrives at, a CTA that has left
         tc_fence_after();
         if ((threadIdx.x >> 5) == 2) tmem_free<kPair>(tmem, kTmemCols);
     }

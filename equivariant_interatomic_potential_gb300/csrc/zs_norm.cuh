@@ -219,11 +219,6 @@ struct NormRing {
     }
 };
 
-__device__ __forceinline__ void cluster_barrier() {
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
 // Sums over the threads of a row.  Rows of up to 32 threads stay within a
 // warp.  Wider ones go through shared memory: `red` holds two rounds of a
 // float4 for each warp of each CTA of the row, taken in turn, so that one
