@@ -154,9 +154,11 @@ struct RingPos {
 // ---------------------------------------------------------------- tcgen05
 
 // kPair: both CTAs of a cluster of two take part (a warp of each allocates and
-// frees; the first one's products are of both).
+// frees; the first one's products are of both).  Instructions of a whole warp,
+// whose threads may come from loops of their own.
 template <bool kPair>
 __device__ __forceinline__ void tmem_alloc(uint32_t dst_smem, uint32_t cols) {
+    __syncwarp();
     if constexpr (kPair) {
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" :: "r"(dst_smem), "r"(cols) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
@@ -167,6 +169,7 @@ __device__ __forceinline__ void tmem_alloc(uint32_t dst_smem, uint32_t cols) {
 }
 template <bool kPair>
 __device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t cols) {
+    __syncwarp();
     if constexpr (kPair) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" :: "r"(addr), "r"(cols) : "memory");
     else asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(addr), "r"(cols) : "memory");
 }
@@ -588,6 +591,7 @@ __device__ __forceinline__ void store_tile(uint32_t tmem, int c0, int c1, TO* ro
         uint32_t w[32];
         float f[32];
         if (tmem != kNoTile) {
+            __syncwarp();   // from the stores of the columns before, which some lanes leave out
             tmem_ld32(tmem + c, w);
             tmem_ld_wait();
         } else {
