@@ -376,6 +376,21 @@ __device__ __noinline__ int order_in_64_bits(const RouteShape& s, int lane, cons
     return lane < imin(n, s.k) ? (int)space.taken[lane].x : -1;
 }
 
+// Whether what is near the last choice behind those that the rounds took (a lane's first key `head`, the others from list[next]
+// on) is all of the last choice's logit and bias.
+template <typename T, int V>
+__device__ __noinline__ bool alike_behind(const RouteShape& s, int lane, const T* __restrict__ row, const float* __restrict__ bias,
+                                          RouteSpace<V>& space, uint32_t head, int next, uint32_t last, float error) {
+    const int e = expert_of<V>(s, space.taken[s.k - 1]);
+    const float z = logit(row, e), b = bias ? __ldg(bias + e) : 0.f;
+    bool alike = true;
+    for (uint32_t key = head; key >= kOpen && near_keys<V>(last, key, error); key = space.list[next++][lane]) {   // ends in 0
+        const int f = expert_of<V>(s, make_uint2(key, lane));
+        alike = alike && logit(row, f) == z && (!bias || __ldg(bias + f) == b);
+    }
+    return __all_sync(kAll, alike);
+}
+
 // A warp's row r0.
 template <typename T, int V, bool kScored>
 __device__ __forceinline__ void route_row(const RouteShape& s, int64_t r0, int lane, RouteSpace<V>& space, const T* __restrict__ logits,
@@ -516,9 +531,14 @@ __device__ __forceinline__ void route_row(const RouteShape& s, int64_t r0, int l
         }
     }
     bool far = __any_sync(kAll, odd);
-    if (!kExact<T, kScored> && !far && __any_sync(kAll, near)) {
-        far = n > kRouteMaxK || (kScored && !s.sigmoid && bias);
-        if (!far) id = order_in_64_bits<T, V, kScored>(s, lane, row, bias, space, n, top);
+    if (!kExact<T, kScored> && !far) {
+        if (__any_sync(kAll, near)) {
+            far = n > kRouteMaxK || (kScored && !s.sigmoid && bias);
+            if (!far) id = order_in_64_bits<T, V, kScored>(s, lane, row, bias, space, n, top);
+        } else if (n > kRouteMaxK) {   // there may be more of them than were taken
+            const int moved = (int)(next - (uint32_t)__cvta_generic_to_shared(&space.list[1][lane])) / 128;
+            far = !alike_behind<T, V>(s, lane, row, bias, space, head, 1 + moved, last, error);
+        }
     }
     if (far) id = choose_in_64_bits<T, V, kScored>(s, lane, row, bias);
 

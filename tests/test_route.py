@@ -432,3 +432,23 @@ def test_a_single_open_expert_against_two():
     z = torch.tensor([[20.0, 20.0, 0.0, -float("inf"), 0.0, 0.0, 0.0, 0.0]], device="cuda")
     ids, _ = zs.zs_route(z, 3, torch.zeros(8, device="cuda"), "softmax", 4, 2, 2)
     assert ids.tolist() == [[0, 1, 4]]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("E,k", [(64, 1), (96, 4), (260, 8), (1000, 32)])
+def test_more_alike_than_are_looked_at(E, k):
+    """Most experts of a row are alike, and a few behind them are larger by what only 64 bits tell, or the logits' last bits."""
+    rng = np.random.default_rng(E)
+    M = 40
+    z = np.full((M, E), -30.0, np.float32)
+    for i in range(1, M):
+        at = rng.permutation(E)[:i % 7]
+        z[i, at] = np.nextafter(z[i, at], np.float32(0))
+    check(torch.from_numpy(z).cuda(), z.astype(np.float64), k, None, "sigmoid", 1, 1, 1, True, 1.0, "f32", rng)
+    check(torch.from_numpy(z).cuda(), z.astype(np.float64), k, np.zeros(E, np.float32), "softmax", 1, 1, 1, True, 1.0, "f32", rng)
+    high = np.full((M, E), 18.5, np.float32)                     # sigmoids of 1 but for 2^-27
+    for i in range(1, M):
+        high[i, rng.permutation(E)[:i % 7]] = 27.25
+    for groups, top in ((1, 1), (4, 2)):
+        check(torch.from_numpy(high).bfloat16().cuda(), high.astype(np.float64), k, np.zeros(E, np.float32), "sigmoid", groups, top, 1, False,
+              1.0, "bf16", rng)
