@@ -613,7 +613,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_rows_of_few(RouteShape
         int n = 0, before = 0;
         float last = 0.f;
 #pragma unroll 1
-        for (; n < s.k + kScored; ++n) {   // scores are looked at once more, for the one behind the choice
+        for (;;) {   // scores are looked at behind the choice too, as long as they are near to its last one
             float best = -INFINITY;
             int at = -1;
 #pragma unroll
@@ -622,11 +622,15 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_rows_of_few(RouteShape
             if (at < 0) break;
             if (kScored && n > 0 && last - best <= 2.f * error + 0x1p-22f * (fabsf(last) + fabsf(best)))   // as near_keys
                 left = left || !(logit(row, before) == logit(row, at) && (!bias || __ldg(bias + before) == __ldg(bias + at)));
-            if (n == s.k) break;
-            order |= (uint64_t)at << (4 * n);
+            else if (n == s.k) break;
+            if (n < s.k) {
+                order |= (uint64_t)at << (4 * n);
+                before = at;
+                last = best;
+                ++n;
+            }
+            if (left || (!kScored && n == s.k)) break;
             open &= ~(1u << at);
-            before = at;
-            last = best;
         }
         if (!left) {
             auto chosen = [&](int j) { return (int)(order >> (4 * j)) & 15; };

@@ -452,3 +452,23 @@ def test_more_alike_than_are_looked_at(E, k):
     for groups, top in ((1, 1), (4, 2)):
         check(torch.from_numpy(high).bfloat16().cuda(), high.astype(np.float64), k, np.zeros(E, np.float32), "sigmoid", groups, top, 1, False,
               1.0, "bf16", rng)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("E,k", [(11, 1), (16, 3), (8, 7), (3, 1)])
+def test_few_experts_alike_behind_the_choice(E, k):
+    """A thread's row: behind the choice several scores that 32 bits do not tell from its last one, the larger not first."""
+    rng = np.random.default_rng(E)
+    M = 4200
+    a = np.where(rng.random((M, E)) < 0.4, 18.5, -3.0)           # sigmoids of 1 but for 2^-27
+    a[rng.random((M, E)) < 0.2] = 27.25
+    a[1::7, 1:] = 18.5
+    a[2::7] = -30.0
+    a[2::7, E - 1] = -29.5
+    z, zd = held(a, "bf16")
+    for bias in (np.zeros(E, np.float32), np.full(E, 0.75, np.float32)):
+        check(z.cuda(), zd, k, bias, "sigmoid", 1, 1, 1, False, 1.0, "bf16", rng)
+    peak = np.where(a > 0, 20.0, a)
+    peak[:, 0] = 60.0                                            # a softmax below 2^-57 for the others
+    z, zd = held(peak, "bf16")
+    check(z.cuda(), zd, k, np.zeros(E, np.float32), "softmax", 1, 1, 1, False, 1.0, "bf16", rng)
