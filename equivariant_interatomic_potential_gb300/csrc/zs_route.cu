@@ -161,6 +161,10 @@ __device__ __forceinline__ double score_in_64_bits(const RouteShape& s, double z
     return bias ? a + (double)__ldg(bias + e) : a;
 }
 
+// A softmax's exponentials sort like its scores, and their sums like the scores', where the division by the row's sum, at most
+// 1024, loses nothing of them.
+constexpr double kLeastExp = 0x1p-1000;
+
 // The `need` groups of the mask `groups` with the largest values, as a mask: lane g holds group g's.  NaN are above all,
 // equal ones go by their number.
 __device__ __forceinline__ unsigned best_groups(unsigned groups, int need, int lane, double value) {
@@ -302,10 +306,10 @@ __device__ __forceinline__ bool near_keys(uint32_t a, uint32_t b, float error) {
 // Of the groups of the mask `border`, between which 32 bits do not tell, the `need` best as a mask: the elements of each
 // that may be among its two largest, in 64 bits, a lane each; groups of nothing but one logit and bias (a router that has
 // learnt nothing), and all of one or all of two terms, by their numbers.  0 where there are too many, or a softmax has a
-// bias.  `head` is a lane's first key.
+// bias or scores so small that they may be alike.  `head` is a lane's first key, `row_top` the row's largest logit.
 template <typename T, int V>
 __device__ __noinline__ unsigned border_groups(const RouteShape& s, int lane, const T* __restrict__ row, const float* __restrict__ bias,
-                                               RouteSpace<V>& space, uint32_t head, float error, unsigned border, int need) {
+                                               RouteSpace<V>& space, uint32_t head, float error, float row_top, unsigned border, int need) {
     const Lane l(s, lane);
     uint32_t first = head & ~kPlace<V>, second = V > 1 ? space.list[1][lane] & ~kPlace<V> : 0;
     if (first < kOpen) first = 0;
@@ -339,12 +343,8 @@ __device__ __noinline__ unsigned border_groups(const RouteShape& s, int lane, co
         return __all_sync(kAll, alike) ? best_groups(border, need, lane, 0.0) : 0;
     }
     const int e = lane < n ? expert_of<V>(s, space.taken[lane]) : 0, group = lane < n ? e / s.per : -1;
-    double a = lane < n ? (double)logit(row, e) : -INFINITY, top = 0.0;
-    if (!s.sigmoid) {   // sums of a softmax's scores sort like those of its exponentials
-        top = a;
-        for (int o = 16; o > 0; o >>= 1) top = fmax(top, __shfl_xor_sync(kAll, top, o));
-    }
-    if (lane < n) a = score_in_64_bits<true>(s, a, top, 1.0, bias, e);
+    const double a = lane < n ? score_in_64_bits<true>(s, logit(row, e), row_top, 1.0, bias, e) : -INFINITY;
+    if (!s.sigmoid && __any_sync(kAll, lane < n && a < kLeastExp)) return 0;
     double one = -INFINITY, two = -INFINITY;   // the two largest of group `lane`
     for (int j = 0; j < n; ++j) {
         const double other = __shfl_sync(kAll, a, j);
@@ -364,6 +364,7 @@ __device__ __noinline__ int order_in_64_bits(const RouteShape& s, int lane, cons
     const bool open = lane < n;
     const int e = open ? expert_of<V>(s, space.taken[lane]) : -1;
     const double a = open ? score_in_64_bits<kScored>(s, logit(row, e), top, 1.0, bias, e) : -INFINITY;
+    if (kScored && !s.sigmoid && __any_sync(kAll, open && a < kLeastExp)) return choose_in_64_bits<T, V, kScored>(s, lane, row, bias);
     int ahead = 0;
     for (int j = 0; j < n; ++j) {
         const double other = __shfl_sync(kAll, a, j);
@@ -479,7 +480,7 @@ __device__ __forceinline__ void route_row(const RouteShape& s, int64_t r0, int l
                 border |= (unsigned)__shfl_sync(kAll, (int)at_border, g << s.lane_bits) << g;
                 sure |= (unsigned)__shfl_sync(kAll, (int)(kept && speaks && !at_border), g << s.lane_bits) << g;
             }
-            const unsigned mask = border_groups<T, V>(s, lane, row, bias, space, head, error, border, s.top_groups - __popc(sure));
+            const unsigned mask = border_groups<T, V>(s, lane, row, bias, space, head, error, top, border, s.top_groups - __popc(sure));
             odd = odd || mask == 0;
             if (mask) kept = (mask | sure) >> l.group & 1u;
         }

@@ -472,3 +472,27 @@ def test_few_experts_alike_behind_the_choice(E, k):
     peak[:, 0] = 60.0                                            # a softmax below 2^-57 for the others
     z, zd = held(peak, "bf16")
     check(z.cuda(), zd, k, np.zeros(E, np.float32), "softmax", 1, 1, 1, False, 1.0, "bf16", rng)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("per", [2, 10])
+def test_groups_far_below_the_largest_logit(per):
+    """Scores that are 0 in 64 bits, beside a logit that is 746 or more larger, are alike whatever their logits; so are those
+    that a division by the row's sum makes alike (2^-1074 and three times that over eight)."""
+    rng = np.random.default_rng(per)
+    for far in (1000.0, 746.0):
+        z = np.zeros((1, 4, per), np.float32)
+        z[0, 0] = far
+        z[0, 2] = 1.0 if far == 1000.0 else 0.25
+        z = z.reshape(1, -1)
+        for group_top in (1, 2):
+            check(torch.from_numpy(z).cuda(), z.astype(np.float64), per + 1, None, "softmax", 4, 2, group_top, True, 1.0, "f32", rng)
+    unit = np.float32(1074 * np.log(2))                          # exp(-unit): 2^-1074
+    z = np.zeros((40, 4, 8), np.float32)                         # a sum of eight and a little
+    for i in range(40):
+        z[i, 1:] = -(unit - np.log(rng.integers(1, 4, (3, 8))).astype(np.float32))
+    z = z.reshape(40, 32)
+    assert np.array_equal(np.unique(np.exp(z[:, 8:].astype(np.float64))), np.array([1, 2, 3]) * 2.0 ** -1074)
+    for top_groups, k in ((1, 8), (2, 16), (3, 20)):
+        for group_top in (1, 2):
+            check(torch.from_numpy(z).cuda(), z.astype(np.float64), k, None, "softmax", 4, top_groups, group_top, False, 1.0, "f32", rng)
