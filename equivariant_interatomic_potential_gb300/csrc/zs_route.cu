@@ -384,6 +384,15 @@ __device__ __noinline__ bool alike_behind(const RouteShape& s, int lane, const T
                                           RouteSpace<V>& space, uint32_t head, int next, uint32_t last, float error) {
     const int e = expert_of<V>(s, space.taken[s.k - 1]);
     const float z = logit(row, e), b = bias ? __ldg(bias + e) : 0.f;
+    // A row of one logit and bias (a router that has learnt nothing) in the row's order, 32 neighbours at a time: a lane's own
+    // experts are a cache line apart from the next one's (32768 rows of 1024 equal fp32 logits: 130 us, 212 without).
+    bool same = true;
+#pragma unroll 8
+    for (int f = lane; f < s.E; f += 32) {
+        const float v = logit(row, f), w = bias ? __ldg(bias + f) : b;
+        same = same & ((v == z) | (v == -INFINITY)) & (w == b);
+    }
+    if (__all_sync(kAll, same)) return true;
     bool alike = true;
     for (uint32_t key = head; key >= kOpen && near_keys<V>(last, key, error); key = space.list[next++][lane]) {   // ends in 0
         const int f = expert_of<V>(s, make_uint2(key, lane));
