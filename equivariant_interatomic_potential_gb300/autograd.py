@@ -576,6 +576,8 @@ def expert_block(x: torch.Tensor, logits: torch.Tensor, w_in: torch.Tensor, w_ou
     """A layer of experts: y[i] = the sum over the row's k experts e, by their weights, of
     w_out[e] activation(w_in[e] x[i]).  x (M, C), logits (M, E), w_in (E, H, C), w_out (E, N, H); y (M, N),
     differentiable in x, the logits and both weights."""
+    if not logits.shape[-1] == w_in.shape[0] == w_out.shape[0]:
+        raise ValueError(f"logits of {logits.shape[-1]} experts, w_in of {w_in.shape[0]} and w_out of {w_out.shape[0]}")
     ids, weights = route(logits, k, bias, score, groups, top_groups, group_top, renormalise, scale)
     row_ptr, perm = build_csr(ids.view(-1), w_in.shape[0])
     xs, slot = dispatch(x, row_ptr, perm, k)

@@ -370,3 +370,11 @@ def test_example_gradients_against_differences():
             p += 1e-3 * v
         slope, terms = float(up - down) / 2e-3, g.double() * v.double()
         assert abs(slope - float(terms.sum())) <= 1e-2 * float(terms.abs().sum()), name
+
+
+@pytest.mark.parametrize("logits,w_in,w_out", [(6, 5, 5), (5, 6, 6), (6, 6, 5), (5, 5, 6)])
+def test_numbers_of_experts_that_differ_are_refused(logits, w_in, w_out):
+    # assignments to experts that have no weights would be dropped, after the weights were renormalised over them
+    x = torch.zeros(4, 8)
+    with pytest.raises(ValueError, match=f"{logits} experts, w_in of {w_in} and w_out of {w_out}"):
+        ag.expert_block(x, torch.zeros(4, logits), torch.zeros(w_in, 16, 8), torch.zeros(w_out, 8, 16), 2)
