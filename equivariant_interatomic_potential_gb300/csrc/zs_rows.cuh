@@ -50,16 +50,16 @@ __device__ __forceinline__ uint4 shifted(uint4 a, uint4 b, int o) {
                       __funnelshift_r(w[3], w[4], s));
 }
 
-// A matrix that is read: rows ld apart, all of it in [p, end).  Around `inner` rows from row `margin` on there are three
-// pieces and more of it on both sides.
+// A matrix that is read: rows ld apart.  Around `inner` rows from row `margin` on there are three pieces and more of it on both
+// sides.
 template <typename T>
 struct Rows {
-    const T *p, *end;
+    const T* p;
     int64_t ld;
     int32_t margin;
     uint32_t inner;
     Rows(const void* p_, int64_t rows, int64_t ld_, int32_t C)
-        : p(static_cast<const T*>(p_)), end(p + (rows > 0 ? (rows - 1) * ld_ + C : 0)), ld(ld_) {
+        : p(static_cast<const T*>(p_)), ld(ld_) {
         margin = (int32_t)((3 * kVec<T> + (int64_t)C - 1) / C);   // a row takes C and more
         inner = rows > 2 * (int64_t)margin ? (uint32_t)(rows - 2 * margin) : 0u;
     }
