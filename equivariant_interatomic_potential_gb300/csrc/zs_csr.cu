@@ -10,7 +10,7 @@
 // Counting path (N + 1 <= kCntMaxKeys, every bench-sized graph but the
 // largest): one pass, three launches with no inter-CTA waiting (one launch of
 // one CTA, count_single, for up to kSingleMaxEdges edges; of up to kGroupMaxKeys
-// keys one of a cluster, count_group, from 1024 to 16384 edges):
+// keys one of a cluster, count_group, from 1025 to 16384 edges):
 //   count_rank    -- per tile of edges, each edge's stable rank among the
 //                    tile's edges of the same node (warp match + per-warp
 //                    running counts in shared memory, then a prefix over
@@ -732,11 +732,13 @@ csr_count_scatter(const int32_t* __restrict__ dst, const uint16_t* __restrict__ 
     }
 }
 
-// Small graphs (E <= kCntMaxRounds * kCntThreads edges): the whole counting
-// path in one CTA and one launch -- csr_count_rank's ranking and counts, then
-// csr_count_scatter's node bases and scatter, the counts staying in shared
-// memory (with one tile, every edge's offset within its key is its rank).
-constexpr int kSingleMaxEdges = 8 * kCntThreads;   // 4096: 6.4 to 8.3 us; 8192 edges took 9.4 to 15, 6 in three launches
+// Small graphs (up to kSingleMaxEdges edges, where count_group does not take
+// them): the whole counting path in one CTA and one launch -- csr_count_rank's
+// ranking and counts, then csr_count_scatter's node bases and scatter, the
+// counts staying in shared memory (with one tile, every edge's offset within its
+// key is its rank).
+constexpr int kSingleRounds = 8;
+constexpr int kSingleMaxEdges = kSingleRounds * kCntThreads;   // 4096: 6.4 to 8.3 us; 8192 edges took 9.4 to 15, 6 in three launches
 inline int count_single_smem(int nkeys, int rounds) {
     return count_rank_smem(nkeys, rounds) + 2 * count_pairs(nkeys) * 4;
 }
@@ -959,7 +961,7 @@ extern "C" zs_status zs_build_csr(const int32_t* dst, int64_t E, int32_t N,
         }
         if (E <= kSingleMaxEdges) {
             static std::atomic<uint64_t> single_smem_set[kMaxDevices];
-            set_smem_limit_once(csr_count_single, count_single_smem(kCntMaxKeys, kCntMaxRounds), single_smem_set);
+            set_smem_limit_once(csr_count_single, count_single_smem(kCntMaxKeys, kSingleRounds), single_smem_set);
             const int rounds = (int)((E + kCntThreads - 1) / kCntThreads);
             launch(csr_count_single, 1, kCntThreads, count_single_smem(N + 1, rounds), s, dst, E, N, rounds, perm,
                    row_ptr, bad_dst_count);
@@ -990,9 +992,11 @@ extern "C" zs_status zs_build_csr(const int32_t* dst, int64_t E, int32_t N,
             else if (E <= kFewTiles * 1024) sorted = sort_few<4>(p.passes, dst, E, N, k, v, perm, hist, s);
             else sorted = sort_few<8>(p.passes, dst, E, N, k, v, perm, hist, s);
         } else if (p.passes > 1 && E <= (int64_t)kFewTiles * kTileGroup * kTile) {
-            // twice as large tiles where they are about one for each SM (of 7921: 400000 keys 23.8 us with 8 a thread, 23.3 with
-            // 16; 647170 31.5 and 29.5, 800000 32.8 and 30.4; 1048576 32.9 and 34.6)
-            if (E > 256 * (int64_t)kTile && E <= 400 * (int64_t)kTile) sorted = sort_few<2 * kCsrItems, true>(p.passes, dst, E, N, k, v, perm, hist, s);
+            // Twice as large tiles where these are from 5/6 to 4/3 of the SMs (keys of 7921, us with 8 a thread against 16: 519000,
+            // 127 tiles, 25.4 and 25.6; 560000 26.5 and 26.4; 647170 31.4 and 29.1; 829000, 203 tiles, 33.1 and 30.2; 900000 32.8
+            // and 33.9).
+            const int64_t tiles = (E + 2 * kTile - 1) / (2 * kTile);
+            if (6 * tiles > 5 * num_sms() && 3 * tiles <= 4 * num_sms()) sorted = sort_few<2 * kCsrItems, true>(p.passes, dst, E, N, k, v, perm, hist, s);
             else sorted = sort_few<kCsrItems, true>(p.passes, dst, E, N, k, v, perm, hist, s);
         } else {
             const int32_t* kin = dst;
