@@ -536,7 +536,8 @@ combine.register_autograd(_backward_combine, setup_context=_setup_context_combin
 def dropout(h: torch.Tensor, p: float, seed: int, call: int = 0, step: int = 0, step_at: Optional[torch.Tensor] = None,
             residual: Optional[torch.Tensor] = None) -> torch.Tensor:
     """residual + dropout(h), by the counters (call, step): step a number, or with ``step_at`` one int64 element on
-    the device (step is 0 then), which may move on once the backward pass has run."""
+    the device (step is 0 then), which may move on once the backward pass has run.  The seed is an int64 here: a negative
+    one stands for itself + 2^64."""
     _cuda_only("dropout", h)
     if step_at is not None and step != 0:
         raise ValueError("step and step_at are given")

@@ -9,7 +9,9 @@
 // Bound by memory: an element costs 4 bytes and more (16-bit, no residual), its
 // share of the generator about 6 instructions of the 22 that fit beside it (32
 // bits for each element would take all of them).  32768 x 2048 bf16: 47 us, 56
-// with a residual, 5.7 and 7.1 TB/s.
+// with a residual, 5.7 and 7.1 TB/s; the second is above the rate of a copy since
+// 56 MB of the 134 written are still in L2 at the kernel's end.  Rows at strides,
+// and bases off 16-byte boundaries, go element by element: 164 and 173 us.
 #include <math.h>
 
 #include "zs_rows.cuh"

@@ -18,8 +18,8 @@
 // CTAs goes to the workspace in fp32 and is added up by a second kernel in the
 // CTAs' order.  All sums are in fp32 and in an order that follows from the sizes
 // and the ids.  As many CTAs as run at once: the search for a share's first row
-// and the staging take about 5 us, in which nothing else runs (24 CTAs an SM: 67
-// instead of 47 us).  Both kernels, 647170 rows of 96 floats, skewed over 7921
+// and the staging take about 5 us, in which nothing else runs (24 CTAs an SM: 71
+// instead of 46 us).  Both kernels, 647170 rows of 96 floats, skewed over 7921
 // ids: 47 us, 5.4 TB/s; 16384 rows of 1024 bf16 and a table of 50021: 33 us, 4.2
 // TB/s, of which the join is about 4.
 #include "zs_rows.cuh"
@@ -50,7 +50,8 @@ zs_status embed_forward(const void* w, int64_t w_ld, int32_t V, const int32_t* i
 // ------------------------------------------------------------------ gradient
 
 constexpr int kSumThreads = 256;
-constexpr int kSumBatch = 6;         // rows of dy that a thread loads at a time
+constexpr int kSumBatch = 6;         // rows of dy that a thread loads at a time (of 80 registers: 32 to 46 bytes are spilled
+                                     // for 16-bit rows of whole pieces and fp32 rows of others, 4 for fp32 ones of whole pieces)
 constexpr int kSumMaxC = 1 << 23;    // columns (of the grids)
 constexpr int kSumItems = 4096;      // most items of a CTA (staged in shared memory)
 constexpr int kSumCluster = 8;       // CTAs of a cluster, which adds up what is cut between them itself: where they

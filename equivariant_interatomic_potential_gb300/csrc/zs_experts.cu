@@ -104,8 +104,10 @@ zs_status dispatch(const void* x, int64_t x_ld, const int32_t* row_ptr, const in
 // U pieces of a thread at a time and KJ choices of each: four or eight loads in flight and four or five CTAs an SM.  More
 // loads and fewer CTAs are slower (8 choices of 1024 bf16, 32768 rows: 106 us at 3 CTAs, 97 at 4; 2 choices of 256, 256 MB:
 // 8 loads at 3 CTAs 111, 4 at 5 84), staging slots in shared memory too (115 to 188): the read of rows in any order is the
-// limit, 0.93 of the copy rate.  Where rows have phases of their own a load is of two words, and two choices at a time are
-// the most that five CTAs' registers hold (8 choices of 301 fp16, 256 MB: 79 us; four at four CTAs 87, eight at three 90).
+// limit, 0.93 of the copy rate.  (Two choices of two 16-bit pieces do not fit the 48 registers of five CTAs: 56 bytes of
+// stores and 76 of loads are spilled; four CTAs have not been measured.)  Where rows have phases of their own a load is of
+// two words, and two choices at a time are the most that five CTAs' registers hold (8 choices of 301 fp16, 256 MB: 79 us;
+// four at four CTAs 87, eight at three 90).
 template <typename T, bool kWhole, int KJ, int U>
 __global__ void __launch_bounds__(kMoveThreads, KJ == kChoices ? 4 : 5) combine_rows(
     MoveShape s, int32_t k, int32_t R, Rows<T> h, const int32_t* __restrict__ slot, const float* __restrict__ weights, T* __restrict__ y,
@@ -192,9 +194,9 @@ __device__ __forceinline__ void sum_of_row(float (&dot)[KJ], int lanes, int lane
     }
 }
 
-// `lanes` threads for a row i of dy, which they read once for its k choices: their rows of h in flight together, the
-// products with dy in fp32 registers until the row's end.  Memory: 32768 rows, 8 choices of 1024 bf16: 176 us, 0.95 of the
-// copy rate.
+// `lanes` threads for a row i of dy, which they read once for each KJ of its choices: their rows of h in flight together, the
+// products with dy in fp32 registers until the row's end (of 80 registers, of which eight choices spill 8 to 36 bytes).
+// Memory: 32768 rows, 8 choices of 1024 bf16: 176 us, 0.95 of the copy rate.
 template <typename T, bool kWhole, int KJ>
 __global__ void __launch_bounds__(kBackThreads, 3) combine_rows_backward(
     int64_t M, int32_t k, int32_t R, int32_t P, int32_t C, int lane_bits, Rows<T> dy, Rows<T> h, const int32_t* __restrict__ slot,

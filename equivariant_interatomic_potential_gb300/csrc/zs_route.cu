@@ -15,16 +15,19 @@
 // formed in 32 bits); where two neighbours of the choice, or two groups at its
 // border, lie closer than that (and are not of one logit and bias), the few
 // candidates are put in order in 64 bits, a lane each: one row in some hundred of
-// ordinary ones.  Only where there are more than 32, with NaN, and for a softmax
-// with a bias is all of the row done in 64 bits.  Weights are formed in 32 bits,
-// relative to the largest chosen logit where they are renormalised, so that they
-// never are 0 / 0.
+// ordinary ones.  Where there are more than 32, with NaN, for a softmax with a
+// bias, and where a softmax's scores are below 2^-1000 (which a division by the
+// row's sum may make alike), all of the row is done in 64 bits.  Weights are
+// formed in 32 bits, relative to the largest chosen logit where they are
+// renormalised, so that they never are 0 / 0.
 //
-// What bounds it: instructions.  A row of 256 experts takes about 320 and 25 for
-// each choice, sigmoids and a bias 140 more, groups 160: 32768 rows, 8 choices, 4
-// of 8 groups: 33 us where the bytes are 5.  With 48 warps of 40 registers an SM
-// it issues in three of four cycles.  An unsorted lane (rounds that look
-// at all V keys) took 77 us, several rows a warp 45 (too few CTAs to even out).
+// What bounds it: the instructions of this way of choosing.  32768 rows of 256
+// experts, 8 choices, 4 of 8 groups: 870 a row (25 for each choice, 140 for
+// sigmoids and a bias, 160 for groups), 33 us where the bytes are 5.  48 warps of
+// 40 registers an SM issue in two of three cycles: a warp lives for one row,
+// whose loads and rounds only other warps hide.  An unsorted lane (rounds that
+// look at all V keys) took 77 us, several rows a warp 45 (too few CTAs to even
+// out).
 #include "zs_types.cuh"
 
 namespace zs {
